@@ -18,6 +18,10 @@ never stored, run as hand-written gfx950 HIP kernels behind the C ABI of
 * ``keops_gauss_max``, ``keops_gauss_min`` -- Max/ArgMax and Min/ArgMin of K b
 * ``keops_laplace_sum``  -- the Laplacian kernel sum, exp(-|x - y| / sigma)
 * ``keops_kmin``         -- K nearest neighbours with indices
+* ``keops_cache_append``, ``keops_paged_attention``, ``keops_cache_evict`` -- a paged
+  key/value cache: new tokens into it, causal attention over it (a LogSumExp over keys),
+  eviction from it by accumulated attention weight
+* ``keops_verify_draft`` -- drafted tokens against the target model's probabilities
 
 PyTorch supplies device memory and streams only.
 """
@@ -27,3 +31,4 @@ from .binding import (KEOPS_OPT_FAIL_ALLOC, KEOPS_OPT_FORM, KEOPS_OPT_MFMA, KEOP
                       keops_gauss_grad_y, keops_gauss_lse, keops_gauss_lse_ranges, keops_gauss_max, keops_gauss_min,
                       keops_laplace_sum, keops_gauss_sum, keops_gauss_sum_noalloc, keops_gauss_sum_ranges,
                       keops_kmin, keops_profile_read, keops_set_option, keops_version, lib, status_string)
+from .paged import keops_cache_append, keops_cache_evict, keops_paged_attention, keops_verify_draft  # noqa: F401

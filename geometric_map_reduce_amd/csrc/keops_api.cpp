@@ -13,6 +13,7 @@
 #include <mutex>
 #include <vector>
 
+#include "host.h"
 #include "keops_mi355x.h"
 #include "launch.h"
 
@@ -35,6 +36,8 @@ struct EventPair { hipEvent_t start, stop; };
 std::mutex g_prof_mu;
 std::vector<EventPair> g_prof_events;
 constexpr size_t kMaxProfiled = 4096;
+
+}  // namespace
 
 // Records the start event when profiling is on; returns the pair index or -1.
 int prof_begin(hipStream_t st) {
@@ -64,9 +67,13 @@ void prof_end(int idx, hipStream_t st) {
   if ((size_t)idx < g_prof_events.size()) (void)hipEventRecord(g_prof_events[idx].stop, st);
 }
 
+namespace {
+
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cu_count[kMaxDevices];
 std::once_flag g_pool_once[kMaxDevices];
+
+}  // namespace
 
 // Compute units of the current device (cached).  Also raises the release
 // threshold of the device's default memory pool once, so that stream-ordered
@@ -90,6 +97,8 @@ int device_setup(int *cus) {
   *cus = c;
   return KEOPS_OK;
 }
+
+namespace {
 
 // Address of this device's copy of `scratch`, looked up once per device with that
 // device current (each GPU holds its own copy at its own address).
@@ -124,6 +133,8 @@ struct Arena {
   size_t cap;
 };
 
+}  // namespace
+
 // ---- workspace cache
 // Each (device, stream, slot) keeps one grow-only device buffer, which the calls on
 // that stream reuse in stream order: after the first call of a given size a call
@@ -144,6 +155,8 @@ struct WsEntry {
   int busy;
   uint64_t tick;
 };
+
+namespace {
 std::mutex g_ws_mu;
 std::vector<std::unique_ptr<WsEntry>> g_ws;
 uint64_t g_ws_tick = 0;
@@ -166,108 +179,95 @@ void ws_trim_locked() {
   (void)hipGetLastError();
 }
 
-class Workspace {
- public:
-  Workspace() = default;
-  Workspace(const Workspace &) = delete;
-  Workspace &operator=(const Workspace &) = delete;
-  ~Workspace() { release(); }
+}  // namespace
 
-  // A device buffer of at least `bytes` for work enqueued on `st` (null for 0 bytes).
-  // Returns KEOPS_OK or KEOPS_ERR_ALLOC (nothing enqueued).
-  int acquire(hipStream_t st, int slot, size_t bytes) {
-    release();
-    if (bytes == 0) return KEOPS_OK;
-    if (g_opt_fail_alloc.load(std::memory_order_relaxed) == 1) return KEOPS_ERR_ALLOC;
-    bytes = (bytes + 255) / 256 * 256;
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) {
-      (void)hipGetLastError();
-      return KEOPS_ERR_ALLOC;
+int Workspace::acquire(hipStream_t st, int slot, size_t bytes) {
+  release();
+  if (bytes == 0) return KEOPS_OK;
+  if (g_opt_fail_alloc.load(std::memory_order_relaxed) == 1) return KEOPS_ERR_ALLOC;
+  bytes = (bytes + 255) / 256 * 256;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) {
+    (void)hipGetLastError();
+    return KEOPS_ERR_ALLOC;
+  }
+  if (g_opt_ws_cache.load(std::memory_order_relaxed) == 1) {
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    WsEntry *e = nullptr;
+    for (auto &u : g_ws)
+      if (u->dev == dev && u->st == st && u->slot == slot) { e = u.get(); break; }
+    if (!e && g_ws.size() >= kWsMaxEntries) {
+      // evict the least recently used idle buffer
+      size_t lru = g_ws.size();
+      for (size_t k = 0; k < g_ws.size(); ++k)
+        if (g_ws[k]->busy == 0 && (lru == g_ws.size() || g_ws[k]->tick < g_ws[lru]->tick)) lru = k;
+      if (lru < g_ws.size()) {
+        (void)hipSetDevice(g_ws[lru]->dev);
+        (void)hipFree(g_ws[lru]->ptr);
+        (void)hipSetDevice(dev);
+        g_ws.erase(g_ws.begin() + (ptrdiff_t)lru);
+      }
     }
-    if (g_opt_ws_cache.load(std::memory_order_relaxed) == 1) {
-      std::lock_guard<std::mutex> lk(g_ws_mu);
-      WsEntry *e = nullptr;
-      for (auto &u : g_ws)
-        if (u->dev == dev && u->st == st && u->slot == slot) { e = u.get(); break; }
-      if (!e && g_ws.size() >= kWsMaxEntries) {
-        // evict the least recently used idle buffer
-        size_t lru = g_ws.size();
-        for (size_t k = 0; k < g_ws.size(); ++k)
-          if (g_ws[k]->busy == 0 && (lru == g_ws.size() || g_ws[k]->tick < g_ws[lru]->tick)) lru = k;
-        if (lru < g_ws.size()) {
-          (void)hipSetDevice(g_ws[lru]->dev);
-          (void)hipFree(g_ws[lru]->ptr);
-          (void)hipSetDevice(dev);
-          g_ws.erase(g_ws.begin() + (ptrdiff_t)lru);
-        }
-      }
-      if (!e && g_ws.size() < kWsMaxEntries) {
-        g_ws.push_back(std::unique_ptr<WsEntry>(new WsEntry{dev, st, slot, nullptr, 0, 0, 0}));
-        e = g_ws.back().get();
-      }
-      if (e && e->busy == 0) {
-        if (e->cap < bytes) {
-          const size_t cap = std::max(bytes, (e->cap + e->cap / 4 + 255) / 256 * 256);
-          if (e->ptr) (void)hipFree(e->ptr);
+    if (!e && g_ws.size() < kWsMaxEntries) {
+      g_ws.push_back(std::unique_ptr<WsEntry>(new WsEntry{dev, st, slot, nullptr, 0, 0, 0}));
+      e = g_ws.back().get();
+    }
+    if (e && e->busy == 0) {
+      if (e->cap < bytes) {
+        const size_t cap = std::max(bytes, (e->cap + e->cap / 4 + 255) / 256 * 256);
+        if (e->ptr) (void)hipFree(e->ptr);
+        e->ptr = nullptr;
+        e->cap = 0;
+        if (hipMalloc((void **)&e->ptr, cap) != hipSuccess || !e->ptr) {
+          (void)hipGetLastError();
           e->ptr = nullptr;
-          e->cap = 0;
-          if (hipMalloc((void **)&e->ptr, cap) != hipSuccess || !e->ptr) {
-            (void)hipGetLastError();
-            e->ptr = nullptr;
-            // an empty entry is dropped again; the per-call allocation below may still fit
-            for (size_t k = 0; k < g_ws.size(); ++k)
-              if (g_ws[k].get() == e) { g_ws.erase(g_ws.begin() + (ptrdiff_t)k); break; }
-            e = nullptr;
-          } else {
-            e->cap = cap;
-          }
-        }
-        if (e) {
-          e->busy = 1;
-          e->tick = ++g_ws_tick;
-          entry_ = e;
-          ptr_ = e->ptr;
-          return KEOPS_OK;
+          // an empty entry is dropped again; the per-call allocation below may still fit
+          for (size_t k = 0; k < g_ws.size(); ++k)
+            if (g_ws[k].get() == e) { g_ws.erase(g_ws.begin() + (ptrdiff_t)k); break; }
+          e = nullptr;
+        } else {
+          e->cap = cap;
         }
       }
+      if (e) {
+        e->busy = 1;
+        e->tick = ++g_ws_tick;
+        entry_ = e;
+        ptr_ = e->ptr;
+        return KEOPS_OK;
+      }
     }
-    if (hipMallocAsync((void **)&ptr_, bytes, st) != hipSuccess || !ptr_) {
-      (void)hipGetLastError();
-      ptr_ = nullptr;
-      return KEOPS_ERR_ALLOC;
-    }
-    owned_ = true;
-    st_ = st;
-    return KEOPS_OK;
   }
-
-  char *ptr() const { return ptr_; }
-
- private:
-  void release() {
-    if (owned_ && ptr_) (void)hipFreeAsync(ptr_, st_);
-    if (entry_) {
-      std::lock_guard<std::mutex> lk(g_ws_mu);
-      entry_->busy = 0;
-      if (g_opt_ws_cache.load(std::memory_order_relaxed) != 1) ws_trim_locked();
-    }
+  if (hipMallocAsync((void **)&ptr_, bytes, st) != hipSuccess || !ptr_) {
+    (void)hipGetLastError();
     ptr_ = nullptr;
-    entry_ = nullptr;
-    owned_ = false;
+    return KEOPS_ERR_ALLOC;
   }
+  owned_ = true;
+  st_ = st;
+  return KEOPS_OK;
+}
 
-  char *ptr_ = nullptr;
-  hipStream_t st_ = nullptr;
-  WsEntry *entry_ = nullptr;
-  bool owned_ = false;
-};
+void Workspace::release() {
+  if (owned_ && ptr_) (void)hipFreeAsync(ptr_, st_);
+  if (entry_) {
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    entry_->busy = 0;
+    if (g_opt_ws_cache.load(std::memory_order_relaxed) != 1) ws_trim_locked();
+  }
+  ptr_ = nullptr;
+  entry_ = nullptr;
+  owned_ = false;
+}
+
 
 bool overlaps(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
   if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
   const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
   return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
+
+namespace {
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
@@ -374,7 +374,11 @@ Plan make_plan(int64_t M, int64_t N, int cus, int64_t rows_wide, int64_t rows_na
   return p;
 }
 
+}  // namespace
+
 int check_launch() { return hipGetLastError() == hipSuccess ? KEOPS_OK : KEOPS_ERR_HIP; }
+
+namespace {
 
 // Few rows, many j: lanes own j, rows sit in LDS (M <= kStreamMaxRows by default).
 // Work-groups along j: about kStreamWgsPerCu per CU over all row groups, between

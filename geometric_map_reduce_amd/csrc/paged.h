@@ -1,0 +1,218 @@
+// paged.h -- internal definitions of the paged key/value cache operators: the
+// launch arguments, slot addressing and the 16-bit / 8-bit element types.
+#pragma once
+
+#include "common.h"
+
+namespace kmi {
+
+enum CacheType : int { CT_BF16 = 0, CT_F16 = 1, CT_E4M3 = 2 };
+
+// n / d for n < 2^31: q = (n * mul) >> shift with mul = floor(2^(31+s) / d) + 1,
+// s = ceil(log2 d).  The excess of mul over the exact quotient is at most 1, so the
+// product is high by at most n / 2^(31+s) < 1/d, which never reaches the next whole number.
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+inline FastDiv make_fastdiv(uint32_t d) {
+  uint32_t s = 0;
+  while (((uint64_t)1 << s) < d) ++s;
+  return {(uint32_t)((((uint64_t)1 << (31 + s)) / d) + 1), 31 + s, d};
+}
+__device__ __forceinline__ uint32_t fast_div(const FastDiv &f, uint32_t n) {
+  return (uint32_t)(((uint64_t)n * f.mul) >> f.shift);
+}
+
+// The cache and the batch that uses it.  Strides are in bytes.
+struct CacheView {
+  char *k, *v;
+  float *weights;               // [pages][heads][page_size] or null
+  const float *k_scale, *v_scale;
+  int64_t page_stride, slot_stride, head_stride;
+  FastDiv page;                 // divides a slot number by the page size
+  uint32_t pages;
+  int32_t heads, dim;
+  const int32_t *table;         // [seqs][table_stride]
+  int64_t table_stride;
+  uint32_t table_width;
+  const int32_t *lens;
+  int32_t seqs;
+};
+
+// A slot's place: its page number and its row in it; page < 0 where the table has none
+// (past its width, or an entry outside [0, pages)): such a slot is treated as absent.
+struct SlotPlace {
+  int32_t page;
+  uint32_t row;
+};
+__device__ __forceinline__ SlotPlace slot_place(const CacheView &c, const int32_t *trow, uint32_t j) {
+  const uint32_t pi = fast_div(c.page, j);
+  int32_t pg = -1;
+  if (pi < c.table_width) pg = trow[pi];
+  if ((uint32_t)pg >= c.pages) pg = -1;
+  return {pg, j - pi * c.page.d};
+}
+__device__ __forceinline__ int64_t place_offset(const CacheView &c, SlotPlace p) {
+  return p.page < 0 ? -1 : (int64_t)p.page * c.page_stride + (int64_t)p.row * c.slot_stride;
+}
+
+// New tokens of a sequence: tokens t0 .. t0 + m of the batch, in slots first .. n of the
+// sequence's n slots.  Values outside the call's bounds are cut to them.
+struct SeqSpan {
+  int64_t t0;
+  int32_t m, n, first;
+};
+__device__ __forceinline__ SeqSpan seq_span(const int32_t *starts, const int32_t *lens, int s, int64_t tokens,
+                                            int32_t max_q, int32_t max_len) {
+  int64_t a = starts[s], b = starts[s + 1];
+  a = a < 0 ? 0 : (a > tokens ? tokens : a);
+  b = b < a ? a : (b > tokens ? tokens : b);
+  const int32_t cnt = (int32_t)(b - a);
+  int32_t n = lens[s];
+  n = n < 0 ? 0 : n;
+  SeqSpan r;
+  r.t0 = a;
+  r.first = n - cnt;
+  r.m = cnt < max_q ? cnt : max_q;
+  r.n = n < max_len ? n : max_len;
+  return r;
+}
+
+struct AppendArgs {
+  CacheView c;
+  const char *k, *v;
+  int64_t k_stride, v_stride;   // bytes from token to token
+  const int32_t *starts;
+  int64_t tokens;
+};
+
+struct AttendArgs {
+  CacheView c;
+  const char *q;
+  int64_t q_stride;             // bytes from token to token
+  const int32_t *starts;
+  int64_t tokens;
+  int32_t group;                // query heads that share a key/value head
+  FastDiv gdiv;
+  int32_t max_q, max_len, window;
+  float scale_log2;             // score scale * log2(e)
+  float decay;
+  char *out;                    // [tokens][heads * group][dim]
+  float *lse;                   // [tokens][heads * group]
+  // split over the slots: partials [nsplit][tokens][heads * group]
+  int32_t nsplit, chunk;
+  float *part_o;                // [..][dim], each divided by nothing: sums under the partial maximum
+  float2 *part_ml;              // (maximum in log2 units, sum)
+  // few-rows form with weights: scores [seqs * heads][rows][score_stride] in log2 units
+  float *scores;
+  int64_t score_stride;
+  int32_t score_rows;
+  // many-rows weights: partial sums [nrow][seqs * heads][max_len]
+  int32_t nrow;
+  float *part_w;
+};
+
+struct EvictArgs {
+  CacheView c;
+  int itemsize;
+  const int32_t *new_table;
+  int64_t new_stride;
+  uint32_t new_width;
+  int32_t budget, sink, recent;
+  int32_t *kept, *new_lens;
+};
+
+struct VerifyArgs {
+  const float *target, *draft;
+  const int32_t *tokens, *counts;
+  const float *u_accept, *u_sample;
+  int32_t seqs, drafts, vocab;
+  int32_t *out, *accepted;
+};
+
+// ---------------------------------------------------------------- launches
+void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st);
+// Variants exist for dim 64, 96, 128 and 256; the API checks before it calls.
+constexpr int kFewRowsMax = 32;      // rows (new tokens x group) of the few-rows form
+constexpr int kManyRowsTile = 128;   // rows of a work-group of the many-rows form
+constexpr int kSumSlotsTile = 128;   // slots of a work-group of the column sums
+void launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, dim3 grid, hipStream_t st);
+void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
+void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
+void launch_attend_join(const AttendArgs &a, int type, hipStream_t st);
+void launch_attend_score_sums(const AttendArgs &a, hipStream_t st);
+void launch_attend_sums_join(const AttendArgs &a, hipStream_t st);
+int launch_evict(const EvictArgs &a, hipStream_t st);
+void launch_verify(const VerifyArgs &a, hipStream_t st);
+
+// ---------------------------------------------------------------- element types
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+struct Bf16 {
+  static constexpr uint32_t kExp = 0x7f807f80u;   // exponent bits of a pair
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  // two floats to a pair, to nearest even
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, bf16x2));
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  // two of four e4m3 values to a pair (exact)
+  template <bool HI>
+  static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+  }
+};
+struct F16 {
+  static constexpr uint32_t kExp = 0x7c007c00u;
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x, y}, f16x2));
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w).x; }
+  static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w).y; }
+  template <bool HI>
+  static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+  }
+};
+
+// True where either 16-bit half of w is an infinity or a NaN.
+template <class T>
+__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
+  const uint32_t e = w & T::kExp;
+  return (e & 0xffffu) == (T::kExp & 0xffffu) || (e >> 16) == (T::kExp >> 16);
+}
+
+template <class T>
+__device__ __forceinline__ u32x4 widen_e4m3(u32x2 w) {
+  return (u32x4){T::template from_e4m3<false>(w.x), T::template from_e4m3<true>(w.x),
+                 T::template from_e4m3<false>(w.y), T::template from_e4m3<true>(w.y)};
+}
+
+// Zeros where `keep` is false.
+__device__ __forceinline__ u32x4 keep_if(u32x4 v, bool keep) {
+  const uint32_t m = keep ? 0xffffffffu : 0u;
+  return v & (u32x4){m, m, m, m};
+}
+
+}  // namespace kmi

@@ -1,0 +1,408 @@
+// paged_api.cpp -- the C ABI of the paged key/value cache and of draft verification:
+// argument validation, launch plans and workspace.  No HIP call is made before the
+// arguments are validated, and no exception leaves an entry point.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "host.h"
+#include "keops_mi355x.h"
+#include "paged.h"
+
+namespace kmi {
+namespace {
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr double kMaxWorkspace = 1.0e14;    // more than any device holds; below the 64-bit limit
+// Work-groups that a launch aims for, per compute unit, when it splits a long axis.
+constexpr int64_t kFewWgsPerCu = 4;
+constexpr int64_t kManyWgsPerCu = 2;
+constexpr int64_t kSumsWgsPerCu = 2;
+constexpr int kFewChunk = 128;              // least slots of a split: one tile for each wave
+
+bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+int64_t width_of(int type) { return type == KEOPS_TYPE_E4M3 ? 1 : 2; }
+
+// Bytes from the first to past the last element of the pages.
+int64_t pages_extent(const keops_cache_t &c) {
+  if (c.pages == 0) return 0;
+  const int64_t w = width_of(c.type);
+  return ((c.pages - 1) * c.page_stride + (int64_t)(c.page_size - 1) * c.slot_stride + (c.heads - 1) * c.head_stride + c.dim) * w;
+}
+int64_t weights_extent(const keops_cache_t &c) { return c.weights ? c.pages * c.heads * (int64_t)c.page_size * 4 : 0; }
+
+int check_cache(const keops_cache_t *c, bool scales = true) {
+  if (!c) return KEOPS_ERR_INVALID_ARG;
+  if (c->pages < 0 || c->page_size < 1 || c->heads < 1 || c->dim < 1 || c->seqs < 0 || c->table_width < 0 ||
+      c->table_stride < 0)
+    return KEOPS_ERR_INVALID_ARG;
+  if (c->type != KEOPS_TYPE_BF16 && c->type != KEOPS_TYPE_F16 && c->type != KEOPS_TYPE_E4M3) return KEOPS_ERR_INVALID_ARG;
+  if (scales && c->type == KEOPS_TYPE_E4M3 && (!c->k_scale || !c->v_scale)) return KEOPS_ERR_INVALID_ARG;
+  if (c->pages > 0 && (!c->k_pages || !c->v_pages)) return KEOPS_ERR_INVALID_ARG;
+  const int64_t w = width_of(c->type);
+  for (int64_t st : {c->page_stride, c->slot_stride, c->head_stride})
+    if (st < 0 || st > (int64_t)1 << 48 || st * w % 16) return KEOPS_ERR_INVALID_ARG;
+  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return KEOPS_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)c->weights, (const void *)c->k_scale, (const void *)c->v_scale,
+                        (const void *)c->page_table, (const void *)c->lens})
+    if (!aligned(p, 4)) return KEOPS_ERR_INVALID_ARG;
+  if (c->seqs > 0 && (!c->lens || (c->table_width > 0 && !c->page_table))) return KEOPS_ERR_INVALID_ARG;
+  if (c->dim != 64 && c->dim != 96 && c->dim != 128 && c->dim != 256) return KEOPS_ERR_UNSUPPORTED;
+  if (c->pages > 0x7fffffff || c->heads > 65535) return KEOPS_ERR_UNSUPPORTED;
+  return KEOPS_OK;
+}
+
+CacheView view_of(const keops_cache_t &c) {
+  const int64_t w = width_of(c.type);
+  CacheView v{};
+  v.k = (char *)c.k_pages;
+  v.v = (char *)c.v_pages;
+  v.weights = c.weights;
+  v.k_scale = c.k_scale;
+  v.v_scale = c.v_scale;
+  v.page_stride = c.page_stride * w;
+  v.slot_stride = c.slot_stride * w;
+  v.head_stride = c.head_stride * w;
+  v.page = make_fastdiv((uint32_t)c.page_size);
+  v.pages = (uint32_t)c.pages;
+  v.heads = c.heads;
+  v.dim = c.dim;
+  v.table = c.page_table;
+  v.table_stride = c.table_stride;
+  v.table_width = (uint32_t)c.table_width;
+  v.lens = c.lens;
+  v.seqs = c.seqs;
+  return v;
+}
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Launch plan of one attention call.
+struct AttendPlan {
+  bool few, scores;
+  int row_tiles, score_rows;
+  int64_t nsplit, chunk, nrow, grid, sums_grid, score_stride;
+  int64_t ml_bytes, o_bytes, score_bytes, sums_bytes;
+  int64_t total() const { return ml_bytes + o_bytes + score_bytes + sums_bytes; }
+};
+
+int plan_attend(const keops_cache_t &c, int64_t tokens, int heads, int64_t max_q, int64_t max_len, int window, int cus,
+                AttendPlan *p) {
+  *p = AttendPlan{};
+  const int64_t G = heads / c.heads, rows = max_q * G, S = c.seqs, H = c.heads;
+  p->few = rows <= kFewRowsMax;
+  // slots that the rows of one sequence see at most
+  int64_t span = max_len;
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + max_q - 1);
+  if (p->few) {
+    p->row_tiles = rows <= 16 ? 1 : 2;
+    const int64_t from_tile = std::min<int64_t>(max_len, span + 31);    // a window starts inside a tile
+    p->chunk = std::max<int64_t>(kFewChunk, ceil_div(ceil_div(from_tile * S * H, kFewWgsPerCu * cus), kFewChunk) * kFewChunk);
+    p->nsplit = std::max<int64_t>(1, ceil_div(from_tile, p->chunk));
+    if ((double)S * (double)H * (double)p->nsplit > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+    p->grid = S * H * p->nsplit;
+  } else {
+    const int64_t nrt = ceil_div(rows, kManyRowsTile);
+    if ((double)S * (double)H * (double)nrt > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
+    const int64_t wgs = S * H * nrt;
+    // at least four tiles of slots a split
+    p->nsplit = std::max<int64_t>(1, std::min(ceil_div(kManyWgsPerCu * cus, wgs), span / 256));
+    p->grid = wgs * p->nsplit;
+  }
+  if (c.weights) {
+    // keeping a row's scores costs 8 bytes a slot, reading K again dim times its width
+    p->scores = p->few && rows * 8 <= c.dim * width_of(c.type);
+    if (p->scores) {
+      p->score_rows = (int)rows;
+      p->score_stride = ceil_div(max_len, 32) * 32;
+      if (4.0 * (double)S * (double)H * (double)rows * (double)p->score_stride > kMaxWorkspace) return KEOPS_ERR_ALLOC;
+      p->score_bytes = align256(4 * S * H * rows * p->score_stride);
+      if ((double)S * (double)H * (double)ceil_div(max_len, 256) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+    } else {
+      const int64_t nst = ceil_div(max_len, kSumSlotsTile);
+      if ((double)S * (double)H * (double)nst > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
+      const int64_t wgs = S * H * nst;
+      p->nrow = std::max<int64_t>(1, std::min(ceil_div(kSumsWgsPerCu * cus, std::max<int64_t>(wgs, 1)), rows / 256));
+      p->sums_grid = wgs * p->nrow;
+      if (p->nrow > 1) {
+        if (4.0 * (double)p->nrow * (double)S * (double)H * (double)max_len > kMaxWorkspace) return KEOPS_ERR_ALLOC;
+        p->sums_bytes = align256(4 * p->nrow * S * H * max_len);
+      }
+    }
+  }
+  if (p->nsplit > 1) {
+    const double out_rows = (double)tokens * heads * (double)p->nsplit;
+    if (out_rows * c.dim * 4.0 > kMaxWorkspace) return KEOPS_ERR_ALLOC;
+    if ((double)tokens * heads > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+    p->ml_bytes = align256(p->nsplit * tokens * heads * 8);
+    p->o_bytes = align256(p->nsplit * tokens * heads * c.dim * 4);
+  }
+  return KEOPS_OK;
+}
+
+int check_attend(const keops_cache_t *c, int type, int64_t tokens, int heads, int max_q, int max_len, float scale,
+                 int window, float decay) {
+  if (int rc = check_cache(c)) return rc;
+  if (type != KEOPS_TYPE_BF16 && type != KEOPS_TYPE_F16) return KEOPS_ERR_INVALID_ARG;
+  if (c->type != KEOPS_TYPE_E4M3 && c->type != type) return KEOPS_ERR_INVALID_ARG;
+  if (tokens < 0 || heads < 1 || heads % c->heads || max_q < 0 || max_len < 0 || window < 0) return KEOPS_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(decay)) return KEOPS_ERR_INVALID_ARG;
+  if (tokens > 0x7fffffff || heads > 65535 || (int64_t)max_q * (heads / c->heads) > 0x3fffffff ||
+      max_len > 0x7fffffff - 4096)
+    return KEOPS_ERR_UNSUPPORTED;
+  return KEOPS_OK;
+}
+
+// The caller's workspace, or the library's; the library's is never recorded into a graph,
+// whose replays could outlive it.
+int take_workspace(Workspace &own, void *given, int64_t given_bytes, int64_t need, hipStream_t st, char **ptr) {
+  *ptr = nullptr;
+  if (need == 0) return KEOPS_OK;
+  if (given) {
+    if (given_bytes < need) return KEOPS_ERR_SCRATCH;
+    *ptr = (char *)given;
+    return KEOPS_OK;
+  }
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(st, &cap) != hipSuccess) {
+    (void)hipGetLastError();
+    return KEOPS_ERR_HIP;
+  }
+  if (cap != hipStreamCaptureStatusNone) return KEOPS_ERR_ALLOC;
+  if (int rc = own.acquire(st, 0, (size_t)need)) return rc;
+  *ptr = own.ptr();
+  return KEOPS_OK;
+}
+
+int append_entry(const keops_cache_t *c, const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type,
+                 const int32_t *starts, int64_t tokens, hipStream_t st) {
+  if (int rc = check_cache(c)) return rc;
+  if (type != KEOPS_TYPE_BF16 && type != KEOPS_TYPE_F16) return KEOPS_ERR_INVALID_ARG;
+  if (c->type != KEOPS_TYPE_E4M3 && c->type != type) return KEOPS_ERR_INVALID_ARG;
+  if (tokens < 0) return KEOPS_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)c->heads * c->dim;
+  if (tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16) || k_stride * 2 % 16 || v_stride * 2 % 16 ||
+                     k_stride < 0 || v_stride < 0 || k_stride > (int64_t)1 << 40 || v_stride > (int64_t)1 << 40))
+    return KEOPS_ERR_INVALID_ARG;
+  if (tokens > 0 && c->seqs > 0 && (!starts || !aligned(starts, 4))) return KEOPS_ERR_INVALID_ARG;
+  if (tokens > 0x7fffffff || (double)tokens * (double)(row / 8) > 256.0 * (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+  if (tokens > 0) {
+    const int64_t kb = ((tokens - 1) * k_stride + row) * 2, vb = ((tokens - 1) * v_stride + row) * 2;
+    const int64_t pb = pages_extent(*c);
+    for (const void *p : {(const void *)c->k_pages, (const void *)c->v_pages})
+      if (overlaps(p, pb, k, kb) || overlaps(p, pb, v, vb)) return KEOPS_ERR_INVALID_ARG;
+  }
+  if (tokens == 0 || c->seqs == 0 || c->pages == 0 || c->table_width == 0) return KEOPS_OK;
+  (void)hipGetLastError();
+  AppendArgs a{};
+  a.c = view_of(*c);
+  a.k = (const char *)k;
+  a.v = (const char *)v;
+  a.k_stride = k_stride * 2;
+  a.v_stride = v_stride * 2;
+  a.starts = starts;
+  a.tokens = tokens;
+  launch_append(a, type, c->type, st);
+  return check_launch();
+}
+
+int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int type, int heads, const int32_t *starts,
+                 int64_t tokens, int max_q, int max_len, float scale, int window, float decay, void *out, float *lse,
+                 void *workspace, int64_t workspace_bytes, hipStream_t st) {
+  if (int rc = check_attend(c, type, tokens, heads, max_q, max_len, scale, window, decay)) return rc;
+  const int64_t row = (int64_t)heads * c->dim;
+  if (tokens > 0) {
+    if (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || q_stride < 0 ||
+        q_stride * 2 % 16 || q_stride > (int64_t)1 << 40)
+      return KEOPS_ERR_INVALID_ARG;
+    if (c->seqs > 0 && (!starts || !aligned(starts, 4))) return KEOPS_ERR_INVALID_ARG;
+    const int64_t ob = tokens * row * 2, lb = tokens * heads * 4, qb = ((tokens - 1) * q_stride + row) * 2;
+    const int64_t pb = pages_extent(*c), wb = weights_extent(*c);
+    if (overlaps(out, ob, q, qb) || overlaps(out, ob, lse, lb) || overlaps(lse, lb, q, qb) ||
+        overlaps(out, ob, c->k_pages, pb) || overlaps(out, ob, c->v_pages, pb) || overlaps(out, ob, c->weights, wb) ||
+        overlaps(lse, lb, c->weights, wb) || overlaps(lse, lb, c->k_pages, pb) || overlaps(lse, lb, c->v_pages, pb))
+      return KEOPS_ERR_INVALID_ARG;
+  }
+  if (workspace && (!aligned(workspace, 256) || workspace_bytes < 0)) return KEOPS_ERR_INVALID_ARG;
+  if (tokens == 0 || c->seqs == 0 || max_q == 0) return KEOPS_OK;
+  if (c->pages == 0) return KEOPS_ERR_INVALID_ARG;    // nothing to address
+  (void)hipGetLastError();
+  int cus = 0;
+  if (int rc = device_setup(&cus)) return rc;
+  AttendPlan p;
+  if (int rc = plan_attend(*c, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
+  Workspace own;
+  char *ws = nullptr;
+  if (int rc = take_workspace(own, workspace, workspace_bytes, p.total(), st, &ws)) return rc;
+
+  AttendArgs a{};
+  a.c = view_of(*c);
+  a.q = (const char *)q;
+  a.q_stride = q_stride * 2;
+  a.starts = starts;
+  a.tokens = tokens;
+  a.group = heads / c->heads;
+  a.gdiv = make_fastdiv((uint32_t)a.group);
+  a.max_q = max_q;
+  a.max_len = max_len;
+  a.window = window;
+  a.scale_log2 = scale * kLog2e;
+  a.decay = decay;
+  a.out = (char *)out;
+  a.lse = lse;
+  a.nsplit = (int32_t)p.nsplit;
+  a.chunk = (int32_t)p.chunk;
+  a.part_ml = (float2 *)ws;
+  a.part_o = (float *)(ws + p.ml_bytes);
+  a.scores = p.scores ? (float *)(ws + p.ml_bytes + p.o_bytes) : nullptr;
+  a.score_stride = p.score_stride;
+  a.score_rows = p.score_rows;
+  a.nrow = (int32_t)std::max<int64_t>(1, p.nrow);
+  a.part_w = (float *)(ws + p.ml_bytes + p.o_bytes + p.score_bytes);
+  const bool e4m3 = c->type == KEOPS_TYPE_E4M3;
+  const int prof = prof_begin(st);
+  if (p.few) launch_attend_few(a, type, e4m3, c->dim, p.row_tiles, dim3((unsigned)p.grid), st);
+  else launch_attend_many(a, type, e4m3, c->dim, dim3((unsigned)p.grid), st);
+  prof_end(prof, st);
+  if (p.nsplit > 1) launch_attend_join(a, type, st);
+  if (c->weights && max_len > 0) {
+    if (p.scores) {
+      launch_attend_score_sums(a, st);
+    } else {
+      launch_attend_sums(a, type, e4m3, c->dim, dim3((unsigned)p.sums_grid), st);
+      if (p.nrow > 1) launch_attend_sums_join(a, st);
+    }
+  }
+  return check_launch();
+}
+
+int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_stride, int new_width, int budget,
+                int sink, int recent, int32_t *kept, int32_t *new_lens, hipStream_t st) {
+  if (int rc = check_cache(c, false)) return rc;   // the move copies held values
+  if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget || new_width < 0 || new_stride < 0)
+    return KEOPS_ERR_INVALID_ARG;
+  if (c->seqs > 0) {
+    if (!c->weights || !kept || !new_lens || !aligned(kept, 4) || !aligned(new_lens, 4)) return KEOPS_ERR_INVALID_ARG;
+    if (new_width > 0 && (!new_table || !aligned(new_table, 4))) return KEOPS_ERR_INVALID_ARG;
+    // every kept slot has a place in the new table
+    if (new_width < std::min<int64_t>(ceil_div(budget, c->page_size), c->table_width)) return KEOPS_ERR_INVALID_ARG;
+    const int64_t kb = (int64_t)c->seqs * c->heads * budget * 4, nb = (int64_t)c->seqs * 4;
+    const int64_t pb = pages_extent(*c), wb = weights_extent(*c);
+    if (overlaps(kept, kb, new_lens, nb) || overlaps(kept, kb, c->lens, nb) || overlaps(new_lens, nb, c->lens, nb) ||
+        overlaps(kept, kb, c->weights, wb) || overlaps(kept, kb, c->k_pages, pb) || overlaps(kept, kb, c->v_pages, pb))
+      return KEOPS_ERR_INVALID_ARG;
+  }
+  if ((double)c->seqs * c->heads * (double)budget * (c->dim * width_of(c->type) / 16) > 256.0 * (double)kMaxGrid ||
+      (double)c->table_width * (double)c->page_size > (double)0x7fffffff)
+    return KEOPS_ERR_UNSUPPORTED;
+  if (c->seqs == 0) return KEOPS_OK;
+  (void)hipGetLastError();
+  EvictArgs a{};
+  a.c = view_of(*c);
+  a.itemsize = (int)width_of(c->type);
+  a.new_table = new_table;
+  a.new_stride = new_stride;
+  a.new_width = (uint32_t)new_width;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  if (launch_evict(a, st)) {
+    (void)hipGetLastError();
+    return KEOPS_ERR_HIP;
+  }
+  return check_launch();
+}
+
+int verify_entry(const VerifyArgs &a, hipStream_t st) {
+  if (a.seqs < 0 || a.drafts < 0 || a.vocab < 1) return KEOPS_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)a.target, (const void *)a.draft, (const void *)a.tokens, (const void *)a.counts,
+                        (const void *)a.u_accept, (const void *)a.u_sample, (const void *)a.out, (const void *)a.accepted})
+    if (!aligned(p, 4)) return KEOPS_ERR_INVALID_ARG;
+  if (a.seqs == 0) return KEOPS_OK;
+  if (!a.target || !a.counts || !a.u_sample || !a.out || !a.accepted) return KEOPS_ERR_INVALID_ARG;
+  if (a.drafts > 0 && (!a.tokens || !a.u_accept)) return KEOPS_ERR_INVALID_ARG;
+  if (a.drafts > 1 << 20 || a.vocab > 1 << 30) return KEOPS_ERR_UNSUPPORTED;
+  const int64_t ob = (int64_t)a.seqs * (a.drafts + 1) * 4, ab = (int64_t)a.seqs * 4, tb = ob * a.vocab;
+  if (overlaps(a.out, ob, a.accepted, ab) || overlaps(a.out, ob, a.tokens, (int64_t)a.seqs * a.drafts * 4) ||
+      overlaps(a.out, ob, a.target, tb) || overlaps(a.out, ob, a.counts, ab) || overlaps(a.accepted, ab, a.counts, ab) ||
+      overlaps(a.accepted, ab, a.target, tb) || overlaps(a.out, ob, a.u_accept, (int64_t)a.seqs * a.drafts * 4) ||
+      overlaps(a.out, ob, a.u_sample, ab) || overlaps(a.accepted, ab, a.u_sample, ab))
+    return KEOPS_ERR_INVALID_ARG;
+  (void)hipGetLastError();
+  launch_verify(a, st);
+  return check_launch();
+}
+
+}  // namespace
+}  // namespace kmi
+
+using namespace kmi;
+
+extern "C" {
+
+int keops_cache_append(const keops_cache_t *cache, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                       int32_t type, const int32_t *starts, int64_t tokens, void *stream) {
+  try {
+    return append_entry(cache, k, v, k_stride, v_stride, type, starts, tokens, (hipStream_t)stream);
+  } catch (...) {
+    return KEOPS_ERR_ALLOC;
+  }
+}
+
+int keops_paged_attention(const keops_cache_t *cache, const void *q, int64_t q_stride, int32_t type, int32_t heads,
+                          const int32_t *starts, int64_t tokens, int32_t max_q, int32_t max_len, float scale,
+                          int32_t window, float decay, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+                          void *stream) {
+  try {
+    return attend_entry(cache, q, q_stride, type, heads, starts, tokens, max_q, max_len, scale, window, decay, out, lse,
+                        workspace, workspace_bytes, (hipStream_t)stream);
+  } catch (...) {
+    return KEOPS_ERR_ALLOC;
+  }
+}
+
+int keops_paged_attention_workspace(const keops_cache_t *cache, int32_t type, int32_t heads, int64_t tokens,
+                                    int32_t max_q, int32_t max_len, int32_t window, int64_t *bytes) {
+  try {
+    if (!bytes) return KEOPS_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (int rc = check_attend(cache, type, tokens, heads, max_q, max_len, 1.0f, window, 0.0f)) return rc;
+    if (tokens == 0 || cache->seqs == 0 || max_q == 0) return KEOPS_OK;
+    int cus = 0;
+    if (int rc = device_setup(&cus)) return rc;
+    AttendPlan p;
+    if (int rc = plan_attend(*cache, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
+    *bytes = p.total();
+    return KEOPS_OK;
+  } catch (...) {
+    return KEOPS_ERR_ALLOC;
+  }
+}
+
+int keops_cache_evict(const keops_cache_t *cache, const int32_t *new_table, int64_t new_stride, int32_t new_width,
+                      int32_t budget, int32_t sink, int32_t recent, int32_t *kept, int32_t *new_lens, void *stream) {
+  try {
+    return evict_entry(cache, new_table, new_stride, new_width, budget, sink, recent, kept, new_lens, (hipStream_t)stream);
+  } catch (...) {
+    return KEOPS_ERR_ALLOC;
+  }
+}
+
+int keops_verify_draft(const float *target, const float *draft, const int32_t *tokens, const int32_t *counts,
+                       const float *u_accept, const float *u_sample, int32_t seqs, int32_t drafts, int32_t vocab,
+                       int32_t *out, int32_t *accepted, void *stream) {
+  try {
+    return verify_entry({target, draft, tokens, counts, u_accept, u_sample, seqs, drafts, vocab, out, accepted},
+                        (hipStream_t)stream);
+  } catch (...) {
+    return KEOPS_ERR_ALLOC;
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,458 @@
+// paged_few.h -- attention of few rows over a paged cache (one to a few new tokens a sequence).
+//
+//   out[t, g] = sum_j p_j v_j,   p_j = exp(z_j - lse),  z_j = scale <q[t, g], k_j>,
+//   over the slots j that token t sees: j <= its own slot, and j > its slot - window.
+//
+// The rows of a key/value head are its `group` query heads times the sequence's new tokens; up to
+// 32 of them share one pass over the head's slots, so the cache is read once and HBM bounds it.
+// A work-group takes one chunk of slots of one (sequence, head); its four waves take every
+// fourth tile of 32 slots.
+//
+//  * No LDS between HBM and the matrix instructions.  With S^T = K Q^T the A operand is rows of K
+//    as they lie in memory, and the result leaves lane l with row l % 16 and slots 4 (l / 16) + r
+//    of each 16.  Counting a tile's 32 slots in that order makes the packed p the B operand of
+//    O^T = V^T P^T as it stands.  V^T wants eight slots of one column in a lane: each lane loads
+//    the same few columns of its eight slots and swaps halves of registers (v_perm).
+//  * K of the next tile is loaded once S is formed and V of the next once O is updated, into the
+//    registers just read: each wave keeps about a tile's bytes in flight at all times.
+//  * The running maximum moves only when a score passes it by 2^8 (one branch per tile), so the
+//    sums and p stay below 2^8 times what they would be; sums are in 32 bits, p is rounded to
+//    the cache's 16-bit type for the matrix product (8-bit caches: q's type).
+//  * Slots that no row may see (past the length, of a page that the table lacks) get a zero V.
+//    Slots that some rows see and others do not are only in the tiles of the new tokens and at
+//    the window's edge; if such a tile holds an infinity or NaN in V, it is added slot by slot,
+//    to the rows that see it (0 times infinity would reach the others).
+#pragma once
+
+#include "paged.h"
+
+namespace kmi {
+
+constexpr int kFewWaves = 4;
+constexpr int kFewThreads = kFewWaves * kWave;
+constexpr int kFewTile = 32;       // slots of a wave's tile
+constexpr int kFewBlock = 1024;    // slots whose addresses are held in LDS at a time
+constexpr float kLazy = 8.0f;      // log2 of what a score may pass the running maximum by
+
+// V columns of a lane: pieces of W consecutive columns, column base + (l % 16) W + t.
+template <int D> struct VPieces;
+template <> struct VPieces<64> { static constexpr int n = 1; static constexpr int w[2] = {4, 0}; };
+template <> struct VPieces<96> { static constexpr int n = 2; static constexpr int w[2] = {4, 2}; };
+template <> struct VPieces<128> { static constexpr int n = 1; static constexpr int w[2] = {8, 0}; };
+template <> struct VPieces<256> { static constexpr int n = 2; static constexpr int w[2] = {8, 8}; };
+
+__device__ __forceinline__ float xor_max(float v) {   // over the four lanes of a row
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float xor_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+template <class T, bool E4M3, int D, int NR>
+struct FewRows {
+  static constexpr int kBytes = E4M3 ? 1 : 2;
+  static constexpr int kSteps = D / 32;                 // matrix steps along the head dimension
+  static constexpr int kTiles = D / 16;                 // 16-column tiles of O^T
+  static constexpr int kKRegs = (E4M3 ? 2 : 4) * kSteps;
+  static constexpr int kVRegs = D / 16 * kBytes / 4 > 0 ? (D / 16 * kBytes + 3) / 4 : 1;   // registers of a slot's columns
+  static constexpr int kPad = D + 4;                    // floats of a row in LDS: rows four banks apart
+
+  uint32_t kr[2][kKRegs];
+  uint32_t vr[8][kVRegs];
+
+  // K rows of the tile: lane l has slot l % 16 of each 16, columns 32 s + 8 (l / 16) ..+8.
+  __device__ __forceinline__ void load_k(const char *base, const int64_t *off, int at) {
+    const int lane = threadIdx.x & (kWave - 1), row = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      int64_t o = off[at + 16 * t + row];
+      o = o < 0 ? 0 : o;
+      const char *p = base + o + q * 8 * kBytes;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (E4M3) {
+          const u32x2 w = *(const u32x2 *)(p + s * 32);
+          kr[t][2 * s] = w.x;
+          kr[t][2 * s + 1] = w.y;
+        } else {
+          const u32x4 w = *(const u32x4 *)(p + s * 64);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) kr[t][4 * s + u] = w[u];
+        }
+      }
+    }
+  }
+
+  // V: lane l has slots 4 (l / 16) + i of the first 16 (i < 4) and of the second (i >= 4).
+  __device__ __forceinline__ void load_v(const char *base, const int64_t *off, int at) {
+    const int lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int64_t o = off[at + (i >> 2) * 16 + q * 4 + (i & 3)];
+      o = o < 0 ? 0 : o;
+      const char *p = base + o;
+      int reg = 0, col = 0;
+#pragma unroll
+      for (int n = 0; n < VPieces<D>::n; ++n) {
+        const int w = VPieces<D>::w[n], b = w * kBytes;
+        const char *e = p + (col + c * w) * kBytes;
+        if (b == 16) {
+          const u32x4 x = *(const u32x4 *)e;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) vr[i][(reg + u) % kVRegs] = x[u];
+          reg += 4;
+        } else if (b == 8) {
+          const u32x2 x = *(const u32x2 *)e;
+          vr[i][reg % kVRegs] = x.x;
+          vr[i][(reg + 1) % kVRegs] = x.y;
+          reg += 2;
+        } else if (b == 4) {
+          vr[i][reg % kVRegs] = *(const uint32_t *)e;
+          reg += 1;
+        } else {
+          vr[i][reg % kVRegs] = *(const uint16_t *)e;
+          reg += 1;
+        }
+        col += 16 * w;
+      }
+    }
+  }
+
+  __device__ __forceinline__ u32x4 k_frag(int t, int s) const {
+    if (E4M3) return widen_e4m3<T>((u32x2){kr[t][2 * s], kr[t][2 * s + 1]});
+    return (u32x4){kr[t][4 * s], kr[t][4 * s + 1], kr[t][4 * s + 2], kr[t][4 * s + 3]};
+  }
+
+  // Columns 2 m and 2 m + 1 of slot i's W columns of piece n, as a 16-bit pair.
+  __device__ __forceinline__ uint32_t v_pair(int i, int n, int m) const {
+    if (!E4M3) return vr[i][(n ? VPieces<D>::w[0] / 2 : 0) + m];
+    const int at = (n ? VPieces<D>::w[0] : 0) + 2 * m;    // first of the two bytes
+    const uint32_t w = vr[i][at / 4];
+    return (at & 2) ? T::template from_e4m3<true>(w) : T::template from_e4m3<false>(w);
+  }
+
+  // A operands of column tiles 2 m and 2 m + 1 of piece n: one column of the lane's eight slots.
+  __device__ __forceinline__ void v_frags(int n, int m, u32x4 &lo, u32x4 &hi) const {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t x = v_pair(2 * u, n, m), y = v_pair(2 * u + 1, n, m);
+      lo[u] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+      hi[u] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+    }
+  }
+};
+
+template <class T, bool E4M3, int D, int NR, bool SCORES>
+__global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_few_kernel(AttendArgs a) {
+  using F = FewRows<T, E4M3, D, NR>;
+  constexpr int kRows = 16 * NR;
+  constexpr int kHalfRows = 2 * kRows;     // two waves' rows
+  __shared__ union {
+    int64_t off[kFewBlock];
+    float o[kHalfRows * F::kPad];
+  } sh;
+  __shared__ float sh_m[2][kRows], sh_l[2][kRows];
+
+  const int H = a.c.heads, G = a.group;
+  int b = blockIdx.x;
+  const int h = b % H;
+  b /= H;
+  const int split = b % a.nsplit, s = b / a.nsplit;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, col = lane & 15, q4 = lane >> 4;
+
+  const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
+  const int R = sp.m * G;
+  if (R == 0) return;
+  // slots any row sees: [lo, hi)
+  int lo = 0;
+  if (a.window > 0 && sp.first - a.window + 1 > 0) lo = sp.first - a.window + 1;
+  const int hi = sp.n < sp.first + sp.m ? sp.n : sp.first + sp.m;
+  const int64_t c0 = (int64_t)(lo & ~(kFewTile - 1)) + (int64_t)split * a.chunk;
+  const int c1 = c0 + a.chunk < hi ? (int)(c0 + a.chunk) : hi;
+
+  // rows of this lane: r = 16 nr + col, its token's slot (a padding row sees nothing)
+  int pos[NR];
+  u32x4 qf[NR][F::kSteps];
+  const int64_t heads = (int64_t)H * G;
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr) {
+    const int r = 16 * nr + col;
+    const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
+    pos[nr] = r < R ? sp.first + tok : -1;
+    const char *qp = a.q + (sp.t0 + tok) * a.q_stride + ((int64_t)(h * G + g) * D + q4 * 8) * 2;
+#pragma unroll
+    for (int st = 0; st < F::kSteps; ++st) qf[nr][st] = r < R ? *(const u32x4 *)(qp + st * 64) : (u32x4){0, 0, 0, 0};
+  }
+
+  float m_run[NR], l_run[NR];
+  f32x4 acc[NR][F::kTiles];
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr) {
+    m_run[nr] = -INFINITY;
+    l_run[nr] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < F::kTiles; ++t) acc[nr][t] = (f32x4){0, 0, 0, 0};
+  }
+  const float c = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
+  const char *kbase = a.c.k + (int64_t)h * a.c.head_stride;
+  const char *vbase = a.c.v + (int64_t)h * a.c.head_stride;
+  const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
+  const int last_pos = sp.first + sp.m - 1;
+
+  F f;
+  for (int64_t blk64 = c0; blk64 < c1; blk64 += kFewBlock) {
+    const int blk = (int)blk64;
+    const int cnt = c1 - blk < kFewBlock ? c1 - blk : kFewBlock;
+    const int ntile = (cnt + kFewTile - 1) / kFewTile;
+    __syncthreads();
+    bool absent = false;
+    for (int i = tid; i < ntile * kFewTile; i += kFewThreads) {
+      int64_t o = -1;
+      if (i < cnt) {
+        o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)(blk + i)));
+        absent |= o < 0;
+      }
+      sh.off[i] = o;
+    }
+    const bool holes = __syncthreads_or(absent);
+    int tile = wave;
+    if (tile < ntile) {
+      f.load_k(kbase, sh.off, tile * kFewTile);
+      f.load_v(vbase, sh.off, tile * kFewTile);
+    }
+    for (; tile < ntile; tile += kFewWaves) {
+      const int at = tile * kFewTile, j0 = blk + at;
+      const int next = (tile + kFewWaves < ntile ? tile + kFewWaves : tile) * kFewTile;
+      f32x4 sc[NR][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) sc[nr][t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < F::kSteps; ++st) {
+          const u32x4 kf = f.k_frag(t, st);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) sc[nr][t] = T::mfma16(kf, qf[nr][st], sc[nr][t]);
+        }
+      }
+      f.load_k(kbase, sh.off, next);
+
+      const bool masked = holes || j0 + kFewTile > hi || j0 + kFewTile - 1 > sp.first ||
+                          (a.window > 0 && j0 <= last_pos - a.window);
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int u = (i >> 2) * 16 + q4 * 4 + (i & 3), j = j0 + u;
+          const bool keep = sh.off[at + u] >= 0;
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            const bool sees = keep && j <= pos[nr] && (a.window <= 0 || j > pos[nr] - a.window);
+            if (!sees) sc[nr][i >> 2][i & 3] = -INFINITY;
+          }
+        }
+      }
+      u32x4 pf[NR];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        float z[8], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z[i] = sc[nr][i >> 2][i & 3] * c;
+          top = fmaxf(top, z[i]);
+        }
+        if (SCORES) {
+          const int r = 16 * nr + col;
+          if (r < R) {
+            float *row = a.scores + ((int64_t)(s * H + h) * a.score_rows + r) * a.score_stride + j0 + q4 * 4;
+            *(f32x4 *)row = (f32x4){z[0], z[1], z[2], z[3]};
+            *(f32x4 *)(row + 16) = (f32x4){z[4], z[5], z[6], z[7]};
+          }
+        }
+        if (__any(top > m_run[nr] + kLazy)) {
+          const float m_new = fmaxf(m_run[nr], xor_max(top));
+          const float alpha = m_new == -INFINITY ? 1.0f : fast_exp2(m_run[nr] - m_new);
+          l_run[nr] *= alpha;
+          m_run[nr] = m_new;
+#pragma unroll
+          for (int t = 0; t < F::kTiles; ++t) acc[nr][t] *= alpha;
+        }
+        const float m_use = m_run[nr] == -INFINITY ? 0.0f : m_run[nr];
+        float p[8], sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = fast_exp2(z[i] - m_use);
+          sum += p[i];
+        }
+        l_run[nr] += sum;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pf[nr][u] = T::pack(p[2 * u], p[2 * u + 1]);
+      }
+      bool odd = false;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool keep = sh.off[at + (i >> 2) * 16 + q4 * 4 + (i & 3)] >= 0;
+#pragma unroll
+          for (int u = 0; u < F::kVRegs; ++u) f.vr[i][u] = keep ? f.vr[i][u] : 0u;
+#pragma unroll
+          for (int n = 0; n < VPieces<D>::n; ++n)
+#pragma unroll
+            for (int m = 0; m < VPieces<D>::w[n] / 2; ++m) odd |= any_nonfinite<T>(f.v_pair(i, n, m));
+        }
+      }
+      if (masked && __any(odd)) {
+        for (int u = 0; u < kFewTile; ++u) {
+          const int64_t o = sh.off[at + u];
+          if (o < 0) continue;
+          const int i = (u >> 4) * 4 + (u & 3), j = j0 + u;
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            const uint32_t w01 = (i & 2) ? pf[nr][1] : pf[nr][0], w23 = (i & 2) ? pf[nr][3] : pf[nr][2];
+            const uint32_t w = __shfl((i & 4) ? w23 : w01, ((u >> 2) & 3) * 16 + col);
+            const float p = (i & 1) ? T::hi(w) : T::lo(w);
+            if (!(j <= pos[nr] && (a.window <= 0 || j > pos[nr] - a.window))) continue;
+            int t0 = 0, base = 0;
+#pragma unroll
+            for (int n = 0; n < VPieces<D>::n; ++n) {
+              const int wd = VPieces<D>::w[n];
+#pragma unroll
+              for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+                for (int t = 0; t < wd; t += 2) {
+                  const char *e = vbase + o + (base + (q4 * 4 + rg) * wd + t) * F::kBytes;
+                  const uint32_t x = E4M3 ? T::template from_e4m3<false>(*(const uint16_t *)e) : *(const uint32_t *)e;
+                  acc[nr][t0 + t][rg] += p * T::lo(x);
+                  acc[nr][t0 + t + 1][rg] += p * T::hi(x);
+                }
+              t0 += wd;
+              base += 16 * wd;
+            }
+          }
+        }
+      } else {
+        int t = 0;
+#pragma unroll
+        for (int n = 0; n < VPieces<D>::n; ++n)
+#pragma unroll
+          for (int m = 0; m < VPieces<D>::w[n] / 2; ++m, t += 2) {
+            u32x4 x, y;
+            f.v_frags(n, m, x, y);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              acc[nr][t] = T::mfma16(x, pf[nr], acc[nr][t]);
+              acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
+            }
+          }
+      }
+      f.load_v(vbase, sh.off, next);
+    }
+  }
+
+  // the four waves' sums: 2 and 3 hand theirs to 0 and 1, then 1 to 0
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr) l_run[nr] = xor_sum(l_run[nr]);
+#pragma unroll
+  for (int step = 2; step >= 1; step >>= 1) {
+    __syncthreads();
+    if (wave >= step && wave < 2 * step) {
+      const int w = wave - step;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const int r = 16 * nr + col;
+        if (q4 == 0) {
+          sh_m[w][r] = m_run[nr];
+          sh_l[w][r] = l_run[nr];
+        }
+        float *row = sh.o + (w * kRows + r) * F::kPad;
+#pragma unroll
+        for (int t = 0; t < F::kTiles; ++t) *(f32x4 *)(row + t * 16 + q4 * 4) = acc[nr][t];
+      }
+    }
+    __syncthreads();
+    if (wave < step) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const int r = 16 * nr + col;
+        const float mo = sh_m[wave][r], lo2 = sh_l[wave][r];
+        const float m_new = fmaxf(m_run[nr], mo);
+        const float x = m_new == -INFINITY ? 1.0f : fast_exp2(m_run[nr] - m_new);
+        const float y = m_new == -INFINITY ? 1.0f : fast_exp2(mo - m_new);
+        m_run[nr] = m_new;
+        l_run[nr] = l_run[nr] * x + lo2 * y;
+        const float *row = sh.o + (wave * kRows + r) * F::kPad;
+#pragma unroll
+        for (int t = 0; t < F::kTiles; ++t) acc[nr][t] = acc[nr][t] * x + *(const f32x4 *)(row + t * 16 + q4 * 4) * y;
+      }
+    }
+  }
+  if (wave != 0) return;
+  const float vs = E4M3 ? a.c.v_scale[h] : 1.0f;
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr) {
+    const int r = 16 * nr + col;
+    if (r >= R) continue;
+    const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
+    const int64_t at = (sp.t0 + tok) * heads + h * G + g;
+    const float l = l_run[nr];
+    float *po = nullptr;
+    char *out = nullptr;
+    float mul = vs;
+    if (a.nsplit > 1) {
+      const int64_t part = (int64_t)split * a.tokens * heads + at;
+      if (q4 == 0) a.part_ml[part] = make_float2(m_run[nr], l);
+      po = a.part_o + part * D;
+      if (!(l > 0.0f || l != l)) continue;      // nothing here: the join skips it
+    } else {
+      if (q4 == 0) a.lse[at] = l > 0.0f || l != l ? (m_run[nr] + __log2f(l)) * kLn2 : -INFINITY;
+      mul = l > 0.0f || l != l ? vs / l : 0.0f;
+      out = a.out + at * D * 2;
+    }
+    // accumulator register rg of column tile t: column base + (4 q4 + rg) w + t
+    int t0 = 0, base = 0;
+#pragma unroll
+    for (int n = 0; n < VPieces<D>::n; ++n) {
+      const int w = VPieces<D>::w[n];
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg) {
+        const int d = base + (q4 * 4 + rg) * w;
+#pragma unroll
+        for (int t = 0; t < w; t += 2) {
+          const float x = acc[nr][t0 + t][rg] * mul, y = acc[nr][t0 + t + 1][rg] * mul;
+          if (po) *(f32x2 *)(po + d + t) = (f32x2){x, y};
+          else *(uint32_t *)(out + (d + t) * 2) = T::pack(x, y);
+        }
+      }
+      t0 += w;
+      base += 16 * w;
+    }
+  }
+}
+
+// One (type, cache, dim) of the few-rows form.
+template <class T, bool E4M3, int D>
+void launch_few_dim(const AttendArgs &a, int row_tiles, dim3 grid, hipStream_t st) {
+  if (row_tiles == 1) {
+    if (a.scores) attend_few_kernel<T, E4M3, D, 1, true><<<grid, kFewThreads, 0, st>>>(a);
+    else attend_few_kernel<T, E4M3, D, 1, false><<<grid, kFewThreads, 0, st>>>(a);
+  } else {
+    if (a.scores) attend_few_kernel<T, E4M3, D, 2, true><<<grid, kFewThreads, 0, st>>>(a);
+    else attend_few_kernel<T, E4M3, D, 2, false><<<grid, kFewThreads, 0, st>>>(a);
+  }
+}
+
+template <class T, bool E4M3>
+void launch_few(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st) {
+  if (dim == 64) launch_few_dim<T, E4M3, 64>(a, row_tiles, grid, st);
+  else if (dim == 96) launch_few_dim<T, E4M3, 96>(a, row_tiles, grid, st);
+  else if (dim == 128) launch_few_dim<T, E4M3, 128>(a, row_tiles, grid, st);
+  else launch_few_dim<T, E4M3, 256>(a, row_tiles, grid, st);
+}
+
+void few_bf16(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
+void few_f16(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
+void few_bf16_e4m3(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
+void few_f16_e4m3(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
+
+}  // namespace kmi

@@ -1,0 +1,464 @@
+// paged_many.h -- attention of many rows over a paged cache (a prompt, or a chunk of one), and
+// the column sums that give every slot the attention it received.
+//
+//   out[t, g] = sum_j p_j v_j,   p_j = exp(z_j - lse),  z_j = scale <q[t, g], k_j>
+//   w[j]      = sum over the rows (t, g) of a key/value head of p_j
+//
+// Attention: a work-group takes 128 rows of one (sequence, key/value head), 32 a wave, and walks
+// the slots that any of them sees in tiles.  Tiles of K and V are staged in LDS, two of each, so
+// that the next is on its way while one is used; the matrix products bound it.
+//
+//  * S^T = K Q^T with 32 x 32 x 16 products: Q stays in registers as the B operand, a lane holds one row
+//    and 16 slots of each 32.  Counting the slots in that order makes the packed p the B operand
+//    of O^T = V^T P^T as it stands, and V^T is read from the row-major tile with transposing
+//    LDS reads.  Rows of the tiles are stored with their 16-byte pieces exchanged by slot number,
+//    which keeps both kinds of read off each other's banks.
+//  * Running maximum, sums, absent slots and non-finite values as in the few-rows form.
+//
+// Column sums: one pass over Q with K in registers.  The rows' lse is known, so
+// p = exp(z - lse) needs no running maximum; a wave owns 32 slots and adds up the rows of Q tiles
+// staged in LDS.
+#pragma once
+
+#include "paged.h"
+
+namespace kmi {
+
+constexpr int kManyThreads = 256;
+constexpr float kManyLazy = 8.0f;   // log2 of what a score may pass the running maximum by
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Piece (16 bytes) p of row r of a tile with D 16-bit columns lies at piece p ^ x(r).
+template <int D>
+__device__ __forceinline__ int k_swizzle(int r) { return D == 96 ? (r >> 1) & 3 : r & 7; }
+template <int D>
+__device__ __forceinline__ int v_swizzle(int r) { return D == 96 ? 2 * ((r >> 1) & 1) : 2 * (r & 3); }
+
+__device__ __forceinline__ float half_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+__device__ __forceinline__ float half_sum(float v) { return v + __shfl_xor(v, 32); }
+
+// Slot of accumulator register r in a 32-slot tile for a lane of half hi.
+__device__ __forceinline__ constexpr int slot32(int r, int hi) { return hi * 4 + (r & 3) + 8 * (r >> 2); }
+
+template <class T, bool E4M3, int D>
+__global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
+  constexpr int KT = D > 128 ? 32 : 64;              // slots of a tile
+  constexpr int kSteps = D / 16, kCols = D / 32, kSub = KT / 32;
+  constexpr int kPieces = D / 8;                     // 16-byte pieces of a row in LDS
+  constexpr int kLoads = KT * kPieces / kManyThreads;
+  constexpr int kRegs = E4M3 ? 2 : 4;
+  static_assert(KT * kPieces % kManyThreads == 0, "whole pieces per thread");
+  __shared__ __align__(16) uint16_t sk[2][KT * D];
+  __shared__ __align__(16) uint16_t sv[2][KT * D];
+  __shared__ int64_t off[2][KT];
+  __shared__ int holes[2];
+
+  const int H = a.c.heads, G = a.group;
+  const int64_t heads = (int64_t)H * G;
+  const int rows_most = a.max_q * G;
+  const int nrt = (rows_most + kManyRowsTile - 1) / kManyRowsTile;
+  int b = blockIdx.x;
+  const int h = b % H;
+  b /= H;
+  const int split = b % a.nsplit;
+  b /= a.nsplit;
+  const int rt = nrt - 1 - b % nrt, s = b / nrt;     // the rows that see most come first
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hi = lane >> 5;
+
+  const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
+  const int R = sp.m * G, row0 = rt * kManyRowsTile;
+  if (row0 >= R) return;
+  const int rows = R - row0 < kManyRowsTile ? R - row0 : kManyRowsTile;
+  // slots that any row of the tile sees
+  const int tok0 = (int)fast_div(a.gdiv, (uint32_t)row0), tok1 = (int)fast_div(a.gdiv, (uint32_t)(row0 + rows - 1));
+  const int first_pos = sp.first + tok0, last_pos = sp.first + tok1;
+  int lo = 0;
+  if (a.window > 0 && first_pos - a.window + 1 > 0) lo = first_pos - a.window + 1;
+  const int end = sp.n < last_pos + 1 ? sp.n : last_pos + 1;
+  lo = lo / KT * KT;
+  const int tiles = end > lo ? (end - lo + KT - 1) / KT : 0;
+  const int per = (tiles + a.nsplit - 1) / a.nsplit;
+  const int tile0 = split * per < tiles ? split * per : tiles;
+  const int tile1 = tile0 + per < tiles ? tile0 + per : tiles;
+
+  const int r = row0 + wave * 32 + col;
+  const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
+  const bool real = r < R;
+  const int pos = real ? sp.first + tok : -1;
+  u32x4 qf[kSteps];
+  {
+    const char *qp = a.q + (sp.t0 + tok) * a.q_stride + ((int64_t)(h * G + g) * D + hi * 8) * 2;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) qf[st] = real ? *(const u32x4 *)(qp + st * 32) : (u32x4){0, 0, 0, 0};
+  }
+  float m_run = -INFINITY, l_run = 0.0f;
+  f32x16 acc[kCols];
+#pragma unroll
+  for (int t = 0; t < kCols; ++t)
+#pragma unroll
+    for (int u = 0; u < 16; ++u) acc[t][u] = 0.0f;
+  const float c = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
+  const char *kbase = a.c.k + (int64_t)h * a.c.head_stride;
+  const char *vbase = a.c.v + (int64_t)h * a.c.head_stride;
+  const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
+
+  // addresses of a tile's slots
+  const auto place = [&](int tile) {
+    if (tid < KT) {
+      const int j = lo + tile * KT + tid;
+      const int64_t o = j < end ? place_offset(a.c, slot_place(a.c, trow, (uint32_t)j)) : -1;
+      off[tile & 1][tid] = o;
+      const uint64_t none = __ballot(o < 0);
+      if (tid == 0) holes[tile & 1] = none != 0;
+    }
+  };
+  uint32_t gk[kLoads][kRegs], gv[kLoads][kRegs];
+  uint32_t there = 0;
+  const auto fetch = [&](int tile) {
+    there = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
+      int64_t o = off[tile & 1][row];
+      if (o >= 0) there |= 1u << i;
+      o = o < 0 ? 0 : o;
+      if (E4M3) {
+        const u32x2 x = *(const u32x2 *)(kbase + o + p * 8);
+        const u32x2 y = *(const u32x2 *)(vbase + o + p * 8);
+        gk[i][0] = x.x; gk[i][1] = x.y;
+        gv[i][0] = y.x; gv[i][1] = y.y;
+      } else {
+        const u32x4 x = *(const u32x4 *)(kbase + o + p * 16);
+        const u32x4 y = *(const u32x4 *)(vbase + o + p * 16);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) { gk[i][u % kRegs] = x[u]; gv[i][u % kRegs] = y[u]; }
+      }
+    }
+  };
+  const auto store = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
+      u32x4 x, y;
+      if (E4M3) {
+        x = widen_e4m3<T>((u32x2){gk[i][0], gk[i][1]});
+        y = widen_e4m3<T>((u32x2){gv[i][0], gv[i][1]});
+      } else {
+        x = (u32x4){gk[i][0], gk[i][1], gk[i][2 % kRegs], gk[i][3 % kRegs]};
+        y = (u32x4){gv[i][0], gv[i][1], gv[i][2 % kRegs], gv[i][3 % kRegs]};
+      }
+      *(u32x4 *)&sk[tile & 1][row * D + (p ^ k_swizzle<D>(row)) * 8] = x;
+      *(u32x4 *)&sv[tile & 1][row * D + (p ^ v_swizzle<D>(row)) * 8] = keep_if(y, (there >> i) & 1u);
+    }
+  };
+
+  if (tile0 < tile1) {
+    place(tile0);
+    __syncthreads();
+    fetch(tile0);
+    store(tile0);
+    if (tile0 + 1 < tile1) place(tile0 + 1);
+    __syncthreads();
+  }
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int buf = tile & 1, j0 = lo + tile * KT;
+    const bool more = tile + 1 < tile1;
+    const bool gaps = holes[buf];
+    if (more) fetch(tile + 1);
+    f32x16 sc[kSub];
+#pragma unroll
+    for (int t = 0; t < kSub; ++t) {
+#pragma unroll
+      for (int u = 0; u < 16; ++u) sc[t][u] = 0.0f;
+      const int row = t * 32 + col;
+      const uint16_t *kr = &sk[buf][row * D];
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const u32x4 kf = *(const u32x4 *)(kr + ((2 * st + hi) ^ k_swizzle<D>(row)) * 8);
+        sc[t] = T::mfma32(kf, qf[st], sc[t]);
+      }
+    }
+    const bool masked = gaps || j0 + KT - 1 > first_pos || (a.window > 0 && j0 <= last_pos - a.window);
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < kSub; ++t)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int at = t * 32 + slot32(u, hi), j = j0 + at;
+          const bool sees = off[buf][at] >= 0 && j <= pos && (a.window <= 0 || j > pos - a.window);
+          if (!sees) sc[t][u] = -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < kSub; ++t)
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        sc[t][u] *= c;
+        top = fmaxf(top, sc[t][u]);
+      }
+    if (__any(top > m_run + kManyLazy)) {
+      const float m_new = fmaxf(m_run, half_max(top));
+      const float alpha = m_new == -INFINITY ? 1.0f : fast_exp2(m_run - m_new);
+      l_run *= alpha;
+      m_run = m_new;
+#pragma unroll
+      for (int t = 0; t < kCols; ++t) acc[t] *= alpha;
+    }
+    const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+    u32x4 pf[kSub][2];
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kSub; ++t)
+#pragma unroll
+      for (int u = 0; u < 16; u += 2) {
+        const float x = fast_exp2(sc[t][u] - m_use), y = fast_exp2(sc[t][u + 1] - m_use);
+        sum += x + y;
+        pf[t][u >> 3][(u & 7) >> 1] = T::pack(x, y);
+      }
+    l_run += sum;
+
+    // V^T operand of slots 16 ks .. of sub-tile t, columns 32 n ..: two transposing reads
+    const auto v_frag = [&](int t, int ks, int n) -> u32x4 {
+      const int l16 = lane & 15, row = t * 32 + ks * 16 + hi * 4 + (l16 >> 2);
+      const int colb = n * 32 + ((lane >> 4) & 1) * 16 + (l16 & 3) * 4;
+      const int p = colb >> 3, in = colb & 7;
+      const uint16_t *x = &sv[buf][row * D + (p ^ v_swizzle<D>(row)) * 8 + in];
+      const uint16_t *y = &sv[buf][(row + 8) * D + (p ^ v_swizzle<D>(row + 8)) * 8 + in];
+      const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)x);
+      const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)y);
+      const u32x2 ub = __builtin_bit_cast(u32x2, u), wb = __builtin_bit_cast(u32x2, w);
+      return (u32x4){ub.x, ub.y, wb.x, wb.y};
+    };
+    bool odd = false;
+    if (masked) {
+      for (int i = lane; i < KT * D / 2; i += 64) odd |= any_nonfinite<T>(((const uint32_t *)sv[buf])[i]);
+    }
+    if (masked && __any(odd)) {
+      for (int u = 0; u < KT; ++u) {
+        if (off[buf][u] < 0) continue;
+        const int j = j0 + u, in = u & 31, reg = (in & 3) + 4 * (in >> 3), half = (in >> 2) & 1;
+        uint32_t w = 0;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (t * 8 + k == (u >> 5) * 8 + (reg >> 1)) w = pf[t][k >> 2][k & 3];
+        w = __shfl(w, half * 32 + col);
+        const float p = (reg & 1) ? T::hi(w) : T::lo(w);
+        if (!(j <= pos && (a.window <= 0 || j > pos - a.window))) continue;
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const int d = n * 32 + slot32(k, hi);
+            const uint32_t x = *(const uint32_t *)&sv[buf][u * D + ((d >> 3) ^ v_swizzle<D>(u)) * 8 + (d & 7)];
+            acc[n][k] += p * T::lo(x);
+            acc[n][k + 1] += p * T::hi(x);
+          }
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < kSub; ++t)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) acc[n] = T::mfma32(v_frag(t, ks, n), pf[t][ks], acc[n]);
+    }
+    if (more) store(tile + 1);
+    __syncthreads();
+    if (tile + 2 < tile1) place(tile + 2);
+    __syncthreads();
+  }
+
+  l_run = half_sum(l_run);
+  if (!real) return;
+  const int64_t at = (sp.t0 + tok) * heads + h * G + g;
+  const float vs = E4M3 ? a.c.v_scale[h] : 1.0f;
+  const bool any = l_run > 0.0f || l_run != l_run;
+  if (a.nsplit > 1) {
+    const int64_t part = (int64_t)split * a.tokens * heads + at;
+    if (hi == 0) a.part_ml[part] = make_float2(m_run, l_run);
+    if (!any) return;
+    float *po = a.part_o + part * D;
+#pragma unroll
+    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+      for (int k = 0; k < 16; k += 4)
+        *(f32x4 *)(po + n * 32 + slot32(k, hi)) =
+            (f32x4){acc[n][k] * vs, acc[n][k + 1] * vs, acc[n][k + 2] * vs, acc[n][k + 3] * vs};
+  } else {
+    if (hi == 0) a.lse[at] = any ? (m_run + __log2f(l_run)) * kLn2 : -INFINITY;
+    const float mul = any ? vs / l_run : 0.0f;
+    char *out = a.out + at * D * 2;
+#pragma unroll
+    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+      for (int k = 0; k < 16; k += 4)
+        *(u32x2 *)(out + (n * 32 + slot32(k, hi)) * 2) =
+            (u32x2){T::pack(acc[n][k] * mul, acc[n][k + 1] * mul), T::pack(acc[n][k + 2] * mul, acc[n][k + 3] * mul)};
+  }
+}
+
+// Column sums.  Grid: slot tiles x heads x sequences x row splits.
+template <class T, bool E4M3, int D>
+__global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_kernel(AttendArgs a) {
+  constexpr int QT = 64;                             // rows of a tile
+  constexpr int kSteps = D / 16, kPieces = D / 8;
+  constexpr int kLoads = QT * kPieces / kManyThreads;
+  __shared__ __align__(16) uint16_t sq[2][QT * D];
+  __shared__ __align__(16) float sl[2][QT];
+  __shared__ int sp_[2][QT];
+
+  const int H = a.c.heads, G = a.group;
+  const int64_t heads = (int64_t)H * G;
+  const int nst = (a.max_len + kSumSlotsTile - 1) / kSumSlotsTile;
+  int b = blockIdx.x;
+  const int h = b % H;
+  b /= H;
+  const int st = b % nst;
+  b /= nst;
+  const int s = b % a.c.seqs, rsplit = b / a.c.seqs;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hi = lane >> 5;
+  const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
+  const int slot0 = st * kSumSlotsTile;
+  if (slot0 >= sp.n) return;
+  const int j = slot0 + wave * 32 + col;
+  SlotPlace pl{-1, 0};
+  if (j < sp.n) pl = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)j);
+  const int64_t o = place_offset(a.c, pl);
+  u32x4 kf[kSteps];
+  {
+    const char *kp = a.c.k + (int64_t)h * a.c.head_stride + (o < 0 ? 0 : o);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (E4M3) kf[i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
+      else kf[i] = *(const u32x4 *)(kp + i * 32 + hi * 16);
+    }
+  }
+  // tokens that see any slot of the tile
+  int i0 = slot0 - sp.first, i1 = sp.m;
+  i0 = i0 < 0 ? 0 : i0;
+  if (a.window > 0) {
+    const int64_t e = (int64_t)slot0 + kSumSlotsTile - 1 + a.window - sp.first;
+    i1 = e < i1 ? (int)e : i1;
+  }
+  const int r0 = i0 * G, r1 = i1 > i0 ? i1 * G : i0 * G;
+  int tiles = (r1 - r0 + QT - 1) / QT;
+  const int per = (tiles + a.nrow - 1) / a.nrow;
+  const int tile0 = rsplit * per < tiles ? rsplit * per : tiles;
+  const int tile1 = tile0 + per < tiles ? tile0 + per : tiles;
+  const float c = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
+
+  u32x4 gq[kLoads];
+  float gl = 0.0f;
+  int gp = 0;
+  const auto fetch = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces, r = r0 + tile * QT + row;
+      const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
+      gq[i] = (u32x4){0, 0, 0, 0};
+      if (r < r1) gq[i] = *(const u32x4 *)(a.q + (sp.t0 + tok) * a.q_stride + ((int64_t)(h * G + g) * D) * 2 + p * 16);
+    }
+    if (tid < QT) {
+      const int r = r0 + tile * QT + tid;
+      const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
+      float l = INFINITY;        // a row that is not there, or sees nothing, gives 0
+      if (r < r1) {
+        l = a.lse[(sp.t0 + tok) * heads + h * G + g] * kLog2e;
+        if (l == -INFINITY) l = INFINITY;
+      }
+      gl = l;
+      gp = r < r1 ? sp.first + tok : -1;
+    }
+  };
+  const auto store = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
+      *(u32x4 *)&sq[buf][row * D + (p ^ k_swizzle<D>(row)) * 8] = gq[i];
+    }
+    if (tid < QT) {
+      sl[buf][tid] = gl;
+      sp_[buf][tid] = gp;
+    }
+  };
+  float sum = 0.0f, low = 0.0f;   // running sum and what its roundings lost
+  if (tile0 < tile1) {
+    fetch(tile0);
+    store(0);
+    __syncthreads();
+  }
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int buf = (tile - tile0) & 1;
+    const bool more = tile + 1 < tile1;
+    if (more) fetch(tile + 1);
+    // slots of the first and last row of the tile
+    const int ra = r0 + tile * QT, rb = ra + QT < r1 ? ra + QT - 1 : r1 - 1;
+    const int pa = sp.first + (int)fast_div(a.gdiv, (uint32_t)ra), pb = sp.first + (int)fast_div(a.gdiv, (uint32_t)rb);
+    const bool masked = slot0 + kSumSlotsTile - 1 > pa || (a.window > 0 && slot0 <= pb - a.window);
+#pragma unroll
+    for (int t = 0; t < QT / 32; ++t) {
+      f32x16 sc;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) sc[u] = 0.0f;
+      const int row = t * 32 + col;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const u32x4 qf = *(const u32x4 *)&sq[buf][row * D + ((2 * i + hi) ^ k_swizzle<D>(row)) * 8];
+        sc = T::mfma32(qf, kf[i], sc);
+      }
+      float part = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 l = *(const f32x4 *)&sl[buf][t * 32 + q * 8 + hi * 4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float z = sc[q * 4 + u] * c;
+          if (masked) {
+            const int p = sp_[buf][t * 32 + q * 8 + hi * 4 + u];
+            if (!(j <= p && (a.window <= 0 || j > p - a.window))) z = -INFINITY;
+          }
+          part += z == -INFINITY ? 0.0f : fast_exp2(z - l[u]);
+        }
+      }
+      const float y = part - low, x = sum + y;
+      low = (x - sum) - y;
+      sum = x;
+    }
+    if (more) store(buf ^ 1);
+    __syncthreads();
+  }
+  sum = half_sum(sum);
+  if (j >= sp.n || hi) return;
+  if (a.nrow > 1) {
+    a.part_w[((int64_t)rsplit * a.c.seqs * H + (int64_t)s * H + h) * a.max_len + j] = sum;
+  } else if (pl.page >= 0) {
+    float *w = a.c.weights + ((int64_t)pl.page * H + h) * a.c.page.d + pl.row;
+    *w = a.decay != 0.0f ? a.decay * *w + sum : sum;
+  }
+}
+
+template <class T, bool E4M3>
+void launch_many(const AttendArgs &a, int dim, dim3 grid, hipStream_t st) {
+  if (dim == 64) attend_many_kernel<T, E4M3, 64><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 96) attend_many_kernel<T, E4M3, 96><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 128) attend_many_kernel<T, E4M3, 128><<<grid, kManyThreads, 0, st>>>(a);
+  else attend_many_kernel<T, E4M3, 256><<<grid, kManyThreads, 0, st>>>(a);
+}
+template <class T, bool E4M3>
+void launch_sums(const AttendArgs &a, int dim, dim3 grid, hipStream_t st) {
+  if (dim == 64) attend_sums_kernel<T, E4M3, 64><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 96) attend_sums_kernel<T, E4M3, 96><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 128) attend_sums_kernel<T, E4M3, 128><<<grid, kManyThreads, 0, st>>>(a);
+  else attend_sums_kernel<T, E4M3, 256><<<grid, kManyThreads, 0, st>>>(a);
+}
+
+void many_bf16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
+void many_f16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
+void many_bf16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
+void many_f16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
+
+}  // namespace kmi

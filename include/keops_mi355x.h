@@ -239,6 +239,114 @@ int keops_kmin(const float *x, const float *y, const float *b,
                int64_t M, int64_t N, int32_t D, int32_t K, float sigma,
                float *out_d, int64_t *out_idx, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Paged key/value cache and draft verification (serving large language models)
+ * ---------------------------------------------------------------------------
+ * Attention is the same kind of reduction as above, over keys in place of points:
+ * softmax(scale <q_i, k_j>) is a LogSumExp over j, its output the sum of
+ * exp(z_ij - lse_i) v_j.  The keys and values of a batch of sequences lie in a pool of
+ * pages; nothing of the size queries x keys is stored, but for the scores of a step that
+ * asks for attention weights (below).
+ *
+ * Conventions of these entry points, beside the common ones:
+ *  Sequence s has lens[s] slots; its starts[s+1] - starts[s] new tokens, rows starts[s] ..
+ *  of the token arrays, are its last slots.  Slot j lies in row j % page_size of page
+ *  page_table[s][j / page_size].  A slot whose table entry is outside [0, pages), or past
+ *  the table's width, is absent: attention does not see it, append, weights and eviction
+ *  leave it out.
+ *  lens, starts, tables and scales are device arrays (int32, fp32).  They are read by the
+ *  kernels only: a sequence with more new tokens than max_q or more slots than max_len is
+ *  cut to them, starts outside [0, tokens] likewise; outputs of tokens in no sequence, or
+ *  past max_q, are undefined.
+ *  Strides count elements; the last dimension of every array is contiguous.  k_pages,
+ *  v_pages, q, k, v and out are 16-byte aligned, their strides multiples of 16 bytes.
+ *  k_pages and v_pages share their strides: [pages][page_size][heads][dim] in any order of
+ *  the first three.  dim: 64, 96, 128 or 256.
+ *  Types: KEOPS_TYPE_BF16 or _F16 for q, k, v, out, with a cache of the same type or of
+ *  KEOPS_TYPE_E4M3 (OCP e4m3, finite to 448), whose elements stand for value * scale[head].
+ */
+#define KEOPS_TYPE_BF16 0
+#define KEOPS_TYPE_F16 1
+#define KEOPS_TYPE_E4M3 2
+
+typedef struct {
+  void *k_pages, *v_pages;
+  float *weights;                 /* [pages][heads][page_size], or NULL          */
+  const float *k_scale, *v_scale; /* [heads]; KEOPS_TYPE_E4M3 only (eviction does not read them) */
+  int64_t page_stride, slot_stride, head_stride;
+  int64_t pages;
+  const int32_t *page_table;      /* [seqs][table_width], rows table_stride apart */
+  int64_t table_stride;
+  const int32_t *lens;            /* [seqs]                                      */
+  int32_t page_size, heads, dim, type, table_width, seqs;
+} keops_cache_t;
+
+/*
+ * New keys and values into their slots: row t of k and v ([tokens][heads][dim], rows
+ * k_stride and v_stride apart) to the slot of token t.  E4M3 caches hold the value nearest
+ * to k / k_scale[head] (ties to even), cut to +-448; NaN stays NaN.  Where the cache has
+ * weights, those of the written slots become 0.  starts: [seqs + 1].
+ */
+int keops_cache_append(const keops_cache_t *cache, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                       int32_t type, const int32_t *starts, int64_t tokens, void *stream);
+
+/*
+ * Causal attention of every sequence's new tokens over its slots:
+ *   z_j = scale <q[t, g], k_j>,  lse[t, g] = log sum_j exp(z_j),  out[t, g] = sum_j exp(z_j - lse) v_j
+ * over the slots j <= the token's own, and, with window > 0, j > its own - window.  heads
+ * query heads, a multiple of the cache's; query head g reads key/value head
+ * g / (heads / cache heads).  A token that sees no slot has out = 0 and lse = -inf.
+ * q: [tokens][heads][dim], rows q_stride apart; out: the same shape, dense; lse: [tokens][heads].
+ * Where the cache has weights, slot j's becomes
+ *   decay * old + sum over the new tokens t and the query heads g of the key/value head of exp(z_j - lse)
+ * for every slot of every sequence (decay = 0 does not read the old ones; 1 accumulates).
+ * A value that a row does not see has no effect on it, whatever it holds.
+ * workspace: NULL for the library's (see "Ownership" above), or a 256-byte aligned device
+ * buffer of at least keops_paged_attention_workspace bytes (KEOPS_ERR_SCRATCH if smaller).
+ * Under stream capture a call that needs workspace must bring its own (KEOPS_ERR_ALLOC
+ * otherwise), which has to live as long as the graph.
+ */
+int keops_paged_attention(const keops_cache_t *cache, const void *q, int64_t q_stride, int32_t type, int32_t heads,
+                          const int32_t *starts, int64_t tokens, int32_t max_q, int32_t max_len, float scale,
+                          int32_t window, float decay, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+                          void *stream);
+
+/* Workspace bytes of a keops_paged_attention call with these arguments on the current device. */
+int keops_paged_attention_workspace(const keops_cache_t *cache, int32_t type, int32_t heads, int64_t tokens,
+                                    int32_t max_q, int32_t max_len, int32_t window, int64_t *bytes);
+
+/*
+ * Eviction by attention weight.  Each key/value head of a sequence with more than `budget`
+ * slots keeps the first `sink`, the last `recent`, and of the others the
+ * budget - sink - recent with the largest weights (equal weights: the lower slot; NaN is
+ * largest; an absent slot smallest); a shorter sequence keeps all.  Kept slots move in their
+ * order to slots 0 .. of the pages of new_table ([seqs][new_width], rows new_stride apart):
+ * keys, values and weights.  Pages of new_table are none of page_table's, and no page is in
+ * new_table twice (their contents are undefined otherwise).
+ * kept: [seqs][heads][budget], the old slot numbers, -1 past the end; new_lens: [seqs].
+ * new_width >= min(ceil(budget / page_size), table_width); 1 <= budget, sink + recent <= budget.
+ */
+int keops_cache_evict(const keops_cache_t *cache, const int32_t *new_table, int64_t new_stride, int32_t new_width,
+                      int32_t budget, int32_t sink, int32_t recent, int32_t *kept, int32_t *new_lens, void *stream);
+
+/*
+ * Verification of drafted tokens.  Sequence s drafted tokens[s][0 .. counts[s]) from
+ * draft[s][r][.]; target[s][r][.] are the target model's probabilities at the same places
+ * and at the one after (fp32, each row's scale free).  Token r is taken while
+ *   u_accept[s][r] * draft[s][r][x] < target[s][r][x];
+ * the token after the taken ones is the lowest index whose running sum of the mass m
+ * exceeds u_sample[s] times the total, with m = max(target - draft, 0) at a refused place
+ * (target itself if that is 0 everywhere) and m = target after the last.  Sums in 64 bits.
+ * draft = NULL: the drafted token had probability 1.  A token outside [0, vocab) is refused.
+ * target: [seqs][drafts + 1][vocab], draft: [seqs][drafts][vocab], tokens, u_accept:
+ * [seqs][drafts]; out: [seqs][drafts + 1], the taken tokens, the new one, then -1;
+ * accepted: [seqs], how many were taken.
+ */
+int keops_verify_draft(const float *target, const float *draft, const int32_t *tokens, const int32_t *counts,
+                       const float *u_accept, const float *u_sample, int32_t seqs, int32_t drafts, int32_t vocab,
+                       int32_t *out, int32_t *accepted, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *keops_status_string(int status);
 
