@@ -196,11 +196,42 @@ struct F16 {
   }
 };
 
-// True where either 16-bit half of w is an infinity or a NaN.
+// A half of w where it is an infinity or a NaN, 0 where it is finite.
 template <class T>
-__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
-  const uint32_t e = w & T::kExp;
-  return (e & 0xffffu) == (T::kExp & 0xffffu) || (e >> 16) == (T::kExp >> 16);
+__device__ __forceinline__ float nonfinite_lo(uint32_t w) {
+  return (w & T::kExp & 0xffffu) == (T::kExp & 0xffffu) ? T::lo(w) : 0.0f;
+}
+template <class T>
+__device__ __forceinline__ float nonfinite_hi(uint32_t w) {
+  return (w & T::kExp & 0xffff0000u) == (T::kExp & 0xffff0000u) ? T::hi(w) : 0.0f;
+}
+// Zeros for the halves of w that are infinities or NaNs.
+template <class T>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+  const uint32_t lo = (w & T::kExp & 0xffffu) == (T::kExp & 0xffffu) ? 0xffffu : 0u;
+  const uint32_t hi = (w & T::kExp & 0xffff0000u) == (T::kExp & 0xffff0000u) ? 0xffff0000u : 0u;
+  return w & ~(lo | hi);
+}
+// Zeros for the bytes of w that are NaNs as e4m3.
+__device__ __forceinline__ uint32_t finite_bytes(uint32_t w) {
+  const uint32_t t = (w & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;                // 0 where the byte is a NaN
+  const uint32_t nan = (~(t + 0x7f7f7f7fu) & 0x80808080u) >> 7;      // no carry passes a byte
+  return w & ~(nan * 255u);
+}
+// The lowest n of 32 bits; none for n <= 0.
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+template <class T>
+__device__ __forceinline__ bool clear_nonfinite(u32x4 &x) {
+  bool any = false;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t y = finite_halves<T>(x[u]);
+    any |= y != x[u];
+    x[u] = y;
+  }
+  return any;
 }
 
 template <class T>

@@ -20,8 +20,8 @@
 //    the cache's 16-bit type for the matrix product (8-bit caches: q's type).
 //  * Slots that no row may see (past the length, of a page that the table lacks) get a zero V.
 //    Slots that some rows see and others do not are only in the tiles of the new tokens and at
-//    the window's edge; if such a tile holds an infinity or NaN in V, it is added slot by slot,
-//    to the rows that see it (0 times infinity would reach the others).
+//    the window's edge; if such a tile holds an infinity or NaN in V, it is added after the
+//    products, to the rows that see it (0 times infinity would reach the others).
 #pragma once
 
 #include "paged.h"
@@ -154,6 +154,8 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
     float o[kHalfRows * F::kPad];
   } sh;
   __shared__ float sh_m[2][kRows], sh_l[2][kRows];
+  __shared__ uint32_t present[kFewBlock / kFewTile];     // a tile's slots that are there, as bits
+  __shared__ int sh_odd;
 
   const int H = a.c.heads, G = a.group;
   int b = blockIdx.x;
@@ -202,21 +204,23 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
   const int last_pos = sp.first + sp.m - 1;
 
   F f;
+  bool odd = false;
+  if (tid == 0) sh_odd = 0;
   for (int64_t blk64 = c0; blk64 < c1; blk64 += kFewBlock) {
     const int blk = (int)blk64;
     const int cnt = c1 - blk < kFewBlock ? c1 - blk : kFewBlock;
     const int ntile = (cnt + kFewTile - 1) / kFewTile;
     __syncthreads();
-    bool absent = false;
-    for (int i = tid; i < ntile * kFewTile; i += kFewThreads) {
-      int64_t o = -1;
-      if (i < cnt) {
-        o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)(blk + i)));
-        absent |= o < 0;
-      }
+    for (int i = tid; i < kFewBlock; i += kFewThreads) {
+      const int64_t o = i < cnt ? place_offset(a.c, slot_place(a.c, trow, (uint32_t)(blk + i))) : -1;
       sh.off[i] = o;
+      const uint64_t there = __ballot(o >= 0);
+      if (lane == 0) {
+        present[i / kFewTile] = (uint32_t)there;
+        present[i / kFewTile + 1] = (uint32_t)(there >> 32);
+      }
     }
-    const bool holes = __syncthreads_or(absent);
+    __syncthreads();
     int tile = wave;
     if (tile < ntile) {
       f.load_k(kbase, sh.off, tile * kFewTile);
@@ -224,7 +228,8 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
     }
     for (; tile < ntile; tile += kFewWaves) {
       const int at = tile * kFewTile, j0 = blk + at;
-      const int next = (tile + kFewWaves < ntile ? tile + kFewWaves : tile) * kFewTile;
+      const bool more = tile + kFewWaves < ntile;
+      const int next = (tile + kFewWaves) * kFewTile;
       f32x4 sc[NR][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -237,20 +242,20 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
           for (int nr = 0; nr < NR; ++nr) sc[nr][t] = T::mfma16(kf, qf[nr][st], sc[nr][t]);
         }
       }
-      f.load_k(kbase, sh.off, next);
+      if (more) f.load_k(kbase, sh.off, next);
 
-      const bool masked = holes || j0 + kFewTile > hi || j0 + kFewTile - 1 > sp.first ||
-                          (a.window > 0 && j0 <= last_pos - a.window);
+      const uint32_t there = present[tile];
+      const bool masked = there != 0xffffffffu || j0 + kFewTile - 1 > sp.first || (a.window > 0 && j0 <= last_pos - a.window);
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int u = (i >> 2) * 16 + q4 * 4 + (i & 3), j = j0 + u;
-          const bool keep = sh.off[at + u] >= 0;
+        for (int nr = 0; nr < NR; ++nr) {
+          const int up = pos[nr] - j0;
+          uint32_t own = first_bits(up + 1) & there;      // the row's slots, as bits
+          if (a.window > 0) own &= ~first_bits(up + 1 - a.window);
+          own >>= q4 * 4;
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            const bool sees = keep && j <= pos[nr] && (a.window <= 0 || j > pos[nr] - a.window);
-            if (!sees) sc[nr][i >> 2][i & 3] = -INFINITY;
-          }
+          for (int i = 0; i < 8; ++i)
+            if (!(own & (1u << ((i >> 2) * 16 + (i & 3))))) sc[nr][i >> 2][i & 3] = -INFINITY;
         }
       }
       u32x4 pf[NR];
@@ -289,67 +294,42 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
 #pragma unroll
         for (int u = 0; u < 4; ++u) pf[nr][u] = T::pack(p[2 * u], p[2 * u + 1]);
       }
-      bool odd = false;
       if (masked) {
+        // absent slots are zeros; non-finite values of slots that some rows see and others do
+        // not wait for the end
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool keep = sh.off[at + (i >> 2) * 16 + q4 * 4 + (i & 3)] >= 0;
+          const int u = (i >> 2) * 16 + q4 * 4 + (i & 3), j = j0 + u;
+          const bool keep = (there >> u) & 1u;
+          const bool some = j > sp.first || (a.window > 0 && j <= last_pos - a.window);
 #pragma unroll
-          for (int u = 0; u < F::kVRegs; ++u) f.vr[i][u] = keep ? f.vr[i][u] : 0u;
-#pragma unroll
-          for (int n = 0; n < VPieces<D>::n; ++n)
-#pragma unroll
-            for (int m = 0; m < VPieces<D>::w[n] / 2; ++m) odd |= any_nonfinite<T>(f.v_pair(i, n, m));
+          for (int k = 0; k < F::kVRegs; ++k) {
+            const uint32_t x = keep ? f.vr[i][k] : 0u;
+            const uint32_t y = some ? (E4M3 ? finite_bytes(x) : finite_halves<T>(x)) : x;
+            odd |= y != x;
+            f.vr[i][k] = y;
+          }
         }
       }
-      if (masked && __any(odd)) {
-        for (int u = 0; u < kFewTile; ++u) {
-          const int64_t o = sh.off[at + u];
-          if (o < 0) continue;
-          const int i = (u >> 4) * 4 + (u & 3), j = j0 + u;
+      int t = 0;
+#pragma unroll
+      for (int n = 0; n < VPieces<D>::n; ++n)
+#pragma unroll
+        for (int m = 0; m < VPieces<D>::w[n] / 2; ++m, t += 2) {
+          u32x4 x, y;
+          f.v_frags(n, m, x, y);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) {
-            const uint32_t w01 = (i & 2) ? pf[nr][1] : pf[nr][0], w23 = (i & 2) ? pf[nr][3] : pf[nr][2];
-            const uint32_t w = __shfl((i & 4) ? w23 : w01, ((u >> 2) & 3) * 16 + col);
-            const float p = (i & 1) ? T::hi(w) : T::lo(w);
-            if (!(j <= pos[nr] && (a.window <= 0 || j > pos[nr] - a.window))) continue;
-            int t0 = 0, base = 0;
-#pragma unroll
-            for (int n = 0; n < VPieces<D>::n; ++n) {
-              const int wd = VPieces<D>::w[n];
-#pragma unroll
-              for (int rg = 0; rg < 4; ++rg)
-#pragma unroll
-                for (int t = 0; t < wd; t += 2) {
-                  const char *e = vbase + o + (base + (q4 * 4 + rg) * wd + t) * F::kBytes;
-                  const uint32_t x = E4M3 ? T::template from_e4m3<false>(*(const uint16_t *)e) : *(const uint32_t *)e;
-                  acc[nr][t0 + t][rg] += p * T::lo(x);
-                  acc[nr][t0 + t + 1][rg] += p * T::hi(x);
-                }
-              t0 += wd;
-              base += 16 * wd;
-            }
+            acc[nr][t] = T::mfma16(x, pf[nr], acc[nr][t]);
+            acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
           }
         }
-      } else {
-        int t = 0;
-#pragma unroll
-        for (int n = 0; n < VPieces<D>::n; ++n)
-#pragma unroll
-          for (int m = 0; m < VPieces<D>::w[n] / 2; ++m, t += 2) {
-            u32x4 x, y;
-            f.v_frags(n, m, x, y);
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-              acc[nr][t] = T::mfma16(x, pf[nr], acc[nr][t]);
-              acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
-            }
-          }
-      }
-      f.load_v(vbase, sh.off, next);
+      if (more) f.load_v(vbase, sh.off, next);
     }
   }
 
+  __syncthreads();
+  if (odd) sh_odd = 1;
   // the four waves' sums: 2 and 3 hand theirs to 0 and 1, then 1 to 0
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) l_run[nr] = xor_sum(l_run[nr]);
@@ -388,6 +368,35 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
     }
   }
   if (wave != 0) return;
+  if (sh_odd) {
+    // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
+    for (int64_t j64 = c0; j64 < c1; ++j64) {
+      const int j = (int)j64;
+      if (!(j > sp.first || (a.window > 0 && j <= last_pos - a.window))) continue;
+      const int64_t o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)j));
+      if (o < 0) continue;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        if (j > pos[nr] || (a.window > 0 && j <= pos[nr] - a.window)) continue;
+        int t0 = 0, base = 0;
+#pragma unroll
+        for (int n = 0; n < VPieces<D>::n; ++n) {
+          const int w = VPieces<D>::w[n];
+#pragma unroll
+          for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+            for (int t = 0; t < w; t += 2) {
+              const char *e = vbase + o + (base + (q4 * 4 + rg) * w + t) * F::kBytes;
+              const uint32_t x = E4M3 ? T::template from_e4m3<false>(*(const uint16_t *)e) : *(const uint32_t *)e;
+              acc[nr][t0 + t][rg] += nonfinite_lo<T>(x);
+              acc[nr][t0 + t + 1][rg] += nonfinite_hi<T>(x);
+            }
+          t0 += w;
+          base += 16 * w;
+        }
+      }
+    }
+  }
   const float vs = E4M3 ? a.c.v_scale[h] : 1.0f;
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {

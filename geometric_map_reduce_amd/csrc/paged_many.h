@@ -41,18 +41,32 @@ __device__ __forceinline__ float half_sum(float v) { return v + __shfl_xor(v, 32
 // Slot of accumulator register r in a 32-slot tile for a lane of half hi.
 __device__ __forceinline__ constexpr int slot32(int r, int hi) { return hi * 4 + (r & 3) + 8 * (r >> 2); }
 
+// Zeros that stand in for the rows of absent slots.
+static __device__ const uint32_t kZeroRow[128] = {};
+
+// 16 bytes a lane from global memory to LDS, lane l's at lds + 16 l, without passing registers.
+// Done when vmcnt says so: the compiler does not know, dma_wait() does.  (M0 needs one wait state.)
+__device__ __forceinline__ void dma16(const void *from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
 template <class T, bool E4M3, int D>
 __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
   constexpr int KT = D > 128 ? 32 : 64;              // slots of a tile
   constexpr int kSteps = D / 16, kCols = D / 32, kSub = KT / 32;
   constexpr int kPieces = D / 8;                     // 16-byte pieces of a row in LDS
   constexpr int kLoads = KT * kPieces / kManyThreads;
-  constexpr int kRegs = E4M3 ? 2 : 4;
-  static_assert(KT * kPieces % kManyThreads == 0, "whole pieces per thread");
+  constexpr int kChunk = 8;                          // tiles whose addresses are placed together
+  constexpr int kPlace = kChunk * KT / kManyThreads; // slots a thread places
+  static_assert(KT * kPieces % kManyThreads == 0 && kChunk * KT % kManyThreads == 0, "whole pieces per thread");
   __shared__ __align__(16) uint16_t sk[2][KT * D];
   __shared__ __align__(16) uint16_t sv[2][KT * D];
-  __shared__ int64_t off[2][KT];
-  __shared__ int holes[2];
+  __shared__ int64_t off[2][kChunk * KT];
+  __shared__ uint64_t present[2][kChunk * KT / 64];    // which of 64 slots are there
 
   const int H = a.c.heads, G = a.group;
   const int64_t heads = (int64_t)H * G;
@@ -64,7 +78,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   const int split = b % a.nsplit;
   b /= a.nsplit;
   const int rt = nrt - 1 - b % nrt, s = b / nrt;     // the rows that see most come first
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hi = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, hi = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
   const int R = sp.m * G, row0 = rt * kManyRowsTile;
@@ -77,127 +92,149 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   if (a.window > 0 && first_pos - a.window + 1 > 0) lo = first_pos - a.window + 1;
   const int end = sp.n < last_pos + 1 ? sp.n : last_pos + 1;
   lo = lo / KT * KT;
-  const int tiles = end > lo ? (end - lo + KT - 1) / KT : 0;
-  const int per = (tiles + a.nsplit - 1) / a.nsplit;
-  const int tile0 = split * per < tiles ? split * per : tiles;
-  const int tile1 = tile0 + per < tiles ? tile0 + per : tiles;
+  const int all = end > lo ? (end - lo + KT - 1) / KT : 0;
+  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int tile0 = split * per < all ? split * per : all;
+  const int tiles = tile0 + per < all ? per : all - tile0;
+  lo += tile0 * KT;                                  // this split's tiles: 0 .. tiles
 
   const int r = row0 + wave * 32 + col;
   const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
   const bool real = r < R;
   const int pos = real ? sp.first + tok : -1;
+  // scores are compared before they are scaled: a negative factor's sign goes to Q, a zero one's
+  // scores are zeros
+  const float c0 = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
+  const float c = c0 == 0.0f ? 1.0f : fabsf(c0);
+  const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u, keep = c0 == 0.0f ? 0u : 0xffffffffu;
   u32x4 qf[kSteps];
   {
     const char *qp = a.q + (sp.t0 + tok) * a.q_stride + ((int64_t)(h * G + g) * D + hi * 8) * 2;
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st) qf[st] = real ? *(const u32x4 *)(qp + st * 32) : (u32x4){0, 0, 0, 0};
+    for (int st = 0; st < kSteps; ++st) {
+      qf[st] = real ? *(const u32x4 *)(qp + st * 32) : (u32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) qf[st][u] = (qf[st][u] ^ flip) & keep;
+    }
   }
-  float m_run = -INFINITY, l_run = 0.0f;
+  float m_run = -INFINITY, l_run = 0.0f;             // the maximum in units of the scaled scores
   f32x16 acc[kCols];
 #pragma unroll
   for (int t = 0; t < kCols; ++t)
 #pragma unroll
     for (int u = 0; u < 16; ++u) acc[t][u] = 0.0f;
-  const float c = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
   const char *kbase = a.c.k + (int64_t)h * a.c.head_stride;
   const char *vbase = a.c.v + (int64_t)h * a.c.head_stride;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
 
-  // addresses of a tile's slots
-  const auto place = [&](int tile) {
-    if (tid < KT) {
-      const int j = lo + tile * KT + tid;
-      const int64_t o = j < end ? place_offset(a.c, slot_place(a.c, trow, (uint32_t)j)) : -1;
-      off[tile & 1][tid] = o;
-      const uint64_t none = __ballot(o < 0);
-      if (tid == 0) holes[tile & 1] = none != 0;
+  // Addresses of eight tiles' slots at a time: page numbers are loaded a chunk ahead of their use.
+  int32_t page[kPlace];
+  const auto page_load = [&](int chunk) {
+#pragma unroll
+    for (int i = 0; i < kPlace; ++i) {
+      const int j = lo + chunk * kChunk * KT + i * kManyThreads + tid;
+      page[i] = -1;
+      if (j < end) page[i] = slot_place(a.c, trow, (uint32_t)j).page;
     }
   };
-  uint32_t gk[kLoads][kRegs], gv[kLoads][kRegs];
-  uint32_t there = 0;
-  const auto fetch = [&](int tile) {
-    there = 0;
+  const auto page_put = [&](int chunk) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
-      int64_t o = off[tile & 1][row];
-      if (o >= 0) there |= 1u << i;
-      o = o < 0 ? 0 : o;
-      if (E4M3) {
+    for (int i = 0; i < kPlace; ++i) {
+      const int at = i * kManyThreads + tid, j = lo + chunk * kChunk * KT + at;
+      const uint32_t row = (uint32_t)j - fast_div(a.c.page, (uint32_t)j) * a.c.page.d;
+      off[chunk & 1][at] = place_offset(a.c, SlotPlace{page[i], row});
+      const uint64_t there = __ballot(page[i] >= 0);
+      if (lane == 0) present[chunk & 1][i * 4 + wave] = there;
+    }
+  };
+  const auto present_at = [&](int tile) -> uint64_t {
+    const int at = tile % kChunk * KT;
+    const uint64_t m = present[(tile / kChunk) & 1][at / 64];
+    return KT == 64 ? m : (m >> (at & 63)) & 0xffffffffu;
+  };
+  const auto off_at = [&](int tile) -> const int64_t * { return &off[(tile / kChunk) & 1][tile % kChunk * KT]; };
+
+  // A tile on its way: 16-bit caches go straight to LDS, 8-bit ones by way of registers.
+  uint32_t gk[kLoads][2], gv[kLoads][2];
+  uint32_t held = 0;
+  const auto fetch = [&](int tile) {
+    const int64_t *po = off_at(tile);
+    if (E4M3) {
+      held = 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
+        int64_t o = po[row];
+        if (o >= 0) held |= 1u << i;
+        o = o < 0 ? 0 : o;
         const u32x2 x = *(const u32x2 *)(kbase + o + p * 8);
         const u32x2 y = *(const u32x2 *)(vbase + o + p * 8);
         gk[i][0] = x.x; gk[i][1] = x.y;
         gv[i][0] = y.x; gv[i][1] = y.y;
-      } else {
-        const u32x4 x = *(const u32x4 *)(kbase + o + p * 16);
-        const u32x4 y = *(const u32x4 *)(vbase + o + p * 16);
+      }
+    } else {
+      const uint32_t ldk = lds_address(sk[tile & 1]) + wave * 1024, ldv = lds_address(sv[tile & 1]) + wave * 1024;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) { gk[i][u % kRegs] = x[u]; gv[i][u % kRegs] = y[u]; }
+      for (int i = 0; i < kLoads; ++i) {
+        const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
+        const int64_t o = po[row];
+        const char *fk = o < 0 ? (const char *)kZeroRow : kbase + o;
+        const char *fv = o < 0 ? (const char *)kZeroRow : vbase + o;
+        dma16(fk + (p ^ k_swizzle<D>(row)) * 16, ldk + i * (kManyThreads * 16));
+        dma16(fv + (p ^ v_swizzle<D>(row)) * 16, ldv + i * (kManyThreads * 16));
       }
     }
   };
-  const auto store = [&](int tile) {
+  const auto arrive = [&](int tile) {
+    if (E4M3) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
-      u32x4 x, y;
-      if (E4M3) {
-        x = widen_e4m3<T>((u32x2){gk[i][0], gk[i][1]});
-        y = widen_e4m3<T>((u32x2){gv[i][0], gv[i][1]});
-      } else {
-        x = (u32x4){gk[i][0], gk[i][1], gk[i][2 % kRegs], gk[i][3 % kRegs]};
-        y = (u32x4){gv[i][0], gv[i][1], gv[i][2 % kRegs], gv[i][3 % kRegs]};
+      for (int i = 0; i < kLoads; ++i) {
+        const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
+        const u32x4 x = widen_e4m3<T>((u32x2){gk[i][0], gk[i][1]});
+        const u32x4 y = widen_e4m3<T>((u32x2){gv[i][0], gv[i][1]});
+        *(u32x4 *)&sk[tile & 1][row * D + (p ^ k_swizzle<D>(row)) * 8] = x;
+        *(u32x4 *)&sv[tile & 1][row * D + (p ^ v_swizzle<D>(row)) * 8] = keep_if(y, (held >> i) & 1u);
       }
-      *(u32x4 *)&sk[tile & 1][row * D + (p ^ k_swizzle<D>(row)) * 8] = x;
-      *(u32x4 *)&sv[tile & 1][row * D + (p ^ v_swizzle<D>(row)) * 8] = keep_if(y, (there >> i) & 1u);
+    } else {
+      dma_wait();
     }
   };
 
-  if (tile0 < tile1) {
-    place(tile0);
-    __syncthreads();
-    fetch(tile0);
-    store(tile0);
-    if (tile0 + 1 < tile1) place(tile0 + 1);
-    __syncthreads();
-  }
-  for (int tile = tile0; tile < tile1; ++tile) {
-    const int buf = tile & 1, j0 = lo + tile * KT;
-    const bool more = tile + 1 < tile1;
-    const bool gaps = holes[buf];
-    if (more) fetch(tile + 1);
+  bool odd = false;
+  // One tile.  masked: some row may not see some slot of it.
+  const auto step = [&](bool masked, int buf, int tile, uint64_t there) {
+    const int j0 = lo + tile * KT;
     f32x16 sc[kSub];
-#pragma unroll
-    for (int t = 0; t < kSub; ++t) {
-#pragma unroll
-      for (int u = 0; u < 16; ++u) sc[t][u] = 0.0f;
-      const int row = t * 32 + col;
-      const uint16_t *kr = &sk[buf][row * D];
-#pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const u32x4 kf = *(const u32x4 *)(kr + ((2 * st + hi) ^ k_swizzle<D>(row)) * 8);
-        sc[t] = T::mfma32(kf, qf[st], sc[t]);
-      }
-    }
-    const bool masked = gaps || j0 + KT - 1 > first_pos || (a.window > 0 && j0 <= last_pos - a.window);
-    if (masked) {
-#pragma unroll
-      for (int t = 0; t < kSub; ++t)
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int at = t * 32 + slot32(u, hi), j = j0 + at;
-          const bool sees = off[buf][at] >= 0 && j <= pos && (a.window <= 0 || j > pos - a.window);
-          if (!sees) sc[t][u] = -INFINITY;
-        }
-    }
-    float top = -INFINITY;
 #pragma unroll
     for (int t = 0; t < kSub; ++t)
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        sc[t][u] *= c;
-        top = fmaxf(top, sc[t][u]);
+      for (int u = 0; u < 16; ++u) sc[t][u] = 0.0f;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int t = 0; t < kSub; ++t) {
+        const int row = t * 32 + col;
+        const u32x4 kf = *(const u32x4 *)&sk[buf][row * D + ((2 * st + hi) ^ k_swizzle<D>(col)) * 8];
+        sc[t] = T::mfma32(kf, qf[st], sc[t]);
       }
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < kSub; ++t) {
+        const int up = pos - j0 - 32 * t;
+        uint32_t own = first_bits(up + 1) & (uint32_t)(there >> (32 * t));   // the row's slots, as bits
+        if (a.window > 0) own &= ~first_bits(up + 1 - a.window);
+        own >>= hi * 4;
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          if (!(own & (1u << slot32(u, 0)))) sc[t][u] = -INFINITY;
+      }
+    }
+    float top = sc[0][0];
+#pragma unroll
+    for (int t = 0; t < kSub; ++t)
+#pragma unroll
+      for (int u = t == 0 ? 1 : 0; u < 16; ++u) top = fmaxf(top, sc[t][u]);
+    top *= c;
     if (__any(top > m_run + kManyLazy)) {
       const float m_new = fmaxf(m_run, half_max(top));
       const float alpha = m_new == -INFINITY ? 1.0f : fast_exp2(m_run - m_new);
@@ -213,63 +250,90 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     for (int t = 0; t < kSub; ++t)
 #pragma unroll
       for (int u = 0; u < 16; u += 2) {
-        const float x = fast_exp2(sc[t][u] - m_use), y = fast_exp2(sc[t][u + 1] - m_use);
+        const float x = fast_exp2(__builtin_fmaf(sc[t][u], c, -m_use)), y = fast_exp2(__builtin_fmaf(sc[t][u + 1], c, -m_use));
         sum += x + y;
         pf[t][u >> 3][(u & 7) >> 1] = T::pack(x, y);
       }
     l_run += sum;
 
-    // V^T operand of slots 16 ks .. of sub-tile t, columns 32 n ..: two transposing reads
-    const auto v_frag = [&](int t, int ks, int n) -> u32x4 {
-      const int l16 = lane & 15, row = t * 32 + ks * 16 + hi * 4 + (l16 >> 2);
-      const int colb = n * 32 + ((lane >> 4) & 1) * 16 + (l16 & 3) * 4;
-      const int p = colb >> 3, in = colb & 7;
-      const uint16_t *x = &sv[buf][row * D + (p ^ v_swizzle<D>(row)) * 8 + in];
-      const uint16_t *y = &sv[buf][(row + 8) * D + (p ^ v_swizzle<D>(row + 8)) * 8 + in];
-      const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)x);
-      const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)y);
-      const u32x2 ub = __builtin_bit_cast(u32x2, u), wb = __builtin_bit_cast(u32x2, w);
-      return (u32x4){ub.x, ub.y, wb.x, wb.y};
-    };
-    bool odd = false;
     if (masked) {
-      for (int i = lane; i < KT * D / 2; i += 64) odd |= any_nonfinite<T>(((const uint32_t *)sv[buf])[i]);
-    }
-    if (masked && __any(odd)) {
-      for (int u = 0; u < KT; ++u) {
-        if (off[buf][u] < 0) continue;
-        const int j = j0 + u, in = u & 31, reg = (in & 3) + 4 * (in >> 3), half = (in >> 2) & 1;
-        uint32_t w = 0;
-#pragma unroll
-        for (int t = 0; t < kSub; ++t)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (t * 8 + k == (u >> 5) * 8 + (reg >> 1)) w = pf[t][k >> 2][k & 3];
-        w = __shfl(w, half * 32 + col);
-        const float p = (reg & 1) ? T::hi(w) : T::lo(w);
-        if (!(j <= pos && (a.window <= 0 || j > pos - a.window))) continue;
-#pragma unroll
-        for (int n = 0; n < kCols; ++n)
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const int d = n * 32 + slot32(k, hi);
-            const uint32_t x = *(const uint32_t *)&sv[buf][u * D + ((d >> 3) ^ v_swizzle<D>(u)) * 8 + (d & 7)];
-            acc[n][k] += p * T::lo(x);
-            acc[n][k + 1] += p * T::hi(x);
-          }
+      // non-finite values of slots that some rows see and others do not wait for the end; each
+      // wave clears them for itself before it reads the tile
+      for (int i = lane; i < KT * kPieces; i += 64) {
+        const int j = j0 + i / kPieces;
+        if (!(j > first_pos || (a.window > 0 && j <= last_pos - a.window))) continue;
+        u32x4 x = ((const u32x4 *)sv[buf])[i];
+        if (clear_nonfinite<T>(x)) {
+          odd = true;
+          ((u32x4 *)sv[buf])[i] = x;
+        }
       }
-    } else {
-#pragma unroll
-      for (int t = 0; t < kSub; ++t)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int n = 0; n < kCols; ++n) acc[n] = T::mfma32(v_frag(t, ks, n), pf[t][ks], acc[n]);
     }
-    if (more) store(tile + 1);
+    // V^T operand of slots 16 ks .. of sub-tile t, columns 32 n ..: two transposing reads
+#pragma unroll
+    for (int t = 0; t < kSub; ++t)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+          const int l16 = lane & 15, rr = hi * 4 + (l16 >> 2), row = t * 32 + ks * 16 + rr;
+          const int p = n * 4 + ((lane >> 4) & 1) * 2 + ((l16 & 3) >> 1), in = (l16 & 1) * 4;
+          const uint16_t *x = &sv[buf][row * D + (p ^ v_swizzle<D>(rr)) * 8 + in];
+          const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)x);
+          const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(x + 8 * D));
+          const u32x2 ub = __builtin_bit_cast(u32x2, u), wb = __builtin_bit_cast(u32x2, w);
+          acc[n] = T::mfma32((u32x4){ub.x, ub.y, wb.x, wb.y}, pf[t][ks], acc[n]);
+        }
+  };
+  const auto turn = [&](int buf, int tile) {
+    if (tile + 1 < tiles) fetch(tile + 1);
+    const int j0 = lo + tile * KT;
+    const uint64_t there = present_at(tile);
+    const bool masked = there != (KT == 64 ? ~(uint64_t)0 : 0xffffffffu) || j0 + KT - 1 > first_pos ||
+                        (a.window > 0 && j0 <= last_pos - a.window);
+    step(masked, buf, tile, there);
+    if (tile % kChunk == kChunk / 2 && (tile / kChunk + 1) * kChunk < tiles) {
+      page_put(tile / kChunk + 1);
+      page_load(tile / kChunk + 2);
+    }
+    if (tile + 1 < tiles) arrive(tile + 1);
     __syncthreads();
-    if (tile + 2 < tile1) place(tile + 2);
+  };
+  if (tiles > 0) {
+    page_load(0);
+    page_put(0);
+    page_load(1);
     __syncthreads();
+    fetch(0);
+    arrive(0);
+    __syncthreads();
+  }
+  for (int tile = 0; tile < tiles; ++tile) turn(tile & 1, tile);
+  if (__any(odd)) {
+    // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
+    const int stop = lo + tiles * KT < end ? lo + tiles * KT : end;
+    for (int j = lo; j < stop; ++j) {
+      if (!(j > first_pos || (a.window > 0 && j <= last_pos - a.window))) continue;
+      const int64_t o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)j));
+      if (o < 0 || j > pos || (a.window > 0 && j <= pos - a.window)) continue;
+#pragma unroll
+      for (int n = 0; n < kCols; ++n)
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+          const char *e = vbase + o + (n * 32 + slot32(k, hi)) * (E4M3 ? 1 : 2);
+          u32x2 x;
+          if (E4M3) {
+            const uint32_t w = *(const uint32_t *)e;
+            x = (u32x2){T::template from_e4m3<false>(w), T::template from_e4m3<true>(w)};
+          } else {
+            x = *(const u32x2 *)e;
+          }
+          acc[n][k] += nonfinite_lo<T>(x.x);
+          acc[n][k + 1] += nonfinite_hi<T>(x.x);
+          acc[n][k + 2] += nonfinite_lo<T>(x.y);
+          acc[n][k + 3] += nonfinite_hi<T>(x.y);
+        }
+    }
   }
 
   l_run = half_sum(l_run);
