@@ -150,7 +150,7 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
   constexpr int kRows = 16 * NR;
   constexpr int kHalfRows = 2 * kRows;     // two waves' rows
   __shared__ union {
-    int64_t off[kFewBlock];
+    int64_t off[kFewBlock + kFewTile];
     float o[kHalfRows * F::kPad];
   } sh;
   __shared__ float sh_m[2][kRows], sh_l[2][kRows];
@@ -162,7 +162,8 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
   const int h = b % H;
   b /= H;
   const int split = b % a.nsplit, s = b / a.nsplit;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, col = lane & 15, q4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), col = lane & 15, q4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
 
   const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
   const int R = sp.m * G;
@@ -220,16 +221,18 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
         present[i / kFewTile + 1] = (uint32_t)(there >> 32);
       }
     }
+    if (tid < kFewTile) sh.off[kFewBlock + tid] = -1;
     __syncthreads();
     int tile = wave;
-    if (tile < ntile) {
-      f.load_k(kbase, sh.off, tile * kFewTile);
-      f.load_v(vbase, sh.off, tile * kFewTile);
-    }
+    const int begin = tile < ntile ? tile * kFewTile : kFewBlock;
+    f.load_k(kbase, sh.off, begin);
+    __builtin_amdgcn_sched_barrier(0);
+    f.load_v(vbase, sh.off, begin);
+    __builtin_amdgcn_sched_barrier(0);
     for (; tile < ntile; tile += kFewWaves) {
       const int at = tile * kFewTile, j0 = blk + at;
-      const bool more = tile + kFewWaves < ntile;
-      const int next = (tile + kFewWaves) * kFewTile;
+      // after the last tile one row, again and again: loads without a condition let K be waited for alone
+      const int next = tile + kFewWaves < ntile ? (tile + kFewWaves) * kFewTile : kFewBlock;
       f32x4 sc[NR][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -242,7 +245,8 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
           for (int nr = 0; nr < NR; ++nr) sc[nr][t] = T::mfma16(kf, qf[nr][st], sc[nr][t]);
         }
       }
-      if (more) f.load_k(kbase, sh.off, next);
+      f.load_k(kbase, sh.off, next);
+      __builtin_amdgcn_sched_barrier(0);
 
       const uint32_t there = present[tile];
       const bool masked = there != 0xffffffffu || j0 + kFewTile - 1 > sp.first || (a.window > 0 && j0 <= last_pos - a.window);
@@ -324,7 +328,7 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
             acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
           }
         }
-      if (more) f.load_v(vbase, sh.off, next);
+      f.load_v(vbase, sh.off, next);
     }
   }
 
