@@ -79,7 +79,8 @@ def lib() -> ctypes.CDLL:
             L.keops_paged_attention.argtypes = [P, P, i64, i32, i32, P, i64, i32, i32, f32, i32, f32, P, P, P, i64, P]
             L.keops_paged_attention_workspace.argtypes = [P, i32, i32, i64, i32, i32, i32, ctypes.POINTER(i64)]
             L.keops_cache_evict.argtypes = [P, P, i64, i32, i32, i32, i32, P, P, P]
-            L.keops_verify_draft.argtypes = [P, P, P, P, P, P, i32, i32, i32, P, P, P]
+            L.keops_verify_draft.argtypes = [P, P, P, P, P, P, i32, i32, i32, P, P, P, i64, P]
+            L.keops_verify_draft_workspace.argtypes = [i32, i32, i32, ctypes.POINTER(i64)]
             L.keops_set_option.argtypes = [ctypes.c_int, i64]
             L.keops_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
             L.keops_status_string.argtypes = [ctypes.c_int]
@@ -88,7 +89,7 @@ def lib() -> ctypes.CDLL:
                       "keops_gauss_grad_y", "keops_gauss_grad_b", "keops_gauss_cg", "keops_gauss_sum_ranges", "keops_gauss_lse_ranges",
                       "keops_gauss_grad_x_ranges", "keops_gauss_max", "keops_gauss_min", "keops_laplace_sum",
                       "keops_kmin", "keops_cache_append", "keops_paged_attention", "keops_paged_attention_workspace",
-                      "keops_cache_evict", "keops_verify_draft",
+                      "keops_cache_evict", "keops_verify_draft", "keops_verify_draft_workspace",
                       "keops_set_option", "keops_version", "keops_profile_read"):
                 getattr(L, f).restype = ctypes.c_int
             _lib = L

@@ -128,14 +128,17 @@ struct VerifyArgs {
   const float *u_accept, *u_sample;
   int32_t seqs, drafts, vocab;
   int32_t *out, *accepted;
+  int32_t pieces, piece;        // a row's pieces (at most 64) and the indices of one
+  double2 *sums;                // [seqs][pieces]: what is left of the target's row, and all of it
 };
+constexpr int kVerifyPiece = 2048;   // indices that a work-group takes at a time
 
 // ---------------------------------------------------------------- launches
 void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st);
 // Variants exist for dim 64, 96, 128 and 256; the API checks before it calls.
 constexpr int kFewRowsMax = 32;      // rows (new tokens x group) of the few-rows form
 constexpr int kManyRowsTile = 128;   // rows of a work-group of the many-rows form
-constexpr int kSumSlotsTile = 128;   // slots of a work-group of the column sums
+constexpr int kSumSlotsTile = 256;   // slots of a work-group of the column sums
 void launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, dim3 grid, hipStream_t st);
 void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
 void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);

@@ -17,10 +17,12 @@ namespace {
 constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr double kMaxWorkspace = 1.0e14;    // more than any device holds; below the 64-bit limit
 // Work-groups that a launch aims for, per compute unit, when it splits a long axis.
-constexpr int64_t kFewWgsPerCu = 4;
+constexpr int64_t kFewWgsPerCu = 4;         // one sequence: equal pieces
+constexpr int64_t kFewWgsPerCuRagged = 16;  // several: small pieces even out their lengths
 constexpr int64_t kManyWgsPerCu = 2;
 constexpr int64_t kSumsWgsPerCu = 2;
-constexpr int kFewChunk = 128;              // least slots of a split: one tile for each wave
+constexpr int kFewChunk = 128;              // least slots of a split: one tile for each wave,
+constexpr int kFewChunkFull = 1024;         // or so many where the sequences alone fill the device
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -101,7 +103,9 @@ int plan_attend(const keops_cache_t &c, int64_t tokens, int heads, int64_t max_q
   if (p->few) {
     p->row_tiles = rows <= 16 ? 1 : 2;
     const int64_t from_tile = std::min<int64_t>(max_len, span + 31);    // a window starts inside a tile
-    p->chunk = std::max<int64_t>(kFewChunk, ceil_div(ceil_div(from_tile * S * H, kFewWgsPerCu * cus), kFewChunk) * kFewChunk);
+    const int64_t least = S * H >= 2 * cus ? kFewChunkFull : kFewChunk;
+    const int64_t aim = (S > 1 ? kFewWgsPerCuRagged : kFewWgsPerCu) * cus;
+    p->chunk = std::max(least, ceil_div(ceil_div(from_tile * S * H, aim), kFewChunk) * kFewChunk);
     p->nsplit = std::max<int64_t>(1, ceil_div(from_tile, p->chunk));
     if ((double)S * (double)H * (double)p->nsplit > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
     p->grid = S * H * p->nsplit;
@@ -319,22 +323,41 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
   return check_launch();
 }
 
-int verify_entry(const VerifyArgs &a, hipStream_t st) {
-  if (a.seqs < 0 || a.drafts < 0 || a.vocab < 1) return KEOPS_ERR_INVALID_ARG;
+// A row in at most 64 pieces of whole steps (the pieces' sums are joined by one wave).
+void plan_verify(VerifyArgs *a) {
+  a->piece = (int32_t)(ceil_div(ceil_div(a->vocab, 64), kVerifyPiece) * kVerifyPiece);
+  a->pieces = (int32_t)ceil_div(a->vocab, a->piece);
+}
+
+int check_verify(int seqs, int drafts, int vocab) {
+  if (seqs < 0 || drafts < 0 || vocab < 1) return KEOPS_ERR_INVALID_ARG;
+  if (drafts > 1 << 20 || vocab > 1 << 30 || seqs > 1 << 24) return KEOPS_ERR_UNSUPPORTED;
+  return KEOPS_OK;
+}
+
+int verify_entry(VerifyArgs a, void *workspace, int64_t workspace_bytes, hipStream_t st) {
+  if (int rc = check_verify(a.seqs, a.drafts, a.vocab)) return rc;
   for (const void *p : {(const void *)a.target, (const void *)a.draft, (const void *)a.tokens, (const void *)a.counts,
                         (const void *)a.u_accept, (const void *)a.u_sample, (const void *)a.out, (const void *)a.accepted})
     if (!aligned(p, 4)) return KEOPS_ERR_INVALID_ARG;
+  if (workspace && (!aligned(workspace, 256) || workspace_bytes < 0)) return KEOPS_ERR_INVALID_ARG;
   if (a.seqs == 0) return KEOPS_OK;
   if (!a.target || !a.counts || !a.u_sample || !a.out || !a.accepted) return KEOPS_ERR_INVALID_ARG;
   if (a.drafts > 0 && (!a.tokens || !a.u_accept)) return KEOPS_ERR_INVALID_ARG;
-  if (a.drafts > 1 << 20 || a.vocab > 1 << 30) return KEOPS_ERR_UNSUPPORTED;
-  const int64_t ob = (int64_t)a.seqs * (a.drafts + 1) * 4, ab = (int64_t)a.seqs * 4, tb = ob * a.vocab;
-  if (overlaps(a.out, ob, a.accepted, ab) || overlaps(a.out, ob, a.tokens, (int64_t)a.seqs * a.drafts * 4) ||
-      overlaps(a.out, ob, a.target, tb) || overlaps(a.out, ob, a.counts, ab) || overlaps(a.accepted, ab, a.counts, ab) ||
-      overlaps(a.accepted, ab, a.target, tb) || overlaps(a.out, ob, a.u_accept, (int64_t)a.seqs * a.drafts * 4) ||
-      overlaps(a.out, ob, a.u_sample, ab) || overlaps(a.accepted, ab, a.u_sample, ab))
-    return KEOPS_ERR_INVALID_ARG;
+  const int64_t ob = (int64_t)a.seqs * (a.drafts + 1) * 4, ab = (int64_t)a.seqs * 4, kb = (int64_t)a.seqs * a.drafts * 4;
+  if ((double)ob * a.vocab > kMaxWorkspace) return KEOPS_ERR_UNSUPPORTED;
+  const int64_t tb = ob * a.vocab, db = kb * a.vocab;
+  if (overlaps(a.out, ob, a.accepted, ab)) return KEOPS_ERR_INVALID_ARG;
+  const struct { const void *p; int64_t bytes; } inputs[] = {{a.target, tb}, {a.draft, db}, {a.tokens, kb}, {a.counts, ab},
+                                                            {a.u_accept, kb}, {a.u_sample, ab}};
+  for (const auto &in : inputs)
+    if (overlaps(a.out, ob, in.p, in.bytes) || overlaps(a.accepted, ab, in.p, in.bytes)) return KEOPS_ERR_INVALID_ARG;
   (void)hipGetLastError();
+  plan_verify(&a);
+  Workspace own;
+  char *ws = nullptr;
+  if (int rc = take_workspace(own, workspace, workspace_bytes, (int64_t)a.seqs * a.pieces * 16, st, &ws)) return rc;
+  a.sums = (double2 *)ws;
   launch_verify(a, st);
   return check_launch();
 }
@@ -396,13 +419,28 @@ int keops_cache_evict(const keops_cache_t *cache, const int32_t *new_table, int6
 
 int keops_verify_draft(const float *target, const float *draft, const int32_t *tokens, const int32_t *counts,
                        const float *u_accept, const float *u_sample, int32_t seqs, int32_t drafts, int32_t vocab,
-                       int32_t *out, int32_t *accepted, void *stream) {
+                       int32_t *out, int32_t *accepted, void *workspace, int64_t workspace_bytes, void *stream) {
   try {
-    return verify_entry({target, draft, tokens, counts, u_accept, u_sample, seqs, drafts, vocab, out, accepted},
-                        (hipStream_t)stream);
+    VerifyArgs a{};
+    a.target = target; a.draft = draft; a.tokens = tokens; a.counts = counts;
+    a.u_accept = u_accept; a.u_sample = u_sample;
+    a.seqs = seqs; a.drafts = drafts; a.vocab = vocab;
+    a.out = out; a.accepted = accepted;
+    return verify_entry(a, workspace, workspace_bytes, (hipStream_t)stream);
   } catch (...) {
     return KEOPS_ERR_ALLOC;
   }
+}
+
+int keops_verify_draft_workspace(int32_t seqs, int32_t drafts, int32_t vocab, int64_t *bytes) {
+  if (!bytes) return KEOPS_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (int rc = check_verify(seqs, drafts, vocab)) return rc;
+  VerifyArgs a{};
+  a.vocab = vocab;
+  plan_verify(&a);
+  *bytes = (int64_t)seqs * a.pieces * 16;
+  return KEOPS_OK;
 }
 
 }  // extern "C"

@@ -5,10 +5,13 @@
 // slot).  Kept slots move, in their order, to slots 0 .. of the pages in new_table, keys,
 // values and weights alike; n <= budget keeps them all.
 //
-// Selection: one work-group per (sequence, head) finds the smallest kept weight by four passes
-// over 8 bits of an order-preserving whole number (counts in LDS; integers, so the order of
-// the additions does not matter), then one scan of counts gives every slot its place.  The
-// move is a second kernel, one 16-byte piece of a key and of a value row per thread.
+// Selection: one work-group per (sequence, head) finds the smallest kept weight by three passes
+// over 11, 11 and 10 bits of an order-preserving whole number (counts in LDS; integers, so the
+// order of the additions does not matter), then one scan of counts gives every slot its place.
+// It is bound by the latency of its steps: page numbers and weights are loaded eight at a time,
+// and a wave whose lanes all meet one count adds to it once (cleared weights are all equal).
+// The move is a second kernel, one 16-byte piece of a key and of a value row per thread, bound
+// by HBM.
 #include "paged.h"
 
 namespace kmi {
@@ -16,8 +19,10 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / kWave;
-constexpr int kHistCopies = 8;          // lanes of a wave spread over copies: fewer collisions
-constexpr int kSelectCache = 32768;     // weights held in LDS (128 KB); longer rows are read again
+constexpr int kBins = 2048;             // counts of a pass
+constexpr int kHistCopies = 2;          // even and odd lanes: fewer collisions
+constexpr int kSelectCache = 32768;     // weights held in LDS (132 KB); longer rows are read again
+constexpr int kBatch = 8;
 
 // Whole numbers ordered as the floats are; -0 equals 0, NaN above everything.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -27,7 +32,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 struct SelectShared {
-  uint32_t hist[256 * kHistCopies];
+  uint32_t hist[kBins * kHistCopies];
   uint32_t wave_gt[kSelectWaves], wave_eq[kSelectWaves];
   uint32_t prefix, need;
 };
@@ -56,53 +61,98 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
   for (int r = tid; r < recent; r += kSelectThreads) kept[a.budget - recent + r] = n - recent + r;
   if (need0 == 0) return;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
-  const auto load = [&](int i) -> uint32_t {
-    const SlotPlace p = slot_place(a.c, trow, (uint32_t)(sink + i));
-    // an absent slot comes last
-    return p.page < 0 ? 0u : weight_key(a.c.weights[((int64_t)p.page * H + h) * a.c.page.d + p.row]);
+  // eight keys, slots first + 1024 u: an absent slot's is 0, the least
+  const auto load = [&](int first, uint32_t *k) {
+    SlotPlace p[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = first + u * kSelectThreads;
+      p[u] = SlotPlace{-1, 0};
+      if (i < M) p[u] = slot_place(a.c, trow, (uint32_t)(sink + i));
+    }
+    float w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      w[u] = 0.0f;
+      if (p[u].page >= 0) w[u] = a.c.weights[((int64_t)p[u].page * H + h) * a.c.page.d + p[u].row];
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) k[u] = p[u].page < 0 ? 0u : weight_key(w[u]);
   };
   const bool held = cache_at(M - 1) < cache_words;
-  if (held)
-    for (int i = tid; i < M; i += kSelectThreads) cache[cache_at(i)] = load(i);
-  const auto key = [&](int i) -> uint32_t { return held ? cache[cache_at(i)] : load(i); };
-
-  // the need-th largest key, 8 bits at a time
-  uint32_t prefix = 0, need = (uint32_t)need0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kHistCopies; i += kSelectThreads) sh.hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < M; i += kSelectThreads) {
-      const uint32_t k = key(i);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&sh.hist[((k >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1u);
+  if (held) {
+    for (int i = tid; i < M; i += kBatch * kSelectThreads) {
+      uint32_t k[kBatch];
+      load(i, k);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + u * kSelectThreads < M) cache[cache_at(i + u * kSelectThreads)] = k[u];
     }
+  }
+  const auto key = [&](int i) -> uint32_t {
+    if (held) return cache[cache_at(i)];
+    const SlotPlace p = slot_place(a.c, trow, (uint32_t)(sink + i));
+    return p.page < 0 ? 0u : weight_key(a.c.weights[((int64_t)p.page * H + h) * a.c.page.d + p.row]);
+  };
+
+  // the need-th largest key, digit by digit
+  uint32_t prefix = 0, need = (uint32_t)need0;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+    for (int i = tid; i < kBins * kHistCopies; i += kSelectThreads) sh.hist[i] = 0;
     __syncthreads();
-    if (wave == 0) {
-      // lane l holds bins 4l .. 4l+3; counts from the top bin down
-      uint32_t cnt[4], own = 0;
+    for (int base = tid; base - tid < M; base += kBatch * kSelectThreads) {
+      uint32_t k[kBatch];
+      if (held) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        cnt[b] = 0;
-        for (int c = 0; c < kHistCopies; ++c) cnt[b] += sh.hist[(4 * lane + b) * kHistCopies + c];
-        own += cnt[b];
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = base + u * kSelectThreads;
+          k[u] = i < M ? cache[cache_at(i)] : 0u;
+        }
+      } else {
+        load(base, k);
       }
-      uint32_t above = own;      // sum over lanes >= this one
 #pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t up = __shfl_down(above, o);
-        if (lane + o < kWave) above += up;
-      }
-      above -= own;              // strictly above
-      if (above < need && need <= above + own) {
-#pragma unroll
-        for (int b = 3; b >= 0; --b) {
-          if (above < need && need <= above + cnt[b]) {
-            sh.prefix = prefix | ((uint32_t)(4 * lane + b) << shift);
-            sh.need = need - above;
-          }
-          above += cnt[b];
+      for (int u = 0; u < kBatch; ++u) {
+        const bool in = base + u * kSelectThreads < M && (pass == 0 || (k[u] >> (shift + bits)) == (prefix >> (shift + bits)));
+        const uint32_t bin = (k[u] >> shift) & ((1u << bits) - 1u);
+        const uint64_t who = __ballot(in);
+        if (!who) continue;
+        const uint32_t one = __builtin_amdgcn_readlane(bin, __ffsll((unsigned long long)who) - 1);
+        if (__ballot(in && bin != one) == 0) {
+          if (lane == 0) atomicAdd(&sh.hist[one * kHistCopies], (uint32_t)__popcll(who));
+        } else if (in) {
+          atomicAdd(&sh.hist[bin * kHistCopies + (lane & (kHistCopies - 1))], 1u);
         }
       }
+    }
+    __syncthreads();
+    // thread t has the counts 2 t and 2 t + 1 from the top
+    uint32_t cnt[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int bin = kBins - 1 - (2 * tid + b);
+      cnt[b] = sh.hist[bin * kHistCopies] + sh.hist[bin * kHistCopies + 1];
+    }
+    const uint32_t own = cnt[0] + cnt[1];
+    uint32_t upto = own;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const uint32_t up = __shfl_up(upto, o);
+      if (lane >= o) upto += up;
+    }
+    if (lane == kWave - 1) sh.wave_gt[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) upto += sh.wave_gt[w];
+    uint32_t above = upto - own;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (above < need && need <= above + cnt[b]) {
+        sh.prefix = prefix | ((uint32_t)(kBins - 1 - (2 * tid + b)) << shift);
+        sh.need = need - above;
+      }
+      above += cnt[b];
     }
     __syncthreads();
     prefix = sh.prefix;

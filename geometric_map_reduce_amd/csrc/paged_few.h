@@ -62,17 +62,29 @@ struct FewRows {
   uint32_t kr[2][kKRegs];
   uint32_t vr[8][kVRegs];
 
-  // K rows of the tile: lane l has slot l % 16 of each 16, columns 32 s + 8 (l / 16) ..+8.
+  // 8-bit rows of a multiple of 64 bytes: a lane's 16 bytes are the operands of two matrix steps,
+  // columns 64 s + 16 (l / 16) + 8 u .. of steps 2 s + u.  Any order of the columns will do that Q shares.
+  static constexpr bool kWide = E4M3 && D % 64 == 0;
+  static __device__ __forceinline__ int step_column(int s, int q) {
+    return kWide ? (s >> 1) * 64 + q * 16 + (s & 1) * 8 : s * 32 + q * 8;
+  }
+
+  // K rows of the tile: lane l has slot l % 16 of each 16, columns step_column(s, l / 16) ..+8 of step s.
   __device__ __forceinline__ void load_k(const char *base, const int64_t *off, int at) {
     const int lane = threadIdx.x & (kWave - 1), row = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       int64_t o = off[at + 16 * t + row];
       o = o < 0 ? 0 : o;
-      const char *p = base + o + q * 8 * kBytes;
+      const char *p = base + o + step_column(0, q) * kBytes;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        if (E4M3) {
+        if (kWide) {
+          if (s & 1) continue;
+          const u32x4 w = *(const u32x4 *)(p + s * 32);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) kr[t][(2 * s + u) % kKRegs] = w[u];
+        } else if (E4M3) {
           const u32x2 w = *(const u32x2 *)(p + s * 32);
           kr[t][2 * s] = w.x;
           kr[t][2 * s + 1] = w.y;
@@ -145,7 +157,7 @@ struct FewRows {
 };
 
 template <class T, bool E4M3, int D, int NR, bool SCORES>
-__global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, E4M3, D, NR>;
   constexpr int kRows = 16 * NR;
   constexpr int kHalfRows = 2 * kRows;     // two waves' rows
@@ -184,9 +196,10 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : 2)) void attend_fe
     const int r = 16 * nr + col;
     const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
     pos[nr] = r < R ? sp.first + tok : -1;
-    const char *qp = a.q + (sp.t0 + tok) * a.q_stride + ((int64_t)(h * G + g) * D + q4 * 8) * 2;
+    const char *qp = a.q + (sp.t0 + tok) * a.q_stride + (int64_t)(h * G + g) * D * 2;
 #pragma unroll
-    for (int st = 0; st < F::kSteps; ++st) qf[nr][st] = r < R ? *(const u32x4 *)(qp + st * 64) : (u32x4){0, 0, 0, 0};
+    for (int st = 0; st < F::kSteps; ++st)
+      qf[nr][st] = r < R ? *(const u32x4 *)(qp + F::step_column(st, q4) * 2) : (u32x4){0, 0, 0, 0};
   }
 
   float m_run[NR], l_run[NR];

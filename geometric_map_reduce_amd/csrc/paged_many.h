@@ -16,7 +16,7 @@
 //  * Running maximum, sums, absent slots and non-finite values as in the few-rows form.
 //
 // Column sums: one pass over Q with K in registers.  The rows' lse is known, so
-// p = exp(z - lse) needs no running maximum; a wave owns 32 slots and adds up the rows of Q tiles
+// p = exp(z - lse) needs no running maximum; a wave owns 64 slots and adds up the rows of Q tiles
 // staged in LDS.
 #pragma once
 
@@ -365,15 +365,17 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   }
 }
 
-// Column sums.  Grid: slot tiles x heads x sequences x row splits.
+// Column sums.  Grid: slot tiles x heads x sequences x row splits.  A wave holds K of 64 slots and
+// reads each Q tile from LDS once for both halves: with 32 the LDS reads alone would take as long
+// as the products.
 template <class T, bool E4M3, int D>
 __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_kernel(AttendArgs a) {
   constexpr int QT = 64;                             // rows of a tile
   constexpr int kSteps = D / 16, kPieces = D / 8;
   constexpr int kLoads = QT * kPieces / kManyThreads;
   __shared__ __align__(16) uint16_t sq[2][QT * D];
-  __shared__ __align__(16) float sl[2][QT];
-  __shared__ int sp_[2][QT];
+  __shared__ __align__(16) float sl[2][QT];          // -lse of the rows in log2 units
+  __shared__ __align__(16) int sp_[2][QT];           // their slots
 
   const int H = a.c.heads, G = a.group;
   const int64_t heads = (int64_t)H * G;
@@ -384,21 +386,25 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
   const int st = b % nst;
   b /= nst;
   const int s = b % a.c.seqs, rsplit = b / a.c.seqs;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hi = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, hi = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
   const int slot0 = st * kSumSlotsTile;
   if (slot0 >= sp.n) return;
-  const int j = slot0 + wave * 32 + col;
-  SlotPlace pl{-1, 0};
-  if (j < sp.n) pl = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)j);
-  const int64_t o = place_offset(a.c, pl);
-  u32x4 kf[kSteps];
-  {
+  int j[2];
+  SlotPlace pl[2];
+  u32x4 kf[2][kSteps];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    j[x] = slot0 + wave * 64 + x * 32 + col;
+    pl[x] = SlotPlace{-1, 0};
+    if (j[x] < sp.n) pl[x] = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)j[x]);
+    const int64_t o = place_offset(a.c, pl[x]);
     const char *kp = a.c.k + (int64_t)h * a.c.head_stride + (o < 0 ? 0 : o);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      if (E4M3) kf[i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
-      else kf[i] = *(const u32x4 *)(kp + i * 32 + hi * 16);
+      if (E4M3) kf[x][i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
+      else kf[x][i] = *(const u32x4 *)(kp + i * 32 + hi * 16);
     }
   }
   // tokens that see any slot of the tile
@@ -429,10 +435,10 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
     if (tid < QT) {
       const int r = r0 + tile * QT + tid;
       const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
-      float l = INFINITY;        // a row that is not there, or sees nothing, gives 0
+      float l = -INFINITY;       // a row that is not there, or sees nothing, gives 0
       if (r < r1) {
-        l = a.lse[(sp.t0 + tok) * heads + h * G + g] * kLog2e;
-        if (l == -INFINITY) l = INFINITY;
+        l = -kLog2e * a.lse[(sp.t0 + tok) * heads + h * G + g];
+        if (l == INFINITY) l = -INFINITY;
       }
       gl = l;
       gp = r < r1 ? sp.first + tok : -1;
@@ -449,7 +455,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
       sp_[buf][tid] = gp;
     }
   };
-  float sum = 0.0f, low = 0.0f;   // running sum and what its roundings lost
+  // a tile's terms are added up first: the running sums take one rounding for each
+  float sum[2] = {0.0f, 0.0f}, low[2] = {0.0f, 0.0f};   // and what those roundings lost
   if (tile0 < tile1) {
     fetch(tile0);
     store(0);
@@ -463,45 +470,59 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
     const int ra = r0 + tile * QT, rb = ra + QT < r1 ? ra + QT - 1 : r1 - 1;
     const int pa = sp.first + (int)fast_div(a.gdiv, (uint32_t)ra), pb = sp.first + (int)fast_div(a.gdiv, (uint32_t)rb);
     const bool masked = slot0 + kSumSlotsTile - 1 > pa || (a.window > 0 && slot0 <= pb - a.window);
+    float part[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < QT / 32; ++t) {
-      f32x16 sc;
+      f32x16 sc[2];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) sc[u] = 0.0f;
+      for (int u = 0; u < 16; ++u) sc[0][u] = sc[1][u] = 0.0f;
       const int row = t * 32 + col;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const u32x4 qf = *(const u32x4 *)&sq[buf][row * D + ((2 * i + hi) ^ k_swizzle<D>(row)) * 8];
-        sc = T::mfma32(qf, kf[i], sc);
+        const u32x4 qf = *(const u32x4 *)&sq[buf][row * D + ((2 * i + hi) ^ k_swizzle<D>(col)) * 8];
+        sc[0] = T::mfma32(qf, kf[0][i], sc[0]);
+        sc[1] = T::mfma32(qf, kf[1][i], sc[1]);
       }
-      float part = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const f32x4 l = *(const f32x4 *)&sl[buf][t * 32 + q * 8 + hi * 4];
+        float p[2][4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float z = sc[q * 4 + u] * c;
-          if (masked) {
-            const int p = sp_[buf][t * 32 + q * 8 + hi * 4 + u];
-            if (!(j <= p && (a.window <= 0 || j > p - a.window))) z = -INFINITY;
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) p[x][u] = fast_exp2(__builtin_fmaf(sc[x][q * 4 + u], c, l[u]));
+        if (masked) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int at = sp_[buf][t * 32 + q * 8 + hi * 4 + u];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (j[x] > at || (a.window > 0 && j[x] <= at - a.window)) p[x][u] = 0.0f;
           }
-          part += z == -INFINITY ? 0.0f : fast_exp2(z - l[u]);
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) part[x] += (p[x][0] + p[x][1]) + (p[x][2] + p[x][3]);
       }
-      const float y = part - low, x = sum + y;
-      low = (x - sum) - y;
-      sum = x;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float y = part[x] - low[x], z = sum[x] + y;
+      low[x] = (z - sum[x]) - y;
+      sum[x] = z;
     }
     if (more) store(buf ^ 1);
     __syncthreads();
   }
-  sum = half_sum(sum);
-  if (j >= sp.n || hi) return;
-  if (a.nrow > 1) {
-    a.part_w[((int64_t)rsplit * a.c.seqs * H + (int64_t)s * H + h) * a.max_len + j] = sum;
-  } else if (pl.page >= 0) {
-    float *w = a.c.weights + ((int64_t)pl.page * H + h) * a.c.page.d + pl.row;
-    *w = a.decay != 0.0f ? a.decay * *w + sum : sum;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const float w = half_sum(sum[x]);
+    if (j[x] >= sp.n || hi) continue;
+    if (a.nrow > 1) {
+      a.part_w[((int64_t)rsplit * a.c.seqs * H + (int64_t)s * H + h) * a.max_len + j[x]] = w;
+    } else if (pl[x].page >= 0) {
+      float *to = a.c.weights + ((int64_t)pl[x].page * H + h) * a.c.page.d + pl[x].row;
+      *to = a.decay != 0.0f ? a.decay * *to + w : w;
+    }
   }
 }
 

@@ -9,42 +9,38 @@
 // draft stands for certainty: q_r is 1 at x_r and 0 elsewhere.
 //
 // Running sums are in 64 bits: a 32-bit sum of 10^5 probabilities is off by more than the
-// distance between neighbouring borders.  One read of two rows of the vocabulary: latency and
-// one compute unit's read rate bound it.
+// distance between neighbouring borders.
+//
+// Two kernels: sums of pieces of the row by many work-groups (one read of two rows of the
+// vocabulary, bound by HBM for a batch and by latency for one sequence), then one work-group per
+// sequence that finds the piece and looks through it.
 #include "paged.h"
 
 namespace kmi {
 namespace {
 
-constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / kWave;
+constexpr int kPer = kVerifyPiece / kVerifyThreads;     // indices of a thread in a piece's step
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o);
   return v;
 }
-
-// Mass of index i: what the next token is drawn from.
-struct Mass {
-  const float *p, *q;    // q null: the whole of p, but for index `skip`
-  int skip;
-  __device__ __forceinline__ double operator()(int i) const {
-    double m = (double)p[i];
-    if (q) m -= (double)q[i];
-    if (i == skip) m = 0.0;
-    return m > 0.0 ? m : 0.0;
+__device__ __forceinline__ double wave_scan_f64(double v) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const double up = __shfl_up(v, o);
+    if (lane >= o) v += up;
   }
-};
+  return v;
+}
 
-__global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyArgs a) {
-  __shared__ double wave_total[kVerifyWaves];
-  const int s = blockIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int K = a.drafts, V = a.vocab;
-  int n = a.counts[s];
-  n = n < 0 ? 0 : (n > K ? K : n);
-  // every wave finds the first refusal by itself, 64 drafted tokens at a time
-  int r = n;
+// The first refused of the n drafted tokens (n: none), found by every wave for itself.
+__device__ __forceinline__ int first_refused(const VerifyArgs &a, int s, int n) {
+  const int lane = threadIdx.x & (kWave - 1), K = a.drafts, V = a.vocab;
   for (int base = 0; base < n; base += kWave) {
     const int i = base + lane;
     bool refused = false;
@@ -58,83 +54,141 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyArgs a) {
       refused = !((double)a.u_accept[(int64_t)s * K + i] * qx < px);
     }
     const uint64_t who = __ballot(refused);
-    if (who) {
-      r = base + __ffsll((unsigned long long)who) - 1;
-      break;
-    }
+    if (who) return base + __ffsll((unsigned long long)who) - 1;
   }
-  Mass mass{a.target + ((int64_t)s * (K + 1) + r) * V, nullptr, -1};
+  return n;
+}
+
+__device__ __forceinline__ int drafted(const VerifyArgs &a, int s) {
+  const int n = a.counts[s];
+  return n < 0 ? 0 : (n > a.drafts ? a.drafts : n);
+}
+
+// What the next token is drawn from: the target's row, less the draft's after a refusal.
+struct Rows {
+  const float *p, *q;    // q null: nothing to take off but at index `skip`
+  int skip;
+};
+__device__ __forceinline__ Rows rows_of(const VerifyArgs &a, int s, int r, int n) {
+  Rows x{a.target + ((int64_t)s * (a.drafts + 1) + r) * a.vocab, nullptr, -1};
   if (r < n) {
-    if (a.draft) mass.q = a.draft + ((int64_t)s * K + r) * V;
-    else mass.skip = a.tokens[(int64_t)s * K + r];
+    if (a.draft) x.q = a.draft + ((int64_t)s * a.drafts + r) * a.vocab;
+    else x.skip = a.tokens[(int64_t)s * a.drafts + r];
   }
-  // wave w owns indices [w L, (w + 1) L)
-  const int L = ((V + kVerifyWaves - 1) / kVerifyWaves + kWave - 1) / kWave * kWave;
-  const int i0 = wave * L < V ? wave * L : V, i1 = i0 + L < V ? i0 + L : V;
-  int owner = -1;           // the wave whose range holds the goal
-  double goal = 0.0, before = 0.0;
-  for (int attempt = 0; attempt < 2; ++attempt) {
-    double sum = 0.0;
-    for (int i = i0 + lane; i < i1; i += kWave) sum += mass(i);
-    sum = wave_sum_f64(sum);
-    __syncthreads();
-    if (lane == 0) wave_total[wave] = sum;
-    __syncthreads();
-    double total = 0.0;
-    for (int w = 0; w < kVerifyWaves; ++w) total += wave_total[w];
-    goal = (double)a.u_sample[s] * total;
-    if (total > 0.0 || (!mass.q && mass.skip < 0)) break;
-    mass.q = nullptr;       // nothing left over: the target's own row
-    mass.skip = -1;
-  }
-  double run = 0.0;
-  int last = -1;
-  for (int w = 0; w < kVerifyWaves; ++w) {
-    if (wave_total[w] > 0.0) last = w;
-    if (owner < 0 && run + wave_total[w] > goal) {
-      owner = w;
-      before = run;
-    }
-    run += wave_total[w];
-  }
-  if (owner < 0) {          // u of 1 or more: the last index with mass
-    owner = last;
-    goal = 1.0 / 0.0;
-  }
-  if (wave == (owner < 0 ? 0 : owner)) {
-    // the last index with mass stands in where rounding leaves every running sum at or below the goal
-    int pick = V - 1;
-    double c = before;
-    for (int i = i0; i < i1 && owner >= 0; i += kWave) {
-      const double m = i + lane < i1 ? mass(i + lane) : 0.0;
-      double up = m;
+  return x;
+}
+__device__ __forceinline__ double positive(double v) { return v > 0.0 ? v : 0.0; }
+
+// Sums of piece b of sequence s: of what is left, and of the whole of the target's row.
+__global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyArgs a) {
+  __shared__ double red[2][kVerifyWaves];
+  const int s = blockIdx.x / a.pieces, b = blockIdx.x - s * a.pieces;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int n = drafted(a, s), r = first_refused(a, s, n);
+  const Rows x = rows_of(a, s, r, n);
+  const int i0 = b * a.piece, i1 = i0 + a.piece < a.vocab ? i0 + a.piece : a.vocab;
+  double left = 0.0, whole = 0.0;
+  for (int i = i0 + tid; i < i1; i += kVerifyPiece) {
+    float p[kPer], q[kPer];
 #pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const double u = __shfl_up(up, o);
-        if (lane >= o) up += u;
-      }
-      up += c;
-      const uint64_t has = __ballot(m > 0.0), over = __ballot(m > 0.0 && up > goal);
-      if (over) {
-        pick = i + __ffsll((unsigned long long)over) - 1;
-        break;
-      }
-      if (has) pick = i + 63 - __clzll((long long)has);
-      c = __shfl(up, kWave - 1);
+    for (int u = 0; u < kPer; ++u) {
+      const int k = i + u * kVerifyThreads;
+      p[u] = k < i1 ? x.p[k] : 0.0f;
+      q[u] = x.q && k < i1 ? x.q[k] : 0.0f;
+      if (k == x.skip) q[u] = p[u];
     }
-    if (lane == 0) {
-      a.out[(int64_t)s * (K + 1) + r] = pick;
-      a.accepted[s] = r;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      left += positive((double)p[u] - (double)q[u]);
+      whole += positive((double)p[u]);
     }
   }
-  for (int i = threadIdx.x; i <= K; i += kVerifyThreads)
-    if (i != r) a.out[(int64_t)s * (K + 1) + i] = i < r ? a.tokens[(int64_t)s * K + i] : -1;
+  left = wave_sum_f64(left);
+  whole = wave_sum_f64(whole);
+  if (lane == 0) {
+    red[0][wave] = left;
+    red[1][wave] = whole;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double l = 0.0, w = 0.0;
+    for (int k = 0; k < kVerifyWaves; ++k) {
+      l += red[0][k];
+      w += red[1][k];
+    }
+    a.sums[(int64_t)s * a.pieces + b] = make_double2(l, w);
+    if (b == 0) a.accepted[s] = r;
+  }
+}
+
+__global__ __launch_bounds__(kVerifyThreads) void verify_pick_kernel(VerifyArgs a) {
+  __shared__ double wave_total[kVerifyWaves];
+  __shared__ int first, last;
+  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int K = a.drafts, V = a.vocab, r = a.accepted[s], n = drafted(a, s);
+  if (tid == 0) {
+    first = V;
+    last = -1;
+  }
+  // every wave finds the piece that holds the goal: the first whose running sum passes it, or
+  // the last with mass (u of 1 or more)
+  double2 own = make_double2(0.0, 0.0);
+  if (lane < a.pieces) own = a.sums[(int64_t)s * a.pieces + lane];
+  const bool any = __any(own.x > 0.0);      // nothing left over: the target's own row
+  const double mass = any ? own.x : own.y, upto = wave_scan_f64(mass);
+  double goal = (double)a.u_sample[s] * __shfl(upto, kWave - 1);
+  const uint64_t over = __ballot(mass > 0.0 && upto > goal), has = __ballot(mass > 0.0);
+  int pick = V - 1;
+  if (has) {                                 // the same in every wave
+    const int b = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)has);
+    if (!over) goal = INFINITY;
+    double before = b > 0 ? __shfl(upto, b - 1) : 0.0;
+    Rows x = rows_of(a, s, r, n);
+    if (!any) x = Rows{x.p, nullptr, -1};
+    const int i0 = b * a.piece, i1 = i0 + a.piece < V ? i0 + a.piece : V;
+    for (int base = i0; base < i1; base += kVerifyPiece) {
+      // a thread's kPer indices in a row
+      double m[kPer], sum = 0.0;
+      const int i = base + tid * kPer;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int k = i + u;
+        const float p = k < i1 ? x.p[k] : 0.0f;
+        float q = x.q && k < i1 ? x.q[k] : 0.0f;
+        if (k == x.skip) q = p;
+        m[u] = positive((double)p - (double)q);
+        sum += m[u];
+      }
+      const double scan = wave_scan_f64(sum);
+      __syncthreads();
+      if (lane == kWave - 1) wave_total[wave] = scan;
+      __syncthreads();
+      double c = before + (scan - sum);
+      for (int w = 0; w < wave; ++w) c += wave_total[w];
+      for (int w = 0; w < kVerifyWaves; ++w) before += wave_total[w];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        c += m[u];
+        if (m[u] > 0.0) {
+          if (c > goal) atomicMin(&first, i + u);
+          atomicMax(&last, i + u);
+        }
+      }
+      __syncthreads();
+      if (first < V) break;
+    }
+    // the last index with mass stands in where rounding leaves every running sum at or below the goal
+    pick = first < V ? first : last;
+  }
+  for (int i = tid; i <= K; i += kVerifyThreads)
+    a.out[(int64_t)s * (K + 1) + i] = i < r ? a.tokens[(int64_t)s * K + i] : (i == r ? pick : -1);
 }
 
 }  // namespace
 
 void launch_verify(const VerifyArgs &a, hipStream_t st) {
-  verify_kernel<<<dim3((unsigned)a.seqs), kVerifyThreads, 0, st>>>(a);
+  verify_sums_kernel<<<dim3((unsigned)(a.seqs * a.pieces)), kVerifyThreads, 0, st>>>(a);
+  verify_pick_kernel<<<dim3((unsigned)a.seqs), kVerifyThreads, 0, st>>>(a);
 }
 
 }  // namespace kmi

@@ -112,6 +112,19 @@ def _keep(stream, dev, *tensors):
                 t.record_stream(s)
 
 
+def _graph_workspace(name, dev, *args):
+    """(address, bytes, tensor) of a call's workspace under stream capture, from the graph's own pool, where it
+    lives as long as the graph; nothing otherwise: the library has its own."""
+    if not torch.cuda.is_current_stream_capturing():
+        return None, 0, None
+    need = ctypes.c_int64(0)
+    _check(name, getattr(lib(), name + "_workspace")(*args, ctypes.byref(need)))
+    if need.value == 0:
+        return None, 0, None
+    buf = torch.empty(need.value + 256, dtype=torch.uint8, device=dev)
+    return (buf.data_ptr() + 255) // 256 * 256, need.value, buf
+
+
 def keops_cache_append(k, v, k_pages, v_pages, page_table, lens, starts, weights=None, k_scale=None, v_scale=None,
                        stream=None):
     """Write rows starts[s] .. starts[s+1] of k and v [tokens, heads, dim] to the last slots of sequence s
@@ -149,17 +162,9 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     s = _stream(stream, dev)
     kind = _TYPES[q.dtype]
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    ws, nbytes, buf = None, 0, None
     with _on_device(dev):
-        if torch.cuda.is_current_stream_capturing():
-            # memory of the graph's own pool: it lives as long as the graph
-            need = ctypes.c_int64(0)
-            _check("keops_paged_attention", lib().keops_paged_attention_workspace(
-                ctypes.addressof(c), kind, heads, T, max_q, max_len, window, ctypes.byref(need)))
-            nbytes = need.value
-            if nbytes:
-                buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
-                ws = (buf.data_ptr() + 255) // 256 * 256
+        ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, ctypes.addressof(c), kind, heads, T, max_q, max_len,
+                                           window)
         rc = lib().keops_paged_attention(ctypes.addressof(c), qp, qs, kind, heads, st, T, max_q, max_len, scale, window,
                                          float(decay), out.data_ptr(), lse.data_ptr(), ws, nbytes, s)
     _check("keops_paged_attention", rc)
@@ -214,7 +219,8 @@ def keops_verify_draft(target, draft, tokens, counts, u_accept, u_sample, out=No
     out = _out(out, (S, K + 1), dev, i32)
     accepted = _out(accepted, (S,), dev, i32, name="accepted")
     with _on_device(dev):
-        rc = lib().keops_verify_draft(*args, S, K, V, out.data_ptr(), accepted.data_ptr(), _stream(stream, dev))
+        ws, nbytes, buf = _graph_workspace("keops_verify_draft", dev, S, K, V)
+        rc = lib().keops_verify_draft(*args, S, K, V, out.data_ptr(), accepted.data_ptr(), ws, nbytes, _stream(stream, dev))
     _check("keops_verify_draft", rc)
-    _keep(stream, dev, None if given_out is not None else out, None if given_acc is not None else accepted)
+    _keep(stream, dev, None if given_out is not None else out, None if given_acc is not None else accepted, buf)
     return out, accepted

@@ -341,11 +341,14 @@ int keops_cache_evict(const keops_cache_t *cache, const int32_t *new_table, int6
  * draft = NULL: the drafted token had probability 1.  A token outside [0, vocab) is refused.
  * target: [seqs][drafts + 1][vocab], draft: [seqs][drafts][vocab], tokens, u_accept:
  * [seqs][drafts]; out: [seqs][drafts + 1], the taken tokens, the new one, then -1;
- * accepted: [seqs], how many were taken.
+ * accepted: [seqs], how many were taken.  workspace: as for keops_paged_attention.
  */
 int keops_verify_draft(const float *target, const float *draft, const int32_t *tokens, const int32_t *counts,
                        const float *u_accept, const float *u_sample, int32_t seqs, int32_t drafts, int32_t vocab,
-                       int32_t *out, int32_t *accepted, void *stream);
+                       int32_t *out, int32_t *accepted, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of a keops_verify_draft call. */
+int keops_verify_draft_workspace(int32_t seqs, int32_t drafts, int32_t vocab, int64_t *bytes);
 
 /* Human-readable name of a status code (static storage). */
 const char *keops_status_string(int status);

@@ -107,13 +107,16 @@ def test_evict_refusals(L):
 
 
 def test_verify_refusals(L):
-    def call(target=A, draft=B, tokens=C, counts=D, ua=E, us=F, S=2, K=3, V=100, out=G, acc=0x90000000):
-        return L.keops_verify_draft(target, draft, tokens, counts, ua, us, S, K, V, out, acc, None)
+    def call(target=A, draft=B, tokens=C, counts=D, ua=E, us=F, S=2, K=3, V=100, out=G, acc=0x90000000, ws=None, nbytes=0):
+        return L.keops_verify_draft(target, draft, tokens, counts, ua, us, S, K, V, out, acc, ws, nbytes, None)
     for kw in (dict(target=None), dict(tokens=None), dict(counts=None), dict(ua=None), dict(us=None), dict(out=None), dict(acc=None),
                dict(S=-1), dict(K=-1), dict(V=0), dict(target=A + 2), dict(out=G + 1), dict(out=A), dict(acc=G), dict(out=C),
-               dict(acc=D)):
+               dict(acc=D), dict(ws=0xB0000001, nbytes=64), dict(ws=0xB0000000, nbytes=-1)):
         assert call(**kw) == -1, kw
     assert call(V=(1 << 30) + 1) == -2
+    n = ctypes.c_int64(7)
+    assert L.keops_verify_draft_workspace(5, 3, 131072, ctypes.byref(n)) == 0 and n.value == 5 * 64 * 16
+    assert L.keops_verify_draft_workspace(-1, 3, 10, ctypes.byref(n)) == -1
     assert call(S=0, target=None, tokens=None, counts=None, ua=None, us=None, out=None, acc=None) == 0
 
 
