@@ -99,9 +99,10 @@ struct AttendArgs {
   float decay;
   char *out;                    // [tokens][heads * group][dim]
   float *lse;                   // [tokens][heads * group]
-  // split over the slots: partials [nsplit][tokens][heads * group]
-  int32_t nsplit, chunk;
-  float *part_o;                // [..][dim], each divided by nothing: sums under the partial maximum
+  // parts of a row's sums: many rows [nsplit][tokens][heads * group], few rows [work-groups][2][rows]
+  int32_t nsplit;
+  int32_t whole;                // few rows: a work-group has all slots of one (sequence, head)
+  float *part_o;                // [..][dim], sums under the part's maximum
   float2 *part_ml;              // (maximum in log2 units, sum)
   // few-rows form with weights: scores [seqs * heads][rows][score_stride] in log2 units
   float *scores;
@@ -139,7 +140,10 @@ void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st
 constexpr int kFewRowsMax = 32;      // rows (new tokens x group) of the few-rows form
 constexpr int kManyRowsTile = 128;   // rows of a work-group of the many-rows form
 constexpr int kSumSlotsTile = 256;   // slots of a work-group of the column sums
-void launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, dim3 grid, hipStream_t st);
+// grid 0: the work-groups of the variant that a compute unit holds (-1: HIP error).  join_rows: rows of
+// a work-group of the joining pass, 0: none.
+int launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, int grid, int join_rows,
+                      hipStream_t st);
 void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
 void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st);

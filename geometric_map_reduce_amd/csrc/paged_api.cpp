@@ -17,12 +17,12 @@ namespace {
 constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr double kMaxWorkspace = 1.0e14;    // more than any device holds; below the 64-bit limit
 // Work-groups that a launch aims for, per compute unit, when it splits a long axis.
-constexpr int64_t kFewWgsPerCu = 4;         // one sequence: equal pieces
-constexpr int64_t kFewWgsPerCuRagged = 16;  // several: small pieces even out their lengths
 constexpr int64_t kManyWgsPerCu = 2;
 constexpr int64_t kSumsWgsPerCu = 2;
-constexpr int kFewChunk = 128;              // least slots of a split: one tile for each wave,
-constexpr int kFewChunkFull = 1024;         // or so many where the sequences alone fill the device
+// Few rows: least slots of a work-group's run (one tile of 32 for each wave), and the longest
+// sequences that are left whole when there are enough of them to fill the device.
+constexpr int kFewLeast = 128;
+constexpr int kFewWhole = 1024;
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -85,30 +85,40 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Launch plan of one attention call.
 struct AttendPlan {
-  bool few, scores;
-  int row_tiles, score_rows;
-  int64_t nsplit, chunk, nrow, grid, sums_grid, score_stride;
+  bool few, scores, whole;
+  int row_tiles, score_rows, join_rows;
+  int64_t nsplit, nrow, grid, sums_grid, score_stride;
   int64_t ml_bytes, o_bytes, score_bytes, sums_bytes;
   int64_t total() const { return ml_bytes + o_bytes + score_bytes + sums_bytes; }
 };
 
-int plan_attend(const keops_cache_t &c, int64_t tokens, int heads, int64_t max_q, int64_t max_len, int window, int cus,
+int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int64_t max_q, int64_t max_len, int window, int cus,
                 AttendPlan *p) {
   *p = AttendPlan{};
   const int64_t G = heads / c.heads, rows = max_q * G, S = c.seqs, H = c.heads;
   p->few = rows <= kFewRowsMax;
+  // keeping a row's scores costs 8 bytes a slot, reading K again dim times its width
+  p->scores = c.weights && p->few && rows * 8 <= c.dim * width_of(c.type);
   // slots that the rows of one sequence see at most
   int64_t span = max_len;
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + max_q - 1);
   if (p->few) {
     p->row_tiles = rows <= 16 ? 1 : 2;
     const int64_t from_tile = std::min<int64_t>(max_len, span + 31);    // a window starts inside a tile
-    const int64_t least = S * H >= 2 * cus ? kFewChunkFull : kFewChunk;
-    const int64_t aim = (S > 1 ? kFewWgsPerCuRagged : kFewWgsPerCu) * cus;
-    p->chunk = std::max(least, ceil_div(ceil_div(from_tile * S * H, aim), kFewChunk) * kFewChunk);
-    p->nsplit = std::max<int64_t>(1, ceil_div(from_tile, p->chunk));
-    if ((double)S * (double)H * (double)p->nsplit > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
-    p->grid = S * H * p->nsplit;
+    if ((double)S * (double)H * (double)(from_tile / 32 + 2) > (double)kMaxGrid || (double)S * (double)H * (double)rows > (double)kMaxGrid)
+      return KEOPS_ERR_UNSUPPORTED;
+    AttendArgs probe{};
+    probe.score_stride = p->scores;
+    const int fit = launch_attend_few(probe, type, c.type == KEOPS_TYPE_E4M3, c.dim, p->row_tiles, 0, 0, nullptr);
+    if (fit < 1) return KEOPS_ERR_HIP;
+    const int64_t room = (int64_t)fit * cus;
+    p->whole = from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
+    p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
+    if (!p->whole) {
+      p->join_rows = S * H * rows >= 2048 ? std::min<int64_t>(rows, 1024 / c.dim) : 1;
+      p->ml_bytes = align256(p->grid * 2 * 16 * p->row_tiles * 8);
+      p->o_bytes = align256(p->grid * 2 * 16 * p->row_tiles * c.dim * 4);
+    }
   } else {
     const int64_t nrt = ceil_div(rows, kManyRowsTile);
     if ((double)S * (double)H * (double)nrt > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
@@ -118,8 +128,6 @@ int plan_attend(const keops_cache_t &c, int64_t tokens, int heads, int64_t max_q
     p->grid = wgs * p->nsplit;
   }
   if (c.weights) {
-    // keeping a row's scores costs 8 bytes a slot, reading K again dim times its width
-    p->scores = p->few && rows * 8 <= c.dim * width_of(c.type);
     if (p->scores) {
       p->score_rows = (int)rows;
       p->score_stride = ceil_div(max_len, 32) * 32;
@@ -138,7 +146,7 @@ int plan_attend(const keops_cache_t &c, int64_t tokens, int heads, int64_t max_q
       }
     }
   }
-  if (p->nsplit > 1) {
+  if (!p->few && p->nsplit > 1) {
     const double out_rows = (double)tokens * heads * (double)p->nsplit;
     if (out_rows * c.dim * 4.0 > kMaxWorkspace) return KEOPS_ERR_ALLOC;
     if ((double)tokens * heads > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
@@ -238,7 +246,7 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   int cus = 0;
   if (int rc = device_setup(&cus)) return rc;
   AttendPlan p;
-  if (int rc = plan_attend(*c, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
+  if (int rc = plan_attend(*c, type, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
   Workspace own;
   char *ws = nullptr;
   if (int rc = take_workspace(own, workspace, workspace_bytes, p.total(), st, &ws)) return rc;
@@ -259,7 +267,7 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.out = (char *)out;
   a.lse = lse;
   a.nsplit = (int32_t)p.nsplit;
-  a.chunk = (int32_t)p.chunk;
+  a.whole = p.whole;
   a.part_ml = (float2 *)ws;
   a.part_o = (float *)(ws + p.ml_bytes);
   a.scores = p.scores ? (float *)(ws + p.ml_bytes + p.o_bytes) : nullptr;
@@ -269,10 +277,10 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.part_w = (float *)(ws + p.ml_bytes + p.o_bytes + p.score_bytes);
   const bool e4m3 = c->type == KEOPS_TYPE_E4M3;
   const int prof = prof_begin(st);
-  if (p.few) launch_attend_few(a, type, e4m3, c->dim, p.row_tiles, dim3((unsigned)p.grid), st);
+  if (p.few) launch_attend_few(a, type, e4m3, c->dim, p.row_tiles, (int)p.grid, p.join_rows, st);
   else launch_attend_many(a, type, e4m3, c->dim, dim3((unsigned)p.grid), st);
   prof_end(prof, st);
-  if (p.nsplit > 1) launch_attend_join(a, type, st);
+  if (!p.few && p.nsplit > 1) launch_attend_join(a, type, st);
   if (c->weights && max_len > 0) {
     if (p.scores) {
       launch_attend_score_sums(a, st);
@@ -400,7 +408,7 @@ int keops_paged_attention_workspace(const keops_cache_t *cache, int32_t type, in
     int cus = 0;
     if (int rc = device_setup(&cus)) return rc;
     AttendPlan p;
-    if (int rc = plan_attend(*cache, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
+    if (int rc = plan_attend(*cache, type, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
     *bytes = p.total();
     return KEOPS_OK;
   } catch (...) {

@@ -5,8 +5,8 @@
 //
 // The rows of a key/value head are its `group` query heads times the sequence's new tokens; up to
 // 32 of them share one pass over the head's slots, so the cache is read once and HBM bounds it.
-// A work-group takes one chunk of slots of one (sequence, head); its four waves take every
-// fourth tile of 32 slots.
+// The slots of all sequences and heads are dealt to as many work-groups as the device holds, in equal
+// runs of tiles of 32 slots; a work-group's four waves take every fourth tile of its run.
 //
 //  * No LDS between HBM and the matrix instructions.  With S^T = K Q^T the A operand is rows of K
 //    as they lie in memory, and the result leaves lane l with row l % 16 and slots 4 (l / 16) + r
@@ -23,6 +23,8 @@
 //    the window's edge; if such a tile holds an infinity or NaN in V, it is added after the
 //    products, to the rows that see it (0 times infinity would reach the others).
 #pragma once
+
+#include <atomic>
 
 #include "paged.h"
 
@@ -156,6 +158,71 @@ struct FewRows {
   }
 };
 
+// A sequence's share of the few-rows work: its tiles of 32 slots from the first that any row sees.
+struct FewSpan {
+  SeqSpan sp;
+  int lo, hi, tiles;         // slots [lo, hi), lo a multiple of the tile; at least one tile if there are rows
+};
+__device__ __forceinline__ FewSpan few_span(const AttendArgs &a, int s) {
+  FewSpan f;
+  f.sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
+  f.lo = 0;
+  if (a.window > 0 && f.sp.first - a.window + 1 > 0) f.lo = (f.sp.first - a.window + 1) & ~(kFewTile - 1);
+  f.hi = f.sp.n < f.sp.first + f.sp.m ? f.sp.n : f.sp.first + f.sp.m;
+  f.tiles = f.hi > f.lo ? (f.hi - f.lo + kFewTile - 1) / kFewTile : 1;
+  if (f.sp.m == 0) f.tiles = 0;
+  return f;
+}
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint32_t up = __shfl_up(v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+// All tiles of all sequences and heads in a line, sequence by sequence, head by head, are dealt to
+// the work-groups in equal runs.  Every wave finds out for itself, from the lengths.
+struct FewShare {
+  uint32_t share;            // tiles of a work-group
+  int s;                     // the sequence that holds tile `at` of the line (seqs: past the end)
+  uint32_t base;             // the first of its tiles
+};
+__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int wg, int want_s) {
+  const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
+  const uint32_t H = (uint32_t)a.c.heads;
+  uint32_t total = 0;
+  for (int s0 = 0; s0 < S; s0 += kWave) {
+    const uint32_t own = s0 + lane < S ? (uint32_t)few_span(a, s0 + lane).tiles * H : 0u;
+    total += __shfl(wave_scan_u32(own), kWave - 1);
+  }
+  FewShare r;
+  r.share = (total + wgs - 1) / wgs;
+  r.share = (r.share + kFewWaves - 1) / kFewWaves * kFewWaves;      // a tile for every wave
+  const uint32_t at = (uint32_t)wg * r.share;
+  r.s = S;
+  r.base = total;
+  uint32_t before = 0;
+  for (int s0 = 0; s0 < S; s0 += kWave) {
+    const uint32_t own = s0 + lane < S ? (uint32_t)few_span(a, s0 + lane).tiles * H : 0u;
+    const uint32_t upto = before + wave_scan_u32(own);
+    const bool here = want_s >= 0 ? s0 + lane == want_s : (at >= upto - own && at < upto);
+    const uint64_t who = __ballot(here);
+    if (who) {
+      const int l = __ffsll((unsigned long long)who) - 1;
+      r.s = s0 + l;
+      r.base = __shfl(upto - own, l);
+      break;
+    }
+    before = __shfl(upto, kWave - 1);
+  }
+  r.s = __builtin_amdgcn_readfirstlane(r.s);
+  r.base = __builtin_amdgcn_readfirstlane(r.base);
+  r.share = __builtin_amdgcn_readfirstlane(r.share);
+  return r;
+}
+
 template <class T, bool E4M3, int D, int NR, bool SCORES>
 __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, E4M3, D, NR>;
@@ -170,27 +237,48 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   __shared__ int sh_odd;
 
   const int H = a.c.heads, G = a.group;
-  int b = blockIdx.x;
-  const int h = b % H;
-  b /= H;
-  const int split = b % a.nsplit, s = b / a.nsplit;
+  const int64_t heads = (int64_t)H * G;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), col = lane & 15, q4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
 
-  const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
+  // this work-group's run of tiles: from tile t0 of (s, h) on
+  int s, h, t0;
+  uint32_t left;
+  if (a.whole) {
+    s = blockIdx.x / H;
+    h = blockIdx.x - s * H;
+    t0 = 0;
+    left = 0xffffffffu;
+  } else {
+    const FewShare my = few_share(a, gridDim.x, blockIdx.x, -1);
+    if (my.s >= a.c.seqs) return;
+    s = my.s;
+    left = my.share;
+    const int tiles = few_span(a, s).tiles, at = (int)((uint32_t)blockIdx.x * my.share - my.base);
+    h = at / tiles;
+    t0 = at - h * tiles;
+  }
+  for (;;) {
+  const FewSpan span = few_span(a, s);
+  const SeqSpan &sp = span.sp;
   const int R = sp.m * G;
-  if (R == 0) return;
-  // slots any row sees: [lo, hi)
-  int lo = 0;
-  if (a.window > 0 && sp.first - a.window + 1 > 0) lo = sp.first - a.window + 1;
-  const int hi = sp.n < sp.first + sp.m ? sp.n : sp.first + sp.m;
-  const int64_t c0 = (int64_t)(lo & ~(kFewTile - 1)) + (int64_t)split * a.chunk;
-  const int c1 = c0 + a.chunk < hi ? (int)(c0 + a.chunk) : hi;
+  if (R == 0) {              // `whole` only: the line has no such sequence
+    if (a.whole) return;
+    if (++s >= a.c.seqs) return;
+    h = 0;
+    continue;
+  }
+  const int hi = span.hi;
+  const int t1 = (uint32_t)(span.tiles - t0) > left ? t0 + (int)left : span.tiles;
+  const int c0 = span.lo + t0 * kFewTile;
+  const int c1 = span.lo + t1 * kFewTile < hi ? span.lo + t1 * kFewTile : hi;
+  // where a part goes: a run's first piece (2 wg), or the start of a longer one (2 wg + 1)
+  const bool part = t0 > 0 || t1 < span.tiles;
+  const int64_t part_at = ((int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * kRows;
 
   // rows of this lane: r = 16 nr + col, its token's slot (a padding row sees nothing)
   int pos[NR];
   u32x4 qf[NR][F::kSteps];
-  const int64_t heads = (int64_t)H * G;
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
     const int r = 16 * nr + col;
@@ -220,8 +308,7 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   F f;
   bool odd = false;
   if (tid == 0) sh_odd = 0;
-  for (int64_t blk64 = c0; blk64 < c1; blk64 += kFewBlock) {
-    const int blk = (int)blk64;
+  for (int blk = c0; blk < c1; blk += kFewBlock) {
     const int cnt = c1 - blk < kFewBlock ? c1 - blk : kFewBlock;
     const int ntile = (cnt + kFewTile - 1) / kFewTile;
     __syncthreads();
@@ -384,11 +471,10 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
       }
     }
   }
-  if (wave != 0) return;
+  if (wave == 0) {
   if (sh_odd) {
     // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
-    for (int64_t j64 = c0; j64 < c1; ++j64) {
-      const int j = (int)j64;
+    for (int j = c0; j < c1; ++j) {
       if (!(j > sp.first || (a.window > 0 && j <= last_pos - a.window))) continue;
       const int64_t o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)j));
       if (o < 0) continue;
@@ -425,10 +511,9 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
     float *po = nullptr;
     char *out = nullptr;
     float mul = vs;
-    if (a.nsplit > 1) {
-      const int64_t part = (int64_t)split * a.tokens * heads + at;
-      if (q4 == 0) a.part_ml[part] = make_float2(m_run[nr], l);
-      po = a.part_o + part * D;
+    if (part) {
+      if (q4 == 0) a.part_ml[part_at + r] = make_float2(m_run[nr], l);
+      po = a.part_o + (part_at + r) * D;
       if (!(l > 0.0f || l != l)) continue;      // nothing here: the join skips it
     } else {
       if (q4 == 0) a.lse[at] = l > 0.0f || l != l ? (m_run[nr] + __log2f(l)) * kLn2 : -INFINITY;
@@ -436,7 +521,7 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
       out = a.out + at * D * 2;
     }
     // accumulator register rg of column tile t: column base + (4 q4 + rg) w + t
-    int t0 = 0, base = 0;
+    int ct = 0, base = 0;
 #pragma unroll
     for (int n = 0; n < VPieces<D>::n; ++n) {
       const int w = VPieces<D>::w[n];
@@ -445,40 +530,121 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
         const int d = base + (q4 * 4 + rg) * w;
 #pragma unroll
         for (int t = 0; t < w; t += 2) {
-          const float x = acc[nr][t0 + t][rg] * mul, y = acc[nr][t0 + t + 1][rg] * mul;
+          const float x = acc[nr][ct + t][rg] * mul, y = acc[nr][ct + t + 1][rg] * mul;
           if (po) *(f32x2 *)(po + d + t) = (f32x2){x, y};
           else *(uint32_t *)(out + (d + t) * 2) = T::pack(x, y);
         }
       }
-      t0 += w;
+      ct += w;
       base += 16 * w;
     }
   }
-}
-
-// One (type, cache, dim) of the few-rows form.
-template <class T, bool E4M3, int D>
-void launch_few_dim(const AttendArgs &a, int row_tiles, dim3 grid, hipStream_t st) {
-  if (row_tiles == 1) {
-    if (a.scores) attend_few_kernel<T, E4M3, D, 1, true><<<grid, kFewThreads, 0, st>>>(a);
-    else attend_few_kernel<T, E4M3, D, 1, false><<<grid, kFewThreads, 0, st>>>(a);
-  } else {
-    if (a.scores) attend_few_kernel<T, E4M3, D, 2, true><<<grid, kFewThreads, 0, st>>>(a);
-    else attend_few_kernel<T, E4M3, D, 2, false><<<grid, kFewThreads, 0, st>>>(a);
+  }      // wave 0
+  left -= (uint32_t)(t1 - t0);
+  if (a.whole || left == 0) return;
+  t0 = 0;
+  if (++h == H) {
+    h = 0;
+    if (++s >= a.c.seqs) return;
+  }
+  __syncthreads();             // the next piece writes the same LDS
   }
 }
 
-template <class T, bool E4M3>
-void launch_few(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st) {
-  if (dim == 64) launch_few_dim<T, E4M3, 64>(a, row_tiles, grid, st);
-  else if (dim == 96) launch_few_dim<T, E4M3, 96>(a, row_tiles, grid, st);
-  else if (dim == 128) launch_few_dim<T, E4M3, 128>(a, row_tiles, grid, st);
-  else launch_few_dim<T, E4M3, 256>(a, row_tiles, grid, st);
+// Joins the parts of a (sequence, head): blocks of `rows_per` rows; out = sum_k 2^(m_k - M) o_k /
+// sum_k 2^(m_k - M) l_k over the work-groups k of its run, under a running maximum M, in order within
+// each of the groups of dim / 4 threads, then the groups in order.
+constexpr int kFewJoinThreads = 256;
+template <class T, int D, int NR>
+__global__ __launch_bounds__(kFewJoinThreads) void join_few_kernel(AttendArgs a, int wgs, int rows_per) {
+  constexpr int kLanes = D / 4, kGroups = kFewJoinThreads / kLanes;
+  __shared__ f32x4 part[kFewJoinThreads];
+  __shared__ float2 part_ml[kFewJoinThreads];
+  const int H = a.c.heads, G = a.group, tid = threadIdx.x;
+  const int64_t heads = (int64_t)H * G;
+  const int blocks = (a.max_q * G + rows_per - 1) / rows_per;
+  const int sh = blockIdx.x / blocks, s = sh / H, h = sh - s * H;
+  const FewShare f = few_share(a, wgs, 0, s);
+  const FewSpan span = few_span(a, s);
+  const int R = span.sp.m * G;
+  if (R == 0) return;
+  const uint32_t from = f.base + (uint32_t)h * span.tiles, to = from + span.tiles;
+  const int w0 = (int)(from / f.share), w1 = (int)((to - 1) / f.share);
+  if (w0 == w1) return;        // one work-group had all of it
+  // every row by its own groups: rows_per rows at a time, or all groups on one
+  const int g = tid / kLanes, d4 = tid - g * kLanes;
+  const int per_row = kGroups / rows_per, gr = g / per_row, gk = g - gr * per_row;
+  const int r = (blockIdx.x - sh * blocks) * rows_per + gr;
+  const bool mine = gr < rows_per && r < R;
+  f32x4 acc = (f32x4){0, 0, 0, 0};
+  float l = 0.0f, top = -INFINITY;
+  const auto add = [&](float m, float y, f32x4 o) {
+    if (!(y > 0.0f || y != y)) return;         // a part without a slot: its sums were not written
+    const float m_new = fmaxf(top, m), x = fast_exp2(top - m_new), z = fast_exp2(m - m_new);
+    l = l * x + y * z;
+    acc = acc * x + o * z;
+    top = m_new;
+  };
+  if (mine) {
+#pragma unroll 4
+    for (int w = w0 + gk; w <= w1; w += per_row) {
+      const int64_t at = ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * (16 * NR) + r;
+      const float2 x = a.part_ml[at];
+      const f32x4 o = *(const f32x4 *)(a.part_o + at * D + d4 * 4);
+      add(x.x, x.y, o);
+    }
+  }
+  part[tid] = acc;
+  part_ml[tid] = make_float2(top, l);
+  __syncthreads();
+  if (!mine || gk != 0) return;
+  for (int k = 1; k < per_row; ++k) add(part_ml[tid + k * kLanes].x, part_ml[tid + k * kLanes].y, part[tid + k * kLanes]);
+  const int tok = (int)fast_div(a.gdiv, (uint32_t)r);
+  const int64_t row = (span.sp.t0 + tok) * heads + h * G + (r - tok * G);
+  const bool any = l > 0.0f || l != l;
+  const float mul = any ? 1.0f / l : 0.0f;
+  if (d4 == 0) a.lse[row] = any ? (top + __log2f(l)) * kLn2 : -INFINITY;
+  const f32x4 o = any ? acc * mul : (f32x4){0, 0, 0, 0};
+  *(u32x2 *)(a.out + (row * D + d4 * 4) * 2) = (u32x2){T::pack(o[0], o[1]), T::pack(o[2], o[3])};
 }
 
-void few_bf16(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
-void few_f16(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
-void few_bf16_e4m3(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
-void few_f16_e4m3(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
+// One (type, cache, dim) of the few-rows form.  Returns the work-groups that fit the device at
+// once when `grid` is 0.
+template <class T, bool E4M3, int D, int NR, bool SCORES>
+int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
+  if (grid == 0) {
+    static std::atomic<int> fit{0};
+    int n = fit.load(std::memory_order_relaxed);
+    if (n <= 0) {
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, E4M3, D, NR, SCORES>, kFewThreads,
+                                                       0) != hipSuccess || n < 1)
+        return -1;
+      fit.store(n, std::memory_order_relaxed);
+    }
+    return n;
+  }
+  attend_few_kernel<T, E4M3, D, NR, SCORES><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
+  if (join_rows > 0) {
+    const int64_t rows = ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows;
+    join_few_kernel<T, D, NR><<<dim3((unsigned)(rows * a.c.seqs * a.c.heads)), kFewJoinThreads, 0, st>>>(a, grid, join_rows);
+  }
+  return 0;
+}
+template <class T, bool E4M3, int D>
+int launch_few_dim(const AttendArgs &a, int row_tiles, int grid, int join_rows, hipStream_t st) {
+  if (row_tiles == 1)
+    return a.score_stride ? few_variant<T, E4M3, D, 1, true>(a, grid, join_rows, st)
+                          : few_variant<T, E4M3, D, 1, false>(a, grid, join_rows, st);
+  return a.score_stride ? few_variant<T, E4M3, D, 2, true>(a, grid, join_rows, st)
+                        : few_variant<T, E4M3, D, 2, false>(a, grid, join_rows, st);
+}
+
+template <class T, bool E4M3>
+int launch_few(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st) {
+  if (dim == 64) return launch_few_dim<T, E4M3, 64>(a, row_tiles, grid, join_rows, st);
+  if (dim == 96) return launch_few_dim<T, E4M3, 96>(a, row_tiles, grid, join_rows, st);
+  if (dim == 128) return launch_few_dim<T, E4M3, 128>(a, row_tiles, grid, join_rows, st);
+  return launch_few_dim<T, E4M3, 256>(a, row_tiles, grid, join_rows, st);
+}
 
 }  // namespace kmi

@@ -5,10 +5,10 @@
 namespace kmi {
 
 // paged_few_*.hip and paged_many_*.hip
-void few_bf16(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
-void few_f16(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
-void few_bf16_e4m3(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
-void few_f16_e4m3(const AttendArgs &a, int dim, int row_tiles, dim3 grid, hipStream_t st);
+int few_bf16(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
+int few_f16(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
+int few_bf16_e4m3(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
+int few_f16_e4m3(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
 void many_bf16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
 void many_f16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
 void many_bf16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
@@ -126,9 +126,10 @@ __global__ __launch_bounds__(256) void sums_join_kernel(AttendArgs a) {
 
 }  // namespace
 
-void launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, dim3 grid, hipStream_t st) {
-  if (type == CT_BF16) (e4m3 ? few_bf16_e4m3 : few_bf16)(a, dim, row_tiles, grid, st);
-  else (e4m3 ? few_f16_e4m3 : few_f16)(a, dim, row_tiles, grid, st);
+int launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, int grid, int join_rows,
+                      hipStream_t st) {
+  if (type == CT_BF16) return (e4m3 ? few_bf16_e4m3 : few_bf16)(a, dim, row_tiles, grid, join_rows, st);
+  return (e4m3 ? few_f16_e4m3 : few_f16)(a, dim, row_tiles, grid, join_rows, st);
 }
 
 void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st) {
