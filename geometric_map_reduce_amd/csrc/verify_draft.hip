@@ -166,14 +166,19 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_pick_kernel(VerifyArgs 
       double c = before + (scan - sum);
       for (int w = 0; w < wave; ++w) c += wave_total[w];
       for (int w = 0; w < kVerifyWaves; ++w) before += wave_total[w];
+      int over_at = V, mass_at = -1;         // this thread's first index past the goal, last with mass
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         c += m[u];
         if (m[u] > 0.0) {
-          if (c > goal) atomicMin(&first, i + u);
-          atomicMax(&last, i + u);
+          if (c > goal && over_at == V) over_at = i + u;
+          mass_at = i + u;
         }
       }
+      // the lowest lane that has one, the highest that has one: one addition a wave
+      const uint64_t past = __ballot(over_at < V), some = __ballot(mass_at >= 0);
+      if (past && lane == __ffsll((unsigned long long)past) - 1) atomicMin(&first, over_at);
+      if (some && lane == 63 - __clzll((long long)some)) atomicMax(&last, mass_at);
       __syncthreads();
       if (first < V) break;
     }

@@ -15,7 +15,7 @@ import math
 
 import torch
 
-from .binding import _check, _on_device, _out, _stream, lib
+from .binding import _check, _out, _raw_stream, _stream, lib
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
@@ -30,81 +30,102 @@ class _Cache(ctypes.Structure):
                 ("seqs", ctypes.c_int32)]
 
 
-def _vec(t, name, shape, dtype, dev):
-    """A dense tensor of this shape (None in it: any size) and type on ``dev``; its address."""
+def _tensor(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or t.device != dev or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(want is not None and want != got for want, got in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
-                         f"{['any' if s is None else s for s in shape]} on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
+    return t
+
+
+def _vec(t, name, shape, dtype, dev):
+    """The address of a dense tensor of this shape and type on device number ``dev``."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        _tensor(t, name)
+        raise
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{dev}, "
+                     f"got {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _table(t, name, seqs, dev):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32 or t.device != dev or t.dim() != 2 or t.shape[0] != seqs or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be an int32 tensor [{seqs}, pages of a sequence] on {dev} with contiguous rows")
+    _tensor(t, name)
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 2 or t.shape[0] != seqs or \
+            (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be an int32 tensor [{seqs}, pages of a sequence] on cuda:{dev} with contiguous rows")
     return t.data_ptr(), t.stride(0), t.shape[1]
 
 
 def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales=True):
+    """(the structure of the C ABI, the device's number, (heads, dim, type))."""
     for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (lens, "lens")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-    dev = k_pages.device
-    kind = _TYPES.get(k_pages.dtype)
-    if k_pages.dim() != 4 or kind is None or not k_pages.is_cuda or k_pages.stride(3) != 1:
+    dev, dtype, shape, strides = k_pages.get_device(), k_pages.dtype, k_pages.shape, k_pages.stride()
+    kind = _TYPES.get(dtype)
+    if len(shape) != 4 or kind is None or dev < 0 or strides[3] != 1:
         raise ValueError("k_pages must be a bfloat16, float16 or float8_e4m3fn CUDA tensor "
                          "[pages, page_size, heads, dim] with contiguous rows")
-    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.device != dev or \
-            v_pages.stride() != k_pages.stride():
+    if v_pages.shape != shape or v_pages.dtype is not dtype or v_pages.get_device() != dev or v_pages.stride() != strides:
         raise ValueError("v_pages must have the shape, type, device and strides of k_pages")
-    P, ps, H, D = k_pages.shape
+    P, ps, H, D = shape
     if D not in (64, 96, 128, 256):
         raise ValueError(f"dim must be 64, 96, 128 or 256, got {D}")
-    S = lens.shape[0] if lens.dim() == 1 else -1
-    c = _Cache()
-    c.lens = _vec(lens, "lens", (None,), torch.int32, dev)
-    c.page_table, c.table_stride, c.table_width = _table(page_table, "page_table", S, dev)
-    c.k_pages, c.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
-    # the stride of a dimension of one is never used
-    c.page_stride, c.slot_stride, c.head_stride = (st if n > 1 else 0 for st, n in zip(k_pages.stride()[:3], k_pages.shape))
-    c.pages, c.page_size, c.heads, c.dim, c.type, c.seqs = P, ps, H, D, kind, S
+    if lens.dim() != 1 or lens.dtype is not torch.int32 or lens.get_device() != dev or not lens.is_contiguous():
+        raise ValueError(f"lens must be a contiguous int32 tensor [sequences] on cuda:{dev}")
+    S = lens.shape[0]
+    table, table_stride, width = _table(page_table, "page_table", S, dev)
+    w = ks = vs = None
     if weights is not None:
-        c.weights = _vec(weights, "weights", (P, H, ps), torch.float32, dev)
-    if kind == 2 and scales:
-        if k_scale is None or v_scale is None:
-            raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
-        c.k_scale = _vec(k_scale, "k_scale", (H,), torch.float32, dev)
-        c.v_scale = _vec(v_scale, "v_scale", (H,), torch.float32, dev)
+        w = _vec(weights, "weights", (P, H, ps), torch.float32, dev)
+    if kind == 2:
+        if scales:
+            if k_scale is None or v_scale is None:
+                raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
+            ks = _vec(k_scale, "k_scale", (H,), torch.float32, dev)
+            vs = _vec(v_scale, "v_scale", (H,), torch.float32, dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
-    return c, dev
+    # the stride of a dimension of one is never used
+    c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), w, ks, vs, strides[0] if P > 1 else 0, strides[1] if ps > 1 else 0,
+               strides[2] if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind, width, S)
+    return c, dev, (H, D, dtype)
 
 
-def _rows(t, name, heads, k_pages):
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _rows(t, name, heads, cache, dev):
     """Token rows [tokens, heads, dim], 16-bit, heads dense; rows may be part of wider ones."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    D, dtype = k_pages.shape[3], k_pages.dtype
-    if t.dim() != 3 or t.dtype not in (torch.bfloat16, torch.float16) or t.device != k_pages.device or t.shape[2] != D or \
-            (heads is not None and t.shape[1] != heads) or (dtype.itemsize == 2 and t.dtype != dtype):
+    _tensor(t, name)
+    H, D, held = cache
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 3 or dtype not in _HALF or t.get_device() != dev or shape[2] != D or \
+            (heads is not None and shape[1] != heads) or (held in _HALF and dtype is not held):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {D}], of the cache's type "
-                         f"(bfloat16 or float16 with an 8-bit cache), on {k_pages.device}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+                         f"(bfloat16 or float16 with an 8-bit cache), on cuda:{dev}")
+    T, h, _ = shape
+    s0, s1, s2 = t.stride()
+    if T and (s2 != 1 or (h > 1 and s1 != D)):
         raise ValueError(f"{name} must have dense [heads, dim] rows")
-    if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
+    at = t.data_ptr()
+    if at % 16 or (T > 1 and s0 % 8):
         raise ValueError(f"{name} must be 16-byte aligned, its rows a multiple of 16 bytes apart")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    return at, s0 if T > 1 else h * D
+
+
+def _run(name, dev, stream, fn, *args):
+    """fn(*args, stream) with device ``dev`` current; raises on a status."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _run(name, dev, stream, fn, *args)
+    rc = fn(*args, _stream(stream, torch.device("cuda", dev)) if stream is not None or _raw_stream is None else _raw_stream(dev))
+    if rc:
+        _check(name, rc)
 
 
 def _keep(stream, dev, *tensors):
     """Tensors made here for a call on another stream than the current one belong to that stream too."""
-    if stream is None:
-        return
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
     if s.cuda_stream != torch.cuda.current_stream(dev).cuda_stream:
         for t in tensors:
@@ -118,7 +139,8 @@ def _graph_workspace(name, dev, *args):
     if not torch.cuda.is_current_stream_capturing():
         return None, 0, None
     need = ctypes.c_int64(0)
-    _check(name, getattr(lib(), name + "_workspace")(*args, ctypes.byref(need)))
+    with torch.cuda.device(dev):
+        _check(name, getattr(lib(), name + "_workspace")(*args, ctypes.byref(need)))
     if need.value == 0:
         return None, 0, None
     buf = torch.empty(need.value + 256, dtype=torch.uint8, device=dev)
@@ -129,15 +151,14 @@ def keops_cache_append(k, v, k_pages, v_pages, page_table, lens, starts, weights
                        stream=None):
     """Write rows starts[s] .. starts[s+1] of k and v [tokens, heads, dim] to the last slots of sequence s
     (``lens`` counts them already); clear those slots' ``weights``."""
-    c, dev = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
-    kp, ks = _rows(k, "k", c.heads, k_pages)
-    vp, vs = _rows(v, "v", c.heads, k_pages)
-    if v.shape != k.shape or v.dtype != k.dtype:
+    c, dev, cache = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
+    kp, ks = _rows(k, "k", c.heads, cache, dev)
+    vp, vs = _rows(v, "v", c.heads, cache, dev)
+    if v.shape != k.shape or v.dtype is not k.dtype:
         raise ValueError("v must have the shape and type of k")
     st = _vec(starts, "starts", (c.seqs + 1,), torch.int32, dev)
-    with _on_device(dev):
-        rc = lib().keops_cache_append(ctypes.addressof(c), kp, vp, ks, vs, _TYPES[k.dtype], st, k.shape[0], _stream(stream, dev))
-    _check("keops_cache_append", rc)
+    _run("keops_cache_append", dev, stream, lib().keops_cache_append, ctypes.addressof(c), kp, vp, ks, vs, _TYPES[k.dtype], st,
+         k.shape[0])
 
 
 def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, max_len, scale=None, window=0, weights=None,
@@ -147,8 +168,8 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     ``max_q`` and ``max_len`` bound the new tokens and the slots of any sequence; ``scale`` is
     1 / sqrt(dim) unless given; ``window`` > 0 limits a token to that many slots, its own included.
     With ``weights``, every slot's becomes decay * old + the attention it received in this call."""
-    c, dev = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
-    qp, qs = _rows(q, "q", None, k_pages)
+    c, dev, cache = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
+    qp, qs = _rows(q, "q", None, cache, dev)
     T, heads, D = q.shape
     if heads < 1 or heads % c.heads:
         raise ValueError(f"the query heads must be a multiple of the cache's {c.heads}, got {heads}")
@@ -156,19 +177,17 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     max_q, max_len, window = int(max_q), int(max_len), int(window)
     if min(max_q, max_len, window) < 0 or max(max_q, max_len, window) > 2**31 - 1:
         raise ValueError("max_q, max_len and window must be in [0, 2^31)")
-    given_out, given_lse = out, lse
-    out = _out(out, (T, heads, D), dev, q.dtype)
-    lse = _out(lse, (T, heads), dev, name="lse")
-    s = _stream(stream, dev)
     kind = _TYPES[q.dtype]
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with _on_device(dev):
-        ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, ctypes.addressof(c), kind, heads, T, max_q, max_len,
-                                           window)
-        rc = lib().keops_paged_attention(ctypes.addressof(c), qp, qs, kind, heads, st, T, max_q, max_len, scale, window,
-                                         float(decay), out.data_ptr(), lse.data_ptr(), ws, nbytes, s)
-    _check("keops_paged_attention", rc)
-    _keep(stream, dev, None if given_out is not None else out, None if given_lse is not None else lse, buf)
+    made = (None if out is not None else torch.empty((T, heads, D), dtype=q.dtype, device=q.device),
+            None if lse is not None else torch.empty((T, heads), dtype=torch.float32, device=q.device))
+    out = made[0] if out is None else _out(out, (T, heads, D), q.device, q.dtype)
+    lse = made[1] if lse is None else _out(lse, (T, heads), q.device, name="lse")
+    ca = ctypes.addressof(c)
+    ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, ca, kind, heads, T, max_q, max_len, window)
+    _run("keops_paged_attention", dev, stream, lib().keops_paged_attention, ca, qp, qs, kind, heads, st, T, max_q, max_len,
+         1.0 / math.sqrt(D) if scale is None else float(scale), window, float(decay), out.data_ptr(), lse.data_ptr(), ws, nbytes)
+    if stream is not None:
+        _keep(stream, dev, *made, buf)
     return out, lse
 
 
@@ -177,23 +196,24 @@ def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, bu
     """Keep ``budget`` slots of every sequence and head: the first ``sink``, the last ``recent``, and those with
     the largest weights; move them to the pages of ``new_table``.  Returns (kept [sequences, heads, budget]
     old slot numbers or -1, new lens).  The scales of an 8-bit cache are not needed."""
-    c, dev = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
+    c, dev, _ = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
     if weights is None:
         raise ValueError("eviction needs weights")
     nt, nstride, nwidth = _table(new_table, "new_table", c.seqs, dev)
     budget, sink, recent = int(budget), int(sink), int(recent)
-    if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
-        raise ValueError("need budget >= 1, sink >= 0, recent >= 0 and sink + recent <= budget")
+    if not 1 <= budget < 2**31 or sink < 0 or recent < 0 or sink + recent > budget:
+        raise ValueError("need 1 <= budget < 2^31, sink >= 0, recent >= 0 and sink + recent <= budget")
     if nwidth < min(-(-budget // c.page_size), c.table_width):
         raise ValueError("new_table has too few pages for the budget")
-    given_kept, given_lens = kept, new_lens
-    kept = _out(kept, (c.seqs, c.heads, budget), dev, torch.int32, name="kept")
-    new_lens = _out(new_lens, (c.seqs,), dev, torch.int32, name="new_lens")
-    with _on_device(dev):
-        rc = lib().keops_cache_evict(ctypes.addressof(c), nt, nstride, nwidth, budget, sink, recent, kept.data_ptr(),
-                                     new_lens.data_ptr(), _stream(stream, dev))
-    _check("keops_cache_evict", rc)
-    _keep(stream, dev, None if given_kept is not None else kept, None if given_lens is not None else new_lens)
+    S, H = c.seqs, c.heads
+    made = (None if kept is not None else torch.empty((S, H, budget), dtype=torch.int32, device=k_pages.device),
+            None if new_lens is not None else torch.empty((S,), dtype=torch.int32, device=k_pages.device))
+    kept = made[0] if kept is None else _out(kept, (S, H, budget), k_pages.device, torch.int32, name="kept")
+    new_lens = made[1] if new_lens is None else _out(new_lens, (S,), k_pages.device, torch.int32, name="new_lens")
+    _run("keops_cache_evict", dev, stream, lib().keops_cache_evict, ctypes.addressof(c), nt, nstride, nwidth, budget, sink, recent,
+         kept.data_ptr(), new_lens.data_ptr())
+    if stream is not None:
+        _keep(stream, dev, *made)
     return kept, new_lens
 
 
@@ -201,26 +221,25 @@ def keops_verify_draft(target, draft, tokens, counts, u_accept, u_sample, out=No
     """Drafted ``tokens`` [sequences, drafts] (the first counts[s] of them) against the target's probabilities
     [sequences, drafts + 1, vocab] and the draft's [sequences, drafts, vocab] (None: certain), with given uniform
     numbers.  Returns (tokens [sequences, drafts + 1]: taken, then the new one, then -1; accepted [sequences])."""
-    if not isinstance(target, torch.Tensor) or not isinstance(tokens, torch.Tensor):
-        raise TypeError("target and tokens must be torch.Tensors")
-    if target.dim() != 3 or not target.is_cuda or tokens.dim() != 2:
+    _tensor(target, "target"), _tensor(tokens, "tokens")
+    dev = target.get_device()
+    if target.dim() != 3 or dev < 0 or tokens.dim() != 2:
         raise ValueError("target must be a CUDA tensor [sequences, drafts + 1, vocab], tokens [sequences, drafts]")
-    dev, (S, K), V = target.device, tokens.shape, target.shape[2]
+    (S, K), V = tokens.shape, target.shape[2]
     if V < 1:
         raise ValueError("the vocabulary is empty")
     f32, i32 = torch.float32, torch.int32
-    args = [_vec(target, "target", (S, K + 1, V), f32, dev),
-            None if draft is None else _vec(draft, "draft", (S, K, V), f32, dev),
-            _vec(tokens, "tokens", (S, K), i32, dev), _vec(counts, "counts", (S,), i32, dev),
-            _vec(u_accept, "u_accept", (S, K), f32, dev), _vec(u_sample, "u_sample", (S,), f32, dev)]
-    if K == 0 and draft is not None:
-        args[1] = None
-    given_out, given_acc = out, accepted
-    out = _out(out, (S, K + 1), dev, i32)
-    accepted = _out(accepted, (S,), dev, i32, name="accepted")
-    with _on_device(dev):
-        ws, nbytes, buf = _graph_workspace("keops_verify_draft", dev, S, K, V)
-        rc = lib().keops_verify_draft(*args, S, K, V, out.data_ptr(), accepted.data_ptr(), ws, nbytes, _stream(stream, dev))
-    _check("keops_verify_draft", rc)
-    _keep(stream, dev, None if given_out is not None else out, None if given_acc is not None else accepted, buf)
+    tp = _vec(target, "target", (S, K + 1, V), f32, dev)
+    dp = None if draft is None else _vec(draft, "draft", (S, K, V), f32, dev)
+    xp, cp = _vec(tokens, "tokens", (S, K), i32, dev), _vec(counts, "counts", (S,), i32, dev)
+    ap, sp = _vec(u_accept, "u_accept", (S, K), f32, dev), _vec(u_sample, "u_sample", (S,), f32, dev)
+    made = (None if out is not None else torch.empty((S, K + 1), dtype=i32, device=target.device),
+            None if accepted is not None else torch.empty((S,), dtype=i32, device=target.device))
+    out = made[0] if out is None else _out(out, (S, K + 1), target.device, i32)
+    accepted = made[1] if accepted is None else _out(accepted, (S,), target.device, i32, name="accepted")
+    ws, nbytes, buf = _graph_workspace("keops_verify_draft", dev, S, K, V)
+    _run("keops_verify_draft", dev, stream, lib().keops_verify_draft, tp, dp if K else None, xp, cp, ap, sp, S, K, V, out.data_ptr(),
+         accepted.data_ptr(), ws, nbytes)
+    if stream is not None:
+        _keep(stream, dev, *made, buf)
     return out, accepted
