@@ -149,7 +149,7 @@ void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st);
 void launch_attend_score_sums(const AttendArgs &a, hipStream_t st);
 void launch_attend_sums_join(const AttendArgs &a, hipStream_t st);
-int launch_evict(const EvictArgs &a, hipStream_t st);
+void launch_evict(const EvictArgs &a, hipStream_t st);
 void launch_verify(const VerifyArgs &a, hipStream_t st);
 
 // ---------------------------------------------------------------- element types

@@ -18,7 +18,7 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr double kMaxWorkspace = 1.0e14;    // more than any device holds; below the 64-bit limit
 // Work-groups that a launch aims for, per compute unit, when it splits a long axis.
 constexpr int64_t kManyWgsPerCu = 2;
-constexpr int64_t kSumsWgsPerCu = 2;
+constexpr int64_t kSumsWgsPerCu = 4;
 // Few rows: least slots of a work-group's run (one tile of 32 for each wave), and the longest
 // sequences that are left whole when there are enough of them to fill the device.
 constexpr int kFewLeast = 128;
@@ -138,7 +138,9 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       const int64_t nst = ceil_div(max_len, kSumSlotsTile);
       if ((double)S * (double)H * (double)nst > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
       const int64_t wgs = S * H * nst;
-      p->nrow = std::max<int64_t>(1, std::min(ceil_div(kSumsWgsPerCu * cus, std::max<int64_t>(wgs, 1)), rows / 256));
+      // slots outside every window cost next to nothing
+      const int64_t busy = std::max<int64_t>(1, S * H * std::min(nst, ceil_div(span, kSumSlotsTile) + 1));
+      p->nrow = std::max<int64_t>(1, std::min(ceil_div(kSumsWgsPerCu * cus, busy), rows / 256));
       p->sums_grid = wgs * p->nrow;
       if (p->nrow > 1) {
         if (4.0 * (double)p->nrow * (double)S * (double)H * (double)max_len > kMaxWorkspace) return KEOPS_ERR_ALLOC;
@@ -324,10 +326,7 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
   a.recent = recent;
   a.kept = kept;
   a.new_lens = new_lens;
-  if (launch_evict(a, st)) {
-    (void)hipGetLastError();
-    return KEOPS_ERR_HIP;
-  }
+  launch_evict(a, st);
   return check_launch();
 }
 

@@ -5,13 +5,14 @@
 // slot).  Kept slots move, in their order, to slots 0 .. of the pages in new_table, keys,
 // values and weights alike; n <= budget keeps them all.
 //
-// Selection: one work-group per (sequence, head) finds the smallest kept weight by three passes
-// over 11, 11 and 10 bits of an order-preserving whole number (counts in LDS; integers, so the
-// order of the additions does not matter), then one scan of counts gives every slot its place.
-// It is bound by the latency of its steps: page numbers and weights are loaded eight at a time,
-// and a wave whose lanes all meet one count adds to it once (cleared weights are all equal).
-// The move is a second kernel, one 16-byte piece of a key and of a value row per thread, bound
-// by HBM.
+// Selection: one work-group per (sequence, head) holds up to 32,768 weights in registers as whole
+// numbers of the same order (longer rows are read again for each pass), finds the smallest kept one
+// by three passes over 11, 11 and 10 bits (counts in LDS: whole numbers, so the order of the
+// additions does not matter), and gives every slot its place from the counts of the waves before
+// it.  It is bound by the latency of its steps: page numbers and weights are loaded eight at a
+// time, lanes count in eight copies, and a wave whose lanes all meet one count adds to it once
+// (cleared weights are all equal).  The move is a second kernel, one 16-byte piece of a key and of
+// a value row per thread, bound by HBM.
 #include "paged.h"
 
 namespace kmi {
@@ -20,9 +21,10 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / kWave;
 constexpr int kBins = 2048;             // counts of a pass
-constexpr int kHistCopies = 2;          // even and odd lanes: fewer collisions
-constexpr int kSelectCache = 32768;     // weights held in LDS (132 KB); longer rows are read again
+constexpr int kHistCopies = 8;          // lanes of a wave spread over copies: fewer collisions
+constexpr int kHeld = 32;               // keys of a thread
 constexpr int kBatch = 8;
+constexpr int kSegment = kHeld * kSelectThreads;
 
 // Whole numbers ordered as the floats are; -0 equals 0, NaN above everything.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -33,19 +35,41 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 struct SelectShared {
   uint32_t hist[kBins * kHistCopies];
-  uint32_t wave_gt[kSelectWaves], wave_eq[kSelectWaves];
+  uint32_t place[kHeld * kSelectWaves];  // kept before each 64 slots, two counts in one word
+  __align__(16) uint32_t wave_sum[kSelectWaves];
   uint32_t prefix, need;
 };
 
-// One spare word after every 32 keeps threads that read at a stride of a power of two apart.
-__device__ __forceinline__ int cache_at(int i) { return i + (i >> 5); }
+// Sum of the waves before this one; all of them in `total`.
+__device__ __forceinline__ uint32_t before_wave(const uint32_t *wave_sum, int wave, uint32_t *total) {
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w4 = 0; w4 < kSelectWaves / 4; ++w4) {
+    const u32x4 x = ((const u32x4 *)wave_sum)[w4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      before += w4 * 4 + u < wave ? x[u] : 0u;
+      all += x[u];
+    }
+  }
+  *total = all;
+  return before;
+}
+__device__ __forceinline__ uint32_t scan_u32(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint32_t up = __shfl_up(v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
 
-__global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int cache_words) {
+__global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
   __shared__ SelectShared sh;
-  extern __shared__ uint32_t cache[];
   const int H = a.c.heads;
   const int s = blockIdx.x / H, h = blockIdx.x - s * H;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   int64_t n64 = a.c.lens[s];
   const int64_t most = (int64_t)a.c.table_width * a.c.page.d;
   n64 = n64 < 0 ? 0 : (n64 > most ? most : n64);
@@ -61,62 +85,47 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
   for (int r = tid; r < recent; r += kSelectThreads) kept[a.budget - recent + r] = n - recent + r;
   if (need0 == 0) return;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
-  // eight keys, slots first + 1024 u: an absent slot's is 0, the least
-  const auto load = [&](int first, uint32_t *k) {
-    SlotPlace p[kBatch];
+  const int segments = (M + kSegment - 1) / kSegment;
+  // keys of slots segment + tid + 1024 u: an absent slot's is 0, the least
+  uint32_t key[kHeld];
+  const auto load = [&](int from) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = first + u * kSelectThreads;
-      p[u] = SlotPlace{-1, 0};
-      if (i < M) p[u] = slot_place(a.c, trow, (uint32_t)(sink + i));
+    for (int b = 0; b < kHeld; b += kBatch) {
+      if (from + b * kSelectThreads >= M) break;
+      SlotPlace p[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = from + (b + u) * kSelectThreads + tid;
+        p[u] = SlotPlace{-1, 0};
+        if (i < M) p[u] = slot_place(a.c, trow, (uint32_t)(sink + i));
+      }
+      float w[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        w[u] = 0.0f;
+        if (p[u].page >= 0) w[u] = a.c.weights[((int64_t)p[u].page * H + h) * a.c.page.d + p[u].row];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) key[b + u] = p[u].page < 0 ? 0u : weight_key(w[u]);
     }
-    float w[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      w[u] = 0.0f;
-      if (p[u].page >= 0) w[u] = a.c.weights[((int64_t)p[u].page * H + h) * a.c.page.d + p[u].row];
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) k[u] = p[u].page < 0 ? 0u : weight_key(w[u]);
-  };
-  const bool held = cache_at(M - 1) < cache_words;
-  if (held) {
-    for (int i = tid; i < M; i += kBatch * kSelectThreads) {
-      uint32_t k[kBatch];
-      load(i, k);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (i + u * kSelectThreads < M) cache[cache_at(i + u * kSelectThreads)] = k[u];
-    }
-  }
-  const auto key = [&](int i) -> uint32_t {
-    if (held) return cache[cache_at(i)];
-    const SlotPlace p = slot_place(a.c, trow, (uint32_t)(sink + i));
-    return p.page < 0 ? 0u : weight_key(a.c.weights[((int64_t)p.page * H + h) * a.c.page.d + p.row]);
   };
 
   // the need-th largest key, digit by digit
   uint32_t prefix = 0, need = (uint32_t)need0;
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < kBins * kHistCopies; i += kSelectThreads) sh.hist[i] = 0;
+    for (int i = tid; i < kBins * kHistCopies / 4; i += kSelectThreads) ((u32x4 *)sh.hist)[i] = (u32x4){0, 0, 0, 0};
     __syncthreads();
-    for (int base = tid; base - tid < M; base += kBatch * kSelectThreads) {
-      uint32_t k[kBatch];
-      if (held) {
+#pragma unroll 1
+    for (int from = 0; from < M; from += kSegment) {
+      if (pass == 0 || segments > 1) load(from);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int i = base + u * kSelectThreads;
-          k[u] = i < M ? cache[cache_at(i)] : 0u;
-        }
-      } else {
-        load(base, k);
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const bool in = base + u * kSelectThreads < M && (pass == 0 || (k[u] >> (shift + bits)) == (prefix >> (shift + bits)));
-        const uint32_t bin = (k[u] >> shift) & ((1u << bits) - 1u);
+      for (int u = 0; u < kHeld; ++u) {
+        const int at = from + u * kSelectThreads;
+        if (at >= M) break;
+        const bool in = at + tid < M && (pass == 0 || (key[u] >> (shift + bits)) == (prefix >> (shift + bits)));
+        const uint32_t bin = (key[u] >> shift) & ((1u << bits) - 1u);
         const uint64_t who = __ballot(in);
         if (!who) continue;
         const uint32_t one = __builtin_amdgcn_readlane(bin, __ffsll((unsigned long long)who) - 1);
@@ -132,20 +141,15 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
     uint32_t cnt[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int bin = kBins - 1 - (2 * tid + b);
-      cnt[b] = sh.hist[bin * kHistCopies] + sh.hist[bin * kHistCopies + 1];
+      const u32x4 *c = (const u32x4 *)&sh.hist[(kBins - 1 - (2 * tid + b)) * kHistCopies];
+      const u32x4 x = c[0] + c[1];
+      cnt[b] = (x[0] + x[1]) + (x[2] + x[3]);
     }
-    const uint32_t own = cnt[0] + cnt[1];
-    uint32_t upto = own;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const uint32_t up = __shfl_up(upto, o);
-      if (lane >= o) upto += up;
-    }
-    if (lane == kWave - 1) sh.wave_gt[wave] = upto;
+    const uint32_t own = cnt[0] + cnt[1], upto = scan_u32(own, lane);
+    if (lane == kWave - 1) sh.wave_sum[wave] = upto;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) upto += sh.wave_gt[w];
-    uint32_t above = upto - own;
+    uint32_t total;
+    uint32_t above = upto - own + before_wave(sh.wave_sum, wave, &total);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       if (above < need && need <= above + cnt[b]) {
@@ -158,31 +162,42 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
     prefix = sh.prefix;
     need = sh.need;
   }
-  // keys above `prefix` are kept, and the first `need` of those equal to it.  Each thread owns
-  // a run of slots; one scan of both counts gives its places.
-  const int L = (M + kSelectThreads - 1) / kSelectThreads;
-  const int i0 = tid * L < M ? tid * L : M, i1 = i0 + L < M ? i0 + L : M;
-  uint32_t gt = 0, eq = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    gt += k > prefix;
-    eq += k == prefix;
-  }
-  uint32_t sgt = gt, seq = eq;
+  // keys above `prefix` are kept, and the first `need` of those equal to it
+  uint32_t base_gt = 0, base_eq = 0;
+#pragma unroll 1
+  for (int from = 0; from < M; from += kSegment) {
+    if (segments > 1) load(from);
 #pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint32_t ug = __shfl_up(sgt, o), ue = __shfl_up(seq, o);
-    if (lane >= o) { sgt += ug; seq += ue; }
-  }
-  if (lane == kWave - 1) { sh.wave_gt[wave] = sgt; sh.wave_eq[wave] = seq; }
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) { sgt += sh.wave_gt[w]; seq += sh.wave_eq[w]; }
-  uint32_t bgt = sgt - gt, beq = seq - eq;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    if (k > prefix || (k == prefix && beq < need)) kept[sink + bgt + (beq < need ? beq : need)] = sink + i;
-    bgt += k > prefix;
-    beq += k == prefix;
+    for (int u = 0; u < kHeld; ++u) {
+      const int at = from + u * kSelectThreads;
+      const bool in = at + tid < M;
+      const uint64_t gt = __ballot(in && key[u] > prefix), eq = __ballot(in && key[u] == prefix);
+      if (lane == 0) sh.place[u * kSelectWaves + wave] = (uint32_t)__popcll(gt) | ((uint32_t)__popcll(eq) << 16);
+    }
+    __syncthreads();
+    // 512 counts in slot order, each half at most 32,768 in all
+    uint32_t own = 0, upto = 0, total;
+    if (tid < kHeld * kSelectWaves) own = sh.place[tid];
+    upto = scan_u32(own, lane);
+    if (lane == kWave - 1) sh.wave_sum[wave] = upto;
+    __syncthreads();
+    upto += before_wave(sh.wave_sum, wave, &total);
+    if (tid < kHeld * kSelectWaves) sh.place[tid] = upto - own;
+    __syncthreads();
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int at = from + u * kSelectThreads;
+      if (at >= M) break;
+      const bool in = at + tid < M, is_gt = in && key[u] > prefix, is_eq = in && key[u] == prefix;
+      const uint32_t pre = sh.place[u * kSelectWaves + wave];
+      const uint32_t gt = base_gt + (pre & 0xffffu) + __popcll(__ballot(is_gt) & below);
+      const uint32_t eq = base_eq + (pre >> 16) + __popcll(__ballot(is_eq) & below);
+      if (is_gt || (is_eq && eq < need)) kept[sink + gt + (eq < need ? eq : need)] = sink + at + tid;
+    }
+    base_gt += total & 0xffffu;
+    base_eq += total >> 16;
+    __syncthreads();
   }
 }
 
@@ -216,19 +231,11 @@ __global__ __launch_bounds__(256) void move_kernel(EvictArgs a, int pieces, int6
 
 }  // namespace
 
-int launch_evict(const EvictArgs &a, hipStream_t st) {
-  const int64_t most = (int64_t)a.c.table_width * a.c.page.d;
-  const int64_t keys = most < kSelectCache ? most : kSelectCache;
-  const int words = (int)(keys + keys / 32 + 1);
-  const size_t bytes = (size_t)words * sizeof(uint32_t);
-  if (bytes > 32768 &&
-      hipFuncSetAttribute((const void *)select_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != hipSuccess)
-    return -1;
-  select_kernel<<<dim3((unsigned)(a.c.seqs * a.c.heads)), kSelectThreads, bytes, st>>>(a, words);
+void launch_evict(const EvictArgs &a, hipStream_t st) {
+  select_kernel<<<dim3((unsigned)(a.c.seqs * a.c.heads)), kSelectThreads, 0, st>>>(a);
   const int pieces = a.c.dim * a.itemsize / 16;
   const int64_t total = (int64_t)a.c.seqs * a.c.heads * a.budget * pieces;
   move_kernel<<<dim3((unsigned)((total + 255) / 256)), 256, 0, st>>>(a, pieces, total);
-  return 0;
 }
 
 }  // namespace kmi

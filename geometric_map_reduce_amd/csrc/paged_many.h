@@ -49,7 +49,8 @@ static __device__ const uint32_t kZeroRow[128] = {};
 __device__ __forceinline__ void dma16(const void *from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
 }
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
@@ -60,11 +61,15 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   constexpr int kSteps = D / 16, kCols = D / 32, kSub = KT / 32;
   constexpr int kPieces = D / 8;                     // 16-byte pieces of a row in LDS
   constexpr int kLoads = KT * kPieces / kManyThreads;
-  constexpr int kChunk = 8;                          // tiles whose addresses are placed together
+  // tiles in LDS: as many as leave room for two work-groups on a compute unit (8-bit ones pass
+  // registers, one ahead)
+  constexpr int kBufs = E4M3 ? 2 : (D == 64 || D == 256 ? 4 : (D == 96 ? 3 : 2));
+  constexpr int kChunk = D == 96 ? 4 : 8;            // tiles whose addresses are placed together
   constexpr int kPlace = kChunk * KT / kManyThreads; // slots a thread places
+  static_assert(kBufs <= kChunk, "a chunk is placed before the first fetch from it");
   static_assert(KT * kPieces % kManyThreads == 0 && kChunk * KT % kManyThreads == 0, "whole pieces per thread");
-  __shared__ __align__(16) uint16_t sk[2][KT * D];
-  __shared__ __align__(16) uint16_t sv[2][KT * D];
+  __shared__ __align__(16) uint16_t sk[kBufs][KT * D];
+  __shared__ __align__(16) uint16_t sv[kBufs][KT * D];
   __shared__ int64_t off[2][kChunk * KT];
   __shared__ uint64_t present[2][kChunk * KT / 64];    // which of 64 slots are there
 
@@ -173,7 +178,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
         gv[i][0] = y.x; gv[i][1] = y.y;
       }
     } else {
-      const uint32_t ldk = lds_address(sk[tile & 1]) + wave * 1024, ldv = lds_address(sv[tile & 1]) + wave * 1024;
+      const uint32_t ldk = lds_address(sk[tile % kBufs]) + wave * 1024, ldv = lds_address(sv[tile % kBufs]) + wave * 1024;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
@@ -192,11 +197,13 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
         const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
         const u32x4 x = widen_e4m3<T>((u32x2){gk[i][0], gk[i][1]});
         const u32x4 y = widen_e4m3<T>((u32x2){gv[i][0], gv[i][1]});
-        *(u32x4 *)&sk[tile & 1][row * D + (p ^ k_swizzle<D>(row)) * 8] = x;
-        *(u32x4 *)&sv[tile & 1][row * D + (p ^ v_swizzle<D>(row)) * 8] = keep_if(y, (held >> i) & 1u);
+        *(u32x4 *)&sk[tile % kBufs][row * D + (p ^ k_swizzle<D>(row)) * 8] = x;
+        *(u32x4 *)&sv[tile % kBufs][row * D + (p ^ v_swizzle<D>(row)) * 8] = keep_if(y, (held >> i) & 1u);
       }
+    } else if (tile + kBufs - 2 < tiles) {
+      dma_wait<(kBufs - 2) * 2 * kLoads>();        // the tiles after this one may be on their way
     } else {
-      dma_wait();
+      dma_wait<0>();
     }
   };
 
@@ -286,13 +293,13 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
         }
   };
   const auto turn = [&](int buf, int tile) {
-    if (tile + 1 < tiles) fetch(tile + 1);
+    if (tile + kBufs - 1 < tiles) fetch(tile + kBufs - 1);
     const int j0 = lo + tile * KT;
     const uint64_t there = present_at(tile);
     const bool masked = there != (KT == 64 ? ~(uint64_t)0 : 0xffffffffu) || j0 + KT - 1 > first_pos ||
                         (a.window > 0 && j0 <= last_pos - a.window);
     step(masked, buf, tile, there);
-    if (tile % kChunk == kChunk / 2 && (tile / kChunk + 1) * kChunk < tiles) {
+    if (tile % kChunk == 0 && tile + kChunk < tiles) {      // a chunk ahead of the first fetch from it
       page_put(tile / kChunk + 1);
       page_load(tile / kChunk + 2);
     }
@@ -304,11 +311,11 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     page_put(0);
     page_load(1);
     __syncthreads();
-    fetch(0);
+    for (int t = 0; t < kBufs - 1 && t < tiles; ++t) fetch(t);
     arrive(0);
     __syncthreads();
   }
-  for (int tile = 0; tile < tiles; ++tile) turn(tile & 1, tile);
+  for (int tile = 0; tile < tiles; ++tile) turn(tile % kBufs, tile);
   if (__any(odd)) {
     // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
     const int stop = lo + tiles * KT < end ? lo + tiles * KT : end;
@@ -393,19 +400,11 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
   if (slot0 >= sp.n) return;
   int j[2];
   SlotPlace pl[2];
-  u32x4 kf[2][kSteps];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     j[x] = slot0 + wave * 64 + x * 32 + col;
     pl[x] = SlotPlace{-1, 0};
     if (j[x] < sp.n) pl[x] = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)j[x]);
-    const int64_t o = place_offset(a.c, pl[x]);
-    const char *kp = a.c.k + (int64_t)h * a.c.head_stride + (o < 0 ? 0 : o);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (E4M3) kf[x][i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
-      else kf[x][i] = *(const u32x4 *)(kp + i * 32 + hi * 16);
-    }
   }
   // tokens that see any slot of the tile
   int i0 = slot0 - sp.first, i1 = sp.m;
@@ -419,6 +418,18 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
   const int per = (tiles + a.nrow - 1) / a.nrow;
   const int tile0 = rsplit * per < tiles ? rsplit * per : tiles;
   const int tile1 = tile0 + per < tiles ? tile0 + per : tiles;
+  u32x4 kf[2][kSteps];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    if (tile0 >= tile1) break;       // no row sees the tile
+    const int64_t o = place_offset(a.c, pl[x]);
+    const char *kp = a.c.k + (int64_t)h * a.c.head_stride + (o < 0 ? 0 : o);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (E4M3) kf[x][i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
+      else kf[x][i] = *(const u32x4 *)(kp + i * 32 + hi * 16);
+    }
+  }
   const float c = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
 
   u32x4 gq[kLoads];
