@@ -9,8 +9,8 @@
 // numbers of the same order (longer rows are read again for each pass), finds the smallest kept one
 // by three passes over 11, 11 and 10 bits (counts in LDS: whole numbers, so the order of the
 // additions does not matter), and gives every slot its place from the counts of the waves before
-// it.  It is bound by the latency of its steps: page numbers and weights are loaded eight at a
-// time, lanes count in eight copies, and a wave whose lanes all meet one count adds to it once
+// it.  It is bound by the latency of its steps: a thread loads all its page numbers, then
+// all its weights, lanes count in two copies, and 512 keys of a wave that all meet one count add to it once
 // (cleared weights are all equal).  The move is a second kernel, one 16-byte piece of a key and of
 // a value row per thread, bound by HBM.
 #include "paged.h"
@@ -21,10 +21,10 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / kWave;
 constexpr int kBins = 2048;             // counts of a pass
-constexpr int kHistCopies = 8;          // lanes of a wave spread over copies: fewer collisions
-constexpr int kHeld = 32;               // keys of a thread
-constexpr int kBatch = 8;
-constexpr int kSegment = kHeld * kSelectThreads;
+constexpr int kHistCopies = 2;          // even and odd lanes: fewer collisions
+constexpr int kHistStride = kBins + 32; // a bin's copies lie in different banks
+constexpr int kHeldMost = 32;           // keys of a thread, and for short rows: the loops over them
+constexpr int kHeldFew = 4;             // are unrolled, and code that runs once is paid for by its size
 
 // Whole numbers ordered as the floats are; -0 equals 0, NaN above everything.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -33,11 +33,14 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+template <int kHeld>
 struct SelectShared {
-  uint32_t hist[kBins * kHistCopies];
+  __align__(16) uint32_t hist[kHistStride * kHistCopies];
   uint32_t place[kHeld * kSelectWaves];  // kept before each 64 slots, two counts in one word
   __align__(16) uint32_t wave_sum[kSelectWaves];
-  uint32_t prefix, need;
+  uint32_t prefix, need, count;
+  uint32_t cand_key[kWave], cand_slot[kWave], cands;
+  uint32_t cut_key, cut_slot;
 };
 
 // Sum of the waves before this one; all of them in `total`.
@@ -64,8 +67,10 @@ __device__ __forceinline__ uint32_t scan_u32(uint32_t v, int lane) {
   return v;
 }
 
+template <int kHeld>
 __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
-  __shared__ SelectShared sh;
+  constexpr int kBatch = kHeld < 8 ? kHeld : 8, kSegment = kHeld * kSelectThreads;
+  __shared__ SelectShared<kHeld> sh;
   const int H = a.c.heads;
   const int s = blockIdx.x / H, h = blockIdx.x - s * H;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -86,64 +91,91 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
   if (need0 == 0) return;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
   const int segments = (M + kSegment - 1) / kSegment;
-  // keys of slots segment + tid + 1024 u: an absent slot's is 0, the least
+  // keys of slots segment + tid + 1024 u: an absent slot's is 0, the least.  Page and row go on
+  // by 1024 slots with an addition each.
   uint32_t key[kHeld];
+  const uint32_t ps = a.c.page.d, step_page = kSelectThreads / ps, step_row = kSelectThreads - step_page * ps;
   const auto load = [&](int from) {
+    const uint32_t j0 = (uint32_t)(sink + from + tid);
+    uint32_t pi = fast_div(a.c.page, j0), row = j0 - pi * ps;
+    uint32_t rows = row;
 #pragma unroll
     for (int b = 0; b < kHeld; b += kBatch) {
-      if (from + b * kSelectThreads >= M) break;
-      SlotPlace p[kBatch];
+      if (from + b * kSelectThreads < M) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int i = from + (b + u) * kSelectThreads + tid;
-        p[u] = SlotPlace{-1, 0};
-        if (i < M) p[u] = slot_place(a.c, trow, (uint32_t)(sink + i));
+        for (int u = b; u < b + kBatch; ++u) {
+          int32_t pg = -1;
+          if (pi < a.c.table_width && from + u * kSelectThreads + tid < M) pg = trow[pi];
+          key[u] = (uint32_t)pg;
+          pi += step_page;
+          row += step_row;
+          if (row >= ps) { row -= ps; ++pi; }
+        }
       }
-      float w[kBatch];
+    }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        w[u] = 0.0f;
-        if (p[u].page >= 0) w[u] = a.c.weights[((int64_t)p[u].page * H + h) * a.c.page.d + p[u].row];
+    for (int b = 0; b < kHeld; b += kBatch) {
+      if (from + b * kSelectThreads < M) {
+        float w[kBatch];
+        bool there[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          // at most 2^32 weights: their cache would not fit the device otherwise
+          const uint32_t at = (key[b + u] * (uint32_t)H + (uint32_t)h) * ps + rows;
+          there[u] = key[b + u] < a.c.pages;
+          w[u] = 0.0f;
+          if (there[u]) w[u] = a.c.weights[at];
+          rows += step_row;
+          if (rows >= ps) rows -= ps;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) key[b + u] = there[u] ? weight_key(w[u]) : 0u;
       }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) key[b + u] = p[u].page < 0 ? 0u : weight_key(w[u]);
     }
   };
 
   // the need-th largest key, digit by digit
-  uint32_t prefix = 0, need = (uint32_t)need0;
+  uint32_t prefix = 0, need = (uint32_t)need0, count = 0, cut = 0xffffffffu;
+  if (tid == 0) sh.cands = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < kBins * kHistCopies / 4; i += kSelectThreads) ((u32x4 *)sh.hist)[i] = (u32x4){0, 0, 0, 0};
+    for (int i = tid; i < kHistStride * kHistCopies / 4; i += kSelectThreads) ((u32x4 *)sh.hist)[i] = (u32x4){0, 0, 0, 0};
     __syncthreads();
+    uint32_t *mine = sh.hist + (lane & (kHistCopies - 1)) * kHistStride;
 #pragma unroll 1
     for (int from = 0; from < M; from += kSegment) {
       if (pass == 0 || segments > 1) load(from);
 #pragma unroll
-      for (int u = 0; u < kHeld; ++u) {
-        const int at = from + u * kSelectThreads;
-        if (at >= M) break;
-        const bool in = at + tid < M && (pass == 0 || (key[u] >> (shift + bits)) == (prefix >> (shift + bits)));
-        const uint32_t bin = (key[u] >> shift) & ((1u << bits) - 1u);
-        const uint64_t who = __ballot(in);
-        if (!who) continue;
-        const uint32_t one = __builtin_amdgcn_readlane(bin, __ffsll((unsigned long long)who) - 1);
-        if (__ballot(in && bin != one) == 0) {
-          if (lane == 0) atomicAdd(&sh.hist[one * kHistCopies], (uint32_t)__popcll(who));
-        } else if (in) {
-          atomicAdd(&sh.hist[bin * kHistCopies + (lane & (kHistCopies - 1))], 1u);
+      for (int b = 0; b < kHeld; b += kBatch) {
+        if (from + b * kSelectThreads >= M) continue;
+        uint32_t bin[kBatch];
+        bool in[kBatch], same = true;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          in[u] = from + (b + u) * kSelectThreads + tid < M &&
+                  (pass == 0 || (key[b + u] >> (shift + bits)) == (prefix >> (shift + bits)));
+          bin[u] = (key[b + u] >> shift) & ((1u << bits) - 1u);
+          same &= in[u] && bin[u] == (uint32_t)__builtin_amdgcn_readfirstlane(bin[0]);
         }
+        if (__all(same)) {
+          if (lane == 0) atomicAdd(&mine[bin[0]], (uint32_t)(kBatch * kWave));
+          continue;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (in[u]) atomicAdd(&mine[bin[u]], 1u);
       }
     }
     __syncthreads();
     // thread t has the counts 2 t and 2 t + 1 from the top
-    uint32_t cnt[2];
+    const int low = kBins - 2 - 2 * tid;
+    uint32_t cnt[2] = {0, 0};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const u32x4 *c = (const u32x4 *)&sh.hist[(kBins - 1 - (2 * tid + b)) * kHistCopies];
-      const u32x4 x = c[0] + c[1];
-      cnt[b] = (x[0] + x[1]) + (x[2] + x[3]);
+    for (int c = 0; c < kHistCopies; ++c) {
+      const u32x2 x = *(const u32x2 *)&sh.hist[c * kHistStride + low];
+      cnt[0] += x.y;
+      cnt[1] += x.x;
     }
     const uint32_t own = cnt[0] + cnt[1], upto = scan_u32(own, lane);
     if (lane == kWave - 1) sh.wave_sum[wave] = upto;
@@ -155,49 +187,104 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
       if (above < need && need <= above + cnt[b]) {
         sh.prefix = prefix | ((uint32_t)(kBins - 1 - (2 * tid + b)) << shift);
         sh.need = need - above;
+        sh.count = cnt[b];
       }
       above += cnt[b];
     }
     __syncthreads();
     prefix = sh.prefix;
     need = sh.need;
+    count = sh.count;
+    if (count == need) break;          // all that share the digits so far are kept
+    if (count <= kWave && segments == 1) {
+      // few share them: one wave ranks them by weight and slot
+#pragma unroll
+      for (int b = 0; b < kHeld; b += kBatch) {
+        if (b * kSelectThreads < M) {
+#pragma unroll
+          for (int u = b; u < b + kBatch; ++u) {
+            if (u * kSelectThreads + tid < M && (key[u] >> shift) == (prefix >> shift)) {
+              const uint32_t at = atomicAdd(&sh.cands, 1u);
+              sh.cand_key[at] = key[u];
+              sh.cand_slot[at] = (uint32_t)(u * kSelectThreads + tid);
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (wave == 0) {
+        const uint32_t k = sh.cand_key[lane], i = sh.cand_slot[lane];
+        uint32_t rank = 0;
+        for (uint32_t m = 0; m < count; ++m) {
+          const uint32_t km = __builtin_amdgcn_readlane(k, m), im = __builtin_amdgcn_readlane(i, m);
+          rank += km > k || (km == k && im < i);
+        }
+        if ((uint32_t)lane < count && rank == need - 1) {
+          sh.cut_key = k;
+          sh.cut_slot = i;
+        }
+      }
+      __syncthreads();
+      prefix = sh.cut_key;
+      cut = sh.cut_slot;
+      need = count;                    // settled
+      break;
+    }
   }
-  // keys above `prefix` are kept, and the first `need` of those equal to it
-  uint32_t base_gt = 0, base_eq = 0;
+  // kept: keys above `prefix`, and those equal to it up to slot `cut`.  Without a cut yet and with
+  // more equal keys than wanted, a first round over the equal ones finds the need-th.  In either
+  // round a slot's place is the number of slots before it: counts of the waves, scanned.
 #pragma unroll 1
-  for (int from = 0; from < M; from += kSegment) {
-    if (segments > 1) load(from);
+  for (int round = need == count ? 1 : 0; round < 2; ++round) {
+    uint32_t base = 0;
+#pragma unroll 1
+    for (int from = 0; from < M; from += kSegment) {
+      if (segments > 1) load(from);
+      uint32_t counts = 0;             // lane u counts the wave's 64 slots of step u
+      uint32_t mine = 0;               // and this thread's keep as bits
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const int at = from + u * kSelectThreads;
-      const bool in = at + tid < M;
-      const uint64_t gt = __ballot(in && key[u] > prefix), eq = __ballot(in && key[u] == prefix);
-      if (lane == 0) sh.place[u * kSelectWaves + wave] = (uint32_t)__popcll(gt) | ((uint32_t)__popcll(eq) << 16);
-    }
-    __syncthreads();
-    // 512 counts in slot order, each half at most 32,768 in all
-    uint32_t own = 0, upto = 0, total;
-    if (tid < kHeld * kSelectWaves) own = sh.place[tid];
-    upto = scan_u32(own, lane);
-    if (lane == kWave - 1) sh.wave_sum[wave] = upto;
-    __syncthreads();
-    upto += before_wave(sh.wave_sum, wave, &total);
-    if (tid < kHeld * kSelectWaves) sh.place[tid] = upto - own;
-    __syncthreads();
-    const uint64_t below = ((uint64_t)1 << lane) - 1;
+      for (int b = 0; b < kHeld; b += kBatch) {
+        if (from + b * kSelectThreads < M) {
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const int at = from + u * kSelectThreads;
-      if (at >= M) break;
-      const bool in = at + tid < M, is_gt = in && key[u] > prefix, is_eq = in && key[u] == prefix;
-      const uint32_t pre = sh.place[u * kSelectWaves + wave];
-      const uint32_t gt = base_gt + (pre & 0xffffu) + __popcll(__ballot(is_gt) & below);
-      const uint32_t eq = base_eq + (pre >> 16) + __popcll(__ballot(is_eq) & below);
-      if (is_gt || (is_eq && eq < need)) kept[sink + gt + (eq < need ? eq : need)] = sink + at + tid;
+          for (int u = b; u < b + kBatch; ++u) {
+            const uint32_t i = (uint32_t)(from + u * kSelectThreads + tid);
+            const bool eq = key[u] == prefix;
+            const bool in = i < (uint32_t)M && (round == 0 ? eq : key[u] > prefix || (eq && i <= cut));
+            const uint32_t c = (uint32_t)__popcll(__ballot(in));
+            mine |= in ? 1u << u : 0u;
+            if (lane == u) counts = c;
+          }
+        }
+      }
+      if (lane < kHeld) sh.place[lane * kSelectWaves + wave] = counts;
+      __syncthreads();
+      uint32_t own = 0, total;
+      if (tid < kHeld * kSelectWaves) own = sh.place[tid];
+      uint32_t upto = scan_u32(own, lane);
+      if (lane == kWave - 1) sh.wave_sum[wave] = upto;
+      __syncthreads();
+      upto += before_wave(sh.wave_sum, wave, &total);
+      if (tid < kHeld * kSelectWaves) sh.place[tid] = upto - own;
+      __syncthreads();
+      const uint64_t below = ((uint64_t)1 << lane) - 1;
+      if (lane < kHeld) counts = sh.place[lane * kSelectWaves + wave];
+#pragma unroll
+      for (int b = 0; b < kHeld; b += kBatch) {
+        if (from + b * kSelectThreads < M) {
+#pragma unroll
+          for (int u = b; u < b + kBatch; ++u) {
+            const bool in = (mine >> u) & 1u;
+            const uint32_t place = base + __builtin_amdgcn_readlane(counts, u) + __popcll(__ballot(in) & below);
+            const int i = from + u * kSelectThreads + tid;
+            if (in && round == 1) kept[sink + place] = sink + i;
+            if (in && round == 0 && place == need - 1) sh.cut_slot = (uint32_t)i;
+          }
+        }
+      }
+      base += total;
+      __syncthreads();
     }
-    base_gt += total & 0xffffu;
-    base_eq += total >> 16;
-    __syncthreads();
+    if (round == 0) cut = sh.cut_slot;
   }
 }
 
@@ -232,7 +319,11 @@ __global__ __launch_bounds__(256) void move_kernel(EvictArgs a, int pieces, int6
 }  // namespace
 
 void launch_evict(const EvictArgs &a, hipStream_t st) {
-  select_kernel<<<dim3((unsigned)(a.c.seqs * a.c.heads)), kSelectThreads, 0, st>>>(a);
+  const dim3 grid((unsigned)(a.c.seqs * a.c.heads));
+  if ((int64_t)a.c.table_width * a.c.page.d <= kHeldFew * kSelectThreads)
+    select_kernel<kHeldFew><<<grid, kSelectThreads, 0, st>>>(a);
+  else
+    select_kernel<kHeldMost><<<grid, kSelectThreads, 0, st>>>(a);
   const int pieces = a.c.dim * a.itemsize / 16;
   const int64_t total = (int64_t)a.c.seqs * a.c.heads * a.budget * pieces;
   move_kernel<<<dim3((unsigned)((total + 255) / 256)), 256, 0, st>>>(a, pieces, total);
