@@ -104,7 +104,7 @@ struct AttendArgs {
   int32_t whole;                // few rows: a work-group has all slots of one (sequence, head)
   float *part_o;                // [..][dim], sums under the part's maximum
   float2 *part_ml;              // (maximum in log2 units, sum)
-  // few-rows form with weights: scores [seqs * heads][rows][score_stride] in log2 units
+  // few-rows form with weights: scores [seqs * heads][score_stride / 4][rows][4] in log2 units
   float *scores;
   int64_t score_stride;
   int32_t score_rows;
@@ -140,14 +140,13 @@ void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st
 constexpr int kFewRowsMax = 32;      // rows (new tokens x group) of the few-rows form
 constexpr int kManyRowsTile = 128;   // rows of a work-group of the many-rows form
 constexpr int kSumSlotsTile = 256;   // slots of a work-group of the column sums
-// grid 0: the work-groups of the variant that a compute unit holds (-1: HIP error).  join_rows: rows of
-// a work-group of the joining pass, 0: none.
+// Both passes.  grid 0: the work-groups of the variant that a compute unit holds (-1: HIP error).
+// join_rows: rows of a work-group that joins parts, 0: there are none.
 int launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, int grid, int join_rows,
                       hipStream_t st);
 void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
 void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st);
-void launch_attend_score_sums(const AttendArgs &a, hipStream_t st);
 void launch_attend_sums_join(const AttendArgs &a, hipStream_t st);
 void launch_evict(const EvictArgs &a, hipStream_t st);
 void launch_verify(const VerifyArgs &a, hipStream_t st);

@@ -133,7 +133,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       p->score_stride = ceil_div(max_len, 32) * 32;
       if (4.0 * (double)S * (double)H * (double)rows * (double)p->score_stride > kMaxWorkspace) return KEOPS_ERR_ALLOC;
       p->score_bytes = align256(4 * S * H * rows * p->score_stride);
-      if ((double)S * (double)H * (double)ceil_div(max_len, 256) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+      if ((double)S * (double)H * (double)(ceil_div(max_len, 256) + rows) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
     } else {
       const int64_t nst = ceil_div(max_len, kSumSlotsTile);
       if ((double)S * (double)H * (double)nst > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
@@ -283,13 +283,9 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   else launch_attend_many(a, type, e4m3, c->dim, dim3((unsigned)p.grid), st);
   prof_end(prof, st);
   if (!p.few && p.nsplit > 1) launch_attend_join(a, type, st);
-  if (c->weights && max_len > 0) {
-    if (p.scores) {
-      launch_attend_score_sums(a, st);
-    } else {
-      launch_attend_sums(a, type, e4m3, c->dim, dim3((unsigned)p.sums_grid), st);
-      if (p.nrow > 1) launch_attend_sums_join(a, st);
-    }
+  if (c->weights && max_len > 0 && !p.scores) {
+    launch_attend_sums(a, type, e4m3, c->dim, dim3((unsigned)p.sums_grid), st);
+    if (p.nrow > 1) launch_attend_sums_join(a, st);
   }
   return check_launch();
 }

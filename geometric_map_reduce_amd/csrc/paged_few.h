@@ -374,9 +374,10 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
         if (SCORES) {
           const int r = 16 * nr + col;
           if (r < R) {
-            float *row = a.scores + ((int64_t)(s * H + h) * a.score_rows + r) * a.score_stride + j0 + q4 * 4;
-            *(f32x4 *)row = (f32x4){z[0], z[1], z[2], z[3]};
-            *(f32x4 *)(row + 16) = (f32x4){z[4], z[5], z[6], z[7]};
+            // groups of four slots, a group's rows together: a tile's scores are one run of memory
+            float *at4 = a.scores + (((int64_t)(s * H + h) * (a.score_stride / 4) + (j0 >> 2) + q4) * a.score_rows + r) * 4;
+            *(f32x4 *)at4 = (f32x4){z[0], z[1], z[2], z[3]};
+            *(f32x4 *)(at4 + 16 * a.score_rows) = (f32x4){z[4], z[5], z[6], z[7]};
           }
         }
         if (__any(top > m_run[nr] + kLazy)) {
@@ -551,15 +552,101 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   }
 }
 
-// Joins the parts of a (sequence, head): blocks of `rows_per` rows; out = sum_k 2^(m_k - M) o_k /
-// sum_k 2^(m_k - M) l_k over the work-groups k of its run, under a running maximum M, in order within
-// each of the groups of dim / 4 threads, then the groups in order.
-constexpr int kFewJoinThreads = 256;
+// A part's place: a work-group's run starts a longer row of parts in its second one.
+__device__ __forceinline__ int64_t part_slot(int w, int w0, int rows) { return ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * rows; }
+
+// Weights from kept scores: a thread adds up the rows' 2^(score - lse) for four slots in a row.
+// 25 bytes a slot at four rows: the chain of loads before the sum costs more than they do, so a
+// work-group takes many slots.  lse comes from the parts, so that nothing waits for their join.
+constexpr int kScoreSlots = 1024;
+constexpr int kFinishThreads = 256;
+__device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int wgs, int part_rows, float *lse2) {
+  const int H = a.c.heads, G = a.group, tid = threadIdx.x;
+  const int blocks = (a.max_len + kScoreSlots - 1) / kScoreSlots;
+  const int sh = block / blocks, s = sh / H, h = sh - s * H;
+  const FewSpan span = few_span(a, s);
+  const SeqSpan &sp = span.sp;
+  const int j0 = (block - sh * blocks) * kScoreSlots, j = j0 + 4 * tid;
+  const int R = sp.m * G;
+  if (j0 >= sp.n) return;
+  // four slots share a page, and their weights 16 bytes, where the page size allows
+  const bool together = a.c.page.d % 4 == 0;
+  SlotPlace pl[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    pl[u] = SlotPlace{-1, 0};
+    if (j + u < sp.n && (u == 0 || !together)) pl[u] = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)(j + u));
+  }
+  int w0 = 0, w1 = 0;
+  if (!a.whole && R > 0) {
+    const FewShare f = few_share(a, wgs, 0, s);
+    const uint32_t from = f.base + (uint32_t)h * span.tiles, to = from + span.tiles;
+    w0 = (int)(from / f.share);
+    w1 = (int)((to - 1) / f.share);
+  }
+  if (tid < R) {
+    float l2;
+    if (w0 == w1) {
+      const int tok = (int)fast_div(a.gdiv, tid), g = tid - tok * G;
+      l2 = a.lse[(sp.t0 + tok) * ((int64_t)H * G) + h * G + g] * kLog2e;
+    } else {
+      float top = -INFINITY, l = 0.0f;
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w) {
+        const float2 x = a.part_ml[part_slot(w, w0, part_rows) + tid];
+        if (!(x.y > 0.0f || x.y != x.y)) continue;
+        const float m_new = fmaxf(top, x.x);
+        l = l * fast_exp2(top - m_new) + x.y * fast_exp2(x.x - m_new);
+        top = m_new;
+      }
+      l2 = l > 0.0f || l != l ? top + __log2f(l) : -INFINITY;
+    }
+    lse2[tid] = l2 == -INFINITY ? INFINITY : l2;       // a row that sees nothing gives 0
+  }
+  __syncthreads();
+  if (j >= sp.n) return;
+  const int lo = a.window > 0 && sp.first - a.window + 1 > 0 ? sp.first - a.window + 1 : 0;
+  f32x4 w = (f32x4){0, 0, 0, 0};
+  // scores exist from the tile of `lo` to the end of the tile of `hi`, both multiples of 4
+  if (j + 3 >= lo && j < span.hi) {
+    const float *z = a.scores + ((int64_t)sh * (a.score_stride / 4) + (j >> 2)) * a.score_rows * 4;
+#pragma unroll 4
+    for (int r = 0; r < R; ++r) {
+      const f32x4 x = *(const f32x4 *)(z + r * 4);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] += x[u] == -INFINITY ? 0.0f : fast_exp2(x[u] - lse2[r]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) w[u] = j + u >= lo && j + u < span.hi ? w[u] : 0.0f;
+  if (together && j + 3 < sp.n) {
+    if (pl[0].page < 0) return;
+    f32x4 *at = (f32x4 *)(a.c.weights + ((int64_t)pl[0].page * H + h) * a.c.page.d + pl[0].row);
+    if (a.decay != 0.0f) w += a.decay * *at;
+    *at = w;
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const SlotPlace p = together ? SlotPlace{pl[0].page, pl[0].row + u} : pl[u];
+    if (j + u >= sp.n || p.page < 0) continue;
+    float *at = a.c.weights + ((int64_t)p.page * H + h) * a.c.page.d + p.row;
+    *at = a.decay != 0.0f ? a.decay * *at + w[u] : w[u];
+  }
+}
+
+// The second pass of the few-rows form: work-groups below `joins` join the parts of a (sequence,
+// head), `rows_per` rows each; the others turn kept scores into weights.
+//   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k
+// over the work-groups k of the run, under a running maximum M, in order within each of the groups
+// of dim / 4 threads, then the groups in order.
 template <class T, int D, int NR>
-__global__ __launch_bounds__(kFewJoinThreads) void join_few_kernel(AttendArgs a, int wgs, int rows_per) {
-  constexpr int kLanes = D / 4, kGroups = kFewJoinThreads / kLanes;
-  __shared__ f32x4 part[kFewJoinThreads];
-  __shared__ float2 part_ml[kFewJoinThreads];
+__global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a, int wgs, int joins, int rows_per) {
+  constexpr int kLanes = D / 4, kGroups = kFinishThreads / kLanes;
+  __shared__ f32x4 part[kFinishThreads];
+  __shared__ float2 part_ml[kFinishThreads];
+  __shared__ float lse2[kFewRowsMax];
+  if ((int)blockIdx.x >= joins) return score_sums(a, blockIdx.x - joins, wgs, 16 * NR, lse2);
   const int H = a.c.heads, G = a.group, tid = threadIdx.x;
   const int64_t heads = (int64_t)H * G;
   const int blocks = (a.max_q * G + rows_per - 1) / rows_per;
@@ -571,7 +658,7 @@ __global__ __launch_bounds__(kFewJoinThreads) void join_few_kernel(AttendArgs a,
   const uint32_t from = f.base + (uint32_t)h * span.tiles, to = from + span.tiles;
   const int w0 = (int)(from / f.share), w1 = (int)((to - 1) / f.share);
   if (w0 == w1) return;        // one work-group had all of it
-  // every row by its own groups: rows_per rows at a time, or all groups on one
+  // a row by per_row groups of threads
   const int g = tid / kLanes, d4 = tid - g * kLanes;
   const int per_row = kGroups / rows_per, gr = g / per_row, gk = g - gr * per_row;
   const int r = (blockIdx.x - sh * blocks) * rows_per + gr;
@@ -588,7 +675,7 @@ __global__ __launch_bounds__(kFewJoinThreads) void join_few_kernel(AttendArgs a,
   if (mine) {
 #pragma unroll 4
     for (int w = w0 + gk; w <= w1; w += per_row) {
-      const int64_t at = ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * (16 * NR) + r;
+      const int64_t at = part_slot(w, w0, 16 * NR) + r;
       const float2 x = a.part_ml[at];
       const f32x4 o = *(const f32x4 *)(a.part_o + at * D + d4 * 4);
       add(x.x, x.y, o);
@@ -624,10 +711,11 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
     return n;
   }
   attend_few_kernel<T, E4M3, D, NR, SCORES><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
-  if (join_rows > 0) {
-    const int64_t rows = ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows;
-    join_few_kernel<T, D, NR><<<dim3((unsigned)(rows * a.c.seqs * a.c.heads)), kFewJoinThreads, 0, st>>>(a, grid, join_rows);
-  }
+  const int64_t sh = (int64_t)a.c.seqs * a.c.heads;
+  const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh : 0;
+  const int64_t sums = SCORES ? (a.max_len + kScoreSlots - 1) / kScoreSlots * sh : 0;
+  if (joins + sums > 0)
+    finish_few_kernel<T, D, NR><<<dim3((unsigned)(joins + sums)), kFinishThreads, 0, st>>>(a, grid, (int)joins, join_rows);
   return 0;
 }
 template <class T, bool E4M3, int D>

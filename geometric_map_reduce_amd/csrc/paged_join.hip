@@ -1,5 +1,5 @@
-// paged_join.hip -- second passes of the paged attention: joining the slot splits, and turning
-// kept scores or partial column sums into the slots' attention weights.
+// paged_join.hip -- the paged attention's launches, and the second passes of its many-rows form:
+// joining the slot splits, and partial column sums into the slots' attention weights.
 #include "paged.h"
 
 namespace kmi {
@@ -67,50 +67,6 @@ __device__ __forceinline__ void put_weight(const AttendArgs &a, SlotPlace p, int
   *at = a.decay != 0.0f ? a.decay * *at + w : w;
 }
 
-// Weights of the few-rows form: a thread adds up its rows' 2^(score - lse) for four slots in a row.
-// 25 bytes a slot at four rows: the chain of loads before the sum costs more than they do, so a
-// work-group takes many slots.
-constexpr int kScoreSlots = 1024;
-__global__ __launch_bounds__(256) void score_sums_kernel(AttendArgs a) {
-  __shared__ float lse2[kFewRowsMax];
-  const int H = a.c.heads, G = a.group;
-  const int blocks = (a.max_len + kScoreSlots - 1) / kScoreSlots;
-  const int sh = blockIdx.x / blocks, s = sh / H, h = sh - s * H;
-  const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
-  const int j0 = (blockIdx.x - sh * blocks) * kScoreSlots, j = j0 + 4 * threadIdx.x;
-  const int R = sp.m * G;
-  if (j0 >= sp.n) return;
-  SlotPlace pl[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    pl[u] = SlotPlace{-1, 0};
-    if (j + u < sp.n) pl[u] = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)(j + u));
-  }
-  if (threadIdx.x < R) {
-    const int tok = (int)fast_div(a.gdiv, threadIdx.x), g = threadIdx.x - tok * G;
-    const float l = a.lse[(sp.t0 + tok) * ((int64_t)H * G) + h * G + g] * kLog2e;
-    lse2[threadIdx.x] = l == -INFINITY ? INFINITY : l;
-  }
-  __syncthreads();
-  if (j >= sp.n) return;
-  const int lo = a.window > 0 && sp.first - a.window + 1 > 0 ? sp.first - a.window + 1 : 0;
-  const int end = sp.n < sp.first + sp.m ? sp.n : sp.first + sp.m;
-  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  // scores exist from the tile of `lo` to the end of the tile of `end`, both multiples of 4
-  if (j + 3 >= lo && j < end) {
-    const float *z = a.scores + (int64_t)sh * a.score_rows * a.score_stride + j;
-#pragma unroll 4
-    for (int r = 0; r < R; ++r) {
-      const f32x4 x = *(const f32x4 *)(z + r * a.score_stride);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] += x[u] == -INFINITY ? 0.0f : fast_exp2(x[u] - lse2[r]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (j + u < sp.n) put_weight(a, pl[u], h, j + u >= lo && j + u < end ? w[u] : 0.0f);
-}
-
 // Weights of the many-rows form from its row splits, in order.
 __global__ __launch_bounds__(256) void sums_join_kernel(AttendArgs a) {
   const int H = a.c.heads;
@@ -146,11 +102,6 @@ void launch_attend_join(const AttendArgs &a, int type, hipStream_t st) {
   const dim3 grid((unsigned)(a.tokens * a.c.heads * a.group));
   if (type == CT_BF16) join_kernel<Bf16><<<grid, kJoinThreads, 0, st>>>(a);
   else join_kernel<F16><<<grid, kJoinThreads, 0, st>>>(a);
-}
-
-void launch_attend_score_sums(const AttendArgs &a, hipStream_t st) {
-  const int64_t blocks = (a.max_len + kScoreSlots - 1) / kScoreSlots;
-  score_sums_kernel<<<dim3((unsigned)(blocks * a.c.seqs * a.c.heads)), 256, 0, st>>>(a);
 }
 
 void launch_attend_sums_join(const AttendArgs &a, hipStream_t st) {
