@@ -88,8 +88,8 @@ struct AttendPlan {
   bool few, scores, whole;
   int row_tiles, score_rows, join_rows;
   int64_t nsplit, nrow, grid, sums_grid, score_stride;
-  int64_t ml_bytes, o_bytes, score_bytes, sums_bytes;
-  int64_t total() const { return ml_bytes + o_bytes + score_bytes + sums_bytes; }
+  int64_t line_bytes, ml_bytes, o_bytes, score_bytes, sums_bytes;
+  int64_t total() const { return line_bytes + ml_bytes + o_bytes + score_bytes + sums_bytes; }
 };
 
 int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int64_t max_q, int64_t max_len, int window, int cus,
@@ -115,7 +115,10 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     p->whole = from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
     p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
     if (!p->whole) {
-      p->join_rows = S * H * rows >= 2048 ? std::min<int64_t>(rows, 1024 / c.dim) : 1;
+      // a joining work-group's 1024 / dim groups of threads: one to a row where the parts are few
+      const int64_t groups = 1024 / c.dim, parts = ceil_div(p->grid, S * H) + 1;
+      p->join_rows = (int)std::max<int64_t>(1, std::min(rows, parts <= 4 ? groups : groups / parts));
+      p->line_bytes = align256((S + 1) * 4);
       p->ml_bytes = align256(p->grid * 2 * 16 * p->row_tiles * 8);
       p->o_bytes = align256(p->grid * 2 * 16 * p->row_tiles * c.dim * 4);
     }
@@ -270,6 +273,8 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.lse = lse;
   a.nsplit = (int32_t)p.nsplit;
   a.whole = p.whole;
+  a.line = (uint32_t *)ws;
+  ws += p.line_bytes;
   a.part_ml = (float2 *)ws;
   a.part_o = (float *)(ws + p.ml_bytes);
   a.scores = p.scores ? (float *)(ws + p.ml_bytes + p.o_bytes) : nullptr;

@@ -34,6 +34,7 @@ constexpr int kFewWaves = 4;
 constexpr int kFewThreads = kFewWaves * kWave;
 constexpr int kFewTile = 32;       // slots of a wave's tile
 constexpr int kFewBlock = 1024;    // slots whose addresses are held in LDS at a time
+constexpr int kScoreHeld = 8192;   // scores held in LDS for 16 rows
 constexpr float kLazy = 8.0f;      // log2 of what a score may pass the running maximum by
 
 // V columns of a lane: pieces of W consecutive columns, column base + (l % 16) W + t.
@@ -189,26 +190,29 @@ struct FewShare {
   int s;                     // the sequence that holds tile `at` of the line (seqs: past the end)
   uint32_t base;             // the first of its tiles
 };
-__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int wg, int want_s) {
+__device__ __forceinline__ uint32_t few_total(const AttendArgs &a) {
   const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
-  const uint32_t H = (uint32_t)a.c.heads;
   uint32_t total = 0;
   for (int s0 = 0; s0 < S; s0 += kWave) {
-    const uint32_t own = s0 + lane < S ? (uint32_t)few_span(a, s0 + lane).tiles * H : 0u;
+    const uint32_t own = s0 + lane < S ? (uint32_t)(few_span(a, s0 + lane).tiles * a.c.heads) : 0u;
     total += __shfl(wave_scan_u32(own), kWave - 1);
   }
-  FewShare r;
-  r.share = (total + wgs - 1) / wgs;
-  r.share = (r.share + kFewWaves - 1) / kFewWaves * kFewWaves;      // a tile for every wave
+  return total;
+}
+__device__ __forceinline__ uint32_t share_of(uint32_t total, int wgs) {
+  const uint32_t share = (total + wgs - 1) / wgs;
+  return (share + kFewWaves - 1) / kFewWaves * kFewWaves;      // a tile for every wave
+}
+__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int wg) {
+  const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
+  const uint32_t total = few_total(a);
+  FewShare r{share_of(total, wgs), S, total};
   const uint32_t at = (uint32_t)wg * r.share;
-  r.s = S;
-  r.base = total;
   uint32_t before = 0;
   for (int s0 = 0; s0 < S; s0 += kWave) {
-    const uint32_t own = s0 + lane < S ? (uint32_t)few_span(a, s0 + lane).tiles * H : 0u;
+    const uint32_t own = s0 + lane < S ? (uint32_t)(few_span(a, s0 + lane).tiles * a.c.heads) : 0u;
     const uint32_t upto = before + wave_scan_u32(own);
-    const bool here = want_s >= 0 ? s0 + lane == want_s : (at >= upto - own && at < upto);
-    const uint64_t who = __ballot(here);
+    const uint64_t who = __ballot(at >= upto - own && at < upto);
     if (who) {
       const int l = __ffsll((unsigned long long)who) - 1;
       r.s = s0 + l;
@@ -221,6 +225,25 @@ __device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int 
   r.base = __builtin_amdgcn_readfirstlane(r.base);
   r.share = __builtin_amdgcn_readfirstlane(r.share);
   return r;
+}
+// The same for the second pass, written down by one wave: where each sequence's tiles begin, and
+// after them the share.
+__device__ __forceinline__ void write_line(const AttendArgs &a, int wgs) {
+  const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
+  uint32_t before = 0;
+  for (int s0 = 0; s0 < S; s0 += kWave) {
+    const uint32_t own = s0 + lane < S ? (uint32_t)(few_span(a, s0 + lane).tiles * a.c.heads) : 0u;
+    const uint32_t upto = before + wave_scan_u32(own);
+    if (s0 + lane < S) a.line[s0 + lane] = upto - own;
+    before = __shfl(upto, kWave - 1);
+  }
+  if (lane == 0) a.line[S] = share_of(before, wgs);
+}
+// The work-groups [w0, w1] that share a (sequence, head).
+__device__ __forceinline__ void part_range(const AttendArgs &a, int s, int h, int tiles, int *w0, int *w1) {
+  const uint32_t share = a.line[a.c.seqs], from = a.line[s] + (uint32_t)(h * tiles), to = from + tiles;
+  *w0 = (int)(from / share);
+  *w1 = (int)((to - 1) / share);
 }
 
 template <class T, bool E4M3, int D, int NR, bool SCORES>
@@ -235,6 +258,11 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   __shared__ float sh_m[2][kRows], sh_l[2][kRows];
   __shared__ uint32_t present[kFewBlock / kFewTile];     // a tile's slots that are there, as bits
   __shared__ int sh_odd;
+  // Kept scores of a block of slots, written out together: a store among the loads of every tile
+  // would be waited for with them (22 us of 150 for a step of 32 conversations).
+  __shared__ __align__(16) float scores[SCORES ? kScoreHeld * NR : 4];
+  const int block = SCORES && a.score_rows * kFewBlock > kScoreHeld * NR
+                        ? kScoreHeld * NR / a.score_rows / (kFewTile * kFewWaves) * (kFewTile * kFewWaves) : kFewBlock;
 
   const int H = a.c.heads, G = a.group;
   const int64_t heads = (int64_t)H * G;
@@ -244,13 +272,14 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   // this work-group's run of tiles: from tile t0 of (s, h) on
   int s, h, t0;
   uint32_t left;
+  if (!a.whole && blockIdx.x == 0 && wave == 0) write_line(a, gridDim.x);
   if (a.whole) {
     s = blockIdx.x / H;
     h = blockIdx.x - s * H;
     t0 = 0;
     left = 0xffffffffu;
   } else {
-    const FewShare my = few_share(a, gridDim.x, blockIdx.x, -1);
+    const FewShare my = few_share(a, gridDim.x, blockIdx.x);
     if (my.s >= a.c.seqs) return;
     s = my.s;
     left = my.share;
@@ -308,10 +337,16 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   F f;
   bool odd = false;
   if (tid == 0) sh_odd = 0;
-  for (int blk = c0; blk < c1; blk += kFewBlock) {
-    const int cnt = c1 - blk < kFewBlock ? c1 - blk : kFewBlock;
+  // slots [from, from + cnt) from LDS: whole groups of four, as they lie in memory
+  const auto flush = [&](int from, int cnt) {
+    f32x4 *to = (f32x4 *)(a.scores + ((int64_t)(s * H + h) * (a.score_stride / 4) + (from >> 2)) * a.score_rows * 4);
+    for (int i = tid; i < (cnt + 3) / 4 * a.score_rows; i += kFewThreads) to[i] = ((const f32x4 *)scores)[i];
+  };
+  for (int blk = c0; blk < c1; blk += block) {
+    const int cnt = c1 - blk < block ? c1 - blk : block;
     const int ntile = (cnt + kFewTile - 1) / kFewTile;
     __syncthreads();
+    if (SCORES && blk > c0) flush(blk - block, block);
     for (int i = tid; i < kFewBlock; i += kFewThreads) {
       const int64_t o = i < cnt ? place_offset(a.c, slot_place(a.c, trow, (uint32_t)(blk + i))) : -1;
       sh.off[i] = o;
@@ -374,8 +409,8 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
         if (SCORES) {
           const int r = 16 * nr + col;
           if (r < R) {
-            // groups of four slots, a group's rows together: a tile's scores are one run of memory
-            float *at4 = a.scores + (((int64_t)(s * H + h) * (a.score_stride / 4) + (j0 >> 2) + q4) * a.score_rows + r) * 4;
+            // groups of four slots, a group's rows together
+            float *at4 = scores + (((at >> 2) + q4) * a.score_rows + r) * 4;
             *(f32x4 *)at4 = (f32x4){z[0], z[1], z[2], z[3]};
             *(f32x4 *)(at4 + 16 * a.score_rows) = (f32x4){z[4], z[5], z[6], z[7]};
           }
@@ -434,6 +469,7 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   }
 
   __syncthreads();
+  if (SCORES && c1 > c0) flush(c0 + (c1 - c0 - 1) / block * block, (c1 - c0 - 1) % block + 1);
   if (odd) sh_odd = 1;
   // the four waves' sums: 2 and 3 hand theirs to 0 and 1, then 1 to 0
 #pragma unroll
@@ -558,32 +594,43 @@ __device__ __forceinline__ int64_t part_slot(int w, int w0, int rows) { return (
 // Weights from kept scores: a thread adds up the rows' 2^(score - lse) for four slots in a row.
 // 25 bytes a slot at four rows: the chain of loads before the sum costs more than they do, so a
 // work-group takes many slots.  lse comes from the parts, so that nothing waits for their join.
-constexpr int kScoreSlots = 1024;
 constexpr int kFinishThreads = 256;
-__device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int wgs, int part_rows, float *lse2) {
+constexpr int kScoreGroups = 2, kScoreAhead = 4;      // groups of a thread; rows loaded before lse is known
+constexpr int kScoreSlots = 4 * kScoreGroups * kFinishThreads;
+__device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int part_rows, float *lse2) {
   const int H = a.c.heads, G = a.group, tid = threadIdx.x;
   const int blocks = (a.max_len + kScoreSlots - 1) / kScoreSlots;
   const int sh = block / blocks, s = sh / H, h = sh - s * H;
   const FewSpan span = few_span(a, s);
   const SeqSpan &sp = span.sp;
-  const int j0 = (block - sh * blocks) * kScoreSlots, j = j0 + 4 * tid;
+  const int j0 = (block - sh * blocks) * kScoreSlots;
   const int R = sp.m * G;
   if (j0 >= sp.n) return;
   // four slots share a page, and their weights 16 bytes, where the page size allows
   const bool together = a.c.page.d % 4 == 0;
-  SlotPlace pl[4];
+  const int lo = a.window > 0 && sp.first - a.window + 1 > 0 ? sp.first - a.window + 1 : 0;
+  const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
+  SlotPlace pl[kScoreGroups][4];
+  f32x4 ahead[kScoreGroups][kScoreAhead];
+  const float *z[kScoreGroups];
+  bool seen[kScoreGroups];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    pl[u] = SlotPlace{-1, 0};
-    if (j + u < sp.n && (u == 0 || !together)) pl[u] = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)(j + u));
+  for (int g = 0; g < kScoreGroups; ++g) {
+    const int j = j0 + 4 * (g * kFinishThreads + tid);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      pl[g][u] = SlotPlace{-1, 0};
+      if (j + u < sp.n && (u == 0 || !together)) pl[g][u] = slot_place(a.c, trow, (uint32_t)(j + u));
+    }
+    // scores exist from the tile of `lo` to the group of four of `hi`
+    seen[g] = j + 3 >= lo && j < span.hi;
+    z[g] = a.scores + ((int64_t)sh * (a.score_stride / 4) + (j >> 2)) * a.score_rows * 4;
+#pragma unroll
+    for (int r = 0; r < kScoreAhead; ++r)
+      ahead[g][r] = seen[g] && r < R ? *(const f32x4 *)(z[g] + r * 4) : (f32x4){0, 0, 0, 0};
   }
   int w0 = 0, w1 = 0;
-  if (!a.whole && R > 0) {
-    const FewShare f = few_share(a, wgs, 0, s);
-    const uint32_t from = f.base + (uint32_t)h * span.tiles, to = from + span.tiles;
-    w0 = (int)(from / f.share);
-    w1 = (int)((to - 1) / f.share);
-  }
+  if (!a.whole && R > 0) part_range(a, s, h, span.tiles, &w0, &w1);
   if (tid < R) {
     float l2;
     if (w0 == w1) {
@@ -604,34 +651,38 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int w
     lse2[tid] = l2 == -INFINITY ? INFINITY : l2;       // a row that sees nothing gives 0
   }
   __syncthreads();
-  if (j >= sp.n) return;
-  const int lo = a.window > 0 && sp.first - a.window + 1 > 0 ? sp.first - a.window + 1 : 0;
-  f32x4 w = (f32x4){0, 0, 0, 0};
-  // scores exist from the tile of `lo` to the end of the tile of `hi`, both multiples of 4
-  if (j + 3 >= lo && j < span.hi) {
-    const float *z = a.scores + ((int64_t)sh * (a.score_stride / 4) + (j >> 2)) * a.score_rows * 4;
+#pragma unroll
+  for (int g = 0; g < kScoreGroups; ++g) {
+    const int j = j0 + 4 * (g * kFinishThreads + tid);
+    if (j >= sp.n) break;
+    f32x4 w = (f32x4){0, 0, 0, 0};
+    const auto add = [&](f32x4 x, float l) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] += x[u] == -INFINITY ? 0.0f : fast_exp2(x[u] - l);
+    };
+    if (seen[g]) {
+#pragma unroll
+      for (int r = 0; r < kScoreAhead; ++r)
+        if (r < R) add(ahead[g][r], lse2[r]);
 #pragma unroll 4
-    for (int r = 0; r < R; ++r) {
-      const f32x4 x = *(const f32x4 *)(z + r * 4);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] += x[u] == -INFINITY ? 0.0f : fast_exp2(x[u] - lse2[r]);
+      for (int r = kScoreAhead; r < R; ++r) add(*(const f32x4 *)(z[g] + r * 4), lse2[r]);
     }
-  }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) w[u] = j + u >= lo && j + u < span.hi ? w[u] : 0.0f;
-  if (together && j + 3 < sp.n) {
-    if (pl[0].page < 0) return;
-    f32x4 *at = (f32x4 *)(a.c.weights + ((int64_t)pl[0].page * H + h) * a.c.page.d + pl[0].row);
-    if (a.decay != 0.0f) w += a.decay * *at;
-    *at = w;
-    return;
-  }
+    for (int u = 0; u < 4; ++u) w[u] = j + u >= lo && j + u < span.hi ? w[u] : 0.0f;
+    if (together && j + 3 < sp.n) {
+      if (pl[g][0].page < 0) continue;
+      f32x4 *at = (f32x4 *)(a.c.weights + ((int64_t)pl[g][0].page * H + h) * a.c.page.d + pl[g][0].row);
+      if (a.decay != 0.0f) w += a.decay * *at;
+      *at = w;
+      continue;
+    }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const SlotPlace p = together ? SlotPlace{pl[0].page, pl[0].row + u} : pl[u];
-    if (j + u >= sp.n || p.page < 0) continue;
-    float *at = a.c.weights + ((int64_t)p.page * H + h) * a.c.page.d + p.row;
-    *at = a.decay != 0.0f ? a.decay * *at + w[u] : w[u];
+    for (int u = 0; u < 4; ++u) {
+      const SlotPlace p = together ? SlotPlace{pl[g][0].page, pl[g][0].row + u} : pl[g][u];
+      if (j + u >= sp.n || p.page < 0) continue;
+      float *at = a.c.weights + ((int64_t)p.page * H + h) * a.c.page.d + p.row;
+      *at = a.decay != 0.0f ? a.decay * *at + w[u] : w[u];
+    }
   }
 }
 
@@ -641,22 +692,21 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int w
 // over the work-groups k of the run, under a running maximum M, in order within each of the groups
 // of dim / 4 threads, then the groups in order.
 template <class T, int D, int NR>
-__global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a, int wgs, int joins, int rows_per) {
+__global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a, int joins, int rows_per) {
   constexpr int kLanes = D / 4, kGroups = kFinishThreads / kLanes;
   __shared__ f32x4 part[kFinishThreads];
   __shared__ float2 part_ml[kFinishThreads];
   __shared__ float lse2[kFewRowsMax];
-  if ((int)blockIdx.x >= joins) return score_sums(a, blockIdx.x - joins, wgs, 16 * NR, lse2);
+  if ((int)blockIdx.x >= joins) return score_sums(a, blockIdx.x - joins, 16 * NR, lse2);
   const int H = a.c.heads, G = a.group, tid = threadIdx.x;
   const int64_t heads = (int64_t)H * G;
   const int blocks = (a.max_q * G + rows_per - 1) / rows_per;
   const int sh = blockIdx.x / blocks, s = sh / H, h = sh - s * H;
-  const FewShare f = few_share(a, wgs, 0, s);
   const FewSpan span = few_span(a, s);
   const int R = span.sp.m * G;
   if (R == 0) return;
-  const uint32_t from = f.base + (uint32_t)h * span.tiles, to = from + span.tiles;
-  const int w0 = (int)(from / f.share), w1 = (int)((to - 1) / f.share);
+  int w0, w1;
+  part_range(a, s, h, span.tiles, &w0, &w1);
   if (w0 == w1) return;        // one work-group had all of it
   // a row by per_row groups of threads
   const int g = tid / kLanes, d4 = tid - g * kLanes;
@@ -715,7 +765,7 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
   const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh : 0;
   const int64_t sums = SCORES ? (a.max_len + kScoreSlots - 1) / kScoreSlots * sh : 0;
   if (joins + sums > 0)
-    finish_few_kernel<T, D, NR><<<dim3((unsigned)(joins + sums)), kFinishThreads, 0, st>>>(a, grid, (int)joins, join_rows);
+    finish_few_kernel<T, D, NR><<<dim3((unsigned)(joins + sums)), kFinishThreads, 0, st>>>(a, (int)joins, join_rows);
   return 0;
 }
 template <class T, bool E4M3, int D>
