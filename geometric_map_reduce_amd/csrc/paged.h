@@ -102,7 +102,7 @@ struct AttendArgs {
   // parts of a row's sums: many rows [nsplit][tokens][heads * group], few rows [work-groups][2][rows]
   int32_t nsplit;
   uint32_t *line;               // few rows: where each sequence's tiles begin, and a work-group's share [seqs + 1]
-  int32_t whole;                // few rows: a work-group has all slots of one (sequence, head)
+  int32_t whole;                // few rows: a work-group has all slots of one (sequence, head); 2: of eight waves
   float *part_o;                // [..][dim], sums under the part's maximum
   float2 *part_ml;              // (maximum in log2 units, sum)
   // few-rows form with weights: scores [seqs * heads][score_stride / 4][rows][4] in log2 units

@@ -23,6 +23,10 @@ constexpr int64_t kSumsWgsPerCu = 4;
 // sequences that are left whole when there are enough of them to fill the device.
 constexpr int kFewLeast = 128;
 constexpr int kFewWhole = 1024;
+// Up to here work-groups of eight waves that have a head's slots to themselves beat splitting them and
+// a second pass: 15.6 to 19 us a call at 300 and 600 slots, 18.2 to 18.5 at 1,000, 28.5 to 20.6 at 2,000
+// (one compute unit reads at most some 50 bytes a nanosecond).
+constexpr int kFewWhole8 = 768;
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -85,8 +89,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Launch plan of one attention call.
 struct AttendPlan {
-  bool few, scores, whole;
-  int row_tiles, score_rows, join_rows;
+  bool few, scores;
+  int whole, row_tiles, score_rows, join_rows;
   int64_t nsplit, nrow, grid, sums_grid, score_stride;
   int64_t line_bytes, ml_bytes, o_bytes, score_bytes, sums_bytes;
   int64_t total() const { return line_bytes + ml_bytes + o_bytes + score_bytes + sums_bytes; }
@@ -113,6 +117,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     if (fit < 1) return KEOPS_ERR_HIP;
     const int64_t room = (int64_t)fit * cus;
     p->whole = from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
+    if (!p->whole && from_tile <= kFewWhole8 && S * H <= cus && p->row_tiles == 1 && c.dim <= 128) p->whole = 2;
     p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
     if (!p->whole) {
       // a joining work-group's 1024 / dim groups of threads: one to a row where the parts are few

@@ -246,23 +246,25 @@ __device__ __forceinline__ void part_range(const AttendArgs &a, int s, int h, in
   *w1 = (int)((to - 1) / share);
 }
 
-template <class T, bool E4M3, int D, int NR, bool SCORES>
-__global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
+// NW waves: 4, or 8 where one work-group has a short sequence's head to itself and nothing else
+// would hide its latency.
+template <class T, bool E4M3, int D, int NR, bool SCORES, int NW>
+__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, E4M3, D, NR>;
   constexpr int kRows = 16 * NR;
-  constexpr int kHalfRows = 2 * kRows;     // two waves' rows
+  constexpr int kHalfRows = NW / 2 * kRows;     // half the waves' rows
   __shared__ union {
     int64_t off[kFewBlock + kFewTile];
     float o[kHalfRows * F::kPad];
   } sh;
-  __shared__ float sh_m[2][kRows], sh_l[2][kRows];
+  __shared__ float sh_m[NW / 2][kRows], sh_l[NW / 2][kRows];
   __shared__ uint32_t present[kFewBlock / kFewTile];     // a tile's slots that are there, as bits
   __shared__ int sh_odd;
   // Kept scores of a block of slots, written out together: a store among the loads of every tile
   // would be waited for with them (22 us of 150 for a step of 32 conversations).
   __shared__ __align__(16) float scores[SCORES ? kScoreHeld * NR : 4];
   const int block = SCORES && a.score_rows * kFewBlock > kScoreHeld * NR
-                        ? kScoreHeld * NR / a.score_rows / (kFewTile * kFewWaves) * (kFewTile * kFewWaves) : kFewBlock;
+                        ? kScoreHeld * NR / a.score_rows / (kFewTile * NW) * (kFewTile * NW) : kFewBlock;
 
   const int H = a.c.heads, G = a.group;
   const int64_t heads = (int64_t)H * G;
@@ -340,14 +342,14 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   // slots [from, from + cnt) from LDS: whole groups of four, as they lie in memory
   const auto flush = [&](int from, int cnt) {
     f32x4 *to = (f32x4 *)(a.scores + ((int64_t)(s * H + h) * (a.score_stride / 4) + (from >> 2)) * a.score_rows * 4);
-    for (int i = tid; i < (cnt + 3) / 4 * a.score_rows; i += kFewThreads) to[i] = ((const f32x4 *)scores)[i];
+    for (int i = tid; i < (cnt + 3) / 4 * a.score_rows; i += (NW * kWave)) to[i] = ((const f32x4 *)scores)[i];
   };
   for (int blk = c0; blk < c1; blk += block) {
     const int cnt = c1 - blk < block ? c1 - blk : block;
     const int ntile = (cnt + kFewTile - 1) / kFewTile;
     __syncthreads();
     if (SCORES && blk > c0) flush(blk - block, block);
-    for (int i = tid; i < kFewBlock; i += kFewThreads) {
+    for (int i = tid; i < kFewBlock; i += (NW * kWave)) {
       const int64_t o = i < cnt ? place_offset(a.c, slot_place(a.c, trow, (uint32_t)(blk + i))) : -1;
       sh.off[i] = o;
       const uint64_t there = __ballot(o >= 0);
@@ -364,10 +366,10 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
     __builtin_amdgcn_sched_barrier(0);
     f.load_v(vbase, sh.off, begin);
     __builtin_amdgcn_sched_barrier(0);
-    for (; tile < ntile; tile += kFewWaves) {
+    for (; tile < ntile; tile += NW) {
       const int at = tile * kFewTile, j0 = blk + at;
       // after the last tile one row, again and again: loads without a condition let K be waited for alone
-      const int next = tile + kFewWaves < ntile ? (tile + kFewWaves) * kFewTile : kFewBlock;
+      const int next = tile + NW < ntile ? (tile + NW) * kFewTile : kFewBlock;
       f32x4 sc[NR][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -471,11 +473,11 @@ __global__ __launch_bounds__(kFewThreads, (D * NR > 128 ? 1 : (E4M3 && NR == 1 ?
   __syncthreads();
   if (SCORES && c1 > c0) flush(c0 + (c1 - c0 - 1) / block * block, (c1 - c0 - 1) % block + 1);
   if (odd) sh_odd = 1;
-  // the four waves' sums: 2 and 3 hand theirs to 0 and 1, then 1 to 0
+  // the waves' sums: the upper half hands its to the lower, and again
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) l_run[nr] = xor_sum(l_run[nr]);
 #pragma unroll
-  for (int step = 2; step >= 1; step >>= 1) {
+  for (int step = NW / 2; step >= 1; step >>= 1) {
     __syncthreads();
     if (wave >= step && wave < 2 * step) {
       const int w = wave - step;
@@ -723,12 +725,20 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
     top = m_new;
   };
   if (mine) {
-#pragma unroll 4
-    for (int w = w0 + gk; w <= w1; w += per_row) {
-      const int64_t at = part_slot(w, w0, 16 * NR) + r;
-      const float2 x = a.part_ml[at];
-      const f32x4 o = *(const f32x4 *)(a.part_o + at * D + d4 * 4);
-      add(x.x, x.y, o);
+    // eight parts are loaded before the first is added
+    for (int w = w0 + gk; w <= w1; w += 8 * per_row) {
+      float2 x[8];
+      f32x4 o[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int v = w + u * per_row <= w1 ? w + u * per_row : w1;
+        const int64_t at = part_slot(v, w0, 16 * NR) + r;
+        x[u] = a.part_ml[at];
+        o[u] = *(const f32x4 *)(a.part_o + at * D + d4 * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (w + u * per_row <= w1) add(x[u].x, x[u].y, o[u]);
     }
   }
   part[tid] = acc;
@@ -753,14 +763,18 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
     static std::atomic<int> fit{0};
     int n = fit.load(std::memory_order_relaxed);
     if (n <= 0) {
-      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, E4M3, D, NR, SCORES>, kFewThreads,
-                                                       0) != hipSuccess || n < 1)
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves>,
+                                                       kFewThreads, 0) != hipSuccess || n < 1)
         return -1;
       fit.store(n, std::memory_order_relaxed);
     }
     return n;
   }
-  attend_few_kernel<T, E4M3, D, NR, SCORES><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
+  if constexpr (NR == 1 && D <= 128) {
+    if (a.whole == 2) attend_few_kernel<T, E4M3, D, NR, SCORES, 8><<<dim3((unsigned)grid), 8 * kWave, 0, st>>>(a);
+  }
+  if (!(NR == 1 && D <= 128 && a.whole == 2))
+    attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
   const int64_t sh = (int64_t)a.c.seqs * a.c.heads;
   const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh : 0;
   const int64_t sums = SCORES ? (a.max_len + kScoreSlots - 1) / kScoreSlots * sh : 0;
