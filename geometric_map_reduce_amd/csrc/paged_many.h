@@ -29,20 +29,20 @@ constexpr float kManyLazy = 8.0f;   // log2 of what a score may pass the running
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Piece (16 bytes) p of row r of a tile with D 16-bit columns lies at piece p ^ x(r).
+// Piece (16 bytes) p of row r of a tile with D 16-bit columns lies at piece p ^ x(r).  A read of a wave
+// goes in parts of 256 bytes over 64 banks: 16 rows' pieces of K (rows 0-3, 12-15, 20-23, 24-27 and so
+// on), 4 rows' quadruples of V.  With these x no two of a part share a bank (counted: none; with a
+// rotation by 8 pieces instead of 16 half of the LDS cycles at D = 128 were conflicts).
 template <int D>
-__device__ __forceinline__ int k_swizzle(int r) { return D == 96 ? (r >> 1) & 3 : r & 7; }
+__device__ __forceinline__ int k_swizzle(int r) { return D == 96 ? (r >> 2) & 3 : (D == 64 ? (r >> 1) & 7 : r & 15); }
 template <int D>
-__device__ __forceinline__ int v_swizzle(int r) { return D == 96 ? 2 * ((r >> 1) & 1) : 2 * (r & 3); }
+__device__ __forceinline__ int v_swizzle(int r) { return D == 96 ? 0 : (D == 64 ? 2 * (r & 3) : 4 * (r & 3)); }
 
 __device__ __forceinline__ float half_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
 __device__ __forceinline__ float half_sum(float v) { return v + __shfl_xor(v, 32); }
 
 // Slot of accumulator register r in a 32-slot tile for a lane of half hi.
 __device__ __forceinline__ constexpr int slot32(int r, int hi) { return hi * 4 + (r & 3) + 8 * (r >> 2); }
-
-// Zeros that stand in for the rows of absent slots.
-static __device__ const uint32_t kZeroRow[128] = {};
 
 // 16 bytes a lane from global memory to LDS, lane l's at lds + 16 l, without passing registers.
 // Done when vmcnt says so: the compiler does not know, dma_wait() does.  (M0 needs one wait state.)
@@ -147,7 +147,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     for (int i = 0; i < kPlace; ++i) {
       const int at = i * kManyThreads + tid, j = lo + chunk * kChunk * KT + at;
       const uint32_t row = (uint32_t)j - fast_div(a.c.page, (uint32_t)j) * a.c.page.d;
-      off[chunk & 1][at] = place_offset(a.c, SlotPlace{page[i], row});
+      const int64_t o = place_offset(a.c, SlotPlace{page[i], row});
+      off[chunk & 1][at] = E4M3 || o >= 0 ? o : 0;
       const uint64_t there = __ballot(page[i] >= 0);
       if (lane == 0) present[chunk & 1][i * 4 + wave] = there;
     }
@@ -178,15 +179,16 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
         gv[i][0] = y.x; gv[i][1] = y.y;
       }
     } else {
+      // an absent slot's row is some row of the pool: no row sees its K, and its V is cleared before use
       const uint32_t ldk = lds_address(sk[tile % kBufs]) + wave * 1024, ldv = lds_address(sv[tile % kBufs]) + wave * 1024;
+      int64_t o[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) o[i] = po[(tid + i * kManyThreads) / kPieces];
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
-        const int64_t o = po[row];
-        const char *fk = o < 0 ? (const char *)kZeroRow : kbase + o;
-        const char *fv = o < 0 ? (const char *)kZeroRow : vbase + o;
-        dma16(fk + (p ^ k_swizzle<D>(row)) * 16, ldk + i * (kManyThreads * 16));
-        dma16(fv + (p ^ v_swizzle<D>(row)) * 16, ldv + i * (kManyThreads * 16));
+        dma16(kbase + (p ^ k_swizzle<D>(row)) * 16 + o[i], ldk + i * (kManyThreads * 16));
+        dma16(vbase + (p ^ v_swizzle<D>(row)) * 16 + o[i], ldv + i * (kManyThreads * 16));
       }
     }
   };
@@ -264,10 +266,14 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     l_run += sum;
 
     if (masked) {
-      // non-finite values of slots that some rows see and others do not wait for the end; each
-      // wave clears them for itself before it reads the tile
+      // V of absent slots is cleared, and non-finite values of slots that some rows see and others do
+      // not wait for the end; each wave clears for itself before it reads the tile
       for (int i = lane; i < KT * kPieces; i += 64) {
-        const int j = j0 + i / kPieces;
+        const int u = i / kPieces, j = j0 + u;
+        if (!((there >> u) & 1u)) {
+          ((u32x4 *)sv[buf])[i] = (u32x4){0, 0, 0, 0};
+          continue;
+        }
         if (!(j > first_pos || (a.window > 0 && j <= last_pos - a.window))) continue;
         u32x4 x = ((const u32x4 *)sv[buf])[i];
         if (clear_nonfinite<T>(x)) {
