@@ -131,8 +131,9 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     const int64_t nrt = ceil_div(rows, kManyRowsTile);
     if ((double)S * (double)H * (double)nrt > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
     const int64_t wgs = S * H * nrt;
-    // at least four tiles of slots a split
-    p->nsplit = std::max<int64_t>(1, std::min(ceil_div(kManyWgsPerCu * cus, wgs), span / 256));
+    // as many splits as the device holds at once, of at least four tiles of slots
+    const int64_t room = (c.dim > 128 ? 1 : kManyWgsPerCu) * cus;
+    p->nsplit = std::max<int64_t>(1, std::min(room / wgs, span / 256));
     p->grid = wgs * p->nsplit;
   }
   if (c.weights) {

@@ -18,41 +18,50 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-// One work-group per row: out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, splits in order
-// within each of the groups of dim / 4 threads, then the groups in order.
+// out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k over the splits k under a running maximum M.
+// `per_row` groups of dim / 4 threads share a row (one where the splits are few), splits in order
+// within each, then the groups in order.
 template <class T>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttendArgs a, int per_row) {
   __shared__ f32x4 part[kJoinThreads];
-  __shared__ float red[kJoinThreads / kWave];
-  const int D = a.c.dim, lanes = D / 4, groups = kJoinThreads / lanes, tid = threadIdx.x;
-  const int64_t rows = a.tokens * a.c.heads * a.group, row = blockIdx.x;
-  const float2 *ml = a.part_ml + row;
-  float top = -INFINITY;
-  for (int k = tid; k < a.nsplit; k += kJoinThreads) top = fmaxf(top, ml[(int64_t)k * rows].x);
-  top = block_max(top, red);
-  const float use = top == -INFINITY ? 0.0f : top;
-  const int g = tid / lanes, d4 = tid - g * lanes;
+  __shared__ float2 part_ml[kJoinThreads];
+  const int D = a.c.dim, lanes = D / 4, tid = threadIdx.x;
+  const int g = tid / lanes, d4 = tid - g * lanes, gr = g / per_row, gk = g - gr * per_row;
+  const int rows_per = kJoinThreads / lanes / per_row;
+  const int64_t rows = a.tokens * a.c.heads * a.group, row = (int64_t)blockIdx.x * rows_per + gr;
+  const bool mine = gr < rows_per && row < rows;
   f32x4 acc = (f32x4){0, 0, 0, 0};
-  float l = 0.0f;
-  if (g < groups) {
-    for (int k = g; k < a.nsplit; k += groups) {
-      const float2 x = ml[(int64_t)k * rows];
-      if (!(x.y > 0.0f || x.y != x.y)) continue;
-      const float w = fast_exp2(x.x - use);
-      l += w * x.y;
-      acc += w * *(const f32x4 *)(a.part_o + ((int64_t)k * rows + row) * D + d4 * 4);
+  float l = 0.0f, top = -INFINITY;
+  const auto add = [&](float m, float y, f32x4 o) {
+    if (!(y > 0.0f || y != y)) return;         // a split without a slot: its sums were not written
+    const float m_new = fmaxf(top, m), x = fast_exp2(top - m_new), z = fast_exp2(m - m_new);
+    l = l * x + y * z;
+    acc = acc * x + o * z;
+    top = m_new;
+  };
+  if (mine) {
+    for (int k = gk; k < a.nsplit; k += 4 * per_row) {
+      float2 x[4];
+      f32x4 o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t at = (int64_t)(k + u * per_row < a.nsplit ? k + u * per_row : a.nsplit - 1) * rows + row;
+        x[u] = a.part_ml[at];
+        o[u] = *(const f32x4 *)(a.part_o + at * D + d4 * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k + u * per_row < a.nsplit) add(x[u].x, x[u].y, o[u]);
     }
   }
-  // every group needs all groups' l: it travels with the columns
-  __shared__ float part_l[kJoinThreads];
-  part[tid] = acc;
-  part_l[tid] = l;
-  __syncthreads();
-  if (g != 0) return;
-  for (int k = 1; k < groups; ++k) {
-    acc += part[k * lanes + d4];
-    l += part_l[k * lanes + d4];
+  if (per_row > 1) {
+    part[tid] = acc;
+    part_ml[tid] = make_float2(top, l);
+    __syncthreads();
+    if (mine && gk == 0)
+      for (int k = 1; k < per_row; ++k) add(part_ml[tid + k * lanes].x, part_ml[tid + k * lanes].y, part[tid + k * lanes]);
   }
+  if (!mine || gk != 0) return;
   const bool any = l > 0.0f || l != l;
   const float mul = any ? 1.0f / l : 0.0f;
   if (d4 == 0) a.lse[row] = any ? (top + __log2f(l)) * kLn2 : -INFINITY;
@@ -99,9 +108,11 @@ void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 
 }
 
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st) {
-  const dim3 grid((unsigned)(a.tokens * a.c.heads * a.group));
-  if (type == CT_BF16) join_kernel<Bf16><<<grid, kJoinThreads, 0, st>>>(a);
-  else join_kernel<F16><<<grid, kJoinThreads, 0, st>>>(a);
+  const int groups = kJoinThreads / (a.c.dim / 4), per_row = a.nsplit <= 4 ? 1 : (a.nsplit < groups ? a.nsplit / 4 : groups);
+  const int64_t rows_per = groups / per_row, rows = a.tokens * a.c.heads * a.group;
+  const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per));
+  if (type == CT_BF16) join_kernel<Bf16><<<grid, kJoinThreads, 0, st>>>(a, per_row);
+  else join_kernel<F16><<<grid, kJoinThreads, 0, st>>>(a, per_row);
 }
 
 void launch_attend_sums_join(const AttendArgs &a, hipStream_t st) {
