@@ -56,6 +56,9 @@ __device__ __forceinline__ int64_t place_offset(const CacheView &c, SlotPlace p)
   return p.page < 0 ? -1 : (int64_t)p.page * c.page_stride + (int64_t)p.row * c.slot_stride;
 }
 
+// Slots of a sequence at most: sums of a slot, a window and a tile stay in 32 bits.
+constexpr int32_t kMaxSlots = 1 << 30;
+
 // New tokens of a sequence: tokens t0 .. t0 + m of the batch, in slots first .. n of the
 // sequence's n slots.  Values outside the call's bounds are cut to them.
 struct SeqSpan {
@@ -69,7 +72,7 @@ __device__ __forceinline__ SeqSpan seq_span(const int32_t *starts, const int32_t
   b = b < a ? a : (b > tokens ? tokens : b);
   const int32_t cnt = (int32_t)(b - a);
   int32_t n = lens[s];
-  n = n < 0 ? 0 : n;
+  n = n < 0 ? 0 : (n > kMaxSlots ? kMaxSlots : n);
   SeqSpan r;
   r.t0 = a;
   r.first = n - cnt;

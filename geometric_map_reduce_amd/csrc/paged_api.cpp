@@ -175,7 +175,7 @@ int check_attend(const keops_cache_t *c, int type, int64_t tokens, int heads, in
   if (tokens < 0 || heads < 1 || heads % c->heads || max_q < 0 || max_len < 0 || window < 0) return KEOPS_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(decay)) return KEOPS_ERR_INVALID_ARG;
   if (tokens > 0x7fffffff || heads > 65535 || (int64_t)max_q * (heads / c->heads) > 0x3fffffff ||
-      max_len > 0x7fffffff - 4096)
+      max_len > kMaxSlots)
     return KEOPS_ERR_UNSUPPORTED;
   return KEOPS_OK;
 }
@@ -272,7 +272,7 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.gdiv = make_fastdiv((uint32_t)a.group);
   a.max_q = max_q;
   a.max_len = max_len;
-  a.window = window;
+  a.window = std::min(window, kMaxSlots);
   a.scale_log2 = scale * kLog2e;
   a.decay = decay;
   a.out = (char *)out;
@@ -318,7 +318,8 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
       return KEOPS_ERR_INVALID_ARG;
   }
   if ((double)c->seqs * c->heads * (double)budget * (c->dim * width_of(c->type) / 16) > 256.0 * (double)kMaxGrid ||
-      (double)c->table_width * (double)c->page_size > (double)0x7fffffff)
+      (double)c->table_width * (double)c->page_size > (double)kMaxSlots ||
+      (double)c->pages * c->heads * (double)c->page_size > 4294967295.0)       // the selection's 32-bit weight numbers
     return KEOPS_ERR_UNSUPPORTED;
   if (c->seqs == 0) return KEOPS_OK;
   (void)hipGetLastError();

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
         bool there[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-          // at most 2^32 weights: their cache would not fit the device otherwise
+          // below 2^32: the caller sees to it
           const uint32_t at = (key[b + u] * (uint32_t)H + (uint32_t)h) * ps + rows;
           there[u] = key[b + u] < a.c.pages;
           w[u] = 0.0f;

@@ -249,7 +249,7 @@ __device__ __forceinline__ void part_range(const AttendArgs &a, int s, int h, in
 // NW waves: 4, or 8 where one work-group has a short sequence's head to itself and nothing else
 // would hide its latency.
 template <class T, bool E4M3, int D, int NR, bool SCORES, int NW>
-__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, E4M3, D, NR>;
   constexpr int kRows = 16 * NR;
   constexpr int kHalfRows = NW / 2 * kRows;     // half the waves' rows
@@ -320,6 +320,17 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 ? 1 : (E4M3 
     for (int st = 0; st < F::kSteps; ++st)
       qf[nr][st] = r < R ? *(const u32x4 *)(qp + F::step_column(st, q4) * 2) : (u32x4){0, 0, 0, 0};
   }
+  // hidden scores are -inf before they are scaled: a negative factor's sign goes to Q, a zero one's
+  // scores are zeros
+  const float c0f = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
+  const float c = c0f == 0.0f ? 1.0f : fabsf(c0f);
+  const uint32_t flip = c0f < 0.0f ? 0x80008000u : 0u, keep = c0f == 0.0f ? 0u : 0xffffffffu;
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+    for (int st = 0; st < F::kSteps; ++st)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) qf[nr][st][u] = (qf[nr][st][u] ^ flip) & keep;
 
   float m_run[NR], l_run[NR];
   f32x4 acc[NR][F::kTiles];
@@ -330,7 +341,6 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 ? 1 : (E4M3 
 #pragma unroll
     for (int t = 0; t < F::kTiles; ++t) acc[nr][t] = (f32x4){0, 0, 0, 0};
   }
-  const float c = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
   const char *kbase = a.c.k + (int64_t)h * a.c.head_stride;
   const char *vbase = a.c.v + (int64_t)h * a.c.head_stride;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;

@@ -104,7 +104,7 @@ def attention(b: Batch, decay=0.0):
                         continue
                     z = (k[at] @ x) * b.scale
                     # fp32 sums of D exact products, the scale's and the exponent's roundings
-                    dz = ((k[at].abs() @ x.abs()) * b.scale * (D + 8) * U32 + 8 * U32 * z.abs()).max().item()
+                    dz = ((k[at].abs() @ x.abs()) * abs(b.scale) * (D + 8) * U32 + 8 * U32 * z.abs()).max().item()
                     L = torch.logsumexp(z, 0)
                     p = torch.exp(z - L)
                     out[t, h * G + g] = p @ v[at]

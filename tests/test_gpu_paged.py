@@ -427,3 +427,249 @@ def test_verify_edges():
     us[10], ua[10] = 0.5, 1.0
     check_verify(target, draft, tokens, counts, ua, us)
     check_verify(target, None, tokens, counts, ua, us)
+
+
+# ---- wider ranges
+
+def random_case(seed):
+    """A seeded case of the operators' ranges, small enough for the plain form."""
+    import random
+    rng = random.Random(seed)
+    kv = rng.choice([1, 2, 4])
+    dtype = rng.choice([BF, BF, FP])
+    dim = rng.choice([64, 96, 128, 256])
+    group = rng.choice([1, 2, 4, 5, 7, 8])
+    S = rng.choice([1, 2, 5, 70])
+    top = rng.choice([1, 3, 9, 40])
+    if S == 70:
+        kv, top = 1, rng.choice([1, 2])
+    lens, new = [], []
+    for _ in range(S):
+        n = rng.choice([0, 1, rng.randint(1, 50), rng.randint(1, 700 if S < 70 else 120)])
+        lens.append(n)
+        new.append(min(n, rng.randint(0, top)))
+    return dict(lens=lens, new=new, heads=kv * group, kv_heads=kv, dim=dim, page=rng.choice([1, 5, 16, 20, 64, 128]), dtype=dtype,
+                cache=rng.choice([dtype, dtype, E4])), rng.choice([0, 0, 1, 37, 200]), rng.random() < 0.5
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_random(seed):
+    case, window, weights = random_case(seed)
+    say(f"random attention {seed}: {len(case['lens'])} sequences, {case['heads']}/{case['kv_heads']} x {case['dim']} page {case['page']} "
+        f"{case['dtype']} {case['cache']} window {window} weights {weights} lens {case['lens'][:6]} new {case['new'][:6]}")
+    b = ref.Batch(seed, **case)
+    if b.T == 0:
+        b = ref.Batch(seed, **dict(case, lens=case["lens"] + [9], new=case["new"] + [2]))
+    b.window = window
+    if weights:
+        b.weights = torch.rand((b.P, b.kv, b.page), generator=b.gen)
+    check_attention(b, decay=0.25 if weights and seed % 2 else 0.0)
+
+
+@pytest.mark.parametrize("S", [64, 65, 200])
+def test_many_sequences(S):
+    """More sequences than a wave has lanes, some of them empty; the second pass joins parts of most."""
+    say(f"{S} sequences")
+    lens = [(37 * s) % 300 for s in range(S)]
+    lens[S // 2] = 3000
+    new = [min(n, 1 + s % 2) for s, n in enumerate(lens)]
+    b = ref.Batch(S, lens, new, 4, 1, 64, 16)
+    b.weights = torch.full((b.P, 1, 16), float("nan"))
+    check_attention(b)
+
+
+@pytest.mark.parametrize("new,weights", [(2, False), (2, True), (20, False)])
+def test_negative_and_zero_scale(new, weights):
+    for scale in (-0.11, 0.0):
+        say(f"scale {scale}, {new} new")
+        b = ref.Batch(43, [200, 90], [new, new], 8, 2, 128, 16)
+        b.scale = scale
+        if weights:
+            b.weights = torch.zeros((b.P, 2, 16))
+        check_attention(b)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_lengths_past_the_bounds(new):
+    """max_len and max_q cut; what is inside them is right."""
+    say(f"cut lengths, {new} new")
+    b = ref.Batch(47, [300, 100], [new, new], 4, 2, 64, 16)
+    out, lse = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), put(b.lens_t()), put(b.starts), new, 100)
+    torch.cuda.synchronize()
+    o, z, _, ot, zt, _ = ref.attention(b)
+    close(out[new:].cpu(), o[new:], ot[new:], "out")
+    close(lse[new:].cpu(), z[new:], zt[new:], "lse")
+    if new > 1:
+        full = run_attention(b)[0]
+        out, _ = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), put(b.lens_t()), put(b.starts), new // 2, 300)
+        torch.cuda.synchronize()
+        half = new // 2
+        o, _, _, ot, _, _ = ref.attention(b)
+        close(out[:half].cpu(), o[:half], ot[:half], "first half")
+        assert full.shape == out.shape
+
+
+@pytest.mark.parametrize("n,budget", [(30000, 25000), (70000, 60000), (70000, 100)])
+def test_evict_ties_at_the_border(n, budget):
+    """The border falls among thousands of equal weights: the lower slots stay."""
+    say(f"evict ties, {n} slots, budget {budget}")
+    page = 64
+    used, more = -(-n // page), -(-budget // page)
+    g = torch.Generator().manual_seed(n + budget)
+    w = torch.rand((used + more, 1, page), generator=g)
+    w[w < 0.4 if budget > 1000 else w < 2.0] = 0.0
+    order = torch.randperm(used + more, generator=g).to(torch.int32)
+    flat = w[order[:used].long(), 0].reshape(-1)[:n]
+    mid = torch.sort(flat[3:n - 10], descending=True, stable=True).indices[:budget - 13] + 3
+    want = torch.cat([torch.arange(3), mid.sort().values, torch.arange(n - 10, n)])
+    k = torch.zeros((used + more, page, 1, 64), dtype=BF, device="cuda")
+    kept, _ = gm.keops_cache_evict(k, k.clone(), w.cuda(), order[:used][None].cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+                                   order[used:][None].cuda(), budget, sink=3, recent=10)
+    assert torch.equal(kept.cpu()[0, 0].long(), want)
+
+
+def test_verify_graph():
+    say("graph of a verification")
+    target, draft, tokens, counts, ua, us = (put(t) for t in verify_case(5, 4, 3, 9000))
+    gm.keops_verify_draft(target, draft, tokens, counts, ua, us)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out, acc = gm.keops_verify_draft(target, draft, tokens, counts, ua, us)
+    for rep in range(4):
+        new = verify_case(50 + rep, 4, 3, 9000)
+        for t, x in zip((target, draft, tokens, counts, ua, us), new):
+            t.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        o, a = gm.keops_verify_draft(target, draft, tokens, counts, ua, us)
+        ro, ra = ref.verify(*new)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(acc, a) and torch.equal(o.cpu(), ro) and torch.equal(a.cpu(), ra)
+
+
+def test_failed_workspace_enqueues_nothing():
+    say("failing workspace")
+    b = ref.Batch(53, [900, 500], [1, 1], 8, 2, 128, 16)
+    args = [put(t) for t in (b.q, b.k, b.v, b.table, b.lens_t(), b.starts)]
+    out, lse = torch.full_like(args[0], 3.0), torch.full((2, 8), 3.0, device="cuda")
+    v = [put(t) for t in verify_case(5, 2, 3, 5000)]
+    vo, va = torch.full((2, 4), 7, dtype=torch.int32, device="cuda"), torch.full((2,), 7, dtype=torch.int32, device="cuda")
+    gm.keops_set_option(gm.KEOPS_OPT_FAIL_ALLOC, 1)
+    try:
+        with pytest.raises(gm.KeopsError) as e:
+            gm.keops_paged_attention(*args, 1, 900, out=out, lse=lse)
+        assert e.value.status == -3
+        with pytest.raises(gm.KeopsError) as e:
+            gm.keops_verify_draft(*v, out=vo, accepted=va)
+        assert e.value.status == -3
+    finally:
+        gm.keops_set_option(gm.KEOPS_OPT_FAIL_ALLOC, 0)
+    torch.cuda.synchronize()
+    assert bool((out == 3).all()) and bool((lse == 3).all()) and bool((vo == 7).all()) and bool((va == 7).all())
+    # a workspace for each call gives the same bits
+    want = gm.keops_paged_attention(*args, 1, 900)
+    gm.keops_set_option(gm.KEOPS_OPT_WS_CACHE, 2)
+    try:
+        got = gm.keops_paged_attention(*args, 1, 900)
+        torch.cuda.synchronize()
+    finally:
+        gm.keops_set_option(gm.KEOPS_OPT_WS_CACHE, 0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_wide_windows_and_long_lengths(new):
+    """Windows beyond every slot change nothing; a length beyond all bounds is cut."""
+    say(f"wide windows, {new} new")
+    b = ref.Batch(59, [140], [new], 4, 2, 64, 16)
+    want = run_attention(b)
+    for b.window in (140, 2 ** 30 - 1, 2 ** 31 - 1):
+        got = run_attention(b)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    b.window = 0
+    lens = torch.tensor([2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    out, lse = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), lens, put(b.starts), new, 140)
+    torch.cuda.synchronize()
+    # every token sees all 140 slots of the table
+    n = 140
+    k, v = (b.rows(t, None, 0, 0, n)[0] for t in (b.k, b.v))
+    p = torch.softmax(b.q[0, 0].double() @ k.T * b.scale, 0)
+    assert (out[0, 0].double().cpu() - p @ v).abs().max() <= 2 ** -7 * v.abs().max()
+
+
+def test_binding_refusals():
+    """What the kernels cannot take is named before any launch."""
+    b = ref.Batch(1, [20], [2], 4, 2, 64, 16, junk=0.0)
+    q, k, v, table, lens, starts = (put(t) for t in (b.q, b.k, b.v, b.table, b.lens_t(), b.starts))
+
+    def attend(**kw):
+        a = dict(q=q, k_pages=k, v_pages=v, page_table=table, lens=lens, starts=starts, max_q=2, max_len=20)
+        a.update(kw)
+        return gm.keops_paged_attention(**a)
+    attend()
+    wide = torch.zeros((2, 4, 65), dtype=BF, device="cuda")
+    for kw, what in [(dict(q=q.float()), "q"), (dict(q=q.half()), "q"), (dict(q=q[:, :3].contiguous()), "multiple"), (dict(q=wide[:, :, 1:]), "q"),
+                     (dict(q=q.transpose(0, 1)), "q"), (dict(v_pages=v[:-1]), "v_pages"), (dict(v_pages=v.half()), "v_pages"),
+                     (dict(k_pages=k[..., :32], v_pages=v[..., :32]), "dim"), (dict(k_pages=k.float(), v_pages=v.float()), "k_pages"),
+                     (dict(page_table=table.long()), "page_table"), (dict(page_table=table[0]), "page_table"), (dict(lens=lens.long()), "lens"),
+                     (dict(lens=lens.cpu()), "lens"), (dict(starts=starts[:-1]), "starts"), (dict(max_q=-1), "max_q"),
+                     (dict(weights=torch.zeros((3, 2, 16), device="cuda")), "weights"), (dict(k_scale=torch.ones(2, device="cuda")), "float8"),
+                     (dict(k_pages=k.to(E4), v_pages=v.to(E4)), "k_scale"), (dict(out=torch.empty_like(q, dtype=torch.float32)), "out"),
+                     (dict(lse=torch.empty((2, 4), device="cuda", dtype=BF)), "lse")]:
+        with pytest.raises(ValueError, match=what):
+            attend(**kw)
+    with pytest.raises(gm.KeopsError):
+        attend(scale=float("nan"))
+    with pytest.raises(gm.KeopsError):
+        attend(out=q)
+    with pytest.raises(ValueError, match="k must"):
+        gm.keops_cache_append(q, q, k, v, table, lens, starts)
+    with pytest.raises(ValueError, match="shape and type of k"):
+        gm.keops_cache_append(q[:, :2].contiguous(), q[:1, :2].contiguous(), k, v, table, lens, starts)
+    w = torch.zeros((b.P, 2, 16), device="cuda")
+    for kw in (dict(budget=0), dict(budget=4, sink=3, recent=2), dict(budget=40)):
+        with pytest.raises(ValueError):
+            gm.keops_cache_evict(k, v, w, table, lens, table[:, :1].contiguous(), **kw)
+    with pytest.raises(ValueError, match="weights"):
+        gm.keops_cache_evict(k, v, None, table, lens, table, 4)
+    target, draft, tokens, counts, ua, us = (put(t) for t in verify_case(5, 2, 3, 50))
+    for i, bad in enumerate((target[:, :3].contiguous(), draft.double(), tokens.long(), counts[:1], ua[:, :2].contiguous(), us.double())):
+        a = [target, draft, tokens, counts, ua, us]
+        a[i] = bad
+        with pytest.raises(ValueError):
+            gm.keops_verify_draft(*a)
+
+
+def test_example_decodes():
+    """The example's loop: every round's attention equals the dense formula over the cache as it stands, the weights
+    have grown by what the rows gave, and evicted caches go on."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    rounds = [0]
+
+    def watch(st):
+        rounds[0] += 1
+        if rounds[0] % 5:
+            return
+        m, p = st["model"], st["pages"]
+        for s in range(len(st["lens"])):
+            n, a, e = int(st["lens"][s]), int(st["starts"][s]), int(st["starts"][s + 1])
+            rows = st["table"][s].long()
+            k = p.k[rows].reshape(-1, m.kv, m.dim)[:n].double().cpu()
+            v = p.v[rows].reshape(-1, m.kv, m.dim)[:n].double().cpu()
+            assert torch.equal(k[n - (e - a):], st["k"][a:e].double().cpu())
+            q = st["q"][a:e].double().cpu()
+            for h in range(m.heads):
+                z = q[:, h] @ k[:, h // (m.heads // m.kv)].T / m.dim ** 0.5
+                z.masked_fill_(torch.arange(n) > torch.arange(n - (e - a), n)[:, None], -float("inf"))
+                o = torch.softmax(z, -1) @ v[:, h // (m.heads // m.kv)]
+                assert (st["out"][a:e, h].double().cpu() - o).abs().max() <= 2 ** -7 * v.abs().max()
+    text = ex.decode(rounds=40, watch=watch)
+    assert rounds[0] == 40 and all(40 <= len(t) <= 160 for t in text)
+    assert ex.decode(rounds=10) == [t[:len(u)] for t, u in zip(text, ex.decode(rounds=10))]

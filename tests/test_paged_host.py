@@ -88,6 +88,7 @@ def test_attention_refusals(L):
     assert call_attend(L, cache(pages=0, k_pages=None, v_pages=None)) == -1
     assert call_attend(L, cache(), tokens=1 << 31, out=1 << 50, lse=1 << 52, q=1 << 54) == -2
     assert call_attend(L, cache(), max_q=1 << 30) == -2
+    assert call_attend(L, cache(), max_len=(1 << 30) + 1) == -2
     assert call_attend(L, cache(), tokens=0, q=None, out=None, lse=None, starts=None) == 0
     assert call_attend(L, cache(), max_q=0) == 0
     n = ctypes.c_int64(7)
@@ -103,6 +104,8 @@ def test_evict_refusals(L):
         assert call_evict(L, ok, **kw) == -1, kw
     assert call_evict(L, cache()) == -1                          # no weights
     assert call_evict(L, cache(weights=0xA0000000, table_width=1 << 28), width=1 << 28) == -2
+    far = dict(weights=1 << 50, k_pages=1 << 51, v_pages=1 << 52)
+    assert call_evict(L, cache(pages=1 << 30, **far)) == -2            # weight numbers past 32 bits
     assert call_evict(L, cache(weights=0xA0000000, seqs=0, lens=None, page_table=None), new=None, kept=None, lens=None) == 0
 
 
