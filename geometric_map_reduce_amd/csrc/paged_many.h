@@ -57,21 +57,24 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 
 template <class T, bool E4M3, int D>
 __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
-  constexpr int KT = D > 128 ? 32 : 64;              // slots of a tile
+  // slots of a tile: two halves are two independent chains of products (one of 32 waited for itself:
+  // D = 256 ran at 647 instead of 759 TFLOP/s)
+  constexpr int KT = 64;
   constexpr int kSteps = D / 16, kCols = D / 32, kSub = KT / 32;
   constexpr int kPieces = D / 8;                     // 16-byte pieces of a row in LDS
   constexpr int kLoads = KT * kPieces / kManyThreads;
-  // tiles in LDS: as many as leave room for two work-groups on a compute unit (8-bit ones pass
-  // registers, one ahead)
-  constexpr int kBufs = E4M3 ? 2 : (D == 64 || D == 256 ? 4 : (D == 96 ? 3 : 2));
+  // tiles in LDS: as many as leave room for two work-groups on a compute unit (one at D = 256; 8-bit
+  // ones pass registers, one ahead)
+  constexpr int kBufs = E4M3 ? 2 : (D == 64 ? 4 : (D == 96 ? 3 : 2));
   constexpr int kChunk = D == 96 ? 4 : 8;            // tiles whose addresses are placed together
   constexpr int kPlace = kChunk * KT / kManyThreads; // slots a thread places
   static_assert(kBufs <= kChunk, "a chunk is placed before the first fetch from it");
+  static_assert(KT == kWave, "a wave's ballot is a tile");
   static_assert(KT * kPieces % kManyThreads == 0 && kChunk * KT % kManyThreads == 0, "whole pieces per thread");
   __shared__ __align__(16) uint16_t sk[kBufs][KT * D];
   __shared__ __align__(16) uint16_t sv[kBufs][KT * D];
   __shared__ int64_t off[2][kChunk * KT];
-  __shared__ uint64_t present[2][kChunk * KT / 64];    // which of 64 slots are there
+  __shared__ uint64_t present[2][kChunk];              // which of a tile's slots are there
 
   const int H = a.c.heads, G = a.group;
   const int64_t heads = (int64_t)H * G;
@@ -152,11 +155,6 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
       const uint64_t there = __ballot(page[i] >= 0);
       if (lane == 0) present[chunk & 1][i * 4 + wave] = there;
     }
-  };
-  const auto present_at = [&](int tile) -> uint64_t {
-    const int at = tile % kChunk * KT;
-    const uint64_t m = present[(tile / kChunk) & 1][at / 64];
-    return KT == 64 ? m : (m >> (at & 63)) & 0xffffffffu;
   };
   const auto off_at = [&](int tile) -> const int64_t * { return &off[(tile / kChunk) & 1][tile % kChunk * KT]; };
 
@@ -301,8 +299,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   const auto turn = [&](int buf, int tile) {
     if (tile + kBufs - 1 < tiles) fetch(tile + kBufs - 1);
     const int j0 = lo + tile * KT;
-    const uint64_t there = present_at(tile);
-    const bool masked = there != (KT == 64 ? ~(uint64_t)0 : 0xffffffffu) || j0 + KT - 1 > first_pos ||
+    const uint64_t there = present[(tile / kChunk) & 1][tile % kChunk];
+    const bool masked = there != ~(uint64_t)0 || j0 + KT - 1 > first_pos ||
                         (a.window > 0 && j0 <= last_pos - a.window);
     step(masked, buf, tile, there);
     if (tile % kChunk == 0 && tile + kChunk < tiles) {      // a chunk ahead of the first fetch from it
