@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -20,14 +21,9 @@ from .binding import _check, _out, _raw_stream, _stream, lib
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("weights", ctypes.c_void_p),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
-                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("pages", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
-                ("lens", ctypes.c_void_p), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
-                ("dim", ctypes.c_int32), ("type", ctypes.c_int32), ("table_width", ctypes.c_int32),
-                ("seqs", ctypes.c_int32)]
+# keops_cache_t: k_pages, v_pages, weights, k_scale, v_scale; page, slot and head stride, pages;
+# page_table, table_stride, lens; page_size, heads, dim, type, table_width, seqs
+_CACHE = struct.Struct("=5Q4qQqQ6i")
 
 
 def _tensor(t, name):
@@ -49,18 +45,19 @@ def _vec(t, name, shape, dtype, dev):
 
 
 def _table(t, name, seqs, dev):
-    _tensor(t, name)
-    if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 2 or t.shape[0] != seqs or \
-            (t.stride(1) != 1 and t.shape[1] > 1):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != seqs or t.dtype is not torch.int32 or t.get_device() != dev or \
+            (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be an int32 tensor [{seqs}, pages of a sequence] on cuda:{dev} with contiguous rows")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    return t.data_ptr(), strides[0], shape[1]
 
 
 def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales=True):
-    """(the structure of the C ABI, the device's number, (heads, dim, type))."""
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (lens, "lens")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
+    """(the structure of the C ABI, the device's number, sequences, (heads, dim, type), page size, pages of a sequence)."""
+    if not (isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor) and isinstance(lens, torch.Tensor)):
+        _tensor(k_pages, "k_pages"), _tensor(v_pages, "v_pages"), _tensor(lens, "lens")
     dev, dtype, shape, strides = k_pages.get_device(), k_pages.dtype, k_pages.shape, k_pages.stride()
     kind = _TYPES.get(dtype)
     if len(shape) != 4 or kind is None or dev < 0 or strides[3] != 1:
@@ -75,7 +72,7 @@ def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales
         raise ValueError(f"lens must be a contiguous int32 tensor [sequences] on cuda:{dev}")
     S = lens.shape[0]
     table, table_stride, width = _table(page_table, "page_table", S, dev)
-    w = ks = vs = None
+    w = ks = vs = 0
     if weights is not None:
         w = _vec(weights, "weights", (P, H, ps), torch.float32, dev)
     if kind == 2:
@@ -87,9 +84,9 @@ def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
     # the stride of a dimension of one is never used
-    c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), w, ks, vs, strides[0] if P > 1 else 0, strides[1] if ps > 1 else 0,
-               strides[2] if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind, width, S)
-    return c, dev, (H, D, dtype)
+    c = _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), w, ks, vs, strides[0] if P > 1 else 0, strides[1] if ps > 1 else 0,
+                    strides[2] if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind, width, S)
+    return c, dev, S, (H, D, dtype), ps, width
 
 
 _HALF = (torch.bfloat16, torch.float16)
@@ -151,13 +148,13 @@ def keops_cache_append(k, v, k_pages, v_pages, page_table, lens, starts, weights
                        stream=None):
     """Write rows starts[s] .. starts[s+1] of k and v [tokens, heads, dim] to the last slots of sequence s
     (``lens`` counts them already); clear those slots' ``weights``."""
-    c, dev, cache = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
-    kp, ks = _rows(k, "k", c.heads, cache, dev)
-    vp, vs = _rows(v, "v", c.heads, cache, dev)
+    c, dev, S, cache, _, _ = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
+    kp, ks = _rows(k, "k", cache[0], cache, dev)
+    vp, vs = _rows(v, "v", cache[0], cache, dev)
     if v.shape != k.shape or v.dtype is not k.dtype:
         raise ValueError("v must have the shape and type of k")
-    st = _vec(starts, "starts", (c.seqs + 1,), torch.int32, dev)
-    _run("keops_cache_append", dev, stream, lib().keops_cache_append, ctypes.addressof(c), kp, vp, ks, vs, _TYPES[k.dtype], st,
+    st = _vec(starts, "starts", (S + 1,), torch.int32, dev)
+    _run("keops_cache_append", dev, stream, lib().keops_cache_append, c, kp, vp, ks, vs, _TYPES[k.dtype], st,
          k.shape[0])
 
 
@@ -168,12 +165,12 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     ``max_q`` and ``max_len`` bound the new tokens and the slots of any sequence; ``scale`` is
     1 / sqrt(dim) unless given; ``window`` > 0 limits a token to that many slots, its own included.
     With ``weights``, every slot's becomes decay * old + the attention it received in this call."""
-    c, dev, cache = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
+    c, dev, S, cache, _, _ = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
     qp, qs = _rows(q, "q", None, cache, dev)
     T, heads, D = q.shape
-    if heads < 1 or heads % c.heads:
-        raise ValueError(f"the query heads must be a multiple of the cache's {c.heads}, got {heads}")
-    st = _vec(starts, "starts", (c.seqs + 1,), torch.int32, dev)
+    if heads < 1 or heads % cache[0]:
+        raise ValueError(f"the query heads must be a multiple of the cache's {cache[0]}, got {heads}")
+    st = _vec(starts, "starts", (S + 1,), torch.int32, dev)
     max_q, max_len, window = int(max_q), int(max_len), int(window)
     if min(max_q, max_len, window) < 0 or max(max_q, max_len, window) > 2**31 - 1:
         raise ValueError("max_q, max_len and window must be in [0, 2^31)")
@@ -182,9 +179,8 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
             None if lse is not None else torch.empty((T, heads), dtype=torch.float32, device=q.device))
     out = made[0] if out is None else _out(out, (T, heads, D), q.device, q.dtype)
     lse = made[1] if lse is None else _out(lse, (T, heads), q.device, name="lse")
-    ca = ctypes.addressof(c)
-    ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, ca, kind, heads, T, max_q, max_len, window)
-    _run("keops_paged_attention", dev, stream, lib().keops_paged_attention, ca, qp, qs, kind, heads, st, T, max_q, max_len,
+    ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, c, kind, heads, T, max_q, max_len, window)
+    _run("keops_paged_attention", dev, stream, lib().keops_paged_attention, c, qp, qs, kind, heads, st, T, max_q, max_len,
          1.0 / math.sqrt(D) if scale is None else float(scale), window, float(decay), out.data_ptr(), lse.data_ptr(), ws, nbytes)
     if stream is not None:
         _keep(stream, dev, *made, buf)
@@ -196,21 +192,20 @@ def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, bu
     """Keep ``budget`` slots of every sequence and head: the first ``sink``, the last ``recent``, and those with
     the largest weights; move them to the pages of ``new_table``.  Returns (kept [sequences, heads, budget]
     old slot numbers or -1, new lens).  The scales of an 8-bit cache are not needed."""
-    c, dev, _ = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
+    c, dev, S, (H, _, _), ps, width = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
     if weights is None:
         raise ValueError("eviction needs weights")
-    nt, nstride, nwidth = _table(new_table, "new_table", c.seqs, dev)
+    nt, nstride, nwidth = _table(new_table, "new_table", S, dev)
     budget, sink, recent = int(budget), int(sink), int(recent)
     if not 1 <= budget < 2**31 or sink < 0 or recent < 0 or sink + recent > budget:
         raise ValueError("need 1 <= budget < 2^31, sink >= 0, recent >= 0 and sink + recent <= budget")
-    if nwidth < min(-(-budget // c.page_size), c.table_width):
+    if nwidth < min(-(-budget // ps), width):
         raise ValueError("new_table has too few pages for the budget")
-    S, H = c.seqs, c.heads
     made = (None if kept is not None else torch.empty((S, H, budget), dtype=torch.int32, device=k_pages.device),
             None if new_lens is not None else torch.empty((S,), dtype=torch.int32, device=k_pages.device))
     kept = made[0] if kept is None else _out(kept, (S, H, budget), k_pages.device, torch.int32, name="kept")
     new_lens = made[1] if new_lens is None else _out(new_lens, (S,), k_pages.device, torch.int32, name="new_lens")
-    _run("keops_cache_evict", dev, stream, lib().keops_cache_evict, ctypes.addressof(c), nt, nstride, nwidth, budget, sink, recent,
+    _run("keops_cache_evict", dev, stream, lib().keops_cache_evict, c, nt, nstride, nwidth, budget, sink, recent,
          kept.data_ptr(), new_lens.data_ptr())
     if stream is not None:
         _keep(stream, dev, *made)

@@ -8,9 +8,23 @@ import torch
 
 import geometric_map_reduce_amd as gm
 from geometric_map_reduce_amd import binding
-from geometric_map_reduce_amd.paged import _Cache
+from geometric_map_reduce_amd.paged import _CACHE
 
 A, B, C, D, E, F, G = (0x10000000 * (i + 1) for i in range(7))    # never dereferenced: validation fails first
+
+
+class _Cache(ctypes.Structure):
+    """keops_cache_t as the header declares it."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "weights", "k_scale", "v_scale")] + \
+        [(n, ctypes.c_int64) for n in ("page_stride", "slot_stride", "head_stride", "pages")] + \
+        [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("page_size", "heads", "dim", "type", "table_width", "seqs")]
+
+
+def test_binding_packs_the_structure():
+    vals = list(range(1, 19))
+    c = _Cache.from_buffer_copy(_CACHE.pack(*vals))
+    assert _CACHE.size == ctypes.sizeof(_Cache) and [getattr(c, n) for n, _ in _Cache._fields_] == vals
 
 
 @pytest.fixture(scope="module")
