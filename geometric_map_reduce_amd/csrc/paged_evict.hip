@@ -39,7 +39,7 @@ struct SelectShared {
   uint32_t place[kHeld * kSelectWaves];  // kept before each 64 slots, two counts in one word
   __align__(16) uint32_t wave_sum[kSelectWaves];
   uint32_t prefix, need, count;
-  uint32_t cand_key[kWave], cand_slot[kWave], cands;
+  uint32_t cand_key[kWave], cand_slot[kWave], cand_rank[kWave], cands;
   uint32_t cut_key, cut_slot;
 };
 
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     count = sh.count;
     if (count == need) break;          // all that share the digits so far are kept
     if (count <= kWave && segments == 1) {
-      // few share them: one wave ranks them by weight and slot
+      // few share them: they are ranked by weight and slot, each wave against a part of them
 #pragma unroll
       for (int b = 0; b < kHeld; b += kBatch) {
         if (b * kSelectThreads < M) {
@@ -211,18 +211,19 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
           }
         }
       }
+      if (tid < kWave) sh.cand_rank[tid] = 0;
       __syncthreads();
-      if (wave == 0) {
-        const uint32_t k = sh.cand_key[lane], i = sh.cand_slot[lane];
-        uint32_t rank = 0;
-        for (uint32_t m = 0; m < count; ++m) {
-          const uint32_t km = __builtin_amdgcn_readlane(k, m), im = __builtin_amdgcn_readlane(i, m);
-          rank += km > k || (km == k && im < i);
-        }
-        if ((uint32_t)lane < count && rank == need - 1) {
-          sh.cut_key = k;
-          sh.cut_slot = i;
-        }
+      const uint32_t k = sh.cand_key[lane], i = sh.cand_slot[lane];
+      uint32_t before = 0;
+      for (uint32_t m = wave; m < count; m += kSelectWaves) {
+        const uint32_t km = __builtin_amdgcn_readlane(k, m), im = __builtin_amdgcn_readlane(i, m);
+        before += km > k || (km == k && im < i);
+      }
+      if (before) atomicAdd(&sh.cand_rank[lane], before);
+      __syncthreads();
+      if (tid < (int)count && sh.cand_rank[tid] == need - 1) {
+        sh.cut_key = k;
+        sh.cut_slot = i;
       }
       __syncthreads();
       prefix = sh.cut_key;
