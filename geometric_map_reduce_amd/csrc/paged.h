@@ -167,7 +167,11 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 
+// kShift: p is computed 2^kShift larger.  fp16 ends at 2^-24, and 10^5 slots below that would add up
+// to some 10^-3 of a sum; with p up to 2^15 (2^8 by the lazy maximum, 2^7 here) it ends at 2^-31 of the
+// largest.
 struct Bf16 {
+  static constexpr float kShift = 0.0f;
   static constexpr uint32_t kExp = 0x7f807f80u;   // exponent bits of a pair
   static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -188,6 +192,7 @@ struct Bf16 {
   }
 };
 struct F16 {
+  static constexpr float kShift = 7.0f;
   static constexpr uint32_t kExp = 0x7c007c00u;
   static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);

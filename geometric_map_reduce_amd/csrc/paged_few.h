@@ -18,6 +18,8 @@
 //  * The running maximum moves only when a score passes it by 2^8 (one branch per tile), so the
 //    sums and p stay below 2^8 times what they would be; sums are in 32 bits, p is rounded to
 //    the cache's 16-bit type for the matrix product (8-bit caches: q's type).
+//  * HBM bounds it: 64 sequences of 5,120 slots (bf16, 16 rows a head) read 1.34 GB in 245 us, 5.5 TB/s
+//    with both passes; 131,071 slots of one sequence 5.1 TB/s and 6 us of the second pass.
 //  * Slots that no row may see (past the length, of a page that the table lacks) get a zero V.
 //    Slots that some rows see and others do not are only in the tiles of the new tokens and at
 //    the window's edge; if such a tile holds an infinity or NaN in V, it is added after the
@@ -332,7 +334,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
 #pragma unroll
       for (int u = 0; u < 4; ++u) qf[nr][st][u] = (qf[nr][st][u] ^ flip) & keep;
 
-  float m_run[NR], l_run[NR];
+  float m_run[NR], l_run[NR];      // 2^m_run is the unit of the sums
   f32x4 acc[NR][F::kTiles];
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) {
@@ -427,8 +429,8 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
             *(f32x4 *)(at4 + 16 * a.score_rows) = (f32x4){z[4], z[5], z[6], z[7]};
           }
         }
-        if (__any(top > m_run[nr] + kLazy)) {
-          const float m_new = fmaxf(m_run[nr], xor_max(top));
+        if (__any(top > m_run[nr] + (kLazy + T::kShift))) {
+          const float m_new = fmaxf(m_run[nr], xor_max(top) - T::kShift);
           const float alpha = m_new == -INFINITY ? 1.0f : fast_exp2(m_run[nr] - m_new);
           l_run[nr] *= alpha;
           m_run[nr] = m_new;

@@ -13,7 +13,9 @@
 //
 // Two kernels: sums of pieces of the row by many work-groups (one read of two rows of the
 // vocabulary, bound by HBM for a batch and by latency for one sequence), then one work-group per
-// sequence that finds the piece and looks through it.
+// sequence that finds the piece and looks through it.  64 sequences of 131,072 tokens: 11 us
+// (67 MB at 6 TB/s, part of it from the cache) and 7 us; one of 32,000: 4 and 5 us.  One work-group
+// per sequence for both took 146 us: a compute unit reads some 10 bytes a nanosecond here.
 #include "paged.h"
 
 namespace kmi {

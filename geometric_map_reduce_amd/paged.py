@@ -175,8 +175,8 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     if min(max_q, max_len, window) < 0 or max(max_q, max_len, window) > 2**31 - 1:
         raise ValueError("max_q, max_len and window must be in [0, 2^31)")
     kind = _TYPES[q.dtype]
-    made = (None if out is not None else torch.empty((T, heads, D), dtype=q.dtype, device=q.device),
-            None if lse is not None else torch.empty((T, heads), dtype=torch.float32, device=q.device))
+    made = (None if out is not None else torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, heads, D)),
+            None if lse is not None else q.new_empty((T, heads), dtype=torch.float32))
     out = made[0] if out is None else _out(out, (T, heads, D), q.device, q.dtype)
     lse = made[1] if lse is None else _out(lse, (T, heads), q.device, name="lse")
     ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, c, kind, heads, T, max_q, max_len, window)

@@ -549,6 +549,28 @@ def test_verify_graph():
         assert torch.equal(out, o) and torch.equal(acc, a) and torch.equal(o.cpu(), ro) and torch.equal(a.cpu(), ra)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_many_small_weights(new):
+    """One slot far above 60,000 others, whose weights fp16 cannot hold one by one, but which add up."""
+    say(f"many small weights, {new} new")
+    n, D = 60000 + new, 64
+    b = ref.Batch(61, [n], [new], 1, 1, D, 128, FP)
+    one = torch.zeros(D, dtype=FP)
+    one[0] = 1.0
+    b.q[:] = one * 8
+    b.k[:], b.v[:] = 0.0, 1.0
+    b.k[b.table[0, 0].item(), 0, 0] = one * 19.0          # exp(19) = 2^27.4 times the others
+    b.v[b.table[0, 0].item(), 0, 0] = 0.0
+    out, lse = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), put(b.lens_t()), put(b.starts), new, n, scale=0.125)
+    torch.cuda.synchronize()
+    import math
+    rest = torch.arange(60000, 60000 + new, dtype=torch.float64)
+    total = math.exp(19.0) + rest
+    # the others' p is 2^-27.4 of the largest, held to 2^-32: 2^-4.6 of itself at most
+    assert bool(((out[:, 0, 0].double().cpu() - rest / total).abs() <= rest / total * 2 ** -4.5 + 2 ** -25).all())
+    assert bool(((lse[:, 0].double().cpu() - total.log()).abs() <= 19 * 16 * 2 ** -24 + n * 2 ** -24).all())
+
+
 def test_failed_workspace_enqueues_nothing():
     say("failing workspace")
     b = ref.Batch(53, [900, 500], [1, 1], 8, 2, 128, 16)
