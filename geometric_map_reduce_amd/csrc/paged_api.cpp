@@ -32,13 +32,25 @@ bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 
 
 int64_t width_of(int type) { return type == KEOPS_TYPE_E4M3 ? 1 : 2; }
 
+// Sizes for the overlap checks: exact where a device could hold them, cut at 2^62.
+int64_t cut(double bytes) { return bytes < 4.6e18 ? (int64_t)bytes : (int64_t)1 << 62; }
+
 // Bytes from the first to past the last element of the pages.
 int64_t pages_extent(const keops_cache_t &c) {
   if (c.pages == 0) return 0;
   const int64_t w = width_of(c.type);
-  return ((c.pages - 1) * c.page_stride + (int64_t)(c.page_size - 1) * c.slot_stride + (c.heads - 1) * c.head_stride + c.dim) * w;
+  return cut(((double)(c.pages - 1) * (double)c.page_stride + (double)(c.page_size - 1) * (double)c.slot_stride +
+              (double)(c.heads - 1) * (double)c.head_stride + c.dim) * (double)w);
 }
-int64_t weights_extent(const keops_cache_t &c) { return c.weights ? c.pages * c.heads * (int64_t)c.page_size * 4 : 0; }
+int64_t weights_extent(const keops_cache_t &c) {
+  return c.weights ? cut((double)c.pages * c.heads * (double)c.page_size * 4.0) : 0;
+}
+// Bytes of `tokens` rows of `row` 16-bit elements, `stride` apart.
+int64_t rows_extent(int64_t tokens, int64_t stride, int64_t row) {
+  return cut(((double)(tokens - 1) * (double)stride + (double)row) * 2.0);
+}
+// Elements between 16-bit rows: not negative, whole 16 bytes, within 2^40.
+bool good_stride(int64_t st) { return st >= 0 && st <= (int64_t)1 << 40 && st % 8 == 0; }
 
 int check_cache(const keops_cache_t *c, bool scales = true) {
   if (!c) return KEOPS_ERR_INVALID_ARG;
@@ -50,7 +62,7 @@ int check_cache(const keops_cache_t *c, bool scales = true) {
   if (c->pages > 0 && (!c->k_pages || !c->v_pages)) return KEOPS_ERR_INVALID_ARG;
   const int64_t w = width_of(c->type);
   for (int64_t st : {c->page_stride, c->slot_stride, c->head_stride})
-    if (st < 0 || st > (int64_t)1 << 48 || st * w % 16) return KEOPS_ERR_INVALID_ARG;
+    if (st < 0 || st > (int64_t)1 << 40 || st * w % 16) return KEOPS_ERR_INVALID_ARG;
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return KEOPS_ERR_INVALID_ARG;
   for (const void *p : {(const void *)c->weights, (const void *)c->k_scale, (const void *)c->v_scale,
                         (const void *)c->page_table, (const void *)c->lens})
@@ -208,13 +220,12 @@ int append_entry(const keops_cache_t *c, const void *k, const void *v, int64_t k
   if (c->type != KEOPS_TYPE_E4M3 && c->type != type) return KEOPS_ERR_INVALID_ARG;
   if (tokens < 0) return KEOPS_ERR_INVALID_ARG;
   const int64_t row = (int64_t)c->heads * c->dim;
-  if (tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16) || k_stride * 2 % 16 || v_stride * 2 % 16 ||
-                     k_stride < 0 || v_stride < 0 || k_stride > (int64_t)1 << 40 || v_stride > (int64_t)1 << 40))
+  if (tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !good_stride(k_stride) || !good_stride(v_stride)))
     return KEOPS_ERR_INVALID_ARG;
   if (tokens > 0 && c->seqs > 0 && (!starts || !aligned(starts, 4))) return KEOPS_ERR_INVALID_ARG;
   if (tokens > 0x7fffffff || (double)tokens * (double)(row / 8) > 256.0 * (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
   if (tokens > 0) {
-    const int64_t kb = ((tokens - 1) * k_stride + row) * 2, vb = ((tokens - 1) * v_stride + row) * 2;
+    const int64_t kb = rows_extent(tokens, k_stride, row), vb = rows_extent(tokens, v_stride, row);
     const int64_t pb = pages_extent(*c);
     for (const void *p : {(const void *)c->k_pages, (const void *)c->v_pages})
       if (overlaps(p, pb, k, kb) || overlaps(p, pb, v, vb)) return KEOPS_ERR_INVALID_ARG;
@@ -239,11 +250,10 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   if (int rc = check_attend(c, type, tokens, heads, max_q, max_len, scale, window, decay)) return rc;
   const int64_t row = (int64_t)heads * c->dim;
   if (tokens > 0) {
-    if (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || q_stride < 0 ||
-        q_stride * 2 % 16 || q_stride > (int64_t)1 << 40)
+    if (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !good_stride(q_stride))
       return KEOPS_ERR_INVALID_ARG;
     if (c->seqs > 0 && (!starts || !aligned(starts, 4))) return KEOPS_ERR_INVALID_ARG;
-    const int64_t ob = tokens * row * 2, lb = tokens * heads * 4, qb = ((tokens - 1) * q_stride + row) * 2;
+    const int64_t ob = tokens * row * 2, lb = tokens * heads * 4, qb = rows_extent(tokens, q_stride, row);
     const int64_t pb = pages_extent(*c), wb = weights_extent(*c);
     if (overlaps(out, ob, q, qb) || overlaps(out, ob, lse, lb) || overlaps(lse, lb, q, qb) ||
         overlaps(out, ob, c->k_pages, pb) || overlaps(out, ob, c->v_pages, pb) || overlaps(out, ob, c->weights, wb) ||
@@ -311,7 +321,7 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
     if (new_width > 0 && (!new_table || !aligned(new_table, 4))) return KEOPS_ERR_INVALID_ARG;
     // every kept slot has a place in the new table
     if (new_width < std::min<int64_t>(ceil_div(budget, c->page_size), c->table_width)) return KEOPS_ERR_INVALID_ARG;
-    const int64_t kb = (int64_t)c->seqs * c->heads * budget * 4, nb = (int64_t)c->seqs * 4;
+    const int64_t kb = cut((double)c->seqs * c->heads * (double)budget * 4.0), nb = (int64_t)c->seqs * 4;
     const int64_t pb = pages_extent(*c), wb = weights_extent(*c);
     if (overlaps(kept, kb, new_lens, nb) || overlaps(kept, kb, c->lens, nb) || overlaps(new_lens, nb, c->lens, nb) ||
         overlaps(kept, kb, c->weights, wb) || overlaps(kept, kb, c->k_pages, pb) || overlaps(kept, kb, c->v_pages, pb))
