@@ -82,6 +82,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   __shared__ __align__(16) uint16_t sv[kBufs][KT * D];
   __shared__ int64_t off[2][kChunk * KT];
   __shared__ uint64_t present[2][kChunk];              // which of a tile's slots are there
+  __shared__ int sh_odd;                               // a wave cleared non-finite values for all
 
   const int H = a.c.heads, G = a.group;
   const int64_t heads = (int64_t)H * G;
@@ -214,7 +215,6 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     }
   };
 
-  bool odd = false;
   // One tile.  masked: some row may not see some slot of it.
   const auto step = [&](bool masked, int buf, int tile, uint64_t there) {
     const int j0 = lo + tile * KT;
@@ -272,7 +272,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
 
     if (masked) {
       // V of absent slots is cleared, and non-finite values of slots that some rows see and others do
-      // not wait for the end; each wave clears for itself before it reads the tile
+      // not wait for the end; each wave clears before it reads the tile, and may find it done
+      bool odd = false;
       for (int i = lane; i < KT * kPieces; i += 64) {
         const int u = i / kPieces, j = j0 + u;
         if (!((there >> u) & 1u)) {
@@ -286,6 +287,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
           ((u32x4 *)sv[buf])[i] = x;
         }
       }
+      if (odd) sh_odd = 1;
     }
     // V^T operand of slots 16 ks .. of sub-tile t, columns 32 n ..: two transposing reads
 #pragma unroll
@@ -318,6 +320,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     __syncthreads();
   };
   if (tiles > 0) {
+    if (tid == 0) sh_odd = 0;
     page_load(0);
     page_put(0);
     page_load(1);
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     __syncthreads();
   }
   for (int tile = 0; tile < tiles; ++tile) turn(tile % kBufs, tile);
-  if (__any(odd)) {
+  if (tiles > 0 && sh_odd) {
     // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
     const int stop = lo + tiles * KT < end ? lo + tiles * KT : end;
     for (int j = lo; j < stop; ++j) {

@@ -695,3 +695,32 @@ def test_example_decodes():
     text = ex.decode(rounds=40, watch=watch)
     assert rounds[0] == 40 and all(40 <= len(t) <= 160 for t in text)
     assert ex.decode(rounds=10) == [t[:len(u)] for t, u in zip(text, ex.decode(rounds=10))]
+
+
+@pytest.mark.parametrize("late", [0, 1, 2, 3])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_nonfinite_value_reaches_every_row_that_sees_it(dim, late):
+    """128 rows of one tile, 32 for each wave; the rows of one wave meet a new largest score in the tile that holds
+    an infinity and a NaN, so that it is behind the others there."""
+    say(f"non-finite values for every row that sees them, dim {dim}, wave {late} late")
+    b = ref.Batch(21, [96], [32], 4, 1, dim, 16)
+    b.q.zero_()
+    b.q[8 * late:8 * late + 8, :, 0] = 16.0
+
+    def spot(j):
+        return b.table[0, j // 16].item(), j % 16
+    for j in range(96):
+        pg, row = spot(j)
+        b.k[pg, row, 0, 0] = 1.0 if j < 64 else 64.0
+    for j, col, value in ((65, 3, float("inf")), (66, 7, float("nan"))):
+        pg, row = spot(j)
+        b.v[pg, row, 0, col] = value
+    out, lse, _ = run_attention(b)
+    o, z, _, ot, zt, _ = ref.attention(b)
+    close(lse, z, zt, "lse")
+    for t in range(32):
+        # slot 65 is seen from token 1 on, slot 66 from token 2
+        assert bool((out[t, :, 3] == float("inf")).all()) == (t >= 1), t
+        assert bool(out[t, :, 7].isnan().all()) == (t >= 2), t
+    rest = [c for c in range(dim) if c not in (3, 7)]
+    close(out[..., rest], o[..., rest], ot[..., rest], "out")
