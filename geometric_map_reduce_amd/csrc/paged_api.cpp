@@ -329,6 +329,7 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
   }
   if ((double)c->seqs * c->heads * (double)budget * (c->dim * width_of(c->type) / 16) > 256.0 * (double)kMaxGrid ||
       (double)c->table_width * (double)c->page_size > (double)kMaxSlots ||
+      (double)c->seqs * c->heads > (double)kMaxGrid ||
       (double)c->pages * c->heads * (double)c->page_size > 4294967295.0)       // the selection's 32-bit weight numbers
     return KEOPS_ERR_UNSUPPORTED;
   if (c->seqs == 0) return KEOPS_OK;

@@ -149,3 +149,9 @@ def test_binding_refuses_host_tensors():
         gm.keops_verify_draft(None, None, None, None, None, None)
     with pytest.raises(ValueError, match="target"):
         gm.keops_verify_draft(torch.zeros((1, 2, 8)), None, torch.zeros((1, 1), dtype=torch.int32), None, None, None)
+
+
+def test_evict_refuses_more_heads_of_sequences_than_a_grid_has(L):
+    far = dict(k_pages=1 << 51, v_pages=1 << 52, weights=1 << 53)
+    c = cache(seqs=40000, heads=65535, pages=10, page_size=1, table_width=1, **far)
+    assert call_evict(L, c, budget=1, sink=0, recent=0, kept=1 << 54, lens=1 << 55) == -2
