@@ -23,6 +23,10 @@ LIB = os.path.join(HERE, "libkeops_mi355x.so")
 MICRO_SRC = os.path.join(HERE, "micro", "rates.hip")
 MICRO_LIB = os.path.join(HERE, "libkeops_micro.so")
 
+# the short way from torch tensors to LIB's paged-cache calls: a Python module, host code only
+CALL_SRC = os.path.join(HERE, "native", "paged_call.cpp")
+CALL_LIB = os.path.join(HERE, "_paged_call.so")
+
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CFLAGS = [
@@ -84,6 +88,9 @@ def build(jobs: int | None = None, verbose: bool = False, incremental: bool = Fa
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
     build_micro()
+    if not incremental or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < max(
+            os.path.getmtime(p) for p in (CALL_SRC, os.path.join(INCLUDE, "keops_mi355x.h"))):
+        build_call()
     return LIB
 
 
@@ -95,6 +102,26 @@ def build_micro() -> str:
         raise RuntimeError(f"hipcc failed for {MICRO_SRC}:\n{res.stderr}")
     os.replace(tmp, MICRO_LIB)
     return MICRO_LIB
+
+
+def build_call() -> str:
+    """Compile the Python module of the paged-cache calls; it finds LIB next to itself."""
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALL_LIB + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE]
+    for p in include_paths():
+        cmd += ["-isystem", p]
+    cmd += ["-Wall", CALL_SRC, "-o", tmp, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", HERE,
+            "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALL_SRC}:\n{res.stderr}")
+    os.replace(tmp, CALL_LIB)
+    return CALL_LIB
 
 
 if __name__ == "__main__":

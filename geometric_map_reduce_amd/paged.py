@@ -7,16 +7,21 @@ A cache is a pair of page pools ``k_pages``, ``v_pages`` of shape [pages, page_s
 attention that each slot received.  ``page_table`` [sequences, width], ``lens`` [sequences] and
 ``starts`` [sequences + 1] are int32 tensors on the same device; the calls read none of them on
 the host and never synchronise.
+
+Each call first goes the short way (native/paged_call.cpp), which takes plain arguments on the
+current stream in a microsecond or two and hands back, undone, whatever is anything else; that is
+taken, or refused by name, here.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import os
 import struct
 
 import torch
 
-from .binding import _check, _out, _raw_stream, _stream, lib
+from .binding import LIB_PATH, _check, _out, _raw_stream, _stream, lib
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
@@ -89,6 +94,25 @@ def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales
     return c, dev, S, (H, D, dtype), ps, width
 
 
+_short = None
+
+
+def _native():
+    """The short way's module; nothing before the library is built, which the long way reports."""
+    global _short
+    if not os.path.exists(LIB_PATH):
+        return None
+    lib()
+    try:
+        from . import _paged_call
+    except ImportError as e:
+        raise RuntimeError("the paged calls' module is missing or broken: build it first "
+                           "(python -m geometric_map_reduce_amd.build)") from e
+    _paged_call.bind(_raw_stream)
+    _short = _paged_call
+    return _short
+
+
 _HALF = (torch.bfloat16, torch.float16)
 
 
@@ -148,6 +172,10 @@ def keops_cache_append(k, v, k_pages, v_pages, page_table, lens, starts, weights
                        stream=None):
     """Write rows starts[s] .. starts[s+1] of k and v [tokens, heads, dim] to the last slots of sequence s
     (``lens`` counts them already); clear those slots' ``weights``."""
+    if stream is None:
+        short = _short or _native()
+        if short and short.append(k, v, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts):
+            return
     c, dev, S, cache, _, _ = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
     kp, ks = _rows(k, "k", cache[0], cache, dev)
     vp, vs = _rows(v, "v", cache[0], cache, dev)
@@ -165,6 +193,12 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     ``max_q`` and ``max_len`` bound the new tokens and the slots of any sequence; ``scale`` is
     1 / sqrt(dim) unless given; ``window`` > 0 limits a token to that many slots, its own included.
     With ``weights``, every slot's becomes decay * old + the attention it received in this call."""
+    if stream is None:
+        short = _short or _native()
+        got = short and short.attention(q, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts, max_q, max_len,
+                                        scale, window, decay, out, lse)
+        if got:
+            return got
     c, dev, S, cache, _, _ = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
     qp, qs = _rows(q, "q", None, cache, dev)
     T, heads, D = q.shape
@@ -192,6 +226,12 @@ def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, bu
     """Keep ``budget`` slots of every sequence and head: the first ``sink``, the last ``recent``, and those with
     the largest weights; move them to the pages of ``new_table``.  Returns (kept [sequences, heads, budget]
     old slot numbers or -1, new lens).  The scales of an 8-bit cache are not needed."""
+    if stream is None:
+        short = _short or _native()
+        got = short and short.evict(k_pages, v_pages, weights, page_table, lens, None, None, new_table, budget, sink, recent, kept,
+                                    new_lens)
+        if got:
+            return got
     c, dev, S, (H, _, _), ps, width = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
     if weights is None:
         raise ValueError("eviction needs weights")
@@ -216,6 +256,11 @@ def keops_verify_draft(target, draft, tokens, counts, u_accept, u_sample, out=No
     """Drafted ``tokens`` [sequences, drafts] (the first counts[s] of them) against the target's probabilities
     [sequences, drafts + 1, vocab] and the draft's [sequences, drafts, vocab] (None: certain), with given uniform
     numbers.  Returns (tokens [sequences, drafts + 1]: taken, then the new one, then -1; accepted [sequences])."""
+    if stream is None:
+        short = _short or _native()
+        got = short and short.verify(target, draft, tokens, counts, u_accept, u_sample, out, accepted)
+        if got:
+            return got
     _tensor(target, "target"), _tensor(tokens, "tokens")
     dev = target.get_device()
     if target.dim() != 3 or dev < 0 or tokens.dim() != 2:

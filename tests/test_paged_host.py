@@ -155,3 +155,22 @@ def test_evict_refuses_more_heads_of_sequences_than_a_grid_has(L):
     far = dict(k_pages=1 << 51, v_pages=1 << 52, weights=1 << 53)
     c = cache(seqs=40000, heads=65535, pages=10, page_size=1, table_width=1, **far)
     assert call_evict(L, c, budget=1, sink=0, recent=0, kept=1 << 54, lens=1 << 55) == -2
+
+
+def test_short_way_hands_back_what_it_does_not_take(L):
+    """Nothing that is no plain tensor on the current device is taken, and no argument raises or ends the process."""
+    from geometric_map_reduce_amd import paged
+    short = paged._native()
+    x, i = torch.zeros((1, 2, 64), dtype=torch.bfloat16), torch.zeros((2,), dtype=torch.int32)
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    good = [x, x, k, k, None, i[None], i[:1], None, None, i]
+    for at in range(len(good)):
+        for bad in (None, 3, "k", [x], object(), torch.nn.Parameter(x), x.to("meta"), torch.zeros((0,)), i):
+            a = list(good)
+            a[at] = bad
+            assert short.append(*a) is None
+            assert short.attention(a[0], *a[2:], 1, 16, None, 0, 0.0, None, None) is None
+            assert short.evict(*a[2:8], None, i[None], 4, 0, 0, None, None) is None
+            assert short.verify(*a[:6], None, None) is None
+    assert short.append() is None and short.append(*good, 1) is None and short.attention(*good) is None
+    assert short.evict() is None and short.verify() is None
