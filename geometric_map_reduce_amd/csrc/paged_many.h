@@ -118,6 +118,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
   const bool real = r < R;
   const int pos = real ? sp.first + tok : -1;
+  const bool idle = row0 + wave * 32 >= R;           // a wave without rows only fetches
   // scores are compared before they are scaled: a negative factor's sign goes to Q, a zero one's
   // scores are zeros
   const float c0 = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
@@ -311,7 +312,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     const uint64_t there = present[(tile / kChunk) & 1][tile % kChunk];
     const bool masked = there != ~(uint64_t)0 || j0 + KT - 1 > first_pos ||
                         (a.window > 0 && j0 <= last_pos - a.window);
-    step(masked, buf, tile, there);
+    if (!idle) step(masked, buf, tile, there);
     if (tile % kChunk == 0 && tile + kChunk < tiles) {      // a chunk ahead of the first fetch from it
       page_put(tile / kChunk + 1);
       page_load(tile / kChunk + 2);
@@ -412,11 +413,12 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
   const SeqSpan sp = seq_span(a.starts, a.c.lens, s, a.tokens, a.max_q, a.max_len);
   const int slot0 = st * kSumSlotsTile;
   if (slot0 >= sp.n) return;
+  const int wave0 = slot0 + wave * 64;               // the wave's slots
   int j[2];
   SlotPlace pl[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    j[x] = slot0 + wave * 64 + x * 32 + col;
+    j[x] = wave0 + x * 32 + col;
     pl[x] = SlotPlace{-1, 0};
     if (j[x] < sp.n) pl[x] = slot_place(a.c, a.c.table + (int64_t)s * a.c.table_stride, (uint32_t)j[x]);
   }
@@ -494,10 +496,13 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
     // slots of the first and last row of the tile
     const int ra = r0 + tile * QT, rb = ra + QT < r1 ? ra + QT - 1 : r1 - 1;
     const int pa = sp.first + (int)fast_div(a.gdiv, (uint32_t)ra), pb = sp.first + (int)fast_div(a.gdiv, (uint32_t)rb);
-    const bool masked = slot0 + kSumSlotsTile - 1 > pa || (a.window > 0 && slot0 <= pb - a.window);
+    // of the wave's own 64 slots: none that a row of the tile sees, or some that some row does not see
+    const bool none = wave0 > pb || (a.window > 0 && wave0 + 63 <= pa - a.window);
+    const bool masked = wave0 + 63 > pa || (a.window > 0 && wave0 <= pb - a.window);
     float part[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < QT / 32; ++t) {
+      if (none) break;
       f32x16 sc[2];
 #pragma unroll
       for (int u = 0; u < 16; ++u) sc[0][u] = sc[1][u] = 0.0f;
