@@ -5,16 +5,18 @@
 // slot).  Kept slots move, in their order, to slots 0 .. of the pages in new_table, keys,
 // values and weights alike; n <= budget keeps them all.
 //
-// Selection: one work-group per (sequence, head) holds up to 32,768 weights in registers as whole
-// numbers of the same order (longer rows are read again for each pass) and finds the smallest kept
-// one by up to three passes over 11, 11 and 10 bits, with counts in LDS (whole numbers, so the order
-// of the additions does not matter).  Once no more than 64 keys share the digits found, they are
-// ranked by weight and slot instead.  Every slot's place then comes from the counts of the waves before it.
-// Latency bounds it: a thread loads all its page numbers and then all its weights, and 512 keys of
-// a wave that all meet one count add to it once (cleared weights are all equal).  64 rows of 32,000
-// slots take 45 us, 21 of them for the loads (128 KB by each of 64 compute units), 32 rows of 1,025
-// slots 9 us.  The move is a second kernel, one 16-byte piece of a key and of a value row per
-// thread, bound by HBM: 268 MB read and written in 50 us.
+// Selection: one work-group per (sequence, head) holds up to 32,768 weights in LDS as whole numbers of
+// the same order (longer rows are read again for each pass) and finds the smallest kept one by up to
+// three passes over 11, 11 and 10 bits, with counts in LDS (whole numbers, so the order of the additions
+// does not matter).  Once no more than 64 keys share the digits found, they are ranked by weight and
+// slot instead.  Every slot's place then comes from the counts of the waves before it.
+// A thread has four slots in a row: one page number and one 16-byte load where pages are whole aligned
+// quadruples, slot by slot otherwise.  Latency bounds it: all page numbers and then all weights are
+// loaded at once, and 256 keys of a wave that all meet one count add to it once (cleared weights are all
+// equal).  64 rows of up to 32,768 slots take 30 us, 32 rows of 1,025 slots 12 us.  With the keys in
+// registers the loops over them had to be unrolled, 43 KB of code, and took 32 us (43 us with a slot at
+// a time).  The move is a second kernel, one 16-byte piece of a key and of a value row per thread, bound
+// by HBM: 268 MB read and written in 50 us.
 #include "paged.h"
 
 namespace kmi {
@@ -25,8 +27,9 @@ constexpr int kSelectWaves = kSelectThreads / kWave;
 constexpr int kBins = 2048;             // counts of a pass
 constexpr int kHistCopies = 2;          // even and odd lanes: fewer collisions
 constexpr int kHistStride = kBins + 32; // a bin's copies lie in different banks
-constexpr int kHeldMost = 32;           // keys of a thread, and for short rows: the loops over them
-constexpr int kHeldFew = 4;             // are unrolled, and code that runs once is paid for by its size
+constexpr int kQuad = 4;                // slots in a row of a thread
+constexpr int kGroup = kQuad * kSelectThreads;
+constexpr int kGroupsFew = 1, kGroupsMost = 8;   // groups of keys in LDS: 16 and 128 KB
 
 // Whole numbers ordered as the floats are; -0 equals 0, NaN above everything.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -35,10 +38,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-template <int kHeld>
+template <int kGroups>
 struct SelectShared {
+  __align__(16) uint32_t key[kGroups * kGroup];
   __align__(16) uint32_t hist[kHistStride * kHistCopies];
-  uint32_t place[kHeld * kSelectWaves];  // kept before each 64 slots, two counts in one word
+  uint32_t place[kGroups * kSelectWaves];   // kept before a wave's quadruples of a group
   __align__(16) uint32_t wave_sum[kSelectWaves];
   uint32_t prefix, need, count;
   uint32_t cand_key[kWave], cand_slot[kWave], cand_rank[kWave], cands;
@@ -69,10 +73,10 @@ __device__ __forceinline__ uint32_t scan_u32(uint32_t v, int lane) {
   return v;
 }
 
-template <int kHeld>
+template <int kGroups>
 __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
-  constexpr int kBatch = kHeld < 8 ? kHeld : 8, kSegment = kHeld * kSelectThreads;
-  __shared__ SelectShared<kHeld> sh;
+  constexpr int kSegment = kGroups * kGroup;
+  __shared__ SelectShared<kGroups> sh;
   const int H = a.c.heads;
   const int s = blockIdx.x / H, h = blockIdx.x - s * H;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -87,52 +91,68 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     for (int r = tid; r < a.budget; r += kSelectThreads) kept[r] = r < n ? r : -1;
     return;
   }
-  const int sink = a.sink, recent = a.recent, M = n - sink - recent, need0 = a.budget - sink - recent;
+  const int sink = a.sink, recent = a.recent, need0 = a.budget - sink - recent;
   for (int r = tid; r < sink; r += kSelectThreads) kept[r] = r;
   for (int r = tid; r < recent; r += kSelectThreads) kept[a.budget - recent + r] = n - recent + r;
   if (need0 == 0) return;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
+  // the slots in question, counted from `base0`: skip .. M - 1
+  const int base0 = sink / kQuad * kQuad, skip = sink - base0, M = n - recent - base0;
   const int segments = (M + kSegment - 1) / kSegment;
-  // keys of slots segment + tid + 1024 u: an absent slot's is 0, the least.  Page and row go on
-  // by 1024 slots with an addition each.
-  uint32_t key[kHeld];
-  const uint32_t ps = a.c.page.d, step_page = kSelectThreads / ps, step_row = kSelectThreads - step_page * ps;
+  const auto live = [&](int i) { return i >= skip && i < M; };
+  // groups of a segment that hold any
+  const auto groups_of = [&](int from) {
+    const int left = (M - from + kGroup - 1) / kGroup;
+    return left < kGroups ? left : kGroups;
+  };
+  // keys of a segment to LDS, each thread its own quadruples; an absent slot's is 0, the least
+  const uint32_t ps = a.c.page.d;
+  const bool whole = ps % kQuad == 0 && ((uintptr_t)a.c.weights & 15) == 0;   // a quadruple in one page, aligned
   const auto load = [&](int from) {
-    const uint32_t j0 = (uint32_t)(sink + from + tid);
-    uint32_t pi = fast_div(a.c.page, j0), row = j0 - pi * ps;
-    uint32_t rows = row;
+    const int groups = groups_of(from);
+    if (whole) {
+      // page and row go on by a group's slots with an addition each
+      const uint32_t j0 = (uint32_t)(base0 + from + tid * kQuad), step_page = kGroup / ps, step_row = kGroup - step_page * ps;
+      uint32_t pi = fast_div(a.c.page, j0), row = j0 - pi * ps, page[kGroups], rows = row;
 #pragma unroll
-    for (int b = 0; b < kHeld; b += kBatch) {
-      if (from + b * kSelectThreads < M) {
-#pragma unroll
-        for (int u = b; u < b + kBatch; ++u) {
-          int32_t pg = -1;
-          if (pi < a.c.table_width && from + u * kSelectThreads + tid < M) pg = trow[pi];
-          key[u] = (uint32_t)pg;
-          pi += step_page;
-          row += step_row;
-          if (row >= ps) { row -= ps; ++pi; }
-        }
+      for (int g = 0; g < kGroups; ++g) {
+        int32_t pg = -1;
+        if (pi < a.c.table_width && from + g * kGroup + tid * kQuad < M) pg = trow[pi];
+        page[g] = (uint32_t)pg;
+        pi += step_page;
+        row += step_row;
+        if (row >= ps) { row -= ps; ++pi; }
       }
+      f32x4 w[kGroups];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        w[g] = (f32x4){0, 0, 0, 0};
+        // its number is below 2^32: the caller sees to it
+        if (page[g] < a.c.pages) w[g] = *(const f32x4 *)(a.c.weights + ((page[g] * (uint32_t)H + (uint32_t)h) * ps + rows));
+        rows += step_row;
+        if (rows >= ps) rows -= ps;
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if (g >= groups) break;
+        u32x4 k = (u32x4){0, 0, 0, 0};
+        if (page[g] < a.c.pages)
+          k = (u32x4){weight_key(w[g][0]), weight_key(w[g][1]), weight_key(w[g][2]), weight_key(w[g][3])};
+        ((u32x4 *)sh.key)[g * kSelectThreads + tid] = k;
+      }
+      return;
     }
+#pragma unroll 2
+    for (int g = 0; g < groups; ++g) {
+      u32x4 k = (u32x4){0, 0, 0, 0};
 #pragma unroll
-    for (int b = 0; b < kHeld; b += kBatch) {
-      if (from + b * kSelectThreads < M) {
-        float w[kBatch];
-        bool there[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          // below 2^32: the caller sees to it
-          const uint32_t at = (key[b + u] * (uint32_t)H + (uint32_t)h) * ps + rows;
-          there[u] = key[b + u] < a.c.pages;
-          w[u] = 0.0f;
-          if (there[u]) w[u] = a.c.weights[at];
-          rows += step_row;
-          if (rows >= ps) rows -= ps;
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) key[b + u] = there[u] ? weight_key(w[u]) : 0u;
+      for (int e = 0; e < kQuad; ++e) {
+        const int i = from + g * kGroup + tid * kQuad + e;
+        if (i >= M) continue;
+        const SlotPlace p = slot_place(a.c, trow, (uint32_t)(base0 + i));
+        if (p.page >= 0) k[e] = weight_key(a.c.weights[((uint32_t)p.page * (uint32_t)H + (uint32_t)h) * ps + p.row]);
       }
+      ((u32x4 *)sh.key)[g * kSelectThreads + tid] = k;
     }
   };
 
@@ -148,25 +168,25 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
 #pragma unroll 1
     for (int from = 0; from < M; from += kSegment) {
       if (pass == 0 || segments > 1) load(from);
+      const int groups = groups_of(from);
+      for (int g = 0; g < groups; ++g) {
+        const u32x4 k = ((const u32x4 *)sh.key)[g * kSelectThreads + tid];
+        const int i = from + g * kGroup + tid * kQuad;
+        uint32_t bin[kQuad];
+        bool in[kQuad], same = true;
 #pragma unroll
-      for (int b = 0; b < kHeld; b += kBatch) {
-        if (from + b * kSelectThreads >= M) continue;
-        uint32_t bin[kBatch];
-        bool in[kBatch], same = true;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          in[u] = from + (b + u) * kSelectThreads + tid < M &&
-                  (pass == 0 || (key[b + u] >> (shift + bits)) == (prefix >> (shift + bits)));
-          bin[u] = (key[b + u] >> shift) & ((1u << bits) - 1u);
-          same &= in[u] && bin[u] == (uint32_t)__builtin_amdgcn_readfirstlane(bin[0]);
+        for (int e = 0; e < kQuad; ++e) {
+          in[e] = live(i + e) && (pass == 0 || (k[e] >> (shift + bits)) == (prefix >> (shift + bits)));
+          bin[e] = (k[e] >> shift) & ((1u << bits) - 1u);
+          same &= in[e] && bin[e] == (uint32_t)__builtin_amdgcn_readfirstlane(bin[0]);
         }
         if (__all(same)) {
-          if (lane == 0) atomicAdd(&mine[bin[0]], (uint32_t)(kBatch * kWave));
+          if (lane == 0) atomicAdd(&mine[bin[0]], (uint32_t)(kQuad * kWave));
           continue;
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (in[u]) atomicAdd(&mine[bin[u]], 1u);
+        for (int e = 0; e < kQuad; ++e)
+          if (in[e]) atomicAdd(&mine[bin[e]], 1u);
       }
     }
     __syncthreads();
@@ -200,16 +220,16 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     if (count == need) break;          // all that share the digits so far are kept
     if (count <= kWave && segments == 1) {
       // few share them: they are ranked by weight and slot, each wave against a part of them
+      const int groups = groups_of(0);
+      for (int g = 0; g < groups; ++g) {
+        const u32x4 k = ((const u32x4 *)sh.key)[g * kSelectThreads + tid];
+        const int i = g * kGroup + tid * kQuad;
 #pragma unroll
-      for (int b = 0; b < kHeld; b += kBatch) {
-        if (b * kSelectThreads < M) {
-#pragma unroll
-          for (int u = b; u < b + kBatch; ++u) {
-            if (u * kSelectThreads + tid < M && (key[u] >> shift) == (prefix >> shift)) {
-              const uint32_t at = atomicAdd(&sh.cands, 1u);
-              sh.cand_key[at] = key[u];
-              sh.cand_slot[at] = (uint32_t)(u * kSelectThreads + tid);
-            }
+        for (int e = 0; e < kQuad; ++e) {
+          if (live(i + e) && (k[e] >> shift) == (prefix >> shift)) {
+            const uint32_t at = atomicAdd(&sh.cands, 1u);
+            sh.cand_key[at] = k[e];
+            sh.cand_slot[at] = (uint32_t)(i + e);
           }
         }
       }
@@ -243,45 +263,44 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
 #pragma unroll 1
     for (int from = 0; from < M; from += kSegment) {
       if (segments > 1) load(from);
-      uint32_t counts = 0;             // lane u counts the wave's 64 slots of step u
-      uint32_t mine = 0;               // and this thread's keep as bits
+      const int groups = groups_of(from);
+      uint32_t mine = 0;               // this thread's slots as bits, four a group
+      for (int g = 0; g < groups; ++g) {
+        const u32x4 k = ((const u32x4 *)sh.key)[g * kSelectThreads + tid];
+        const int i = from + g * kGroup + tid * kQuad;
+        uint32_t c = 0;
 #pragma unroll
-      for (int b = 0; b < kHeld; b += kBatch) {
-        if (from + b * kSelectThreads < M) {
-#pragma unroll
-          for (int u = b; u < b + kBatch; ++u) {
-            const uint32_t i = (uint32_t)(from + u * kSelectThreads + tid);
-            const bool eq = key[u] == prefix;
-            const bool in = i < (uint32_t)M && (round == 0 ? eq : key[u] > prefix || (eq && i <= cut));
-            const uint32_t c = (uint32_t)__popcll(__ballot(in));
-            mine |= in ? 1u << u : 0u;
-            if (lane == u) counts = c;
-          }
+        for (int e = 0; e < kQuad; ++e) {
+          const bool eq = k[e] == prefix;
+          const bool in = live(i + e) && (round == 0 ? eq : k[e] > prefix || (eq && (uint32_t)(i + e) <= cut));
+          c += (uint32_t)__popcll(__ballot(in));
+          mine |= (in ? 1u : 0u) << (g * kQuad + e);
         }
+        if (lane == 0) sh.place[g * kSelectWaves + wave] = c;
       }
-      if (lane < kHeld) sh.place[lane * kSelectWaves + wave] = counts;
       __syncthreads();
       uint32_t own = 0, total;
-      if (tid < kHeld * kSelectWaves) own = sh.place[tid];
+      if (tid < groups * kSelectWaves) own = sh.place[tid];
       uint32_t upto = scan_u32(own, lane);
       if (lane == kWave - 1) sh.wave_sum[wave] = upto;
       __syncthreads();
       upto += before_wave(sh.wave_sum, wave, &total);
-      if (tid < kHeld * kSelectWaves) sh.place[tid] = upto - own;
+      if (tid < groups * kSelectWaves) sh.place[tid] = upto - own;
       __syncthreads();
       const uint64_t below = ((uint64_t)1 << lane) - 1;
-      if (lane < kHeld) counts = sh.place[lane * kSelectWaves + wave];
+      for (int g = 0; g < groups; ++g) {
+        const uint32_t four = mine >> (g * kQuad);
+        // the lanes before this one, then the thread's own slots in order
+        uint32_t place = base + sh.place[g * kSelectWaves + wave];
 #pragma unroll
-      for (int b = 0; b < kHeld; b += kBatch) {
-        if (from + b * kSelectThreads < M) {
+        for (int e = 0; e < kQuad; ++e) place += __popcll(__ballot((four >> e) & 1u) & below);
 #pragma unroll
-          for (int u = b; u < b + kBatch; ++u) {
-            const bool in = (mine >> u) & 1u;
-            const uint32_t place = base + __builtin_amdgcn_readlane(counts, u) + __popcll(__ballot(in) & below);
-            const int i = from + u * kSelectThreads + tid;
-            if (in && round == 1) kept[sink + place] = sink + i;
-            if (in && round == 0 && place == need - 1) sh.cut_slot = (uint32_t)i;
-          }
+        for (int e = 0; e < kQuad; ++e) {
+          const bool in = (four >> e) & 1u;
+          const int i = from + g * kGroup + tid * kQuad + e;
+          if (in && round == 1) kept[sink + place] = base0 + i;
+          if (in && round == 0 && place == need - 1) sh.cut_slot = (uint32_t)i;
+          place += in;
         }
       }
       base += total;
@@ -323,10 +342,10 @@ __global__ __launch_bounds__(256) void move_kernel(EvictArgs a, int pieces, int6
 
 void launch_evict(const EvictArgs &a, hipStream_t st) {
   const dim3 grid((unsigned)(a.c.seqs * a.c.heads));
-  if ((int64_t)a.c.table_width * a.c.page.d <= kHeldFew * kSelectThreads)
-    select_kernel<kHeldFew><<<grid, kSelectThreads, 0, st>>>(a);
+  if ((int64_t)a.c.table_width * a.c.page.d <= kGroupsFew * kGroup)
+    select_kernel<kGroupsFew><<<grid, kSelectThreads, 0, st>>>(a);
   else
-    select_kernel<kHeldMost><<<grid, kSelectThreads, 0, st>>>(a);
+    select_kernel<kGroupsMost><<<grid, kSelectThreads, 0, st>>>(a);
   const int pieces = a.c.dim * a.itemsize / 16;
   const int64_t total = (int64_t)a.c.seqs * a.c.heads * a.budget * pieces;
   move_kernel<<<dim3((unsigned)((total + 255) / 256)), 256, 0, st>>>(a, pieces, total);

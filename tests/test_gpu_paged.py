@@ -724,3 +724,31 @@ def test_nonfinite_value_reaches_every_row_that_sees_it(dim, late):
         assert bool(out[t, :, 7].isnan().all()) == (t >= 2), t
     rest = [c for c in range(dim) if c not in (3, 7)]
     close(out[..., rest], o[..., rest], ot[..., rest], "out")
+
+
+@pytest.mark.parametrize("page", [1, 6, 7, 12, 16])
+@pytest.mark.parametrize("n,sink,recent", [(40, 0, 0), (700, 3, 5), (4099, 5, 1), (9000, 1, 77), (33000, 2, 3)])
+def test_evict_pages_and_sinks(page, n, sink, recent):
+    """Quadruples of slots that end inside a page, a sink or the row; weights that are not 16-byte aligned."""
+    say(f"eviction, {n} slots, page {page}, sink {sink}, recent {recent}")
+    budget = max(sink + recent + 1, n // 3)
+    g = torch.Generator().manual_seed(n + page)
+    used, kept_pages = -(-n // page), -(-budget // page)
+    P = used + kept_pages
+    order = torch.randperm(P, generator=g).to(torch.int32)
+    table, new = order[:used][None].clone(), order[used:][None].clone()
+    table[0, used // 2] = -1                                         # a page that is not there
+    store = torch.zeros(P * page + 1, device="cuda")
+    w = store[1:].view(P, 1, page) if page == 16 else torch.zeros((P, 1, page), device="cuda")
+    flat = torch.randint(0, max(2, n // 50), (n,), generator=g).float() + 1
+    j = torch.arange(n)
+    w.copy_(torch.zeros((P, page)).index_put_((order[:used].long()[j // page], j % page), flat).view(P, 1, page))
+    k = torch.randn((P, page, 1, 64), generator=g).to(BF).cuda()
+    v = k.clone()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    kept, new_lens = gm.keops_cache_evict(k, v, w, table.cuda(), lens, new.cuda(), budget, sink=sink, recent=recent)
+    torch.cuda.synchronize()
+    flat[(j // page) == used // 2] = -float("inf")                   # absent: the smallest
+    middle = torch.argsort(-flat[sink:n - recent], stable=True)[:budget - sink - recent] + sink
+    want = torch.cat([j[:sink], middle.sort().values, j[n - recent:]])
+    assert torch.equal(kept[0, 0].cpu().long(), want) and new_lens.item() == budget
