@@ -121,7 +121,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   const int tok = (int)fast_div(a.gdiv, (uint32_t)r), g = r - tok * G;
   const bool real = r < R;
   const int pos = real ? sp.first + tok : -1;
-  const bool idle = row0 + wave * 32 >= R;           // a wave without rows only fetches
+  // a wave without rows only fetches (at D = 256 the branch costs registers: 4,096 tokens after 12,288, 32/8 heads: 2,665 us with it, 2,331 without)
+  const bool idle = D <= 128 && row0 + wave * 32 >= R;
   // scores are compared before they are scaled: a negative factor's sign goes to Q, a zero one's
   // scores are zeros
   const float c0 = E4M3 ? a.scale_log2 * a.c.k_scale[h] : a.scale_log2;
@@ -169,6 +170,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     }
   };
   const auto off_at = [&](int tile) -> const int64_t * { return &off[(tile / kChunk) & 1][tile % kChunk * KT]; };
+
+  const auto there_at = [&](int tile) { return present[(tile / kChunk) & 1][tile % kChunk]; };
 
   // A tile on its way: 16-bit caches go straight to LDS, 8-bit ones by way of registers.
   uint32_t gk[kLoads][2], gv[kLoads][2];
@@ -219,6 +222,21 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     }
   };
 
+  // In a tile with slots that some row does not see: V of absent ones is cleared, and non-finite values of
+  // those that some rows see and others do not wait for the end.  Each thread looks at its own pieces.
+  const auto clear = [&](int buf, int tile, uint64_t there) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = tid + i * kManyThreads, u = id / kPieces, j = lo + tile * KT + u;
+      u32x4 x = ((const u32x4 *)sv[buf])[id];
+      const bool here = (there >> u) & 1u, some = j > first_pos || (a.window > 0 && j <= last_pos - a.window);
+      bool change = !here;
+      if (here && some && clear_nonfinite<T>(x)) odd = change = true;
+      if (change) ((u32x4 *)sv[buf])[id] = keep_if(x, here);
+    }
+    if (odd) sh_odd = 1;
+  };
   // One tile.  masked: some row may not see some slot of it.
   const auto step = [&](bool masked, int buf, int tile, uint64_t there) {
     const int j0 = lo + tile * KT;
@@ -274,25 +292,6 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
       }
     l_run += sum;
 
-    if (masked) {
-      // V of absent slots is cleared, and non-finite values of slots that some rows see and others do
-      // not wait for the end; each wave clears before it reads the tile, and may find it done
-      bool odd = false;
-      for (int i = lane; i < KT * kPieces; i += 64) {
-        const int u = i / kPieces, j = j0 + u;
-        if (!((there >> u) & 1u)) {
-          ((u32x4 *)sv[buf])[i] = (u32x4){0, 0, 0, 0};
-          continue;
-        }
-        if (!(j > first_pos || (a.window > 0 && j <= last_pos - a.window))) continue;
-        u32x4 x = ((const u32x4 *)sv[buf])[i];
-        if (clear_nonfinite<T>(x)) {
-          odd = true;
-          ((u32x4 *)sv[buf])[i] = x;
-        }
-      }
-      if (odd) sh_odd = 1;
-    }
     // V^T operand of slots 16 ks .. of sub-tile t, columns 32 n ..: two transposing reads
 #pragma unroll
     for (int t = 0; t < kSub; ++t)
@@ -309,12 +308,18 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
           acc[n] = T::mfma32((u32x4){ub.x, ub.y, wb.x, wb.y}, pf[t][ks], acc[n]);
         }
   };
+  uint64_t there_next = 0;
   const auto turn = [&](int buf, int tile) {
     if (tile + kBufs - 1 < tiles) fetch(tile + kBufs - 1);
     const int j0 = lo + tile * KT;
-    const uint64_t there = present[(tile / kChunk) & 1][tile % kChunk];
+    const uint64_t there = there_next;
+    there_next = there_at(tile + 1);
     const bool masked = there != ~(uint64_t)0 || j0 + KT - 1 > first_pos ||
                         (a.window > 0 && j0 <= last_pos - a.window);
+    if (masked) {
+      clear(buf, tile, there);
+      __syncthreads();
+    }
     if (!idle) step(masked, buf, tile, there);
     if (tile % kChunk == 0 && tile + kChunk < tiles) {      // a chunk ahead of the first fetch from it
       page_put(tile / kChunk + 1);
@@ -333,6 +338,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     arrive(0);
     __syncthreads();
   }
+  if (tiles > 0) there_next = there_at(0);
   for (int tile = 0; tile < tiles; ++tile) turn(tile % kBufs, tile);
   if (tiles > 0 && sh_odd) {
     // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
