@@ -59,6 +59,37 @@ __device__ __forceinline__ int64_t place_offset(const CacheView &c, SlotPlace p)
 // Slots of a sequence at most: sums of a slot, a window and a tile stay in 32 bits.
 constexpr int32_t kMaxSlots = 1 << 30;
 
+// Lane l takes lane l - N's value within its row of 16 (ROW), or lanes of later rows take an earlier row's
+// last; lanes without a source take 0.  Few cycles each, where a shuffle by way of LDS takes some hundred.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
+  v += dpp_u32<0x111, 0xf>(v);       // row_shr 1, 2, 4, 8
+  v += dpp_u32<0x112, 0xf>(v);
+  v += dpp_u32<0x114, 0xf>(v);
+  v += dpp_u32<0x118, 0xf>(v);
+  v += dpp_u32<0x142, 0xa>(v);       // the last of rows 0 and 2 to rows 1 and 3
+  v += dpp_u32<0x143, 0xc>(v);       // the last of row 1 to rows 2 and 3
+  return v;
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp_u32<CTRL, ROWS>((uint32_t)b) | (uint64_t)dpp_u32<CTRL, ROWS>((uint32_t)(b >> 32)) << 32);
+}
+__device__ __forceinline__ double wave_scan_f64(double v) {
+  v += dpp_f64<0x111, 0xf>(v);
+  v += dpp_f64<0x112, 0xf>(v);
+  v += dpp_f64<0x114, 0xf>(v);
+  v += dpp_f64<0x118, 0xf>(v);
+  v += dpp_f64<0x142, 0xa>(v);
+  v += dpp_f64<0x143, 0xc>(v);
+  return v;
+}
+
 // New tokens of a sequence: tokens t0 .. t0 + m of the batch, in slots first .. n of the
 // sequence's n slots.  Values outside the call's bounds are cut to them.
 struct SeqSpan {

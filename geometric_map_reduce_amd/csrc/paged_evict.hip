@@ -13,7 +13,7 @@
 // A thread has four slots in a row: one page number and one 16-byte load where pages are whole aligned
 // quadruples, slot by slot otherwise.  Latency bounds it: all page numbers and then all weights are
 // loaded at once, and 256 keys of a wave that all meet one count add to it once (cleared weights are all
-// equal).  64 rows of up to 32,768 slots take 30 us, 32 rows of 1,025 slots 12 us.  With the keys in
+// equal).  64 rows of up to 32,768 slots take 30 us, 32 rows of 1,025 slots 10 us.  With the keys in
 // registers the loops over them had to be unrolled, 43 KB of code, and took 32 us (43 us with a slot at
 // a time).  The move is a second kernel, one 16-byte piece of a key and of a value row per thread, bound
 // by HBM: 268 MB read and written in 50 us.
@@ -64,15 +64,6 @@ __device__ __forceinline__ uint32_t before_wave(const uint32_t *wave_sum, int wa
   *total = all;
   return before;
 }
-__device__ __forceinline__ uint32_t scan_u32(uint32_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint32_t up = __shfl_up(v, o);
-    if (lane >= o) v += up;
-  }
-  return v;
-}
-
 template <int kGroups>
 __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
   constexpr int kSegment = kGroups * kGroup;
@@ -199,7 +190,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
       cnt[0] += x.y;
       cnt[1] += x.x;
     }
-    const uint32_t own = cnt[0] + cnt[1], upto = scan_u32(own, lane);
+    const uint32_t own = cnt[0] + cnt[1], upto = wave_scan_u32(own);
     if (lane == kWave - 1) sh.wave_sum[wave] = upto;
     __syncthreads();
     uint32_t total;
@@ -281,7 +272,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
       __syncthreads();
       uint32_t own = 0, total;
       if (tid < groups * kSelectWaves) own = sh.place[tid];
-      uint32_t upto = scan_u32(own, lane);
+      uint32_t upto = wave_scan_u32(own);
       if (lane == kWave - 1) sh.wave_sum[wave] = upto;
       __syncthreads();
       upto += before_wave(sh.wave_sum, wave, &total);

@@ -176,74 +176,65 @@ __device__ __forceinline__ FewSpan few_span(const AttendArgs &a, int s) {
   if (f.sp.m == 0) f.tiles = 0;
   return f;
 }
-__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
-  const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint32_t up = __shfl_up(v, o);
-    if (lane >= o) v += up;
-  }
-  return v;
-}
 // All tiles of all sequences and heads in a line, sequence by sequence, head by head, are dealt to
 // the work-groups in equal runs.  Every wave finds out for itself, from the lengths.
 struct FewShare {
   uint32_t share;            // tiles of a work-group
   int s;                     // the sequence that holds tile `at` of the line (seqs: past the end)
   uint32_t base;             // the first of its tiles
+  FewSpan span;              // of that sequence
 };
-__device__ __forceinline__ uint32_t few_total(const AttendArgs &a) {
-  const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
-  uint32_t total = 0;
-  for (int s0 = 0; s0 < S; s0 += kWave) {
-    const uint32_t own = s0 + lane < S ? (uint32_t)(few_span(a, s0 + lane).tiles * a.c.heads) : 0u;
-    total += __shfl(wave_scan_u32(own), kWave - 1);
-  }
-  return total;
-}
 __device__ __forceinline__ uint32_t share_of(uint32_t total, int wgs) {
   const uint32_t share = (total + wgs - 1) / wgs;
   return (share + kFewWaves - 1) / kFewWaves * kFewWaves;      // a tile for every wave
 }
-__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int wg) {
-  const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
-  const uint32_t total = few_total(a);
-  FewShare r{share_of(total, wgs), S, total};
+__device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+// A lane's sequence of 64 from s0 on: its span, and the line's tiles up to it.
+struct FewLine {
+  FewSpan f;
+  uint32_t own, upto;
+};
+__device__ __forceinline__ FewLine few_line(const AttendArgs &a, int s0, uint32_t before) {
+  const int s = s0 + (int)(threadIdx.x & (kWave - 1));
+  FewLine r{};
+  if (s < a.c.seqs) r.f = few_span(a, s);
+  r.own = s < a.c.seqs ? (uint32_t)(r.f.tiles * a.c.heads) : 0u;
+  r.upto = before + wave_scan_u32(r.own);
+  return r;
+}
+// `note`: write down for the second pass where each sequence's tiles begin, and after them the share.
+__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int wg, bool note) {
+  const int S = a.c.seqs, lane = threadIdx.x & (kWave - 1);
+  FewLine line = few_line(a, 0, 0);
+  if (note && lane < S) a.line[lane] = line.upto - line.own;
+  uint32_t total = lane_of(line.upto, kWave - 1);
+  for (int s0 = kWave; s0 < S; s0 += kWave) {
+    const FewLine next = few_line(a, s0, total);
+    if (note && s0 + lane < S) a.line[s0 + lane] = next.upto - next.own;
+    total = lane_of(next.upto, kWave - 1);
+  }
+  FewShare r{share_of(total, wgs), S, total, {}};
+  if (note && lane == 0) a.line[S] = r.share;
   const uint32_t at = (uint32_t)wg * r.share;
-  uint32_t before = 0;
-  for (int s0 = 0; s0 < S; s0 += kWave) {
-    const uint32_t own = s0 + lane < S ? (uint32_t)(few_span(a, s0 + lane).tiles * a.c.heads) : 0u;
-    const uint32_t upto = before + wave_scan_u32(own);
-    const uint64_t who = __ballot(at >= upto - own && at < upto);
+  for (int s0 = 0;;) {
+    const uint64_t who = __ballot(at >= line.upto - line.own && at < line.upto);
     if (who) {
       const int l = __ffsll((unsigned long long)who) - 1;
       r.s = s0 + l;
-      r.base = __shfl(upto - own, l);
+      r.base = lane_of(line.upto - line.own, l);
+      const FewSpan &f = line.f;
+      r.span = FewSpan{{lane_of((int)f.sp.t0, l), lane_of(f.sp.m, l), lane_of(f.sp.n, l), lane_of(f.sp.first, l)},
+                       lane_of(f.lo, l), lane_of(f.hi, l), lane_of(f.tiles, l)};
       break;
     }
-    before = __shfl(upto, kWave - 1);
+    if ((s0 += kWave) >= S) break;
+    line = few_line(a, s0, lane_of(line.upto, kWave - 1));
   }
-  r.s = __builtin_amdgcn_readfirstlane(r.s);
-  r.base = __builtin_amdgcn_readfirstlane(r.base);
-  r.share = __builtin_amdgcn_readfirstlane(r.share);
   return r;
 }
-// The same for the second pass, written down by one wave: where each sequence's tiles begin, and
-// after them the share.
-__device__ __forceinline__ void write_line(const AttendArgs &a, int wgs) {
-  const int lane = threadIdx.x & (kWave - 1), S = a.c.seqs;
-  uint32_t before = 0;
-  for (int s0 = 0; s0 < S; s0 += kWave) {
-    const uint32_t own = s0 + lane < S ? (uint32_t)(few_span(a, s0 + lane).tiles * a.c.heads) : 0u;
-    const uint32_t upto = before + wave_scan_u32(own);
-    if (s0 + lane < S) a.line[s0 + lane] = upto - own;
-    before = __shfl(upto, kWave - 1);
-  }
-  if (lane == 0) a.line[S] = share_of(before, wgs);
-}
 // The work-groups [w0, w1] that share a (sequence, head).
-__device__ __forceinline__ void part_range(const AttendArgs &a, int s, int h, int tiles, int *w0, int *w1) {
-  const uint32_t share = a.line[a.c.seqs], from = a.line[s] + (uint32_t)(h * tiles), to = from + tiles;
+__device__ __forceinline__ void part_range(uint32_t share, uint32_t begin, int h, int tiles, int *w0, int *w1) {
+  const uint32_t from = begin + (uint32_t)(h * tiles), to = from + tiles;
   *w0 = (int)(from / share);
   *w1 = (int)((to - 1) / share);
 }
@@ -276,28 +267,30 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   // this work-group's run of tiles: from tile t0 of (s, h) on
   int s, h, t0;
   uint32_t left;
-  if (!a.whole && blockIdx.x == 0 && wave == 0) write_line(a, gridDim.x);
+  FewSpan span;
   if (a.whole) {
     s = blockIdx.x / H;
     h = blockIdx.x - s * H;
     t0 = 0;
     left = 0xffffffffu;
+    span = few_span(a, s);
   } else {
-    const FewShare my = few_share(a, gridDim.x, blockIdx.x);
+    const FewShare my = few_share(a, gridDim.x, blockIdx.x, blockIdx.x == 0 && wave == 0);
     if (my.s >= a.c.seqs) return;
     s = my.s;
     left = my.share;
-    const int tiles = few_span(a, s).tiles, at = (int)((uint32_t)blockIdx.x * my.share - my.base);
-    h = at / tiles;
-    t0 = at - h * tiles;
+    span = my.span;
+    const int at = (int)((uint32_t)blockIdx.x * my.share - my.base);
+    h = at / span.tiles;
+    t0 = at - h * span.tiles;
   }
   for (;;) {
-  const FewSpan span = few_span(a, s);
   const SeqSpan &sp = span.sp;
   const int R = sp.m * G;
   if (R == 0) {              // `whole` only: the line has no such sequence
     if (a.whole) return;
     if (++s >= a.c.seqs) return;
+    span = few_span(a, s);
     h = 0;
     continue;
   }
@@ -597,6 +590,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   if (++h == H) {
     h = 0;
     if (++s >= a.c.seqs) return;
+    span = few_span(a, s);
   }
   __syncthreads();             // the next piece writes the same LDS
   }
@@ -644,7 +638,7 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int p
       ahead[g][r] = seen[g] && r < R ? *(const f32x4 *)(z[g] + r * 4) : (f32x4){0, 0, 0, 0};
   }
   int w0 = 0, w1 = 0;
-  if (!a.whole && R > 0) part_range(a, s, h, span.tiles, &w0, &w1);
+  if (!a.whole && R > 0) part_range(a.line[a.c.seqs], a.line[s], h, span.tiles, &w0, &w1);
   if (tid < R) {
     float l2;
     if (w0 == w1) {
@@ -716,11 +710,12 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
   const int64_t heads = (int64_t)H * G;
   const int blocks = (a.max_q * G + rows_per - 1) / rows_per;
   const int sh = blockIdx.x / blocks, s = sh / H, h = sh - s * H;
+  const uint32_t share = a.line[a.c.seqs], begin = a.line[s];     // on their way with the lengths
   const FewSpan span = few_span(a, s);
   const int R = span.sp.m * G;
   if (R == 0) return;
   int w0, w1;
-  part_range(a, s, h, span.tiles, &w0, &w1);
+  part_range(share, begin, h, span.tiles, &w0, &w1);
   if (w0 == w1) return;        // one work-group had all of it
   // a row by per_row groups of threads
   const int g = tid / kLanes, d4 = tid - g * kLanes;

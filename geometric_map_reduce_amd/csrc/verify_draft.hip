@@ -14,7 +14,7 @@
 // Two kernels: sums of pieces of the row by many work-groups (one read of two rows of the
 // vocabulary, bound by HBM for a batch and by latency for one sequence), then one work-group per
 // sequence that finds the piece and looks through it.  64 sequences of 131,072 tokens: 11 us
-// (67 MB at 6 TB/s, part of it from the cache) and 7 us; one of 32,000: 4 and 5 us.  One work-group
+// (67 MB at 6 TB/s, part of it from the cache) and 5 us; one of 32,000: 3.6 and 4.4 us.  One work-group
 // per sequence for both took 146 us: a compute unit reads some 10 bytes a nanosecond here.
 #include "paged.h"
 
@@ -24,21 +24,6 @@ namespace {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / kWave;
 constexpr int kPer = kVerifyPiece / kVerifyThreads;     // indices of a thread in a piece's step
-
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o);
-  return v;
-}
-__device__ __forceinline__ double wave_scan_f64(double v) {
-  const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const double up = __shfl_up(v, o);
-    if (lane >= o) v += up;
-  }
-  return v;
-}
 
 // The first refused of the n drafted tokens (n: none), found by every wave for itself.
 __device__ __forceinline__ int first_refused(const VerifyArgs &a, int s, int n) {
@@ -105,9 +90,9 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyArgs 
       whole += positive((double)p[u]);
     }
   }
-  left = wave_sum_f64(left);
-  whole = wave_sum_f64(whole);
-  if (lane == 0) {
+  left = wave_scan_f64(left);
+  whole = wave_scan_f64(whole);
+  if (lane == kWave - 1) {
     red[0][wave] = left;
     red[1][wave] = whole;
   }
