@@ -540,9 +540,10 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
     // slots of the first and last row of the tile
     const int ra = r0 + tile * QT, rb = ra + QT < r1 ? ra + QT - 1 : r1 - 1;
     const int pa = sp.first + (int)fast_div(a.gdiv, (uint32_t)ra), pb = sp.first + (int)fast_div(a.gdiv, (uint32_t)rb);
-    // of the wave's own 64 slots: none that a row of the tile sees, or some that some row does not see
+    // of the wave's own 64 slots: none that a row of the tile sees, or some that some row does not see (a row
+    // that is not there sees none: its zeros times an infinite key are not)
     const bool none = wave0 > pb || (a.window > 0 && wave0 + 63 <= pa - a.window);
-    const bool masked = wave0 + 63 > pa || (a.window > 0 && wave0 <= pb - a.window);
+    const bool masked = wave0 + 63 > pa || (a.window > 0 && wave0 <= pb - a.window) || ra + QT > r1;
     float part[2] = {0.0f, 0.0f};
     if (!none) {
       if (masked) add_tile(std::true_type{}, buf, part);

@@ -752,3 +752,18 @@ def test_evict_pages_and_sinks(page, n, sink, recent):
     middle = torch.argsort(-flat[sink:n - recent], stable=True)[:budget - sink - recent] + sink
     want = torch.cat([j[:sink], middle.sort().values, j[n - recent:]])
     assert torch.equal(kept[0, 0].cpu().long(), want) and new_lens.item() == budget
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_infinite_key_of_weight_zero(new):
+    """A key that every row's score sends to -infinity has no part in any output, and a weight of exactly 0."""
+    say(f"infinite key, {new} new")
+    b = ref.Batch(67, [300], [new], 2, 1, 64, 16)
+    b.q[:, :, 0] = -b.q[:, :, 0].abs() - 1
+    b.k[b.table[0, 0].item(), 3, 0, 0] = float("inf")
+    b.weights = torch.ones((b.P, 1, 16))
+    out, lse, w = run_attention(b)
+    assert w[b.table[0, 0].item(), 0, 3].item() == 0
+    assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+    total = sum(w[b.table[0, j // 16].item(), 0, j % 16].item() for j in range(300))
+    assert abs(total - 2 * new) <= 2 * new * 2 ** -16
