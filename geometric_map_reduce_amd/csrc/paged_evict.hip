@@ -9,14 +9,15 @@
 // the same order (longer rows are read again for each pass) and finds the smallest kept one by up to
 // three passes over 11, 11 and 10 bits, with counts in LDS (whole numbers, so the order of the additions
 // does not matter).  Once no more than 64 keys share the digits found, they are ranked by weight and
-// slot instead.  Every slot's place then comes from the counts of the waves before it.
-// A thread has four slots in a row: one page number and one 16-byte load where pages are whole aligned
-// quadruples, slot by slot otherwise.  Latency bounds it: all page numbers and then all weights are
-// loaded at once, and 256 keys of a wave that all meet one count add to it once (cleared weights are all
-// equal).  64 rows of up to 32,768 slots take 30 us, 32 rows of 1,025 slots 10 us.  With the keys in
-// registers the loops over them had to be unrolled, 43 KB of code, and took 32 us (43 us with a slot at
-// a time).  The move is a second kernel, one 16-byte piece of a key and of a value row per thread, bound
-// by HBM: 268 MB read and written in 50 us.
+// slot instead.  In the end a thread has up to 32 slots in a row and writes down its own; their places
+// come from a scan of the threads' counts.
+// Loading, a thread has four slots in a row: one page number and one 16-byte load where pages are whole
+// aligned quadruples, slot by slot otherwise.  64 rows of up to 32,768 slots take 22 us (9 for the loads
+// and the first pass, on 64 compute units), 32 rows of 1,025 slots 9 us; instructions bound the long rows,
+// latency the short ones.  256 keys of a wave that all meet one count add to it once (cleared weights are
+// all equal).  Slot by slot loads and keys in registers under unrolled loops took 43 us, 16-byte loads 32,
+// keys in LDS 30 (the last round by ballots over the waves).  The move is a second kernel, one 16-byte
+// piece of a key and of a value row per thread, bound by HBM: 268 MB read and written in 49 us.
 #include "paged.h"
 
 namespace kmi {
@@ -38,11 +39,14 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Where a quadruple of keys lies in LDS: threads that read a group, one quadruple each, and threads that read
+// eight in a row both meet all banks.
+__device__ __forceinline__ int quad_at(int q) { return q ^ ((q >> 4) & 7); }
+
 template <int kGroups>
 struct SelectShared {
-  __align__(16) uint32_t key[kGroups * kGroup];
+  u32x4 key[kGroups * kSelectThreads];
   __align__(16) uint32_t hist[kHistStride * kHistCopies];
-  uint32_t place[kGroups * kSelectWaves];   // kept before a wave's quadruples of a group
   __align__(16) uint32_t wave_sum[kSelectWaves];
   uint32_t prefix, need, count;
   uint32_t cand_key[kWave], cand_slot[kWave], cand_rank[kWave], cands;
@@ -66,7 +70,7 @@ __device__ __forceinline__ uint32_t before_wave(const uint32_t *wave_sum, int wa
 }
 template <int kGroups>
 __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
-  constexpr int kSegment = kGroups * kGroup;
+  constexpr int kSegment = kGroups * kGroup, kBatch = kGroups < 4 ? kGroups : 4;
   __shared__ SelectShared<kGroups> sh;
   const int H = a.c.heads;
   const int s = blockIdx.x / H, h = blockIdx.x - s * H;
@@ -90,13 +94,22 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
   // the slots in question, counted from `base0`: skip .. M - 1
   const int base0 = sink / kQuad * kQuad, skip = sink - base0, M = n - recent - base0;
   const int segments = (M + kSegment - 1) / kSegment;
-  const auto live = [&](int i) { return i >= skip && i < M; };
-  // groups of a segment that hold any
+  // groups of a segment that hold any, in whole batches: a batch's keys leave LDS together
   const auto groups_of = [&](int from) {
-    const int left = (M - from + kGroup - 1) / kGroup;
+    const int left = (M - from + kBatch * kGroup - 1) / (kBatch * kGroup) * kBatch;
     return left < kGroups ? left : kGroups;
   };
-  // keys of a segment to LDS, each thread its own quadruples; an absent slot's is 0, the least
+  const auto quads = [&](int g, u32x4 (&k)[kBatch]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) k[u] = sh.key[quad_at((g + u) * kSelectThreads + tid)];
+  };
+  // Keys of a segment to LDS, each thread its own quadruples.  An absent slot's is 1, below every weight's, and
+  // that of a place outside skip .. M is 0: it is never among the largest that there are.
+  const auto put = [&](int g, int i, u32x4 k) {      // slots i .. of group g
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) k[e] = i + e >= skip && i + e < M ? k[e] : 0u;
+    sh.key[quad_at(g * kSelectThreads + tid)] = k;
+  };
   const uint32_t ps = a.c.page.d;
   const bool whole = ps % kQuad == 0 && ((uintptr_t)a.c.weights & 15) == 0;   // a quadruple in one page, aligned
   const auto load = [&](int from) {
@@ -126,16 +139,16 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         if (g >= groups) break;
-        u32x4 k = (u32x4){0, 0, 0, 0};
+        u32x4 k = (u32x4){1, 1, 1, 1};
         if (page[g] < a.c.pages)
           k = (u32x4){weight_key(w[g][0]), weight_key(w[g][1]), weight_key(w[g][2]), weight_key(w[g][3])};
-        ((u32x4 *)sh.key)[g * kSelectThreads + tid] = k;
+        put(g, from + g * kGroup + tid * kQuad, k);
       }
       return;
     }
 #pragma unroll 2
     for (int g = 0; g < groups; ++g) {
-      u32x4 k = (u32x4){0, 0, 0, 0};
+      u32x4 k = (u32x4){1, 1, 1, 1};
 #pragma unroll
       for (int e = 0; e < kQuad; ++e) {
         const int i = from + g * kGroup + tid * kQuad + e;
@@ -143,7 +156,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
         const SlotPlace p = slot_place(a.c, trow, (uint32_t)(base0 + i));
         if (p.page >= 0) k[e] = weight_key(a.c.weights[((uint32_t)p.page * (uint32_t)H + (uint32_t)h) * ps + p.row]);
       }
-      ((u32x4 *)sh.key)[g * kSelectThreads + tid] = k;
+      put(g, from + g * kGroup + tid * kQuad, k);
     }
   };
 
@@ -160,24 +173,28 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     for (int from = 0; from < M; from += kSegment) {
       if (pass == 0 || segments > 1) load(from);
       const int groups = groups_of(from);
-      for (int g = 0; g < groups; ++g) {
-        const u32x4 k = ((const u32x4 *)sh.key)[g * kSelectThreads + tid];
-        const int i = from + g * kGroup + tid * kQuad;
-        uint32_t bin[kQuad];
-        bool in[kQuad], same = true;
+#pragma unroll 1
+      for (int g0 = 0; g0 < groups; g0 += kBatch) {
+        u32x4 k[kBatch];
+        quads(g0, k);
 #pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-          in[e] = live(i + e) && (pass == 0 || (k[e] >> (shift + bits)) == (prefix >> (shift + bits)));
-          bin[e] = (k[e] >> shift) & ((1u << bits) - 1u);
-          same &= in[e] && bin[e] == (uint32_t)__builtin_amdgcn_readfirstlane(bin[0]);
-        }
-        if (__all(same)) {
-          if (lane == 0) atomicAdd(&mine[bin[0]], (uint32_t)(kQuad * kWave));
-          continue;
-        }
+        for (int u = 0; u < kBatch; ++u) {
+          uint32_t bin[kQuad];
+          bool in[kQuad], same = true;
 #pragma unroll
-        for (int e = 0; e < kQuad; ++e)
-          if (in[e]) atomicAdd(&mine[bin[e]], 1u);
+          for (int e = 0; e < kQuad; ++e) {
+            in[e] = pass == 0 || (k[u][e] >> (shift + bits)) == (prefix >> (shift + bits));
+            bin[e] = (k[u][e] >> shift) & ((1u << bits) - 1u);
+            same &= in[e] && bin[e] == (uint32_t)__builtin_amdgcn_readfirstlane(bin[0]);
+          }
+          if (__all(same)) {
+            if (lane == 0) atomicAdd(&mine[bin[0]], (uint32_t)(kQuad * kWave));
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < kQuad; ++e)
+            if (in[e]) atomicAdd(&mine[bin[e]], 1u);
+        }
       }
     }
     __syncthreads();
@@ -212,15 +229,20 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     if (count <= kWave && segments == 1) {
       // few share them: they are ranked by weight and slot, each wave against a part of them
       const int groups = groups_of(0);
-      for (int g = 0; g < groups; ++g) {
-        const u32x4 k = ((const u32x4 *)sh.key)[g * kSelectThreads + tid];
-        const int i = g * kGroup + tid * kQuad;
+#pragma unroll 1
+      for (int g0 = 0; g0 < groups; g0 += kBatch) {
+        u32x4 k[kBatch];
+        quads(g0, k);
 #pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-          if (live(i + e) && (k[e] >> shift) == (prefix >> shift)) {
-            const uint32_t at = atomicAdd(&sh.cands, 1u);
-            sh.cand_key[at] = k[e];
-            sh.cand_slot[at] = (uint32_t)(i + e);
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = (g0 + u) * kGroup + tid * kQuad;
+#pragma unroll
+          for (int e = 0; e < kQuad; ++e) {
+            if ((k[u][e] >> shift) == (prefix >> shift)) {
+              const uint32_t at = atomicAdd(&sh.cands, 1u);
+              sh.cand_key[at] = k[u][e];
+              sh.cand_slot[at] = (uint32_t)(i + e);
+            }
           }
         }
       }
@@ -247,52 +269,37 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
   }
   // kept: keys above `prefix`, and those equal to it up to slot `cut`.  Without a cut yet and with
   // more equal keys than wanted, a first round over the equal ones finds the need-th.  In either
-  // round a slot's place is the number of slots before it: counts of the waves, scanned.
+  // round a slot's place is the number of slots before it: counts of the threads, scanned.
 #pragma unroll 1
   for (int round = need == count ? 1 : 0; round < 2; ++round) {
     uint32_t base = 0;
 #pragma unroll 1
     for (int from = 0; from < M; from += kSegment) {
       if (segments > 1) load(from);
-      const int groups = groups_of(from);
-      uint32_t mine = 0;               // this thread's slots as bits, four a group
+      // here a thread has `groups` quadruples in a row, 32 slots at most
+      const int groups = groups_of(from), first = tid * groups;
+      if (segments > 1) __syncthreads();
+      uint32_t mine = 0;               // its slots as bits
       for (int g = 0; g < groups; ++g) {
-        const u32x4 k = ((const u32x4 *)sh.key)[g * kSelectThreads + tid];
-        const int i = from + g * kGroup + tid * kQuad;
-        uint32_t c = 0;
+        const u32x4 k = sh.key[quad_at(first + g)];
+        const int i = from + (first + g) * kQuad;
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) {
           const bool eq = k[e] == prefix;
-          const bool in = live(i + e) && (round == 0 ? eq : k[e] > prefix || (eq && (uint32_t)(i + e) <= cut));
-          c += (uint32_t)__popcll(__ballot(in));
-          mine |= (in ? 1u : 0u) << (g * kQuad + e);
+          const bool in = round == 0 ? eq : k[e] > prefix || (eq && (uint32_t)(i + e) <= cut);
+          mine |= (in ? 1u << e : 0u) << (g * kQuad);
         }
-        if (lane == 0) sh.place[g * kSelectWaves + wave] = c;
       }
-      __syncthreads();
-      uint32_t own = 0, total;
-      if (tid < groups * kSelectWaves) own = sh.place[tid];
-      uint32_t upto = wave_scan_u32(own);
+      const uint32_t own = (uint32_t)__popc(mine);
+      uint32_t total;
+      const uint32_t upto = wave_scan_u32(own);
       if (lane == kWave - 1) sh.wave_sum[wave] = upto;
       __syncthreads();
-      upto += before_wave(sh.wave_sum, wave, &total);
-      if (tid < groups * kSelectWaves) sh.place[tid] = upto - own;
-      __syncthreads();
-      const uint64_t below = ((uint64_t)1 << lane) - 1;
-      for (int g = 0; g < groups; ++g) {
-        const uint32_t four = mine >> (g * kQuad);
-        // the lanes before this one, then the thread's own slots in order
-        uint32_t place = base + sh.place[g * kSelectWaves + wave];
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) place += __popcll(__ballot((four >> e) & 1u) & below);
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-          const bool in = (four >> e) & 1u;
-          const int i = from + g * kGroup + tid * kQuad + e;
-          if (in && round == 1) kept[sink + place] = base0 + i;
-          if (in && round == 0 && place == need - 1) sh.cut_slot = (uint32_t)i;
-          place += in;
-        }
+      uint32_t place = base + upto - own + before_wave(sh.wave_sum, wave, &total);
+      for (; mine; mine &= mine - 1, ++place) {
+        const int i = from + first * kQuad + __ffs(mine) - 1;
+        if (round == 1) kept[sink + place] = base0 + i;
+        else if (place == need - 1) sh.cut_slot = (uint32_t)i;
       }
       base += total;
       __syncthreads();
