@@ -28,6 +28,11 @@ constexpr int kFewWhole = 1024;
 // (one compute unit reads at most some 50 bytes a nanosecond).
 constexpr int kFewWhole8 = 768;
 
+// Keys and values that a call reads at most, in bytes, from which on they pass the caches by.  The last level holds
+// 256 MB: 525 MB took 107 us by way of it and 98 past it, and 230 MB that it still held from the call before 47
+// and 51 us.  Lengths may fall short of their bound, so not at 256 MB itself.
+constexpr double kFarBytes = 384e6;
+
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
 int64_t width_of(int type) { return type == KEOPS_TYPE_E4M3 ? 1 : 2; }
@@ -101,7 +106,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Launch plan of one attention call.
 struct AttendPlan {
-  bool few, scores;
+  bool few, scores, far;
   int whole, row_tiles, score_rows, join_rows;
   int64_t nsplit, nrow, grid, sums_grid, score_stride;
   int64_t line_bytes, ml_bytes, o_bytes, score_bytes, sums_bytes;
@@ -131,6 +136,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     p->whole = from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
     if (!p->whole && from_tile <= kFewWhole8 && S * H <= cus && p->row_tiles == 1 && c.dim <= 128) p->whole = 2;
     p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
+    p->far = !p->whole && 2.0 * (double)S * (double)H * (double)from_tile * (double)(c.dim * width_of(c.type)) > kFarBytes;
     if (!p->whole) {
       // a joining work-group's 1024 / dim groups of threads: one to a row where the parts are few
       const int64_t groups = 1024 / c.dim, parts = ceil_div(p->grid, S * H) + 1;
@@ -289,6 +295,7 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.lse = lse;
   a.nsplit = (int32_t)p.nsplit;
   a.whole = p.whole;
+  a.far = p.far;
   a.line = (uint32_t *)ws;
   ws += p.line_bytes;
   a.part_ml = (float2 *)ws;

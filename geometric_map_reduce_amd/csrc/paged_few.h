@@ -46,6 +46,11 @@ template <> struct VPieces<96> { static constexpr int n = 2; static constexpr in
 template <> struct VPieces<128> { static constexpr int n = 1; static constexpr int w[2] = {8, 0}; };
 template <> struct VPieces<256> { static constexpr int n = 2; static constexpr int w[2] = {8, 8}; };
 
+// A load of what is read once, past the caches if `far`.
+template <class V, bool FAR>
+__device__ __forceinline__ V load_once(const void *p) {
+  return FAR ? __builtin_nontemporal_load((const V *)p) : *(const V *)p;
+}
 __device__ __forceinline__ float xor_max(float v) {   // over the four lanes of a row
   v = fmaxf(v, __shfl_xor(v, 16));
   return fmaxf(v, __shfl_xor(v, 32));
@@ -75,6 +80,7 @@ struct FewRows {
   }
 
   // K rows of the tile: lane l has slot l % 16 of each 16, columns step_column(s, l / 16) ..+8 of step s.
+  template <bool FAR>
   __device__ __forceinline__ void load_k(const char *base, const int64_t *off, int at) {
     const int lane = threadIdx.x & (kWave - 1), row = lane & 15, q = lane >> 4;
 #pragma unroll
@@ -86,15 +92,15 @@ struct FewRows {
       for (int s = 0; s < kSteps; ++s) {
         if (kWide) {
           if (s & 1) continue;
-          const u32x4 w = *(const u32x4 *)(p + s * 32);
+          const u32x4 w = load_once<u32x4, FAR>((p + s * 32));
 #pragma unroll
           for (int u = 0; u < 4; ++u) kr[t][(2 * s + u) % kKRegs] = w[u];
         } else if (E4M3) {
-          const u32x2 w = *(const u32x2 *)(p + s * 32);
+          const u32x2 w = load_once<u32x2, FAR>((p + s * 32));
           kr[t][2 * s] = w.x;
           kr[t][2 * s + 1] = w.y;
         } else {
-          const u32x4 w = *(const u32x4 *)(p + s * 64);
+          const u32x4 w = load_once<u32x4, FAR>((p + s * 64));
 #pragma unroll
           for (int u = 0; u < 4; ++u) kr[t][4 * s + u] = w[u];
         }
@@ -103,6 +109,7 @@ struct FewRows {
   }
 
   // V: lane l has slots 4 (l / 16) + i of the first 16 (i < 4) and of the second (i >= 4).
+  template <bool FAR>
   __device__ __forceinline__ void load_v(const char *base, const int64_t *off, int at) {
     const int lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
 #pragma unroll
@@ -116,20 +123,20 @@ struct FewRows {
         const int w = VPieces<D>::w[n], b = w * kBytes;
         const char *e = p + (col + c * w) * kBytes;
         if (b == 16) {
-          const u32x4 x = *(const u32x4 *)e;
+          const u32x4 x = load_once<u32x4, FAR>(e);
 #pragma unroll
           for (int u = 0; u < 4; ++u) vr[i][(reg + u) % kVRegs] = x[u];
           reg += 4;
         } else if (b == 8) {
-          const u32x2 x = *(const u32x2 *)e;
+          const u32x2 x = load_once<u32x2, FAR>(e);
           vr[i][reg % kVRegs] = x.x;
           vr[i][(reg + 1) % kVRegs] = x.y;
           reg += 2;
         } else if (b == 4) {
-          vr[i][reg % kVRegs] = *(const uint32_t *)e;
+          vr[i][reg % kVRegs] = load_once<uint32_t, FAR>(e);
           reg += 1;
         } else {
-          vr[i][reg % kVRegs] = *(const uint16_t *)e;
+          vr[i][reg % kVRegs] = load_once<uint16_t, FAR>(e);
           reg += 1;
         }
         col += 16 * w;
@@ -241,7 +248,8 @@ __device__ __forceinline__ void part_range(uint32_t share, uint32_t begin, int h
 
 // NW waves: 4, or 8 where one work-group has a short sequence's head to itself and nothing else
 // would hide its latency.
-template <class T, bool E4M3, int D, int NR, bool SCORES, int NW>
+// FAR: the call's keys and values are more than the last-level cache holds, and pass it by.
+template <class T, bool E4M3, int D, int NR, bool SCORES, int NW, bool FAR>
 __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, E4M3, D, NR>;
   constexpr int kRows = 16 * NR;
@@ -367,9 +375,9 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
     __syncthreads();
     int tile = wave;
     const int begin = tile < ntile ? tile * kFewTile : kFewBlock;
-    f.load_k(kbase, sh.off, begin);
+    f.template load_k<FAR>(kbase, sh.off, begin);
     __builtin_amdgcn_sched_barrier(0);
-    f.load_v(vbase, sh.off, begin);
+    f.template load_v<FAR>(vbase, sh.off, begin);
     __builtin_amdgcn_sched_barrier(0);
     for (; tile < ntile; tile += NW) {
       const int at = tile * kFewTile, j0 = blk + at;
@@ -387,7 +395,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
           for (int nr = 0; nr < NR; ++nr) sc[nr][t] = T::mfma16(kf, qf[nr][st], sc[nr][t]);
         }
       }
-      f.load_k(kbase, sh.off, next);
+      f.template load_k<FAR>(kbase, sh.off, next);
       __builtin_amdgcn_sched_barrier(0);
 
       const uint32_t there = present[tile];
@@ -471,7 +479,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
             acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
           }
         }
-      f.load_v(vbase, sh.off, next);
+      f.template load_v<FAR>(vbase, sh.off, next);
     }
   }
 
@@ -770,7 +778,7 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
     static std::atomic<int> fit{0};
     int n = fit.load(std::memory_order_relaxed);
     if (n <= 0) {
-      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves>,
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, false>,
                                                        kFewThreads, 0) != hipSuccess || n < 1)
         return -1;
       fit.store(n, std::memory_order_relaxed);
@@ -778,10 +786,12 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
     return n;
   }
   if constexpr (NR == 1 && D <= 128) {
-    if (a.whole == 2) attend_few_kernel<T, E4M3, D, NR, SCORES, 8><<<dim3((unsigned)grid), 8 * kWave, 0, st>>>(a);
+    if (a.whole == 2) attend_few_kernel<T, E4M3, D, NR, SCORES, 8, false><<<dim3((unsigned)grid), 8 * kWave, 0, st>>>(a);
   }
-  if (!(NR == 1 && D <= 128 && a.whole == 2))
-    attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
+  if (a.far)
+    attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, true><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
+  else if (!(NR == 1 && D <= 128 && a.whole == 2))
+    attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, false><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
   const int64_t sh = (int64_t)a.c.seqs * a.c.heads;
   const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh : 0;
   const int64_t sums = SCORES ? (a.max_len + kScoreSlots - 1) / kScoreSlots * sh : 0;
