@@ -287,6 +287,13 @@ __device__ __forceinline__ u32x4 widen_e4m3(u32x2 w) {
                  T::template from_e4m3<false>(w.y), T::template from_e4m3<true>(w.y)};
 }
 
+// A load of what is read once, past the caches if FAR.
+template <class V, bool FAR>
+__device__ __forceinline__ V load_once(const void *p) {
+  return FAR ? __builtin_nontemporal_load((const V *)p) : *(const V *)p;
+}
+constexpr double kLastLevel = 256e6;     // bytes of the last-level cache
+
 // Zeros where `keep` is false.
 __device__ __forceinline__ u32x4 keep_if(u32x4 v, bool keep) {
   const uint32_t m = keep ? 0xffffffffu : 0u;

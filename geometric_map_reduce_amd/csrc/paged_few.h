@@ -46,11 +46,6 @@ template <> struct VPieces<96> { static constexpr int n = 2; static constexpr in
 template <> struct VPieces<128> { static constexpr int n = 1; static constexpr int w[2] = {8, 0}; };
 template <> struct VPieces<256> { static constexpr int n = 2; static constexpr int w[2] = {8, 8}; };
 
-// A load of what is read once, past the caches if `far`.
-template <class V, bool FAR>
-__device__ __forceinline__ V load_once(const void *p) {
-  return FAR ? __builtin_nontemporal_load((const V *)p) : *(const V *)p;
-}
 __device__ __forceinline__ float xor_max(float v) {   // over the four lanes of a row
   v = fmaxf(v, __shfl_xor(v, 16));
   return fmaxf(v, __shfl_xor(v, 32));

@@ -767,3 +767,26 @@ def test_infinite_key_of_weight_zero(new):
     assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
     total = sum(w[b.table[0, j // 16].item(), 0, j % 16].item() for j in range(300))
     assert abs(total - 2 * new) <= 2 * new * 2 ** -16
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_append_e4m3_scales(dtype):
+    """Every 16-bit value over scales of all kinds equals the value nearest to the fp32 quotient."""
+    say(f"e4m3 quotients, {dtype}")
+    g = torch.Generator().manual_seed(71)
+    bits = (torch.randint(0, 1 << 23, (40,), generator=g) + (torch.randint(100, 150, (40,), generator=g) << 23)).to(torch.int32)
+    special = [1.0, -0.5, 3.0, 2.0 ** -61, 2.0 ** -60, 2.0 ** 60, 2.0 ** 61, 1e-38, 1e-42, 3e38, float("inf"), float("nan"), 0.0,
+               float(torch.tensor(0x3fffffff, dtype=torch.int32).view(torch.float32)), float(torch.tensor(0x3f7fffff, dtype=torch.int32).view(torch.float32))]
+    x = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(dtype).view(-1, 1, 64).cuda()
+    T = x.shape[0]
+    table, lens = torch.arange(T // 16, dtype=torch.int32, device="cuda")[None], torch.tensor([T], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    for i, s in enumerate(bits.view(torch.float32).tolist() + special):
+        scale = torch.tensor([s], device="cuda")
+        k = torch.zeros((T // 16, 16, 1, 64), device="cuda").to(E4)
+        v = torch.zeros_like(k)
+        gm.keops_cache_append(x, x, k, v, table, lens, starts, k_scale=scale, v_scale=torch.ones_like(scale))
+        want = (x.float() / scale).clamp(-448, 448).to(E4).view(torch.uint8).view(-1)
+        got = k.view(torch.uint8).view(-1)
+        nan = (want & 0x7f) == 0x7f
+        assert torch.equal(got[~nan], want[~nan]) and bool(((got[nan] & 0x7f) == 0x7f).all()), (i, s)
