@@ -225,8 +225,11 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   // In a tile with slots that some row does not see: V of absent ones is cleared, and non-finite values of
   // those that some rows see and others do not wait for the end.  Each thread looks at its own pieces.
   const auto clear = [&](int buf, int tile, uint64_t there) {
+    // unrolled it takes 39 registers more at D = 96: 773 to 811 us for 4,096 tokens after 12,288; elsewhere rolled
+    // is slower by a percent
+    constexpr int kUnroll = D == 96 ? 1 : kLoads;
     bool odd = false;
-#pragma unroll
+#pragma unroll kUnroll
     for (int i = 0; i < kLoads; ++i) {
       const int id = tid + i * kManyThreads, u = id / kPieces, j = lo + tile * KT + u;
       u32x4 x = ((const u32x4 *)sv[buf])[id];
