@@ -18,8 +18,8 @@
 //  * The running maximum moves only when a score passes it by 2^8 (one branch per tile), so the
 //    sums and p stay below 2^8 times what they would be; sums are in 32 bits, p is rounded to
 //    the cache's 16-bit type for the matrix product (8-bit caches: q's type).
-//  * HBM bounds it: 64 sequences of 5,120 slots (bf16, 16 rows a head) read 1.34 GB in 245 us, 5.5 TB/s
-//    with both passes; 131,071 slots of one sequence 5.1 TB/s and 6 us of the second pass.
+//  * HBM bounds it: 64 sequences of 5,120 slots (bf16, 16 rows a head) read 1.34 GB in 242 us, 5.6 TB/s
+//    with both passes; 131,071 slots of one sequence 5.4 TB/s and 5 us of the second pass.
 //  * Slots that no row may see (past the length, of a page that the table lacks) get a zero V.
 //    Slots that some rows see and others do not are only in the tiles of the new tokens and at
 //    the window's edge; if such a tile holds an infinity or NaN in V, it is added after the

@@ -7,8 +7,8 @@
 // Attention: a work-group takes 128 rows of one (sequence, key/value head), 32 a wave, and walks
 // the slots that any of them sees in tiles of 64.  Tiles of K and V lie in LDS, the next ones on
 // their way while one is used.  The matrix products and the clock that they leave bound it: 4,096
-// tokens after 12,288 slots (32/8 heads of 128, bf16) take 960 us, 1,003 TFLOP/s at 2.0 GHz, where
-// the largest library product reaches 1,367; without the exponentials they would take 912.
+// tokens after 12,288 slots (32/8 heads of 128, bf16) take 945 us, 1,018 TFLOP/s, on a card whose
+// large library product reaches 1,268 (1,120 us on one that runs that at 1,199).
 //
 //  * S^T = K Q^T with 32 x 32 x 16 products: Q stays in registers as the B operand, a lane holds one row
 //    and 16 slots of each 32.  Counting the slots in that order makes the packed p the B operand
