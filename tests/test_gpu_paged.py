@@ -790,3 +790,44 @@ def test_append_e4m3_scales(dtype):
         got = k.view(torch.uint8).view(-1)
         nan = (want & 0x7f) == 0x7f
         assert torch.equal(got[~nan], want[~nan]) and bool(((got[nan] & 0x7f) == 0x7f).all()), (i, s)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("new,weights", [(1, False), (2, True), (7, False), (6, True)])
+def test_loads_past_the_caches(dtype, cache, dim, new, weights):
+    """The bounds of a call, not its lengths, say that its keys and values may be more than a cache holds."""
+    say(f"loads past the caches, {dtype} {cache}, dim {dim}, {new} new, weights {weights}")
+    lens = [300, 77, 40]
+    b = ref.Batch(73, lens, [new, 1, 0], 8, 2, dim, 24, dtype, cache)
+    if weights:
+        b.weights = torch.zeros((b.P, 2, 24))
+    w = put(b.weights)
+    most = 1 << 19                                          # 2 x 3 x 2 x 2^19 rows: 402 MB and more
+    out, lse = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), put(b.lens_t()), put(b.starts), new, most,
+                                        weights=w, k_scale=put(b.k_scale), v_scale=put(b.v_scale))
+    torch.cuda.synchronize()
+    o, z, ww, ot, zt, wt = ref.attention(b)
+    close(lse.cpu(), z, zt, "lse")
+    close(out.cpu(), o, ot, "out")
+    if weights:
+        close(w.cpu(), ww, wt, "weights")
+
+
+def test_eviction_past_the_caches():
+    say("eviction with a budget of more than a cache holds")
+    n, budget, page = 100, 600000, 16
+    g = torch.Generator().manual_seed(79)
+    k = torch.randn((16, page, 1, 64), generator=g).to(BF).cuda()
+    v = torch.randn((16, page, 1, 64), generator=g).to(BF).cuda()
+    w = torch.rand((16, 1, page), generator=g).cuda()
+    k0, v0, w0 = k.clone(), v.clone(), w.clone()
+    table = torch.tensor([[9, 4, 1, 14, 6, 0, 11]], dtype=torch.int32).cuda()
+    new = torch.tensor([[2, 3, 5, 7, 8, 10, 12]], dtype=torch.int32).cuda()
+    kept, lens = gm.keops_cache_evict(k, v, w, table, torch.tensor([n], dtype=torch.int32).cuda(), new, budget)
+    torch.cuda.synchronize()
+    assert lens.item() == n and torch.equal(kept[0, 0, :n].cpu(), torch.arange(n, dtype=torch.int32)) and bool((kept[0, 0, n:] == -1).all())
+    for pool, old in ((k, k0), (v, v0)):
+        got, want = (p[t[0].long()].reshape(-1, 64)[:n] for p, t in ((pool, new), (old, table)))
+        assert torch.equal(got, want)
+    assert torch.equal(w[new[0].long()].reshape(-1)[:n], w0[table[0].long()].reshape(-1)[:n])
