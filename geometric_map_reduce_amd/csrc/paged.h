@@ -137,6 +137,7 @@ struct AttendArgs {
   int32_t nsplit;
   uint32_t *line;               // few rows: where each sequence's tiles begin, and a work-group's share [seqs + 1]
   int32_t whole;                // few rows: a work-group has all slots of one (sequence, head); 2: of eight waves
+  int32_t join_slices;          // few rows: work-groups that share the columns of a row in the join
   bool far;                     // few rows, not `whole`: more keys and values than the last-level cache holds
   float *part_o;                // [..][dim], sums under the part's maximum
   float2 *part_ml;              // (maximum in log2 units, sum)

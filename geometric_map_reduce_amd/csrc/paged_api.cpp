@@ -28,6 +28,9 @@ constexpr int kFewWhole = 1024;
 // (one compute unit reads at most some 50 bytes a nanosecond).
 constexpr int kFewWhole8 = 768;
 
+// Parts of a row from which on its join is shared by columns: 400 parts (one head's 51,206 slots) take 22.6 us
+// a call unshared and 19.6 shared, 196 parts 16.8 and 16.4, 128 parts 31.6 and 33.1 (four heads').
+constexpr int64_t kJoinParts = 192;
 // Keys and values that a call reads at most, in bytes, from which on they pass the caches by.  The last level holds
 // 256 MB: 525 MB took 107 us by way of it and 98 past it, and 230 MB that it still held from the call before 47
 // and 51 us.  Lengths may fall short of their bound, so not at 256 MB itself.
@@ -107,7 +110,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Launch plan of one attention call.
 struct AttendPlan {
   bool few, scores, far;
-  int whole, row_tiles, score_rows, join_rows;
+  int whole, row_tiles, score_rows, join_rows, join_slices;
   int64_t nsplit, nrow, grid, sums_grid, score_stride;
   int64_t line_bytes, ml_bytes, o_bytes, score_bytes, sums_bytes;
   int64_t total() const { return line_bytes + ml_bytes + o_bytes + score_bytes + sums_bytes; }
@@ -126,7 +129,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
   if (p->few) {
     p->row_tiles = rows <= 16 ? 1 : 2;
     const int64_t from_tile = std::min<int64_t>(max_len, span + 31);    // a window starts inside a tile
-    if ((double)S * (double)H * (double)(from_tile / 32 + 2) > (double)kMaxGrid || (double)S * (double)H * (double)rows > (double)kMaxGrid)
+    if ((double)S * (double)H * (double)(from_tile / 32 + 2) > (double)kMaxGrid || (double)S * (double)H * (double)rows * 8.0 > (double)kMaxGrid)
       return KEOPS_ERR_UNSUPPORTED;
     AttendArgs probe{};
     probe.score_stride = p->scores;
@@ -141,6 +144,8 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       // a joining work-group's 1024 / dim groups of threads: one to a row where the parts are few
       const int64_t groups = 1024 / c.dim, parts = ceil_div(p->grid, S * H) + 1;
       p->join_rows = (int)std::max<int64_t>(1, std::min(rows, parts <= 4 ? groups : groups / parts));
+      // many parts: 32 columns to a work-group, so that 32 groups of threads share a row's parts
+      p->join_slices = parts > kJoinParts ? c.dim / 32 : 1;
       p->line_bytes = align256((S + 1) * 4);
       p->ml_bytes = align256(p->grid * 2 * 16 * p->row_tiles * 8);
       p->o_bytes = align256(p->grid * 2 * 16 * p->row_tiles * c.dim * 4);
@@ -160,7 +165,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       p->score_stride = ceil_div(max_len, 32) * 32;
       if (4.0 * (double)S * (double)H * (double)rows * (double)p->score_stride > kMaxWorkspace) return KEOPS_ERR_ALLOC;
       p->score_bytes = align256(4 * S * H * rows * p->score_stride);
-      if ((double)S * (double)H * (double)(ceil_div(max_len, 256) + rows) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+      if ((double)S * (double)H * (double)(ceil_div(max_len, 256) + rows * 8) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
     } else {
       const int64_t nst = ceil_div(max_len, kSumSlotsTile);
       if ((double)S * (double)H * (double)nst > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
@@ -296,6 +301,7 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.nsplit = (int32_t)p.nsplit;
   a.whole = p.whole;
   a.far = p.far;
+  a.join_slices = std::max(1, p.join_slices);
   a.line = (uint32_t *)ws;
   ws += p.line_bytes;
   a.part_ml = (float2 *)ws;

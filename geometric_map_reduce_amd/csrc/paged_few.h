@@ -642,25 +642,32 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int p
   }
   int w0 = 0, w1 = 0;
   if (!a.whole && R > 0) part_range(a.line[a.c.seqs], a.line[s], h, span.tiles, &w0, &w1);
-  if (tid < R) {
-    float l2;
-    if (w0 == w1) {
-      const int tok = (int)fast_div(a.gdiv, tid), g = tid - tok * G;
-      l2 = a.lse[(sp.t0 + tok) * ((int64_t)H * G) + h * G + g] * kLog2e;
-    } else {
-      float top = -INFINITY, l = 0.0f;
+  // the rows' lse: `width` lanes a row, each every width-th part in order, then the lanes two by two
+  const int width = R <= 4 ? 64 : (R <= 8 ? 32 : (R <= 16 ? 16 : 8)), r = tid / width;
+  static_assert(kFinishThreads / 8 >= kFewRowsMax, "every row has its lanes");
+  float l2 = -INFINITY;
+  if (w0 == w1) {
+    const int tok = (int)fast_div(a.gdiv, r), g = r - tok * G;
+    if (r < R) l2 = a.lse[(sp.t0 + tok) * ((int64_t)H * G) + h * G + g] * kLog2e;
+  } else {
+    float top = -INFINITY, l = 0.0f;
+    const auto add = [&](float m, float y) {
+      if (!(y > 0.0f || y != y)) return;
+      const float m_new = fmaxf(top, m);
+      l = l * fast_exp2(top - m_new) + y * fast_exp2(m - m_new);
+      top = m_new;
+    };
+    if (r < R) {
 #pragma unroll 4
-      for (int w = w0; w <= w1; ++w) {
-        const float2 x = a.part_ml[part_slot(w, w0, part_rows) + tid];
-        if (!(x.y > 0.0f || x.y != x.y)) continue;
-        const float m_new = fmaxf(top, x.x);
-        l = l * fast_exp2(top - m_new) + x.y * fast_exp2(x.x - m_new);
-        top = m_new;
+      for (int w = w0 + (tid & (width - 1)); w <= w1; w += width) {
+        const float2 x = a.part_ml[part_slot(w, w0, part_rows) + r];
+        add(x.x, x.y);
       }
-      l2 = l > 0.0f || l != l ? top + __log2f(l) : -INFINITY;
     }
-    lse2[tid] = l2 == -INFINITY ? INFINITY : l2;       // a row that sees nothing gives 0
+    for (int o = 1; o < width; o <<= 1) add(__shfl_xor(top, o), __shfl_xor(l, o));
+    l2 = l > 0.0f || l != l ? top + __log2f(l) : -INFINITY;
   }
+  if (r < R && (tid & (width - 1)) == 0) lse2[r] = l2 == -INFINITY ? INFINITY : l2;   // a row that sees nothing gives 0
   __syncthreads();
 #pragma unroll
   for (int g = 0; g < kScoreGroups; ++g) {
@@ -698,13 +705,13 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int p
 }
 
 // The second pass of the few-rows form: work-groups below `joins` join the parts of a (sequence,
-// head), `rows_per` rows each; the others turn kept scores into weights.
+// head), `rows_per` rows each, `slices` of them a row's columns; the others turn kept scores into weights.
 //   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k
 // over the work-groups k of the run, under a running maximum M, in order within each of the groups
 // of dim / 4 threads, then the groups in order.
 template <class T, int D, int NR>
-__global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a, int joins, int rows_per) {
-  constexpr int kLanes = D / 4, kGroups = kFinishThreads / kLanes;
+__global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a, int joins, int rows_per, int slices) {
+  const int lanes = D / 4 / slices, groups = kFinishThreads / lanes;      // threads of a group, a float4 each
   __shared__ f32x4 part[kFinishThreads];
   __shared__ float2 part_ml[kFinishThreads];
   __shared__ float lse2[kFewRowsMax];
@@ -712,7 +719,8 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
   const int H = a.c.heads, G = a.group, tid = threadIdx.x;
   const int64_t heads = (int64_t)H * G;
   const int blocks = (a.max_q * G + rows_per - 1) / rows_per;
-  const int sh = blockIdx.x / blocks, s = sh / H, h = sh - s * H;
+  const int block = blockIdx.x / slices, slice = blockIdx.x - block * slices;
+  const int sh = block / blocks, s = sh / H, h = sh - s * H;
   const uint32_t share = a.line[a.c.seqs], begin = a.line[s];     // on their way with the lengths
   const FewSpan span = few_span(a, s);
   const int R = span.sp.m * G;
@@ -721,9 +729,9 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
   part_range(share, begin, h, span.tiles, &w0, &w1);
   if (w0 == w1) return;        // one work-group had all of it
   // a row by per_row groups of threads
-  const int g = tid / kLanes, d4 = tid - g * kLanes;
-  const int per_row = kGroups / rows_per, gr = g / per_row, gk = g - gr * per_row;
-  const int r = (blockIdx.x - sh * blocks) * rows_per + gr;
+  const int g = tid / lanes, d4 = tid - g * lanes + slice * lanes;
+  const int per_row = groups / rows_per, gr = g / per_row, gk = g - gr * per_row;
+  const int r = (block - sh * blocks) * rows_per + gr;
   const bool mine = gr < rows_per && r < R;
   f32x4 acc = (f32x4){0, 0, 0, 0};
   float l = 0.0f, top = -INFINITY;
@@ -755,7 +763,7 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
   part_ml[tid] = make_float2(top, l);
   __syncthreads();
   if (!mine || gk != 0) return;
-  for (int k = 1; k < per_row; ++k) add(part_ml[tid + k * kLanes].x, part_ml[tid + k * kLanes].y, part[tid + k * kLanes]);
+  for (int k = 1; k < per_row; ++k) add(part_ml[tid + k * lanes].x, part_ml[tid + k * lanes].y, part[tid + k * lanes]);
   const int tok = (int)fast_div(a.gdiv, (uint32_t)r);
   const int64_t row = (span.sp.t0 + tok) * heads + h * G + (r - tok * G);
   const bool any = l > 0.0f || l != l;
@@ -788,10 +796,10 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
   else if (!(NR == 1 && D <= 128 && a.whole == 2))
     attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, false><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
   const int64_t sh = (int64_t)a.c.seqs * a.c.heads;
-  const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh : 0;
+  const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh * a.join_slices : 0;
   const int64_t sums = SCORES ? (a.max_len + kScoreSlots - 1) / kScoreSlots * sh : 0;
   if (joins + sums > 0)
-    finish_few_kernel<T, D, NR><<<dim3((unsigned)(joins + sums)), kFinishThreads, 0, st>>>(a, (int)joins, join_rows);
+    finish_few_kernel<T, D, NR><<<dim3((unsigned)(joins + sums)), kFinishThreads, 0, st>>>(a, (int)joins, join_rows, a.join_slices);
   return 0;
 }
 template <class T, bool E4M3, int D>

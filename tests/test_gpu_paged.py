@@ -831,3 +831,13 @@ def test_eviction_past_the_caches():
         got, want = (p[t[0].long()].reshape(-1, 64)[:n] for p, t in ((pool, new), (old, table)))
         assert torch.equal(got, want)
     assert torch.equal(w[new[0].long()].reshape(-1)[:n], w0[table[0].long()].reshape(-1)[:n])
+
+
+@pytest.mark.parametrize("dim,dtype,cache", [(64, BF, BF), (96, FP, E4), (128, BF, BF), (256, FP, FP)])
+@pytest.mark.parametrize("new,heads", [(1, 1), (1, 5), (3, 5), (2, 16)])
+def test_many_parts(dim, dtype, cache, new, heads):
+    """One head over many work-groups: joined by columns, and its rows' lse by many lanes."""
+    say(f"many parts, dim {dim}, {dtype}, {cache}, {new} x {heads} rows")
+    b = ref.Batch(83, [27000, 300], [new, 1], heads, 1, dim, 64, dtype, cache)
+    b.weights = torch.zeros((b.P, 1, 64))
+    check_attention(b)
