@@ -20,6 +20,10 @@
 
 #include "keops_mi355x.h"
 
+#ifndef PAGED_CALL_DEVICE      // the tests' build takes host tensors, over a stand-in for the library
+#define PAGED_CALL_DEVICE c10::DeviceType::CUDA
+#endif
+
 namespace {
 
 PyObject *g_raw_stream = nullptr;     // torch's current raw stream of a device
@@ -50,7 +54,10 @@ struct Call {
     if (a.bad) ok = false;
     return a.t;
   }
-  bool on_device(const at::Tensor &t) const { return t.is_cuda() && t.get_device() == dev; }
+  bool on_device(const at::Tensor &t) const {
+    const c10::Device d = t.device();
+    return d.type() == PAGED_CALL_DEVICE && d.index() == dev;
+  }
   // the address of a dense tensor of this type and shape, null where it is another
   void *dense(const at::Tensor *t, at::ScalarType type, at::IntArrayRef shape) {
     if (!t) return nullptr;
@@ -61,9 +68,9 @@ struct Call {
     return t->data_ptr();
   }
   bool begin(const at::Tensor &t) {
-    if (!t.is_cuda()) return false;
-    dev = t.get_device();
-    const c10::impl::VirtualGuardImpl guard(c10::DeviceType::CUDA);
+    if (t.device().type() != PAGED_CALL_DEVICE) return false;
+    dev = t.device().index();
+    const c10::impl::VirtualGuardImpl guard(PAGED_CALL_DEVICE);
     return guard.getDevice().index() == dev;
   }
 };
@@ -150,13 +157,15 @@ bool stream_of(const Call &c, void **stream) {
   return !PyErr_Occurred();
 }
 
+// Runs f without the interpreter's lock, which is back also where f throws.  No tensor is asked for
+// anything in there: one without memory of its own (torch.vmap's, torch.func's) throws at its address.
 template <class F>
 int unlocked(F f) {
-  int rc;
-  Py_BEGIN_ALLOW_THREADS
-  rc = f();
-  Py_END_ALLOW_THREADS
-  return rc;
+  struct Lock {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
 }
 
 // Runs f; anything thrown, and any Python error, is a call for the long way.
@@ -209,12 +218,12 @@ PyObject *append(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (!c.ok || k->sizes() != v->sizes() || k->scalar_type() != v->scalar_type() || !rows_of(c, *k, cache, &ks) ||
         !rows_of(c, *v, cache, &vs) || k->size(1) != cache.heads)
       return nullptr;
-    const void *at = c.dense(starts, at::kInt, {(int64_t)cache.seqs + 1});
+    const int32_t *at = (const int32_t *)c.dense(starts, at::kInt, {(int64_t)cache.seqs + 1});
     if (!c.ok || !stream_of(c, &st)) return nullptr;
-    const int rc = unlocked([&] {
-      return keops_cache_append(&cache, k->data_ptr(), v->data_ptr(), ks, vs, type_of(k->scalar_type()), (const int32_t *)at,
-                                k->size(0), st);
-    });
+    const void *kp = k->data_ptr(), *vp = v->data_ptr();
+    const int type = type_of(k->scalar_type());
+    const int64_t T = k->size(0);
+    const int rc = unlocked([&] { return keops_cache_append(&cache, kp, vp, ks, vs, type, at, T, st); });
     return rc == KEOPS_OK ? Py_NewRef(Py_True) : nullptr;
   });
 }
@@ -236,15 +245,18 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const double decay = PyFloat_AS_DOUBLE(o[13]);
     const int64_t T = q->size(0), heads = q->size(1);
     if (cache.heads < 1 || heads < 1 || heads % cache.heads) return nullptr;
-    const void *at = c.dense(starts, at::kInt, {(int64_t)cache.seqs + 1});
+    const int32_t *at = (const int32_t *)c.dense(starts, at::kInt, {(int64_t)cache.seqs + 1});
     at::Tensor out, lse;
     if (!c.ok || !output(c, o[14], q->scalar_type(), {T, heads, cache.dim}, *q, &out) ||
         !output(c, o[15], at::kFloat, {T, heads}, *q, &lse) || !stream_of(c, &st))
       return nullptr;
+    const void *qp = q->data_ptr();
+    const int type = type_of(q->scalar_type());
+    void *op = out.data_ptr();
+    float *lp = (float *)lse.data_ptr();
     const int rc = unlocked([&] {
-      return keops_paged_attention(&cache, q->data_ptr(), stride, type_of(q->scalar_type()), (int32_t)heads, (const int32_t *)at, T,
-                                   max_q, max_len, (float)scale, window, (float)decay, out.data_ptr(), (float *)lse.data_ptr(),
-                                   nullptr, 0, st);
+      return keops_paged_attention(&cache, qp, stride, type, (int32_t)heads, at, T, max_q, max_len, (float)scale, window,
+                                   (float)decay, op, lp, nullptr, 0, st);
     });
     return rc == KEOPS_OK ? pair(out, o[14], lse, o[15]) : nullptr;
   });
@@ -271,10 +283,8 @@ PyObject *evict(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (!output(c, o[11], at::kInt, {cache.seqs, cache.heads, budget}, *nt, &kept) ||
         !output(c, o[12], at::kInt, {cache.seqs}, *nt, &lens) || !stream_of(c, &st))
       return nullptr;
-    const int rc = unlocked([&] {
-      return keops_cache_evict(&cache, table, stride, width, budget, sink, recent, (int32_t *)kept.data_ptr(),
-                               (int32_t *)lens.data_ptr(), st);
-    });
+    int32_t *kp = (int32_t *)kept.data_ptr(), *lp = (int32_t *)lens.data_ptr();
+    const int rc = unlocked([&] { return keops_cache_evict(&cache, table, stride, width, budget, sink, recent, kp, lp, st); });
     return rc == KEOPS_OK ? pair(kept, o[11], lens, o[12]) : nullptr;
   });
 }
@@ -297,9 +307,9 @@ PyObject *verify(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (!c.ok || !output(c, o[6], at::kInt, {S, K + 1}, *target, &out) || !output(c, o[7], at::kInt, {S}, *target, &accepted) ||
         !stream_of(c, &st))
       return nullptr;
+    int32_t *op = (int32_t *)out.data_ptr(), *np = (int32_t *)accepted.data_ptr();
     const int rc = unlocked([&] {
-      return keops_verify_draft(tp, K ? dp : nullptr, xp, cp, ap, sp, (int32_t)S, (int32_t)K, (int32_t)V, (int32_t *)out.data_ptr(),
-                                (int32_t *)accepted.data_ptr(), nullptr, 0, st);
+      return keops_verify_draft(tp, K ? dp : nullptr, xp, cp, ap, sp, (int32_t)S, (int32_t)K, (int32_t)V, op, np, nullptr, 0, st);
     });
     return rc == KEOPS_OK ? pair(out, o[6], accepted, o[7]) : nullptr;
   });
