@@ -1,9 +1,11 @@
 // paged_evict.hip -- eviction from a paged cache by attention weight.
 //
-// Of a sequence's n slots each key/value head keeps `budget`: the first `sink`, the last
-// `recent`, and of those between the ones with the largest weights (equal weights: the lower
-// slot).  Kept slots move, in their order, to slots 0 .. of the pages in new_table, keys,
-// values and weights alike; n <= budget keeps them all.
+// Of a sequence's slots that are there each key/value head keeps `budget`: those among the
+// first `sink`, those among the last `recent`, and of the others the ones with the largest weights
+// (equal weights: the lower slot).  Kept slots move, in their order, to slots 0 .. of the pages in
+// new_table, keys, values and weights alike; where no more than `budget` are there, all of them.
+// A slot of a page that is not there is left out: a row kept for it would be one that nothing writes
+// and every later query sees.  (Pages are the same for all heads, so the heads keep equally many.)
 //
 // Selection: one work-group per (sequence, head) holds up to 32,768 weights in LDS as whole numbers of
 // the same order (longer rows are read again for each pass) and finds the smallest kept one by up to
@@ -32,9 +34,10 @@ constexpr int kQuad = 4;                // slots in a row of a thread
 constexpr int kGroup = kQuad * kSelectThreads;
 constexpr int kGroupsFew = 1, kGroupsMost = 8;   // groups of keys in LDS: 16 and 128 KB
 
-// Whole numbers ordered as the floats are; -0 equals 0, NaN above everything.
+// Whole numbers ordered as the floats are; -0 equals 0, NaN above everything but kForced.
+constexpr uint32_t kAbsent = 1u, kForced = 0xffffffffu;      // below and above the keys of all weights
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0xffffffffu;
+  if (w != w) return kForced - 1;
   const uint32_t b = __float_as_uint(w == 0.0f ? 0.0f : w);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
@@ -81,16 +84,31 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
   n64 = n64 < 0 ? 0 : (n64 > most ? most : n64);
   const int n = (int)n64;
   int32_t *kept = a.kept + ((int64_t)s * H + h) * a.budget;
-  if (h == 0 && tid == 0) a.new_lens[s] = n < a.budget ? n : a.budget;
-  if (n <= a.budget) {
+  const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
+  const uint32_t ps = a.c.page.d;
+  // slots of pages that are not there: they are left out, whatever their place
+  uint32_t lost = 0;
+  for (int64_t j = (int64_t)tid * ps; j < n; j += (int64_t)kSelectThreads * ps)
+    if ((uint32_t)trow[fast_div(a.c.page, (uint32_t)j)] >= a.c.pages) lost += n - j < (int64_t)ps ? (uint32_t)(n - j) : ps;
+  const uint32_t lost_upto = wave_scan_u32(lost);
+  if (lane == kWave - 1) sh.wave_sum[wave] = lost_upto;
+  __syncthreads();
+  uint32_t absent;
+  before_wave(sh.wave_sum, 0, &absent);
+  absent = __builtin_amdgcn_readfirstlane(absent);
+  const bool holes = absent != 0;
+  const int keep = n - (int)absent < a.budget ? n - (int)absent : a.budget;
+  if (h == 0 && tid == 0) a.new_lens[s] = keep;
+  if (!holes && n <= a.budget) {
     for (int r = tid; r < a.budget; r += kSelectThreads) kept[r] = r < n ? r : -1;
     return;
   }
-  const int sink = a.sink, recent = a.recent, need0 = a.budget - sink - recent;
+  // with holes the first and the last slots are chosen like the others, by a key above all weights'
+  const int sink = holes ? 0 : a.sink, recent = holes ? 0 : a.recent, need0 = keep - sink - recent;
   for (int r = tid; r < sink; r += kSelectThreads) kept[r] = r;
   for (int r = tid; r < recent; r += kSelectThreads) kept[a.budget - recent + r] = n - recent + r;
+  for (int r = keep + tid; r < a.budget; r += kSelectThreads) kept[r] = -1;
   if (need0 == 0) return;
-  const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
   // the slots in question, counted from `base0`: skip .. M - 1
   const int base0 = sink / kQuad * kQuad, skip = sink - base0, M = n - recent - base0;
   const int segments = (M + kSegment - 1) / kSegment;
@@ -103,14 +121,18 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) k[u] = sh.key[quad_at((g + u) * kSelectThreads + tid)];
   };
-  // Keys of a segment to LDS, each thread its own quadruples.  An absent slot's is 1, below every weight's, and
+  // Keys of a segment to LDS, each thread its own quadruples.  An absent slot's is below every weight's, and
   // that of a place outside skip .. M is 0: it is never among the largest that there are.
   const auto put = [&](int g, int i, u32x4 k) {      // slots i .. of group g
+    if (holes) {                                     // base0 is 0
+#pragma unroll
+      for (int e = 0; e < kQuad; ++e)
+        if (k[e] != kAbsent && (i + e < a.sink || i + e >= n - a.recent)) k[e] = kForced;
+    }
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) k[e] = i + e >= skip && i + e < M ? k[e] : 0u;
     sh.key[quad_at(g * kSelectThreads + tid)] = k;
   };
-  const uint32_t ps = a.c.page.d;
   const bool whole = ps % kQuad == 0 && ((uintptr_t)a.c.weights & 15) == 0;   // a quadruple in one page, aligned
   const auto load = [&](int from) {
     const int groups = groups_of(from);
@@ -139,7 +161,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         if (g >= groups) break;
-        u32x4 k = (u32x4){1, 1, 1, 1};
+        u32x4 k = (u32x4){kAbsent, kAbsent, kAbsent, kAbsent};
         if (page[g] < a.c.pages)
           k = (u32x4){weight_key(w[g][0]), weight_key(w[g][1]), weight_key(w[g][2]), weight_key(w[g][3])};
         put(g, from + g * kGroup + tid * kQuad, k);
@@ -148,7 +170,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     }
 #pragma unroll 2
     for (int g = 0; g < groups; ++g) {
-      u32x4 k = (u32x4){1, 1, 1, 1};
+      u32x4 k = (u32x4){kAbsent, kAbsent, kAbsent, kAbsent};
 #pragma unroll
       for (int e = 0; e < kQuad; ++e) {
         const int i = from + g * kGroup + tid * kQuad + e;

@@ -225,7 +225,8 @@ def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, bu
                       new_lens=None, stream=None):
     """Keep ``budget`` slots of every sequence and head: the first ``sink``, the last ``recent``, and those with
     the largest weights; move them to the pages of ``new_table``.  Returns (kept [sequences, heads, budget]
-    old slot numbers or -1, new lens).  The scales of an 8-bit cache are not needed."""
+    old slot numbers or -1, new lens).  Slots whose page the table lacks are left out, and not counted in the
+    new lens.  The scales of an 8-bit cache are not needed."""
     if stream is None:
         short = _short or _native()
         got = short and short.evict(k_pages, v_pages, weights, page_table, lens, None, None, new_table, budget, sink, recent, kept,

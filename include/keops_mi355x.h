@@ -319,14 +319,16 @@ int keops_paged_attention_workspace(const keops_cache_t *cache, int32_t type, in
                                     int32_t max_q, int32_t max_len, int32_t window, int64_t *bytes);
 
 /*
- * Eviction by attention weight.  Each key/value head of a sequence with more than `budget`
- * slots keeps the first `sink`, the last `recent`, and of the others the
- * budget - sink - recent with the largest weights (equal weights: the lower slot; NaN is
- * largest; an absent slot smallest); a shorter sequence keeps all.  Kept slots move in their
+ * Eviction by attention weight.  Of a sequence's slots that are not absent each key/value
+ * head keeps `budget`: those among the first `sink` slots, those among the last `recent`, and
+ * of the others the ones with the largest weights (equal weights: the lower slot; NaN is
+ * largest); where there are no more than `budget`, all.  Absent slots are left out, so a table
+ * with holes ends without them.  Kept slots move in their
  * order to slots 0 .. of the pages of new_table ([seqs][new_width], rows new_stride apart):
  * keys, values and weights.  Pages of new_table are none of page_table's, and no page is in
  * new_table twice (their contents are undefined otherwise).
- * kept: [seqs][heads][budget], the old slot numbers, -1 past the end; new_lens: [seqs].
+ * kept: [seqs][heads][budget], the old slot numbers, -1 past the end; new_lens: [seqs], the
+ * smaller of `budget` and the slots that are not absent.
  * new_width >= min(ceil(budget / page_size), table_width); 1 <= budget, sink + recent <= budget.
  */
 int keops_cache_evict(const keops_cache_t *cache, const int32_t *new_table, int64_t new_stride, int32_t new_width,

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_reference as ref
-from test_gpu_paged import put, say
+from test_gpu_paged import BF, E4, FP, close, put, say
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,81 @@ def test_batched_tensors_are_refused():
         torch.vmap(lambda t: (gm.keops_cache_append(t, t, k, v, table, lens, starts), t)[1])(torch.stack([rows, rows]))
     got = gm.keops_paged_attention(q, k, v, table, lens, starts, 2, 20)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---- eviction from tables with holes
+
+def evict_reference(b, new_table, budget, sink, recent):
+    """From the definition: of the slots that are there the ones among the first `sink` and the last `recent`, and the
+    heaviest of the others (NaN above all; equal weights: the lower slot), `budget` in all, in their order."""
+    S, H = len(b.lens), b.kv
+    kept, lens = torch.full((S, H, budget), -1, dtype=torch.int32), torch.zeros(S, dtype=torch.int32)
+    k, v, w = b.k.clone(), b.v.clone(), b.weights.clone()
+    for s, n in enumerate(b.lens):
+        there = [j for j in range(n) if 0 <= b.table[s, j // b.page].item() < b.P]
+        lens[s] = min(budget, len(there))
+        for h in range(H):
+            def rank(j):
+                x = b.weights[b.table[s, j // b.page].item(), h, j % b.page].item()
+                if j < sink or j >= n - recent:
+                    return (0, 0.0, j)
+                return (1, 0.0, j) if x != x else (2, -x, j)
+            for r, j in enumerate(sorted(sorted(there, key=rank)[:budget])):
+                kept[s, h, r] = j
+                pg, to = b.table[s, j // b.page].item(), new_table[s, r // b.page].item()
+                k.view(torch.uint8)[to, r % b.page, h] = b.k.view(torch.uint8)[pg, j % b.page, h]
+                v.view(torch.uint8)[to, r % b.page, h] = b.v.view(torch.uint8)[pg, j % b.page, h]
+                w[to, h, r % b.page] = b.weights[pg, h, j % b.page]
+    return kept, lens, k, v, w
+
+
+# lens, page, cache, budget, sink, recent, the pages of the table that are missing
+HOLES = [
+    ([100, 33], 16, BF, 200, 4, 20, [(0, 2), (1, 0)]),                     # all kept but for the holes
+    ([100, 90], 16, BF, 60, 20, 30, [(0, 0), (0, 6), (1, 1), (1, 5)]),     # holes among the first and the last
+    ([100, 40], 16, FP, 70, 0, 0, [(0, 1), (0, 3), (0, 4), (1, 0), (1, 1), (1, 2)]),   # fewer there than the budget; none at all
+    ([64, 64], 6, E4, 50, 7, 9, [(0, 0), (0, 1), (1, 10)]),
+    ([40], 1, BF, 35, 3, 3, [(0, 0), (0, 39), (0, 20)]),
+    ([9000], 16, BF, 4000, 10, 1000, [(0, 0), (0, 300), (0, 562)]),
+    ([40000], 64, BF, 39990, 4, 100, [(0, 1), (0, 624)]),                  # longer than what LDS holds; fewer there than the budget
+    ([40000], 24, BF, 500, 30, 100, [(0, 0), (0, 1666)]),
+]
+
+
+@pytest.mark.parametrize("lens,page,cache,budget,sink,recent,missing", HOLES)
+@pytest.mark.parametrize("ties", [False, True])
+def test_eviction_leaves_out_absent_slots(lens, page, cache, budget, sink, recent, missing, ties):
+    """An absent slot is not kept, and nothing of what the new pages held before is seen afterwards."""
+    say(f"eviction with holes, {lens} page {page} {cache} budget {budget} sink {sink} recent {recent} missing {missing} ties {ties}")
+    H, dim, S = (2 if lens[0] < 1000 else 1), 64, len(lens)
+    more = sum(-(-min(n, budget) // page) for n in lens)
+    b = ref.Batch(89, lens, [0] * S, H, H, dim, page, FP if cache == FP else BF, cache, spare=more + 1)
+    b.weights = torch.rand((b.P, H, page), generator=b.gen)
+    if ties:
+        b.weights = (b.weights * 3).floor() / 2
+        b.weights.view(-1)[::13] = float("nan")
+        b.weights.view(-1)[::17] = float("inf")
+    for n, (s, at) in enumerate(missing):
+        b.table[s, at] = (-1, b.P, 2 ** 31 - 1)[n % 3]
+    new = torch.full((S, max(-(-min(n, budget) // page) for n in lens)), -1, dtype=torch.int32)
+    at = 0
+    for s, n in enumerate(lens):
+        u = -(-min(n, budget) // page)
+        new[s, :u] = b.free[at:at + u]
+        at += u
+    kp, vp, wp = put(b.k), put(b.v), put(b.weights)
+    kept, nl = gm.keops_cache_evict(kp, vp, wp, put(b.table), put(b.lens_t()), put(new), budget, sink=sink, recent=recent)
+    torch.cuda.synchronize()
+    rkept, rl, rk, rv, rw = evict_reference(b, new, budget, sink, recent)
+    for name, got, want in (("lens", nl, rl), ("kept", kept, rkept), ("keys", kp, rk), ("values", vp, rv), ("weights", wp, rw)):
+        same = torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
+        assert same, name
+    # a token of each sequence over what is left: the pools' other rows hold NaN
+    b.table, b.lens, b.new, b.k, b.v = new, rl.tolist(), [1] * S, rk, rv
+    b.T, b.starts = S, torch.arange(S + 1, dtype=torch.int32)
+    b.q = (torch.randn((S, H, dim), generator=b.gen) * 2).to(b.dtype)
+    out, lse = gm.keops_paged_attention(put(b.q), kp, vp, put(new), nl, put(b.starts), 1, max(b.lens), k_scale=put(b.k_scale),
+                                        v_scale=put(b.v_scale))
+    o, z, _, ot, zt, _ = ref.attention(b)
+    close(lse.cpu(), z, zt, "lse")
+    close(out.cpu(), o, ot, "out")
