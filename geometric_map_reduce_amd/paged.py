@@ -145,18 +145,28 @@ def _run(name, dev, stream, fn, *args):
         _check(name, rc)
 
 
-def _keep(stream, dev, *tensors):
-    """Tensors made here for a call on another stream than the current one belong to that stream too."""
+def _other(stream, dev):
+    """The stream that a call names, where it is not the current one; else None.
+
+    What the call makes comes from that stream's memory: a block of the current stream's may still be in use by
+    work queued there, of which the other stream knows nothing."""
+    if stream is None:
+        return None
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
-    if s.cuda_stream != torch.cuda.current_stream(dev).cuda_stream:
+    return None if s.cuda_stream == torch.cuda.current_stream(dev).cuda_stream else s
+
+
+def _keep(other, dev, *tensors):
+    """Outputs made on another stream than the current one, where the caller reads them, belong to that too."""
+    if other is not None:
         for t in tensors:
             if t is not None:
-                t.record_stream(s)
+                t.record_stream(torch.cuda.current_stream(dev))
 
 
 def _graph_workspace(name, dev, *args):
-    """(address, bytes, tensor) of a call's workspace under stream capture, from the graph's own pool, where it
-    lives as long as the graph; nothing otherwise: the library has its own."""
+    """(address, bytes, tensor) of a call's workspace where the current stream is captured, from the graph's own
+    pool, where it lives as long as the graph; nothing otherwise: the library has its own."""
     if not torch.cuda.is_current_stream_capturing():
         return None, 0, None
     need = ctypes.c_int64(0)
@@ -209,15 +219,16 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
     if min(max_q, max_len, window) < 0 or max(max_q, max_len, window) > 2**31 - 1:
         raise ValueError("max_q, max_len and window must be in [0, 2^31)")
     kind = _TYPES[q.dtype]
-    made = (None if out is not None else torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, heads, D)),
-            None if lse is not None else q.new_empty((T, heads), dtype=torch.float32))
-    out = made[0] if out is None else _out(out, (T, heads, D), q.device, q.dtype)
-    lse = made[1] if lse is None else _out(lse, (T, heads), q.device, name="lse")
-    ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, c, kind, heads, T, max_q, max_len, window)
+    other = _other(stream, dev)
+    with torch.cuda.stream(other):
+        made = (None if out is not None else torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, heads, D)),
+                None if lse is not None else q.new_empty((T, heads), dtype=torch.float32))
+        out = made[0] if out is None else _out(out, (T, heads, D), q.device, q.dtype)
+        lse = made[1] if lse is None else _out(lse, (T, heads), q.device, name="lse")
+        ws, nbytes, buf = _graph_workspace("keops_paged_attention", dev, c, kind, heads, T, max_q, max_len, window)
     _run("keops_paged_attention", dev, stream, lib().keops_paged_attention, c, qp, qs, kind, heads, st, T, max_q, max_len,
          1.0 / math.sqrt(D) if scale is None else float(scale), window, float(decay), out.data_ptr(), lse.data_ptr(), ws, nbytes)
-    if stream is not None:
-        _keep(stream, dev, *made, buf)
+    _keep(other, dev, *made)
     return out, lse
 
 
@@ -242,14 +253,15 @@ def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, bu
         raise ValueError("need 1 <= budget < 2^31, sink >= 0, recent >= 0 and sink + recent <= budget")
     if nwidth < min(-(-budget // ps), width):
         raise ValueError("new_table has too few pages for the budget")
-    made = (None if kept is not None else torch.empty((S, H, budget), dtype=torch.int32, device=k_pages.device),
-            None if new_lens is not None else torch.empty((S,), dtype=torch.int32, device=k_pages.device))
+    other = _other(stream, dev)
+    with torch.cuda.stream(other):
+        made = (None if kept is not None else torch.empty((S, H, budget), dtype=torch.int32, device=k_pages.device),
+                None if new_lens is not None else torch.empty((S,), dtype=torch.int32, device=k_pages.device))
     kept = made[0] if kept is None else _out(kept, (S, H, budget), k_pages.device, torch.int32, name="kept")
     new_lens = made[1] if new_lens is None else _out(new_lens, (S,), k_pages.device, torch.int32, name="new_lens")
     _run("keops_cache_evict", dev, stream, lib().keops_cache_evict, c, nt, nstride, nwidth, budget, sink, recent,
          kept.data_ptr(), new_lens.data_ptr())
-    if stream is not None:
-        _keep(stream, dev, *made)
+    _keep(other, dev, *made)
     return kept, new_lens
 
 
@@ -274,13 +286,14 @@ def keops_verify_draft(target, draft, tokens, counts, u_accept, u_sample, out=No
     dp = None if draft is None else _vec(draft, "draft", (S, K, V), f32, dev)
     xp, cp = _vec(tokens, "tokens", (S, K), i32, dev), _vec(counts, "counts", (S,), i32, dev)
     ap, sp = _vec(u_accept, "u_accept", (S, K), f32, dev), _vec(u_sample, "u_sample", (S,), f32, dev)
-    made = (None if out is not None else torch.empty((S, K + 1), dtype=i32, device=target.device),
-            None if accepted is not None else torch.empty((S,), dtype=i32, device=target.device))
-    out = made[0] if out is None else _out(out, (S, K + 1), target.device, i32)
-    accepted = made[1] if accepted is None else _out(accepted, (S,), target.device, i32, name="accepted")
-    ws, nbytes, buf = _graph_workspace("keops_verify_draft", dev, S, K, V)
+    other = _other(stream, dev)
+    with torch.cuda.stream(other):
+        made = (None if out is not None else torch.empty((S, K + 1), dtype=i32, device=target.device),
+                None if accepted is not None else torch.empty((S,), dtype=i32, device=target.device))
+        out = made[0] if out is None else _out(out, (S, K + 1), target.device, i32)
+        accepted = made[1] if accepted is None else _out(accepted, (S,), target.device, i32, name="accepted")
+        ws, nbytes, buf = _graph_workspace("keops_verify_draft", dev, S, K, V)
     _run("keops_verify_draft", dev, stream, lib().keops_verify_draft, tp, dp if K else None, xp, cp, ap, sp, S, K, V, out.data_ptr(),
          accepted.data_ptr(), ws, nbytes)
-    if stream is not None:
-        _keep(stream, dev, *made, buf)
+    _keep(other, dev, *made)
     return out, accepted

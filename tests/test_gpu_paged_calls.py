@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_reference as ref
-from test_gpu_paged import BF, E4, FP, close, put, say
+from test_gpu_paged import BF, E4, FP, close, put, say, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,55 @@ def test_eviction_leaves_out_absent_slots(lens, page, cache, budget, sink, recen
     o, z, _, ot, zt, _ = ref.attention(b)
     close(lse.cpu(), z, zt, "lse")
     close(out.cpu(), o, ot, "out")
+
+
+# ---- streams
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_of_another_stream_are_its_own(handle):
+    """A block of the output's size is free in the current stream's pool, with a write to it still queued there."""
+    say(f"outputs of another stream, its handle {handle}")
+    b = ref.Batch(19, [500, 300], [1, 1], 8, 2, 128, 16, junk=0.0)
+    b.weights = torch.rand((b.P, 2, 16), generator=b.gen)
+    args = [put(t) for t in (b.q, b.k, b.v, b.table, b.lens_t(), b.starts)]
+    free = torch.arange(b.P, b.P + 40, dtype=torch.int32)[None].repeat(2, 1)         # pages that are not there: nothing moves
+    ver = [put(t) for t in verify_case(5, 2, 3, 5000)]
+    w = put(b.weights)
+
+    def calls(s):
+        return (*gm.keops_paged_attention(*args, 1, 500, stream=s),
+                *gm.keops_cache_evict(args[1], args[2], w, args[3], args[4], free.cuda(), 64, recent=9, stream=s),
+                *gm.keops_verify_draft(*ver, stream=s))
+    want = calls(None)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                       # 8 ms of the current stream, or more
+    for t in want:
+        x = torch.full_like(t, 77)                      # queued behind it
+        del x
+    got = calls(st.cuda_stream if handle else st)
+    st.synchronize()
+    on_time = [t.clone() for t in got]                  # read behind the sleep and the writes
+    torch.cuda.synchronize()
+    for x, y in zip(on_time, want):
+        assert torch.equal(x, y)
+
+
+def test_capture_of_the_stream_that_is_given():
+    """The workspace of a call on a captured stream is the graph's, whichever stream is current."""
+    say("a captured stream that is not the current one")
+    b = ref.Batch(23, [900, 300], [1, 1], 8, 2, 128, 16, junk=0.0)
+    args = [put(t) for t in (b.q, b.k, b.v, b.table, b.lens_t(), b.starts)]
+    want = gm.keops_paged_attention(*args, 1, 900)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            out, lse = gm.keops_paged_attention(*args, 1, 900, stream=side)
+    for _ in range(3):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        gm.keops_paged_attention(*args, 1, 900)
