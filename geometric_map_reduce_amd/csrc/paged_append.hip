@@ -5,8 +5,9 @@
 // for every token t of every sequence s (8-bit caches: the e4m3 value nearest to
 // k / k_scale[h], cut to +-448), and weight 0 for the slot where weights are kept.  A copy:
 // each element is read once and written once, so memory bounds a long prompt (16,384 tokens of 8 x 128
-// bf16 with weights: 28 us a call, 4.8 TB/s, the rate of a large copy) and the chain starts -> lens ->
-// table -> store a single step (64 sequences: 3.5 us of the GPU's time, a launch and four loads).
+// bf16 with weights: 28 us a call, 4.8 TB/s, the rate of a large copy) and a chain of loads a single
+// step: the halving of starts, its own start and length, the table's entry (64 sequences: nine loads in turn, 3.5 us
+// of the GPU's time with the launch).
 #include "paged.h"
 
 namespace kmi {
@@ -44,10 +45,11 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
     if (a.starts[mid] <= t) lo = mid; else hi = mid;
   }
   if (!live) return;
-  const int64_t b0 = a.starts[lo], b1 = a.starts[lo + 1];
-  if (t < b0 || t >= b1) return;
-  const int64_t j = (int64_t)a.c.lens[lo] - (b1 - b0) + (t - b0);
-  if (j < 0 || j > 0x7fffffff) return;
+  // the slot that attention takes the token to be in, starts outside the tokens included
+  const SeqSpan sp = seq_span(a.starts, a.c.lens, lo, a.tokens, 0x7fffffff, 0x7fffffff);
+  if (t < sp.t0 || t >= sp.t0 + sp.m) return;
+  const int64_t j = sp.first + (t - sp.t0);
+  if (j < 0) return;
   const SlotPlace p = slot_place(a.c, a.c.table + (int64_t)lo * a.c.table_stride, (uint32_t)j);
   if (p.page < 0) return;
   const int h = e * 8 / a.c.dim, d = e * 8 - h * a.c.dim;

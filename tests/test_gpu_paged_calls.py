@@ -163,3 +163,45 @@ def test_capture_of_the_stream_that_is_given():
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
         gm.keops_paged_attention(*args, 1, 900)
+
+
+# ---- starts outside the tokens
+
+@pytest.mark.parametrize("starts,tokens,lens,want", [
+    ([0, 5], 3, [10], [(0, 7, 0), (0, 8, 1), (0, 9, 2)]),
+    ([-4, 2], 5, [10], [(0, 8, 0), (0, 9, 1)]),
+    ([3, 9, 20], 6, [10, 12], [(0, 7, 3), (0, 8, 4), (0, 9, 5)]),
+    ([0, 2, 2 ** 31 - 1], 4, [2, 7], [(0, 0, 0), (0, 1, 1), (1, 5, 2), (1, 6, 3)]),
+    ([0, 9], 4, [3], [(0, 0, 1), (0, 1, 2), (0, 2, 3)]),
+])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, E4)])
+def test_append_cuts_starts_as_attention_does(starts, tokens, lens, want, dtype, cache):
+    """Starts outside [0, tokens] are cut to them: (sequence, slot, token) of each row that is written; attention of the
+    same call sees each token in that slot."""
+    say(f"append, starts {starts} of {tokens} tokens, {dtype} {cache}")
+    S = len(lens)
+    b = ref.Batch(97, lens, [0] * S, 2, 2, 64, 4, dtype, cache, junk=0.0)
+    b.weights = torch.rand((b.P, 2, 4), generator=b.gen) + 1
+    rows = (torch.randn((tokens, 2, 64), generator=b.gen) * 2).to(dtype)
+    b.starts = torch.tensor(starts, dtype=torch.int32)
+    rk, rv, rw = b.k.clone(), b.v.clone(), b.weights.clone()
+    for s, j, t in want:
+        pg = b.table[s, j // 4].item()
+        for h in range(2):
+            for pool, scale in ((rk, b.k_scale), (rv, b.v_scale)):
+                x = rows[t, h] if scale is None else (rows[t, h].float() / scale[h]).clamp(-448, 448)
+                pool.view(torch.uint8)[pg, j % 4, h] = x.to(cache).view(torch.uint8)
+        rw[pg, :, j % 4] = 0.0
+    kp, vp, wp, k = put(b.k), put(b.v), put(b.weights), put(rows)
+    gm.keops_cache_append(k, k, kp, vp, put(b.table), put(b.lens_t()), put(b.starts), weights=wp, k_scale=put(b.k_scale),
+                          v_scale=put(b.v_scale))
+    torch.cuda.synchronize()
+    for name, got, rest in (("keys", kp, rk), ("values", vp, rv), ("weights", wp, rw)):
+        same = torch.equal(got.cpu().view(torch.uint8), rest.view(torch.uint8))
+        assert same, name
+    # a window of one slot: each token gets the value of its own
+    out, _ = gm.keops_paged_attention(k, kp, vp, put(b.table), put(b.lens_t()), put(b.starts), tokens, 16, window=1, k_scale=put(b.k_scale),
+                                      v_scale=put(b.v_scale))
+    for s, j, t in want:
+        v, _ = b.rows(rv, b.v_scale, s, 0, lens[s])
+        assert (out[t, 0].double().cpu() - v[j]).abs().max() <= torch.finfo(dtype).eps * v[j].abs().max(), (s, j, t)
