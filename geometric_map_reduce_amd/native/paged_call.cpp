@@ -5,8 +5,10 @@
 // address from Python takes as long.  Each function here checks what the C ABI cannot see (types,
 // devices, shapes, strides), allocates the outputs and makes the call.  It returns None, with nothing
 // enqueued, for whatever is not plain and right: a wrong argument, another device than the current one,
-// a status.  paged.py then takes the call through its own checks, which name what is wrong, or through
-// a graph's workspace.  Enqueueing one conversation's step took 15.3 us by way of Python alone.
+// a status that the C ABI decides before its first launch.  paged.py then takes the call through its own
+// checks, which name what is wrong, or through a graph's workspace.  A HIP error may come after a launch:
+// its status is returned, and the call is not made again.  Enqueueing one conversation's step took 15.3 us
+// by way of Python alone.
 #include <Python.h>
 
 #include <torch/csrc/autograd/python_variable.h>
@@ -193,6 +195,13 @@ PyObject *pair(const at::Tensor &a, PyObject *a_given, const at::Tensor &b, PyOb
   return r;
 }
 
+// What a call ends with.  `result` was made before it, so that nothing can fail once work is enqueued.
+PyObject *ended(int rc, PyObject *result) {
+  if (rc == KEOPS_OK) return result;
+  Py_DECREF(result);
+  return rc == KEOPS_ERR_HIP ? PyLong_FromLong(rc) : nullptr;
+}
+
 // An output: the caller's dense tensor, or a new one.
 bool output(Call &c, PyObject *given, at::ScalarType type, at::IntArrayRef shape, const at::Tensor &like, at::Tensor *out) {
   if (given != Py_None) {
@@ -206,7 +215,7 @@ bool output(Call &c, PyObject *given, at::ScalarType type, at::IntArrayRef shape
   return true;
 }
 
-// (k, v, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts) -> True
+// (k, v, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts) -> True; here and below a status, or None
 PyObject *append(PyObject *, PyObject *const *o, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject * {
     Call c;
@@ -224,7 +233,7 @@ PyObject *append(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int type = type_of(k->scalar_type());
     const int64_t T = k->size(0);
     const int rc = unlocked([&] { return keops_cache_append(&cache, kp, vp, ks, vs, type, at, T, st); });
-    return rc == KEOPS_OK ? Py_NewRef(Py_True) : nullptr;
+    return ended(rc, Py_NewRef(Py_True));
   });
 }
 
@@ -244,21 +253,23 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const double scale = o[11] == Py_None ? 1.0 / std::sqrt((double)cache.dim) : PyFloat_AS_DOUBLE(o[11]);
     const double decay = PyFloat_AS_DOUBLE(o[13]);
     const int64_t T = q->size(0), heads = q->size(1);
+    const void *qp = q->data_ptr();
     if (cache.heads < 1 || heads < 1 || heads % cache.heads) return nullptr;
     const int32_t *at = (const int32_t *)c.dense(starts, at::kInt, {(int64_t)cache.seqs + 1});
     at::Tensor out, lse;
     if (!c.ok || !output(c, o[14], q->scalar_type(), {T, heads, cache.dim}, *q, &out) ||
         !output(c, o[15], at::kFloat, {T, heads}, *q, &lse) || !stream_of(c, &st))
       return nullptr;
-    const void *qp = q->data_ptr();
     const int type = type_of(q->scalar_type());
     void *op = out.data_ptr();
     float *lp = (float *)lse.data_ptr();
+    PyObject *result = pair(out, o[14], lse, o[15]);
+    if (!result) return nullptr;
     const int rc = unlocked([&] {
       return keops_paged_attention(&cache, qp, stride, type, (int32_t)heads, at, T, max_q, max_len, (float)scale, window,
                                    (float)decay, op, lp, nullptr, 0, st);
     });
-    return rc == KEOPS_OK ? pair(out, o[14], lse, o[15]) : nullptr;
+    return ended(rc, result);
   });
 }
 
@@ -284,8 +295,10 @@ PyObject *evict(PyObject *, PyObject *const *o, Py_ssize_t n) {
         !output(c, o[12], at::kInt, {cache.seqs}, *nt, &lens) || !stream_of(c, &st))
       return nullptr;
     int32_t *kp = (int32_t *)kept.data_ptr(), *lp = (int32_t *)lens.data_ptr();
+    PyObject *result = pair(kept, o[11], lens, o[12]);
+    if (!result) return nullptr;
     const int rc = unlocked([&] { return keops_cache_evict(&cache, table, stride, width, budget, sink, recent, kp, lp, st); });
-    return rc == KEOPS_OK ? pair(kept, o[11], lens, o[12]) : nullptr;
+    return ended(rc, result);
   });
 }
 
@@ -308,10 +321,12 @@ PyObject *verify(PyObject *, PyObject *const *o, Py_ssize_t n) {
         !stream_of(c, &st))
       return nullptr;
     int32_t *op = (int32_t *)out.data_ptr(), *np = (int32_t *)accepted.data_ptr();
+    PyObject *result = pair(out, o[6], accepted, o[7]);
+    if (!result) return nullptr;
     const int rc = unlocked([&] {
       return keops_verify_draft(tp, K ? dp : nullptr, xp, cp, ap, sp, (int32_t)S, (int32_t)K, (int32_t)V, op, np, nullptr, 0, st);
     });
-    return rc == KEOPS_OK ? pair(out, o[6], accepted, o[7]) : nullptr;
+    return ended(rc, result);
   });
 }
 

@@ -10,7 +10,8 @@ the host and never synchronise.
 
 Each call first goes the short way (native/paged_call.cpp), which takes plain arguments on the
 current stream in a microsecond or two and hands back, undone, whatever is anything else; that is
-taken, or refused by name, here.
+taken, or refused by name, here.  A HIP error is raised as it comes: some of a call's launches may
+have been made by then, so the call is not made again.
 """
 from __future__ import annotations
 
@@ -113,6 +114,13 @@ def _native():
     return _short
 
 
+def _ended(name, got):
+    """What the short way gave; raises on a status."""
+    if type(got) is int:
+        _check(name, got)
+    return got
+
+
 _HALF = (torch.bfloat16, torch.float16)
 
 
@@ -184,7 +192,9 @@ def keops_cache_append(k, v, k_pages, v_pages, page_table, lens, starts, weights
     (``lens`` counts them already); clear those slots' ``weights``."""
     if stream is None:
         short = _short or _native()
-        if short and short.append(k, v, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts):
+        got = short and short.append(k, v, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts)
+        if got:
+            _ended("keops_cache_append", got)
             return
     c, dev, S, cache, _, _ = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
     kp, ks = _rows(k, "k", cache[0], cache, dev)
@@ -208,7 +218,7 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
         got = short and short.attention(q, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts, max_q, max_len,
                                         scale, window, decay, out, lse)
         if got:
-            return got
+            return _ended("keops_paged_attention", got)
     c, dev, S, cache, _, _ = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale)
     qp, qs = _rows(q, "q", None, cache, dev)
     T, heads, D = q.shape
@@ -243,7 +253,7 @@ def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, bu
         got = short and short.evict(k_pages, v_pages, weights, page_table, lens, None, None, new_table, budget, sink, recent, kept,
                                     new_lens)
         if got:
-            return got
+            return _ended("keops_cache_evict", got)
     c, dev, S, (H, _, _), ps, width = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
     if weights is None:
         raise ValueError("eviction needs weights")
@@ -273,7 +283,7 @@ def keops_verify_draft(target, draft, tokens, counts, u_accept, u_sample, out=No
         short = _short or _native()
         got = short and short.verify(target, draft, tokens, counts, u_accept, u_sample, out, accepted)
         if got:
-            return got
+            return _ended("keops_verify_draft", got)
     _tensor(target, "target"), _tensor(tokens, "tokens")
     dev = target.get_device()
     if target.dim() != 3 or dev < 0 or tokens.dim() != 2:

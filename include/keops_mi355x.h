@@ -45,7 +45,8 @@
  *             threads on different streams.  Calls running concurrently on
  *             one GPU do not share memory.
  *  Errors:    0 = KEOPS_OK, negative = error (see below); no exception ever
- *             crosses the ABI, and on an error nothing has been enqueued.
+ *             crosses the ABI, and on an error nothing has been enqueued (but after
+ *             KEOPS_ERR_HIP, where some of a call's launches may have been).
  *  Sizes:     M = 0 is a no-op.  N = 0: sums and gradients are 0, LogSumExp
  *             is -inf; K-min needs 1 <= K <= N.
  *  Supported: D in 1..8, 16, 32, 50, 64, 100; E in 1..4; K in 1..16 or 32.

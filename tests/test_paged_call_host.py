@@ -106,3 +106,36 @@ def test_batched_tensors_are_handed_back(built):
     code = f"import sys; sys.path.insert(0, {HERE!r}); import test_paged_call_host as t; t.every_batched_argument({built!r})"
     res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, f"ended with {res.returncode} after\n{res.stdout}\n{res.stderr[-2000:]}"
+
+
+INVALID, UNSUPPORTED, ALLOC, HIP, SCRATCH = -1, -2, -3, -4, -5
+
+
+@pytest.mark.parametrize("outputs", [False, True])
+def test_statuses(built, outputs):
+    """What an entry point refuses before it enqueues anything is handed back, to be named by the long way.  A HIP error
+    may come after a launch: it is given back as it is, and the call is not repeated."""
+    short, stub = load(built)
+    for status in (INVALID, UNSUPPORTED, ALLOC, HIP, SCRATCH):
+        for name, args in arguments(outputs).items():
+            stub.stub_set(status)
+            got = getattr(short, name)(*args)
+            assert stub.stub_calls() == 1
+            assert got is None if status != HIP else type(got) is int and got == HIP, (name, status, got)
+
+
+@pytest.mark.parametrize("name,call", [
+    ("append", lambda m, a: m.keops_cache_append(*a[:4], *a[5:7], a[9])),
+    ("attention", lambda m, a: m.keops_paged_attention(*a[:3], *a[4:6], a[8], 1, 16)),
+    ("evict", lambda m, a: m.keops_cache_evict(*a[:5], a[7], 4)),
+    ("verify", lambda m, a: m.keops_verify_draft(*a[:6]))])
+def test_a_hip_error_is_raised_once(built, monkeypatch, name, call):
+    from geometric_map_reduce_amd import KeopsError, binding, paged
+    short, stub = load(built)
+    monkeypatch.setattr(paged, "_short", short)
+    monkeypatch.setattr(binding, "status_string", lambda rc: "HIP error")
+    monkeypatch.setattr(paged, "_run", lambda *a: pytest.fail("the call went the long way too"))
+    stub.stub_set(HIP)
+    with pytest.raises(KeopsError) as e:
+        call(paged, arguments()[name])
+    assert e.value.status == HIP and stub.stub_calls() == 1
