@@ -36,6 +36,13 @@ constexpr int64_t kJoinParts = 192;
 // and 51 us.  Lengths may fall short of their bound, so not at 256 MB itself.
 constexpr double kFarBytes = 384e6;
 
+// Kept scores take 4 bytes a row and slot of the call's bounds, which may lie far above its lengths; a slot's are
+// a quarter of its key and value at most, so more than twice the pool means bounds of eight times what it holds.
+// Past that, and past 4 GB, the weights come from the column sums instead, which need no scores.  They cost 64
+// sequences of 4,000 slots (4 rows, 8 heads of 128, bounds of 131,072) 474 us in place of 311, 16 of 20,000 slots
+// (32 rows) 462 in place of 604.  Up to half a GB is a five-hundredth of the device's memory, and always taken.
+constexpr double kScoresAlways = 512e6, kScoresMost = 4294967296.0;
+
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
 int64_t width_of(int type) { return type == KEOPS_TYPE_E4M3 ? 1 : 2; }
@@ -122,7 +129,12 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
   const int64_t G = heads / c.heads, rows = max_q * G, S = c.seqs, H = c.heads;
   p->few = rows <= kFewRowsMax;
   // keeping a row's scores costs 8 bytes a slot, reading K again dim times its width
-  p->scores = c.weights && p->few && rows * 8 <= c.dim * width_of(c.type);
+  const double heads_of_seqs = (double)S * (double)H;
+  const double score_bytes = 4.0 * heads_of_seqs * (double)rows * (double)(ceil_div(max_len, 32) * 32);
+  const double pool_bytes = 2.0 * (double)c.pages * c.page_size * (double)H * (double)(c.dim * width_of(c.type));
+  const bool sums_fit = heads_of_seqs * (double)ceil_div(max_len, kSumSlotsTile) <= (double)kMaxGrid / 1024;
+  p->scores = c.weights && p->few && rows * 8 <= c.dim * width_of(c.type) &&
+              (score_bytes <= std::max(kScoresAlways, std::min(2.0 * pool_bytes, kScoresMost)) || !sums_fit);
   // slots that the rows of one sequence see at most
   int64_t span = max_len;
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + max_q - 1);
@@ -163,12 +175,12 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     if (p->scores) {
       p->score_rows = (int)rows;
       p->score_stride = ceil_div(max_len, 32) * 32;
-      if (4.0 * (double)S * (double)H * (double)rows * (double)p->score_stride > kMaxWorkspace) return KEOPS_ERR_ALLOC;
+      if (score_bytes > kMaxWorkspace) return KEOPS_ERR_ALLOC;
       p->score_bytes = align256(4 * S * H * rows * p->score_stride);
       if ((double)S * (double)H * (double)(ceil_div(max_len, 256) + rows * 8) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
     } else {
       const int64_t nst = ceil_div(max_len, kSumSlotsTile);
-      if ((double)S * (double)H * (double)nst > (double)kMaxGrid / 1024) return KEOPS_ERR_UNSUPPORTED;
+      if (!sums_fit) return KEOPS_ERR_UNSUPPORTED;
       const int64_t wgs = S * H * nst;
       // slots outside every window cost next to nothing
       const int64_t busy = std::max<int64_t>(1, S * H * std::min(nst, ceil_div(span, kSumSlotsTile) + 1));

@@ -205,3 +205,44 @@ def test_append_cuts_starts_as_attention_does(starts, tokens, lens, want, dtype,
     for s, j, t in want:
         v, _ = b.rows(rv, b.v_scale, s, 0, lens[s])
         assert (out[t, 0].double().cpu() - v[j]).abs().max() <= torch.finfo(dtype).eps * v[j].abs().max(), (s, j, t)
+
+
+# ---- bounds far above the lengths, with weights
+
+def workspace(S, H, rows, dim, pages, page, max_q, max_len):
+    """What a call's workspace takes: nothing is launched, and no address read."""
+    import ctypes
+
+    from geometric_map_reduce_amd.paged import _CACHE
+    row = H * dim
+    c = _CACHE.pack(1 << 44, 2 << 44, 3 << 44, 0, 0, page * row, row, dim, pages, 4 << 44, 8192, 5 << 44, page, H, dim, 0, 8192, S)
+    n = ctypes.c_int64(0)
+    rc = gm.lib().keops_paged_attention_workspace(c, 0, H * rows // max_q, S * max_q, max_q, max_len, 0, ctypes.byref(n))
+    assert rc == 0
+    return n.value
+
+
+def test_kept_scores_do_not_outgrow_the_cache():
+    say("workspace of steps with weights")
+    # one long conversation among short ones: 2.1 GB of scores for 0.8 GB of keys and values
+    assert workspace(64, 8, 8, 128, 194000 // 16, 16, 1, 131072) < 1e8
+    # more than 4 GB, whatever the cache
+    assert workspace(64, 8, 32, 128, 64 * 8192, 16, 4, 131072) < 1e8
+    # as large as the lengths may want: kept
+    assert workspace(64, 8, 8, 128, 64 * 8192, 16, 1, 131072) > 4 * 64 * 8 * 8 * 131072
+    assert workspace(32, 8, 4, 128, 32 * 313, 16, 1, 8000) > 4 * 32 * 8 * 4 * 8000
+
+
+@pytest.mark.parametrize("new,dtype,cache", [(1, BF, BF), (2, FP, FP), (2, BF, E4)])
+def test_weights_under_far_bounds(new, dtype, cache):
+    """Weights by the column sums instead of kept scores, of few rows."""
+    say(f"weights under far bounds, {new} new, {dtype} {cache}")
+    b = ref.Batch(101, [300, 77, 0, 2000], [new, 1, 0, new], 8, 2, 128, 24, dtype, cache)
+    b.weights = torch.rand((b.P, 2, 24), generator=b.gen)
+    w = put(b.weights)
+    out, lse = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), put(b.lens_t()), put(b.starts), new, 1 << 23,
+                                        weights=w, decay=0.5, k_scale=put(b.k_scale), v_scale=put(b.v_scale))
+    o, z, ww, ot, zt, wt = ref.attention(b, 0.5)
+    close(lse.cpu(), z, zt, "lse")
+    close(out.cpu(), o, ot, "out")
+    close(w.cpu(), ww, wt, "weights")
