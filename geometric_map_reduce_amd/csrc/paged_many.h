@@ -55,10 +55,15 @@ __device__ __forceinline__ float half_sum(float v) { return v + __shfl_xor(v, 32
 __device__ __forceinline__ constexpr int slot32(int r, int hi) { return hi * 4 + (r & 3) + 8 * (r >> 2); }
 
 // 16 bytes a lane from global memory to LDS, lane l's at lds + 16 l, without passing registers.
-// Done when vmcnt says so: the compiler does not know, dma_wait() does.  (M0 needs one wait state.)
+// Done when vmcnt says so: the compiler does not know, dma_wait() does.  (M0 needs one wait state.)  M0 is named
+// as changed: the compiler keeps no value in it for long, and warns of that, but may set it once for two of its
+// own uses that this lies between.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void *from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 template <int LEFT>
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
