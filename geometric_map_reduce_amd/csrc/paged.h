@@ -177,6 +177,21 @@ void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st
 constexpr int kFewRowsMax = 32;      // rows (new tokens x group) of the few-rows form
 constexpr int kManyRowsTile = 128;   // rows of a work-group of the many-rows form
 constexpr int kSumSlotsTile = 256;   // slots of a work-group of the column sums
+// Threads of a work-group, for the plans.
+constexpr int kFinishThreads = 256;  // few rows: the second pass
+constexpr int kJoinThreads = 256;    // many rows: the join
+constexpr int kSelectThreads = 1024; // eviction: the selection
+constexpr int kVerifyThreads = 256;
+constexpr int kScoreSlots = 2048;    // slots of a work-group that turns kept scores into weights
+// Groups of threads that share a row of the many-rows join, and its work-groups.
+inline int join_per_row(int dim, int nsplit) {
+  const int groups = kJoinThreads / (dim / 4);
+  return nsplit <= 4 ? 1 : (nsplit < groups ? nsplit / 4 : groups);
+}
+inline int64_t join_blocks(int64_t rows, int dim, int nsplit) {
+  const int64_t rows_per = kJoinThreads / (dim / 4) / join_per_row(dim, nsplit);
+  return (rows + rows_per - 1) / rows_per;
+}
 // Both passes.  grid 0: the work-groups of the variant that a compute unit holds (-1: HIP error).
 // join_rows: rows of a work-group that joins parts, 0: there are none.
 int launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, int grid, int join_rows,

@@ -15,6 +15,9 @@ namespace kmi {
 namespace {
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
+// A launch has fewer than 2^32 threads (HIP's limit along an axis).
+bool launchable(double blocks, int threads) { return blocks * threads < 4294967296.0; }
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;    // of 256 threads
 constexpr double kMaxWorkspace = 1.0e14;    // more than any device holds; below the 64-bit limit
 // Work-groups that a launch aims for, per compute unit, when it splits a long axis.
 constexpr int64_t kManyWgsPerCu = 2;
@@ -150,6 +153,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     const int64_t room = (int64_t)fit * cus;
     p->whole = from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
     if (!p->whole && from_tile <= kFewWhole8 && S * H <= cus && p->row_tiles == 1 && c.dim <= 128) p->whole = 2;
+    if (p->whole && !launchable((double)S * (double)H, p->whole == 2 ? 512 : 256)) return KEOPS_ERR_UNSUPPORTED;
     p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
     p->far = !p->whole && 2.0 * (double)S * (double)H * (double)from_tile * (double)(c.dim * width_of(c.type)) > kFarBytes;
     if (!p->whole) {
@@ -169,6 +173,8 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     // as many splits as the device holds at once, of at least four tiles of slots
     const int64_t room = (c.dim > 128 ? 1 : kManyWgsPerCu) * cus;
     p->nsplit = std::max<int64_t>(1, std::min(room / wgs, span / 256));
+    // the join looks through all tokens' rows
+    if (p->nsplit > 1 && !launchable((double)join_blocks(tokens * heads, c.dim, (int)p->nsplit), kJoinThreads)) p->nsplit = 1;
     p->grid = wgs * p->nsplit;
   }
   if (c.weights) {
@@ -177,14 +183,13 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       p->score_stride = ceil_div(max_len, 32) * 32;
       if (score_bytes > kMaxWorkspace) return KEOPS_ERR_ALLOC;
       p->score_bytes = align256(4 * S * H * rows * p->score_stride);
-      if ((double)S * (double)H * (double)(ceil_div(max_len, 256) + rows * 8) > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
     } else {
       const int64_t nst = ceil_div(max_len, kSumSlotsTile);
       if (!sums_fit) return KEOPS_ERR_UNSUPPORTED;
       const int64_t wgs = S * H * nst;
       // slots outside every window cost next to nothing
       const int64_t busy = std::max<int64_t>(1, S * H * std::min(nst, ceil_div(span, kSumSlotsTile) + 1));
-      p->nrow = std::max<int64_t>(1, std::min(ceil_div(kSumsWgsPerCu * cus, busy), rows / 256));
+      p->nrow = std::max<int64_t>(1, std::min({ceil_div(kSumsWgsPerCu * cus, busy), rows / 256, kMaxBlocks / std::max<int64_t>(1, wgs)}));
       p->sums_grid = wgs * p->nrow;
       if (p->nrow > 1) {
         if (4.0 * (double)p->nrow * (double)S * (double)H * (double)max_len > kMaxWorkspace) return KEOPS_ERR_ALLOC;
@@ -192,10 +197,14 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       }
     }
   }
+  if (p->few) {
+    const double joins = p->join_rows ? heads_of_seqs * (double)ceil_div(rows, p->join_rows) * p->join_slices : 0.0;
+    const double sums = p->scores ? heads_of_seqs * (double)ceil_div(max_len, kScoreSlots) : 0.0;
+    if (!launchable(joins + sums, kFinishThreads)) return KEOPS_ERR_UNSUPPORTED;
+  }
   if (!p->few && p->nsplit > 1) {
     const double out_rows = (double)tokens * heads * (double)p->nsplit;
     if (out_rows * c.dim * 4.0 > kMaxWorkspace) return KEOPS_ERR_ALLOC;
-    if ((double)tokens * heads > (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
     p->ml_bytes = align256(p->nsplit * tokens * heads * 8);
     p->o_bytes = align256(p->nsplit * tokens * heads * c.dim * 4);
   }
@@ -246,7 +255,7 @@ int append_entry(const keops_cache_t *c, const void *k, const void *v, int64_t k
   if (tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !good_stride(k_stride) || !good_stride(v_stride)))
     return KEOPS_ERR_INVALID_ARG;
   if (tokens > 0 && c->seqs > 0 && (!starts || !aligned(starts, 4))) return KEOPS_ERR_INVALID_ARG;
-  if (tokens > 0x7fffffff || (double)tokens * (double)(row / 8) > 256.0 * (double)kMaxGrid) return KEOPS_ERR_UNSUPPORTED;
+  if (tokens > 0x7fffffff || !launchable(std::ceil((double)tokens * (double)(row / 8) / 256.0), 256)) return KEOPS_ERR_UNSUPPORTED;
   if (tokens > 0) {
     const int64_t kb = rows_extent(tokens, k_stride, row), vb = rows_extent(tokens, v_stride, row);
     const int64_t pb = pages_extent(*c);
@@ -352,9 +361,9 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
         overlaps(kept, kb, c->weights, wb) || overlaps(kept, kb, c->k_pages, pb) || overlaps(kept, kb, c->v_pages, pb))
       return KEOPS_ERR_INVALID_ARG;
   }
-  if ((double)c->seqs * c->heads * (double)budget * (c->dim * width_of(c->type) / 16) > 256.0 * (double)kMaxGrid ||
+  if (!launchable(std::ceil((double)c->seqs * c->heads * (double)budget * (double)(c->dim * width_of(c->type) / 16) / 256.0), 256) ||
       (double)c->table_width * (double)c->page_size > (double)kMaxSlots ||
-      (double)c->seqs * c->heads > (double)kMaxGrid ||
+      !launchable((double)c->seqs * c->heads, kSelectThreads) ||
       (double)c->pages * c->heads * (double)c->page_size > 4294967295.0)       // the selection's 32-bit weight numbers
     return KEOPS_ERR_UNSUPPORTED;
   if (c->seqs == 0) return KEOPS_OK;
@@ -382,8 +391,11 @@ void plan_verify(VerifyArgs *a) {
 
 int check_verify(int seqs, int drafts, int vocab) {
   if (seqs < 0 || drafts < 0 || vocab < 1) return KEOPS_ERR_INVALID_ARG;
-  if (drafts > 1 << 20 || vocab > 1 << 30 || seqs > 1 << 24) return KEOPS_ERR_UNSUPPORTED;
-  return KEOPS_OK;
+  if (drafts > 1 << 20 || vocab > 1 << 30) return KEOPS_ERR_UNSUPPORTED;
+  VerifyArgs a{};
+  a.vocab = vocab;
+  plan_verify(&a);
+  return launchable((double)seqs * a.pieces, kVerifyThreads) ? KEOPS_OK : KEOPS_ERR_UNSUPPORTED;
 }
 
 int verify_entry(VerifyArgs a, void *workspace, int64_t workspace_bytes, hipStream_t st) {

@@ -25,7 +25,6 @@
 namespace kmi {
 namespace {
 
-constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / kWave;
 constexpr int kBins = 2048;             // counts of a pass
 constexpr int kHistCopies = 2;          // even and odd lanes: fewer collisions

@@ -605,9 +605,8 @@ __device__ __forceinline__ int64_t part_slot(int w, int w0, int rows) { return (
 // Weights from kept scores: a thread adds up the rows' 2^(score - lse) for four slots in a row.
 // 25 bytes a slot at four rows: the chain of loads before the sum costs more than they do, so a
 // work-group takes many slots.  lse comes from the parts, so that nothing waits for their join.
-constexpr int kFinishThreads = 256;
 constexpr int kScoreGroups = 2, kScoreAhead = 4;      // groups of a thread; rows loaded before lse is known
-constexpr int kScoreSlots = 4 * kScoreGroups * kFinishThreads;
+static_assert(kScoreSlots == 4 * kScoreGroups * kFinishThreads, "four slots a group");
 __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int part_rows, float *lse2) {
   const int H = a.c.heads, G = a.group, tid = threadIdx.x;
   const int blocks = (a.max_len + kScoreSlots - 1) / kScoreSlots;

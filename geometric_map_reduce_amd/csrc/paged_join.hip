@@ -16,8 +16,6 @@ void many_f16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream
 
 namespace {
 
-constexpr int kJoinThreads = 256;
-
 // out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k over the splits k under a running maximum M.
 // `per_row` groups of dim / 4 threads share a row (one where the splits are few), splits in order
 // within each, then the groups in order.
@@ -108,9 +106,8 @@ void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 
 }
 
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st) {
-  const int groups = kJoinThreads / (a.c.dim / 4), per_row = a.nsplit <= 4 ? 1 : (a.nsplit < groups ? a.nsplit / 4 : groups);
-  const int64_t rows_per = groups / per_row, rows = a.tokens * a.c.heads * a.group;
-  const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per));
+  const int per_row = join_per_row(a.c.dim, a.nsplit);
+  const dim3 grid((unsigned)join_blocks(a.tokens * a.c.heads * a.group, a.c.dim, a.nsplit));
   if (type == CT_BF16) join_kernel<Bf16><<<grid, kJoinThreads, 0, st>>>(a, per_row);
   else join_kernel<F16><<<grid, kJoinThreads, 0, st>>>(a, per_row);
 }

@@ -21,7 +21,6 @@
 namespace kmi {
 namespace {
 
-constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / kWave;
 constexpr int kPer = kVerifyPiece / kVerifyThreads;     // indices of a thread in a piece's step
 

@@ -263,7 +263,8 @@ int keops_kmin(const float *x, const float *y, const float *b,
  *  Strides count elements; the last dimension of every array is contiguous.  k_pages,
  *  v_pages, q, k, v and out are 16-byte aligned, their strides multiples of 16 bytes.
  *  A page in the tables of several sequences is read for each; it holds the weights of one of them.
- *  At most 2^30 slots a sequence.
+ *  At most 2^30 slots a sequence.  Work of 2^32 threads or more in one launch (some 68 GB of
+ *  keys to append or to move in 16-byte pieces) is KEOPS_ERR_UNSUPPORTED.
  *  k_pages and v_pages share their strides: [pages][page_size][heads][dim] in any order of
  *  the first three.  dim: 64, 96, 128 or 256.
  *  Types: KEOPS_TYPE_BF16 or _F16 for q, k, v, out, with a cache of the same type or of

@@ -222,6 +222,26 @@ def workspace(S, H, rows, dim, pages, page, max_q, max_len):
     return n.value
 
 
+def test_plans_stay_below_the_threads_of_a_launch():
+    """Fewer than 2^32: refused, or with fewer parts."""
+    say("plans of many work-groups")
+    import ctypes
+
+    from geometric_map_reduce_amd.paged import _CACHE
+
+    def plan(S, H, heads, tokens, max_q, max_len, weights=0, dim=64):
+        row = H * dim
+        c = _CACHE.pack(1 << 44, 2 << 44, weights, 0, 0, 16 * row, row, dim, 100, 4 << 44, 8192, 5 << 44, 16, H, dim, 0, 8192, S)
+        n = ctypes.c_int64(0)
+        return gm.lib().keops_paged_attention_workspace(c, 0, heads, tokens, max_q, max_len, 0, ctypes.byref(n)), n.value
+    assert plan(1 << 20, 16, 16, 1 << 20, 1, 100) == (-2, 0)              # a work-group to each of 2^24 heads
+    assert plan((1 << 20) - 1, 16, 16, 1 << 20, 1, 100) == (0, 0)
+    # 2^27 rows in the token arrays, 64 of them in the one sequence: no parts that a join would look through
+    assert plan(1, 8, 8, 1 << 24, 64, 20000, dim=256) == (0, 0)
+    assert plan(1, 8, 8, 64, 64, 20000, dim=256)[1] > 0
+    assert plan(1, 8, 8, 64, 64, 0, weights=3 << 44) == (0, 0)              # no slots: no work-groups to share rows
+
+
 def test_kept_scores_do_not_outgrow_the_cache():
     say("workspace of steps with weights")
     # one long conversation among short ones: 2.1 GB of scores for 0.8 GB of keys and values

@@ -174,3 +174,17 @@ def test_short_way_hands_back_what_it_does_not_take(L):
             assert short.verify(*a[:6], None, None) is None
     assert short.append() is None and short.append(*good, 1) is None and short.attention(*good) is None
     assert short.evict() is None and short.verify() is None
+
+
+def test_calls_of_more_threads_than_a_launch_has_are_refused(L):
+    """A launch has fewer than 2^32 threads."""
+    far = dict(k_pages=1 << 51, v_pages=1 << 52, weights=1 << 53)
+    c = cache(weights=1 << 53)
+    assert call_append(L, c, k=1 << 54, v=1 << 55, tokens=1 << 28) == -2           # 16 pieces a token
+    evict = dict(kept=1 << 54, lens=1 << 55, sink=0, recent=0)
+    assert call_evict(L, cache(seqs=4096, heads=16, **far), budget=8192, **evict) == -2
+    assert call_evict(L, cache(seqs=65536, heads=64, **far), budget=1, **evict) == -2
+    n = ctypes.c_int64(7)
+    assert L.keops_verify_draft_workspace(1 << 24, 0, 1, ctypes.byref(n)) == -2
+    assert L.keops_verify_draft_workspace(1 << 18, 0, 131072, ctypes.byref(n)) == -2
+    assert L.keops_verify_draft(1 << 54, None, None, D, None, F, 1 << 24, 0, 1, 1 << 55, 1 << 56, None, 0, None) == -2
