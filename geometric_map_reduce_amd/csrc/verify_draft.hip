@@ -32,12 +32,12 @@ __device__ __forceinline__ int first_refused(const VerifyArgs &a, int s, int n) 
     bool refused = false;
     if (i < n) {
       const int x = a.tokens[(int64_t)s * K + i];
-      double px = 0.0, qx = 1.0;
+      refused = true;
       if (x >= 0 && x < V) {
-        px = (double)a.target[((int64_t)s * (K + 1) + i) * V + x];
-        if (a.draft) qx = (double)a.draft[((int64_t)s * K + i) * V + x];
+        const double px = (double)a.target[((int64_t)s * (K + 1) + i) * V + x];
+        const double qx = a.draft ? (double)a.draft[((int64_t)s * K + i) * V + x] : 1.0;
+        refused = !((double)a.u_accept[(int64_t)s * K + i] * qx < px);
       }
-      refused = !((double)a.u_accept[(int64_t)s * K + i] * qx < px);
     }
     const uint64_t who = __ballot(refused);
     if (who) return base + __ffsll((unsigned long long)who) - 1;

@@ -266,3 +266,18 @@ def test_weights_under_far_bounds(new, dtype, cache):
     close(lse.cpu(), z, zt, "lse")
     close(out.cpu(), o, ot, "out")
     close(w.cpu(), ww, wt, "weights")
+
+
+# ---- verification
+
+@pytest.mark.parametrize("given", [False, True])
+def test_tokens_outside_the_vocabulary_are_refused_whatever_the_number(given):
+    say(f"verification of tokens outside the vocabulary, draft {given}")
+    target, draft, tokens, counts, ua, us = verify_case(103, 6, 3, 257)
+    counts[:] = 3
+    for s, x in enumerate((-1, 257, 2 ** 31 - 1, -2 ** 31)):
+        tokens[s, s % 3] = x
+        ua[s] = -0.5
+    out, acc = gm.keops_verify_draft(put(target), put(draft) if given else None, put(tokens), put(counts), put(ua), put(us))
+    ro, ra = ref.verify(target, draft if given else None, tokens, counts, ua, us)
+    assert acc.tolist() == ra.tolist() and out.tolist() == ro.tolist()
