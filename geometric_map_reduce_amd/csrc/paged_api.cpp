@@ -151,7 +151,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     const int fit = launch_attend_few(probe, type, c.type == KEOPS_TYPE_E4M3, c.dim, p->row_tiles, 0, 0, nullptr);
     if (fit < 1) return KEOPS_ERR_HIP;
     const int64_t room = (int64_t)fit * cus;
-    p->whole = from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
+    p->whole = rows == 0 || from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
     if (!p->whole && from_tile <= kFewWhole8 && S * H <= cus && p->row_tiles == 1 && c.dim <= 128) p->whole = 2;
     if (p->whole && !launchable((double)S * (double)H, p->whole == 2 ? 512 : 256)) return KEOPS_ERR_UNSUPPORTED;
     p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
@@ -224,6 +224,11 @@ int check_attend(const keops_cache_t *c, int type, int64_t tokens, int heads, in
   return KEOPS_OK;
 }
 
+// Whether a call has work: tokens that count, or, without any, weights that decay all the same.
+bool has_work(const keops_cache_t &c, int64_t tokens, int max_q) {
+  return c.seqs > 0 && ((tokens > 0 && max_q > 0) || (c.weights && c.pages > 0));
+}
+
 // The caller's workspace, or the library's; the library's is never recorded into a graph,
 // whose replays could outlive it.
 int take_workspace(Workspace &own, void *given, int64_t given_bytes, int64_t need, hipStream_t st, char **ptr) {
@@ -293,8 +298,10 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
       return KEOPS_ERR_INVALID_ARG;
   }
   if (workspace && (!aligned(workspace, 256) || workspace_bytes < 0)) return KEOPS_ERR_INVALID_ARG;
-  if (tokens == 0 || c->seqs == 0 || max_q == 0) return KEOPS_OK;
+  if (!has_work(*c, tokens, max_q)) return KEOPS_OK;
   if (c->pages == 0) return KEOPS_ERR_INVALID_ARG;    // nothing to address
+  if (!starts || !aligned(starts, 4)) return KEOPS_ERR_INVALID_ARG;
+  if (tokens == 0) max_q = 0;
   (void)hipGetLastError();
   int cus = 0;
   if (int rc = device_setup(&cus)) return rc;
@@ -459,11 +466,11 @@ int keops_paged_attention_workspace(const keops_cache_t *cache, int32_t type, in
     if (!bytes) return KEOPS_ERR_INVALID_ARG;
     *bytes = 0;
     if (int rc = check_attend(cache, type, tokens, heads, max_q, max_len, 1.0f, window, 0.0f)) return rc;
-    if (tokens == 0 || cache->seqs == 0 || max_q == 0) return KEOPS_OK;
+    if (!has_work(*cache, tokens, max_q)) return KEOPS_OK;
     int cus = 0;
     if (int rc = device_setup(&cus)) return rc;
     AttendPlan p;
-    if (int rc = plan_attend(*cache, type, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
+    if (int rc = plan_attend(*cache, type, tokens, heads, tokens ? max_q : 0, max_len, window, cus, &p)) return rc;
     *bytes = p.total();
     return KEOPS_OK;
   } catch (...) {

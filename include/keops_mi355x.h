@@ -304,7 +304,8 @@ int keops_cache_append(const keops_cache_t *cache, const void *k, const void *v,
  * q: [tokens][heads][dim], rows q_stride apart; out: the same shape, dense; lse: [tokens][heads].
  * Where the cache has weights, slot j's becomes
  *   decay * old + sum over the new tokens t and the query heads g of the key/value head of exp(z_j - lse)
- * for every slot of every sequence (decay = 0 does not read the old ones; 1 accumulates).
+ * for every slot of every sequence (decay = 0 does not read the old ones; 1 accumulates), also
+ * where no sequence has a new token.
  * A value that a row does not see has no effect on it, whatever it holds.
  * workspace: NULL for the library's (see "Ownership" above), or a 256-byte aligned device
  * buffer of at least keops_paged_attention_workspace bytes (KEOPS_ERR_SCRATCH if smaller).

@@ -281,3 +281,25 @@ def test_tokens_outside_the_vocabulary_are_refused_whatever_the_number(given):
     out, acc = gm.keops_verify_draft(put(target), put(draft) if given else None, put(tokens), put(counts), put(ua), put(us))
     ro, ra = ref.verify(target, draft if given else None, tokens, counts, ua, us)
     assert acc.tolist() == ra.tolist() and out.tolist() == ro.tolist()
+
+
+# ---- no new tokens
+
+@pytest.mark.parametrize("tokens,max_q", [(0, 0), (0, 1), (0, 500), (3, 0)])
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, E4)])
+def test_weights_without_new_tokens(tokens, max_q, decay, dtype, cache):
+    """A call in which no sequence has a token that counts gives no slot anything: the weights become decay * old."""
+    say(f"weights, {tokens} tokens, max_q {max_q}, decay {decay}, {cache}")
+    b = ref.Batch(107, [300, 0, 20], [tokens, 0, 0], 8, 2, 64, 16, dtype, cache, junk=0.0)
+    b.weights = torch.rand((b.P, 2, 16), generator=b.gen)
+    w = put(b.weights)
+    out, lse = gm.keops_paged_attention(put(b.q), put(b.k), put(b.v), put(b.table), put(b.lens_t()), put(b.starts), max_q, 300,
+                                        weights=w, decay=decay, k_scale=put(b.k_scale), v_scale=put(b.v_scale))
+    torch.cuda.synchronize()
+    assert out.shape == (tokens, 8, 64) and lse.shape == (tokens, 8)
+    want = b.weights.clone()
+    for s, n in ((0, 300), (2, 20)):
+        for j in range(n):
+            want[b.table[s, j // 16].item(), :, j % 16] *= decay
+    assert torch.equal(w.cpu(), want)
