@@ -6,6 +6,10 @@ draft model.  Each round the draft proposes a few tokens per conversation; the t
 decides how many stand, and a conversation that outgrows its budget is cut down to it by attention weight
 (``keops_cache_evict``).  Lengths stay on the device; the host keeps the page lists.
 
+The weights take up the attention of all drafted rows, before it is known which of them are refused, so a refused
+token has a say in what is evicted.  Where that matters, leave ``weights`` out of the call that verifies, and let a
+second call over the rows that were accepted accumulate them; it reads the cache once more.
+
     python examples/paged_decode.py
 """
 from __future__ import annotations

@@ -138,7 +138,7 @@ struct AttendArgs {
   uint32_t *line;               // few rows: where each sequence's tiles begin, and a work-group's share [seqs + 1]
   int32_t whole;                // few rows: a work-group has all slots of one (sequence, head); 2: of eight waves
   int32_t join_slices;          // few rows: work-groups that share the columns of a row in the join
-  bool far;                     // few rows, not `whole`: more keys and values than the last-level cache holds
+  bool far;                     // few rows, not `whole`: the bounds allow for more keys and values than a cache holds
   float *part_o;                // [..][dim], sums under the part's maximum
   float2 *part_ml;              // (maximum in log2 units, sum)
   // few-rows form with weights: scores [seqs * heads][score_stride / 4][rows][4] in log2 units

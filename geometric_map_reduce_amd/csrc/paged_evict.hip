@@ -15,8 +15,9 @@
 // come from a scan of the threads' counts.
 // Loading, a thread has four slots in a row: one page number and one 16-byte load where pages are whole
 // aligned quadruples, slot by slot otherwise.  64 rows of up to 32,768 slots take 22 us (9 for the loads
-// and the first pass, on 64 compute units), 32 rows of 1,025 slots 9 us; instructions bound the long rows,
-// latency the short ones.  256 keys of a wave that all meet one count add to it once (cleared weights are
+// and the first pass, on 64 compute units), 32 rows of 1,025 slots 9.5 us; instructions bound the long rows,
+// latency the short ones.  0.6 to 1 us of either is the look through the table for pages that are not there.
+// 256 keys of a wave that all meet one count add to it once (cleared weights are
 // all equal).  Slot by slot loads and keys in registers under unrolled loops took 43 us, 16-byte loads 32,
 // keys in LDS 30 (the last round by ballots over the waves).  The move is a second kernel, one 16-byte
 // piece of a key and of a value row per thread, bound by HBM: 268 MB read and written in 49 us.

@@ -16,8 +16,10 @@
 //  * K of the next tile is loaded once S is formed and V of the next once O is updated, into the
 //    registers just read: each wave keeps about a tile's bytes in flight at all times.
 //  * The running maximum moves only when a score passes it by 2^8 (one branch per tile), so the
-//    sums and p stay below 2^8 times what they would be; sums are in 32 bits, p is rounded to
-//    the cache's 16-bit type for the matrix product (8-bit caches: q's type).
+//    sums and p stay below 2^8 times what they would be; sums are in 32 bits, of p as it is.  p is
+//    rounded to the cache's 16-bit type (8-bit caches: q's) for the product with V: the matrix
+//    instructions take two 16-bit operands, or two fp32 ones at a sixteenth of the rate.  The output's
+//    error against 64 bits goes from its own rounding's 0.0017 to 0.0022 by it (bf16).
 //  * HBM bounds it: 64 sequences of 5,120 slots (bf16, 16 rows a head) read 1.34 GB in 242 us, 5.6 TB/s
 //    with both passes; 131,071 slots of one sequence 5.4 TB/s and 5 us of the second pass.
 //  * Slots that no row may see (past the length, of a page that the table lacks) get a zero V.
@@ -243,7 +245,7 @@ __device__ __forceinline__ void part_range(uint32_t share, uint32_t begin, int h
 
 // NW waves: 4, or 8 where one work-group has a short sequence's head to itself and nothing else
 // would hide its latency.
-// FAR: the call's keys and values are more than the last-level cache holds, and pass it by.
+// FAR: the call's keys and values, by its bounds, are more than the last-level cache holds, and pass it by.
 template <class T, bool E4M3, int D, int NR, bool SCORES, int NW, bool FAR>
 __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, E4M3, D, NR>;

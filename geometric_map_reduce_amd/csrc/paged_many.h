@@ -7,8 +7,8 @@
 // Attention: a work-group takes 128 rows of one (sequence, key/value head), 32 a wave, and walks
 // the slots that any of them sees in tiles of 64.  Tiles of K and V lie in LDS, the next ones on
 // their way while one is used.  The matrix products and the clock that they leave bound it: 4,096
-// tokens after 12,288 slots (32/8 heads of 128, bf16) take 945 us, 1,018 TFLOP/s, on a card whose
-// large library product reaches 1,268 (1,120 us on one that runs that at 1,199).
+// tokens after 12,288 slots (32/8 heads of 128, bf16) take 946 to 967 us, by card, 1,017 TFLOP/s where a
+// large library product reaches 1,268 (1,120 us on a card that runs that at 1,199).
 //
 //  * S^T = K Q^T with 32 x 32 x 16 products: Q stays in registers as the B operand, a lane holds one row
 //    and 16 slots of each 32.  Counting the slots in that order makes the packed p the B operand
@@ -16,16 +16,18 @@
 //    LDS reads.
 //  * Which slots a row sees are bits: the slots that are there, the slot of the token, the window.  Only
 //    tiles where some row does not see some slot look at them.
-//  * Running maximum, sums, absent slots and non-finite values as in the few-rows form; p is rounded
-//    to 16 bits for the matrix product, its sum is of the unrounded values.
+//  * Running maximum, sums, absent slots, non-finite values and the rounding of p to 16 bits for the
+//    matrix product as in the few-rows form.
 //  * Few rows and long caches: the slots are split over as many work-groups as the device holds at
 //    once, and a second kernel joins the parts.
 //
 // Column sums: one pass over Q with K in registers.  The rows' lse is known, so
 // p = exp(z - lse) needs no running maximum; a wave owns 64 slots and adds up the rows of Q tiles
-// staged in LDS.  The exponentials bound it: nine prompts of up to 777 tokens with a window of 1,024
-// (16/4 heads of 64) take 34 us.  A tile's arithmetic has no branch: hidden slots get a score of -inf by
-// selection (left to a condition each, 64 jumps a tile, it took 45 us).
+// staged in LDS.  Nine prompts of up to 777 tokens with a window of 1,024 (16/4 heads of 64) take 34 us.
+// Waiting bounds that: matrix instructions take 3 us of it and vector instructions, the exponentials among
+// them, 8, and the waves stand still for 44 % of their time (counters): 3,600 short work-groups, each with a
+// chain length, table, key before its first product and a barrier a tile.  A tile's arithmetic has no branch:
+// hidden slots get a score of -inf by selection (left to a condition each, 64 jumps a tile, it took 45 us).
 #pragma once
 
 #include <type_traits>

@@ -8,6 +8,9 @@ attention that each slot received.  ``page_table`` [sequences, width], ``lens`` 
 ``starts`` [sequences + 1] are int32 tensors on the same device; the calls read none of them on
 the host and never synchronise.
 
+None of these has a gradient: outputs are constants to autograd, also where an input requires one,
+and writes to the pools and to ``weights`` do not raise the tensors' version counters.
+
 Each call first goes the short way (native/paged_call.cpp), which takes plain arguments on the
 current stream in a microsecond or two and hands back, undone, whatever is anything else; that is
 taken, or refused by name, here.  A HIP error is raised as it comes: some of a call's launches may
@@ -189,7 +192,7 @@ def _graph_workspace(name, dev, *args):
 def keops_cache_append(k, v, k_pages, v_pages, page_table, lens, starts, weights=None, k_scale=None, v_scale=None,
                        stream=None):
     """Write rows starts[s] .. starts[s+1] of k and v [tokens, heads, dim] to the last slots of sequence s
-    (``lens`` counts them already); clear those slots' ``weights``."""
+    (``lens`` counts them already); clear those slots' ``weights``.  No gradient."""
     if stream is None:
         short = _short or _native()
         got = short and short.append(k, v, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts)
@@ -212,7 +215,8 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
 
     ``max_q`` and ``max_len`` bound the new tokens and the slots of any sequence; ``scale`` is
     1 / sqrt(dim) unless given; ``window`` > 0 limits a token to that many slots, its own included.
-    With ``weights``, every slot's becomes decay * old + the attention it received in this call."""
+    With ``weights``, every slot's becomes decay * old + the attention it received in this call, from all of
+    q's rows: drafted tokens that are refused later have had their part.  No gradient."""
     if stream is None:
         short = _short or _native()
         got = short and short.attention(q, k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, starts, max_q, max_len,
