@@ -163,8 +163,14 @@ def _other(stream, dev):
     work queued there, of which the other stream knows nothing."""
     if stream is None:
         return None
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
-    return None if s.cuda_stream == torch.cuda.current_stream(dev).cuda_stream else s
+    given = isinstance(stream, torch.cuda.Stream)
+    handle = stream.cuda_stream if given else int(stream)
+    if handle == torch.cuda.current_stream(dev).cuda_stream:
+        return None
+    if given:
+        return stream
+    # ExternalStream takes the default stream's handle, 0, for none
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
 
 
 def _keep(other, dev, *tensors):

@@ -303,3 +303,16 @@ def test_weights_without_new_tokens(tokens, max_q, decay, dtype, cache):
         for j in range(n):
             want[b.table[s, j // 16].item(), :, j % 16] *= decay
     assert torch.equal(w.cpu(), want)
+
+
+def test_the_default_stream_by_its_handle():
+    say("the default stream by its handle, another one current")
+    b = ref.Batch(19, [500, 300], [1, 1], 8, 2, 128, 16, junk=0.0)
+    args = [put(t) for t in (b.q, b.k, b.v, b.table, b.lens_t(), b.starts)]
+    want = gm.keops_paged_attention(*args, 1, 500)
+    torch.cuda.synchronize()
+    for current in (torch.cuda.default_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(current):
+            got = gm.keops_paged_attention(*args, 1, 500, stream=0)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -77,3 +77,31 @@ def test_the_current_stream_needs_nothing(calls, monkeypatch):
     for s in (None, Stream(1)):
         made, kept = calls(s)
         assert all(s == 1 for _, s in made) and not kept
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_the_default_streams_handle_is_the_default_stream(calls, monkeypatch, current):
+    """0 is a handle, but torch.cuda.ExternalStream takes it for none and hands out a stream of its pool."""
+    now = [Stream(current)]
+
+    @contextlib.contextmanager
+    def stream(s):
+        now.append(s or now[-1])
+        yield
+        now.pop()
+    empty = torch.Tensor.new_empty
+    seen = []
+
+    def new_empty(t, *a, **k):
+        seen.append(now[-1].cuda_stream)
+        return empty(t, *a, **k)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: now[-1])
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev=None: Stream(0))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle or 999))
+    monkeypatch.setattr(torch.Tensor, "new_empty", new_empty)
+    calls(0)
+    assert seen and all(s == 0 for s in seen), seen
+    seen.clear()
+    calls(7)
+    assert seen and all(s == 7 for s in seen), seen
