@@ -22,6 +22,11 @@ never stored, run as hand-written gfx950 HIP kernels behind the C ABI of
   key/value cache: new tokens into it, causal attention over it (a LogSumExp over keys),
   eviction from it by accumulated attention weight
 * ``keops_verify_draft`` -- drafted tokens against the target model's probabilities
+* ``keops_rotary`` -- rotary positions of queries and keys, and their gradient;
+  ``keops_rotary_frequencies`` -- their frequencies, also for long texts
+* ``keops_cache_append_rotary`` -- the append with the rotation on the way
+* ``keops_cache_read`` -- the values that slots of an 8-bit or 4-bit cache stand for
+* ``keops_adjust_logits`` -- penalties for repeated tokens, biases and masks on logits
 
 PyTorch supplies device memory and streams only.
 """
@@ -32,3 +37,5 @@ from .binding import (KEOPS_OPT_FAIL_ALLOC, KEOPS_OPT_FORM, KEOPS_OPT_MFMA, KEOP
                       keops_laplace_sum, keops_gauss_sum, keops_gauss_sum_noalloc, keops_gauss_sum_ranges,
                       keops_kmin, keops_profile_read, keops_set_option, keops_version, lib, status_string)
 from .paged import keops_cache_append, keops_cache_evict, keops_paged_attention, keops_verify_draft  # noqa: F401
+from .step import (keops_adjust_logits, keops_cache_append_rotary, keops_cache_read, keops_rotary,  # noqa: F401
+                   keops_rotary_frequencies)

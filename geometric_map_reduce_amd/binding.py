@@ -81,6 +81,10 @@ def lib() -> ctypes.CDLL:
             L.keops_cache_evict.argtypes = [P, P, i64, i32, i32, i32, i32, P, P, P]
             L.keops_verify_draft.argtypes = [P, P, P, P, P, P, i32, i32, i32, P, P, P, i64, P]
             L.keops_verify_draft_workspace.argtypes = [i32, i32, i32, ctypes.POINTER(i64)]
+            L.keops_rotary.argtypes = [P, i64, i32, i64, i32, i32, P, P, i32, P, i64, P]
+            L.keops_cache_append_rotary.argtypes = [P, P, P, P, i64, i64, i64, i32, i32, P, i64, P, P, P, i64, P]
+            L.keops_cache_read.argtypes = [P, P, P, i64, i64, i32, P, i64, P]
+            L.keops_adjust_logits.argtypes = [P, i64, i32, i64, i32, P, P, i64, P]
             L.keops_set_option.argtypes = [ctypes.c_int, i64]
             L.keops_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
             L.keops_status_string.argtypes = [ctypes.c_int]
@@ -90,6 +94,7 @@ def lib() -> ctypes.CDLL:
                       "keops_gauss_grad_x_ranges", "keops_gauss_max", "keops_gauss_min", "keops_laplace_sum",
                       "keops_kmin", "keops_cache_append", "keops_paged_attention", "keops_paged_attention_workspace",
                       "keops_cache_evict", "keops_verify_draft", "keops_verify_draft_workspace",
+                      "keops_rotary", "keops_cache_append_rotary", "keops_cache_read", "keops_adjust_logits",
                       "keops_set_option", "keops_version", "keops_profile_read"):
                 getattr(L, f).restype = ctypes.c_int
             _lib = L

@@ -23,9 +23,9 @@ LIB = os.path.join(HERE, "libkeops_mi355x.so")
 MICRO_SRC = os.path.join(HERE, "micro", "rates.hip")
 MICRO_LIB = os.path.join(HERE, "libkeops_micro.so")
 
-# the short way from torch tensors to LIB's paged-cache calls: a Python module, host code only
-CALL_SRC = os.path.join(HERE, "native", "paged_call.cpp")
-CALL_LIB = os.path.join(HERE, "_paged_call.so")
+# the short way from torch tensors to LIB's calls over a paged cache and around it: Python modules, host code only
+NATIVE = os.path.join(HERE, "native")
+CALLS = {os.path.join(NATIVE, name + ".cpp"): os.path.join(HERE, f"_{name}.so") for name in ("paged_call", "step_call")}
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -88,9 +88,10 @@ def build(jobs: int | None = None, verbose: bool = False, incremental: bool = Fa
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
     build_micro()
-    if not incremental or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < max(
-            os.path.getmtime(p) for p in (CALL_SRC, os.path.join(INCLUDE, "keops_mi355x.h"))):
-        build_call()
+    shared = (os.path.join(NATIVE, "call.h"), os.path.join(INCLUDE, "keops_mi355x.h"))
+    for src, so in CALLS.items():
+        if not incremental or not os.path.exists(so) or os.path.getmtime(so) < max(os.path.getmtime(p) for p in (src, *shared)):
+            build_call(src, so)
     return LIB
 
 
@@ -104,24 +105,24 @@ def build_micro() -> str:
     return MICRO_LIB
 
 
-def build_call() -> str:
-    """Compile the Python module of the paged-cache calls; it finds LIB next to itself."""
+def build_call(src: str, so: str) -> str:
+    """Compile a Python module of the short way; it finds LIB next to itself."""
     import sysconfig
     import torch
     from torch.utils.cpp_extension import include_paths
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = CALL_LIB + ".tmp%d" % os.getpid()
+    tmp = so + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE]
     for p in include_paths():
         cmd += ["-isystem", p]
-    cmd += ["-Wall", CALL_SRC, "-o", tmp, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", HERE,
+    cmd += ["-Wall", src, "-o", tmp, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", HERE,
             "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"g++ failed for {CALL_SRC}:\n{res.stderr}")
-    os.replace(tmp, CALL_LIB)
-    return CALL_LIB
+        raise RuntimeError(f"g++ failed for {src}:\n{res.stderr}")
+    os.replace(tmp, so)
+    return so
 
 
 if __name__ == "__main__":

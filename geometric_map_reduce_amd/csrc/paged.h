@@ -6,7 +6,13 @@
 
 namespace kmi {
 
-enum CacheType : int { CT_BF16 = 0, CT_F16 = 1, CT_E4M3 = 2 };
+enum CacheType : int { CT_BF16 = 0, CT_F16 = 1, CT_E4M3 = 2, CT_F32 = 3, CT_E2M1 = 4 };
+
+// Bits of a held element.  4: e2m1, whose blocks of 32 columns share a power of two.
+__host__ __device__ constexpr int held_bits(int type) {
+  return type == CT_E2M1 ? 4 : (type == CT_E4M3 ? 8 : (type == CT_F32 ? 32 : 16));
+}
+constexpr int kPowerBlock = 32;
 
 // n / d for n < 2^31: q = (n * mul) >> shift with mul = floor(2^(31+s) / d) + 1,
 // s = ceil(log2 d).  The excess of mul over the exact quotient is at most 1, so the
@@ -28,6 +34,7 @@ struct CacheView {
   char *k, *v;
   float *weights;               // [pages][heads][page_size] or null
   const float *k_scale, *v_scale;
+  uint8_t *k_power, *v_power;   // e2m1: [pages][heads][page_size][dim / 32], b for 2^(b - 127), 255 for NaN
   int64_t page_stride, slot_stride, head_stride;
   FastDiv page;                 // divides a slot number by the page size
   uint32_t pages;
@@ -54,6 +61,12 @@ __device__ __forceinline__ SlotPlace slot_place(const CacheView &c, const int32_
 }
 __device__ __forceinline__ int64_t place_offset(const CacheView &c, SlotPlace p) {
   return p.page < 0 ? -1 : (int64_t)p.page * c.page_stride + (int64_t)p.row * c.slot_stride;
+}
+
+// A slot and head's number among all of the pool, for arrays [pages][heads][page_size]: below 2^32 for e2m1
+// caches and evictions, the API sees to it.
+__device__ __forceinline__ uint32_t place_number(const CacheView &c, SlotPlace p, int h) {
+  return p.page < 0 ? 0u : ((uint32_t)p.page * (uint32_t)c.heads + (uint32_t)h) * c.page.d + p.row;
 }
 
 // Slots of a sequence at most: sums of a slot, a window and a tile stay in 32 bits.
@@ -152,7 +165,7 @@ struct AttendArgs {
 
 struct EvictArgs {
   CacheView c;
-  int itemsize;
+  int row_bytes;                // of a slot and head's key
   const int32_t *new_table;
   int64_t new_stride;
   uint32_t new_width;
@@ -194,10 +207,10 @@ inline int64_t join_blocks(int64_t rows, int dim, int nsplit) {
 }
 // Both passes.  grid 0: the work-groups of the variant that a compute unit holds (-1: HIP error).
 // join_rows: rows of a work-group that joins parts, 0: there are none.
-int launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, int grid, int join_rows,
+int launch_attend_few(const AttendArgs &a, int type, int bits, int dim, int row_tiles, int grid, int join_rows,
                       hipStream_t st);
-void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
-void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st);
+void launch_attend_many(const AttendArgs &a, int type, int bits, int dim, dim3 grid, hipStream_t st);
+void launch_attend_sums(const AttendArgs &a, int type, int bits, int dim, dim3 grid, hipStream_t st);
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st);
 void launch_attend_sums_join(const AttendArgs &a, hipStream_t st);
 void launch_evict(const EvictArgs &a, hipStream_t st);
@@ -238,6 +251,13 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
   }
+  // The two e2m1 values of byte B of w times 2^(power - 127), to nearest: exact but where they pass bf16's
+  // largest (infinite), NaN for power 255.  (The instruction takes the power from a float's exponent bits.)
+  static constexpr uint32_t kE2m1Top = 252u;      // up to this power every value is finite
+  template <int B>
+  static __device__ __forceinline__ uint32_t from_e2m1(uint32_t w, uint32_t power) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(power << 23), B));
+  }
 };
 struct F16 {
   static constexpr float kShift = 7.0f;
@@ -256,6 +276,11 @@ struct F16 {
   template <bool HI>
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+  }
+  static constexpr uint32_t kE2m1Top = 140u;      // 6 2^13
+  template <int B>
+  static __device__ __forceinline__ uint32_t from_e2m1(uint32_t w, uint32_t power) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, __uint_as_float(power << 23), B));
   }
 };
 
@@ -301,6 +326,28 @@ template <class T>
 __device__ __forceinline__ u32x4 widen_e4m3(u32x2 w) {
   return (u32x4){T::template from_e4m3<false>(w.x), T::template from_e4m3<true>(w.x),
                  T::template from_e4m3<false>(w.y), T::template from_e4m3<true>(w.y)};
+}
+
+// Eight e2m1 values.
+template <class T>
+__device__ __forceinline__ u32x4 widen_e2m1(uint32_t w, uint32_t power) {
+  return (u32x4){T::template from_e2m1<0>(w, power), T::template from_e2m1<1>(w, power),
+                 T::template from_e2m1<2>(w, power), T::template from_e2m1<3>(w, power)};
+}
+// Byte m of w, m known at compile time after unrolling.
+template <class T>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, uint32_t power, int m) {
+  return m == 0 ? T::template from_e2m1<0>(w, power) : m == 1 ? T::template from_e2m1<1>(w, power)
+       : m == 2 ? T::template from_e2m1<2>(w, power) : T::template from_e2m1<3>(w, power);
+}
+// Zeros for the codes of w that are infinities or NaNs under `power`.
+template <class T>
+__device__ __forceinline__ uint32_t finite_codes(uint32_t w, uint32_t power) {
+  // a code's magnitude 0 .. 7 may go up to this
+  const uint32_t over = power > T::kE2m1Top ? power - T::kE2m1Top : 0u;
+  const int most = power == 255u ? -1 : over == 0u ? 7 : over == 1u ? 5 : over == 2u ? 3 : over == 3u ? 1 : 0;
+  const uint32_t past = ((w & 0x77777777u) + (uint32_t)(7 - most) * 0x11111111u) & 0x88888888u;   // no carry passes a code
+  return w & ~((past >> 3) * 15u);
 }
 
 // A load of what is read once, past the caches if FAR.

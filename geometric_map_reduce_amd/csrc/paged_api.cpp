@@ -7,16 +7,11 @@
 #include <cmath>
 #include <cstdint>
 
-#include "host.h"
-#include "keops_mi355x.h"
-#include "paged.h"
+#include "paged_host.h"
 
 namespace kmi {
 namespace {
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
-// A launch has fewer than 2^32 threads (HIP's limit along an axis).
-bool launchable(double blocks, int threads) { return blocks * threads < 4294967296.0; }
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;    // of 256 threads
 constexpr double kMaxWorkspace = 1.0e14;    // more than any device holds; below the 64-bit limit
 // Work-groups that a launch aims for, per compute unit, when it splits a long axis.
@@ -46,77 +41,6 @@ constexpr double kFarBytes = 384e6;
 // (32 rows) 462 in place of 604.  Up to half a GB is a five-hundredth of the device's memory, and always taken.
 constexpr double kScoresAlways = 512e6, kScoresMost = 4294967296.0;
 
-bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
-
-int64_t width_of(int type) { return type == KEOPS_TYPE_E4M3 ? 1 : 2; }
-
-// Sizes for the overlap checks: exact where a device could hold them, cut at 2^62.
-int64_t cut(double bytes) { return bytes < 4.6e18 ? (int64_t)bytes : (int64_t)1 << 62; }
-
-// Bytes from the first to past the last element of the pages.
-int64_t pages_extent(const keops_cache_t &c) {
-  if (c.pages == 0) return 0;
-  const int64_t w = width_of(c.type);
-  return cut(((double)(c.pages - 1) * (double)c.page_stride + (double)(c.page_size - 1) * (double)c.slot_stride +
-              (double)(c.heads - 1) * (double)c.head_stride + c.dim) * (double)w);
-}
-int64_t weights_extent(const keops_cache_t &c) {
-  return c.weights ? cut((double)c.pages * c.heads * (double)c.page_size * 4.0) : 0;
-}
-// Bytes of `tokens` rows of `row` 16-bit elements, `stride` apart.
-int64_t rows_extent(int64_t tokens, int64_t stride, int64_t row) {
-  return cut(((double)(tokens - 1) * (double)stride + (double)row) * 2.0);
-}
-// Elements between 16-bit rows: not negative, whole 16 bytes, within 2^40.
-bool good_stride(int64_t st) { return st >= 0 && st <= (int64_t)1 << 40 && st % 8 == 0; }
-
-int check_cache(const keops_cache_t *c, bool scales = true) {
-  if (!c) return KEOPS_ERR_INVALID_ARG;
-  if (c->pages < 0 || c->page_size < 1 || c->heads < 1 || c->dim < 1 || c->seqs < 0 || c->table_width < 0 ||
-      c->table_stride < 0)
-    return KEOPS_ERR_INVALID_ARG;
-  if (c->type != KEOPS_TYPE_BF16 && c->type != KEOPS_TYPE_F16 && c->type != KEOPS_TYPE_E4M3) return KEOPS_ERR_INVALID_ARG;
-  if (scales && c->type == KEOPS_TYPE_E4M3 && (!c->k_scale || !c->v_scale)) return KEOPS_ERR_INVALID_ARG;
-  if (c->pages > 0 && (!c->k_pages || !c->v_pages)) return KEOPS_ERR_INVALID_ARG;
-  const int64_t w = width_of(c->type);
-  for (int64_t st : {c->page_stride, c->slot_stride, c->head_stride})
-    if (st < 0 || st > (int64_t)1 << 40 || st * w % 16) return KEOPS_ERR_INVALID_ARG;
-  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return KEOPS_ERR_INVALID_ARG;
-  for (const void *p : {(const void *)c->weights, (const void *)c->k_scale, (const void *)c->v_scale,
-                        (const void *)c->page_table, (const void *)c->lens})
-    if (!aligned(p, 4)) return KEOPS_ERR_INVALID_ARG;
-  if (c->seqs > 0 && (!c->lens || (c->table_width > 0 && !c->page_table))) return KEOPS_ERR_INVALID_ARG;
-  if (c->dim != 64 && c->dim != 96 && c->dim != 128 && c->dim != 256) return KEOPS_ERR_UNSUPPORTED;
-  if (c->pages > 0x7fffffff || c->heads > 65535) return KEOPS_ERR_UNSUPPORTED;
-  return KEOPS_OK;
-}
-
-CacheView view_of(const keops_cache_t &c) {
-  const int64_t w = width_of(c.type);
-  CacheView v{};
-  v.k = (char *)c.k_pages;
-  v.v = (char *)c.v_pages;
-  v.weights = c.weights;
-  v.k_scale = c.k_scale;
-  v.v_scale = c.v_scale;
-  v.page_stride = c.page_stride * w;
-  v.slot_stride = c.slot_stride * w;
-  v.head_stride = c.head_stride * w;
-  v.page = make_fastdiv((uint32_t)c.page_size);
-  v.pages = (uint32_t)c.pages;
-  v.heads = c.heads;
-  v.dim = c.dim;
-  v.table = c.page_table;
-  v.table_stride = c.table_stride;
-  v.table_width = (uint32_t)c.table_width;
-  v.lens = c.lens;
-  v.seqs = c.seqs;
-  return v;
-}
-
-int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Launch plan of one attention call.
 struct AttendPlan {
   bool few, scores, far;
@@ -134,9 +58,9 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
   // keeping a row's scores costs 8 bytes a slot, reading K again dim times its width
   const double heads_of_seqs = (double)S * (double)H;
   const double score_bytes = 4.0 * heads_of_seqs * (double)rows * (double)(ceil_div(max_len, 32) * 32);
-  const double pool_bytes = 2.0 * (double)c.pages * c.page_size * (double)H * (double)(c.dim * width_of(c.type));
+  const double pool_bytes = 2.0 * (double)c.pages * c.page_size * (double)H * (double)row_bytes(c);
   const bool sums_fit = heads_of_seqs * (double)ceil_div(max_len, kSumSlotsTile) <= (double)kMaxGrid / 1024;
-  p->scores = c.weights && p->few && rows * 8 <= c.dim * width_of(c.type) &&
+  p->scores = c.weights && p->few && rows * 8 <= row_bytes(c) &&
               (score_bytes <= std::max(kScoresAlways, std::min(2.0 * pool_bytes, kScoresMost)) || !sums_fit);
   // slots that the rows of one sequence see at most
   int64_t span = max_len;
@@ -148,14 +72,14 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
       return KEOPS_ERR_UNSUPPORTED;
     AttendArgs probe{};
     probe.score_stride = p->scores;
-    const int fit = launch_attend_few(probe, type, c.type == KEOPS_TYPE_E4M3, c.dim, p->row_tiles, 0, 0, nullptr);
+    const int fit = launch_attend_few(probe, type, held_bits(c.type), c.dim, p->row_tiles, 0, 0, nullptr);
     if (fit < 1) return KEOPS_ERR_HIP;
     const int64_t room = (int64_t)fit * cus;
     p->whole = rows == 0 || from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
     if (!p->whole && from_tile <= kFewWhole8 && S * H <= cus && p->row_tiles == 1 && c.dim <= 128) p->whole = 2;
     if (p->whole && !launchable((double)S * (double)H, p->whole == 2 ? 512 : 256)) return KEOPS_ERR_UNSUPPORTED;
     p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
-    p->far = !p->whole && 2.0 * (double)S * (double)H * (double)from_tile * (double)(c.dim * width_of(c.type)) > kFarBytes;
+    p->far = !p->whole && 2.0 * (double)S * (double)H * (double)from_tile * (double)row_bytes(c) > kFarBytes;
     if (!p->whole) {
       // a joining work-group's 1024 / dim groups of threads: one to a row where the parts are few
       const int64_t groups = 1024 / c.dim, parts = ceil_div(p->grid, S * H) + 1;
@@ -214,8 +138,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
 int check_attend(const keops_cache_t *c, int type, int64_t tokens, int heads, int max_q, int max_len, float scale,
                  int window, float decay) {
   if (int rc = check_cache(c)) return rc;
-  if (type != KEOPS_TYPE_BF16 && type != KEOPS_TYPE_F16) return KEOPS_ERR_INVALID_ARG;
-  if (c->type != KEOPS_TYPE_E4M3 && c->type != type) return KEOPS_ERR_INVALID_ARG;
+  if (!good_rows_type(*c, type)) return KEOPS_ERR_INVALID_ARG;
   if (tokens < 0 || heads < 1 || heads % c->heads || max_q < 0 || max_len < 0 || window < 0) return KEOPS_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(decay)) return KEOPS_ERR_INVALID_ARG;
   if (tokens > 0x7fffffff || heads > 65535 || (int64_t)max_q * (heads / c->heads) > 0x3fffffff ||
@@ -253,8 +176,7 @@ int take_workspace(Workspace &own, void *given, int64_t given_bytes, int64_t nee
 int append_entry(const keops_cache_t *c, const void *k, const void *v, int64_t k_stride, int64_t v_stride, int type,
                  const int32_t *starts, int64_t tokens, hipStream_t st) {
   if (int rc = check_cache(c)) return rc;
-  if (type != KEOPS_TYPE_BF16 && type != KEOPS_TYPE_F16) return KEOPS_ERR_INVALID_ARG;
-  if (c->type != KEOPS_TYPE_E4M3 && c->type != type) return KEOPS_ERR_INVALID_ARG;
+  if (!good_rows_type(*c, type)) return KEOPS_ERR_INVALID_ARG;
   if (tokens < 0) return KEOPS_ERR_INVALID_ARG;
   const int64_t row = (int64_t)c->heads * c->dim;
   if (tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !good_stride(k_stride) || !good_stride(v_stride)))
@@ -263,9 +185,11 @@ int append_entry(const keops_cache_t *c, const void *k, const void *v, int64_t k
   if (tokens > 0x7fffffff || !launchable(std::ceil((double)tokens * (double)(row / 8) / 256.0), 256)) return KEOPS_ERR_UNSUPPORTED;
   if (tokens > 0) {
     const int64_t kb = rows_extent(tokens, k_stride, row), vb = rows_extent(tokens, v_stride, row);
-    const int64_t pb = pages_extent(*c);
+    const int64_t pb = pages_extent(*c), eb = powers_extent(*c);
     for (const void *p : {(const void *)c->k_pages, (const void *)c->v_pages})
       if (overlaps(p, pb, k, kb) || overlaps(p, pb, v, vb)) return KEOPS_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)c->k_powers, (const void *)c->v_powers})
+      if (overlaps(p, eb, k, kb) || overlaps(p, eb, v, vb)) return KEOPS_ERR_INVALID_ARG;
   }
   if (tokens == 0 || c->seqs == 0 || c->pages == 0 || c->table_width == 0) return KEOPS_OK;
   (void)hipGetLastError();
@@ -291,7 +215,10 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
       return KEOPS_ERR_INVALID_ARG;
     if (c->seqs > 0 && (!starts || !aligned(starts, 4))) return KEOPS_ERR_INVALID_ARG;
     const int64_t ob = tokens * row * 2, lb = tokens * heads * 4, qb = rows_extent(tokens, q_stride, row);
-    const int64_t pb = pages_extent(*c), wb = weights_extent(*c);
+    const int64_t pb = pages_extent(*c), wb = weights_extent(*c), eb = powers_extent(*c);
+    if (overlaps(out, ob, c->k_powers, eb) || overlaps(out, ob, c->v_powers, eb) || overlaps(lse, lb, c->k_powers, eb) ||
+        overlaps(lse, lb, c->v_powers, eb))
+      return KEOPS_ERR_INVALID_ARG;
     if (overlaps(out, ob, q, qb) || overlaps(out, ob, lse, lb) || overlaps(lse, lb, q, qb) ||
         overlaps(out, ob, c->k_pages, pb) || overlaps(out, ob, c->v_pages, pb) || overlaps(out, ob, c->weights, wb) ||
         overlaps(lse, lb, c->weights, wb) || overlaps(lse, lb, c->k_pages, pb) || overlaps(lse, lb, c->v_pages, pb))
@@ -339,14 +266,14 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.score_rows = p.score_rows;
   a.nrow = (int32_t)std::max<int64_t>(1, p.nrow);
   a.part_w = (float *)(ws + p.ml_bytes + p.o_bytes + p.score_bytes);
-  const bool e4m3 = c->type == KEOPS_TYPE_E4M3;
+  const int bits = held_bits(c->type);
   const int prof = prof_begin(st);
-  if (p.few) launch_attend_few(a, type, e4m3, c->dim, p.row_tiles, (int)p.grid, p.join_rows, st);
-  else launch_attend_many(a, type, e4m3, c->dim, dim3((unsigned)p.grid), st);
+  if (p.few) launch_attend_few(a, type, bits, c->dim, p.row_tiles, (int)p.grid, p.join_rows, st);
+  else launch_attend_many(a, type, bits, c->dim, dim3((unsigned)p.grid), st);
   prof_end(prof, st);
   if (!p.few && p.nsplit > 1) launch_attend_join(a, type, st);
   if (c->weights && max_len > 0 && !p.scores) {
-    launch_attend_sums(a, type, e4m3, c->dim, dim3((unsigned)p.sums_grid), st);
+    launch_attend_sums(a, type, bits, c->dim, dim3((unsigned)p.sums_grid), st);
     if (p.nrow > 1) launch_attend_sums_join(a, st);
   }
   return check_launch();
@@ -363,12 +290,13 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
     // every kept slot has a place in the new table
     if (new_width < std::min<int64_t>(ceil_div(budget, c->page_size), c->table_width)) return KEOPS_ERR_INVALID_ARG;
     const int64_t kb = cut((double)c->seqs * c->heads * (double)budget * 4.0), nb = (int64_t)c->seqs * 4;
-    const int64_t pb = pages_extent(*c), wb = weights_extent(*c);
+    const int64_t pb = pages_extent(*c), wb = weights_extent(*c), eb = powers_extent(*c);
+    if (overlaps(kept, kb, c->k_powers, eb) || overlaps(kept, kb, c->v_powers, eb)) return KEOPS_ERR_INVALID_ARG;
     if (overlaps(kept, kb, new_lens, nb) || overlaps(kept, kb, c->lens, nb) || overlaps(new_lens, nb, c->lens, nb) ||
         overlaps(kept, kb, c->weights, wb) || overlaps(kept, kb, c->k_pages, pb) || overlaps(kept, kb, c->v_pages, pb))
       return KEOPS_ERR_INVALID_ARG;
   }
-  if (!launchable(std::ceil((double)c->seqs * c->heads * (double)budget * (double)(c->dim * width_of(c->type) / 16) / 256.0), 256) ||
+  if (!launchable(std::ceil((double)c->seqs * c->heads * (double)budget * (double)(c->dim * held_bits(c->type) / 128) / 256.0), 256) ||
       (double)c->table_width * (double)c->page_size > (double)kMaxSlots ||
       !launchable((double)c->seqs * c->heads, kSelectThreads) ||
       (double)c->pages * c->heads * (double)c->page_size > 4294967295.0)       // the selection's 32-bit weight numbers
@@ -377,7 +305,7 @@ int evict_entry(const keops_cache_t *c, const int32_t *new_table, int64_t new_st
   (void)hipGetLastError();
   EvictArgs a{};
   a.c = view_of(*c);
-  a.itemsize = (int)width_of(c->type);
+  a.row_bytes = c->dim * held_bits(c->type) / 8;
   a.new_table = new_table;
   a.new_stride = new_stride;
   a.new_width = (uint32_t)new_width;

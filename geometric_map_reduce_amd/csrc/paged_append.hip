@@ -3,23 +3,18 @@
 //   pages[table[s, j / page]][j % page][h] = k[t, h]      j = first_s + (t - starts_s)
 //
 // for every token t of every sequence s (8-bit caches: the e4m3 value nearest to
-// k / k_scale[h], cut to +-448), and weight 0 for the slot where weights are kept.  A copy:
+// k / k_scale[h], cut to +-448; 4-bit ones: blocks of 32 columns, four threads each, under a power of two
+// that their largest magnitude decides), and weight 0 for the slot where weights are kept.  A copy:
 // each element is read once and written once, so memory bounds a long prompt (16,384 tokens of 8 x 128
 // bf16 with weights: 28 us a call, 4.8 TB/s, the rate of a large copy) and a chain of loads a single
 // step: the halving of starts, its own start and length, the table's entry (64 sequences: nine loads in turn, 3.5 us
 // of the GPU's time with the launch).
-#include "paged.h"
+#include "step.h"
 
 namespace kmi {
 namespace {
 
 constexpr int kAppendThreads = 256;
-
-// e4m3 of x / s: IEEE division, cut to the largest finite value, NaN kept.
-__device__ __forceinline__ float e4m3_quotient(float x, float s) {
-  const float q = x / s;
-  return q != q ? q : fminf(fmaxf(q, -448.0f), 448.0f);
-}
 
 template <bool BF>
 __device__ __forceinline__ float widen16(uint32_t w, int hi) {
@@ -31,8 +26,9 @@ __device__ __forceinline__ float widen16(uint32_t w, int hi) {
 // One thread moves 8 elements (16 bytes) of a key row and the same 8 of the value row.
 // Threads of a token are adjacent, so its row of heads x dim elements is read in one
 // sweep; each thread finds the owner sequence in the sorted starts by halving.
-template <bool BF, bool E4M3>
+template <bool BF, int BITS>
 __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
+  constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4;
   const int per = a.c.heads * a.c.dim / 8;   // 8-element pieces of a token
   const int64_t piece = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
   const int64_t t = piece / per;
@@ -55,8 +51,21 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
   const int h = e * 8 / a.c.dim, d = e * 8 - h * a.c.dim;
   const u32x4 kv = *(const u32x4 *)(a.k + t * a.k_stride + (int64_t)e * 16);
   const u32x4 vv = *(const u32x4 *)(a.v + t * a.v_stride + (int64_t)e * 16);
-  const int64_t off = place_offset(a.c, p) + (int64_t)h * a.c.head_stride + (int64_t)d * (E4M3 ? 1 : 2);
-  if (E4M3) {
+  const int64_t off = place_offset(a.c, p) + (int64_t)h * a.c.head_stride + (int64_t)d * BITS / 8;
+  if (E2M1) {
+    using T = typename std::conditional<BF, Bf16, F16>::type;
+    float x[8], y[8];
+    widen8<T>(kv, x);
+    widen8<T>(vv, y);
+    uint32_t kp, vp;
+    *(uint32_t *)(a.c.k + off) = to_e2m1(x, T::kE2m1Top, &kp);
+    *(uint32_t *)(a.c.v + off) = to_e2m1(y, T::kE2m1Top, &vp);
+    if (d % kPowerBlock == 0) {
+      const uint64_t at = (uint64_t)place_number(a.c, p, h) * (a.c.dim / kPowerBlock) + d / kPowerBlock;
+      a.c.k_power[at] = (uint8_t)kp;
+      a.c.v_power[at] = (uint8_t)vp;
+    }
+  } else if (E4M3) {
     const float ks = a.c.k_scale[h], vs = a.c.v_scale[h];
     u32x2 ko, vo;
 #pragma unroll
@@ -88,11 +97,14 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
 void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st) {
   const int64_t pieces = a.tokens * (a.c.heads * a.c.dim / 8);
   const dim3 grid((unsigned)((pieces + kAppendThreads - 1) / kAppendThreads));
-  if (cache_type == CT_E4M3) {
-    if (type == CT_BF16) append_kernel<true, true><<<grid, kAppendThreads, 0, st>>>(a);
-    else append_kernel<false, true><<<grid, kAppendThreads, 0, st>>>(a);
+  if (cache_type == CT_E2M1) {
+    if (type == CT_BF16) append_kernel<true, 4><<<grid, kAppendThreads, 0, st>>>(a);
+    else append_kernel<false, 4><<<grid, kAppendThreads, 0, st>>>(a);
+  } else if (cache_type == CT_E4M3) {
+    if (type == CT_BF16) append_kernel<true, 8><<<grid, kAppendThreads, 0, st>>>(a);
+    else append_kernel<false, 8><<<grid, kAppendThreads, 0, st>>>(a);
   } else {
-    append_kernel<true, false><<<grid, kAppendThreads, 0, st>>>(a);
+    append_kernel<true, 16><<<grid, kAppendThreads, 0, st>>>(a);
   }
 }
 

@@ -356,8 +356,17 @@ __global__ __launch_bounds__(256) void move_kernel(EvictArgs a, int pieces, int6
   const u32x4 v = load_once<u32x4, FAR>(a.c.v + fo);
   *(u32x4 *)(a.c.k + dst) = k;
   *(u32x4 *)(a.c.v + dst) = v;
-  if (piece == 0)
-    a.c.weights[((int64_t)to.page * a.c.heads + h) * a.c.page.d + to.row] =
+  if (piece != 0) return;
+  if (a.c.k_power) {
+    // e2m1: the blocks' powers, 2, 3, 4 or 8 bytes
+    const int blocks = a.c.dim / kPowerBlock;
+    const uint64_t pf = (uint64_t)place_number(a.c, from, h) * blocks, pt = (uint64_t)place_number(a.c, to, h) * blocks;
+    for (int b = 0; b < blocks; ++b) {
+      a.c.k_power[pt + b] = a.c.k_power[pf + b];
+      a.c.v_power[pt + b] = a.c.v_power[pf + b];
+    }
+  }
+  a.c.weights[((int64_t)to.page * a.c.heads + h) * a.c.page.d + to.row] =
         a.c.weights[((int64_t)from.page * a.c.heads + h) * a.c.page.d + from.row];
 }
 
@@ -369,7 +378,7 @@ void launch_evict(const EvictArgs &a, hipStream_t st) {
     select_kernel<kGroupsFew><<<grid, kSelectThreads, 0, st>>>(a);
   else
     select_kernel<kGroupsMost><<<grid, kSelectThreads, 0, st>>>(a);
-  const int pieces = a.c.dim * a.itemsize / 16;
+  const int pieces = a.row_bytes / 16;
   const int64_t total = (int64_t)a.c.seqs * a.c.heads * a.budget * pieces;
   const dim3 move((unsigned)((total + 255) / 256));
   if (64.0 * (double)total > kLastLevel) move_kernel<true><<<move, 256, 0, st>>>(a, pieces, total);

@@ -57,33 +57,62 @@ __device__ __forceinline__ float xor_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-template <class T, bool E4M3, int D, int NR>
+template <class T, int BITS, int D, int NR>
 struct FewRows {
-  static constexpr int kBytes = E4M3 ? 1 : 2;
+  static constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4;
+  static constexpr int kBytes = E4M3 ? 1 : 2;           // of an element (e2m1: two to a byte)
   static constexpr int kSteps = D / 32;                 // matrix steps along the head dimension
   static constexpr int kTiles = D / 16;                 // 16-column tiles of O^T
-  static constexpr int kKRegs = (E4M3 ? 2 : 4) * kSteps;
-  static constexpr int kVRegs = D / 16 * kBytes / 4 > 0 ? (D / 16 * kBytes + 3) / 4 : 1;   // registers of a slot's columns
+  static constexpr int kKRegs = (E2M1 ? 1 : E4M3 ? 2 : 4) * kSteps;
+  static constexpr int kVRegs = E2M1 ? VPieces<D>::n : D / 16 * kBytes / 4 > 0 ? (D / 16 * kBytes + 3) / 4 : 1;   // registers of a slot's columns
   static constexpr int kPad = D + 4;                    // floats of a row in LDS: rows four banks apart
 
   uint32_t kr[2][kKRegs];
   uint32_t vr[8][kVRegs];
+  // e2m1: the powers of the lane's blocks, of K the one of its first columns and, if there are two, of its last
+  static constexpr int kKPowers = D == 96 || D == 256 ? 2 : 1;
+  uint32_t kp[2][kKPowers], vp[8][VPieces<D>::n];
 
   // 8-bit rows of a multiple of 64 bytes: a lane's 16 bytes are the operands of two matrix steps,
   // columns 64 s + 16 (l / 16) + 8 u .. of steps 2 s + u.  Any order of the columns will do that Q shares.
   static constexpr bool kWide = E4M3 && D % 64 == 0;
+  // 4-bit ones: a lane's columns lie in a row (D = 256: in two), D / 8 bytes.
   static __device__ __forceinline__ int step_column(int s, int q) {
+    if (E2M1) return D == 256 ? (s >> 2) * 128 + q * 32 + (s & 3) * 8 : q * (D / 4) + s * 8;
     return kWide ? (s >> 1) * 64 + q * 16 + (s & 1) * 8 : s * 32 + q * 8;
   }
 
   // K rows of the tile: lane l has slot l % 16 of each 16, columns step_column(s, l / 16) ..+8 of step s.
+  // powers, number: e2m1 only, the pool's powers and the slots' numbers in them.
   template <bool FAR>
-  __device__ __forceinline__ void load_k(const char *base, const int64_t *off, int at) {
+  __device__ __forceinline__ void load_k(const char *base, const int64_t *off, const uint8_t *powers, const uint32_t *number, int at) {
     const int lane = threadIdx.x & (kWave - 1), row = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       int64_t o = off[at + 16 * t + row];
       o = o < 0 ? 0 : o;
+      if (E2M1) {
+        const char *p = base + o + step_column(0, q) / 2;
+        if (D == 64) {
+          const u32x2 w = load_once<u32x2, FAR>(p);
+          kr[t][0] = w.x;
+          kr[t][1 % kKRegs] = w.y;
+        } else if (D == 96) {
+#pragma unroll
+          for (int u = 0; u < 3; ++u) kr[t][u % kKRegs] = load_once<uint32_t, FAR>(p + 4 * u);
+        } else {
+#pragma unroll
+          for (int s = 0; s < kSteps; s += 4) {
+            const u32x4 w = load_once<u32x4, FAR>(p + s * 16);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) kr[t][(s + u) % kKRegs] = w[u];
+          }
+        }
+        const uint8_t *e = powers + (uint64_t)number[at + 16 * t + row] * (D / kPowerBlock);
+        kp[t][0] = load_once<uint8_t, FAR>(e + step_column(0, q) / kPowerBlock);
+        if (kKPowers > 1) kp[t][kKPowers - 1] = load_once<uint8_t, FAR>(e + step_column(kSteps - 1, q) / kPowerBlock);
+        continue;
+      }
       const char *p = base + o + step_column(0, q) * kBytes;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
@@ -107,12 +136,26 @@ struct FewRows {
 
   // V: lane l has slots 4 (l / 16) + i of the first 16 (i < 4) and of the second (i >= 4).
   template <bool FAR>
-  __device__ __forceinline__ void load_v(const char *base, const int64_t *off, int at) {
+  __device__ __forceinline__ void load_v(const char *base, const int64_t *off, const uint8_t *powers, const uint32_t *number, int at) {
     const int lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      int64_t o = off[at + (i >> 2) * 16 + q * 4 + (i & 3)];
+      const int u = at + (i >> 2) * 16 + q * 4 + (i & 3);
+      int64_t o = off[u];
       o = o < 0 ? 0 : o;
+      if (E2M1) {
+        const uint8_t *e = powers + (uint64_t)number[u] * (D / kPowerBlock);
+        int col = 0;
+#pragma unroll
+        for (int n = 0; n < VPieces<D>::n; ++n) {
+          const int w = VPieces<D>::w[n], at_col = col + c * w;
+          const char *p = base + o + at_col / 2;
+          vr[i][n % kVRegs] = w == 8 ? load_once<uint32_t, FAR>(p) : w == 4 ? load_once<uint16_t, FAR>(p) : load_once<uint8_t, FAR>(p);
+          vp[i][n] = load_once<uint8_t, FAR>(e + at_col / kPowerBlock);
+          col += 16 * w;
+        }
+        continue;
+      }
       const char *p = base + o;
       int reg = 0, col = 0;
 #pragma unroll
@@ -142,12 +185,22 @@ struct FewRows {
   }
 
   __device__ __forceinline__ u32x4 k_frag(int t, int s) const {
+    if (E2M1) {
+      uint32_t power = kp[t][0];
+      if (D == 256) power = kp[t][(s >> 2) % kKPowers];
+      if (D == 96) {
+        const int q = (threadIdx.x & (kWave - 1)) >> 4;
+        power = (3 * q + s) >> 2 == (3 * q) >> 2 ? kp[t][0] : kp[t][kKPowers - 1];
+      }
+      return widen_e2m1<T>(kr[t][s], power);
+    }
     if (E4M3) return widen_e4m3<T>((u32x2){kr[t][2 * s], kr[t][2 * s + 1]});
     return (u32x4){kr[t][4 * s], kr[t][4 * s + 1], kr[t][4 * s + 2], kr[t][4 * s + 3]};
   }
 
   // Columns 2 m and 2 m + 1 of slot i's W columns of piece n, as a 16-bit pair.
   __device__ __forceinline__ uint32_t v_pair(int i, int n, int m) const {
+    if (E2M1) return e2m1_pair<T>(vr[i][n % kVRegs], vp[i][n], m);
     if (!E4M3) return vr[i][(n ? VPieces<D>::w[0] / 2 : 0) + m];
     const int at = (n ? VPieces<D>::w[0] : 0) + 2 * m;    // first of the two bytes
     const uint32_t w = vr[i][at / 4];
@@ -246,9 +299,10 @@ __device__ __forceinline__ void part_range(uint32_t share, uint32_t begin, int h
 // NW waves: 4, or 8 where one work-group has a short sequence's head to itself and nothing else
 // would hide its latency.
 // FAR: the call's keys and values, by its bounds, are more than the last-level cache holds, and pass it by.
-template <class T, bool E4M3, int D, int NR, bool SCORES, int NW, bool FAR>
-__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (E4M3 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
-  using F = FewRows<T, E4M3, D, NR>;
+template <class T, int BITS, int D, int NR, bool SCORES, int NW, bool FAR>
+__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (BITS < 16 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
+  using F = FewRows<T, BITS, D, NR>;
+  constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4;
   constexpr int kRows = 16 * NR;
   constexpr int kHalfRows = NW / 2 * kRows;     // half the waves' rows
   __shared__ union {
@@ -258,6 +312,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   __shared__ float sh_m[NW / 2][kRows], sh_l[NW / 2][kRows];
   __shared__ uint32_t present[kFewBlock / kFewTile];     // a tile's slots that are there, as bits
   __shared__ int sh_odd;
+  __shared__ uint32_t number[E2M1 ? kFewBlock + kFewTile : 1];     // the slots' among all powers
   // Kept scores of a block of slots, written out together: a store among the loads of every tile
   // would be waited for with them (22 us of 150 for a step of 32 conversations).
   __shared__ __align__(16) float scores[SCORES ? kScoreHeld * NR : 4];
@@ -343,6 +398,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   }
   const char *kbase = a.c.k + (int64_t)h * a.c.head_stride;
   const char *vbase = a.c.v + (int64_t)h * a.c.head_stride;
+  const uint8_t *kpow = a.c.k_power, *vpow = a.c.v_power;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
   const int last_pos = sp.first + sp.m - 1;
 
@@ -360,8 +416,10 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
     __syncthreads();
     if (SCORES && blk > c0) flush(blk - block, block);
     for (int i = tid; i < kFewBlock; i += (NW * kWave)) {
-      const int64_t o = i < cnt ? place_offset(a.c, slot_place(a.c, trow, (uint32_t)(blk + i))) : -1;
+      const SlotPlace pl = i < cnt ? slot_place(a.c, trow, (uint32_t)(blk + i)) : SlotPlace{-1, 0};
+      const int64_t o = place_offset(a.c, pl);
       sh.off[i] = o;
+      if (E2M1) number[i] = place_number(a.c, pl, h);
       const uint64_t there = __ballot(o >= 0);
       if (lane == 0) {
         present[i / kFewTile] = (uint32_t)there;
@@ -369,12 +427,13 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
       }
     }
     if (tid < kFewTile) sh.off[kFewBlock + tid] = -1;
+    if (E2M1 && tid < kFewTile) number[kFewBlock + tid] = 0;
     __syncthreads();
     int tile = wave;
     const int begin = tile < ntile ? tile * kFewTile : kFewBlock;
-    f.template load_k<FAR>(kbase, sh.off, begin);
+    f.template load_k<FAR>(kbase, sh.off, kpow, number, begin);
     __builtin_amdgcn_sched_barrier(0);
-    f.template load_v<FAR>(vbase, sh.off, begin);
+    f.template load_v<FAR>(vbase, sh.off, vpow, number, begin);
     __builtin_amdgcn_sched_barrier(0);
     for (; tile < ntile; tile += NW) {
       const int at = tile * kFewTile, j0 = blk + at;
@@ -392,7 +451,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
           for (int nr = 0; nr < NR; ++nr) sc[nr][t] = T::mfma16(kf, qf[nr][st], sc[nr][t]);
         }
       }
-      f.template load_k<FAR>(kbase, sh.off, next);
+      f.template load_k<FAR>(kbase, sh.off, kpow, number, next);
       __builtin_amdgcn_sched_barrier(0);
 
       const uint32_t there = present[tile];
@@ -456,6 +515,18 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
           const bool some = j > sp.first || (a.window > 0 && j <= last_pos - a.window);
 #pragma unroll
           for (int k = 0; k < F::kVRegs; ++k) {
+            if (E2M1) {
+              uint32_t &w = f.vr[i][k], &power = f.vp[i][k % VPieces<D>::n];
+              w = keep ? w : 0u;
+              power = keep ? power : 127u;
+              if (some && power > T::kE2m1Top) {
+                const uint32_t y = finite_codes<T>(w, power);
+                odd |= y != w || power == 255u;       // 255: a NaN whatever the code
+                w = y;
+                power = power == 255u ? 127u : power;
+              }
+              continue;
+            }
             const uint32_t x = keep ? f.vr[i][k] : 0u;
             const uint32_t y = some ? (E4M3 ? finite_bytes(x) : finite_halves<T>(x)) : x;
             odd |= y != x;
@@ -476,7 +547,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
             acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
           }
         }
-      f.template load_v<FAR>(vbase, sh.off, next);
+      f.template load_v<FAR>(vbase, sh.off, vpow, number, next);
     }
   }
 
@@ -525,8 +596,10 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
     // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
     for (int j = c0; j < c1; ++j) {
       if (!(j > sp.first || (a.window > 0 && j <= last_pos - a.window))) continue;
-      const int64_t o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)j));
+      const SlotPlace pl = slot_place(a.c, trow, (uint32_t)j);
+      const int64_t o = place_offset(a.c, pl);
       if (o < 0) continue;
+      const uint8_t *powers = E2M1 ? vpow + (uint64_t)place_number(a.c, pl, h) * (D / kPowerBlock) : nullptr;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         if (j > pos[nr] || (a.window > 0 && j <= pos[nr] - a.window)) continue;
@@ -538,8 +611,10 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
           for (int rg = 0; rg < 4; ++rg)
 #pragma unroll
             for (int t = 0; t < w; t += 2) {
-              const char *e = vbase + o + (base + (q4 * 4 + rg) * w + t) * F::kBytes;
-              const uint32_t x = E4M3 ? T::template from_e4m3<false>(*(const uint16_t *)e) : *(const uint32_t *)e;
+              const int d = base + (q4 * 4 + rg) * w + t;
+              const char *e = vbase + o + (E2M1 ? d / 2 : d * F::kBytes);
+              const uint32_t x = E2M1 ? T::template from_e2m1<0>(*(const uint8_t *)e, powers[d / kPowerBlock])
+                               : E4M3 ? T::template from_e4m3<false>(*(const uint16_t *)e) : *(const uint32_t *)e;
               acc[nr][t0 + t][rg] += nonfinite_lo<T>(x);
               acc[nr][t0 + t + 1][rg] += nonfinite_hi<T>(x);
             }
@@ -776,13 +851,13 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
 
 // One (type, cache, dim) of the few-rows form.  Returns the work-groups that fit the device at
 // once when `grid` is 0.
-template <class T, bool E4M3, int D, int NR, bool SCORES>
+template <class T, int BITS, int D, int NR, bool SCORES>
 int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
   if (grid == 0) {
     static std::atomic<int> fit{0};
     int n = fit.load(std::memory_order_relaxed);
     if (n <= 0) {
-      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, false>,
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void *)attend_few_kernel<T, BITS, D, NR, SCORES, kFewWaves, false>,
                                                        kFewThreads, 0) != hipSuccess || n < 1)
         return -1;
       fit.store(n, std::memory_order_relaxed);
@@ -790,12 +865,12 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
     return n;
   }
   if constexpr (NR == 1 && D <= 128) {
-    if (a.whole == 2) attend_few_kernel<T, E4M3, D, NR, SCORES, 8, false><<<dim3((unsigned)grid), 8 * kWave, 0, st>>>(a);
+    if (a.whole == 2) attend_few_kernel<T, BITS, D, NR, SCORES, 8, false><<<dim3((unsigned)grid), 8 * kWave, 0, st>>>(a);
   }
   if (a.far)
-    attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, true><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
+    attend_few_kernel<T, BITS, D, NR, SCORES, kFewWaves, true><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
   else if (!(NR == 1 && D <= 128 && a.whole == 2))
-    attend_few_kernel<T, E4M3, D, NR, SCORES, kFewWaves, false><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
+    attend_few_kernel<T, BITS, D, NR, SCORES, kFewWaves, false><<<dim3((unsigned)grid), kFewThreads, 0, st>>>(a);
   const int64_t sh = (int64_t)a.c.seqs * a.c.heads;
   const int64_t joins = join_rows > 0 ? ((int64_t)a.max_q * a.group + join_rows - 1) / join_rows * sh * a.join_slices : 0;
   const int64_t sums = SCORES ? (a.max_len + kScoreSlots - 1) / kScoreSlots * sh : 0;
@@ -803,21 +878,21 @@ int few_variant(const AttendArgs &a, int grid, int join_rows, hipStream_t st) {
     finish_few_kernel<T, D, NR><<<dim3((unsigned)(joins + sums)), kFinishThreads, 0, st>>>(a, (int)joins, join_rows, a.join_slices);
   return 0;
 }
-template <class T, bool E4M3, int D>
+template <class T, int BITS, int D>
 int launch_few_dim(const AttendArgs &a, int row_tiles, int grid, int join_rows, hipStream_t st) {
   if (row_tiles == 1)
-    return a.score_stride ? few_variant<T, E4M3, D, 1, true>(a, grid, join_rows, st)
-                          : few_variant<T, E4M3, D, 1, false>(a, grid, join_rows, st);
-  return a.score_stride ? few_variant<T, E4M3, D, 2, true>(a, grid, join_rows, st)
-                        : few_variant<T, E4M3, D, 2, false>(a, grid, join_rows, st);
+    return a.score_stride ? few_variant<T, BITS, D, 1, true>(a, grid, join_rows, st)
+                          : few_variant<T, BITS, D, 1, false>(a, grid, join_rows, st);
+  return a.score_stride ? few_variant<T, BITS, D, 2, true>(a, grid, join_rows, st)
+                        : few_variant<T, BITS, D, 2, false>(a, grid, join_rows, st);
 }
 
-template <class T, bool E4M3>
+template <class T, int BITS>
 int launch_few(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st) {
-  if (dim == 64) return launch_few_dim<T, E4M3, 64>(a, row_tiles, grid, join_rows, st);
-  if (dim == 96) return launch_few_dim<T, E4M3, 96>(a, row_tiles, grid, join_rows, st);
-  if (dim == 128) return launch_few_dim<T, E4M3, 128>(a, row_tiles, grid, join_rows, st);
-  return launch_few_dim<T, E4M3, 256>(a, row_tiles, grid, join_rows, st);
+  if (dim == 64) return launch_few_dim<T, BITS, 64>(a, row_tiles, grid, join_rows, st);
+  if (dim == 96) return launch_few_dim<T, BITS, 96>(a, row_tiles, grid, join_rows, st);
+  if (dim == 128) return launch_few_dim<T, BITS, 128>(a, row_tiles, grid, join_rows, st);
+  return launch_few_dim<T, BITS, 256>(a, row_tiles, grid, join_rows, st);
 }
 
 }  // namespace kmi

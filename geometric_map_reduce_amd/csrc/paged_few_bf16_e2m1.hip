@@ -1,0 +1,7 @@
+// Few-rows paged attention: bf16 queries, e2m1 cache.
+#include "paged_few.h"
+namespace kmi {
+int few_bf16_e2m1(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st) {
+  return launch_few<Bf16, 4>(a, dim, row_tiles, grid, join_rows, st);
+}
+}  // namespace kmi

@@ -2,6 +2,6 @@
 #include "paged_few.h"
 namespace kmi {
 int few_f16(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st) {
-  return launch_few<F16, false>(a, dim, row_tiles, grid, join_rows, st);
+  return launch_few<F16, 16>(a, dim, row_tiles, grid, join_rows, st);
 }
 }  // namespace kmi

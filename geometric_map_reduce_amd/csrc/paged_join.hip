@@ -5,14 +5,10 @@
 namespace kmi {
 
 // paged_few_*.hip and paged_many_*.hip
-int few_bf16(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
-int few_f16(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
-int few_bf16_e4m3(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
-int few_f16_e4m3(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
-void many_bf16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
-void many_f16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
-void many_bf16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
-void many_f16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
+using FewLaunch = int(const AttendArgs &a, int dim, int row_tiles, int grid, int join_rows, hipStream_t st);
+using ManyLaunch = void(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
+FewLaunch few_bf16, few_f16, few_bf16_e4m3, few_f16_e4m3, few_bf16_e2m1, few_f16_e2m1;
+ManyLaunch many_bf16, many_f16, many_bf16_e4m3, many_f16_e4m3, many_bf16_e2m1, many_f16_e2m1;
 
 namespace {
 
@@ -89,20 +85,24 @@ __global__ __launch_bounds__(256) void sums_join_kernel(AttendArgs a) {
 
 }  // namespace
 
-int launch_attend_few(const AttendArgs &a, int type, bool e4m3, int dim, int row_tiles, int grid, int join_rows,
+int launch_attend_few(const AttendArgs &a, int type, int bits, int dim, int row_tiles, int grid, int join_rows,
                       hipStream_t st) {
-  if (type == CT_BF16) return (e4m3 ? few_bf16_e4m3 : few_bf16)(a, dim, row_tiles, grid, join_rows, st);
-  return (e4m3 ? few_f16_e4m3 : few_f16)(a, dim, row_tiles, grid, join_rows, st);
+  FewLaunch *f = type == CT_BF16 ? (bits == 4 ? few_bf16_e2m1 : bits == 8 ? few_bf16_e4m3 : few_bf16)
+                                 : (bits == 4 ? few_f16_e2m1 : bits == 8 ? few_f16_e4m3 : few_f16);
+  return f(a, dim, row_tiles, grid, join_rows, st);
 }
 
-void launch_attend_many(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st) {
-  if (type == CT_BF16) (e4m3 ? many_bf16_e4m3 : many_bf16)(a, dim, false, grid, st);
-  else (e4m3 ? many_f16_e4m3 : many_f16)(a, dim, false, grid, st);
+static ManyLaunch *many_of(int type, int bits) {
+  return type == CT_BF16 ? (bits == 4 ? many_bf16_e2m1 : bits == 8 ? many_bf16_e4m3 : many_bf16)
+                         : (bits == 4 ? many_f16_e2m1 : bits == 8 ? many_f16_e4m3 : many_f16);
 }
 
-void launch_attend_sums(const AttendArgs &a, int type, bool e4m3, int dim, dim3 grid, hipStream_t st) {
-  if (type == CT_BF16) (e4m3 ? many_bf16_e4m3 : many_bf16)(a, dim, true, grid, st);
-  else (e4m3 ? many_f16_e4m3 : many_f16)(a, dim, true, grid, st);
+void launch_attend_many(const AttendArgs &a, int type, int bits, int dim, dim3 grid, hipStream_t st) {
+  many_of(type, bits)(a, dim, false, grid, st);
+}
+
+void launch_attend_sums(const AttendArgs &a, int type, int bits, int dim, dim3 grid, hipStream_t st) {
+  many_of(type, bits)(a, dim, true, grid, st);
 }
 
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st) {

@@ -72,8 +72,9 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
 
-template <class T, bool E4M3, int D>
+template <class T, int BITS, int D>
 __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
+  constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4, NARROW = E4M3 || E2M1;
   // slots of a tile: two halves are two independent chains of products (one of 32 waited for itself:
   // D = 256 ran at 647 instead of 759 TFLOP/s)
   constexpr int KT = 64;
@@ -81,8 +82,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   constexpr int kPieces = D / 8;                     // 16-byte pieces of a row in LDS
   constexpr int kLoads = KT * kPieces / kManyThreads;
   // tiles in LDS: as many as leave room for two work-groups on a compute unit (one at D = 256; 8-bit
-  // ones pass registers, one ahead)
-  constexpr int kBufs = E4M3 ? 2 : (D == 64 ? 4 : (D == 96 ? 3 : 2));
+  // and 4-bit ones pass registers, one ahead)
+  constexpr int kBufs = NARROW ? 2 : (D == 64 ? 4 : (D == 96 ? 3 : 2));
   constexpr int kChunk = D == 96 ? 4 : 8;            // tiles whose addresses are placed together
   constexpr int kPlace = kChunk * KT / kManyThreads; // slots a thread places
   static_assert(kBufs <= kChunk, "a chunk is placed before the first fetch from it");
@@ -91,6 +92,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   __shared__ __align__(16) uint16_t sk[kBufs][KT * D];
   __shared__ __align__(16) uint16_t sv[kBufs][KT * D];
   __shared__ int64_t off[2][kChunk * KT];
+  __shared__ uint32_t number[E2M1 ? 2 : 1][E2M1 ? kChunk * KT : 1];     // the slots' among all powers
   __shared__ uint64_t present[2][kChunk];              // which of a tile's slots are there
   __shared__ int sh_odd;                               // a wave cleared non-finite values for all
 
@@ -171,7 +173,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
       const int at = i * kManyThreads + tid, j = lo + chunk * kChunk * KT + at;
       const uint32_t row = (uint32_t)j - fast_div(a.c.page, (uint32_t)j) * a.c.page.d;
       const int64_t o = place_offset(a.c, SlotPlace{page[i], row});
-      off[chunk & 1][at] = E4M3 || o >= 0 ? o : 0;
+      off[chunk & 1][at] = NARROW || o >= 0 ? o : 0;
+      if (E2M1) number[chunk & 1][at] = place_number(a.c, SlotPlace{page[i], row}, h);
       const uint64_t there = __ballot(page[i] >= 0);
       if (lane == 0) present[chunk & 1][i * 4 + wave] = there;
     }
@@ -180,12 +183,31 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
 
   const auto there_at = [&](int tile) { return present[(tile / kChunk) & 1][tile % kChunk]; };
 
-  // A tile on its way: 16-bit caches go straight to LDS, 8-bit ones by way of registers.
-  uint32_t gk[kLoads][2], gv[kLoads][2];
+  // A tile on its way: 16-bit caches go straight to LDS, narrower ones by way of registers.  A thread of a 4-bit
+  // one has whole blocks, 16 bytes and their power: those of K first, then those of V (no wave has both but at D = 96).
+  constexpr int kBlocks = D / kPowerBlock, kItems = (2 * KT * kBlocks + kManyThreads - 1) / kManyThreads;
+  uint32_t gk[E4M3 ? kLoads : 1][2], gv[E4M3 ? kLoads : 1][2];
+  u32x4 gb[E2M1 ? kItems : 1];
+  uint32_t gp[E2M1 ? kItems : 1];
   uint32_t held = 0;
   const auto fetch = [&](int tile) {
     const int64_t *po = off_at(tile);
-    if (E4M3) {
+    if constexpr (E2M1) {
+      held = 0;
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        int id = tid + i * kManyThreads;
+        const bool v = id >= KT * kBlocks;
+        id -= v ? KT * kBlocks : 0;
+        if (id >= KT * kBlocks) break;               // D = 96: the last half round
+        const int row = id / kBlocks, b = id - row * kBlocks;
+        int64_t o = po[row];
+        if (o >= 0) held |= 1u << i;
+        o = o < 0 ? 0 : o;
+        gb[i] = *(const u32x4 *)((v ? vbase : kbase) + o + b * 16);
+        gp[i] = (v ? a.c.v_power : a.c.k_power)[(uint64_t)number[(tile / kChunk) & 1][tile % kChunk * KT + row] * kBlocks + b];
+      }
+    } else if constexpr (E4M3) {
       held = 0;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -213,7 +235,21 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     }
   };
   const auto arrive = [&](int tile) {
-    if (E4M3) {
+    if constexpr (E2M1) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        int id = tid + i * kManyThreads;
+        const bool v = id >= KT * kBlocks;
+        id -= v ? KT * kBlocks : 0;
+        if (id >= KT * kBlocks) break;
+        const int row = id / kBlocks, b = id - row * kBlocks;
+        uint16_t *to = (v ? sv[tile % kBufs] : sk[tile % kBufs]) + row * D;
+        const int x = v ? v_swizzle<D>(row) : k_swizzle<D>(row);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *(u32x4 *)&to[((4 * b + u) ^ x) * 8] = keep_if(widen_e2m1<T>(gb[i][u], gp[i]), (held >> i) & 1u);
+      }
+    } else if constexpr (E4M3) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int id = tid + i * kManyThreads, row = id / kPieces, p = id - row * kPieces;
@@ -355,15 +391,20 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
     const int stop = lo + tiles * KT < end ? lo + tiles * KT : end;
     for (int j = lo; j < stop; ++j) {
       if (!(j > first_pos || (a.window > 0 && j <= last_pos - a.window))) continue;
-      const int64_t o = place_offset(a.c, slot_place(a.c, trow, (uint32_t)j));
+      const SlotPlace pl = slot_place(a.c, trow, (uint32_t)j);
+      const int64_t o = place_offset(a.c, pl);
       if (o < 0 || j > pos || (a.window > 0 && j <= pos - a.window)) continue;
 #pragma unroll
       for (int n = 0; n < kCols; ++n)
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
-          const char *e = vbase + o + (n * 32 + slot32(k, hi)) * (E4M3 ? 1 : 2);
+          const int d = n * 32 + slot32(k, hi);
+          const char *e = vbase + o + d * BITS / 8;
           u32x2 x;
-          if (E4M3) {
+          if (E2M1) {
+            const uint32_t w = *(const uint16_t *)e, power = a.c.v_power[(uint64_t)place_number(a.c, pl, h) * kBlocks + n];
+            x = (u32x2){T::template from_e2m1<0>(w, power), T::template from_e2m1<1>(w, power)};
+          } else if (E4M3) {
             const uint32_t w = *(const uint32_t *)e;
             x = (u32x2){T::template from_e4m3<false>(w), T::template from_e4m3<true>(w)};
           } else {
@@ -409,8 +450,9 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
 // Column sums.  Grid: slot tiles x heads x sequences x row splits.  A wave holds K of 64 slots and
 // reads each Q tile from LDS once for both halves: with 32 the LDS reads alone would take as long
 // as the products.
-template <class T, bool E4M3, int D>
+template <class T, int BITS, int D>
 __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_kernel(AttendArgs a) {
+  constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4;
   constexpr int QT = 64;                             // rows of a tile
   constexpr int kSteps = D / 16, kPieces = D / 8;
   constexpr int kLoads = QT * kPieces / kManyThreads;
@@ -459,9 +501,11 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
     if (tile0 >= tile1) break;       // no row sees the tile
     const int64_t o = place_offset(a.c, pl[x]);
     const char *kp = a.c.k + (int64_t)h * a.c.head_stride + (o < 0 ? 0 : o);
+    const uint8_t *powers = E2M1 ? a.c.k_power + (uint64_t)place_number(a.c, pl[x], h) * (D / kPowerBlock) : nullptr;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      if (E4M3) kf[x][i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
+      if (E2M1) kf[x][i] = widen_e2m1<T>(*(const uint32_t *)(kp + i * 8 + hi * 4), powers[i / 2]);
+      else if (E4M3) kf[x][i] = widen_e4m3<T>(*(const u32x2 *)(kp + i * 16 + hi * 8));
       else kf[x][i] = *(const u32x4 *)(kp + i * 32 + hi * 16);
     }
   }
@@ -581,24 +625,19 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_sums_ker
   }
 }
 
-template <class T, bool E4M3>
+template <class T, int BITS>
 void launch_many(const AttendArgs &a, int dim, dim3 grid, hipStream_t st) {
-  if (dim == 64) attend_many_kernel<T, E4M3, 64><<<grid, kManyThreads, 0, st>>>(a);
-  else if (dim == 96) attend_many_kernel<T, E4M3, 96><<<grid, kManyThreads, 0, st>>>(a);
-  else if (dim == 128) attend_many_kernel<T, E4M3, 128><<<grid, kManyThreads, 0, st>>>(a);
-  else attend_many_kernel<T, E4M3, 256><<<grid, kManyThreads, 0, st>>>(a);
+  if (dim == 64) attend_many_kernel<T, BITS, 64><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 96) attend_many_kernel<T, BITS, 96><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 128) attend_many_kernel<T, BITS, 128><<<grid, kManyThreads, 0, st>>>(a);
+  else attend_many_kernel<T, BITS, 256><<<grid, kManyThreads, 0, st>>>(a);
 }
-template <class T, bool E4M3>
+template <class T, int BITS>
 void launch_sums(const AttendArgs &a, int dim, dim3 grid, hipStream_t st) {
-  if (dim == 64) attend_sums_kernel<T, E4M3, 64><<<grid, kManyThreads, 0, st>>>(a);
-  else if (dim == 96) attend_sums_kernel<T, E4M3, 96><<<grid, kManyThreads, 0, st>>>(a);
-  else if (dim == 128) attend_sums_kernel<T, E4M3, 128><<<grid, kManyThreads, 0, st>>>(a);
-  else attend_sums_kernel<T, E4M3, 256><<<grid, kManyThreads, 0, st>>>(a);
+  if (dim == 64) attend_sums_kernel<T, BITS, 64><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 96) attend_sums_kernel<T, BITS, 96><<<grid, kManyThreads, 0, st>>>(a);
+  else if (dim == 128) attend_sums_kernel<T, BITS, 128><<<grid, kManyThreads, 0, st>>>(a);
+  else attend_sums_kernel<T, BITS, 256><<<grid, kManyThreads, 0, st>>>(a);
 }
-
-void many_bf16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
-void many_f16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
-void many_bf16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
-void many_f16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st);
 
 }  // namespace kmi

@@ -2,7 +2,7 @@
 #include "paged_many.h"
 namespace kmi {
 void many_bf16(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st) {
-  if (sums) launch_sums<Bf16, false>(a, dim, grid, st);
-  else launch_many<Bf16, false>(a, dim, grid, st);
+  if (sums) launch_sums<Bf16, 16>(a, dim, grid, st);
+  else launch_many<Bf16, 16>(a, dim, grid, st);
 }
 }  // namespace kmi

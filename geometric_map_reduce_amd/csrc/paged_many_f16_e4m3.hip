@@ -2,7 +2,7 @@
 #include "paged_many.h"
 namespace kmi {
 void many_f16_e4m3(const AttendArgs &a, int dim, bool sums, dim3 grid, hipStream_t st) {
-  if (sums) launch_sums<F16, true>(a, dim, grid, st);
-  else launch_many<F16, true>(a, dim, grid, st);
+  if (sums) launch_sums<F16, 8>(a, dim, grid, st);
+  else launch_many<F16, 8>(a, dim, grid, st);
 }
 }  // namespace kmi

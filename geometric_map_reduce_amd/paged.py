@@ -2,8 +2,9 @@
 include/keops_mi355x.h, where the operators are defined).
 
 A cache is a pair of page pools ``k_pages``, ``v_pages`` of shape [pages, page_size, heads, dim]
-(any order of strides in the first three, the same for both), bfloat16, float16 or float8_e4m3fn with
-``k_scale``, ``v_scale`` [heads]; ``weights`` [pages, heads, page_size] float32 holds the
+(any order of strides in the first three, the same for both), bfloat16, float16, float8_e4m3fn with
+``k_scale``, ``v_scale`` [heads], or float4_e2m1fn_x2 (two values an element: [.., dim / 2]) with ``k_scale``,
+``v_scale`` [pages, heads, page_size, dim / 32] float8_e8m0fnu, a power of two for 32 columns; ``weights`` [pages, heads, page_size] float32 holds the
 attention that each slot received.  ``page_table`` [sequences, width], ``lens`` [sequences] and
 ``starts`` [sequences + 1] are int32 tensors on the same device; the calls read none of them on
 the host and never synchronise.
@@ -19,6 +20,7 @@ have been made by then, so the call is not made again.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import struct
@@ -27,7 +29,7 @@ import torch
 
 from .binding import LIB_PATH, _check, _out, _raw_stream, _stream, lib
 
-_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2, torch.float4_e2m1fn_x2: 4}
 
 
 # keops_cache_t: k_pages, v_pages, weights, k_scale, v_scale; page, slot and head stride, pages;
@@ -70,11 +72,14 @@ def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales
     dev, dtype, shape, strides = k_pages.get_device(), k_pages.dtype, k_pages.shape, k_pages.stride()
     kind = _TYPES.get(dtype)
     if len(shape) != 4 or kind is None or dev < 0 or strides[3] != 1:
-        raise ValueError("k_pages must be a bfloat16, float16 or float8_e4m3fn CUDA tensor "
+        raise ValueError("k_pages must be a bfloat16, float16, float8_e4m3fn or float4_e2m1fn_x2 CUDA tensor "
                          "[pages, page_size, heads, dim] with contiguous rows")
     if v_pages.shape != shape or v_pages.dtype is not dtype or v_pages.get_device() != dev or v_pages.stride() != strides:
         raise ValueError("v_pages must have the shape, type, device and strides of k_pages")
     P, ps, H, D = shape
+    two = 1
+    if kind == 4:       # an element of two values
+        D, two = 2 * D, 2
     if D not in (64, 96, 128, 256):
         raise ValueError(f"dim must be 64, 96, 128 or 256, got {D}")
     if lens.dim() != 1 or lens.dtype is not torch.int32 or lens.get_device() != dev or not lens.is_contiguous():
@@ -90,30 +95,39 @@ def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales
                 raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
             ks = _vec(k_scale, "k_scale", (H,), torch.float32, dev)
             vs = _vec(v_scale, "v_scale", (H,), torch.float32, dev)
+    elif kind == 4:
+        if k_scale is None or v_scale is None:
+            raise ValueError("a float4_e2m1fn_x2 cache needs k_scale and v_scale")
+        ks = _vec(k_scale, "k_scale", (P, H, ps, D // 32), torch.float8_e8m0fnu, dev)
+        vs = _vec(v_scale, "v_scale", (P, H, ps, D // 32), torch.float8_e8m0fnu, dev)
     elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
+        raise ValueError("k_scale and v_scale belong to a float8_e4m3fn or float4_e2m1fn_x2 cache")
     # the stride of a dimension of one is never used
-    c = _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), w, ks, vs, strides[0] if P > 1 else 0, strides[1] if ps > 1 else 0,
-                    strides[2] if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind, width, S)
+    c = _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), w, ks, vs, strides[0] * two if P > 1 else 0,
+                    strides[1] * two if ps > 1 else 0, strides[2] * two if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind, width, S)
     return c, dev, S, (H, D, dtype), ps, width
 
 
 _short = None
 
 
-def _native():
-    """The short way's module; nothing before the library is built, which the long way reports."""
-    global _short
+def _module(name):
+    """A module of the short way; nothing before the library is built, which the long way reports."""
     if not os.path.exists(LIB_PATH):
         return None
     lib()
     try:
-        from . import _paged_call
+        module = importlib.import_module("." + name, __package__)
     except ImportError as e:
-        raise RuntimeError("the paged calls' module is missing or broken: build it first "
+        raise RuntimeError(f"the module {name} is missing or broken: build it first "
                            "(python -m geometric_map_reduce_amd.build)") from e
-    _paged_call.bind(_raw_stream)
-    _short = _paged_call
+    module.bind(_raw_stream)
+    return module
+
+
+def _native():
+    global _short
+    _short = _module("_paged_call")
     return _short
 
 
@@ -135,7 +149,7 @@ def _rows(t, name, heads, cache, dev):
     if len(shape) != 3 or dtype not in _HALF or t.get_device() != dev or shape[2] != D or \
             (heads is not None and shape[1] != heads) or (held in _HALF and dtype is not held):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {D}], of the cache's type "
-                         f"(bfloat16 or float16 with an 8-bit cache), on cuda:{dev}")
+                         f"(bfloat16 or float16 with an 8-bit or 4-bit cache), on cuda:{dev}")
     T, h, _ = shape
     s0, s1, s2 = t.stride()
     if T and (s2 != 1 or (h > 1 and s1 != D)):
@@ -253,18 +267,19 @@ def keops_paged_attention(q, k_pages, v_pages, page_table, lens, starts, max_q, 
 
 
 def keops_cache_evict(k_pages, v_pages, weights, page_table, lens, new_table, budget, sink=0, recent=0, kept=None,
-                      new_lens=None, stream=None):
+                      new_lens=None, stream=None, k_scale=None, v_scale=None):
     """Keep ``budget`` slots of every sequence and head: the first ``sink``, the last ``recent``, and those with
     the largest weights; move them to the pages of ``new_table``.  Returns (kept [sequences, heads, budget]
     old slot numbers or -1, new lens).  Slots whose page the table lacks are left out, and not counted in the
-    new lens.  The scales of an 8-bit cache are not needed."""
+    new lens.  The scales of an 8-bit cache are not needed; those of a 4-bit cache belong to its slots and move
+    with them."""
     if stream is None:
         short = _short or _native()
-        got = short and short.evict(k_pages, v_pages, weights, page_table, lens, None, None, new_table, budget, sink, recent, kept,
+        got = short and short.evict(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, new_table, budget, sink, recent, kept,
                                     new_lens)
         if got:
             return _ended("keops_cache_evict", got)
-    c, dev, S, (H, _, _), ps, width = _cache(k_pages, v_pages, weights, page_table, lens, None, None, scales=False)
+    c, dev, S, (H, _, _), ps, width = _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales=False)
     if weights is None:
         raise ValueError("eviction needs weights")
     nt, nstride, nwidth = _table(new_table, "new_table", S, dev)

@@ -267,17 +267,33 @@ int keops_kmin(const float *x, const float *y, const float *b,
  *  keys to append or to move in 16-byte pieces) is KEOPS_ERR_UNSUPPORTED.
  *  k_pages and v_pages share their strides: [pages][page_size][heads][dim] in any order of
  *  the first three.  dim: 64, 96, 128 or 256.
- *  Types: KEOPS_TYPE_BF16 or _F16 for q, k, v, out, with a cache of the same type or of
- *  KEOPS_TYPE_E4M3 (OCP e4m3, finite to 448), whose elements stand for value * scale[head].
+ *  Types: KEOPS_TYPE_BF16 or _F16 for q, k, v, out, with a cache of the same type, of
+ *  KEOPS_TYPE_E4M3 (OCP e4m3, finite to 448), whose elements stand for value * scale[head],
+ *  or of KEOPS_TYPE_E2M1: 4 bits an element (OCP e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign),
+ *  two to a byte, the first in its low half; each 32 columns of a row share a power of two, a
+ *  byte b that stands for 2^(b - 127), 255 for NaN.  The powers of keys and values are dense
+ *  arrays [pages][heads][page_size][dim / 32], 16-byte aligned, of at most 2^32 - 1 slots and
+ *  heads.  A held value is read as the nearest one of the rows' type (bf16: exact but for
+ *  powers past 252, fp16: exact for powers of 104 to 140).
+ *  KEOPS_TYPE_F32 is for keops_rotary and keops_adjust_logits only.
  */
 #define KEOPS_TYPE_BF16 0
 #define KEOPS_TYPE_F16 1
 #define KEOPS_TYPE_E4M3 2
+#define KEOPS_TYPE_F32 3
+#define KEOPS_TYPE_E2M1 4
 
 typedef struct {
   void *k_pages, *v_pages;
   float *weights;                 /* [pages][heads][page_size], or NULL          */
-  const float *k_scale, *v_scale; /* [heads]; KEOPS_TYPE_E4M3 only (eviction does not read them) */
+  union {
+    const float *k_scale;         /* [heads]; KEOPS_TYPE_E4M3 only (eviction does not read them) */
+    uint8_t *k_powers;            /* KEOPS_TYPE_E2M1: of the blocks                */
+  };
+  union {
+    const float *v_scale;
+    uint8_t *v_powers;
+  };
   int64_t page_stride, slot_stride, head_stride;
   int64_t pages;
   const int32_t *page_table;      /* [seqs][table_width], rows table_stride apart */
@@ -291,9 +307,61 @@ typedef struct {
  * k_stride and v_stride apart) to the slot of token t.  E4M3 caches hold the value nearest
  * to k / k_scale[head] (ties to even), cut to +-448; NaN stays NaN.  Where the cache has
  * weights, those of the written slots become 0.  starts: [seqs + 1].
+ * E2M1 caches: a block of 32 columns takes the least power under which none of them rounds to
+ * more than 6 (at most 2^125 for bf16 rows and 2^13 for fp16 ones, so that held values are
+ * finite in the rows' type; elements past 6 under that are cut to it), each column the nearest
+ * value, halfway the one with the even code.  A block with a NaN or an infinity becomes NaN.
  */
 int keops_cache_append(const keops_cache_t *cache, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
                        int32_t type, const int32_t *starts, int64_t tokens, void *stream);
+
+/*
+ * Rotary positions.  Pair i of a head turns by the angle position * freqs[i] (64 bits, the
+ * product as it is; angles up to 2^50):
+ *   a' = factor (a cos - b sin),  b' = factor (a sin + b cos)
+ * Half layout: a is column i, b column i + pairs; interleaved: columns 2 i and 2 i + 1.
+ * Columns from 2 pairs on stay as they are.  Scaled frequencies and a factor other than 1 serve
+ * texts longer than those that a model was trained on.
+ */
+typedef struct {
+  const double *freqs;            /* [pairs], radians a position; device           */
+  double factor;
+  int32_t pairs;                  /* 2 pairs <= dim                                */
+  int32_t interleaved;
+} keops_rotary_t;
+
+/*
+ * out = x rotated, x [tokens][heads][dim] of KEOPS_TYPE_BF16, _F16 or _F32, token t's row at
+ * x + t x_stride, its heads dense; out likewise, out_stride at least a row.  dim up to 65536, pairs
+ * up to 8192, element-aligned; heads of whole aligned 16 bytes run fastest.  out may be x itself, with the same stride, and must not overlap it otherwise.
+ * inverse: the angles' signs turned, which with the same factor is the gradient: out = dL/dx for
+ * x = dL/dout.  positions: [tokens] int32, of either sign.
+ */
+int keops_rotary(const void *x, int64_t x_stride, int32_t type, int64_t tokens, int32_t heads, int32_t dim,
+                 const int32_t *positions, const keops_rotary_t *rotary, int32_t inverse, void *out, int64_t out_stride,
+                 void *stream);
+
+/*
+ * keops_cache_append with rotary positions on the way: q_out = q rotated, k rotated into its
+ * slot, v into its slot as it is.  The position of token t is positions[t], or, where positions
+ * is NULL, the number of its slot.  Rounded once: an 8-bit or 4-bit cache holds what is nearest
+ * to the rotated key (E4M3: its quotient) itself.  q: [tokens][heads][dim], rows q_stride apart;
+ * q_out likewise, q_out_stride apart, heads any number (0: no q, q_out is not read).  Rows of q_out
+ * of tokens in no sequence stay as they were; a token without a slot has its q rotated.
+ */
+int keops_cache_append_rotary(const keops_cache_t *cache, const void *q, const void *k, const void *v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int32_t type, int32_t heads, const int32_t *starts,
+                              int64_t tokens, const int32_t *positions, const keops_rotary_t *rotary, void *q_out,
+                              int64_t q_out_stride, void *stream);
+
+/*
+ * The values held in the slots of every sequence's last starts[s+1] - starts[s] tokens, as 16-bit
+ * rows: k and v [tokens][heads][dim], rows k_stride and v_stride apart (starts 0 .. lens: whole
+ * sequences).  type: the cache's own, or either 16-bit one of an 8-bit or 4-bit cache, to nearest.
+ * Rows of slots that are absent are 0, those of tokens in no sequence stay as they were.
+ */
+int keops_cache_read(const keops_cache_t *cache, void *k, void *v, int64_t k_stride, int64_t v_stride, int32_t type,
+                     const int32_t *starts, int64_t tokens, void *stream);
 
 /*
  * Causal attention of every sequence's new tokens over its slots:
@@ -356,6 +424,39 @@ int keops_verify_draft(const float *target, const float *draft, const int32_t *t
 
 /* Workspace bytes of a keops_verify_draft call. */
 int keops_verify_draft_workspace(int32_t seqs, int32_t drafts, int32_t vocab, int64_t *bytes);
+
+/*
+ * Logits by a text's penalties, biases and masks.  Row r of sequence s (rows starts[s] ..
+ * starts[s+1]) has seen the text up to token j = lens[s] - (starts[s+1] - starts[s]) + r, as a
+ * token's query has seen the slots up to its own; a row before the text's start has seen nothing.
+ * With c the times that a vocabulary entry x occurs among text[s][prompt_lens[s] .. j]:
+ *   z = logits[t][x]
+ *   if x occurs in text[s][0 .. j]:  z = z > 0 ? z / repetition[s] : z * repetition[s]
+ *   z = z - frequency[s] c - (c > 0 ? presence[s] : 0) + (bias of x in the list of s, if any)
+ *   z = -inf where x's bit of the row's mask is 0
+ * in 64 bits where a rule touches an entry, rounded once; untouched entries stay as they are.
+ * A NULL array leaves its rule out.  Entries of text and bias_tokens outside [0, vocab) count for
+ * nothing; of several equal bias_tokens the last stands.  mask: [rows][ceil(vocab / 32)], bit
+ * x % 32 of word x / 32, rows mask_stride apart.  Rows of no sequence stay as they were.
+ * logits and out: [rows][vocab] of KEOPS_TYPE_BF16, _F16 or _F32, rows stride and out_stride
+ * apart; out may be logits itself, with the same stride, and must not overlap it otherwise.
+ */
+typedef struct {
+  const int32_t *starts;          /* [seqs + 1]                                    */
+  const int32_t *text;            /* [seqs][text_width], rows text_stride apart    */
+  int64_t text_stride;
+  const int32_t *lens;            /* [seqs], needed with text                      */
+  const int32_t *prompt_lens;     /* [seqs]; NULL: 0                               */
+  const float *repetition, *presence, *frequency;     /* [seqs], with text         */
+  const int32_t *bias_tokens;     /* [seqs][biases], dense                         */
+  const float *bias;              /* [seqs][biases]                                */
+  const int32_t *mask;
+  int64_t mask_stride;
+  int32_t seqs, text_width, biases;
+} keops_logit_rules_t;
+
+int keops_adjust_logits(const void *logits, int64_t stride, int32_t type, int64_t rows, int32_t vocab,
+                        const keops_logit_rules_t *rules, void *out, int64_t out_stride, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *keops_status_string(int status);

@@ -1,0 +1,791 @@
+"""Rotary positions, the rotating append, the 4-bit cache, reading slots back and the adjustment of logits on the GPU,
+through the binding, against plain 64-bit forms (step_reference.py, paged_reference.py).  Tolerances are the bounds
+derived there; what is held in 4 or 8 bits has to be equal."""
+from __future__ import annotations
+
+import random
+
+import pytest
+import torch
+
+import paged_reference as ref
+import step_reference as sref
+from step_reference import E2, Batch4
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import geometric_map_reduce_amd as gm
+
+BF, FP, F32, E4, E8 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+
+
+def say(msg):
+    print(msg, flush=True)
+
+
+def put(t):
+    return None if t is None else t.cuda()
+
+
+def close(got, want, tol, what):
+    got, want = got.double(), want.double()
+    same = (got == want) | (got.isnan() & want.isnan())
+    bad = ~(same | ((got - want).abs() <= tol))
+    if bool(bad.any()):
+        i = tuple(torch.nonzero(bad)[0].tolist())
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {i}: {got[i].item()} for "
+                             f"{want[i].item()}, tolerance {tol[i].item() if torch.is_tensor(tol) else tol}")
+
+
+def pools(b):
+    """(pages, scales) of keys and values on the GPU, as a call takes them."""
+    k, v = put(b.k), put(b.v)
+    if isinstance(b, Batch4):
+        return k.view(E2), v.view(E2), put(b.k_scale).view(E8), put(b.v_scale).view(E8)
+    return k, v, put(b.k_scale), put(b.v_scale)
+
+
+def raw(t):
+    return t.cpu().view(torch.uint8)
+
+
+# ---- rotary positions
+
+ROTARY = [
+    # tokens, heads, dim, rotated columns
+    (1, 1, 2, 2), (1, 40, 128, 128), (7, 3, 128, 64), (33, 5, 96, 96), (5, 2, 80, 40), (64, 1, 64, 2), (3, 2, 6, 4), (9, 3, 7, 6),
+    (4, 2, 256, 0), (300, 8, 256, 256), (2, 1, 4096, 4096), (1100, 2, 64, 48), (2500, 3, 32, 24), (1, 1, 1, 0),
+]
+
+
+@pytest.mark.parametrize("tokens,heads,dim,rot", ROTARY)
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary(tokens, heads, dim, rot, dtype, interleaved):
+    say(f"rotary {tokens} x {heads} x {dim}, {rot} turn, {dtype}, interleaved {interleaved}")
+    g = torch.Generator().manual_seed(tokens * 7 + dim)
+    x = torch.randn((tokens, heads, dim), generator=g).to(dtype)
+    at = torch.randint(-(1 << 20), 1 << 20, (tokens,), generator=g).to(torch.int32)
+    at[0] = 0 if tokens > 1 else 2 ** 31 - 1
+    at[-1] = -2 ** 31 if tokens > 2 else at[-1]
+    freqs = gm.keops_rotary_frequencies(rot, 500000.0) if rot else torch.zeros(0, dtype=torch.float64)
+    for factor, inverse in ((1.0, False), (-1.3, True)):
+        y = gm.keops_rotary(put(x), put(at), put(freqs), interleaved=interleaved, factor=factor, inverse=inverse)
+        want = sref.rotate(x, at, freqs, interleaved, factor, inverse)
+        close(y.cpu(), want, sref.rotate_bound(x, want, freqs, dtype, factor), "rotary")
+        assert torch.equal(y[..., rot:].cpu(), x[..., rot:])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rotary_in_place_and_in_wider_rows(dtype, interleaved):
+    """Queries and keys of one product's rows, in place; values beside them and guards stay."""
+    for dim, rot in ((64, 64), (64, 20), (36, 36), (10, 6)):
+        say(f"rotary in place, {dim} {rot} {dtype} {interleaved}")
+        g = torch.Generator().manual_seed(dim)
+        wide = torch.randn((50, 3, 4, dim), generator=g).to(dtype)
+        at = torch.arange(50, dtype=torch.int32)
+        freqs = gm.keops_rotary_frequencies(rot)
+        dev = put(wide)
+        x = dev[:, 1]
+        want = gm.keops_rotary(x, put(at), put(freqs), interleaved=interleaved)
+        assert gm.keops_rotary(x, put(at), put(freqs), interleaved=interleaved, out=x) is x
+        assert torch.equal(x, want)
+        ref64 = sref.rotate(wide[:, 1], at, freqs, interleaved)
+        close(want.cpu(), ref64, sref.rotate_bound(wide[:, 1], ref64, freqs, dtype), "rotary")
+        assert torch.equal(dev[:, 0].cpu(), wide[:, 0]) and torch.equal(dev[:, 2].cpu(), wide[:, 2])
+        # from a place that 16 bytes do not divide
+        flat = torch.randn(50 * 4 * dim + 1, generator=g).to(dtype)
+        x = flat[1:].view(50, 4, dim)
+        got = gm.keops_rotary(put(flat)[1:].view(50, 4, dim), put(at), put(freqs), interleaved=interleaved)
+        ref64 = sref.rotate(x, at, freqs, interleaved)
+        close(got.cpu(), ref64, sref.rotate_bound(x, ref64, freqs, dtype), "rotary")
+
+
+def test_rotary_gradient():
+    """The inverse rotation is the gradient: against the plain form's by autograd and against differences."""
+    say("rotary gradient")
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((20, 3, 24), generator=g)
+    dy = torch.randn((20, 3, 24), generator=g)
+    at = torch.randint(0, 5000, (20,), generator=g).to(torch.int32)
+    freqs = gm.keops_rotary_frequencies(16)
+    for interleaved in (False, True):
+        leaf = x.double().requires_grad_()
+        sref.rotate(leaf, at, freqs, interleaved, 1.7).backward(dy.double())
+        args = put(at), put(freqs), interleaved, 1.7
+        got = gm.keops_rotary(put(dy), *args, inverse=True).cpu()
+        close(got, leaf.grad, sref.rotate_bound(dy, leaf.grad, freqs, F32, 1.7), "gradient")
+        # the map is linear: a difference along any direction is its value there
+        h = torch.randn(x.shape, generator=g)
+        step = (gm.keops_rotary(put(x + h), *args).double() - gm.keops_rotary(put(x - h), *args).double()).cpu() / 2
+        # of some 1,440 products of size up to 1.7 * 4 * 4, each rounded a few times
+        assert abs((step * dy).sum() - (got.double() * h).sum()) <= 1440 * 30 * 16 * ref.U32
+
+
+def test_rotary_far_angles_and_non_finite():
+    say("rotary far angles")
+    at = torch.tensor([2 ** 31 - 1, 2 ** 30 + 7, -2 ** 31, 999999999], dtype=torch.int32)
+    freqs = torch.tensor([1.0, 3.1415926535897931, 0.3, 1234.5678], dtype=torch.float64)
+    x = torch.tensor([1.0, 0.5, 0.0, -2.0, 0.0, 1.0, 1.0, 3.0])[None, None].repeat(4, 1, 1)
+    y = gm.keops_rotary(put(x), put(at), put(freqs))
+    want = sref.rotate(x, at, freqs)
+    close(y.cpu(), want, sref.rotate_bound(x, want, freqs, F32), "far angles")
+    x[1, 0, 2] = float("nan")
+    x[2, 0, 1] = float("inf")
+    y = gm.keops_rotary(put(x), put(at), put(freqs)).cpu()
+    for t, c in ((1, 2), (2, 1)):
+        assert not bool(y[t, 0, [c, c + 4]].isfinite().any())
+        others = [i for i in range(8) if i % 4 != c % 4]
+        close(y[t, 0, others], want[t, 0, others], sref.rotate_bound(x[t:t + 1].nan_to_num(0, 0, 0), want[t:t + 1], freqs, F32)[0, 0, others], "others")
+
+
+# ---- the rotating append
+
+APPEND = [
+    # lens, new, query heads, key/value heads, dim, page, rotated columns
+    ([1], [1], 1, 1, 64, 16, 64), ([40, 0, 300, 7], [3, 0, 300, 1], 4, 2, 96, 20, 96), ([129] * 70, [1] * 70, 8, 4, 128, 32, 64),
+    ([50, 2], [5, 4], 0, 3, 256, 1, 256), ([77], [60], 6, 2, 128, 24, 40), ([30, 900], [2, 5], 2, 1, 64, 7, 6), ([5000], [5000], 2, 1, 64, 64, 64),
+]
+
+
+def append_batch(lens, new, heads, kv, dim, page, dtype, cache, seed=31):
+    if cache == E2:
+        b = Batch4(seed, lens, new, max(heads, 1), kv, dim, page, dtype, junk=0.0)
+    else:
+        b = ref.Batch(seed, lens, new, max(heads, 1), kv, dim, page, dtype, cache, junk=0.0)
+    wide = (torch.randn((b.T, heads + 2 * kv, dim), generator=b.gen) * 2).to(dtype)
+    return b, wide
+
+
+def check_append(b, wide, heads, freqs, positions, interleaved, factor, weights=None, own=False):
+    """Pools, weights and queries after a call; `own`: through keops_cache_append, without a rotation."""
+    kv = b.kv
+    k, v, ks, vs = pools(b)
+    w, dev = put(weights), put(wide)
+    where = torch.tensor([0] * b.T, dtype=torch.int32)
+    for t, _, j, _, _ in sref.places(b):
+        where[t] = j
+    at = where if positions is None else positions
+    args = (k, v, put(b.table), put(b.lens_t()), put(b.starts))
+    if own:
+        gm.keops_cache_append(dev[:, heads:heads + kv], dev[:, heads + kv:], *args, weights=w, k_scale=ks, v_scale=vs)
+        key = wide[:, heads:heads + kv]
+    else:
+        q = gm.keops_cache_append_rotary(dev[:, :heads], dev[:, heads:heads + kv], dev[:, heads + kv:], *args, put(freqs),
+                                         positions=put(positions), interleaved=interleaved, factor=factor, weights=w, k_scale=ks, v_scale=vs)
+        want = sref.rotate(wide[:, :heads], at, freqs, interleaved, factor)
+        tol = sref.rotate_bound(wide[:, :heads], want, freqs, b.dtype, factor)
+        close(q.cpu(), want, tol, "queries")
+        key = sref.rotate(wide[:, heads:heads + kv], at, freqs, interleaved, factor)
+    val = wide[:, heads + kv:]
+    torch.cuda.synchronize()
+    if isinstance(b, Batch4):
+        for name, got, w4 in zip(("keys", "values", "powers of keys", "powers of values"), (k, v, ks, vs), sref.append_4bit(b, key, val)):
+            assert torch.equal(raw(got), w4), name
+    else:
+        for name, got, pool, x, scale in (("keys", k, b.k, key, b.k_scale), ("values", v, b.v, val, b.v_scale)):
+            got = got.cpu()
+            seen = torch.zeros(pool.shape[:2], dtype=torch.bool)
+            for t, s, j, pg, row in sref.places(b):
+                if pg < 0:
+                    continue
+                seen[pg, row] = True
+                if scale is None:
+                    r = x[t].double()
+                    tol = sref.rotate_bound(wide[t:t + 1, heads:heads + kv], r[None], freqs, b.dtype, factor)[0] if name == "keys" and not own else 0.0
+                    close(got[pg, row], r, tol, name)
+                elif name == "keys":
+                    assert torch.equal(got[pg, row].float(), nearest_8bit(x[t].double() / scale.double()[:, None])), (name, t)
+                else:
+                    assert torch.equal(got[pg, row].float(), (x[t].float() / scale[:, None]).clamp(-448, 448).to(E4).float()), (name, t)
+            assert torch.equal(raw(got)[~seen], raw(pool)[~seen]), name
+    if weights is not None:
+        want = weights.clone()
+        for t, s, j, pg, row in sref.places(b):
+            if pg >= 0:
+                want[pg, :, row] = 0.0
+        assert torch.equal(w.cpu(), want)
+
+
+def nearest_8bit(x):
+    """e4m3 values nearest to x in 64 bits, halfway to the even code, cut to +-448."""
+    level = torch.arange(127, dtype=torch.uint8).view(E4).double()
+    away = (x.abs()[..., None] - level).abs()
+    code = away.argmin(-1)
+    tie = (away == away.amin(-1, keepdim=True)).sum(-1) > 1
+    code = torch.where(tie & (code % 2 == 1), code + 1, code)
+    return torch.copysign(level[code], x).float()
+
+
+@pytest.mark.parametrize("lens,new,heads,kv,dim,page,rot", APPEND)
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4), (FP, E4), (BF, E2), (FP, E2)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_rotary(lens, new, heads, kv, dim, page, rot, dtype, cache, interleaved):
+    say(f"rotating append {len(lens)} sequences, {heads}/{kv} x {dim}, page {page}, {rot} turn, {dtype} {cache}, interleaved {interleaved}")
+    b, wide = append_batch(lens, new, heads, kv, dim, page, dtype, cache)
+    if len(lens) == 4:
+        b.table[0, 0] = b.P + 5
+    freqs = gm.keops_rotary_frequencies(rot, 10000.0)
+    given = None
+    if interleaved:
+        given = torch.randint(-100000, 1 << 20, (b.T,), generator=b.gen).to(torch.int32)
+    weights = torch.rand((b.P, kv, page), generator=b.gen) + 1 if kv != 4 else None
+    check_append(b, wide, heads, freqs, given, interleaved, 1.0 if rot == dim else 1.25, weights)
+
+
+@pytest.mark.parametrize("cache", [E2, E4, BF])
+def test_append_rotary_at_position_zero_is_the_append(cache):
+    """Where nothing turns, keys come out as those of keops_cache_append, ties of every kind included."""
+    say(f"rotating append at position 0, {cache}")
+    b, _ = append_batch([2048], [2048], 0, 1, 64, 64, BF, cache)
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF).reshape(1024, 1, 64).repeat(2, 1, 1)
+    x = torch.where(x.isnan(), torch.ones_like(x), x)
+    x[1024:] = torch.randn((1024, 1, 64), generator=b.gen).to(BF).mul(4).round().div(4)         # small whole quarters: many ties
+    if cache == E4:
+        b.k_scale, b.v_scale = torch.tensor([0.75]), torch.tensor([0.75])
+    freqs = gm.keops_rotary_frequencies(64)
+    got = []
+    for own in (True, False):
+        k, v, ks, vs = pools(b)
+        args = (put(x), put(x), k, v, put(b.table), put(b.lens_t()), put(b.starts))
+        if own:
+            gm.keops_cache_append(*args, k_scale=ks, v_scale=vs)
+        else:
+            gm.keops_cache_append_rotary(put(x)[:, :0], *args, put(freqs), positions=torch.zeros(2048, dtype=torch.int32).cuda(),
+                                         k_scale=ks, v_scale=vs)
+        got.append([k.cpu(), v.cpu()] + ([raw(ks), raw(vs)] if cache == E2 else []))
+    for name, p, q in zip("kvxy", *got):
+        if cache == BF and name == "k":
+            p, q = p.float(), q.float()              # 0 (-inf) is NaN under a rotation, and -0 may be 0
+            fine = p.isfinite()
+            other = torch.cat([fine[..., 32:], fine[..., :32]], -1)
+            assert torch.equal(p[fine & other], q[fine & other])
+        elif cache == BF:
+            assert torch.equal(p, q)
+        elif cache == E4 and name == "k":
+            # an infinity beside a value: 0 times it is NaN; a quotient rounded to 32 bits first may meet a tie
+            p, q = p.float(), q.float()
+            fine = p.isfinite() & q.isfinite() & (p.abs() < 448)
+            assert torch.equal(p[fine], q[fine]) and fine.double().mean() > 0.7
+        elif cache == E2 and name in "kx":
+            # blocks next to an infinity's: 0 times it is NaN
+            if name == "k":
+                fine = (got[1][2] != 255).permute(0, 2, 1, 3).repeat_interleave(16, -1)
+                a, c = raw(p), raw(q)
+                # the sign of a zero does not count
+                zero = lambda t: t & ~(((t & 0x07) == 0).byte() * 0x08) & ~(((t & 0x70) == 0).byte() * 0x80)  # noqa: E731
+                assert torch.equal(zero(a)[fine], zero(c)[fine])
+            else:
+                assert torch.equal(p[q != 255], q[q != 255])
+        else:
+            assert torch.equal(raw(p), raw(q))
+
+
+def test_append_4bit_every_16_bit_value():
+    """Every bf16 and fp16 value, in blocks of one magnitude and in blocks of all: least powers, subnormals, infinities."""
+    for dtype in (BF, FP):
+        for order in ("rows", "columns"):
+            say(f"append in 4 bits, every {dtype}, {order}")
+            x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dtype)
+            x = x.reshape(1024, 1, 64) if order == "rows" else x.reshape(64, 1, 1024).permute(2, 1, 0).contiguous()
+            b = Batch4(37, [1024], [1024], 1, 1, 64, 64, dtype, junk=0.0)
+            wide = torch.cat([x, x], 1)
+            check_append(b, wide, 0, None, None, False, 1.0, own=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("lens,new,heads,kv,dim,page,rot", APPEND)
+def test_append_4bit(lens, new, heads, kv, dim, page, rot, dtype):
+    say(f"append in 4 bits {len(lens)} sequences, {kv} x {dim}, page {page}, {dtype}")
+    b, wide = append_batch(lens, new, heads, kv, dim, page, dtype, E2)
+    if len(lens) == 4:
+        b.table[0, 0] = -7
+    wide[0, -1, 3] = float("nan")
+    check_append(b, wide, heads, None, None, False, 1.0, torch.rand((b.P, kv, page), generator=b.gen) + 1, own=True)
+
+
+def test_append_rotary_rows_of_no_sequence_stay():
+    say("rotating append, rows behind the last sequence")
+    b, wide = append_batch([20, 9], [3, 2], 4, 2, 64, 16, BF, BF)
+    wide = torch.cat([wide, torch.randn((4, 8, 64), generator=b.gen).to(BF)])
+    k, v, _, _ = pools(b)
+    dev, out = put(wide), torch.full((9, 4, 64), 7.0, dtype=BF, device="cuda")
+    freqs = gm.keops_rotary_frequencies(64).cuda()
+    gm.keops_cache_append_rotary(dev[:, :4], dev[:, 4:6], dev[:, 6:], k, v, put(b.table), put(b.lens_t()), put(b.starts), freqs, out=out)
+    assert bool((out[5:] == 7).all()) and not bool((out[:5] == 7).any())
+    # fewer slots than new tokens: a token before the first slot has its query turned to its place before it
+    lens = torch.tensor([1, 9], dtype=torch.int32)
+    out2 = gm.keops_cache_append_rotary(dev[:5, :4], dev[:5, 4:6], dev[:5, 6:], k, v, put(b.table), lens.cuda(), put(b.starts), freqs)
+    at = torch.tensor([-2, -1, 0, 7, 8], dtype=torch.int32)
+    want = sref.rotate(wide[:5, :4], at, freqs.cpu())
+    close(out2.cpu(), want, sref.rotate_bound(wide[:5, :4], want, freqs.cpu(), BF), "queries")
+
+
+# ---- attention over 4 bits
+
+def run_attention(b, decay=0.0, max_len=None, **kw):
+    w = put(b.weights)
+    k, v, ks, vs = pools(b)
+    out, lse = gm.keops_paged_attention(put(b.q), k, v, put(b.table), put(b.lens_t()), put(b.starts), max(b.new + [0]),
+                                        max(b.lens + [0]) if max_len is None else max_len, scale=b.scale, window=b.window, weights=w,
+                                        decay=decay, k_scale=ks, v_scale=vs, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), lse.cpu(), None if w is None else w.cpu()
+
+
+def check_attention(b, decay=0.0, **kw):
+    out, lse, w = run_attention(b, decay, **kw)
+    o, z, ww, ot, zt, wt = ref.attention(b, decay)
+    close(lse, z, zt, "lse")
+    close(out, o, ot, "out")
+    if w is not None:
+        close(w, ww, wt, "weights")
+
+
+ATTEND = [
+    # lens, new, query heads, key/value heads, dim, page, type, window
+    ([1], [1], 1, 1, 64, 16, BF, 0), ([1], [1], 8, 2, 128, 16, FP, 0), ([33], [1], 4, 1, 128, 16, BF, 0),
+    ([1000], [1], 32, 8, 128, 16, BF, 0), ([1000, 1, 77, 513], [1, 1, 1, 1], 8, 2, 64, 20, FP, 0),
+    ([300, 129, 4000], [4, 2, 3], 8, 2, 128, 32, BF, 0), ([300, 0, 40], [4, 0, 3], 10, 2, 96, 24, FP, 0),
+    ([700, 64], [9, 1], 14, 2, 96, 7, BF, 0), ([500, 31], [3, 2], 7, 1, 256, 64, BF, 100), ([260], [1], 5, 1, 256, 128, FP, 33),
+    ([200, 90], [4, 3], 8, 1, 256, 16, FP, 0), ([64, 65, 63], [64, 65, 63], 4, 2, 64, 16, BF, 0),
+    ([130, 257], [130, 200], 4, 1, 128, 24, FP, 0), ([300], [150], 2, 1, 96, 128, BF, 0), ([333, 80], [40, 80], 8, 2, 256, 20, BF, 0),
+    ([222], [60], 8, 1, 256, 16, FP, 17), ([2000], [12], 8, 1, 128, 64, BF, 0), ([777, 400, 100], [300, 10, 100], 8, 4, 64, 24, FP, 128),
+    ([1500], [5], 8, 8, 128, 1, BF, 64), ([1500], [3], 4, 2, 96, 64, BF, 0), ([27000, 300], [2, 1], 5, 1, 64, 64, BF, 0),
+]
+
+
+@pytest.mark.parametrize("lens,new,heads,kv,dim,page,dtype,window", ATTEND)
+@pytest.mark.parametrize("weights", [False, True])
+def test_attention(lens, new, heads, kv, dim, page, dtype, window, weights):
+    say(f"attention in 4 bits {lens} {new} {heads}/{kv} {dim} page {page} {dtype} window {window} weights {weights}")
+    b = Batch4(sum(lens) + dim, lens, new, heads, kv, dim, page, dtype)
+    b.window = window
+    if weights:
+        b.weights = torch.rand((b.P, kv, page), generator=b.gen)
+    check_attention(b, decay=0.5 if weights and len(lens) > 1 else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("new,weights", [(1, False), (2, True), (7, False), (6, True)])
+def test_attention_past_the_caches(dtype, dim, new, weights):
+    say(f"attention in 4 bits past the caches, {dtype}, dim {dim}, {new} new, weights {weights}")
+    b = Batch4(73, [300, 77, 40], [new, 1, 0], 8, 2, dim, 24, dtype)
+    if weights:
+        b.weights = torch.zeros((b.P, 2, 24))
+    check_attention(b, max_len=1 << 21)                     # 2 x 3 x 2 x 2^21 rows of 34 bytes: 428 MB and more
+
+
+@pytest.mark.parametrize("dim,new,dtype", [(64, 3, BF), (128, 3, FP), (96, 3, BF), (256, 3, BF), (64, 40, BF), (128, 40, FP), (256, 40, BF),
+                                           (96, 40, FP), (128, 3, BF), (128, 40, BF)])
+def test_hidden_values_reach_no_row(dim, new, dtype):
+    """NaN blocks and blocks past the type's largest number, in the key and value of a later token and below the window,
+    change nothing for the rows that do not see them; the rows that see them get what the formula gives."""
+    say(f"hidden non-finite blocks, dim {dim}, {new} new, {dtype}")
+    b = Batch4(9, [140], [new], 4, 2, dim, 16, dtype)
+    b.window = 101
+    first = 140 - new
+    spots = (139, first - 100, first + 1)
+    for j in spots:
+        pg, row = b.table[0, j // 16].item(), j % 16
+        b.v_scale[pg, 0, row, 0] = 255                       # a block of NaN
+        b.v[pg, row, 1] = 0
+        b.v[pg, row, 1, 20] = 0x07                           # column 40 alone
+        b.v_scale[pg, 1, row, 1] = 254 if dtype == BF else 142
+    pg, row = b.table[0, 139 // 16].item(), 139 % 16
+    b.k_scale[pg, 0, row, 0] = 255
+    out, lse, _ = run_attention(b)
+    o, z, _, ot, zt, _ = ref.attention(b)
+    for t in range(new):
+        sees = [j for j in spots if first + t - 101 < j <= first + t]
+        for h in range(4):
+            if not sees:
+                assert bool(out[t, h].isfinite().all()) and bool(lse[t, h].isfinite())
+                close(out[t, h], o[t, h], ot[t, h], f"row {t}")
+                continue
+            if h < 2:
+                assert bool(out[t, h, :32].isnan().all()), (t, h)
+                if 139 not in sees:
+                    assert bool(out[t, h, 32:].isfinite().all())
+                    close(out[t, h, 32:], o[t, h, 32:], ot[t, h, 32:], f"row {t}")
+            else:
+                assert out[t, h, 40] == float("inf"), (t, h, out[t, h, 40])
+                rest = [c for c in range(dim) if c != 40]
+                close(out[t, h, rest], o[t, h, rest], ot[t, h, rest], f"row {t}")
+
+
+@pytest.mark.parametrize("new", [2, 30])
+def test_absent_pages(new):
+    say(f"absent pages in 4 bits, {new} new")
+    b = Batch4(11, [100, 64], [new, new], 8, 2, 64, 16)
+    b.weights = torch.rand((b.P, 2, 16), generator=b.gen)
+    b.table[0, 1] = -1
+    b.table[0, 3] = b.P
+    b.table[1, :4] = 2 ** 31 - 1
+    check_attention(b)
+    out, lse, _ = run_attention(b)
+    assert bool((out[new:] == 0).all()) and bool((lse[new:] == -float("inf")).all())
+    b.table = b.table[:, :5].contiguous()
+    check_attention(b)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_random(seed):
+    rng = random.Random(seed)
+    S, kv, dim = rng.choice([1, 2, 5, 70]), rng.choice([1, 2, 4]), rng.choice([64, 96, 128, 256])
+    top = rng.choice([1, 1, 3, 6, 40, 150])
+    lens, new = [], []
+    for _ in range(S):
+        n = rng.choice([0, 1, rng.randint(1, 50), rng.randint(1, 500 if S < 70 else 90)])
+        lens.append(n)
+        new.append(min(n, rng.randint(0, top)))
+    if not sum(new):
+        lens, new = lens + [9], new + [2]
+    heads, page = kv * rng.choice([1, 2, 4, 5]), rng.choice([1, 5, 16, 20, 64, 128])
+    dtype, window, weights = rng.choice([BF, FP]), rng.choice([0, 0, 1, 37, 200]), rng.random() < 0.5
+    say(f"random attention in 4 bits {seed}: {S} sequences, {heads}/{kv} x {dim} page {page} {dtype} window {window} weights {weights} "
+        f"lens {lens[:6]} new {new[:6]}")
+    b = Batch4(seed, lens, new, heads, kv, dim, page, dtype)
+    b.window = window
+    if weights:
+        b.weights = torch.rand((b.P, b.kv, b.page), generator=b.gen)
+    check_attention(b, decay=0.25 if weights and seed % 2 else 0.0)
+
+
+@pytest.mark.parametrize("new", [1, 33])
+def test_strides(new):
+    """Keys and values interleaved in one pool, heads outside slots."""
+    say(f"strides of a 4-bit cache, {new} new")
+    b = Batch4(13, [90, 41], [new, min(new, 41)], 8, 2, 128, 16, junk=0.0)
+    want = run_attention(b)
+    both = torch.stack([b.k, b.v], 1).cuda().view(E2)
+    heads = torch.stack([b.k, b.v], 1).transpose(2, 3).contiguous().cuda().transpose(2, 3).view(E2)
+    ks, vs = put(b.k_scale).view(E8), put(b.v_scale).view(E8)
+    for pool in (both, heads):
+        out, lse = gm.keops_paged_attention(put(b.q), pool[:, 0], pool[:, 1], put(b.table), put(b.lens_t()), put(b.starts), new, 90,
+                                            k_scale=ks, v_scale=vs)
+        assert torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+        k, v = gm.keops_cache_read(pool[:, 0], pool[:, 1], put(b.table), put(b.lens_t()), put(b.starts), b.T, k_scale=ks, v_scale=vs)
+        for got, p, s in ((k, b.k, b.k_scale), (v, b.v, b.v_scale)):
+            for t, _, _, pg, row in sref.places(b):
+                assert torch.equal(got[t].cpu().double(), sref.from_4bit(p[pg, row], s[pg, :, row]))
+
+
+def test_far_pages():
+    """Byte offsets past 2^32 in the pool, and numbers of slots and heads past 2^31."""
+    say("far pages of a 4-bit cache")
+    b = Batch4(17, [70], [2], 8, 4, 64, 16, junk=0.0)
+    P = (2 ** 31 + 2 ** 28) // (16 * 4)
+    k, v = (torch.zeros((P, 16, 4, 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((P, 4, 16, 2), 127, dtype=torch.uint8, device="cuda") for _ in range(2))
+    far = torch.arange(P - b.table.shape[1], P, dtype=torch.int32)
+    for to, frm in ((k, b.k), (v, b.v), (ks, b.k_scale), (vs, b.v_scale)):
+        to[far.long().cuda()] = put(frm)[put(b.table)[0].long()]
+    cache = (k.view(E2), v.view(E2), far[None].cuda(), put(b.lens_t()), put(b.starts))
+    scales = dict(k_scale=ks.view(E8), v_scale=vs.view(E8))
+    o, z, _, ot, zt, _ = ref.attention(b)
+    for max_q in (2, 40):                                     # both forms
+        out, lse = gm.keops_paged_attention(put(b.q), *cache, max_q, 70, **scales)
+        close(out.cpu(), o, ot, "out")
+        close(lse.cpu(), z, zt, "lse")
+    nk, nv = torch.randn((2, 4, 64)).to(BF), torch.randn((2, 4, 64)).to(BF)
+    gm.keops_cache_append(put(nk), put(nv), *cache, **scales)
+    codes, power = sref.to_4bit(nk, BF)
+    assert torch.equal(k[P - 1, 4:6].cpu(), codes) and torch.equal(ks[P - 1, :, 4:6].cpu(), power.permute(1, 0, 2))
+    rk, rv = gm.keops_cache_read(*cache, 2, **scales)
+    assert torch.equal(rk.cpu().double(), sref.from_4bit(codes, power))
+    assert torch.equal(rv.cpu().double(), sref.from_4bit(*sref.to_4bit(nv, BF)))
+
+
+def test_results_repeat_on_every_stream():
+    """The same bits on the current stream, on another, and under a graph that is replayed between eager calls."""
+    for new in (1, 40):
+        say(f"4-bit attention repeated, {new} new")
+        b = Batch4(29, [2000, 700], [new, new], 8, 2, 128, 16, junk=0.0)
+        k, v, ks, vs = pools(b)
+        args = (put(b.q), k, v, put(b.table), put(b.lens_t()), put(b.starts), new, 2000)
+        kw = dict(k_scale=ks, v_scale=vs)
+        want = gm.keops_paged_attention(*args, **kw)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        here, there = gm.keops_paged_attention(*args, **kw), gm.keops_paged_attention(*args, stream=st, **kw)     # two at once
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            cap = gm.keops_paged_attention(*args, **kw)
+        for got in (here, there):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for _ in range(3):
+            cap[0].zero_()
+            cap[1].zero_()
+            graph.replay()
+            eager = gm.keops_paged_attention(*args, **kw)
+            torch.cuda.synchronize()
+            for got in (cap, eager):
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---- eviction and reading
+
+@pytest.mark.parametrize("lens,heads,dim,page,budget,sink,recent", [
+    ([1], 1, 64, 16, 1, 0, 0), ([20, 5, 17], 2, 64, 16, 16, 1, 4), ([100, 33], 2, 96, 24, 32, 4, 28), ([257], 1, 256, 20, 100, 0, 50),
+    ([300, 10], 3, 128, 7, 11, 0, 0)])
+def test_evict(lens, heads, dim, page, budget, sink, recent):
+    say(f"evict from 4 bits {lens} {heads} x {dim} page {page} budget {budget} sink {sink} recent {recent}")
+    more = sum(-(-min(n, budget) // page) for n in lens)
+    b = Batch4(41, lens, [0] * len(lens), heads, heads, dim, page, BF, junk=0.0, spare=more + 1)
+    b.weights = torch.rand((b.P, heads, page), generator=b.gen)
+    width = max(-(-min(n, budget) // page) for n in lens)
+    new = torch.full((len(lens), width), -1, dtype=torch.int32)
+    at = 0
+    for s, n in enumerate(lens):
+        c = -(-min(n, budget) // page)
+        new[s, :c] = b.free[at:at + c]
+        at += c
+    rkept, rl, rk, rv, rw = ref.evict(b, new, budget, sink, recent)
+    rks, rvs = b.k_scale.clone(), b.v_scale.clone()
+    for s in range(len(lens)):
+        for h in range(heads):
+            for r, j in enumerate(rkept[s, h].tolist()):
+                if j >= 0:
+                    frm, to = b.table[s, j // page].item(), new[s, r // page].item()
+                    rks[to, h, r % page], rvs[to, h, r % page] = b.k_scale[frm, h, j % page], b.v_scale[frm, h, j % page]
+    k, v, ks, vs = pools(b)
+    w = put(b.weights)
+    kept, nl = gm.keops_cache_evict(k, v, w, put(b.table), put(b.lens_t()), put(new), budget, sink=sink, recent=recent, k_scale=ks,
+                                    v_scale=vs)
+    for name, got, want in (("lens", nl, rl), ("kept", kept, rkept), ("keys", k, rk), ("values", v, rv), ("weights", w, rw),
+                            ("powers of keys", ks, rks), ("powers of values", vs, rvs)):
+        assert torch.equal(raw(got), want.view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4), (FP, E4), (BF, E2), (FP, E2)])
+@pytest.mark.parametrize("lens,new,heads,kv,dim,page,rot", APPEND)
+def test_read(lens, new, heads, kv, dim, page, rot, dtype, cache):
+    say(f"read {len(lens)} sequences, {kv} x {dim}, page {page}, {dtype} {cache}")
+    b, _ = append_batch(lens, new, heads, kv, dim, page, dtype, cache)
+    if len(lens) == 4:
+        b.table[0, 0] = -1
+        b.table[2, 3] = b.P
+    k, v, ks, vs = pools(b)
+    tokens = b.T + 2                                         # two rows of no sequence
+    out = tuple(torch.full((tokens, kv, dim), 5.0, dtype=dtype, device="cuda") for _ in range(2))
+    args = (k, v, put(b.table), put(b.lens_t()), put(b.starts))
+    got = gm.keops_cache_read(*args, tokens, dtype=dtype, k_scale=ks, v_scale=vs, out=out)
+    assert got[0] is out[0] and got[1] is out[1]
+    plain = gm.keops_cache_read(*args, b.T, dtype=dtype, k_scale=ks, v_scale=vs)
+    both = torch.zeros((b.T, 2, kv, dim), dtype=dtype, device="cuda")     # keys and values in alternate rows
+    gm.keops_cache_read(*args, b.T, dtype=dtype, k_scale=ks, v_scale=vs, out=(both[:, 0], both[:, 1]))
+    for name, x, y, z, pool, scale in (("k", out[0], plain[0], both[:, 0], b.k, b.k_scale), ("v", out[1], plain[1], both[:, 1], b.v, b.v_scale)):
+        x = x.cpu()
+        assert torch.equal(x[:b.T], y.cpu()) and torch.equal(y, z) and bool((x[b.T:] == 5).all()), name
+        for t, s, j, pg, row in sref.places(b):
+            if pg < 0:
+                want = torch.zeros((kv, dim))
+            elif cache == E2:
+                want = sref.from_4bit(pool[pg, row], scale[pg, :, row])
+            else:
+                want = pool[pg, row].float() * (1.0 if scale is None else scale[:, None])
+            assert torch.equal(x[t], want.to(dtype)), (name, t)
+
+
+# ---- logits
+
+def logit_case(seed, S, new, V, width, dtype, biases, mask=True, penalties=True):
+    g = torch.Generator().manual_seed(seed)
+    rng = random.Random(seed)
+    lens, rows = [], [0]
+    for s in range(S):
+        lens.append(rng.choice([width, rng.randint(0, width)]))
+        rows.append(rows[-1] + rng.randint(0 if s else 1, new))
+    T = rows[-1] + 1                                         # and one row of no sequence
+    z = (torch.randn((T, V), generator=g) * 3).to(dtype)
+    c = dict(starts=torch.tensor(rows, dtype=torch.int32))
+    if penalties:
+        text = (V * torch.rand((S, width), generator=g) ** 4).to(torch.int32)
+        text[torch.rand((S, width), generator=g) < 0.05] = -1
+        text[torch.rand((S, width), generator=g) < 0.02] = V + 3
+        c.update(text=text, lens=torch.tensor(lens, dtype=torch.int32), prompt=torch.tensor([n // 3 for n in lens], dtype=torch.int32),
+                 rep=0.5 + torch.rand(S, generator=g), pres=torch.rand(S, generator=g) - 0.3, freq=torch.rand(S, generator=g))
+    if biases:
+        ids = torch.randint(-2, V + 2, (S, biases), generator=g).to(torch.int32)
+        if biases > 2:
+            ids[:, biases // 2] = ids[:, 0]                  # twice the same: the last stands
+        c.update(ids=ids, bias=torch.randn((S, biases), generator=g) * 4)
+    if mask:
+        m = torch.randint(-2 ** 31, 2 ** 31, (T, -(-V // 32)), generator=g).to(torch.int32)
+        m[0] = 0                                             # nothing is left
+        c.update(mask=m)
+    return z, c
+
+
+def run_logits(z, c, **kw):
+    names = dict(text="tokens", prompt="prompt_lens", rep="repetition", pres="presence", freq="frequency", ids="bias_tokens")
+    args = {names.get(k, k): put(v) for k, v in c.items() if k != "starts"}
+    return gm.keops_adjust_logits(z, put(c["starts"]), **args, **kw)
+
+
+def check_logits(got, z, c, fill):
+    want = sref.logits(z, **c)
+    none = want.isnan() & ~z.isnan()
+    got = got.cpu()
+    assert bool((got[none] == fill).all()), "rows of no sequence"
+    half = torch.finfo(z.dtype).eps / 2
+    floor = {FP: 2.0 ** -25, BF: 2.0 ** -134, F32: 2.0 ** -150}[z.dtype]
+    want = torch.where(none, got.double(), want)
+    # rounded once from 64 bits (by way of 32 where the type has 16)
+    close(got, want, want.abs() * half * (1 + 2.0 ** -7) + floor, "logits")
+    same = (want == z.double()) & ~none
+    assert torch.equal(got[same], z[same])
+
+
+@pytest.mark.parametrize("S,new,V,width,biases", [(1, 1, 1, 1, 1), (1, 1, 32, 5, 0), (1, 1, 33, 40, 3), (3, 4, 1000, 60, 7),
+                                                  (5, 2, 4099, 300, 40), (2, 3, 9001, 2500, 300), (70, 1, 257, 20, 2)])
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_logits(S, new, V, width, biases, dtype):
+    say(f"logits {S} x {new} x {V}, text {width}, {biases} biases, {dtype}")
+    z, c = logit_case(S * 100 + V, S, new, V, width, dtype, biases)
+    out = torch.full_like(z, 9.0).cuda()
+    assert run_logits(put(z), c, out=out) is out
+    check_logits(out, z, c, 9.0)
+    # in place, in rows wider than the vocabulary, from a place that 16 bytes do not divide
+    wide = torch.full((z.shape[0], V + 5), 3.0, dtype=dtype).cuda()
+    view = wide[:, 1:V + 1]
+    view.copy_(put(z))
+    view[z.shape[0] - 1] = 9.0
+    zz = z.clone()
+    zz[-1] = 9.0
+    assert run_logits(view, c, out=view) is view
+    check_logits(view, zz, c, 9.0)
+    assert bool((wide[:, 0] == 3).all()) and bool((wide[:, V + 1:] == 3).all())
+
+
+@pytest.mark.parametrize("rules", ["text", "bias", "mask", "none", "repetition", "presence", "no prompt"])
+def test_logits_rules_apart(rules):
+    say(f"logits, {rules}")
+    z, c = logit_case(5, 3, 3, 777, 90, F32, 11 if rules == "bias" else 0, rules == "mask", rules not in ("bias", "mask", "none"))
+    for name in {"repetition": ("pres", "freq", "prompt"), "presence": ("rep", "freq"), "no prompt": ("prompt",)}.get(rules, ()):
+        del c[name]
+    out = torch.full_like(z, 9.0).cuda()
+    run_logits(put(z), c, out=out)
+    check_logits(out, z, c, 9.0)
+    assert run_logits(put(z), c).shape == z.shape
+
+
+def test_logits_non_finite():
+    """Infinities and NaN pass through the rules; a masked one is -inf whatever it was."""
+    say("logits, non-finite")
+    V = 64
+    z = torch.zeros((1, V))
+    z[0, :4] = torch.tensor([float("inf"), -float("inf"), float("nan"), 1e38])
+    z[0, 32:36] = z[0, :4]
+    mask = torch.tensor([[-1, 0]], dtype=torch.int32)
+    text = torch.tensor([[0, 1, 2, 3, 3, 5, -1]], dtype=torch.int32)
+    c = dict(starts=torch.tensor([0, 1], dtype=torch.int32), text=text, lens=torch.tensor([7], dtype=torch.int32), rep=torch.tensor([0.001]),
+             freq=torch.tensor([1.0]), mask=mask)
+    got = run_logits(put(z), c).cpu()
+    assert got[0, 0] == float("inf") and got[0, 1] == -float("inf") and bool(got[0, 2].isnan()) and got[0, 3] == float("inf")
+    assert bool((got[0, 32:] == -float("inf")).all()) and got[0, 5] == -1.0 and bool((got[0, 6:32] == 0).all())
+    c["rep"] = torch.tensor([0.0])
+    got = run_logits(put(z), c).cpu()
+    assert got[0, 0] == float("inf") and got[0, 3] == float("inf") and bool(got[0, 1].isnan()) and got[0, 5] == -1.0
+
+
+def test_logits_follow_drafted_tokens():
+    """Each of a sequence's rows has seen one token more; starts past the rows are cut, lens past the text too."""
+    say("logits of drafted tokens")
+    V, text = 40, torch.tensor([[3, 7, 7, 9, 11, 3]], dtype=torch.int32)
+    z = torch.ones((4, V))
+    for starts, lens in (([0, 4], [6]), ([0, 9], [6]), ([0, 4], [9]), ([0, 4], [2]), ([-3, 4], [6])):
+        c = dict(starts=torch.tensor(starts, dtype=torch.int32), text=text, lens=torch.tensor(lens, dtype=torch.int32),
+                 freq=torch.tensor([1.0]), rep=torch.tensor([2.0]))
+        check_logits(run_logits(put(z), c), z, c, 0.0)
+
+
+def test_logits_streams_and_graph():
+    say("logits on streams and in a graph")
+    z, c = logit_case(8, 6, 4, 5000, 700, BF, 30)
+    c["starts"][-1] = z.shape[0]
+    dev = put(z)
+    want = run_logits(dev, c)
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    assert torch.equal(run_logits(dev, c, stream=st), want)
+    held = {k: put(v) for k, v in c.items()}
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        got = run_logits(dev, held)
+    for rep in range(3):
+        dev.copy_(torch.randn(z.shape, generator=torch.Generator().manual_seed(rep)).to(BF))
+        graph.replay()
+        eager = run_logits(dev, held)
+        torch.cuda.synchronize()
+        assert torch.equal(got, eager)
+
+
+# ---- together
+
+@pytest.mark.parametrize("cache", [BF, E4, E2])
+def test_a_step(cache):
+    """The rotating append, attention, the adjustment of logits and verification as a serving step runs them, eager and as
+    a graph that is replayed with other contents."""
+    say(f"a serving step over {cache}")
+    S, m, H, kv, D, V = 3, 3, 4, 2, 64, 300
+    lens = [40, 9, 130]
+    b, wide = append_batch(lens, [m] * S, H, kv, D, 16, BF, cache, seed=51)
+    k, v, ks, vs = pools(b)
+    table, n, starts = put(b.table), put(b.lens_t()), put(b.starts)
+    freqs = gm.keops_rotary_frequencies(D).cuda()
+    g = torch.Generator().manual_seed(4)
+    head = torch.randn((H * D, V), generator=g).cuda() / 8
+    text = torch.randint(0, V, (S, 130), generator=g).to(torch.int32).cuda()
+    rules = dict(tokens=text, lens=n, repetition=torch.full((S,), 1.2).cuda(), presence=torch.full((S,), 0.3).cuda(),
+                 mask=torch.randint(-2 ** 31, 2 ** 31, (S * m, -(-V // 32)), generator=g).to(torch.int32).cuda())
+    drafts = torch.randint(0, V, (S, m - 1), generator=g).to(torch.int32).cuda()
+    counts, ua, us = torch.full((S,), m - 1, dtype=torch.int32).cuda(), torch.rand((S, m - 1), generator=g).cuda(), torch.rand(S, generator=g).cuda()
+    dev = put(wide)
+
+    def step():
+        q = gm.keops_cache_append_rotary(dev[:, :H], dev[:, H:H + kv], dev[:, H + kv:], k, v, table, n, starts, freqs, k_scale=ks, v_scale=vs)
+        out, lse = gm.keops_paged_attention(q, k, v, table, n, starts, m, 130, k_scale=ks, v_scale=vs)
+        z = gm.keops_adjust_logits(out.float().flatten(1) @ head, starts, **rules)
+        p = torch.softmax(z, -1)
+        return (q, out, lse, z, *gm.keops_verify_draft(p.view(S, m, V), None, drafts, counts, ua, us))
+    eager = step()
+    torch.cuda.synchronize()
+    # the parts against their plain forms, each from the part before it
+    at = torch.cat([torch.arange(x - m, x) for x in lens])
+    wq = sref.rotate(wide[:, :H], at, freqs.cpu())
+    close(eager[0].cpu(), wq, sref.rotate_bound(wide[:, :H], wq, freqs.cpu(), BF), "queries")
+    b.q, b.k, b.v = eager[0].cpu(), raw(k) if cache == E2 else k.cpu(), raw(v) if cache == E2 else v.cpu()
+    if cache == E2:
+        b.k_scale, b.v_scale = raw(ks), raw(vs)
+    o, lse, _, ot, zt, _ = ref.attention(b)
+    close(eager[1].cpu(), o, ot, "out")
+    close(eager[2].cpu(), lse, zt, "lse")
+    z = (eager[1].float().flatten(1) @ head).cpu()
+    wz = sref.logits(z, starts.cpu(), text.cpu(), lens, None, rules["repetition"].cpu(), rules["presence"].cpu(), None, None, None,
+                     rules["mask"].cpu())
+    close(eager[3].cpu(), wz, wz.abs() * ref.U32 * 1.01, "logits")
+    p = torch.softmax(eager[3], -1).view(S, m, V)
+    tokens, accepted = ref.verify(p.cpu(), None, drafts.cpu(), counts.cpu(), ua.cpu(), us.cpu())
+    assert torch.equal(eager[4].cpu(), tokens) and torch.equal(eager[5].cpu(), accepted)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for rep in range(3):
+        dev.copy_(torch.randn(wide.shape, generator=torch.Generator().manual_seed(rep)).to(BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        for x, y in zip(kept, step()):
+            assert torch.equal(x, y)
