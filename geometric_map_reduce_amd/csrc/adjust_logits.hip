@@ -2,17 +2,22 @@
 //
 //   z = l;  seen: z > 0 ? z / r : z r;  z -= f c + (c > 0 ? p : 0);  z += bias;  masked: z = -inf
 //
-// A row sees its sequence's text up to its own token.  A work-group has a piece of a row's vocabulary: it counts the
-// text's tokens of that piece in LDS (whole numbers, so the order of the additions does not matter), notes which bias of
-// the list each entry takes (the largest place, so the last of equal ones), then goes over the logits once.  Few
-// entries of a piece are touched; those are computed in 64 bits one after the other, the others pass by.
+// A row sees its sequence's text up to its own token.  A work-group has a piece of the vocabulary and up to
+// kLogitRows rows of a sequence in a row: it counts the text's tokens of its piece in LDS (whole numbers, so the order of the
+// additions does not matter), marks the entries that the list of biases names and the tokens by which the rows' texts
+// grow, and goes over its rows.  Few entries of a piece are touched; those are computed in 64 bits one after the
+// other, the others pass by.
 #include "step.h"
 
 namespace kmi {
 namespace {
 
-constexpr uint32_t kInPrompt = 0x80000000u;
+// An entry's word: seen in the prompt, named by the list of biases, a token that a later row of the work-group has
+// seen, and how often it was seen past the prompt up to the first row (a text has less than 2^29 tokens).
+constexpr uint32_t kInPrompt = 0x80000000u, kBiased = 0x40000000u, kLater = 0x20000000u, kMade = 0x1fffffffu;
 constexpr int kChunk = 8;                    // entries of a thread at a time
+constexpr int kStrip = 512;                  // a wave's entries at a time
+constexpr int kListed = 512;                 // biases of a piece that are held in LDS
 
 template <class T> struct Logit;
 template <> struct Logit<Bf16> {
@@ -31,116 +36,211 @@ template <> struct Logit<float> {
   static __device__ __forceinline__ E put(float x) { return x; }
 };
 
-template <class T>
-__global__ __launch_bounds__(kLogitThreads) void adjust_kernel(LogitArgs a) {
+// CHUNKS: of a row's piece for each thread.
+template <class T, int CHUNKS>
+__global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
   typedef typename Logit<T>::E E;
-  constexpr int kWords = kChunk * sizeof(E) / 16;
-  extern __shared__ uint32_t table[];        // [piece] counts with text, then [piece] places with biases
+  constexpr int kWords = kChunk * sizeof(E) / 16, kPiece = CHUNKS * kChunk * kLogitThreads;
+  __shared__ __align__(16) uint32_t table[kPiece];
+  __shared__ __align__(16) int listed_token[kListed];
+  __shared__ int listed_at[kListed], listed;
+  __shared__ float listed_bias[kListed];
+  __shared__ int later[kLogitRows];          // the token of row r's text that the row before has not seen
   const int tid = threadIdx.x;
-  const int pieces = (a.vocab + a.piece - 1) / a.piece;
+  const int pieces = (a.vocab + kPiece - 1) / kPiece;
   const int64_t t = blockIdx.x / pieces;
-  const int i0 = (int)(blockIdx.x - t * pieces) * a.piece, i1 = i0 + a.piece < a.vocab ? i0 + a.piece : a.vocab;
+  const int piece = (int)(blockIdx.x - t * pieces), V = a.vocab;
   const int s = owner_of(a.starts, a.seqs, t);
   int64_t begin = a.starts[s], end = a.starts[s + 1];
   begin = begin < 0 ? 0 : begin;
   end = end > a.rows ? a.rows : end;
-  if (t < begin || t >= end) return;
-  uint32_t *counts = table, *which = table + (a.text ? a.piece : 0);
-  const int entries = a.piece * ((a.text ? 1 : 0) + (a.biases ? 1 : 0));
-  for (int i = tid * 4; i < entries; i += kLogitThreads * 4) *(u32x4 *)(table + i) = (u32x4){0, 0, 0, 0};
-  __syncthreads();
-  double rep = 1.0, pres = 0.0, freq = 0.0;
-  if (a.text) {
-    if (a.repetition) rep = (double)a.repetition[s];
-    if (a.presence) pres = (double)a.presence[s];
-    if (a.frequency) freq = (double)a.frequency[s];
-    int64_t n = a.lens[s] - (end - t) + 1;   // tokens up to the row's own
-    n = n < a.text_width ? n : a.text_width;
-    const int prompt = a.prompt_lens ? a.prompt_lens[s] : 0;
-    const int32_t *text = a.text + s * a.text_stride;
-    for (int64_t i = tid; i < n; i += kLogitThreads) {
-      const int x = text[i];
-      if (x < i0 || x >= i1) continue;
-      if (i < prompt) atomicOr(&counts[x - i0], kInPrompt);
-      else atomicAdd(&counts[x - i0], 1u);
-    }
-  }
-  for (int i = tid; i < a.biases; i += kLogitThreads) {
-    const int x = a.bias_tokens[(int64_t)s * a.biases + i];
-    if (x >= i0 && x < i1) atomicMax(&which[x - i0], (uint32_t)i + 1u);
-  }
-  __syncthreads();
-  const double inverse = 1.0 / rep;
-  const E *in = (const E *)a.logits + t * a.stride;
-  E *out = (E *)a.out + t * a.out_stride;
-  const uint32_t *mask = a.mask ? a.mask + t * a.mask_stride : nullptr;
-  for (int x0 = i0 + tid * kChunk; x0 < i1; x0 += kLogitThreads * kChunk) {
-    const bool full = a.whole && x0 + kChunk <= i1;
-    union { u32x4 w[kWords]; E e[kChunk]; } u;
-    if (full) {
+  if (t < begin || t >= end || (t - begin) % kLogitRows) return;      // of no sequence, or the rows of another work-group
+  const int rows = end - t < kLogitRows ? (int)(end - t) : kLogitRows;
+
+  // Strips of 512 entries are dealt to the pieces in turn: a text's common tokens lie close together.
+  const auto entry = [&](int c) {            // the first of the thread's chunk c, whose word is at c * 4096 + 8 tid
+    const int strip = (c * kLogitThreads + tid) * kChunk / kStrip;
+    return (int64_t)(strip * pieces + piece) * kStrip + tid * kChunk % kStrip;
+  };
+  const auto place = [&](int x) {            // where x's word is; -1: another piece's
+    const int strip = x / kStrip, mine = (int)fast_div(a.pieces_div, (uint32_t)strip);
+    return x >= 0 && x < V && strip - mine * pieces == piece ? mine * kStrip + x % kStrip : -1;
+  };
+  // a row's piece and its mask, on their way while the table is made
+  union Held { u32x4 w[kWords]; E e[kChunk]; };
+  Held u[CHUNKS];
+  uint32_t bits[CHUNKS];
+  const auto fetch = [&](int r) {
+    const E *in = (const E *)a.logits + (t + r) * a.stride;
+    const uint32_t *mask = a.mask ? a.mask + (t + r) * a.mask_stride : nullptr;
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) u.w[k] = ((const u32x4 *)(in + x0))[k];
-    } else {
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int64_t x0 = entry(c);
+      if (a.whole && x0 + kChunk <= V) {
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) u.e[k] = x0 + k < i1 ? in[x0 + k] : E(0);
-    }
-    uint32_t bits = 0xffu;
-    if (mask) bits = (mask[x0 >> 5] >> (x0 & 31)) & 0xffu;
-    uint32_t touched = 0;
+        for (int k = 0; k < kWords; ++k) u[c].w[k] = ((const u32x4 *)(in + x0))[k];
+      } else {
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) {
-      uint32_t any = 0;
-      if (a.text) any |= counts[x0 - i0 + k];
-      if (a.biases) any |= which[x0 - i0 + k];
-      touched |= any ? 1u << k : 0u;
-    }
-    touched &= bits;
-    while (touched) {
-      const int k = __ffs(touched) - 1;
-      touched &= touched - 1;
-      float l = 0.0f;
-#pragma unroll
-      for (int m = 0; m < kChunk; ++m) l = m == k ? Logit<T>::get(u.e[m]) : l;
-      double z = (double)l;
-      const uint32_t c = a.text ? counts[x0 - i0 + k] : 0u;
-      if (c) {
-        if (z > 0.0) {
-          double q = z * inverse;
-          if (__builtin_fabs(q) < INFINITY) q = __builtin_fma(__builtin_fma(-q, rep, z), inverse, q);
-          z = q;
-        } else {
-          z *= rep;
-        }
-        const uint32_t made = c & ~kInPrompt;
-        if (made) z -= freq * (double)made + pres;
+        for (int k = 0; k < kChunk; ++k) u[c].e[k] = x0 + k < V ? in[x0 + k] : E(0);
       }
-      const uint32_t w = a.biases ? which[x0 - i0 + k] : 0u;
-      if (w) z += (double)a.bias[(int64_t)s * a.biases + (w - 1)];
-      const E e = Logit<T>::put((float)z);
-#pragma unroll
-      for (int m = 0; m < kChunk; ++m) u.e[m] = m == k ? e : u.e[m];
+      bits[c] = mask && x0 < V ? mask[x0 >> 5] >> (x0 & 31) : 0xffu;
     }
-    const E none = Logit<T>::put(-INFINITY);
+  };
+  fetch(0);
+  const bool rules = a.text || a.biases;
+  double rep = 1.0, pres = 0.0, freq = 0.0;
+  int64_t n = 0;                             // tokens of the text up to the row's own
+  int prompt = 0;
+  const int32_t *text = a.text + s * a.text_stride;
+  const auto count = [&](int x, int64_t i) {
+    const int at = place(x);
+    if (at < 0) return;
+    if (i < prompt) atomicOr(&table[at], kInPrompt);
+    else atomicAdd(&table[at], 1u);
+  };
+  if (rules) {
+    for (int i = tid * 4; i < kPiece; i += kLogitThreads * 4) *(u32x4 *)(table + i) = (u32x4){0, 0, 0, 0};
+    if (tid == 0) listed = 0;
+    for (int i = tid; i < kListed; i += kLogitThreads) listed_token[i] = -1;
+    __syncthreads();
+    if (a.text) {
+      if (a.repetition) rep = (double)a.repetition[s];
+      if (a.presence) pres = (double)a.presence[s];
+      if (a.frequency) freq = (double)a.frequency[s];
+      if (a.prompt_lens) prompt = a.prompt_lens[s];
+      n = a.lens[s] - (end - t) + 1;
+      const int64_t m = n < a.text_width ? n : a.text_width;
+      if (tid < kLogitRows) {
+        const int64_t i = n + tid - 1;
+        const int x = tid > 0 && i >= 0 && i < a.text_width ? text[i] : -1;
+        const int at = tid < rows ? place(x) : -1;
+        later[tid] = at < 0 ? -1 : x;
+        if (at >= 0) atomicOr(&table[at], kLater);
+      }
+      if (((uintptr_t)text & 15) == 0) {
+        for (int64_t i = 4 * tid; i < m; i += 4 * kLogitThreads) {
+          if (i + 4 <= m) {
+            const u32x4 four = *(const u32x4 *)(text + i);
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) u.e[k] = (bits >> k) & 1u ? u.e[k] : none;
-    if (full) {
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) ((u32x4 *)(out + x0))[k] = u.w[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k)
-        if (x0 + k < i1) out[x0 + k] = u.e[k];
+            for (int k = 0; k < 4; ++k) count((int)four[k], i + k);
+          } else {
+            for (int k = 0; i + k < m; ++k) count(text[i + k], i + k);
+          }
+        }
+      } else {
+        for (int64_t i = tid; i < m; i += kLogitThreads) count(text[i], i);
+      }
     }
+    for (int i = tid; i < a.biases; i += kLogitThreads) {
+      const int x = a.bias_tokens[(int64_t)s * a.biases + i], word = place(x);
+      if (word < 0) continue;
+      atomicOr(&table[word], kBiased);
+      const int at = atomicAdd(&listed, 1);
+      if (at < kListed) {
+        listed_token[at] = x;
+        listed_at[at] = i;
+        listed_bias[at] = a.bias[(int64_t)s * a.biases + i];
+      }
+    }
+    __syncthreads();
   }
+  const double inverse = 1.0 / rep;
+  // of equal biases the last in the list, whichever order they came to LDS in
+  const int biases = listed;
+  const auto bias_of = [&](int x) {
+    int last = -1;
+    float v = 0.0f;
+    if (biases <= kListed) {
+      for (int i = 0; i < biases; i += 4) {
+        const u32x4 four = *(const u32x4 *)(listed_token + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((int)four[k] == x && listed_at[i + k] > last) {
+            last = listed_at[i + k];
+            v = listed_bias[i + k];
+          }
+      }
+    } else {
+      for (int i = a.biases - 1; i >= 0 && last < 0; --i)
+        if (a.bias_tokens[(int64_t)s * a.biases + i] == x) last = i;
+      v = a.bias[(int64_t)s * a.biases + last];
+    }
+    return (double)v;
+  };
+  const E none = Logit<T>::put(-INFINITY);
+  for (int r = 0; r < rows; ++r) {
+    E *out = (E *)a.out + (t + r) * a.out_stride;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int64_t x0 = entry(c);
+      const int word = (c * kLogitThreads + tid) * kChunk;
+      if (x0 >= V) break;
+      uint32_t touched = 0;
+      if (rules) {
+        const u32x4 lo = *(const u32x4 *)(table + word), hi = *(const u32x4 *)(table + word + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) touched |= (lo[k] ? 1u << k : 0u) | (hi[k] ? 16u << k : 0u);
+        touched &= bits[c];
+      }
+      while (touched) {
+        const int k = __ffs(touched) - 1;
+        touched &= touched - 1;
+        float l = 0.0f;
+#pragma unroll
+        for (int m = 0; m < kChunk; ++m) l = m == k ? Logit<T>::get(u[c].e[m]) : l;
+        double z = (double)l;
+        const uint32_t w = table[word + k];
+        uint32_t made = w & kMade;
+        bool seen = (w & (kInPrompt | kMade)) != 0;
+        if (w & kLater) {
+          for (int m = 1; m <= r; ++m)
+            if (later[m] == (int)x0 + k) {
+              seen = true;
+              made += n + m - 1 >= prompt ? 1u : 0u;
+            }
+        }
+        if (seen) {
+          if (z > 0.0) {
+            double q = z * inverse;          // an exact quotient comes out exact
+            if (__builtin_fabs(q) < INFINITY) q = __builtin_fma(__builtin_fma(-q, rep, z), inverse, q);
+            z = q;
+          } else {
+            z *= rep;
+          }
+          if (made) z -= freq * (double)made + pres;
+        }
+        if (w & kBiased) z += bias_of((int)x0 + k);
+        const E e = Logit<T>::put((float)z);
+#pragma unroll
+        for (int m = 0; m < kChunk; ++m) u[c].e[m] = m == k ? e : u[c].e[m];
+      }
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) u[c].e[k] = (bits[c] >> k) & 1u ? u[c].e[k] : none;
+      if (a.whole && x0 + kChunk <= V) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) ((u32x4 *)(out + x0))[k] = u[c].w[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k)
+          if (x0 + k < V) out[x0 + k] = u[c].e[k];
+      }
+    }
+    if (r + 1 < rows) fetch(r + 1);
+  }
+}
+
+template <class T>
+void launch_type(const LogitArgs &a, dim3 grid, hipStream_t st) {
+  if (a.piece == kLogitPiece) adjust_kernel<T, 2><<<grid, kLogitThreads, 0, st>>>(a);
+  else adjust_kernel<T, 1><<<grid, kLogitThreads, 0, st>>>(a);
 }
 
 }  // namespace
 
 void launch_adjust_logits(const LogitArgs &a, int type, dim3 grid, hipStream_t st) {
-  const size_t lds = (size_t)a.piece * 4 * ((a.text ? 1 : 0) + (a.biases ? 1 : 0));
-  if (type == CT_BF16) adjust_kernel<Bf16><<<grid, kLogitThreads, lds, st>>>(a);
-  else if (type == CT_F16) adjust_kernel<F16><<<grid, kLogitThreads, lds, st>>>(a);
-  else adjust_kernel<float><<<grid, kLogitThreads, lds, st>>>(a);
+  if (type == CT_BF16) launch_type<Bf16>(a, grid, st);
+  else if (type == CT_F16) launch_type<F16>(a, grid, st);
+  else launch_type<float>(a, grid, st);
 }
 
 }  // namespace kmi

@@ -60,9 +60,12 @@ struct LogitArgs {
   const uint32_t *mask;
   int64_t mask_stride;
   int32_t seqs, text_width, biases;
+  FastDiv pieces_div;
   bool whole;                        // rows of logits and out start on 16 bytes
 };
-constexpr int kLogitThreads = 256;
+constexpr int kLogitThreads = 512;
+constexpr int kLogitRows = 8;        // rows of a sequence that a work-group takes at most
+constexpr int kLogitPiece = 8192;    // vocabulary entries of a work-group, or half of them
 
 void launch_rotary(const RotaryArgs &a, int type, int piece, dim3 grid, hipStream_t st);
 void launch_append_rotary(const AppendRotaryArgs &a, int type, int bits, dim3 grid, hipStream_t st);

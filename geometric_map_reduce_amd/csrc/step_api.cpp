@@ -202,7 +202,7 @@ int logits_entry(const void *logits, int64_t stride, int type, int64_t rows, int
     for (const auto &in : inputs)
       if (in.p && overlaps(out, ob, in.p, in.bytes)) return KEOPS_ERR_INVALID_ARG;
   }
-  if (rows > 0x7fffffff || vocab > 1 << 30) return KEOPS_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffff || vocab > 1 << 30 || r->text_width > (1 << 29) - kLogitRows) return KEOPS_ERR_UNSUPPORTED;
   if (rows == 0 || r->seqs == 0) return KEOPS_OK;
   LogitArgs a{};
   a.logits = logits;
@@ -228,7 +228,8 @@ int logits_entry(const void *logits, int64_t stride, int type, int64_t rows, int
   a.biases = r->biases;
   const int to = 16 / bytes;
   a.whole = aligned(logits, 16) && aligned(out, 16) && a.stride % to == 0 && a.out_stride % to == 0;
-  a.piece = 4096;
+  a.piece = (double)rows * (double)ceil_div(vocab, kLogitPiece) >= 256.0 ? kLogitPiece : kLogitPiece / 2;
+  a.pieces_div = make_fastdiv((uint32_t)ceil_div(vocab, a.piece));
   const double blocks = (double)rows * (double)ceil_div(vocab, a.piece);
   if (blocks > (double)kMaxGrid || !launchable(blocks, kLogitThreads)) return KEOPS_ERR_UNSUPPORTED;
   (void)hipGetLastError();
