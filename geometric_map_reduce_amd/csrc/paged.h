@@ -149,6 +149,8 @@ struct AttendArgs {
   // parts of a row's sums: many rows [nsplit][tokens][heads * group], few rows [work-groups][2][rows]
   int32_t nsplit;
   uint32_t *line;               // few rows: where each sequence's tiles begin, and a work-group's share [seqs + 1]
+  bool by_head;                 // few rows, not `whole`: a work-group's run has one head's tiles (4-bit caches), of
+  int32_t head_group;           // so many heads (4-bit caches; divides the heads and the waves)
   int32_t whole;                // few rows: a work-group has all slots of one (sequence, head); 2: of eight waves
   int32_t join_slices;          // few rows: work-groups that share the columns of a row in the join
   bool far;                     // few rows, not `whole`: the bounds allow for more keys and values than a cache holds

@@ -43,8 +43,8 @@ constexpr double kScoresAlways = 512e6, kScoresMost = 4294967296.0;
 
 // Launch plan of one attention call.
 struct AttendPlan {
-  bool few, scores, far;
-  int whole, row_tiles, score_rows, join_rows, join_slices;
+  bool few, scores, far, by_head;
+  int whole, head_group, row_tiles, score_rows, join_rows, join_slices;
   int64_t nsplit, nrow, grid, sums_grid, score_stride;
   int64_t line_bytes, ml_bytes, o_bytes, score_bytes, sums_bytes;
   int64_t total() const { return line_bytes + ml_bytes + o_bytes + score_bytes + sums_bytes; }
@@ -78,17 +78,25 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     p->whole = rows == 0 || from_tile <= kFewLeast || (from_tile <= kFewWhole && S * H * 2 >= room);
     if (!p->whole && from_tile <= kFewWhole8 && S * H <= cus && p->row_tiles == 1 && c.dim <= 128) p->whole = 2;
     if (p->whole && !launchable((double)S * (double)H, p->whole == 2 ? 512 : 256)) return KEOPS_ERR_UNSUPPORTED;
-    p->grid = p->whole ? S * H : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
+    p->by_head = !p->whole && c.type == KEOPS_TYPE_E2M1;
+    // neighbouring heads whose rows make up a line of 128 bytes go together
+    p->head_group = 1;
+    if (p->by_head && !p->scores)
+      while (p->head_group * c.dim / 2 < 128 && H % (2 * p->head_group) == 0) p->head_group *= 2;
+    const int64_t groups = H / p->head_group;
+    p->grid = p->whole ? S * H
+              : p->by_head ? std::max<int64_t>(1, std::min(room / groups, ceil_div(S * from_tile, kFewLeast))) * groups
+                           : std::min(room, ceil_div(S * H * from_tile, kFewLeast));
     p->far = !p->whole && 2.0 * (double)S * (double)H * (double)from_tile * (double)row_bytes(c) > kFarBytes;
     if (!p->whole) {
       // a joining work-group's 1024 / dim groups of threads: one to a row where the parts are few
-      const int64_t groups = 1024 / c.dim, parts = ceil_div(p->grid, S * H) + 1;
+      const int64_t groups = 1024 / c.dim, parts = ceil_div(p->grid * p->head_group, S * H) + 1;
       p->join_rows = (int)std::max<int64_t>(1, std::min(rows, parts <= 4 ? groups : groups / parts));
       // many parts: 32 columns to a work-group, so that 32 groups of threads share a row's parts
       p->join_slices = parts > kJoinParts ? c.dim / 32 : 1;
       p->line_bytes = align256((S + 1) * 4);
-      p->ml_bytes = align256(p->grid * 2 * 16 * p->row_tiles * 8);
-      p->o_bytes = align256(p->grid * 2 * 16 * p->row_tiles * c.dim * 4);
+      p->ml_bytes = align256(p->grid * p->head_group * 2 * 16 * p->row_tiles * 8);
+      p->o_bytes = align256(p->grid * p->head_group * 2 * 16 * p->row_tiles * c.dim * 4);
     }
   } else {
     const int64_t nrt = ceil_div(rows, kManyRowsTile);
@@ -256,6 +264,8 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.nsplit = (int32_t)p.nsplit;
   a.whole = p.whole;
   a.far = p.far;
+  a.by_head = p.by_head;
+  a.head_group = std::max(1, p.head_group);
   a.join_slices = std::max(1, p.join_slices);
   a.line = (uint32_t *)ws;
   ws += p.line_bytes;

@@ -73,6 +73,20 @@ struct FewRows {
   static constexpr int kKPowers = D == 96 || D == 256 ? 2 : 1;
   uint32_t kp[2][kKPowers], vp[8][VPieces<D>::n];
 
+  // e2m1: a tile's keys, values and powers pass through LDS of the wave's own.  Neighbouring lanes load neighbouring
+  // blocks of a slot (not a slot a lane, the operands' own order: four times the addresses to look up), the keys are read back as the A operand and the values as eight slots of a lane's columns.
+  static constexpr int kBlocks = D / kPowerBlock, kLoads = E2M1 ? (32 * kBlocks + kWave - 1) / kWave : 1;
+  static constexpr int kGroup = 36;                     // words of an 8-column group of V, a slot each and a pad: no two lanes' banks meet
+  static constexpr int kStageV = 16 * D, kStageP = kStageV + D / 8 * kGroup * 4;
+  static constexpr int kStageBytes = E2M1 ? kStageP + 64 * kBlocks : 0;
+  u32x4 ks[kLoads], vs[kLoads];
+  u32x2 pw;
+  // where block b of a slot's key lies, in 16 bytes: the 16 slots that are read together meet all banks
+  static __device__ __forceinline__ int key_unit(int slot, int b) {
+    const int x = D == 64 ? (slot >> 3) & 1 : D == 128 ? (slot >> 2) & 3 : D == 256 ? (slot >> 1) & 7 : 0;
+    return slot * kBlocks + (b ^ x);
+  }
+
   // 8-bit rows of a multiple of 64 bytes: a lane's 16 bytes are the operands of two matrix steps,
   // columns 64 s + 16 (l / 16) + 8 u .. of steps 2 s + u.  Any order of the columns will do that Q shares.
   static constexpr bool kWide = E4M3 && D % 64 == 0;
@@ -83,36 +97,13 @@ struct FewRows {
   }
 
   // K rows of the tile: lane l has slot l % 16 of each 16, columns step_column(s, l / 16) ..+8 of step s.
-  // powers, number: e2m1 only, the pool's powers and the slots' numbers in them.
   template <bool FAR>
-  __device__ __forceinline__ void load_k(const char *base, const int64_t *off, const uint8_t *powers, const uint32_t *number, int at) {
+  __device__ __forceinline__ void load_k(const char *base, const int64_t *off, int at) {
     const int lane = threadIdx.x & (kWave - 1), row = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       int64_t o = off[at + 16 * t + row];
       o = o < 0 ? 0 : o;
-      if (E2M1) {
-        const char *p = base + o + step_column(0, q) / 2;
-        if (D == 64) {
-          const u32x2 w = load_once<u32x2, FAR>(p);
-          kr[t][0] = w.x;
-          kr[t][1 % kKRegs] = w.y;
-        } else if (D == 96) {
-#pragma unroll
-          for (int u = 0; u < 3; ++u) kr[t][u % kKRegs] = load_once<uint32_t, FAR>(p + 4 * u);
-        } else {
-#pragma unroll
-          for (int s = 0; s < kSteps; s += 4) {
-            const u32x4 w = load_once<u32x4, FAR>(p + s * 16);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) kr[t][(s + u) % kKRegs] = w[u];
-          }
-        }
-        const uint8_t *e = powers + (uint64_t)number[at + 16 * t + row] * (D / kPowerBlock);
-        kp[t][0] = load_once<uint8_t, FAR>(e + step_column(0, q) / kPowerBlock);
-        if (kKPowers > 1) kp[t][kKPowers - 1] = load_once<uint8_t, FAR>(e + step_column(kSteps - 1, q) / kPowerBlock);
-        continue;
-      }
       const char *p = base + o + step_column(0, q) * kBytes;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
@@ -136,26 +127,12 @@ struct FewRows {
 
   // V: lane l has slots 4 (l / 16) + i of the first 16 (i < 4) and of the second (i >= 4).
   template <bool FAR>
-  __device__ __forceinline__ void load_v(const char *base, const int64_t *off, const uint8_t *powers, const uint32_t *number, int at) {
+  __device__ __forceinline__ void load_v(const char *base, const int64_t *off, int at) {
     const int lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int u = at + (i >> 2) * 16 + q * 4 + (i & 3);
-      int64_t o = off[u];
+      int64_t o = off[at + (i >> 2) * 16 + q * 4 + (i & 3)];
       o = o < 0 ? 0 : o;
-      if (E2M1) {
-        const uint8_t *e = powers + (uint64_t)number[u] * (D / kPowerBlock);
-        int col = 0;
-#pragma unroll
-        for (int n = 0; n < VPieces<D>::n; ++n) {
-          const int w = VPieces<D>::w[n], at_col = col + c * w;
-          const char *p = base + o + at_col / 2;
-          vr[i][n % kVRegs] = w == 8 ? load_once<uint32_t, FAR>(p) : w == 4 ? load_once<uint16_t, FAR>(p) : load_once<uint8_t, FAR>(p);
-          vp[i][n] = load_once<uint8_t, FAR>(e + at_col / kPowerBlock);
-          col += 16 * w;
-        }
-        continue;
-      }
       const char *p = base + o;
       int reg = 0, col = 0;
 #pragma unroll
@@ -182,6 +159,114 @@ struct FewRows {
         col += 16 * w;
       }
     }
+  }
+
+  // A wave's share of the blocks of a tile: 2^lg waves, each with a head of its own, load the slots' blocks of all their
+  // heads, which lie side by side, so that a request to L2 is for a whole line (L1 has so many of them under way).
+  // place: this wave's among them.
+  struct Share {
+    int lg, place;
+    __device__ __forceinline__ void item(int n, int *slot, int *head, int *b) const {
+      const int i = n * kWave + (int)(threadIdx.x & (kWave - 1)), at = i / kBlocks;
+      *b = i - at * kBlocks;
+      *head = at & ((1 << lg) - 1);
+      *slot = (at >> lg) + place * (32 >> lg);
+    }
+    static __device__ __forceinline__ bool has(int n) {        // D = 96: the last half round is empty
+      return 32 * kBlocks % kWave == 0 || n * kWave + (int)(threadIdx.x & (kWave - 1)) < 32 * kBlocks;
+    }
+  };
+  // A tile's K, V and powers on their way.  kbase, vbase: of the first head; number: the slots' numbers among its powers.
+  template <bool FAR>
+  __device__ __forceinline__ void load_staged(const Share &sh, int64_t head_stride, const char *kbase, const char *vbase, const int64_t *off,
+                                              const uint8_t *kpow, const uint8_t *vpow, const uint32_t *number, int at) {
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      int slot, head, b;
+      sh.item(n, &slot, &head, &b);
+      if (!sh.has(n)) continue;
+      int64_t o = off[at + slot];
+      o = (o < 0 ? 0 : o) + head * head_stride + b * 16;
+      ks[n] = load_once<u32x4, FAR>(kbase + o);
+      vs[n] = load_once<u32x4, FAR>(vbase + o);
+    }
+    // a slot's powers, of K by the lower lanes and of V by the upper ones
+    const uint8_t *e = (lane < 32 ? kpow : vpow) + (uint64_t)number[at + (lane & 31)] * kBlocks;
+    if (D == 64) pw.x = load_once<uint16_t, FAR>(e);
+    else if (D == 96) pw.x = load_once<uint8_t, FAR>(e) | (uint32_t)load_once<uint8_t, FAR>(e + 1) << 8 | (uint32_t)load_once<uint8_t, FAR>(e + 2) << 16;
+    else if (D == 128) pw.x = load_once<uint32_t, FAR>(e);
+    else pw = load_once<u32x2, FAR>(e);
+  }
+  // What has arrived to LDS: blocks to the places of their heads, from `all` on, and powers to the wave's own.
+  __device__ __forceinline__ void put_staged(const Share &sh, char *all, char *stage) {
+    const int lane = threadIdx.x & (kWave - 1);
+    uint8_t *const sp = (uint8_t *)(stage + kStageP);   // K [slot][block], then V [block][slot]
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      int slot, head, b;
+      sh.item(n, &slot, &head, &b);
+      if (!sh.has(n)) continue;
+      char *const to = all + head * kStageBytes;
+      ((u32x4 *)to)[key_unit(slot, b)] = ks[n];
+      uint32_t *const sv = (uint32_t *)(to + kStageV);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sv[(4 * b + u) * kGroup + slot] = vs[n][u];
+    }
+    const int slot = lane & 31;
+    const int v = lane >> 5;                            // K: bytes 0 .. of the slot; V: a block's bytes 32 apart
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+      sp[v ? 32 * (kBlocks + b) + slot : slot * kBlocks + b] = (uint8_t)((b < 4 ? pw.x : pw.y) >> (8 * (b & 3)));
+  }
+  // K and its powers from there.
+  __device__ __forceinline__ void take_keys(const char *stage) {
+    const int lane = threadIdx.x & (kWave - 1), row = lane & 15, q = lane >> 4;
+    const uint8_t *const sp = (const uint8_t *)(stage + kStageP);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int slot = 16 * t + row;
+      if (D == 64) {
+        const u32x2 w = *(const u32x2 *)(stage + key_unit(slot, q >> 1) * 16 + (q & 1) * 8);
+        kr[t][0] = w.x;
+        kr[t][1 % kKRegs] = w.y;
+      } else if (D == 96) {
+#pragma unroll
+        for (int u = 0; u < 3; ++u) kr[t][u % kKRegs] = *(const uint32_t *)(stage + slot * 48 + q * 12 + u * 4);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSteps; s += 4) {
+          const u32x4 w = ((const u32x4 *)stage)[key_unit(slot, q + s)];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) kr[t][(s + u) % kKRegs] = w[u];
+        }
+      }
+      kp[t][0] = sp[slot * kBlocks + step_column(0, q) / kPowerBlock];
+      if (kKPowers > 1) kp[t][kKPowers - 1] = sp[slot * kBlocks + step_column(kSteps - 1, q) / kPowerBlock];
+    }
+  }
+  // V as load_v has it: slots 4 q + i of the first 16 and of the second.
+  __device__ __forceinline__ void take_staged(const char *stage) {
+    const int lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
+    const uint32_t *const sv = (const uint32_t *)(stage + kStageV);
+    const uint8_t *const sp = (const uint8_t *)(stage + kStageP) + 32 * kBlocks;
+    int base = 0;
+#pragma unroll
+    for (int n = 0; n < VPieces<D>::n; ++n) {
+      const int w = VPieces<D>::w[n], col = base + c * w;       // the piece's first
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const u32x4 x = *(const u32x4 *)(sv + col / 8 * kGroup + 16 * t + 4 * q);
+        const uint32_t p = *(const uint32_t *)(sp + col / kPowerBlock * 32 + 16 * t + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vr[4 * t + i][n % kVRegs] = w == 8 ? x[i] : x[i] >> (col & 7) * 4;
+          vp[4 * t + i][n] = (p >> (8 * i)) & 0xffu;
+        }
+      }
+      base += 16 * w;
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 
   __device__ __forceinline__ u32x4 k_frag(int t, int s) const {
@@ -251,22 +336,23 @@ struct FewLine {
   FewSpan f;
   uint32_t own, upto;
 };
-__device__ __forceinline__ FewLine few_line(const AttendArgs &a, int s0, uint32_t before) {
+__device__ __forceinline__ FewLine few_line(const AttendArgs &a, int s0, uint32_t before, int heads) {
   const int s = s0 + (int)(threadIdx.x & (kWave - 1));
   FewLine r{};
   if (s < a.c.seqs) r.f = few_span(a, s);
-  r.own = s < a.c.seqs ? (uint32_t)(r.f.tiles * a.c.heads) : 0u;
+  r.own = s < a.c.seqs ? (uint32_t)(r.f.tiles * heads) : 0u;
   r.upto = before + wave_scan_u32(r.own);
   return r;
 }
-// `note`: write down for the second pass where each sequence's tiles begin, and after them the share.
-__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int wg, bool note) {
+// `note`: write down for the second pass where each sequence's tiles begin, and after them the share.  heads: those
+// whose tiles are in the line, all of them or one.
+__device__ __forceinline__ FewShare few_share(const AttendArgs &a, int heads, int wgs, int wg, bool note) {
   const int S = a.c.seqs, lane = threadIdx.x & (kWave - 1);
-  FewLine line = few_line(a, 0, 0);
+  FewLine line = few_line(a, 0, 0, heads);
   if (note && lane < S) a.line[lane] = line.upto - line.own;
   uint32_t total = lane_of(line.upto, kWave - 1);
   for (int s0 = kWave; s0 < S; s0 += kWave) {
-    const FewLine next = few_line(a, s0, total);
+    const FewLine next = few_line(a, s0, total, heads);
     if (note && s0 + lane < S) a.line[s0 + lane] = next.upto - next.own;
     total = lane_of(next.upto, kWave - 1);
   }
@@ -285,13 +371,13 @@ __device__ __forceinline__ FewShare few_share(const AttendArgs &a, int wgs, int 
       break;
     }
     if ((s0 += kWave) >= S) break;
-    line = few_line(a, s0, lane_of(line.upto, kWave - 1));
+    line = few_line(a, s0, lane_of(line.upto, kWave - 1), heads);
   }
   return r;
 }
-// The work-groups [w0, w1] that share a (sequence, head).
-__device__ __forceinline__ void part_range(uint32_t share, uint32_t begin, int h, int tiles, int *w0, int *w1) {
-  const uint32_t from = begin + (uint32_t)(h * tiles), to = from + tiles;
+// The work-groups [w0, w1] that share a (sequence, head), counted among those of the head if each has its own.
+__device__ __forceinline__ void part_range(const AttendArgs &a, uint32_t share, uint32_t begin, int h, int tiles, int *w0, int *w1) {
+  const uint32_t from = begin + (a.by_head ? 0u : (uint32_t)(h * tiles)), to = from + tiles;
   *w0 = (int)(from / share);
   *w1 = (int)((to - 1) / share);
 }
@@ -300,13 +386,18 @@ __device__ __forceinline__ void part_range(uint32_t share, uint32_t begin, int h
 // would hide its latency.
 // FAR: the call's keys and values, by its bounds, are more than the last-level cache holds, and pass it by.
 template <class T, int BITS, int D, int NR, bool SCORES, int NW, bool FAR>
-__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (BITS < 16 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES && NR == 2) ? 1 : (BITS == 8 && NR == 1 ? 3 : 2))) void attend_few_kernel(AttendArgs a) {
   using F = FewRows<T, BITS, D, NR>;
   constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4;
   constexpr int kRows = 16 * NR;
   constexpr int kHalfRows = NW / 2 * kRows;     // half the waves' rows
-  __shared__ union {
-    int64_t off[kFewBlock + kFewTile];
+  // e2m1: heads that go together have two tiles in LDS in turn, so that one barrier a tile will do
+  constexpr int kSets = E2M1 && !SCORES && NW == 4 && D < 256 ? 2 : 1;
+  __shared__ __align__(16) union {
+    struct {
+      char staged[E2M1 ? kSets * NW * F::kStageBytes : 16];
+      int64_t off[kFewBlock + kFewTile];
+    };
     float o[kHalfRows * F::kPad];
   } sh;
   __shared__ float sh_m[NW / 2][kRows], sh_l[NW / 2][kRows];
@@ -328,14 +419,37 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   int s, h, t0;
   uint32_t left;
   FewSpan span;
+  // A 4-bit row is less than a line of L2, and L1 has only so many requests under way, of a line or of a part of one.  A
+  // work-group has a run of tiles of `hg` neighbouring heads, whose waves load for each other (FewRows::Share), and
+  // the work-groups of all heads at the same slots run on one XCD.  64 conversations with 4 rows each, heads of 64
+  // bytes side by side in a slot, took 127 us with a head's run anywhere, 107 on one XCD, 101 once neighbouring
+  // lanes loaded neighbouring blocks, and 87 with whole lines; 84 where the pool has the heads apart.
+  const int hg = E2M1 ? a.head_group : 1, wph = NW / hg;       // waves of a head
+  const int lane_wave = E2M1 ? wave % wph : wave;              // this one's place among them
+  int unit = 0, first_head = 0;
+  if (E2M1) {
+    const int groups = H / hg, units = gridDim.x / groups, paired = units / 8 * 8 * groups;
+    const int b = blockIdx.x, k = b < paired ? b >> 3 : b - paired;
+    first_head = k % groups * hg;
+    unit = b < paired ? k / groups * 8 + (b & 7) : units / 8 * 8 + k / groups;
+    h = first_head + wave / wph;
+  }
+  const int mine = E2M1 ? unit * H + h : (int)blockIdx.x;      // where its parts go
   if (a.whole) {
-    s = blockIdx.x / H;
-    h = blockIdx.x - s * H;
+    s = mine / H;
+    if (!E2M1) h = mine - s * H;
     t0 = 0;
     left = 0xffffffffu;
     span = few_span(a, s);
+  } else if (E2M1) {
+    const FewShare my = few_share(a, 1, gridDim.x / (H / hg), unit, blockIdx.x == 0 && wave == 0);
+    if (my.s >= a.c.seqs) return;
+    s = my.s;
+    left = my.share;
+    span = my.span;
+    t0 = (int)((uint32_t)unit * my.share - my.base);
   } else {
-    const FewShare my = few_share(a, gridDim.x, blockIdx.x, blockIdx.x == 0 && wave == 0);
+    const FewShare my = few_share(a, H, gridDim.x, blockIdx.x, blockIdx.x == 0 && wave == 0);
     if (my.s >= a.c.seqs) return;
     s = my.s;
     left = my.share;
@@ -351,7 +465,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
     if (a.whole) return;
     if (++s >= a.c.seqs) return;
     span = few_span(a, s);
-    h = 0;
+    if (!E2M1) h = 0;
     continue;
   }
   const int hi = span.hi;
@@ -360,7 +474,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   const int c1 = span.lo + t1 * kFewTile < hi ? span.lo + t1 * kFewTile : hi;
   // where a part goes: a run's first piece (2 wg), or the start of a longer one (2 wg + 1)
   const bool part = t0 > 0 || t1 < span.tiles;
-  const int64_t part_at = ((int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * kRows;
+  const int64_t part_at = ((int64_t)mine * 2 + (t0 > 0 ? 0 : 1)) * kRows;
 
   // rows of this lane: r = 16 nr + col, its token's slot (a padding row sees nothing)
   int pos[NR];
@@ -398,11 +512,17 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   }
   const char *kbase = a.c.k + (int64_t)h * a.c.head_stride;
   const char *vbase = a.c.v + (int64_t)h * a.c.head_stride;
-  const uint8_t *kpow = a.c.k_power, *vpow = a.c.v_power;
+  // from the first head's numbers
+  const uint64_t past = E2M1 ? (uint64_t)(h - first_head) * a.c.page.d * (D / kPowerBlock) : 0;
+  const uint8_t *kpow = a.c.k_power + past, *vpow = a.c.v_power + past;
   const int32_t *trow = a.c.table + (int64_t)s * a.c.table_stride;
   const int last_pos = sp.first + sp.m - 1;
 
-  F f;
+  F f, f1;                   // f1: e2m1, the tile after the next
+  // places in LDS by tile, then by head
+  char *const all = sh.staged + (E2M1 ? lane_wave * hg * F::kStageBytes : 0), *const stage = all + (E2M1 ? wave / wph * F::kStageBytes : 0);
+  const typename F::Share sharing{hg == 4 ? 2 : hg == 2 ? 1 : 0, wave / wph};
+  const char *kfirst = a.c.k + (int64_t)first_head * a.c.head_stride, *vfirst = a.c.v + (int64_t)first_head * a.c.head_stride;
   bool odd = false;
   if (tid == 0) sh_odd = 0;
   // slots [from, from + cnt) from LDS: whole groups of four, as they lie in memory
@@ -419,7 +539,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
       const SlotPlace pl = i < cnt ? slot_place(a.c, trow, (uint32_t)(blk + i)) : SlotPlace{-1, 0};
       const int64_t o = place_offset(a.c, pl);
       sh.off[i] = o;
-      if (E2M1) number[i] = place_number(a.c, pl, h);
+      if (E2M1) number[i] = place_number(a.c, pl, first_head);
       const uint64_t there = __ballot(o >= 0);
       if (lane == 0) {
         present[i / kFewTile] = (uint32_t)there;
@@ -429,16 +549,21 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
     if (tid < kFewTile) sh.off[kFewBlock + tid] = -1;
     if (E2M1 && tid < kFewTile) number[kFewBlock + tid] = 0;
     __syncthreads();
-    int tile = wave;
-    const int begin = tile < ntile ? tile * kFewTile : kFewBlock;
-    f.template load_k<FAR>(kbase, sh.off, kpow, number, begin);
-    __builtin_amdgcn_sched_barrier(0);
-    f.template load_v<FAR>(vbase, sh.off, vpow, number, begin);
-    __builtin_amdgcn_sched_barrier(0);
-    for (; tile < ntile; tile += NW) {
+    // after the last tile one row, again and again: loads without a condition let K be waited for alone
+    const auto begin_of = [&](int tile) { return tile < ntile ? tile * kFewTile : kFewBlock; };
+    const auto load_next = [&](F &f, int at) {
+      f.template load_staged<FAR>(sharing, a.c.head_stride, kfirst, vfirst, sh.off, kpow, vpow, number, at);
+    };
+    const auto put = [&](F &f, int set) {
+      const int from = set % kSets * NW * F::kStageBytes;
+      f.put_staged(sharing, all + from, stage + from);
+      if (hg > 1) __syncthreads();
+      else __builtin_amdgcn_wave_barrier();
+      return stage + from;
+    };
+    const auto step = [&](F &f, int tile, int next, const char *stage) {
       const int at = tile * kFewTile, j0 = blk + at;
-      // after the last tile one row, again and again: loads without a condition let K be waited for alone
-      const int next = tile + NW < ntile ? (tile + NW) * kFewTile : kFewBlock;
+      if constexpr (E2M1) f.take_keys(stage);
       f32x4 sc[NR][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -451,7 +576,8 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
           for (int nr = 0; nr < NR; ++nr) sc[nr][t] = T::mfma16(kf, qf[nr][st], sc[nr][t]);
         }
       }
-      f.template load_k<FAR>(kbase, sh.off, kpow, number, next);
+      if constexpr (E2M1) load_next(f, next);
+      else f.template load_k<FAR>(kbase, sh.off, next);
       __builtin_amdgcn_sched_barrier(0);
 
       const uint32_t there = present[tile];
@@ -505,6 +631,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
 #pragma unroll
         for (int u = 0; u < 4; ++u) pf[nr][u] = T::pack(p[2 * u], p[2 * u + 1]);
       }
+      if constexpr (E2M1) f.take_staged(stage);
       if (masked) {
         // absent slots are zeros; non-finite values of slots that some rows see and others do
         // not wait for the end
@@ -547,7 +674,35 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
             acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
           }
         }
-      f.template load_v<FAR>(vbase, sh.off, vpow, number, next);
+      if constexpr (!E2M1) f.template load_v<FAR>(vbase, sh.off, next);
+    };
+    int tile = lane_wave;
+    if constexpr (E2M1) {
+      // two tiles on their way: a 4-bit one alone is too few bytes
+      load_next(f, begin_of(tile));
+      __builtin_amdgcn_sched_barrier(0);
+      load_next(f1, begin_of(tile + wph));
+      __builtin_amdgcn_sched_barrier(0);
+      // Always both tiles of a turn: with a way around the second, each would wait for the other's loads too.  All
+      // waves take the same turns; in the last one a wave may be past the last tile.
+      const int turns = (ntile + wph - 1) / wph;
+      int i = 0;
+      for (; i + 2 < turns; i += 2, tile += 2 * wph) {
+        step(f, tile, begin_of(tile + 2 * wph), put(f, 0));
+        step(f1, tile + wph, begin_of(tile + 3 * wph), put(f1, 1));
+      }
+      const char *at0 = put(f, 0);
+      if (tile < ntile) step(f, tile, kFewBlock, at0);
+      if (i + 1 < turns) {
+        const char *at1 = put(f1, 1);
+        if (tile + wph < ntile) step(f1, tile + wph, kFewBlock, at1);
+      }
+    } else {
+      f.template load_k<FAR>(kbase, sh.off, begin_of(tile));
+      __builtin_amdgcn_sched_barrier(0);
+      f.template load_v<FAR>(vbase, sh.off, begin_of(tile));
+      __builtin_amdgcn_sched_barrier(0);
+      for (; tile < ntile; tile += wph) step(f, tile, begin_of(tile + wph), nullptr);
     }
   }
 
@@ -559,9 +714,12 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   for (int nr = 0; nr < NR; ++nr) l_run[nr] = xor_sum(l_run[nr]);
 #pragma unroll
   for (int step = NW / 2; step >= 1; step >>= 1) {
+    if (2 * step > wph) continue;
+    // a head's waves hand over in a part of the LDS of their own
+    const int from = E2M1 ? wave / wph * (wph / 2) : 0;
     __syncthreads();
-    if (wave >= step && wave < 2 * step) {
-      const int w = wave - step;
+    if (lane_wave >= step && lane_wave < 2 * step) {
+      const int w = from + lane_wave - step;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         const int r = 16 * nr + col;
@@ -575,23 +733,24 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
       }
     }
     __syncthreads();
-    if (wave < step) {
+    if (lane_wave < step) {
+      const int w = from + lane_wave;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         const int r = 16 * nr + col;
-        const float mo = sh_m[wave][r], lo2 = sh_l[wave][r];
+        const float mo = sh_m[w][r], lo2 = sh_l[w][r];
         const float m_new = fmaxf(m_run[nr], mo);
         const float x = m_new == -INFINITY ? 1.0f : fast_exp2(m_run[nr] - m_new);
         const float y = m_new == -INFINITY ? 1.0f : fast_exp2(mo - m_new);
         m_run[nr] = m_new;
         l_run[nr] = l_run[nr] * x + lo2 * y;
-        const float *row = sh.o + (wave * kRows + r) * F::kPad;
+        const float *row = sh.o + (w * kRows + r) * F::kPad;
 #pragma unroll
         for (int t = 0; t < F::kTiles; ++t) acc[nr][t] = acc[nr][t] * x + *(const f32x4 *)(row + t * 16 + q4 * 4) * y;
       }
     }
   }
-  if (wave == 0) {
+  if (lane_wave == 0) {
   if (sh_odd) {
     // p is above 0 wherever a row sees a slot: an infinity or NaN in it is the sum
     for (int j = c0; j < c1; ++j) {
@@ -599,7 +758,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
       const SlotPlace pl = slot_place(a.c, trow, (uint32_t)j);
       const int64_t o = place_offset(a.c, pl);
       if (o < 0) continue;
-      const uint8_t *powers = E2M1 ? vpow + (uint64_t)place_number(a.c, pl, h) * (D / kPowerBlock) : nullptr;
+      const uint8_t *powers = E2M1 ? a.c.v_power + (uint64_t)place_number(a.c, pl, h) * (D / kPowerBlock) : nullptr;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         if (j > pos[nr] || (a.window > 0 && j <= pos[nr] - a.window)) continue;
@@ -663,12 +822,12 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
       base += 16 * w;
     }
   }
-  }      // wave 0
+  }      // the first wave
   left -= (uint32_t)(t1 - t0);
   if (a.whole || left == 0) return;
   t0 = 0;
-  if (++h == H) {
-    h = 0;
+  if (E2M1 || ++h == H) {
+    if (!E2M1) h = 0;
     if (++s >= a.c.seqs) return;
     span = few_span(a, s);
   }
@@ -677,7 +836,10 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
 }
 
 // A part's place: a work-group's run starts a longer row of parts in its second one.
-__device__ __forceinline__ int64_t part_slot(int w, int w0, int rows) { return ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * rows; }
+__device__ __forceinline__ int64_t part_slot(const AttendArgs &a, int w, int w0, int h, int rows) {
+  const int64_t wg = a.by_head ? (int64_t)w * a.c.heads + h : w;
+  return (wg * 2 + (w == w0 ? 1 : 0)) * rows;
+}
 
 // Weights from kept scores: a thread adds up the rows' 2^(score - lse) for four slots in a row.
 // 25 bytes a slot at four rows: the chain of loads before the sum costs more than they do, so a
@@ -717,7 +879,7 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int p
       ahead[g][r] = seen[g] && r < R ? *(const f32x4 *)(z[g] + r * 4) : (f32x4){0, 0, 0, 0};
   }
   int w0 = 0, w1 = 0;
-  if (!a.whole && R > 0) part_range(a.line[a.c.seqs], a.line[s], h, span.tiles, &w0, &w1);
+  if (!a.whole && R > 0) part_range(a, a.line[a.c.seqs], a.line[s], h, span.tiles, &w0, &w1);
   // the rows' lse: `width` lanes a row, each every width-th part in order, then the lanes two by two
   const int width = R <= 4 ? 64 : (R <= 8 ? 32 : (R <= 16 ? 16 : 8)), r = tid / width;
   static_assert(kFinishThreads / 8 >= kFewRowsMax, "every row has its lanes");
@@ -736,7 +898,7 @@ __device__ __forceinline__ void score_sums(const AttendArgs &a, int block, int p
     if (r < R) {
 #pragma unroll 4
       for (int w = w0 + (tid & (width - 1)); w <= w1; w += width) {
-        const float2 x = a.part_ml[part_slot(w, w0, part_rows) + r];
+        const float2 x = a.part_ml[part_slot(a, w, w0, h, part_rows) + r];
         add(x.x, x.y);
       }
     }
@@ -802,7 +964,7 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
   const int R = span.sp.m * G;
   if (R == 0) return;
   int w0, w1;
-  part_range(share, begin, h, span.tiles, &w0, &w1);
+  part_range(a, share, begin, h, span.tiles, &w0, &w1);
   if (w0 == w1) return;        // one work-group had all of it
   // a row by per_row groups of threads
   const int g = tid / lanes, d4 = tid - g * lanes + slice * lanes;
@@ -826,7 +988,7 @@ __global__ __launch_bounds__(kFinishThreads) void finish_few_kernel(AttendArgs a
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int v = w + u * per_row <= w1 ? w + u * per_row : w1;
-        const int64_t at = part_slot(v, w0, 16 * NR) + r;
+        const int64_t at = part_slot(a, v, w0, h, 16 * NR) + r;
         x[u] = a.part_ml[at];
         o[u] = *(const f32x4 *)(a.part_o + at * D + d4 * 4);
       }
