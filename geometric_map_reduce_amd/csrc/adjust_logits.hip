@@ -2,19 +2,22 @@
 //
 //   z = l;  seen: z > 0 ? z / r : z r;  z -= f c + (c > 0 ? p : 0);  z += bias;  masked: z = -inf
 //
-// A row sees its sequence's text up to its own token.  A work-group has a piece of the vocabulary and up to
-// kLogitRows rows of a sequence in a row: it counts the text's tokens of its piece in LDS (whole numbers, so the order of the
-// additions does not matter), marks the entries that the list of biases names and the tokens by which the rows' texts
-// grow, and goes over its rows.  Few entries of a piece are touched; those are computed in 64 bits one after the
-// other, the others pass by.
+// A row sees its sequence's text up to its own token.  A work-group has a piece of a row: with the logits on their way it
+// counts the text's tokens of its piece in LDS (whole numbers, so the order of the additions does not matter) and
+// marks the entries that the list of biases names, then goes over the logits once.  Few entries of a piece are touched;
+// those are computed in 64 bits one after the other, the others pass by.
+// 158 rows of 131,072 bf16 entries with texts of up to 4,096 tokens take 28 us, 16 without rules, where a copy takes 12
+// to 18, by whether the cache still holds them: the text's way through LDS comes before the first store.  Pieces of 16,384
+// took 35 us; rows that share a sequence's table, one after the other in a work-group, 33, and twice as long for
+// those of the longest draft.
 #include "step.h"
 
 namespace kmi {
 namespace {
 
-// An entry's word: seen in the prompt, named by the list of biases, a token that a later row of the work-group has
-// seen, and how often it was seen past the prompt up to the first row (a text has less than 2^29 tokens).
-constexpr uint32_t kInPrompt = 0x80000000u, kBiased = 0x40000000u, kLater = 0x20000000u, kMade = 0x1fffffffu;
+// An entry's word: seen in the prompt, named by the list of biases, and how often it was seen past the prompt (a
+// text has less than 2^30 tokens).
+constexpr uint32_t kInPrompt = 0x80000000u, kBiased = 0x40000000u, kMade = 0x3fffffffu;
 constexpr int kChunk = 8;                    // entries of a thread at a time
 constexpr int kStrip = 512;                  // a wave's entries at a time
 constexpr int kListed = 512;                 // biases of a piece that are held in LDS
@@ -45,7 +48,6 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
   __shared__ __align__(16) int listed_token[kListed];
   __shared__ int listed_at[kListed], listed;
   __shared__ float listed_bias[kListed];
-  __shared__ int later[kLogitRows];          // the token of row r's text that the row before has not seen
   const int tid = threadIdx.x;
   const int pieces = (a.vocab + kPiece - 1) / kPiece;
   const int64_t t = blockIdx.x / pieces;
@@ -54,8 +56,7 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
   int64_t begin = a.starts[s], end = a.starts[s + 1];
   begin = begin < 0 ? 0 : begin;
   end = end > a.rows ? a.rows : end;
-  if (t < begin || t >= end || (t - begin) % kLogitRows) return;      // of no sequence, or the rows of another work-group
-  const int rows = end - t < kLogitRows ? (int)(end - t) : kLogitRows;
+  if (t < begin || t >= end) return;         // of no sequence
 
   // Strips of 512 entries are dealt to the pieces in turn: a text's common tokens lie close together.
   const auto entry = [&](int c) {            // the first of the thread's chunk c, whose word is at c * 4096 + 8 tid
@@ -66,30 +67,26 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
     const int strip = x / kStrip, mine = (int)fast_div(a.pieces_div, (uint32_t)strip);
     return x >= 0 && x < V && strip - mine * pieces == piece ? mine * kStrip + x % kStrip : -1;
   };
-  // a row's piece and its mask, on their way while the table is made
+  // the piece and its mask, on their way while the table is made
   union Held { u32x4 w[kWords]; E e[kChunk]; };
   Held u[CHUNKS];
   uint32_t bits[CHUNKS];
-  const auto fetch = [&](int r) {
-    const E *in = (const E *)a.logits + (t + r) * a.stride;
-    const uint32_t *mask = a.mask ? a.mask + (t + r) * a.mask_stride : nullptr;
+  const E *in = (const E *)a.logits + t * a.stride;
+  const uint32_t *mask = a.mask ? a.mask + t * a.mask_stride : nullptr;
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-      const int64_t x0 = entry(c);
-      if (a.whole && x0 + kChunk <= V) {
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int64_t x0 = entry(c);
+    if (a.whole && x0 + kChunk <= V) {
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) u[c].w[k] = ((const u32x4 *)(in + x0))[k];
-      } else {
+      for (int k = 0; k < kWords; ++k) u[c].w[k] = ((const u32x4 *)(in + x0))[k];
+    } else {
 #pragma unroll
-        for (int k = 0; k < kChunk; ++k) u[c].e[k] = x0 + k < V ? in[x0 + k] : E(0);
-      }
-      bits[c] = mask && x0 < V ? mask[x0 >> 5] >> (x0 & 31) : 0xffu;
+      for (int k = 0; k < kChunk; ++k) u[c].e[k] = x0 + k < V ? in[x0 + k] : E(0);
     }
-  };
-  fetch(0);
+    bits[c] = mask && x0 < V ? mask[x0 >> 5] >> (x0 & 31) : 0xffu;
+  }
   const bool rules = a.text || a.biases;
   double rep = 1.0, pres = 0.0, freq = 0.0;
-  int64_t n = 0;                             // tokens of the text up to the row's own
   int prompt = 0;
   const int32_t *text = a.text + s * a.text_stride;
   const auto count = [&](int x, int64_t i) {
@@ -108,15 +105,8 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
       if (a.presence) pres = (double)a.presence[s];
       if (a.frequency) freq = (double)a.frequency[s];
       if (a.prompt_lens) prompt = a.prompt_lens[s];
-      n = a.lens[s] - (end - t) + 1;
+      const int64_t n = a.lens[s] - (end - t) + 1;       // tokens up to the row's own
       const int64_t m = n < a.text_width ? n : a.text_width;
-      if (tid < kLogitRows) {
-        const int64_t i = n + tid - 1;
-        const int x = tid > 0 && i >= 0 && i < a.text_width ? text[i] : -1;
-        const int at = tid < rows ? place(x) : -1;
-        later[tid] = at < 0 ? -1 : x;
-        if (at >= 0) atomicOr(&table[at], kLater);
-      }
       if (((uintptr_t)text & 15) == 0) {
         for (int64_t i = 4 * tid; i < m; i += 4 * kLogitThreads) {
           if (i + 4 <= m) {
@@ -168,64 +158,52 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
     return (double)v;
   };
   const E none = Logit<T>::put(-INFINITY);
-  for (int r = 0; r < rows; ++r) {
-    E *out = (E *)a.out + (t + r) * a.out_stride;
+  E *out = (E *)a.out + t * a.out_stride;
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-      const int64_t x0 = entry(c);
-      const int word = (c * kLogitThreads + tid) * kChunk;
-      if (x0 >= V) break;
-      uint32_t touched = 0;
-      if (rules) {
-        const u32x4 lo = *(const u32x4 *)(table + word), hi = *(const u32x4 *)(table + word + 4);
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int64_t x0 = entry(c);
+    const int word = (c * kLogitThreads + tid) * kChunk;
+    if (x0 >= V) break;
+    uint32_t touched = 0;
+    if (rules) {
+      const u32x4 lo = *(const u32x4 *)(table + word), hi = *(const u32x4 *)(table + word + 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) touched |= (lo[k] ? 1u << k : 0u) | (hi[k] ? 16u << k : 0u);
-        touched &= bits[c];
-      }
-      while (touched) {
-        const int k = __ffs(touched) - 1;
-        touched &= touched - 1;
-        float l = 0.0f;
-#pragma unroll
-        for (int m = 0; m < kChunk; ++m) l = m == k ? Logit<T>::get(u[c].e[m]) : l;
-        double z = (double)l;
-        const uint32_t w = table[word + k];
-        uint32_t made = w & kMade;
-        bool seen = (w & (kInPrompt | kMade)) != 0;
-        if (w & kLater) {
-          for (int m = 1; m <= r; ++m)
-            if (later[m] == (int)x0 + k) {
-              seen = true;
-              made += n + m - 1 >= prompt ? 1u : 0u;
-            }
-        }
-        if (seen) {
-          if (z > 0.0) {
-            double q = z * inverse;          // an exact quotient comes out exact
-            if (__builtin_fabs(q) < INFINITY) q = __builtin_fma(__builtin_fma(-q, rep, z), inverse, q);
-            z = q;
-          } else {
-            z *= rep;
-          }
-          if (made) z -= freq * (double)made + pres;
-        }
-        if (w & kBiased) z += bias_of((int)x0 + k);
-        const E e = Logit<T>::put((float)z);
-#pragma unroll
-        for (int m = 0; m < kChunk; ++m) u[c].e[m] = m == k ? e : u[c].e[m];
-      }
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k) u[c].e[k] = (bits[c] >> k) & 1u ? u[c].e[k] : none;
-      if (a.whole && x0 + kChunk <= V) {
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) ((u32x4 *)(out + x0))[k] = u[c].w[k];
-      } else {
-#pragma unroll
-        for (int k = 0; k < kChunk; ++k)
-          if (x0 + k < V) out[x0 + k] = u[c].e[k];
-      }
+      for (int k = 0; k < 4; ++k) touched |= (lo[k] ? 1u << k : 0u) | (hi[k] ? 16u << k : 0u);
+      touched &= bits[c];
     }
-    if (r + 1 < rows) fetch(r + 1);
+    while (touched) {
+      const int k = __ffs(touched) - 1;
+      touched &= touched - 1;
+      float l = 0.0f;
+#pragma unroll
+      for (int m = 0; m < kChunk; ++m) l = m == k ? Logit<T>::get(u[c].e[m]) : l;
+      double z = (double)l;
+      const uint32_t w = table[word + k];
+      if (w & (kInPrompt | kMade)) {
+        if (z > 0.0) {
+          double q = z * inverse;            // an exact quotient comes out exact
+          if (__builtin_fabs(q) < INFINITY) q = __builtin_fma(__builtin_fma(-q, rep, z), inverse, q);
+          z = q;
+        } else {
+          z *= rep;
+        }
+        if (w & kMade) z -= freq * (double)(w & kMade) + pres;
+      }
+      if (w & kBiased) z += bias_of((int)x0 + k);
+      const E e = Logit<T>::put((float)z);
+#pragma unroll
+      for (int m = 0; m < kChunk; ++m) u[c].e[m] = m == k ? e : u[c].e[m];
+    }
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) u[c].e[k] = (bits[c] >> k) & 1u ? u[c].e[k] : none;
+    if (a.whole && x0 + kChunk <= V) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) ((u32x4 *)(out + x0))[k] = u[c].w[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (x0 + k < V) out[x0 + k] = u[c].e[k];
+    }
   }
 }
 

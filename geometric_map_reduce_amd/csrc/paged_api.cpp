@@ -81,7 +81,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     p->by_head = !p->whole && c.type == KEOPS_TYPE_E2M1;
     // neighbouring heads whose rows make up a line of 128 bytes go together
     p->head_group = 1;
-    if (p->by_head && !p->scores)
+    if (p->by_head && !p->scores && ceil_div(S * from_tile, kFewLeast) * H >= room)
       while (p->head_group * c.dim / 2 < 128 && H % (2 * p->head_group) == 0) p->head_group *= 2;
     const int64_t groups = H / p->head_group;
     p->grid = p->whole ? S * H

@@ -64,7 +64,6 @@ struct LogitArgs {
   bool whole;                        // rows of logits and out start on 16 bytes
 };
 constexpr int kLogitThreads = 512;
-constexpr int kLogitRows = 8;        // rows of a sequence that a work-group takes at most
 constexpr int kLogitPiece = 8192;    // vocabulary entries of a work-group, or half of them
 
 void launch_rotary(const RotaryArgs &a, int type, int piece, dim3 grid, hipStream_t st);
