@@ -385,13 +385,30 @@ def test_attention_past_the_caches(dtype, dim, new, weights):
     check_attention(b, max_len=1 << 21)                     # 2 x 3 x 2 x 2^21 rows of 34 bytes: 428 MB and more
 
 
-@pytest.mark.parametrize("dim,new,dtype", [(64, 3, BF), (128, 3, FP), (96, 3, BF), (256, 3, BF), (64, 40, BF), (128, 40, FP), (256, 40, BF),
-                                           (96, 40, FP), (128, 3, BF), (128, 40, BF)])
-def test_hidden_values_reach_no_row(dim, new, dtype):
+@pytest.mark.parametrize("dim,kv,dtype", [(64, 4, BF), (64, 2, FP), (64, 3, BF), (96, 4, FP), (96, 8, BF), (96, 1, BF), (128, 8, BF), (128, 6, FP),
+                                          (128, 5, BF), (256, 2, BF), (64, 12, BF), (128, 2, FP)])
+@pytest.mark.parametrize("new,group,window,weights", [(1, 4, 0, False), (3, 2, 0, False), (2, 9, 70, False), (1, 1, 0, True)])
+def test_attention_heads_together(dim, kv, dtype, new, group, window, weights):
+    """Bounds under which one, two or four neighbouring heads go together, in runs over several sequences."""
+    say(f"neighbouring heads, {kv} x {dim}, {dtype}, {new} new, group {group}, window {window}, weights {weights}")
+    lens = [700, 0, 333, 90, 1025]
+    b = Batch4(61 + dim + kv, lens, [min(new, n) for n in lens], kv * group, kv, dim, 24, dtype)
+    b.window = window
+    b.table[0, 3] = -1
+    if weights:
+        b.weights = torch.rand((b.P, kv, 24), generator=b.gen)
+    check_attention(b, max_len=30000)
+
+
+@pytest.mark.parametrize("dim,new,dtype,kv", [(64, 3, BF, 2), (128, 3, FP, 2), (96, 3, BF, 2), (256, 3, BF, 2), (64, 40, BF, 2), (128, 40, FP, 2),
+                                              (256, 40, BF, 2), (96, 40, FP, 2), (128, 3, BF, 2), (128, 40, BF, 2), (64, 3, BF, 4), (96, 3, FP, 8),
+                                              (128, 3, BF, 6)])
+@pytest.mark.parametrize("max_len", [None, 30000])
+def test_hidden_values_reach_no_row(dim, new, dtype, kv, max_len):
     """NaN blocks and blocks past the type's largest number, in the key and value of a later token and below the window,
     change nothing for the rows that do not see them; the rows that see them get what the formula gives."""
-    say(f"hidden non-finite blocks, dim {dim}, {new} new, {dtype}")
-    b = Batch4(9, [140], [new], 4, 2, dim, 16, dtype)
+    say(f"hidden non-finite blocks, {kv} x {dim}, {new} new, {dtype}, bound {max_len}")
+    b = Batch4(9, [140], [new], 2 * kv, kv, dim, 16, dtype)
     b.window = 101
     first = 140 - new
     spots = (139, first - 100, first + 1)
@@ -403,12 +420,12 @@ def test_hidden_values_reach_no_row(dim, new, dtype):
         b.v_scale[pg, 1, row, 1] = 254 if dtype == BF else 142
     pg, row = b.table[0, 139 // 16].item(), 139 % 16
     b.k_scale[pg, 0, row, 0] = 255
-    out, lse, _ = run_attention(b)
+    out, lse, _ = run_attention(b, max_len=max_len)
     o, z, _, ot, zt, _ = ref.attention(b)
     for t in range(new):
         sees = [j for j in spots if first + t - 101 < j <= first + t]
-        for h in range(4):
-            if not sees:
+        for h in range(2 * kv):
+            if not sees or h >= 4:
                 assert bool(out[t, h].isfinite().all()) and bool(lse[t, h].isfinite())
                 close(out[t, h], o[t, h], ot[t, h], f"row {t}")
                 continue
