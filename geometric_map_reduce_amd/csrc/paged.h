@@ -165,6 +165,17 @@ struct AttendArgs {
   float *part_w;
 };
 
+// A 4-bit cache's slots to pages of 16 bits, [seqs * width][heads][page_size][dim], and their table [seqs][width].
+struct WidenArgs {
+  CacheView c;
+  char *k, *v;
+  int32_t *table;
+  int32_t width;
+  const int32_t *starts;
+  int64_t tokens;
+  int32_t max_q, max_len, window;
+};
+
 struct EvictArgs {
   CacheView c;
   int row_bytes;                // of a slot and head's key
@@ -191,6 +202,7 @@ void launch_append(const AppendArgs &a, int type, int cache_type, hipStream_t st
 // Variants exist for dim 64, 96, 128 and 256; the API checks before it calls.
 constexpr int kFewRowsMax = 32;      // rows (new tokens x group) of the few-rows form
 constexpr int kManyRowsTile = 128;   // rows of a work-group of the many-rows form
+constexpr int kManySlotsTile = 64;   // slots of a tile of it
 constexpr int kSumSlotsTile = 256;   // slots of a work-group of the column sums
 // Threads of a work-group, for the plans.
 constexpr int kFinishThreads = 256;  // few rows: the second pass
@@ -216,6 +228,7 @@ void launch_attend_sums(const AttendArgs &a, int type, int bits, int dim, dim3 g
 void launch_attend_join(const AttendArgs &a, int type, hipStream_t st);
 void launch_attend_sums_join(const AttendArgs &a, hipStream_t st);
 void launch_evict(const EvictArgs &a, hipStream_t st);
+void launch_widen(const WidenArgs &a, int type, hipStream_t st);
 void launch_verify(const VerifyArgs &a, hipStream_t st);
 
 // ---------------------------------------------------------------- element types

@@ -41,13 +41,21 @@ constexpr double kFarBytes = 384e6;
 // (32 rows) 462 in place of 604.  Up to half a GB is a five-hundredth of the device's memory, and always taken.
 constexpr double kScoresAlways = 512e6, kScoresMost = 4294967296.0;
 
+// Rows of a sequence's head from which on a 4-bit cache is widened to 16 bits before attention, not in each of its
+// work-groups.  16,384 slots of 8 x 128: 4,096 tokens of 4 rows a head 1,103 to 943 us, 512 tokens 182 to 167, 256
+// 110 to 107, 128 61 to 73; 8,192 slots of dim 256 and 2,048 tokens 769 to 606.  And what that may take: of memory, and
+// beside the pool, for the bounds may lie far above the lengths.
+constexpr int64_t kWidenRows = 1024;
+constexpr double kWidenMost = 4294967296.0;
+
 // Launch plan of one attention call.
 struct AttendPlan {
   bool few, scores, far, by_head;
   int whole, head_group, row_tiles, score_rows, join_rows, join_slices;
   int64_t nsplit, nrow, grid, sums_grid, score_stride;
   int64_t line_bytes, ml_bytes, o_bytes, score_bytes, sums_bytes;
-  int64_t total() const { return line_bytes + ml_bytes + o_bytes + score_bytes + sums_bytes; }
+  int64_t wide_width, wide_bytes, wide_table;    // widened: pages of a sequence, bytes of the keys, or the values, and of the table
+  int64_t total() const { return line_bytes + ml_bytes + o_bytes + score_bytes + sums_bytes + 2 * wide_bytes + wide_table; }
 };
 
 int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int64_t max_q, int64_t max_len, int window, int cus,
@@ -108,6 +116,15 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     // the join looks through all tokens' rows
     if (p->nsplit > 1 && !launchable((double)join_blocks(tokens * heads, c.dim, (int)p->nsplit), kJoinThreads)) p->nsplit = 1;
     p->grid = wgs * p->nsplit;
+    if (c.type == KEOPS_TYPE_E2M1 && rows >= kWidenRows) {
+      const int64_t width = std::min<int64_t>(ceil_div(max_len, c.page_size), c.table_width);
+      const double slots = (double)S * (double)width * c.page_size, bytes = slots * (double)H * c.dim * 2.0;
+      if (width > 0 && slots <= 2.0 * (double)c.pages * c.page_size && 2.0 * bytes <= kWidenMost) {
+        p->wide_width = width;
+        p->wide_bytes = align256((int64_t)bytes);
+        p->wide_table = align256(S * width * 4);
+      }
+    }
   }
   if (c.weights) {
     if (p->scores) {
@@ -277,9 +294,27 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   a.nrow = (int32_t)std::max<int64_t>(1, p.nrow);
   a.part_w = (float *)(ws + p.ml_bytes + p.o_bytes + p.score_bytes);
   const int bits = held_bits(c->type);
+  if (p.wide_width) {
+    char *wide = ws + p.ml_bytes + p.o_bytes + p.score_bytes + p.sums_bytes;
+    WidenArgs w{a.c, wide, wide + p.wide_bytes, (int32_t *)(wide + 2 * p.wide_bytes), (int32_t)p.wide_width, starts, tokens, max_q, max_len, a.window};
+    launch_widen(w, type, st);
+  }
   const int prof = prof_begin(st);
   if (p.few) launch_attend_few(a, type, bits, c->dim, p.row_tiles, (int)p.grid, p.join_rows, st);
-  else launch_attend_many(a, type, bits, c->dim, dim3((unsigned)p.grid), st);
+  else if (p.wide_width) {
+    AttendArgs b = a;
+    char *wide = ws + p.ml_bytes + p.o_bytes + p.score_bytes + p.sums_bytes;
+    b.c.k = wide;
+    b.c.v = wide + p.wide_bytes;
+    b.c.table = (const int32_t *)(wide + 2 * p.wide_bytes);
+    b.c.table_stride = p.wide_width;
+    b.c.table_width = (uint32_t)p.wide_width;
+    b.c.pages = (uint32_t)(c->seqs * p.wide_width);
+    b.c.slot_stride = c->dim * 2;
+    b.c.head_stride = (int64_t)c->page_size * b.c.slot_stride;
+    b.c.page_stride = c->heads * b.c.head_stride;
+    launch_attend_many(b, type, 16, c->dim, dim3((unsigned)p.grid), st);
+  } else launch_attend_many(a, type, bits, c->dim, dim3((unsigned)p.grid), st);
   prof_end(prof, st);
   if (!p.few && p.nsplit > 1) launch_attend_join(a, type, st);
   if (c->weights && max_len > 0 && !p.scores) {

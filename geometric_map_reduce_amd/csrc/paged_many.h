@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void attend_many_ker
   constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4, NARROW = E4M3 || E2M1;
   // slots of a tile: two halves are two independent chains of products (one of 32 waited for itself:
   // D = 256 ran at 647 instead of 759 TFLOP/s)
-  constexpr int KT = 64;
+  constexpr int KT = kManySlotsTile;
   constexpr int kSteps = D / 16, kCols = D / 32, kSub = KT / 32;
   constexpr int kPieces = D / 8;                     // 16-byte pieces of a row in LDS
   constexpr int kLoads = KT * kPieces / kManyThreads;

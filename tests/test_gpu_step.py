@@ -360,6 +360,9 @@ ATTEND = [
     ([130, 257], [130, 200], 4, 1, 128, 24, FP, 0), ([300], [150], 2, 1, 96, 128, BF, 0), ([333, 80], [40, 80], 8, 2, 256, 20, BF, 0),
     ([222], [60], 8, 1, 256, 16, FP, 17), ([2000], [12], 8, 1, 128, 64, BF, 0), ([777, 400, 100], [300, 10, 100], 8, 4, 64, 24, FP, 128),
     ([1500], [5], 8, 8, 128, 1, BF, 64), ([1500], [3], 4, 2, 96, 64, BF, 0), ([27000, 300], [2, 1], 5, 1, 64, 64, BF, 0),
+    # widened to 16 bits first
+    ([500, 90, 0, 70], [270, 90, 0, 1], 8, 2, 64, 24, FP, 0), ([400], [130], 8, 1, 128, 16, BF, 0), ([300, 290], [140, 1], 8, 1, 96, 7, BF, 50),
+    ([290], [260], 8, 2, 256, 64, FP, 130), ([1100, 300], [130, 128], 8, 1, 64, 1, BF, 65),
 ]
 
 
@@ -402,36 +405,37 @@ def test_attention_heads_together(dim, kv, dtype, new, group, window, weights):
 
 @pytest.mark.parametrize("dim,new,dtype,kv", [(64, 3, BF, 2), (128, 3, FP, 2), (96, 3, BF, 2), (256, 3, BF, 2), (64, 40, BF, 2), (128, 40, FP, 2),
                                               (256, 40, BF, 2), (96, 40, FP, 2), (128, 3, BF, 2), (128, 40, BF, 2), (64, 3, BF, 4), (96, 3, FP, 8),
-                                              (128, 3, BF, 6)])
+                                              (128, 3, BF, 6), (64, 100, BF, 2), (128, 100, FP, 2), (256, 100, BF, 4), (96, 90, BF, 2)])
 @pytest.mark.parametrize("max_len", [None, 30000])
 def test_hidden_values_reach_no_row(dim, new, dtype, kv, max_len):
     """NaN blocks and blocks past the type's largest number, in the key and value of a later token and below the window,
     change nothing for the rows that do not see them; the rows that see them get what the formula gives."""
     say(f"hidden non-finite blocks, {kv} x {dim}, {new} new, {dtype}, bound {max_len}")
-    b = Batch4(9, [140], [new], 2 * kv, kv, dim, 16, dtype)
+    group = 12 if new > 80 else 2                            # 12: widened to 16 bits first, but under the wider bound
+    b = Batch4(9, [240], [new], group * kv, kv, dim, 16, dtype)
     b.window = 101
-    first = 140 - new
-    spots = (139, first - 100, first + 1)
+    first = 240 - new
+    spots = (239, first - 100, first + 1)
     for j in spots:
         pg, row = b.table[0, j // 16].item(), j % 16
         b.v_scale[pg, 0, row, 0] = 255                       # a block of NaN
         b.v[pg, row, 1] = 0
         b.v[pg, row, 1, 20] = 0x07                           # column 40 alone
         b.v_scale[pg, 1, row, 1] = 254 if dtype == BF else 142
-    pg, row = b.table[0, 139 // 16].item(), 139 % 16
+    pg, row = b.table[0, 239 // 16].item(), 239 % 16
     b.k_scale[pg, 0, row, 0] = 255
     out, lse, _ = run_attention(b, max_len=max_len)
     o, z, _, ot, zt, _ = ref.attention(b)
     for t in range(new):
         sees = [j for j in spots if first + t - 101 < j <= first + t]
-        for h in range(2 * kv):
-            if not sees or h >= 4:
+        for h in range(group * kv):
+            if not sees or h >= 2 * group:
                 assert bool(out[t, h].isfinite().all()) and bool(lse[t, h].isfinite())
                 close(out[t, h], o[t, h], ot[t, h], f"row {t}")
                 continue
-            if h < 2:
+            if h < group:
                 assert bool(out[t, h, :32].isnan().all()), (t, h)
-                if 139 not in sees:
+                if 239 not in sees:
                     assert bool(out[t, h, 32:].isfinite().all())
                     close(out[t, h, 32:], o[t, h, 32:], ot[t, h, 32:], f"row {t}")
             else:
@@ -440,10 +444,10 @@ def test_hidden_values_reach_no_row(dim, new, dtype, kv, max_len):
                 close(out[t, h, rest], o[t, h, rest], ot[t, h, rest], f"row {t}")
 
 
-@pytest.mark.parametrize("new", [2, 30])
-def test_absent_pages(new):
-    say(f"absent pages in 4 bits, {new} new")
-    b = Batch4(11, [100, 64], [new, new], 8, 2, 64, 16)
+@pytest.mark.parametrize("new,heads", [(2, 8), (30, 8), (40, 64)])
+def test_absent_pages(new, heads):
+    say(f"absent pages in 4 bits, {new} new, {heads} heads")
+    b = Batch4(11, [100, 64], [new, new], heads, 2, 64, 16)
     b.weights = torch.rand((b.P, 2, 16), generator=b.gen)
     b.table[0, 1] = -1
     b.table[0, 3] = b.P
@@ -510,7 +514,7 @@ def test_far_pages():
     cache = (k.view(E2), v.view(E2), far[None].cuda(), put(b.lens_t()), put(b.starts))
     scales = dict(k_scale=ks.view(E8), v_scale=vs.view(E8))
     o, z, _, ot, zt, _ = ref.attention(b)
-    for max_q in (2, 40):                                     # both forms
+    for max_q in (2, 40, 600):                                # each form
         out, lse = gm.keops_paged_attention(put(b.q), *cache, max_q, 70, **scales)
         close(out.cpu(), o, ot, "out")
         close(lse.cpu(), z, zt, "lse")
@@ -523,9 +527,32 @@ def test_far_pages():
     assert torch.equal(rv.cpu().double(), sref.from_4bit(*sref.to_4bit(nv, BF)))
 
 
+def test_widened_slots_do_not_see_what_was_left():
+    """The workspace of a call that widens the cache first holds NaN of another one."""
+    say("a workspace full of NaN")
+    for window in (0, 100):
+        b = Batch4(33, [500, 333], [140, 130], 8, 1, 64, 16)
+        b.window = window
+        k, v, ks, vs = pools(b)
+        args = (put(b.q), k, v, put(b.table), put(b.lens_t()), put(b.starts), 140, 500)
+        kw = dict(k_scale=ks, v_scale=vs, window=window)
+        st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=st):
+            fill = torch.empty(16 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+            del fill                                         # its memory is the workspace's next
+            out, lse = gm.keops_paged_attention(*args, **kw)
+        o, z, _, ot, zt, _ = ref.attention(b)
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            close(out.cpu(), o, ot, "out")
+            close(lse.cpu(), z, zt, "lse")
+
+
 def test_results_repeat_on_every_stream():
     """The same bits on the current stream, on another, and under a graph that is replayed between eager calls."""
-    for new in (1, 40):
+    for new in (1, 40, 300):
         say(f"4-bit attention repeated, {new} new")
         b = Batch4(29, [2000, 700], [new, new], 8, 2, 128, 16, junk=0.0)
         k, v, ks, vs = pools(b)
