@@ -28,8 +28,8 @@ __device__ __forceinline__ void turn8(const char *x, int d, const double2 *cs, i
       if (d / 2 + k >= n) continue;
       const double2 by = cs[d / 2 + k];
       const R c = (R)by.x, s = (R)by.y, a = (R)own[2 * k], b = (R)own[2 * k + 1];
-      out[2 * k] = a * c - b * s;
-      out[2 * k + 1] = a * s + b * c;
+      out[2 * k] = fma(a, c, b * -s);
+      out[2 * k + 1] = fma(b, c, a * s);
     }
   } else if (n % 8 == 0) {
     const bool second = d >= n;
@@ -40,7 +40,7 @@ __device__ __forceinline__ void turn8(const char *x, int d, const double2 *cs, i
     for (int u = 0; u < 8; ++u) {
       const double2 by = cs[i + u];
       const R c = (R)by.x, s = second ? (R)by.y : -(R)by.y;
-      out[u] = (R)own[u] * c + (R)other[u] * s;
+      out[u] = fma((R)own[u], c, (R)other[u] * s);
     }
   } else {
 #pragma unroll
@@ -51,9 +51,15 @@ __device__ __forceinline__ void turn8(const char *x, int d, const double2 *cs, i
       const float other = T::lo(*(const uint16_t *)(x + (second ? i : i + n) * 2));
       const double2 by = cs[i];
       const R c = (R)by.x, s = second ? (R)by.y : -(R)by.y;
-      out[u] = (R)own[u] * c + (R)other * s;
+      out[u] = fma((R)own[u], c, (R)other * s);
     }
   }
+}
+
+template <class T>
+__device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
+  return (u32x4){T::pack(held(x[0]), held(x[1])), T::pack(held(x[2]), held(x[3])), T::pack(held(x[4]), held(x[5])),
+                 T::pack(held(x[6]), held(x[7]))};
 }
 
 template <class T, int BITS>
@@ -97,8 +103,7 @@ __global__ __launch_bounds__(kTurnThreads) void append_rotary_kernel(AppendRotar
     if (head < a.heads) {
       float x[8];
       turn8<T>(a.q + (t0 + t) * a.q_stride + (int64_t)head * D * 2, d, cs, n, a.r.interleaved, x);
-      *(u32x4 *)(a.q_out + (t0 + t) * a.q_out_stride + ((int64_t)head * D + d) * 2) =
-          (u32x4){T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
+      *(u32x4 *)(a.q_out + (t0 + t) * a.q_out_stride + ((int64_t)head * D + d) * 2) = pack8<T>(x);
       continue;
     }
     const SlotPlace p = place[t];
@@ -115,7 +120,7 @@ __global__ __launch_bounds__(kTurnThreads) void append_rotary_kernel(AppendRotar
       }
       float y[8];
       turn8<T>(x, d, cs, n, a.r.interleaved, y);
-      *(u32x4 *)to = (u32x4){T::pack(y[0], y[1]), T::pack(y[2], y[3]), T::pack(y[4], y[5]), T::pack(y[6], y[7])};
+      *(u32x4 *)to = pack8<T>(y);
     } else {
       float y[8];
       if (key) {

@@ -89,6 +89,13 @@ __device__ __forceinline__ int owner_of(const int32_t *starts, int seqs, int64_t
   return lo;
 }
 
+// x as it is in 32 bits: no instruction that rounds a multiply-add straight to 16 bits takes x's place, which the
+// compiler uses in one loop and not in the next.
+__device__ __forceinline__ float held(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
 // x rounded to 32 bits towards an odd last place where it is not exact: what is rounded to far fewer bits
 // after that comes out as if from x itself.
 __device__ __forceinline__ float round_to_odd(double x) {

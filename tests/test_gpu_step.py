@@ -241,6 +241,31 @@ def test_append_rotary(lens, new, heads, kv, dim, page, rot, dtype, cache, inter
     check_append(b, wide, heads, freqs, given, interleaved, 1.0 if rot == dim else 1.25, weights)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot", [(128, 128), (64, 24), (96, 96), (96, 40), (256, 256)])
+def test_append_rotary_is_rotary(dim, rot, interleaved, dtype):
+    """Queries, and keys of a 16-bit cache, have the bits that keops_rotary gives them."""
+    say(f"append rotary and rotary {dim} {rot} {interleaved} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(dim + rot)
+    n, page = [900, 1, 411], 64
+    T = sum(n)
+    q, k, v = (torch.randn((T, h, dim), generator=g, device="cuda").to(dtype) for h in (6, 2, 2))
+    kp, vp = (torch.zeros((24, page, 2, dim), dtype=dtype, device="cuda") for _ in range(2))
+    table = torch.randperm(24, generator=torch.Generator().manual_seed(1))[:24].int().view(1, 24).repeat(3, 1).cuda()
+    table[1], table[2, :7] = table[0, 15], table[0, 16:23]
+    lens = torch.tensor(n, dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 900, 901, T], dtype=torch.int32, device="cuda")
+    freqs = gm.keops_rotary_frequencies(rot, device="cuda")
+    at = torch.cat([torch.arange(x) for x in n]).int().cuda()
+    for positions, p in ((None, at), (at * 1000 - 5, at * 1000 - 5)):
+        turned = gm.keops_cache_append_rotary(q, k, v, kp, vp, table, lens, starts, freqs, positions=positions, interleaved=interleaved,
+                                              factor=1.25)
+        assert torch.equal(turned, gm.keops_rotary(q, p, freqs, interleaved=interleaved, factor=1.25))
+        kr, vr = gm.keops_cache_read(kp, vp, table, lens, starts, T)
+        assert torch.equal(kr, gm.keops_rotary(k, p, freqs, interleaved=interleaved, factor=1.25)) and torch.equal(vr, v)
+
+
 @pytest.mark.parametrize("cache", [E2, E4, BF])
 def test_append_rotary_at_position_zero_is_the_append(cache):
     """Where nothing turns, keys come out as those of keops_cache_append, ties of every kind included."""
