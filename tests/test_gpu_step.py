@@ -858,3 +858,38 @@ def test_a_step(cache):
         kept = [t.clone() for t in got]
         for x, y in zip(kept, step()):
             assert torch.equal(x, y)
+
+
+def test_example_decodes_over_4_bits():
+    """The example's other way runs, repeats itself, and its rules hold; what attention gave is the formula's over the values
+    that the cache holds."""
+    import importlib.util
+    import os
+    say("example, 4 bits and rules")
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    rounds = [0]
+
+    def watch(st):
+        rounds[0] += 1
+        if rounds[0] % 5:
+            return
+        m, p, n = st["model"], st["pages"], st["lens"].tolist()
+        whole = torch.tensor([0] + n, dtype=torch.int32).cumsum(0).int().cuda()
+        k, v = (t.double().cpu() for t in gm.keops_cache_read(p.k, p.v, st["table"], st["lens"], whole, sum(n), **p.scales))
+        for s in range(len(n)):
+            a, e, at = int(st["starts"][s]), int(st["starts"][s + 1]), int(whole[s])
+            q = st["q"][a:e].double().cpu()
+            for h in range(m.heads):
+                g = h // (m.heads // m.kv)
+                z = q[:, h] @ k[at:at + n[s], g].T / m.dim ** 0.5
+                z.masked_fill_(torch.arange(n[s]) > torch.arange(n[s] - (e - a), n[s])[:, None], -float("inf"))
+                o = torch.softmax(z, -1) @ v[at:at + n[s], g]
+                assert (st["out"][a:e, h].double().cpu() - o).abs().max() <= 2 ** -7 * v.abs().max()
+    text = ex.decode(rounds=40, watch=watch, four_bit=True, rules=True)
+    assert rounds[0] == 40 and all(40 <= len(t) <= 160 for t in text)
+    # what was taken or drawn has mass under the rules
+    assert all(x < 199 // 2 for t in text for x in t)
+    assert ex.decode(rounds=10, four_bit=True, rules=True) == [t[:len(u)] for t, u in zip(text, ex.decode(rounds=10, four_bit=True, rules=True))]
