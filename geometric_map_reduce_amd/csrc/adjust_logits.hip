@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
       if (w & (kInPrompt | kMade)) {
         if (z > 0.0) {
           double q = z * inverse;            // an exact quotient comes out exact
-          if (__builtin_fabs(q) < INFINITY) q = __builtin_fma(__builtin_fma(-q, rep, z), inverse, q);
+          if (__builtin_fabs(q) < INFINITY && q != 0.0) q = __builtin_fma(__builtin_fma(-q, rep, z), inverse, q);
           z = q;
         } else {
           z *= rep;

@@ -116,7 +116,7 @@ __device__ __forceinline__ float e4m3_quotient(float x, float s) {
 __device__ __forceinline__ float e4m3_of(double x, double s, double inverse) {
   double q = x * inverse;
   const double left = __builtin_fma(-q, s, x);          // exact quotients come out exact
-  if (__builtin_fabs(q) < INFINITY) q = __builtin_fma(left, inverse, q);
+  if (__builtin_fabs(q) < INFINITY && q != 0.0) q = __builtin_fma(left, inverse, q);     // 0 and by an infinite s as it is
   const float f = round_to_odd(q);
   return f != f ? f : fminf(fmaxf(f, -448.0f), 448.0f);
 }

@@ -332,8 +332,9 @@ typedef struct {
 
 /*
  * out = x rotated, x [tokens][heads][dim] of KEOPS_TYPE_BF16, _F16 or _F32, token t's row at
- * x + t x_stride, its heads dense; out likewise, out_stride at least a row.  dim up to 65536, pairs
- * up to 8192, element-aligned; heads of whole aligned 16 bytes run fastest.  out may be x itself, with the same stride, and must not overlap it otherwise.
+ * x + t x_stride, its heads dense; out likewise, out_stride at least a row.  dim up to 65536,
+ * pairs up to 8192, element-aligned; heads of whole aligned 16 bytes run fastest.  out may be x
+ * itself, with the same stride, and must not overlap it otherwise.
  * inverse: the angles' signs turned, which with the same factor is the gradient: out = dL/dx for
  * x = dL/dout.  positions: [tokens] int32, of either sign.
  */
@@ -440,6 +441,7 @@ int keops_verify_draft_workspace(int32_t seqs, int32_t drafts, int32_t vocab, in
  * x % 32 of word x / 32, rows mask_stride apart.  Rows of no sequence stay as they were.
  * logits and out: [rows][vocab] of KEOPS_TYPE_BF16, _F16 or _F32, rows stride and out_stride
  * apart; out may be logits itself, with the same stride, and must not overlap it otherwise.
+ * vocab up to 2^30, text_width below that.
  */
 typedef struct {
   const int32_t *starts;          /* [seqs + 1]                                    */

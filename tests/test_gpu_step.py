@@ -314,6 +314,30 @@ def test_append_rotary_at_position_zero_is_the_append(cache):
             assert torch.equal(raw(p), raw(q))
 
 
+def test_append_rotary_extreme_scales():
+    """An e4m3 cache's quotients by infinite, zero, subnormal and huge scales are the append's."""
+    say("append rotary, extreme scales")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((40, 4, 64), generator=g, device="cuda").bfloat16() for _ in range(2))
+    k[3] = 0
+    scale = torch.tensor([float("inf"), 0.0, 2.0 ** -140, 3e38]).cuda()
+    table = torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3)
+    lens, starts = torch.tensor([40], dtype=torch.int32).cuda(), torch.tensor([0, 40], dtype=torch.int32).cuda()
+    held = []
+    for turn in (False, True):
+        kp, vp = (torch.zeros((3, 16, 4, 64), dtype=torch.uint8, device="cuda").view(E4) for _ in range(2))
+        if turn:
+            gm.keops_cache_append_rotary(k[:, :0], k, v, kp, vp, table, lens, starts, gm.keops_rotary_frequencies(64, device="cuda"),
+                                         positions=torch.zeros(40, dtype=torch.int32, device="cuda"), k_scale=scale, v_scale=scale)
+        else:
+            gm.keops_cache_append(k, v, kp, vp, table, lens, starts, k_scale=scale, v_scale=scale)
+        held.append((raw(kp), raw(vp)))
+    assert bool((held[0][0][:, :, 0] & 0x7f == 0).all())
+    for x, y in zip(*held):
+        none = (x & 0x7f == 0x7f) & (y & 0x7f == 0x7f)
+        assert bool((none | (x == y)).all())
+
+
 def test_append_4bit_every_16_bit_value():
     """Every bf16 and fp16 value, in blocks of one magnitude and in blocks of all: least powers, subnormals, infinities."""
     for dtype in (BF, FP):
@@ -767,6 +791,18 @@ def test_logits_non_finite():
     c["rep"] = torch.tensor([0.0])
     got = run_logits(put(z), c).cpu()
     assert got[0, 0] == float("inf") and got[0, 3] == float("inf") and bool(got[0, 1].isnan()) and got[0, 5] == -1.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_logits_infinite_repetition(dtype):
+    """Divided by an infinity, a positive logit is 0, a negative one goes to -inf, and 0 times it is none."""
+    say(f"logits, infinite repetition, {dtype}")
+    z = torch.tensor([[2.0, -2.0, 0.0, 1e-38, 5.0]]).to(dtype)
+    text = torch.tensor([[0, 1, 2, 3]], dtype=torch.int32)
+    c = dict(starts=torch.tensor([0, 1], dtype=torch.int32), text=text, lens=torch.tensor([4], dtype=torch.int32),
+             rep=torch.tensor([float("inf")]))
+    got = run_logits(put(z), c).cpu()
+    assert got[0, 0] == 0 and got[0, 1] == -float("inf") and bool(got[0, 2].isnan()) and got[0, 3] == 0 and got[0, 4] == 5
 
 
 def test_logits_follow_drafted_tokens():
