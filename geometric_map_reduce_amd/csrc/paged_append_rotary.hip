@@ -9,6 +9,11 @@
 // tokens' cosines and sines into LDS, in 64 bits, then each takes eight columns of a head at a time.  Queries and
 // 16-bit keys are turned in 32 bits.  Keys that go into 8 or 4 bits are turned in 64: at 2^-24 some of every
 // million would be decided wrongly at the borders between held values.
+//
+// Memory bounds a prompt: 16,384 tokens of 32 + 8 heads of 128 into 4 bits take 79 us (353 MB, 4.5 TB/s); cosines and
+// sines held in 32 bits for the queries as well changed nothing, the next items' loads ahead of this one's arithmetic
+// cost registers and 16 us.  1,200 tokens of nine sequences take 13 us, a chain: the sequence's number, its length, the
+// table's entry, then the angles, then three turns of loads; one token of 64 sequences 3.9 us.
 #include "step.h"
 
 namespace kmi {

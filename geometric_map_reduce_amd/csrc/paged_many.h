@@ -18,6 +18,8 @@
 //    tiles where some row does not see some slot look at them.
 //  * Running maximum, sums, absent slots, non-finite values and the rounding of p to 16 bits for the
 //    matrix product as in the few-rows form.
+//  * 4-bit caches: from 1,024 rows of a head on the slots are widened to 16 bits once, before (paged_read.hip), since
+//    each of the many work-groups of a head would do it again; fewer rows widen their tiles on the way to LDS.
 //  * Few rows and long caches: the slots are split over as many work-groups as the device holds at
 //    once, and a second kernel joins the parts.
 //

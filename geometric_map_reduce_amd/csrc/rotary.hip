@@ -11,7 +11,7 @@
 // into LDS (all heads share them), then go over the rows: a thread takes V pairs of a head at a time, two pieces
 // of V columns, which makes it safe to write where it read.  Bound by HBM where there are many tokens: 16,384 tokens of
 // 40 heads of 128 columns, 168 MB in and as many out, take 72.7 us (4.6 TB/s; a large copy reaches 4.8).
-// One token is one launch: 2.8 us on the GPU, of them the angles' 64-bit reduction and series about 1.
+// 16 tokens of them are one launch's latency: 2.8 us on the GPU.
 #include "step.h"
 
 namespace kmi {
