@@ -60,7 +60,7 @@ struct LogitArgs {
   const uint32_t *mask;
   int64_t mask_stride;
   int32_t seqs, text_width, biases;
-  FastDiv pieces_div;
+  float pieces_inverse;
   bool whole;                        // rows of logits and out start on 16 bytes
 };
 constexpr int kLogitThreads = 512;

@@ -229,7 +229,7 @@ int logits_entry(const void *logits, int64_t stride, int type, int64_t rows, int
   const int to = 16 / bytes;
   a.whole = aligned(logits, 16) && aligned(out, 16) && a.stride % to == 0 && a.out_stride % to == 0;
   a.piece = (double)rows * (double)ceil_div(vocab, kLogitPiece) >= 256.0 ? kLogitPiece : kLogitPiece / 2;
-  a.pieces_div = make_fastdiv((uint32_t)ceil_div(vocab, a.piece));
+  a.pieces_inverse = 1.0f / (float)ceil_div(vocab, a.piece);
   const double blocks = (double)rows * (double)ceil_div(vocab, a.piece);
   if (blocks > (double)kMaxGrid || !launchable(blocks, kLogitThreads)) return KEOPS_ERR_UNSUPPORTED;
   (void)hipGetLastError();

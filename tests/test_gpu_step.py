@@ -742,7 +742,8 @@ def check_logits(got, z, c, fill):
 
 
 @pytest.mark.parametrize("S,new,V,width,biases", [(1, 1, 1, 1, 1), (1, 1, 32, 5, 0), (1, 1, 33, 40, 3), (3, 4, 1000, 60, 7),
-                                                  (5, 2, 4099, 300, 40), (2, 3, 9001, 2500, 300), (70, 1, 257, 20, 2)])
+                                                  (5, 2, 4099, 300, 40), (2, 3, 9001, 2500, 300), (70, 1, 257, 20, 2),
+                                                  (1, 2, 900, 30, 700), (2, 2, 3500, 9000, 600)])
 @pytest.mark.parametrize("dtype", [BF, FP, F32])
 def test_logits(S, new, V, width, biases, dtype):
     say(f"logits {S} x {new} x {V}, text {width}, {biases} biases, {dtype}")
