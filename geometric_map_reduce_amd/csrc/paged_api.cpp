@@ -41,8 +41,8 @@ constexpr double kFarBytes = 384e6;
 // (32 rows) 462 in place of 604.  Up to half a GB is a five-hundredth of the device's memory, and always taken.
 constexpr double kScoresAlways = 512e6, kScoresMost = 4294967296.0;
 
-// Rows of a sequence's head from which on a 4-bit cache is widened to 16 bits before attention, not in each of its
-// work-groups.  16,384 slots of 8 x 128: 4,096 tokens of 4 rows a head 1,103 to 943 us, 512 tokens 182 to 167, 256
+// Rows of a sequence's head, by the bound and by the mean of the sequences, from which on a 4-bit cache is widened to 16
+// bits before attention, not in each of its work-groups.  16,384 slots of 8 x 128: 4,096 tokens of 4 rows a head 1,103 to 943 us, 512 tokens 182 to 167, 256
 // 110 to 107, 128 61 to 73; 8,192 slots of dim 256 and 2,048 tokens 769 to 606.  And what that may take: of memory, and
 // beside the pool, for the bounds may lie far above the lengths.
 constexpr int64_t kWidenRows = 1024;
@@ -116,7 +116,7 @@ int plan_attend(const keops_cache_t &c, int type, int64_t tokens, int heads, int
     // the join looks through all tokens' rows
     if (p->nsplit > 1 && !launchable((double)join_blocks(tokens * heads, c.dim, (int)p->nsplit), kJoinThreads)) p->nsplit = 1;
     p->grid = wgs * p->nsplit;
-    if (c.type == KEOPS_TYPE_E2M1 && rows >= kWidenRows) {
+    if (c.type == KEOPS_TYPE_E2M1 && rows >= kWidenRows && (double)tokens * (heads / c.heads) >= (double)kWidenRows * (double)S) {
       const int64_t width = std::min<int64_t>(ceil_div(max_len, c.page_size), c.table_width);
       const double slots = (double)S * (double)width * c.page_size, bytes = slots * (double)H * c.dim * 2.0;
       if (width > 0 && slots <= 2.0 * (double)c.pages * c.page_size && 2.0 * bytes <= kWidenMost) {

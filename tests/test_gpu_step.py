@@ -576,6 +576,17 @@ def test_far_pages():
     assert torch.equal(rv.cpu().double(), sref.from_4bit(*sref.to_4bit(nv, BF)))
 
 
+@pytest.mark.parametrize("lens,new", [([700, 60, 31], [300, 1, 2]), ([700, 600, 31], [300, 256, 2]), ([300, 1, 0, 290], [300, 1, 0, 290])])
+@pytest.mark.parametrize("weights", [False, True])
+def test_prompts_beside_single_tokens(lens, new, weights):
+    """Prompts whose caches are widened first, and ones that are not since most sequences have few rows."""
+    say(f"prompts beside single tokens {lens} {new} {weights}")
+    b = Batch4(57, lens, new, 8, 2, 64, 16)
+    if weights:
+        b.weights = torch.rand((b.P, 2, 16), generator=b.gen)
+    check_attention(b, 0.5)
+
+
 def test_widened_slots_do_not_see_what_was_left():
     """The workspace of a call that widens the cache first holds NaN of another one."""
     say("a workspace full of NaN")
