@@ -81,7 +81,8 @@ struct FewRows {
   uint32_t kp[2][kKPowers], vp[8][VPieces<D>::n];
 
   // e2m1: a tile's keys, values and powers pass through LDS of the wave's own.  Neighbouring lanes load neighbouring
-  // blocks of a slot (not a slot a lane, the operands' own order: four times the addresses to look up), the keys are read back as the A operand and the values as eight slots of a lane's columns.
+  // blocks of a slot (not a slot a lane, the operands' own order: four times the addresses to look up), the keys are
+  // read back as the A operand and the values as eight slots of a lane's columns.
   static constexpr int kBlocks = D / kPowerBlock, kLoads = E2M1 ? (32 * kBlocks + kWave - 1) / kWave : 1;
   static constexpr int kGroup = 36;                     // words of an 8-column group of V, a slot each and a pad: no two lanes' banks meet
   static constexpr int kStageV = 16 * D, kStageP = kStageV + D / 8 * kGroup * 4;

@@ -4,7 +4,8 @@ include/keops_mi355x.h, where the operators are defined).
 A cache is a pair of page pools ``k_pages``, ``v_pages`` of shape [pages, page_size, heads, dim]
 (any order of strides in the first three, the same for both), bfloat16, float16, float8_e4m3fn with
 ``k_scale``, ``v_scale`` [heads], or float4_e2m1fn_x2 (two values an element: [.., dim / 2]) with ``k_scale``,
-``v_scale`` [pages, heads, page_size, dim / 32] float8_e8m0fnu, a power of two for 32 columns; ``weights`` [pages, heads, page_size] float32 holds the
+``v_scale`` [pages, heads, page_size, dim / 32] float8_e8m0fnu, a power of two for 32 columns;
+``weights`` [pages, heads, page_size] float32 holds the
 attention that each slot received.  ``page_table`` [sequences, width], ``lens`` [sequences] and
 ``starts`` [sequences + 1] are int32 tensors on the same device; the calls read none of them on
 the host and never synchronise.
@@ -104,7 +105,8 @@ def _cache(k_pages, v_pages, weights, page_table, lens, k_scale, v_scale, scales
         raise ValueError("k_scale and v_scale belong to a float8_e4m3fn or float4_e2m1fn_x2 cache")
     # the stride of a dimension of one is never used
     c = _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), w, ks, vs, strides[0] * two if P > 1 else 0,
-                    strides[1] * two if ps > 1 else 0, strides[2] * two if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind, width, S)
+                    strides[1] * two if ps > 1 else 0, strides[2] * two if H > 1 else 0, P, table, table_stride, lens.data_ptr(), ps, H, D, kind,
+                    width, S)
     return c, dev, S, (H, D, dtype), ps, width
 
 
