@@ -849,6 +849,31 @@ def test_logits_streams_and_graph():
         assert torch.equal(got, eager)
 
 
+def test_rows_far_apart():
+    """Rows past 2^31 elements come out as the same rows by themselves."""
+    say("rotary, 2.2e9 elements")
+    T, H, D = 270000, 64, 128
+    g = torch.Generator(device="cuda").manual_seed(9)
+    freqs, at = gm.keops_rotary_frequencies(D, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+    x = torch.zeros((T, H, D), dtype=BF, device="cuda")
+    for end in (slice(0, 70), slice(T // 2, T // 2 + 70), slice(T - 70, T)):
+        x[end] = torch.randn((70, H, D), generator=g, device="cuda").to(BF)
+    y = gm.keops_rotary(x, at, freqs)
+    for end in (slice(0, 70), slice(T // 2, T // 2 + 70), slice(T - 70, T)):
+        assert torch.equal(y[end], gm.keops_rotary(x[end].clone(), at[end].clone(), freqs))
+    del x, y
+    say("logits, 2.6e9 entries")
+    T, V = 20000, 131072
+    z = torch.zeros((T, V), dtype=BF, device="cuda")
+    text = torch.tensor([[V - 1, 5, 5, 70000]], dtype=torch.int32, device="cuda").repeat(2, 1)
+    rules = dict(tokens=text, lens=torch.tensor([4, 4], dtype=torch.int32, device="cuda"), frequency=torch.ones(2, device="cuda"))
+    last = torch.randn((2, V), generator=g, device="cuda").to(BF)
+    z[T - 2:] = last
+    gm.keops_adjust_logits(z, torch.tensor([0, T - 2, T], dtype=torch.int32, device="cuda"), out=z, **rules)
+    want = gm.keops_adjust_logits(last, torch.tensor([0, 0, 2], dtype=torch.int32, device="cuda"), **rules)
+    assert torch.equal(z[T - 2:], want) and not torch.equal(want, last) and not bool(z[:T - 8].any())
+
+
 # ---- together
 
 @pytest.mark.parametrize("cache", [BF, E4, E2])
