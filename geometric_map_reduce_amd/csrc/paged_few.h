@@ -19,7 +19,8 @@
 //    sums and p stay below 2^8 times what they would be; sums are in 32 bits, of p as it is.  p is
 //    rounded to the cache's 16-bit type (8-bit caches: q's) for the product with V: the matrix
 //    instructions take two 16-bit operands, or two fp32 ones at a sixteenth of the rate.  The output's
-//    error against 64 bits goes from its own rounding's 0.0017 to 0.0022 by it (bf16).
+//    error against 64 bits goes from its own rounding's 0.0017 to 0.0022 by it (bf16); 4-bit caches of up to 16
+//    rows have the remainder of p multiplied as well.
 //  * HBM bounds it: 64 sequences of 5,120 slots (bf16, 16 rows a head) read 1.34 GB in 242 us, 5.6 TB/s
 //    with both passes; 131,071 slots of one sequence 5.4 TB/s and 5 us of the second pass.
 //  * 4-bit caches: a head's row is half a line or less, and a lane's piece of it is 4 or 8 bytes, so that loads as above
@@ -28,7 +29,7 @@
 //    tiles of a wave are on their way at a time.  Where the device is filled all the same, neighbouring heads whose
 //    rows make up a 128-byte line go to the same work-group, whose waves load whole lines for each other; all heads of
 //    the same slots run on one XCD, whose L2 then holds the lines of the powers that they share.  64 sequences of up
-//    to 8,192 slots with 4 drafts (8 heads of 128): 129 us without, 85 so; 131,071 slots of one sequence 56 and 44.
+//    to 8,192 slots with 4 drafts (8 heads of 128): 129 us without, 85 so, 90 with p in two parts; 131,071 slots of one sequence 56 and 44.
 //  * Slots that no row may see (past the length, of a page that the table lacks) get a zero V.
 //    Slots that some rows see and others do not are only in the tiles of the new tokens and at
 //    the window's edge; if such a tile holds an infinity or NaN in V, it is added after the
@@ -398,6 +399,11 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   using F = FewRows<T, BITS, D, NR>;
   constexpr bool E4M3 = BITS == 8, E2M1 = BITS == 4;
   constexpr int kRows = 16 * NR;
+  // 4-bit caches of up to 16 rows: p's rounding to 16 bits is multiplied with V too, so that of a row that few slots
+  // decide no more is lost than the output's rounding (0.0017 of 64 bits in bf16, else 0.0023; up to half as much again
+  // as that in single rows).  The products are there to be had: one token 1 to 3 % of the time, 16 rows 9.  32 rows
+  // would take 14; the other caches' results are as they were.
+  constexpr bool kBoth = E2M1 && NR == 1;
   constexpr int kHalfRows = NW / 2 * kRows;     // half the waves' rows
   // e2m1: heads that go together have two tiles in LDS in turn, so that one barrier a tile will do
   constexpr int kSets = E2M1 && !SCORES && NW == 4 && D < 256 ? 2 : 1;
@@ -602,7 +608,7 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
             if (!(own & (1u << ((i >> 2) * 16 + (i & 3))))) sc[nr][i >> 2][i & 3] = -INFINITY;
         }
       }
-      u32x4 pf[NR];
+      u32x4 pf[NR], pr;          // p, and what its rounding left
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         float z[8], top = -INFINITY;
@@ -638,6 +644,11 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
         l_run[nr] += sum;
 #pragma unroll
         for (int u = 0; u < 4; ++u) pf[nr][u] = T::pack(p[2 * u], p[2 * u + 1]);
+        if constexpr (kBoth) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            pr[u] = T::pack(p[2 * u] - T::lo(pf[nr][u]), p[2 * u + 1] - T::hi(pf[nr][u]));
+        }
       }
       if constexpr (E2M1) f.take_staged(stage);
       if (masked) {
@@ -680,6 +691,10 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
           for (int nr = 0; nr < NR; ++nr) {
             acc[nr][t] = T::mfma16(x, pf[nr], acc[nr][t]);
             acc[nr][t + 1] = T::mfma16(y, pf[nr], acc[nr][t + 1]);
+            if constexpr (kBoth) {
+              acc[nr][t] = T::mfma16(x, pr, acc[nr][t]);
+              acc[nr][t + 1] = T::mfma16(y, pr, acc[nr][t + 1]);
+            }
           }
         }
       if constexpr (!E2M1) f.template load_v<FAR>(vbase, sh.off, next);

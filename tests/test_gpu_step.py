@@ -576,6 +576,39 @@ def test_far_pages():
     assert torch.equal(rv.cpu().double(), sref.from_4bit(*sref.to_4bit(nv, BF)))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("new,weights", [(1, False), (1, True), (4, False)])
+def test_few_rows_lose_no_more_than_the_outputs_rounding(dim, dtype, new, weights):
+    """Up to 16 rows: what is left of p's rounding is multiplied with V too.
+
+    p as two parts is off by half * half of itself.  A score is off by (dim + 8) 2^-24 of the sum of its products' magnitudes
+    (additions in 32 bits), which p is off by relatively, numerator and sum alike; exp2 and the sums of n terms add
+    (n + 8) 2^-24 each.  That times sum p |v| / sum p, and the output's own rounding."""
+    say(f"few rows over 4 bits, {dim} {dtype} {new} {weights}")
+    b = Batch4(61, [5, 40, 300, 1900], [new] * 4, 8, 2, dim, 16, dtype, junk=0.0)
+    if weights:
+        b.weights = torch.zeros((b.P, 2, 16))
+    out = run_attention(b)[0].double()
+    k, v, ks, vs = pools(b)
+    whole = torch.tensor([0] + b.lens, dtype=torch.int32).cumsum(0).int()
+    K, V = (t.double().cpu() for t in gm.keops_cache_read(k, v, put(b.table), put(b.lens_t()), whole.cuda(), int(whole[-1]), dtype=dtype,
+                                                          k_scale=ks, v_scale=vs))
+    half, scale = torch.finfo(dtype).eps / 2, dim ** -0.5 if b.scale is None else b.scale
+    for s, n in enumerate(b.lens):
+        a, e, at = int(b.starts[s]), int(b.starts[s + 1]), int(whole[s])
+        for h in range(8):
+            q, kk, vv = b.q[a:e, h].double(), K[at:at + n, h // 4], V[at:at + n, h // 4]
+            z = q @ kk.T * scale
+            off = ((q.abs() @ kk.abs().T) * abs(scale)).amax(1) * (dim + 8) * 2.0 ** -24
+            z.masked_fill_(torch.arange(n) > torch.arange(n - (e - a), n)[:, None], -float("inf"))
+            p = torch.softmax(z, -1)
+            o = p @ vv
+            near = (half * half + 2 * off + 2 * (n + 8) * 2.0 ** -24)[:, None] * (p @ vv.abs())
+            floor = 2.0 ** -25 if dtype is FP else 0.0
+            close(out[a:e, h], o, o.abs() * half + near * (1 + half) + floor, "out")
+
+
 @pytest.mark.parametrize("lens,new", [([700, 60, 31], [300, 1, 2]), ([700, 600, 31], [300, 256, 2]), ([300, 1, 0, 290], [300, 1, 0, 290])])
 @pytest.mark.parametrize("weights", [False, True])
 def test_prompts_beside_single_tokens(lens, new, weights):
