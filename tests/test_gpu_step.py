@@ -493,6 +493,71 @@ def test_hidden_values_reach_no_row(dim, new, dtype, kv, max_len):
                 close(out[t, h, rest], o[t, h, rest], ot[t, h, rest], f"row {t}")
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("new,group,weights", [(1, 1, False), (1, 4, True), (4, 4, False), (3, 5, True), (6, 4, False), (40, 4, True), (260, 4, False)])
+@pytest.mark.parametrize("max_len", [None, 30000])
+def test_infinite_values_that_every_row_sees(dim, dtype, new, group, weights, max_len):
+    """Blocks of NaN and past the type's largest number in slots that every row sees, of a tile in the middle, of the last
+    one and of the first new token: the columns with them are what the formula gives, the others are as close as ever."""
+    say(f"infinite blocks, dim {dim}, {new} new, group {group}, {dtype}, weights {weights}, bound {max_len}")
+    kv, n = (4 if dim < 256 else 2), 200 + new
+    b = Batch4(19 + dim, [n], [new], kv * group, kv, dim, 16, dtype)
+    b.q = (b.q / 4).to(dtype)                                # every weight is far above what 16 bits end at
+    if weights:
+        b.weights = torch.rand((b.P, kv, 16), generator=b.gen)
+    top = 254 if dtype == BF else 142                        # 6 under it is infinite
+    for i, j in enumerate((5, 100, 200)):                    # 200: the first new token's own
+        pg, row = b.table[0, j // 16].item(), j % 16
+        for h in range(1, kv):
+            b.v_scale[pg, h, row, 1] = top
+            b.v[pg, row, h, 16:32] = 0
+            b.v[pg, row, h, 20] = (0x07, 0x70, 0xf7)[i]      # column 40: +, 0, +; column 41: 0, +, -
+            b.v[pg, row, h, 24] = (0x7f, 0x00, 0x00)[i]      # column 48: -; 49: +
+    pg, row = b.table[0, 33 // 16].item(), 33 % 16
+    b.v_scale[pg, 0, row, 0] = 255
+    out, lse, w = run_attention(b, max_len=max_len)
+    o, z, ww, ot, zt, wt = ref.attention(b)
+    close(lse, z, zt, "lse")
+    if weights:
+        close(w, ww, wt, "weights")
+    inf = float("inf")
+    for h in range(kv):
+        got, want, tol = (x[:, h * group:(h + 1) * group] for x in (out, o, ot))
+        odd = list(range(32)) if h == 0 else [40, 41, 48, 49]
+        rest = [c for c in range(dim) if c not in odd]
+        assert bool(got[..., rest].isfinite().all()), h
+        close(got[..., rest], want[..., rest], tol[..., rest], f"head {h}")
+        if h == 0:
+            assert bool(got[..., odd].isnan().all())
+        else:
+            assert bool((got[..., 40] == inf).all()) and bool(got[..., 41].isnan().all()), (h, got[0, 0, odd])
+            assert bool((got[..., 48] == -inf).all()) and bool((got[..., 49] == inf).all()), (h, got[0, 0, odd])
+
+
+@pytest.mark.parametrize("new,heads", [(1, 2), (3, 8), (20, 2), (40, 2), (260, 8)])
+def test_fp16_rows_over_what_bf16_rows_held(new, heads):
+    """A value past fp16's largest number that bf16 rows left in a 4-bit cache is an infinity to fp16 rows."""
+    say(f"fp16 rows over a cache of bf16 rows, {new} new, {heads} heads")
+    n = 300 + new
+    b, _ = append_batch([n], [n], heads, 2, 64, 16, BF, E2)
+    k, v, ks, vs = pools(b)
+    rows = torch.randn((n, 2, 64), generator=b.gen).to(BF)
+    rows[:, 1, 32:] = 0                                      # under the power of 10^5, other values are 0 or infinite too
+    rows[7, 1, 37], rows[150, 1, 50], rows[300, 1, 63] = 1e5, -1e5, 1e5
+    args = (put(b.table), put(b.lens_t()))
+    keys = torch.randn((n, 2, 64), generator=b.gen).to(BF)
+    gm.keops_cache_append(put(keys), put(rows), k, v, *args, put(b.starts), k_scale=ks, v_scale=vs)
+    q = (torch.randn((new, heads, 64), generator=b.gen) / 2).half()
+    starts = torch.tensor([0, new], dtype=torch.int32).cuda()
+    out = gm.keops_paged_attention(put(q), k, v, *args, starts, new, n, k_scale=ks, v_scale=vs)[0].cpu()
+    inf, group = float("inf"), heads // 2
+    want = torch.zeros(32)
+    want[37 - 32], want[50 - 32], want[63 - 32] = inf, -inf, inf
+    assert bool(out[:, :group].isfinite().all()) and bool(out[:, group:, :32].isfinite().all())
+    assert torch.equal(out[:, group:, 32:].float(), want.expand(new, group, 32))
+
+
 @pytest.mark.parametrize("new,heads", [(2, 8), (30, 8), (40, 64)])
 def test_absent_pages(new, heads):
     say(f"absent pages in 4 bits, {new} new, {heads} heads")
