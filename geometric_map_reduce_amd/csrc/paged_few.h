@@ -744,6 +744,8 @@ __global__ __launch_bounds__(NW * kWave, NW > 4 ? 2 : (D * NR > 128 || (SCORES &
   __syncthreads();
   if (SCORES && c1 > c0) flush(c0 + (c1 - c0 - 1) / block * block, (c1 - c0 - 1) % block + 1);
   if (odd) sh_odd = 1;
+  // other lanes read it: the hand-over's barriers come in between, unless each wave has a head of its own
+  if (E2M1 && wph == 1) __syncthreads();
   // the waves' sums: the upper half hands its to the lower, and again
 #pragma unroll
   for (int nr = 0; nr < NR; ++nr) l_run[nr] = xor_sum(l_run[nr]);

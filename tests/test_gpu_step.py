@@ -558,6 +558,27 @@ def test_fp16_rows_over_what_bf16_rows_held(new, heads):
     assert torch.equal(out[:, group:, 32:].float(), want.expand(new, group, 32))
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (64, FP), (96, BF), (96, FP)])
+@pytest.mark.parametrize("group", [1, 4, 6])
+def test_hidden_infinities_of_heads_that_go_together(dim, dtype, group):
+    """A work-group's four waves have a head each (their bounds fill the device): an infinity in the last slot of one head
+    reaches that head's last row, all its lanes, and nothing else."""
+    say(f"hidden infinities, four heads together, dim {dim}, group {group}, {dtype}")
+    new, kv = 3, 8
+    for first in (0, 2, 7):
+        b = Batch4(29, [300], [new], group * kv, kv, dim, 16, dtype)
+        pg, row = b.table[0, 299 // 16].item(), 299 % 16
+        b.v_scale[pg, first, row] = 254 if dtype == BF else 142
+        b.v[pg, row, first] = 0x77                           # 6 under that, in every column
+        out, lse, _ = run_attention(b, max_len=30000)
+        o, z, _, ot, zt, _ = ref.attention(b)
+        close(lse, z, zt, "lse")
+        there = torch.zeros((new, group * kv), dtype=torch.bool)
+        there[-1, first * group:(first + 1) * group] = True
+        assert bool((out[there] == float("inf")).all()) and bool(out[~there].isfinite().all())
+        close(out[~there], o[~there], ot[~there], "rows without it")
+
+
 @pytest.mark.parametrize("new,heads", [(2, 8), (30, 8), (40, 64)])
 def test_absent_pages(new, heads):
     say(f"absent pages in 4 bits, {new} new, {heads} heads")
