@@ -579,6 +579,28 @@ def test_hidden_infinities_of_heads_that_go_together(dim, dtype, group):
         close(out[~there], o[~there], ot[~there], "rows without it")
 
 
+@pytest.mark.parametrize("cache,dim,rows,least", [(E4, 64, 16, 4), (E4, 64, 32, 2), (E4, 96, 16, 3), (E4, 96, 32, 2), (E4, 128, 16, 3), (E4, 128, 32, 2),
+                                                  (E4, 256, 16, 1), (E4, 256, 32, 1), (BF, 64, 16, 3), (BF, 64, 32, 2), (BF, 96, 16, 2),
+                                                  (BF, 96, 32, 2), (BF, 128, 16, 2), (BF, 128, 32, 1), (BF, 256, 16, 1), (BF, 256, 32, 1)])
+def test_work_groups_of_a_compute_unit(cache, dim, rows, least):
+    """As many work-groups of few-rows attention share a compute unit as did before there were 4-bit caches: seen from the
+    workspace, which has two parts of 16 or 32 rows, their sums and their maxima, for each of them."""
+    import ctypes
+    from geometric_map_reduce_amd import paged
+    say(f"work-groups of a compute unit, {cache}, {dim}, {rows} rows")
+    S, n = 64, 1 << 17
+    k = torch.zeros((8, 16, 8, dim), dtype=torch.uint8 if cache == E4 else cache, device="cuda")
+    k = k.view(E4) if cache == E4 else k
+    scale = torch.ones(8, device="cuda") if cache == E4 else None
+    table, lens = torch.zeros((S, n // 16), dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    c = paged._cache(k, k, None, table, lens, scale, scale)[0]
+    need = ctypes.c_int64(0)
+    assert gm.lib().keops_paged_attention_workspace(c, 0, 8 * rows, S, 1, n, 0, ctypes.byref(need)) == 0
+    groups = (need.value - 512) / (2 * rows * (dim * 4 + 8))
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert groups / cus > least - 0.01, (groups, cus)
+
+
 @pytest.mark.parametrize("new,heads", [(2, 8), (30, 8), (40, 64)])
 def test_absent_pages(new, heads):
     say(f"absent pages in 4 bits, {new} new, {heads} heads")
