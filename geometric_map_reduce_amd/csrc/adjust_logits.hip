@@ -26,20 +26,27 @@ constexpr int kStrip = 512;                  // a wave's entries at a time
 constexpr int kListed = 256;                 // biases of a piece that are held in LDS
 
 template <class T> struct Logit;
+// put: rounded once, from 64 bits.
 template <> struct Logit<Bf16> {
   typedef uint16_t E;
   static __device__ __forceinline__ float get(E x) { return __uint_as_float((uint32_t)x << 16); }
-  static __device__ __forceinline__ E put(float x) { return (E)Bf16::pack(x, x); }
+  static __device__ __forceinline__ E put(double x) {
+    const float f = round_to_odd(x);
+    return (E)Bf16::pack(f, f);
+  }
 };
 template <> struct Logit<F16> {
   typedef uint16_t E;
   static __device__ __forceinline__ float get(E x) { return (float)__builtin_bit_cast(_Float16, x); }
-  static __device__ __forceinline__ E put(float x) { return (E)F16::pack(x, x); }
+  static __device__ __forceinline__ E put(double x) {
+    const float f = round_to_odd(x);
+    return (E)F16::pack(f, f);
+  }
 };
 template <> struct Logit<float> {
   typedef float E;
   static __device__ __forceinline__ float get(E x) { return x; }
-  static __device__ __forceinline__ E put(float x) { return x; }
+  static __device__ __forceinline__ E put(double x) { return (float)x; }
 };
 
 // A thread's entries.  Entry k, in a register that is not known beforehand, by selection.
@@ -230,10 +237,10 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
     double z = w & (kInPrompt | kMade) ? l > 0.0 ? q : l * rep : l;
     z = made ? z - (freq * (double)made + pres) : z;
     if (w & kBiased) z += bias_of(x);
-    return Logit<T>::put((float)z);
+    return Logit<T>::put(z);
   };
   // the piece, masked
-  const uint32_t none = sizeof(E) == 4 ? __float_as_uint(-INFINITY) : (uint32_t)Logit<T>::put(-INFINITY) * 0x10001u;
+  const uint32_t none = sizeof(E) == 4 ? __float_as_uint(-INFINITY) : (uint32_t)Logit<T>::put(-(double)INFINITY) * 0x10001u;
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     const int64_t x0 = start(c);

@@ -958,6 +958,44 @@ def test_logits_infinite_repetition(dtype):
     assert got[0, 0] == 0 and got[0, 1] == -float("inf") and bool(got[0, 2].isnan()) and got[0, 3] == 0 and got[0, 4] == 5
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("rule", ["frequency", "presence", "repetition", "bias"])
+def test_logits_are_rounded_once(dtype, rule):
+    """Results just beside a tie of the 16-bit type, nearer to it than 32 bits can tell: to the nearer neighbour."""
+    say(f"logits next to ties, {dtype}, {rule}")
+    V, base = 64, 256.0 if dtype == BF else 2048.0           # base: numbers are 2 apart from there on
+    steps = torch.arange(32, dtype=torch.float64) * 2
+    for side in (1, -1):
+        add = torch.tensor(1.0 + side * 2.0 ** -20)
+        z = torch.zeros((1, V), dtype=dtype)
+        z[0, :32] = (base + steps).to(dtype)
+        want = base + steps + (2 if side > 0 else 0)
+        c = dict(starts=torch.tensor([0, 1], dtype=torch.int32))
+        text = torch.arange(32, dtype=torch.int32)[None]
+        if rule == "bias":
+            c.update(ids=text, bias=add.expand(1, 32).contiguous())
+        elif rule == "repetition":
+            # 2 / r is above or below a tie of the type, 1 + half a step: r the next 32-bit number to 2 / that
+            half = torch.finfo(dtype).eps / 2
+            r = torch.tensor(2.0 / (1 + half), dtype=torch.float64).float()
+            while (2.0 / r.double() > 1 + half) != (side > 0):
+                r = torch.nextafter(r, torch.tensor(0.0 if side > 0 else 9.0))
+            z[0, :32] = 2.0
+            want = torch.full((32,), 1 + 2 * half if side > 0 else 1.0, dtype=torch.float64)
+            c.update(text=text, lens=torch.tensor([32], dtype=torch.int32), rep=r[None])
+        else:
+            c.update(text=text, lens=torch.tensor([32], dtype=torch.int32), **{"pres" if rule == "presence" else "freq": -add[None]})
+        step = 2 * half if rule == "repetition" else 2.0
+        assert bool(((sref.logits(z, **c)[0, :32] - want).abs() < step / 2).all())         # the nearest number of the type
+        for rows in (1, 300):                                # a work-group's piece is of either size
+            if rows > 1:
+                c["starts"] = torch.tensor([0, rows], dtype=torch.int32)
+                if "lens" in c:
+                    c["lens"] = torch.tensor([31 + rows], dtype=torch.int32)
+            got = run_logits(put(z.expand(rows, V).contiguous()), c).cpu()
+            assert torch.equal(got[0, :32].double(), want), (side, rows, got[0, :32], want)
+
+
 def test_logits_follow_drafted_tokens():
     """Each of a sequence's rows has seen one token more; starts past the rows are cut, lens past the text too."""
     say("logits of drafted tokens")
