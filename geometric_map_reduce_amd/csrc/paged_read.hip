@@ -18,12 +18,14 @@ __device__ __forceinline__ u32x4 held8(const char *at, float scale, const uint8_
   if (BITS == 16) return *(const u32x4 *)at;
   if (BITS == 4) return widen_e2m1<T>(*(const uint32_t *)at, *power);
   const u32x2 w = *(const u32x2 *)at;
+  // the product has up to 28 bits: 32 bits with an odd last place where it is not one of theirs
+  const double by = (double)scale;
   u32x4 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-    r[2 * i] = T::pack(a.x * scale, a.y * scale);
-    r[2 * i + 1] = T::pack(b.x * scale, b.y * scale);
+    r[2 * i] = T::pack(round_to_odd(a.x * by), round_to_odd(a.y * by));
+    r[2 * i + 1] = T::pack(round_to_odd(b.x * by), round_to_odd(b.y * by));
   }
   return r;
 }

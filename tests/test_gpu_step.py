@@ -658,6 +658,49 @@ def test_strides(new):
                 assert torch.equal(got[t].cpu().double(), sref.from_4bit(p[pg, row], s[pg, :, row]))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_read_of_8_bits_is_rounded_once(dtype):
+    """An e4m3 value times its scale has up to 28 bits: where these lie just beside a tie of the 16-bit type, 32 bits have
+    only the tie.  Every value, under scales that put some of them there."""
+    say(f"reading 8 bits, next to ties, {dtype}")
+    import math
+    from fractions import Fraction
+    codes = [c for c in range(256) if c & 0x7f != 0x7f]
+    value = torch.tensor(codes, dtype=torch.uint8).view(E4).double().tolist()
+    place = torch.finfo(dtype).eps / 2                       # of a tie, beside 1
+    near = []
+    for m in (9, 11, 13, 15):                                # odd parts of e4m3 values
+        for i in range(8):
+            tie = Fraction(1) + Fraction(2 * i + 1) * Fraction(place)
+            s = float(torch.tensor(float(tie * 8 / m), dtype=torch.float64).float())
+            for _ in range(40):
+                x = Fraction(s) * m / 8
+                s2 = float(torch.tensor(float(x), dtype=torch.float64).float())
+                if x != tie and Fraction(s2) == tie:
+                    near.append(s)
+                    break
+                s = float(torch.nextafter(torch.tensor(s, dtype=torch.float32), torch.tensor(0.0)))
+    assert len(near) >= 4, near
+    H = len(near)
+    k = torch.zeros((16, 16, H, 64), dtype=torch.uint8)
+    k[:] = torch.tensor(codes + [0, 0], dtype=torch.uint8).repeat(16 * 16 * 64 // 256).view(16, 16, 1, 64)
+    scale = torch.tensor(near, dtype=torch.float32)
+    table = torch.arange(16, dtype=torch.int32)[None]
+    n = torch.tensor([256], dtype=torch.int32)
+    starts = torch.tensor([0, 256], dtype=torch.int32)
+    got = gm.keops_cache_read(put(k).view(E4), put(k).view(E4), put(table), put(n), put(starts), 256, dtype=dtype, k_scale=put(scale),
+                              v_scale=put(scale))
+    bits = 1 - int(math.log2(torch.finfo(dtype).eps))        # of a number of the type
+    low = -24 if dtype == FP else -133                       # the smallest one's power
+    for h in range(H):
+        for i, x in enumerate(value):
+            want = Fraction(x) * Fraction(float(scale[h]))
+            step = Fraction(2) ** max(math.frexp(float(want))[1] - bits, low)
+            nearest = float(round(want / step) * step)       # a tie goes to the even one
+            for t in got:
+                assert t[i // 64, h, i % 64].item() == nearest, (h, x, float(scale[h]), float(want))
+
+
 def test_far_pages():
     """Byte offsets past 2^32 in the pool, and numbers of slots and heads past 2^31."""
     say("far pages of a 4-bit cache")
