@@ -178,8 +178,8 @@ bool has_work(const keops_cache_t &c, int64_t tokens, int max_q) {
 }
 
 // The caller's workspace, or the library's; the library's is never recorded into a graph,
-// whose replays could outlive it.
-int take_workspace(Workspace &own, void *given, int64_t given_bytes, int64_t need, hipStream_t st, char **ptr) {
+// whose replays could outlive it.  short_of: where to note that the device has no such memory.
+int take_workspace(Workspace &own, void *given, int64_t given_bytes, int64_t need, hipStream_t st, char **ptr, bool *short_of = nullptr) {
   *ptr = nullptr;
   if (need == 0) return KEOPS_OK;
   if (given) {
@@ -193,7 +193,10 @@ int take_workspace(Workspace &own, void *given, int64_t given_bytes, int64_t nee
     return KEOPS_ERR_HIP;
   }
   if (cap != hipStreamCaptureStatusNone) return KEOPS_ERR_ALLOC;
-  if (int rc = own.acquire(st, 0, (size_t)need)) return rc;
+  if (int rc = own.acquire(st, 0, (size_t)need)) {
+    if (short_of) *short_of = rc == KEOPS_ERR_ALLOC;
+    return rc;
+  }
   *ptr = own.ptr();
   return KEOPS_OK;
 }
@@ -261,7 +264,13 @@ int attend_entry(const keops_cache_t *c, const void *q, int64_t q_stride, int ty
   if (int rc = plan_attend(*c, type, tokens, heads, max_q, max_len, window, cus, &p)) return rc;
   Workspace own;
   char *ws = nullptr;
-  if (int rc = take_workspace(own, workspace, workspace_bytes, p.total(), st, &ws)) return rc;
+  bool short_of = false;
+  if (int rc = take_workspace(own, workspace, workspace_bytes, p.total(), st, &ws, &short_of)) {
+    // a 4-bit cache is for those who are short of memory: its slots need not be widened first
+    if (!short_of || !p.wide_width) return rc;
+    p.wide_width = p.wide_bytes = p.wide_table = 0;
+    if ((rc = take_workspace(own, workspace, workspace_bytes, p.total(), st, &ws))) return rc;
+  }
 
   AttendArgs a{};
   a.c = view_of(*c);

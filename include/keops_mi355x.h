@@ -379,7 +379,8 @@ int keops_cache_read(const keops_cache_t *cache, void *k, void *v, int64_t k_str
  * workspace: NULL for the library's (see "Ownership" above), or a 256-byte aligned device
  * buffer of at least keops_paged_attention_workspace bytes (KEOPS_ERR_SCRATCH if smaller).
  * Under stream capture a call that needs workspace must bring its own (KEOPS_ERR_ALLOC
- * otherwise), which has to live as long as the graph.
+ * otherwise), which has to live as long as the graph.  Prompts over an E2M1 cache take up to 4 GB
+ * to hold its slots in 16 bits; where the library cannot allocate that, they do without, slower.
  */
 int keops_paged_attention(const keops_cache_t *cache, const void *q, int64_t q_stride, int32_t type, int32_t heads,
                           const int32_t *starts, int64_t tokens, int32_t max_q, int32_t max_len, float scale,
@@ -489,7 +490,8 @@ const char *keops_status_string(int status);
  *                          frees the cached buffers no call holds
  *   KEOPS_OPT_FAIL_ALLOC -- test switch: 1 = every workspace allocation fails,
  *                          so that a call needing workspace returns
- *                          KEOPS_ERR_ALLOC with nothing enqueued
+ *                          KEOPS_ERR_ALLOC with nothing enqueued (or takes a
+ *                          form without workspace, if it has one)
  * Returns KEOPS_OK, or KEOPS_ERR_INVALID_ARG for an unknown option or value.
  */
 #define KEOPS_OPT_SPLIT_J 1

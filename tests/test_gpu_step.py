@@ -701,6 +701,34 @@ def test_read_of_8_bits_is_rounded_once(dtype):
                 assert t[i // 64, h, i % 64].item() == nearest, (h, x, float(scale[h]), float(want))
 
 
+@pytest.mark.parametrize("lens,new,heads,kv,dim,dtype,window", [([400], [130], 8, 1, 128, BF, 0), ([500, 90, 0, 70], [270, 90, 0, 1], 8, 2, 64, FP, 0),
+                                                               ([300, 290], [140, 140], 8, 1, 96, BF, 50), ([290], [260], 8, 2, 256, FP, 130)])
+def test_attention_without_memory_to_widen(lens, new, heads, kv, dim, dtype, window):
+    """Where there is no memory for the slots in 16 bits, prompts over a 4-bit cache are attended without."""
+    say(f"no memory to widen, {lens} {new} {heads}/{kv} x {dim} {dtype} window {window}")
+    b = Batch4(sum(lens) + dim, lens, new, heads, kv, dim, 24, dtype)
+    b.window = window
+    check_attention(b)
+    gm.keops_set_option(gm.KEOPS_OPT_FAIL_ALLOC, 1)
+    try:
+        check_attention(b)
+    finally:
+        gm.keops_set_option(gm.KEOPS_OPT_FAIL_ALLOC, 0)
+    # a call whose form without it needs workspace too has none: nothing is enqueued
+    b = Batch4(7, [1300], [130], 8, 1, 64, 24, BF)
+    k, v, ks, vs = pools(b)
+    out, lse = torch.full((130, 8, 64), 3.0, dtype=BF, device="cuda"), torch.full((130, 8), 3.0, device="cuda")
+    gm.keops_set_option(gm.KEOPS_OPT_FAIL_ALLOC, 1)
+    try:
+        with pytest.raises(gm.KeopsError) as e:
+            gm.keops_paged_attention(put(b.q), k, v, put(b.table), put(b.lens_t()), put(b.starts), 130, 1300, k_scale=ks, v_scale=vs, out=out, lse=lse)
+        assert e.value.status == -3
+    finally:
+        gm.keops_set_option(gm.KEOPS_OPT_FAIL_ALLOC, 0)
+    torch.cuda.synchronize()
+    assert bool((out == 3).all()) and bool((lse == 3).all())
+
+
 def test_far_pages():
     """Byte offsets past 2^32 in the pool, and numbers of slots and heads past 2^31."""
     say("far pages of a 4-bit cache")
