@@ -202,7 +202,8 @@ int logits_entry(const void *logits, int64_t stride, int type, int64_t rows, int
     for (const auto &in : inputs)
       if (in.p && overlaps(out, ob, in.p, in.bytes)) return KEOPS_ERR_INVALID_ARG;
   }
-  if (rows > 0x7fffffff || vocab > 1 << 30 || r->text_width >= 1 << 30) return KEOPS_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffff || vocab > 1 << 30 || r->text_width >= 1 << 30 || r->biases > 1 << 30)
+    return KEOPS_ERR_UNSUPPORTED;
   if (rows == 0 || r->seqs == 0) return KEOPS_OK;
   LogitArgs a{};
   a.logits = logits;

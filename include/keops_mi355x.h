@@ -442,7 +442,7 @@ int keops_verify_draft_workspace(int32_t seqs, int32_t drafts, int32_t vocab, in
  * x % 32 of word x / 32, rows mask_stride apart.  Rows of no sequence stay as they were.
  * logits and out: [rows][vocab] of KEOPS_TYPE_BF16, _F16 or _F32, rows stride and out_stride
  * apart; out may be logits itself, with the same stride, and must not overlap it otherwise.
- * vocab up to 2^30, text_width below that.
+ * vocab and biases up to 2^30, text_width below that.
  */
 typedef struct {
   const int32_t *starts;          /* [seqs + 1]                                    */

@@ -182,6 +182,13 @@ def call_logits(L, r, z=0x400000000, stride=100, type=3, rows=5, vocab=100, out=
     return L.keops_adjust_logits(z, stride, type, rows, vocab, None if r is None else ctypes.addressof(r), out, os, None)
 
 
+def test_long_lists_of_biases_are_refused(L):
+    """Past 2^30 entries a thread's place in the list, half a thousand further each turn, could pass 31 bits."""
+    far = dict(bias_tokens=1 << 45, bias=1 << 46, seqs=1)
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        assert call_logits(L, rules(biases=n, **far)) == -2
+
+
 def test_logits_refusals(L):
     assert call_logits(L, None) == -1
     for kw in (dict(starts=None), dict(lens=None), dict(bias=None), dict(bias_tokens=None), dict(seqs=-1), dict(text_width=-1), dict(biases=-1),
