@@ -23,7 +23,10 @@ namespace {
 constexpr uint32_t kInPrompt = 0x80000000u, kBiased = 0x40000000u, kMade = 0x3fffffffu;
 constexpr int kChunk = 8;                    // entries of a thread at a time
 constexpr int kStrip = 512;                  // a wave's entries at a time
-constexpr int kListed = 256;                 // biases of a piece that are held in LDS
+// Lists of up to so many biases have those of the piece in LDS, to be looked through for each entry that one names: one
+// row of 32,000 entries takes 5 us with 16 biases, 11 with 256.  Longer ones have for each entry of the piece its last place
+// in the list, in as much LDS as the counts take: 6 us with 300, 10 with 10,000, where looking through the list took 5.9 ms.
+constexpr int kListed = 256;
 
 template <class T> struct Logit;
 // put: rounded once, from 64 bits.
@@ -79,8 +82,8 @@ union Held {
   }
 };
 
-// CHUNKS: of a row's piece for each thread.
-template <class T, int CHUNKS>
+// CHUNKS: of a row's piece for each thread.  LONG: lists of more than kListed biases.
+template <class T, int CHUNKS, bool LONG>
 __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
   typedef typename Logit<T>::E E;
   constexpr int kWords = kChunk * sizeof(E) / 16, kPiece = CHUNKS * kChunk * kLogitThreads;
@@ -88,6 +91,7 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
   __shared__ __align__(16) int listed_token[kListed];
   __shared__ int listed_at[kListed], listed;
   __shared__ float listed_bias[kListed];
+  __shared__ __align__(16) uint32_t named[LONG ? kPiece : 4];          // an entry's last place in the list and 1
   __shared__ double shared_inverse;
   const int tid = threadIdx.x;
   const int pieces = (a.vocab + kPiece - 1) / kPiece;
@@ -169,7 +173,10 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
       const int64_t n = len - (end - t) + 1;
       m = (int)(n < 0 ? 0 : n < a.text_width ? n : a.text_width);
     }
-    for (int i = tid * 4; i < kPiece; i += kLogitThreads * 4) *(u32x4 *)(table + i) = (u32x4){0, 0, 0, 0};
+    for (int i = tid * 4; i < kPiece; i += kLogitThreads * 4) {
+      *(u32x4 *)(table + i) = (u32x4){0, 0, 0, 0};
+      if (LONG) *(u32x4 *)(named + i) = (u32x4){0, 0, 0, 0};
+    }
     for (int i = tid; i < kPiece / 32; i += kLogitThreads) touched[i] = 0;
     if (tid == 0) listed = 0;
     for (int i = tid; i < kListed; i += kLogitThreads) listed_token[i] = -1;
@@ -195,40 +202,37 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
       if (word < 0) continue;
       atomicOr(&table[word], kBiased);
       touch(word);
-      const int at = atomicAdd(&listed, 1);
-      if (at < kListed) {
-        listed_token[at] = x;
-        listed_at[at] = i;
-        listed_bias[at] = i == tid ? first_bias : bias[i];
+      if (LONG) {
+        atomicMax(&named[word], (uint32_t)i + 1u);
+        continue;
       }
+      const int at = atomicAdd(&listed, 1);
+      listed_token[at] = x;
+      listed_at[at] = i;
+      listed_bias[at] = i == tid ? first_bias : bias[i];
     }
     __syncthreads();
   }
   // of equal biases the last in the list, whichever order they came to LDS in
   const int biases = listed;
-  const auto bias_of = [&](int x) {
+  const auto bias_of = [&](int x, int word) {
+    if (LONG) return (double)bias[named[word] - 1u];
     int last = -1;
     float v = 0.0f;
-    if (biases <= kListed) {
-      for (int i = 0; i < biases; i += 4) {
-        const u32x4 four = *(const u32x4 *)(listed_token + i);
+    for (int i = 0; i < biases; i += 4) {
+      const u32x4 four = *(const u32x4 *)(listed_token + i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((int)four[k] == x && listed_at[i + k] > last) {
-            last = listed_at[i + k];
-            v = listed_bias[i + k];
-          }
-      }
-    } else {
-      for (int i = a.biases - 1; i >= 0 && last < 0; --i)
-        if (bias_tokens[i] == x) last = i;
-      v = bias[last];
+      for (int k = 0; k < 4; ++k)
+        if ((int)four[k] == x && listed_at[i + k] > last) {
+          last = listed_at[i + k];
+          v = listed_bias[i + k];
+        }
     }
     return (double)v;
   };
   const double inverse = shared_inverse;
-  // A logit by its entry's word.
-  const auto ruled = [&](E e, uint32_t w, int x) {
+  // A logit by its entry's word, the word-th of the piece.
+  const auto ruled = [&](E e, uint32_t w, int x, int word) {
     const uint32_t made = w & kMade;
     const double l = (double)Logit<T>::get(e);
     double q = l * inverse;                  // an exact quotient comes out exact
@@ -236,7 +240,7 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
     q = __builtin_fabs(q) < INFINITY && q != 0.0 ? exact : q;
     double z = w & (kInPrompt | kMade) ? l > 0.0 ? q : l * rep : l;
     z = made ? z - (freq * (double)made + pres) : z;
-    if (w & kBiased) z += bias_of(x);
+    if (w & kBiased) z += bias_of(x, word);
     return Logit<T>::put(z);
   };
   // the piece, masked
@@ -265,14 +269,14 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
         for (int k = 0; k < kChunk; ++k) {
           const bool mine = (own >> k) & 1u;
           if (!__any(mine)) continue;
-          const E y = ruled(u[c].e[k], mine ? seen[k] : 0u, (int)x0 + k);
+          const E y = ruled(u[c].e[k], mine ? seen[k] : 0u, (int)x0 + k, word + k);
           u[c].e[k] = mine ? y : u[c].e[k];
         }
       }
     } else {
       for (uint32_t left = own; left; left &= left - 1) {
         const int k = __ffs(left) - 1;
-        u[c].put(k, ruled(u[c].at(k), table[word + k], (int)x0 + k));
+        u[c].put(k, ruled(u[c].at(k), table[word + k], (int)x0 + k, word + k));
       }
     }
     if (mask) {
@@ -300,10 +304,15 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
   }
 }
 
+template <class T, int CHUNKS>
+void launch_chunks(const LogitArgs &a, dim3 grid, hipStream_t st) {
+  if (a.biases > kListed) adjust_kernel<T, CHUNKS, true><<<grid, kLogitThreads, 0, st>>>(a);
+  else adjust_kernel<T, CHUNKS, false><<<grid, kLogitThreads, 0, st>>>(a);
+}
 template <class T>
 void launch_type(const LogitArgs &a, dim3 grid, hipStream_t st) {
-  if (a.piece == kLogitPiece) adjust_kernel<T, 2><<<grid, kLogitThreads, 0, st>>>(a);
-  else adjust_kernel<T, 1><<<grid, kLogitThreads, 0, st>>>(a);
+  if (a.piece == kLogitPiece) launch_chunks<T, 2>(a, grid, st);
+  else launch_chunks<T, 1>(a, grid, st);
 }
 
 }  // namespace

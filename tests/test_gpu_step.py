@@ -1067,6 +1067,43 @@ def test_logits_are_rounded_once(dtype, rule):
             assert torch.equal(got[0, :32].double(), want), (side, rows, got[0, :32], want)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,biases", [(1, 256), (1, 257), (2, 5000), (300, 700), (1, 40000)])
+def test_logits_long_lists(dtype, rows, biases):
+    """Lists past what a work-group holds, tokens in them many times over: the last bias stands."""
+    say(f"logits, {rows} rows, {biases} biases, {dtype}")
+    V, g = 9001, torch.Generator().manual_seed(biases)
+    z = torch.randn((rows, V), generator=g).to(dtype)
+    ids = torch.randint(-5, V + 5, (1, biases), generator=g).to(torch.int32)
+    ids[0, biases // 2:] = ids[0, biases // 2:] // 40 * 40   # a few tokens, many times
+    c = dict(starts=torch.tensor([0, rows], dtype=torch.int32), ids=ids, bias=torch.randn((1, biases), generator=g) * 4,
+             text=torch.arange(0, V, 7, dtype=torch.int32)[None], lens=torch.tensor([V], dtype=torch.int32), freq=torch.tensor([0.7]))
+    got = run_logits(put(z), c)
+    few = sorted({0, rows // 2, rows - 1})                   # rows differ in their logits alone: the text is past its width
+    check_logits(got[few].cpu(), z[few], dict(c, starts=torch.tensor([0, len(few)], dtype=torch.int32)), 0.0)
+
+
+def test_logits_long_lists_take_their_length():
+    """40 times the list takes no more than 100 times as long (it took 1,000 times)."""
+    say("logits, time of long lists")
+    V, g, took = 32000, torch.Generator().manual_seed(1), []
+    z, starts = torch.randn((1, V), generator=g).cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda()
+    for n in (250, 10000):
+        ids, bias = torch.randperm(V, generator=g)[None, :n].to(torch.int32).cuda(), torch.randn((1, n), generator=g).cuda()
+        out = gm.keops_adjust_logits(z, starts, bias_tokens=ids, bias=bias)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(5):
+            gm.keops_adjust_logits(z, starts, bias_tokens=ids, bias=bias, out=out)
+        b.record()
+        torch.cuda.synchronize()
+        took.append(a.elapsed_time(b))
+        want = z.clone()
+        want[0, ids[0].long()] = (z[0, ids[0].long()].double() + bias[0].double()).float()
+        assert torch.equal(out, want)
+    assert took[1] < 100 * took[0], took
+
+
 def test_logits_follow_drafted_tokens():
     """Each of a sequence's rows has seen one token more; starts past the rows are cut, lens past the text too."""
     say("logits of drafted tokens")
