@@ -3,6 +3,8 @@
 // paged_call.cpp, None stands for a call that the long way takes or refuses by name.
 #include "call.h"
 
+#include <c10/core/GradMode.h>
+
 namespace {
 
 // A C double from a Python float or int.
@@ -31,10 +33,16 @@ bool rows_output(Call &c, PyObject *given, const at::Tensor &like, at::IntArrayR
   }
   const at::Tensor *t = c.need(given);
   if (!t || t->scalar_type() != like.scalar_type() || !c.on_device(*t) || t->sizes() != shape) return false;
+  if (t->requires_grad() && c10::GradMode::is_enabled()) return false;
   *out = *t;
   return true;
 }
 PyObject *single(const at::Tensor &t, PyObject *given) { return given == Py_None ? THPVariable_Wrap(t) : Py_NewRef(given); }
+// What such a call ends with: autograd is told that the caller's tensor has changed.
+PyObject *ended(int rc, PyObject *result, const at::Tensor &out, PyObject *given) {
+  if (rc == KEOPS_OK && given != Py_None && !out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+  return ended(rc, result);
+}
 
 // Rows [tokens, heads, dim] with dense heads: the distance of rows.
 bool dense_heads(const at::Tensor &t, int64_t *stride) {
@@ -67,7 +75,7 @@ PyObject *rotary(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (!result) return nullptr;
     const int inverse = o[5] == Py_True;
     const int rc = unlocked([&] { return keops_rotary(xp, xs, type, T, (int32_t)H, (int32_t)D, at, &r, inverse, op, os, st); });
-    return ended(rc, result);
+    return ended(rc, result, out, o[6]);
   });
 }
 
@@ -100,7 +108,7 @@ PyObject *append_rotary(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int rc = unlocked([&] {
       return keops_cache_append_rotary(&cache, qp, kp, vp, qs, ks, vs, type, (int32_t)heads, at, T, pos, &r, op, os, st);
     });
-    return ended(rc, result);
+    return ended(rc, result, out, o[15]);
   });
 }
 
@@ -167,7 +175,7 @@ PyObject *adjust(PyObject *, PyObject *const *o, Py_ssize_t n) {
     PyObject *result = single(out, o[11]);
     if (!result) return nullptr;
     const int rc = unlocked([&] { return keops_adjust_logits(lp, stride, type, T, (int32_t)V, &r, op, os, st); });
-    return ended(rc, result);
+    return ended(rc, result, out, o[11]);
   });
 }
 

@@ -2,7 +2,8 @@
 slots back, and the adjustment of logits (C ABI in include/keops_mi355x.h, where they are defined).
 
 Conventions are those of ``paged.py``.  ``keops_rotary`` is differentiated by calling it on the gradient with
-``inverse=True``; to autograd the outputs of all of these are constants.
+``inverse=True``; to autograd the outputs of all of these are constants.  A tensor given as ``out`` has its version
+counter raised, and is refused where it requires a gradient and gradients are enabled.
 
 Each call first goes the short way (native/step_call.cpp), as the paged calls do.
 """
@@ -84,7 +85,16 @@ def _given(t, name, like, shape):
     _tensor(t, name)
     if t.dtype is not like.dtype or t.device != like.device or t.shape != torch.Size(shape):
         raise ValueError(f"{name} must be a {like.dtype} tensor of shape {list(shape)} on {like.device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} must not require a gradient: the call has none")
     return t
+
+
+def _written(*tensors):
+    """Tells autograd that the caller's tensors have changed."""
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
 
 
 def keops_rotary(x, positions, freqs, interleaved=False, factor=1.0, inverse=False, out=None, stream=None):
@@ -93,7 +103,7 @@ def keops_rotary(x, positions, freqs, interleaved=False, factor=1.0, inverse=Fal
     bfloat16, float16 or float32; ``positions`` int32 [tokens], ``freqs`` float64.
 
     ``inverse`` turns the other way: of the gradient with respect to the output it makes the one with respect to x.
-    ``out`` may be x."""
+    No gradient of its own: the output is a constant to autograd, also where x requires one.  ``out`` may be x."""
     if stream is None:
         short = _short or _native()
         got = short and short.rotary(x, positions, freqs, interleaved, factor, inverse, out)
@@ -116,6 +126,8 @@ def keops_rotary(x, positions, freqs, interleaved=False, factor=1.0, inverse=Fal
     _run("keops_rotary", dev, stream, lib().keops_rotary, x.data_ptr(), xs, kind, T, H, D, at, r, bool(inverse), out.data_ptr(),
          _dense_heads(out, "out"))
     _keep(other, dev, made)
+    if made is None:
+        _written(out)
     return out
 
 
@@ -150,6 +162,8 @@ def keops_cache_append_rotary(q, k, v, k_pages, v_pages, page_table, lens, start
     _run("keops_cache_append_rotary", dev, stream, lib().keops_cache_append_rotary, c, qp, kp, vp, qs, ks, vs, _TYPES[k.dtype], heads,
          st, T, at, r, out.data_ptr(), _dense_heads(out, "out"))
     _keep(other, dev, made)
+    if made is None:
+        _written(out)
     return out
 
 
@@ -179,6 +193,8 @@ def keops_cache_read(k_pages, v_pages, page_table, lens, starts, tokens, dtype=N
     _run("keops_cache_read", dev, stream, lib().keops_cache_read, c, k.data_ptr(), v.data_ptr(), _dense_heads(k, "out"),
          _dense_heads(v, "out"), _TYPES[dtype], st, T)
     _keep(other, dev, *made)
+    if out is not None:
+        _written(k, v)
     return k, v
 
 
@@ -192,7 +208,8 @@ def keops_adjust_logits(logits, starts, tokens=None, lens=None, prompt_lens=None
     occurs c > 0 times past the first prompt_lens[s] tokens loses c frequency[s] + presence[s].  The lists
     ``bias_tokens`` int32 and ``bias`` float32 [sequences, n] add to the entries that they name (-1: none; of equal ones the
     last).  ``mask`` int32 [rows, ceil(vocab / 32)]: entry x stays where bit x % 32 of word x // 32 is set, and becomes
-    -inf elsewhere.  Penalties are float32 [sequences].  Rows of no sequence are not written.  ``out`` may be logits."""
+    -inf elsewhere.  Penalties are float32 [sequences].  Rows of no sequence are not written.  ``out`` may be logits.
+    No gradient."""
     if stream is None:
         short = _short or _native()
         got = short and short.adjust(logits, starts, tokens, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias, mask,
@@ -247,4 +264,6 @@ def keops_adjust_logits(logits, starts, tokens=None, lens=None, prompt_lens=None
     _run("keops_adjust_logits", dev, stream, lib().keops_adjust_logits, logits.data_ptr(), logits.stride(0) if T > 1 else V, kind, T, V,
          rules, out.data_ptr(), out.stride(0) if T > 1 else V)
     _keep(other, dev, made)
+    if made is None:
+        _written(out)
     return out

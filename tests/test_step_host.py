@@ -296,6 +296,43 @@ def test_eviction_needs_the_powers_of_a_4_bit_cache(host):
         gm.keops_cache_evict(pages, pages, torch.zeros((4, 2, 16)), i, i[0, :1], i, 4)
 
 
+def calls_with_outputs():
+    """(call, the outputs given to it) of each call that writes to tensors of the caller's, the pools aside."""
+    bf, i32 = torch.bfloat16, torch.int32
+    x, at, f = torch.zeros((2, 2, 64), dtype=bf), torch.zeros(2, dtype=i32), torch.zeros(32, dtype=torch.float64)
+    pages = torch.zeros((4, 16, 2, 64), dtype=bf)
+    table, lens, starts = torch.zeros((1, 4), dtype=i32), torch.ones(1, dtype=i32), torch.tensor([0, 2], dtype=i32)
+    z, q, k, v = torch.zeros((2, 40)), x.clone(), x.clone(), x.clone()
+    return [(lambda: gm.keops_rotary(x, at, f, out=x), [x]),
+            (lambda: gm.keops_cache_append_rotary(k, k, v, pages, pages.clone(), table, lens, starts, f, out=q), [q]),
+            (lambda: gm.keops_cache_read(pages, pages.clone(), table, lens, starts, 2, out=(k, v)), [k, v]),
+            (lambda: gm.keops_adjust_logits(z, starts, out=z), [z])]
+
+
+def check_outputs_and_autograd():
+    for call, outs in calls_with_outputs():
+        before = [t._version for t in outs]
+        call()
+        assert [t._version for t in outs] == [n + 1 for n in before]
+        # of a tensor that a graph has, the backward pass would not know that it was changed
+        outs[0].requires_grad_()
+        with pytest.raises(ValueError, match="out must not require a gradient"):
+            call()
+        with torch.no_grad():
+            call()
+    y = torch.zeros((2, 2, 64), dtype=torch.bfloat16, requires_grad=True).exp()       # kept for the backward pass
+    gm.keops_rotary(y.detach(), torch.zeros(2, dtype=torch.int32), torch.zeros(32, dtype=torch.float64), out=y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        x = torch.zeros((2, 2, 64), dtype=torch.bfloat16)                             # has no version
+    gm.keops_rotary(x, torch.zeros(2, dtype=torch.int32), torch.zeros(32, dtype=torch.float64), out=x)
+
+
+def test_given_outputs_and_autograd(host):
+    check_outputs_and_autograd()
+
+
 # ---- the compiled way from tensors
 
 @pytest.fixture(scope="module")
@@ -359,6 +396,14 @@ def test_plain_calls_reach_the_library(built, cache):
     a = arguments(outputs=True, cache=cache)
     for name in ("rotary", "append_rotary", "adjust"):
         assert getattr(short, name)(*a[name]) is a[name][-1]
+
+
+def test_given_outputs_and_autograd_the_short_way(built, host, monkeypatch):
+    short, stub = load(built)
+    stub.stub_set(0)
+    monkeypatch.setattr(step, "_short", short)
+    check_outputs_and_autograd()
+    assert host == ["keops_cache_read"] * 2 and stub.stub_calls() == 8      # outputs of reading are given the long way
 
 
 def test_short_way_hands_back_what_it_does_not_take(built):
