@@ -7,7 +7,7 @@
 // (whole numbers, so the order of the additions does not matter), marks those and the entries that the list of biases
 // names as bits, and goes over the logits once.  Few entries of a piece are touched; those are computed in 64 bits one
 // after the other, the others pass by.
-// 158 rows of 131,072 bf16 entries with texts of up to 4,096 tokens take 24 us, 14 without rules, where a copy takes 12
+// 157 rows of 131,072 bf16 entries with texts of up to 4,096 tokens take 25 us, 14 without rules, where a copy takes 12
 // to 18, by whether the cache still holds them: the text's way through LDS comes before the first store, 2,512
 // work-groups of it, four to a compute unit.  Loads that had a condition of their own were each waited for, 28 us.  Pieces
 // of 16,384 took 35 us; rows that share a sequence's table, one after the other in a work-group, 33, and twice as long for
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_kernel(LogitArgs a) {
     const uint32_t own = rules ? ((const uint8_t *)touched)[word / kChunk] & bits : 0u;
     // Few work-groups wait for the slowest lane, that of a text's common tokens, which lie together: the lanes' first
     // entries, then their second ones, without a branch in them (one row of 32,000 fp32 entries: 4.8 us of the GPU, 5.7
-    // otherwise, 7.0 without a mask).  Many have more to do: each lane its own entries (158 rows: 24.4 us, 26 otherwise).
+    // otherwise, 7.0 without a mask).  Many have more to do: each lane its own entries (157 rows: 24.4 us, 26 otherwise).
     if constexpr (CHUNKS == 1) {
       if (__any(own)) {
         uint32_t seen[kChunk];

@@ -23,7 +23,7 @@ constexpr int kFewLeast = 128;
 constexpr int kFewWhole = 1024;
 // Up to here work-groups of eight waves that have a head's slots to themselves beat splitting them and
 // a second pass: 15.6 to 19 us a call at 300 and 600 slots, 18.2 to 18.5 at 1,000, 28.5 to 20.6 at 2,000
-// (one compute unit reads at most some 50 bytes a nanosecond).
+// (one compute unit reads at most some 50 bytes a nanosecond).  Measured on 16-bit caches; narrower ones take the same border.
 constexpr int kFewWhole8 = 768;
 
 // Parts of a row from which on its join is shared by columns: 400 parts (one head's 51,206 slots) take 22.6 us
@@ -44,7 +44,7 @@ constexpr double kScoresAlways = 512e6, kScoresMost = 4294967296.0;
 // Rows of a sequence's head, by the bound and by the mean of the sequences, from which on a 4-bit cache is widened to 16
 // bits before attention, not in each of its work-groups.  16,384 slots of 8 x 128: 4,096 tokens of 4 rows a head 1,103 to 943 us, 512 tokens 182 to 167, 256
 // 110 to 107, 128 61 to 73; 8,192 slots of dim 256 and 2,048 tokens 769 to 606.  And what that may take: of memory, and
-// beside the pool, for the bounds may lie far above the lengths.
+// beside the pool, for the bounds may lie far above the lengths.  Without that memory the call does without: the same bits.
 constexpr int64_t kWidenRows = 1024;
 constexpr double kWidenMost = 4294967296.0;
 

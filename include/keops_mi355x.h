@@ -380,7 +380,8 @@ int keops_cache_read(const keops_cache_t *cache, void *k, void *v, int64_t k_str
  * buffer of at least keops_paged_attention_workspace bytes (KEOPS_ERR_SCRATCH if smaller).
  * Under stream capture a call that needs workspace must bring its own (KEOPS_ERR_ALLOC
  * otherwise), which has to live as long as the graph.  Prompts over an E2M1 cache take up to 4 GB
- * to hold its slots in 16 bits; where the library cannot allocate that, they do without, slower.
+ * to hold its slots in 16 bits; where the library cannot allocate that, they do without: the same
+ * bits, slower.
  */
 int keops_paged_attention(const keops_cache_t *cache, const void *q, int64_t q_stride, int32_t type, int32_t heads,
                           const int32_t *starts, int64_t tokens, int32_t max_q, int32_t max_len, float scale,
