@@ -134,7 +134,7 @@ def keops_rotary(x, positions, freqs, interleaved=False, factor=1.0, inverse=Fal
 def keops_cache_append_rotary(q, k, v, k_pages, v_pages, page_table, lens, starts, freqs, positions=None, interleaved=False,
                               factor=1.0, weights=None, k_scale=None, v_scale=None, out=None, stream=None):
     """``keops_cache_append`` of k, rotated, and v, and the rotated queries q [tokens, query heads, dim], which are
-    returned (``out``: where to).  A token's position is that of ``positions`` int32 [tokens], or its slot's number.
+    returned (``out``: where to, not into q).  A token's position is that of ``positions`` int32 [tokens], or its slot's number.
     Rotation as in ``keops_rotary``; an 8-bit or 4-bit cache holds what is nearest to the rotated key itself.  Rows of
     tokens in no sequence are not written.  No gradient."""
     if stream is None:

@@ -347,7 +347,8 @@ int keops_rotary(const void *x, int64_t x_stride, int32_t type, int64_t tokens, 
  * slot, v into its slot as it is.  The position of token t is positions[t], or, where positions
  * is NULL, the number of its slot.  Rounded once: an 8-bit or 4-bit cache holds what is nearest
  * to the rotated key (E4M3: its quotient) itself.  q: [tokens][heads][dim], rows q_stride apart;
- * q_out likewise, q_out_stride apart, heads any number (0: no q, q_out is not read).  Rows of q_out
+ * q_out likewise, q_out_stride apart, heads any number (0: no q, q_out is not read); it must not
+ * overlap q (a token's pieces are read by several threads), k, v or the pool.  Rows of q_out
  * of tokens in no sequence stay as they were; a token without a slot has its q rotated.
  */
 int keops_cache_append_rotary(const keops_cache_t *cache, const void *q, const void *k, const void *v, int64_t q_stride,
